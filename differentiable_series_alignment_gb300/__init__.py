@@ -11,6 +11,10 @@ README ("Usage", "Fused Mode", "Normalization", "Time Series Barycenters"):
     soft_dtw_cost(C, gamma=1.0) -> (B,) losses of a given (B,N,M) cost, differentiable in C
     softdtw_barycenter(sequences, gamma=1.0, max_iter=100, lr=0.1, fused=True) -> (T, D)
 
+Operators of the sequence encoder whose outputs are aligned (encoder.py), differentiable:
+    layer_norm(x, weight, bias), rotary(q, k, table=rotary_table(length, dim)),
+    attention(q, k, v, causal=False, window=None, q_lengths=None, k_lengths=None)
+
 PyTorch supplies device memory and streams only; every step of the method runs
 in libsdtw.so's kernels.
 """
@@ -27,7 +31,10 @@ from ._lib import (CHECKPOINT, EXTENDED, FUSED, OP_BARYCENTER, OP_COST, OP_FWD_B
                    sdtw_backward_varlen, sdtw_barycenter_step_clipped, sdtw_debug_set_wait, sdtw_forward_varlen,
                    sdtw_distance, sdtw_forward, sdtw_forward_cost, sdtw_last_device_status, sdtw_normalized,
                    sdtw_workspace_bytes, workspace, host_workspace, sdtw_host_workspace_bytes,
-                   sdtw_value_and_grad_host)
+                   sdtw_value_and_grad_host, Attention, attention_problem, sdtw_attention_backward,
+                   sdtw_attention_forward, sdtw_attention_workspace_bytes, sdtw_encoder_status,
+                   sdtw_layernorm_backward, sdtw_layernorm_forward, sdtw_layernorm_workspace_bytes, sdtw_rotary)
+from .encoder import attention, layer_norm, rotary, rotary_table
 
 __all__ = [
     "SoftDTW", "soft_dtw_cost", "softdtw_barycenter", "SdtwError", "load", "workspace",
@@ -38,6 +45,9 @@ __all__ = [
     "OP_COST", "auto_precision", "value_and_grad_host", "host_workspace", "sdtw_host_workspace_bytes",
     "sdtw_value_and_grad_host", "sdtw_normalized_unequal", "OP_NORMALIZED_UNEQUAL", "CHECKPOINT",
     "sdtw_normalized_backward", "sdtw_normalized_unequal_backward", "sdtw_debug_set_options",
+    "layer_norm", "rotary", "rotary_table", "attention", "Attention", "attention_problem",
+    "sdtw_attention_forward", "sdtw_attention_backward", "sdtw_attention_workspace_bytes", "sdtw_encoder_status",
+    "sdtw_layernorm_forward", "sdtw_layernorm_backward", "sdtw_layernorm_workspace_bytes", "sdtw_rotary",
 ]
 
 

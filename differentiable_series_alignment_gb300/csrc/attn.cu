@@ -1,0 +1,558 @@
+// attn.cu -- attention on the FP32 pipe: fp32 tensors, and 16-bit ones whose head size
+// or alignment the tensor-core kernels cannot take.
+//
+//   S = scale q k^T on the visible keys, lse = log sum exp S, P = exp(S - lse), o = P v
+//   delta = sum_d do o, dP = do v^T, dS = P (dP - delta)
+//   dq = scale dS k, dk = scale dS^T q, dv = P^T do
+//
+// Forward: one CTA per 64 packed rows (rows of the heads that share a key head, see
+// encoder.h) walks the keys in tiles of 64 with the running maximum and sum of the
+// softmax; S never leaves the SM. Backward: P is computed again from lse. One kernel
+// walks the keys for a tile of rows and gives dq, another walks the rows for a tile of
+// keys and gives dk and dv, summed over the heads that share them: no atomics, the same
+// bits every time, at the price of computing S and dP twice.
+// 256 threads hold 4 x 4 of every 64 x 64 product (rows ty + 16 i, columns tx + 16 j), so
+// that a step of four features costs 8 16-byte shared loads for 64 FMAs; row pitches of
+// D + 4 floats keep those loads free of bank conflicts.
+#include <cfloat>
+
+#include "common.cuh"
+#include "encoder.h"
+
+namespace sdtw {
+namespace {
+
+constexpr int kT = 64;            // rows and keys per tile
+constexpr int kThr = 256;
+constexpr int kPitchP = kT + 4;   // pitch of a 64 x 64 tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Rows [0, kT) of a tile: row_ptr(i) is the row's first element or null (zeros).
+template <typename T, int DP, typename F>
+__device__ __forceinline__ void load_tile(float* dst, int D, F row_ptr)
+{
+    constexpr int LD = DP + 4;
+    for (int e = threadIdx.x; e < kT * (DP / 4); e += kThr) {
+        const int r = e / (DP / 4), c = (e % (DP / 4)) * 4;
+        const T* src = row_ptr(r);
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = (src && c + q < D) ? to_f32(src[c + q]) : 0.f;
+        *reinterpret_cast<float4*>(dst + r * LD + c) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// acc[i][j] = sum_d a[ty + 16 i][d] * b[tx + 16 j][d]
+template <int DP>
+__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx)
+{
+    constexpr int LD = DP + 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * LD + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LD + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+
+// out[i][c] += sum_k p[ty + 16 i][k] * v[k][column c of this thread]; columns tx * 4 + 64 cc
+// (DP >= 64), tx * 2 (DP = 32).
+template <int DP> struct Cols {
+    static constexpr int W = DP >= 64 ? 4 : 2;     // consecutive columns
+    static constexpr int N = DP >= 64 ? DP / 64 : 1;
+    static __device__ __forceinline__ int at(int tx, int cc, int w) { return tx * W + 64 * cc + w; }
+};
+template <int DP>
+__device__ __forceinline__ void mul_tile(float (&out)[4][Cols<DP>::N * Cols<DP>::W], const float* p, const float* v, int ty,
+                                         int tx)
+{
+    constexpr int LD = DP + 4, W = Cols<DP>::W, NC = Cols<DP>::N;
+#pragma unroll 2
+    for (int k = 0; k < kT; k += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPitchP + k);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                float y[W];
+                const float* src = v + (k + q) * LD + Cols<DP>::at(tx, cc, 0);
+                if (W == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(src);
+                    y[0] = t.x, y[1] = t.y, y[W - 2] = t.z, y[W - 1] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(src);
+                    y[0] = t.x, y[1] = t.y;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = q == 0 ? x[i].x : q == 1 ? x[i].y : q == 2 ? x[i].z : x[i].w;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) out[i][cc * W + w] = fmaf(a, y[w], out[i][cc * W + w]);
+                }
+            }
+    }
+}
+
+// max / sum over the 16 lanes (tx) that share a row
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o, 16));
+    return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
+    return v;
+}
+
+template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_simt(const AttnParams p)
+{
+    extern __shared__ float sm[];
+    constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
+    float* Q = sm;
+    float* K = Q + kT * LD;
+    float* V = K + kT * LD;
+    float* P = V + kT * LD;
+    const sdtw_attention& a = p.a;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    // the last rows see the most keys under a causal mask: they start first
+    const int r0 = (((p.rows + kT - 1) / kT) - 1 - (int)(blockIdx.x / heads)) * kT;
+    const int last = min(r0 + kT, p.rows) - 1;
+    const RowRange rr(a, b);
+    const int n_first = r0 / p.G, n_last = min(last / p.G, rr.n_b - 1);
+    int lo = 0, hi = 0;
+    if (n_first <= n_last) {
+        lo = rr.lo(n_first);
+        hi = rr.hi(n_last);
+    }
+    // this CTA's share of the key tiles
+    int t_lo = lo / kT, t_hi = hi > lo ? (hi + kT - 1) / kT : t_lo;
+    if (p.splits > 1) {
+        const int per = (t_hi - t_lo + p.splits - 1) / p.splits;
+        t_lo = min(t_lo + per * (int)blockIdx.y, t_hi);
+        t_hi = min(t_lo + per, t_hi);
+    }
+    const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
+    const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
+    const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
+    load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+        const int r = r0 + i;
+        if (r >= p.rows) return nullptr;
+        const int n = r / p.G;
+        if (n >= rr.n_b) return nullptr;
+        return q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2];
+    });
+    int klo[4], khi[4];   // visible keys of this thread's rows
+    float m[4], l[4], o[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+        const int n = r / p.G;
+        const bool live = r < p.rows && n < rr.n_b;
+        klo[i] = live ? rr.lo(n) : 0;
+        khi[i] = live ? rr.hi(n) : 0;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+    }
+    const float s2 = a.scale * kLog2e;
+    for (int t = t_lo; t < t_hi; ++t) {
+        const int j0 = t * kT;
+        __syncthreads();
+        load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+        load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+        __syncthreads();
+        float s[4][4];
+        dot_tile<DP>(s, Q, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = j0 + tx + 16 * j;
+                s[i][j] = (key >= klo[i] && key < khi[i]) ? s[i][j] * s2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            mx = max16(mx);
+            const float base = mx == -INFINITY ? 0.f : mx;   // nothing seen yet: every term is 0
+            const float keep = ex2(m[i] - base);
+            m[i] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = ex2(s[i][j] - base);
+                sum += e;
+                P[(ty + 16 * i) * kPitchP + tx + 16 * j] = e;
+            }
+            l[i] = l[i] * keep + sum;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] *= keep;
+        }
+        __syncthreads();
+        mul_tile<DP>(o, P, V, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+        const float total = sum16(l[i]);
+        if (r >= p.rows) continue;
+        const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+        const float lse = total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
+        const int n = r / p.G, h = hk * p.G + r % p.G;
+        if (p.splits > 1) {
+            const long long row = (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
+                if (d < a.D) p.part_o[row * a.D + d] = o[i][c] * inv;
+            }
+            if (tx == 0) p.part_lse[row] = lse;
+        } else {
+            const long long at = (((long long)b * a.N + n) * a.Hq + h) * a.D;
+            T* out = static_cast<T*>(p.out) + at;
+            T* rest = p.out_rest ? static_cast<T*>(p.out_rest) + at : nullptr;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
+                if (d < a.D) store_rounded(out + d, rest ? rest + d : nullptr, o[i][c] * inv);
+            }
+            if (tx == 0 && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse;
+        }
+    }
+}
+
+// o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp lse_s: the shares of the key axis
+// joined, one warp per packed row.
+template <typename T> __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p)
+{
+    const sdtw_attention& a = p.a;
+    const long long all = (long long)a.B * a.Hkv * p.rows;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= all) return;
+    const int r = (int)(row % p.rows);
+    const int hk = (int)(row / p.rows % a.Hkv), b = (int)(row / p.rows / a.Hkv);
+    const int n = r / p.G, h = hk * p.G + r % p.G;
+    float m = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; ++s) {
+        const float w = ex2((p.part_lse[s * all + row] - base) * kLog2e);
+        total += w;
+        const float* src = p.part_o + (s * all + row) * a.D;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (lane + 32 * q < a.D) acc[q] = fmaf(w, src[lane + 32 * q], acc[q]);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const long long at = (((long long)b * a.N + n) * a.Hq + h) * a.D + lane;
+    T* out = static_cast<T*>(p.out) + at;
+    T* rest = p.out_rest ? static_cast<T*>(p.out_rest) + at : nullptr;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (lane + 32 * q < a.D) store_rounded(out + 32 * q, rest ? rest + 32 * q : nullptr, acc[q] * inv);
+    if (lane == 0 && p.lse)
+        p.lse[((long long)b * a.Hq + h) * a.N + n] = total == 0.f ? -INFINITY : m + logf(total);
+}
+
+// What the backward kernels need of a row: lse in base-2 units (+inf where the row sees
+// nothing or does not exist, which makes its probabilities 0) and delta = sum_d do o. The
+// difference dP - delta cancels where one key has most of a row, so o is taken with what
+// its rounding to 16 bits left; with the rounded o alone dq and dk were up to 5 times
+// further from their 64-bit values than a plain fp32 pass on short fp16 sequences.
+// One warp per packed row, in packed order and padded to whole tiles.
+template <typename T> __global__ void __launch_bounds__(256) attn_rowinfo_kernel(const AttnParams p)
+{
+    const sdtw_attention& a = p.a;
+    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (at >= (long long)a.B * a.Hkv * p.rows_pad) return;
+    const int r = (int)(at % p.rows_pad);
+    const int hk = (int)(at / p.rows_pad % a.Hkv), b = (int)(at / p.rows_pad / a.Hkv);
+    const int n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
+    const int n = r / p.G, h = hk * p.G + r % p.G;
+    float lse = -INFINITY, delta = 0.f;
+    if (r < p.rows && n < n_b) {
+        lse = p.lse_in[((long long)b * a.Hq + h) * a.N + n];
+        const long long o = (((long long)b * a.N + n) * a.Hq + h) * a.D;
+        const T* x = static_cast<const T*>(p.out) + o;
+        const T* rest = p.out_rest ? static_cast<const T*>(p.out_rest) + o : nullptr;
+        const T* g = static_cast<const T*>(p.dout) + o;
+        for (int d = lane; d < a.D; d += 32)
+            delta = fmaf(to_f32(x[d]) + (rest ? to_f32(rest[d]) : 0.f), to_f32(g[d]), delta);
+#pragma unroll
+        for (int q = 16; q > 0; q >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, q);
+    }
+    if (lane == 0) {
+        const bool none = lse == -INFINITY;
+        p.row_lse[at] = none ? INFINITY : lse * kLog2e - (float)p.grad_shift;
+        p.row_delta[at] = none ? 0.f : delta;
+    }
+}
+
+// dq of 64 packed rows: S and dP = do v^T per key tile, dq += dS k.
+template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_simt(const AttnParams p)
+{
+    extern __shared__ float sm[];
+    constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
+    float* Q = sm;
+    float* G = Q + kT * LD;
+    float* K = G + kT * LD;
+    float* V = K + kT * LD;
+    float* S = V + kT * LD;
+    const sdtw_attention& a = p.a;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int r0 = (((p.rows + kT - 1) / kT) - 1 - (int)(blockIdx.x / heads)) * kT;
+    const int last = min(r0 + kT, p.rows) - 1;
+    const RowRange rr(a, b);
+    const int n_first = r0 / p.G, n_last = min(last / p.G, rr.n_b - 1);
+    int lo = 0, hi = 0;
+    if (n_first <= n_last) {
+        lo = rr.lo(n_first);
+        hi = rr.hi(n_last);
+    }
+    const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
+    const T* dout = static_cast<const T*>(p.dout);
+    const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
+    const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
+    load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+        const int r = r0 + i;
+        const int n = r / p.G;
+        return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
+    });
+    load_tile<T, DP>(G, a.D, [&](int i) -> const T* {
+        const int r = r0 + i;
+        const int n = r / p.G;
+        return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
+    });
+    int klo[4], khi[4];
+    float lse[4], delta[4], dq[4][NC];
+    const long long info = ((long long)b * a.Hkv + hk) * p.rows_pad;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+        const int n = r / p.G;
+        const bool live = r < p.rows && n < rr.n_b;
+        klo[i] = live ? rr.lo(n) : 0;
+        khi[i] = live ? rr.hi(n) : 0;
+        lse[i] = p.row_lse[info + r];
+        delta[i] = p.row_delta[info + r];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) dq[i][c] = 0.f;
+    }
+    const float s2 = a.scale * kLog2e, back = ex2(-(float)p.grad_shift);
+    for (int j0 = lo / kT * kT; j0 < hi; j0 += kT) {
+        __syncthreads();
+        load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+        load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<DP>(s, Q, K, ty, tx);
+        dot_tile<DP>(dp, G, V, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = j0 + tx + 16 * j;
+                const bool see = key >= klo[i] && key < khi[i];
+                S[(ty + 16 * i) * kPitchP + tx + 16 * j] =
+                    see ? ex2(fmaf(s[i][j], s2, -lse[i])) * (dp[i][j] - delta[i]) : 0.f;
+            }
+        __syncthreads();
+        mul_tile<DP>(dq, S, K, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+        if (r >= p.rows) continue;
+        T* out = static_cast<T*>(p.dq) + (((long long)b * a.N + r / p.G) * a.Hq + hk * p.G + r % p.G) * a.D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
+            if (d < a.D) out[d] = from_f32<T>(dq[i][c] * back * a.scale);
+        }
+    }
+}
+
+// dk and dv of 64 keys: S^T and dP^T per tile of packed rows, dv += P^T do, dk += dS^T q.
+template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dkv_simt(const AttnParams p)
+{
+    extern __shared__ float sm[];
+    constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
+    float* K = sm;
+    float* V = K + kT * LD;
+    float* Q = V + kT * LD;
+    float* G = Q + kT * LD;
+    float* P = G + kT * LD;
+    float* S = P + kT * kPitchP;
+    const sdtw_attention& a = p.a;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int j0 = (int)(blockIdx.x / heads) * kT;   // the first keys are seen by the most rows
+    const RowRange rr(a, b);
+    // rows that see any key of the tile
+    const int j_last = min(j0 + kT, rr.m_b) - 1;
+    int row_lo = 0, row_hi = 0;
+    if (j0 <= j_last) {
+        row_lo = rr.row_lo(j0) * p.G;
+        row_hi = rr.row_hi(j_last) * p.G;
+    }
+    const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
+    const T* dout = static_cast<const T*>(p.dout);
+    const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
+    const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
+    load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+    load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+    float dk[4][NC], dv[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) dk[i][c] = dv[i][c] = 0.f;
+    const float s2 = a.scale * kLog2e, back = ex2(-(float)p.grad_shift);
+    const long long info = ((long long)b * a.Hkv + hk) * p.rows_pad;
+    for (int r0 = row_lo / kT * kT; r0 < row_hi; r0 += kT) {
+        __syncthreads();
+        load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+            const int r = r0 + i;
+            const int n = r / p.G;
+            return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
+        });
+        load_tile<T, DP>(G, a.D, [&](int i) -> const T* {
+            const int r = r0 + i;
+            const int n = r / p.G;
+            return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
+        });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<DP>(s, K, Q, ty, tx);
+        dot_tile<DP>(dp, V, G, ty, tx);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = r0 + tx + 16 * j;
+            const int n = r / p.G;
+            const bool live = n < rr.n_b;
+            const int klo = live ? rr.lo(n) : 0, khi = live ? rr.hi(n) : 0;
+            const float lse = p.row_lse[info + r], delta = p.row_delta[info + r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = j0 + ty + 16 * i;
+                const bool see = key >= klo && key < khi;
+                const float e = see ? ex2(fmaf(s[i][j], s2, -lse)) : 0.f;
+                P[(ty + 16 * i) * kPitchP + tx + 16 * j] = e;
+                S[(ty + 16 * i) * kPitchP + tx + 16 * j] = see ? e * (dp[i][j] - delta) : 0.f;
+            }
+        }
+        __syncthreads();
+        mul_tile<DP>(dv, P, G, ty, tx);
+        mul_tile<DP>(dk, S, Q, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + ty + 16 * i;
+        if (j >= a.M) continue;
+        const long long o = (((long long)b * a.M + j) * a.Hkv + hk) * a.D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
+            if (d < a.D) {
+                if (p.dk) static_cast<T*>(p.dk)[o + d] = from_f32<T>(dk[i][c] * back * a.scale);
+                if (p.dv) static_cast<T*>(p.dv)[o + d] = from_f32<T>(dv[i][c] * back);
+            }
+        }
+    }
+}
+
+template <typename K> cudaError_t launch(K kernel, dim3 grid, size_t smem, const AttnParams& p, cudaStream_t s)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThr, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int DP> cudaError_t fwd_simt(const AttnParams& p, cudaStream_t s)
+{
+    const unsigned tiles = (unsigned)((p.rows + kT - 1) / kT);
+    const size_t smem = sizeof(float) * (3 * kT * (DP + 4) + kT * kPitchP);
+    return launch(attn_fwd_simt<T, DP>, dim3(tiles * p.a.B * p.a.Hkv, p.splits), smem, p, s);
+}
+
+template <typename T, int DP> cudaError_t bwd_simt(const AttnParams& p, cudaStream_t s)
+{
+    const size_t tile = sizeof(float) * kT * (DP + 4), sq = sizeof(float) * kT * kPitchP;
+    if (p.dq) {
+        const unsigned tiles = (unsigned)((p.rows + kT - 1) / kT);
+        cudaError_t e = launch(attn_dq_simt<T, DP>, dim3(tiles * p.a.B * p.a.Hkv), 4 * tile + sq, p, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.dk || p.dv)
+        return launch(attn_dkv_simt<T, DP>, dim3((unsigned)((p.a.M + kT - 1) / kT) * p.a.B * p.a.Hkv), 4 * tile + 2 * sq, p, s);
+    return cudaSuccess;
+}
+
+template <typename T> cudaError_t fwd_typed(const AttnParams& p, cudaStream_t s)
+{
+    return p.a.D <= 32 ? fwd_simt<T, 32>(p, s) : p.a.D <= 64 ? fwd_simt<T, 64>(p, s) : fwd_simt<T, 128>(p, s);
+}
+template <typename T> cudaError_t bwd_typed(const AttnParams& p, cudaStream_t s)
+{
+    return p.a.D <= 32 ? bwd_simt<T, 32>(p, s) : p.a.D <= 64 ? bwd_simt<T, 64>(p, s) : bwd_simt<T, 128>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_forward_simt(const AttnParams& p, cudaStream_t s)
+{
+    if (p.a.dtype == SDTW_F32) return fwd_typed<float>(p, s);
+    if (p.a.dtype == SDTW_BF16) return fwd_typed<__nv_bfloat16>(p, s);
+    return fwd_typed<__half>(p, s);
+}
+
+cudaError_t launch_attn_backward_simt(const AttnParams& p, cudaStream_t s)
+{
+    if (p.a.dtype == SDTW_F32) return bwd_typed<float>(p, s);
+    if (p.a.dtype == SDTW_BF16) return bwd_typed<__nv_bfloat16>(p, s);
+    return bwd_typed<__half>(p, s);
+}
+
+cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(((long long)p.a.B * p.a.Hkv * p.rows + 3) / 4);
+    if (p.a.dtype == SDTW_F32) attn_combine_kernel<float><<<grid, 128, 0, s>>>(p);
+    else if (p.a.dtype == SDTW_BF16) attn_combine_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
+    else attn_combine_kernel<__half><<<grid, 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_rowinfo(const AttnParams& p, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(((long long)p.a.B * p.a.Hkv * p.rows_pad + 7) / 8);
+    if (p.a.dtype == SDTW_F32) attn_rowinfo_kernel<float><<<grid, 256, 0, s>>>(p);
+    else if (p.a.dtype == SDTW_BF16) attn_rowinfo_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+    else attn_rowinfo_kernel<__half><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace sdtw

@@ -1,0 +1,111 @@
+// encoder.h -- host-side declarations of the sequence-encoder operators' launchers
+// (layer norm, rotary positions, attention) and the element types they share.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/sdtw.h"
+
+namespace sdtw {
+
+// Elements of 32 or 16 bits; all arithmetic is in fp32, each result rounded once.
+template <typename T> __device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v) { return static_cast<T>(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+// v rounded into *out and, where rest is wanted, what that rounding left, rounded too.
+template <typename T> __device__ __forceinline__ void store_rounded(T* out, T* rest, float v) {
+    const T r = from_f32<T>(v);
+    *out = r;
+    if (rest) *rest = from_f32<T>(v - to_f32(r));
+}
+
+// VEC consecutive elements, loaded and stored as one access of VEC * sizeof(T) bytes.
+template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack {
+    T e[VEC];
+};
+
+inline int dtype_size(int dtype) { return dtype == SDTW_F32 ? 4 : 2; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct NormParams {
+    const void *x, *weight, *bias, *dy;
+    void *y, *dx, *dweight, *dbias;
+    float *mean, *rstd;
+    float* partial;   // backward: [2][ctas][C] sums of the weight's and the bias's gradient
+    long long rows;
+    int C, dtype, wdtype;
+    float eps;
+};
+int norm_partial_ctas(long long rows, int C, int sms);   // CTAs of the backward = partial rows
+cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s);
+
+struct RotaryParams {
+    const void* in[2];        // q, k (k may be null)
+    void* out[2];             // contiguous (B, N, H, D)
+    long long stride[2][3];   // batch, position, head strides of the inputs, in elements
+    int H[2];
+    const float* table;       // (length, R / 2, 2): cos, sin
+    const int* positions;     // (B, N), (N) or null: 0 .. N-1
+    long long pos_stride_b;   // N or 0
+    int B, N, D, R, length, dtype, interleaved, inverse;
+};
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t s);
+
+// Attention over "packed rows": the G = Hq / Hkv query heads that share a key head are
+// rows of one problem, row r = n G + (head in group), so that a tile of keys is read
+// once for all of them, and a single new token of G heads is a problem of G rows.
+struct AttnParams {
+    sdtw_attention a;
+    int G;                    // Hq / Hkv
+    int rows;                 // N * G
+    void* out;                // (B, N, Hq, D)
+    void* out_rest;           // like out, or null: what the rounding of out left
+    float* lse;               // (B, Hq, N) or null (forward)
+    // keys split over CTAs: each writes its normalised rows and their lse here
+    int splits;
+    float* part_o;            // [splits][B][Hkv][rows][D]
+    float* part_lse;          // [splits][B][Hkv][rows]
+    // backward
+    const void* dout;
+    void *dq, *dk, *dv;
+    const float* lse_in;      // (B, Hq, N)
+    // [B][Hkv][rows_pad]: lse in base-2 units less grad_shift, +inf where a row sees nothing. The backward
+    // kernels so hold 2^grad_shift P and dS and scale their results back: probabilities near the
+    // bottom of the format's range reach the products instead of being flushed to 0.
+    float* row_lse;
+    int grad_shift;
+    float* row_delta;         // [B][Hkv][rows_pad]: sum_d do * o
+    int rows_pad;             // rows rounded up to 128
+};
+cudaError_t launch_attn_forward_simt(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_rowinfo(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_backward_simt(const AttnParams& p, cudaStream_t s);
+
+// Keys that packed row r of batch element b sees: [lo, hi), empty where lo >= hi.
+// Row n of n_b stands at key n + (m_b - n_b): the last row at the last key.
+struct RowRange {
+    int n_b, m_b, shift, left, right;
+    __device__ __forceinline__ RowRange(const sdtw_attention& a, int b) {
+        n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
+        m_b = a.k_lengths ? min(max(a.k_lengths[b], 0), a.M) : a.M;
+        shift = m_b - n_b;
+        left = a.window_left;
+        right = a.window_right;
+    }
+    __device__ __forceinline__ int lo(int n) const { return left < 0 ? 0 : max(0, n + shift - left); }
+    __device__ __forceinline__ int hi(int n) const { return right < 0 ? m_b : min(m_b, n + shift + right + 1); }
+    // rows that see key j: [row_lo, row_hi)
+    __device__ __forceinline__ int row_lo(int j) const { return right < 0 ? 0 : max(0, j - shift - right); }
+    __device__ __forceinline__ int row_hi(int j) const { return left < 0 ? n_b : min(n_b, j - shift + left + 1); }
+};
+
+}  // namespace sdtw

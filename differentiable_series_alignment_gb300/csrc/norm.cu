@@ -1,0 +1,378 @@
+// norm.cu -- layer norm over the last dimension, forward and backward.
+//
+//   mu = mean x, r = 1 / sqrt(mean (x - mu)^2 + eps), xh = (x - mu) r, y = xh w + b
+//   g = dy w, dx = r (g - mean g - xh mean(g xh)), dw = sum_rows dy xh, db = sum_rows dy
+//
+// A row is read once: L lanes of a warp (short rows) or a whole CTA (long rows) keep it
+// in registers, so that the variance is the mean square of centred values (no
+// cancellation of E[x^2] - mu^2) at no further traffic. Rows too long for that are read
+// again from the cache. The weights' gradients are summed in registers over the rows
+// that a CTA takes (a column stays with its thread), then over the CTAs by a second
+// launch in a fixed order: no atomics, the same bits every time.
+#include "encoder.h"
+
+namespace sdtw {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int W> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, W);
+    return v;
+}
+
+// Sum over the row's threads: L lanes of a warp, or (L = kThreads) the CTA.
+template <int L> __device__ __forceinline__ float row_sum(float v, float* red) {
+    if (L <= 32) return group_sum<L < 32 ? L : 32>(v);
+    v = group_sum<32>(v);
+    __syncthreads();   // red may still be read from the previous sum
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+    return s;
+}
+
+template <typename W> __device__ __forceinline__ float wload(const void* p, int c) {
+    return to_f32(static_cast<const W*>(p)[c]);
+}
+__device__ __forceinline__ float wval(const void* p, int c, int wdtype, float none) {
+    if (p == nullptr) return none;
+    if (wdtype == SDTW_F32) return static_cast<const float*>(p)[c];
+    if (wdtype == SDTW_BF16) return wload<__nv_bfloat16>(p, c);
+    return wload<__half>(p, c);
+}
+__device__ __forceinline__ void wstore(void* p, int c, int wdtype, float v) {
+    if (wdtype == SDTW_F32) static_cast<float*>(p)[c] = v;
+    else if (wdtype == SDTW_BF16) static_cast<__nv_bfloat16*>(p)[c] = from_f32<__nv_bfloat16>(v);
+    else static_cast<__half*>(p)[c] = from_f32<__half>(v);
+}
+
+// L threads per row, K packs of VEC elements per thread; C is a multiple of VEC.
+template <typename T, int VEC, int K, int L>
+__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormParams p)
+{
+    __shared__ float red[kThreads / 32];
+    using P = Pack<T, VEC>;
+    const int lane = threadIdx.x % L;
+    const long long step = (long long)gridDim.x * (kThreads / L);
+    const int packs = p.C / VEC;
+    const float inv_c = 1.f / (float)p.C;
+    // every thread of a warp (of the CTA, for long rows) makes the same number of rounds:
+    // the sums below are collective
+    for (long long r0 = (long long)blockIdx.x * (kThreads / L); r0 < p.rows; r0 += step) {
+        const long long r = r0 + threadIdx.x / L;
+        const bool live = r < p.rows;
+        const P* src = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + (live ? r : 0) * p.C);
+        P v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (lane + k * L < packs) v[k] = src[lane + k * L];
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (lane + k * L < packs)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s += to_f32(v[k].e[e]);
+        const float mu = row_sum<L>(s, red) * inv_c;
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (lane + k * L < packs)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float d = to_f32(v[k].e[e]) - mu;
+                    q = fmaf(d, d, q);
+                }
+        const float rs = 1.f / sqrtf(row_sum<L>(q, red) * inv_c + p.eps);
+        if (live) {
+            P* dst = reinterpret_cast<P*>(static_cast<T*>(p.y) + r * p.C);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (lane + k * L < packs) {
+                    P o;
+                    const int c0 = (lane + k * L) * VEC;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        o.e[e] = from_f32<T>(fmaf((to_f32(v[k].e[e]) - mu) * rs, wval(p.weight, c0 + e, p.wdtype, 1.f),
+                                                  wval(p.bias, c0 + e, p.wdtype, 0.f)));
+                    dst[lane + k * L] = o;
+                }
+            if (lane == 0 && p.mean) {
+                p.mean[r] = mu;
+                p.rstd[r] = rs;
+            }
+        }
+    }
+}
+
+// Rows of any length, element by element: the row is read again from the cache.
+template <typename T> __global__ void __launch_bounds__(kThreads) norm_fwd_long_kernel(const NormParams p)
+{
+    __shared__ float red[kThreads / 32];
+    const float inv_c = 1.f / (float)p.C;
+    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const T* src = static_cast<const T*>(p.x) + r * p.C;
+        T* dst = static_cast<T*>(p.y) + r * p.C;
+        float s = 0.f;
+        for (int c = threadIdx.x; c < p.C; c += kThreads) s += to_f32(src[c]);
+        const float mu = row_sum<kThreads>(s, red) * inv_c;
+        float q = 0.f;
+        for (int c = threadIdx.x; c < p.C; c += kThreads) {
+            const float d = to_f32(src[c]) - mu;
+            q = fmaf(d, d, q);
+        }
+        const float rs = 1.f / sqrtf(row_sum<kThreads>(q, red) * inv_c + p.eps);
+        for (int c = threadIdx.x; c < p.C; c += kThreads)
+            dst[c] = from_f32<T>(fmaf((to_f32(src[c]) - mu) * rs, wval(p.weight, c, p.wdtype, 1.f),
+                                      wval(p.bias, c, p.wdtype, 0.f)));
+        if (threadIdx.x == 0 && p.mean) {
+            p.mean[r] = mu;
+            p.rstd[r] = rs;
+        }
+    }
+}
+
+template <typename T, int VEC, int K, int L>
+__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormParams p)
+{
+    __shared__ float red[kThreads / 32];
+    extern __shared__ float fold[];   // L < kThreads: [kThreads / L][C] sums of one gradient at a time
+    using P = Pack<T, VEC>;
+    const int lane = threadIdx.x % L, group = threadIdx.x / L;
+    const long long step = (long long)gridDim.x * (kThreads / L);
+    const int packs = p.C / VEC;
+    const float inv_c = 1.f / (float)p.C;
+    float dw[K][VEC], db[K][VEC];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
+    for (long long r0 = (long long)blockIdx.x * (kThreads / L); r0 < p.rows; r0 += step) {
+        const long long r = r0 + group;
+        const bool live = r < p.rows;
+        const long long at = (live ? r : 0) * p.C;
+        const P* xs = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + at);
+        const P* gs = reinterpret_cast<const P*>(static_cast<const T*>(p.dy) + at);
+        P xv[K], gv[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (lane + k * L < packs) {
+                xv[k] = xs[lane + k * L];
+                gv[k] = gs[lane + k * L];
+            }
+        const float mu = p.mean[live ? r : 0], rs = p.rstd[live ? r : 0];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (lane + k * L < packs)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float xh = (to_f32(xv[k].e[e]) - mu) * rs, dy = to_f32(gv[k].e[e]);
+                    const float g = dy * wval(p.weight, (lane + k * L) * VEC + e, p.wdtype, 1.f);
+                    s1 += g;
+                    s2 = fmaf(g, xh, s2);
+                    if (live) {
+                        dw[k][e] = fmaf(dy, xh, dw[k][e]);
+                        db[k][e] += dy;
+                    }
+                }
+        s1 = row_sum<L>(s1, red) * inv_c;
+        s2 = row_sum<L>(s2, red) * inv_c;
+        if (live && p.dx) {
+            P* dst = reinterpret_cast<P*>(static_cast<T*>(p.dx) + at);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (lane + k * L < packs) {
+                    P o;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float xh = (to_f32(xv[k].e[e]) - mu) * rs;
+                        const float g = to_f32(gv[k].e[e]) * wval(p.weight, (lane + k * L) * VEC + e, p.wdtype, 1.f);
+                        o.e[e] = from_f32<T>(rs * (g - s1 - xh * s2));
+                    }
+                    dst[lane + k * L] = o;
+                }
+        }
+    }
+    if (!p.partial) return;
+    for (int which = 0; which < 2; ++which) {
+        float* out = p.partial + ((long long)which * gridDim.x + blockIdx.x) * p.C;
+        if (L == kThreads) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (lane + k * L < packs)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) out[(lane + k * L) * VEC + e] = which ? db[k][e] : dw[k][e];
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (lane + k * L < packs)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        fold[group * p.C + (lane + k * L) * VEC + e] = which ? db[k][e] : dw[k][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.C; c += kThreads) {
+                float s = 0.f;
+                for (int g = 0; g < kThreads / L; ++g) s += fold[g * p.C + c];
+                out[c] = s;
+            }
+        }
+    }
+}
+
+// Rows of any length: dx by rows, reading the row twice; the columns' sums go straight
+// to this CTA's partial row, which it alone touches.
+template <typename T> __global__ void __launch_bounds__(kThreads) norm_bwd_long_kernel(const NormParams p)
+{
+    __shared__ float red[kThreads / 32];
+    const float inv_c = 1.f / (float)p.C;
+    float* pw = p.partial ? p.partial + (long long)blockIdx.x * p.C : nullptr;
+    float* pb = p.partial ? p.partial + ((long long)gridDim.x + blockIdx.x) * p.C : nullptr;
+    if (pw)
+        for (int c = threadIdx.x; c < p.C; c += kThreads) pw[c] = pb[c] = 0.f;
+    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const T* xs = static_cast<const T*>(p.x) + r * p.C;
+        const T* gs = static_cast<const T*>(p.dy) + r * p.C;
+        const float mu = p.mean[r], rs = p.rstd[r];
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = threadIdx.x; c < p.C; c += kThreads) {
+            const float xh = (to_f32(xs[c]) - mu) * rs, dy = to_f32(gs[c]);
+            const float g = dy * wval(p.weight, c, p.wdtype, 1.f);
+            s1 += g;
+            s2 = fmaf(g, xh, s2);
+            if (pw) {
+                pw[c] = fmaf(dy, xh, pw[c]);
+                pb[c] += dy;
+            }
+        }
+        s1 = row_sum<kThreads>(s1, red) * inv_c;
+        s2 = row_sum<kThreads>(s2, red) * inv_c;
+        if (p.dx) {
+            T* dst = static_cast<T*>(p.dx) + r * p.C;
+            for (int c = threadIdx.x; c < p.C; c += kThreads) {
+                const float xh = (to_f32(xs[c]) - mu) * rs;
+                const float g = to_f32(gs[c]) * wval(p.weight, c, p.wdtype, 1.f);
+                dst[c] = from_f32<T>(rs * (g - s1 - xh * s2));
+            }
+        }
+    }
+}
+
+// dw, db: the CTAs' partial rows added in a fixed order. 32 columns by 8 row lanes.
+__global__ void __launch_bounds__(256) norm_fold_kernel(const NormParams p, int ctas)
+{
+    __shared__ float part[8][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+    const float* src = p.partial + (long long)blockIdx.y * ctas * p.C;
+    float s = 0.f;
+    if (c < p.C)
+        for (int t = lane; t < ctas; t += 8) s += src[(long long)t * p.C + c];
+    part[lane][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (lane == 0 && c < p.C) {
+#pragma unroll
+        for (int g = 1; g < 8; ++g) s += part[g][threadIdx.x & 31];
+        void* dst = blockIdx.y ? p.dbias : p.dweight;
+        if (dst) wstore(dst, c, p.wdtype, s);
+    }
+}
+
+int device_sms()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        n = 152;
+    return n;
+}
+
+// Threads per row: the fewest lanes that hold the row in K <= 4 packs each.
+int lanes_for(int packs)
+{
+    for (int L = 4; L <= 32; L *= 2)
+        if (packs <= (L < 32 ? L : 4 * L)) return L;
+    return packs <= 4 * kThreads ? kThreads : 0;
+}
+
+template <typename T, int VEC, int K, int L>
+cudaError_t run_norm(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+{
+    const int per = kThreads / L;
+    if (!backward) {
+        const long long need = (p.rows + per - 1) / per;
+        const long long most = (long long)device_sms() * 8;
+        norm_fwd_kernel<T, VEC, K, L><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(p);
+    } else {
+        const size_t smem = L == kThreads ? 0 : (size_t)per * p.C * sizeof(float);
+        norm_bwd_kernel<T, VEC, K, L><<<ctas, kThreads, smem, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t pick_norm(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+{
+    const int packs = p.C / VEC;
+    const int L = lanes_for(packs);
+    switch (L) {
+        case 4: return run_norm<T, VEC, 1, 4>(p, backward, ctas, s);
+        case 8: return run_norm<T, VEC, 1, 8>(p, backward, ctas, s);
+        case 16: return run_norm<T, VEC, 1, 16>(p, backward, ctas, s);
+        case 32:
+            if (packs <= 32) return run_norm<T, VEC, 1, 32>(p, backward, ctas, s);
+            if (packs <= 64) return run_norm<T, VEC, 2, 32>(p, backward, ctas, s);
+            return run_norm<T, VEC, 4, 32>(p, backward, ctas, s);
+        case kThreads:
+            if (packs <= kThreads) return run_norm<T, VEC, 1, kThreads>(p, backward, ctas, s);
+            if (packs <= 2 * kThreads) return run_norm<T, VEC, 2, kThreads>(p, backward, ctas, s);
+            return run_norm<T, VEC, 4, kThreads>(p, backward, ctas, s);
+    }
+    if (!backward) {
+        const long long most = (long long)device_sms() * 8;
+        norm_fwd_long_kernel<T><<<(unsigned)(p.rows < most ? p.rows : most), kThreads, 0, s>>>(p);
+    } else {
+        norm_bwd_long_kernel<T><<<ctas, kThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t norm_typed(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+{
+    constexpr int VEC = 16 / sizeof(T);
+    const bool packed = p.C % VEC == 0 && aligned16(p.x) &&
+                        (backward ? aligned16(p.dy) && aligned16(p.dx) : aligned16(p.y));
+    return packed ? pick_norm<T, VEC>(p, backward, ctas, s) : pick_norm<T, 1>(p, backward, ctas, s);
+}
+
+cudaError_t norm_any(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+{
+    if (p.dtype == SDTW_F32) return norm_typed<float>(p, backward, ctas, s);
+    if (p.dtype == SDTW_BF16) return norm_typed<__nv_bfloat16>(p, backward, ctas, s);
+    return norm_typed<__half>(p, backward, ctas, s);
+}
+
+}  // namespace
+
+// Two CTAs per SM keep the partial sums short; fewer where there are few rows.
+int norm_partial_ctas(long long rows, int C, int sms)
+{
+    (void)C;
+    const long long most = 2ll * sms, need = (rows + 7) / 8;
+    return (int)(need < most ? (need < 1 ? 1 : need) : most);
+}
+
+cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t s) { return norm_any(p, false, 0, s); }
+
+cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s)
+{
+    cudaError_t e = norm_any(p, true, ctas, s);
+    if (e != cudaSuccess || !p.partial) return e;
+    norm_fold_kernel<<<dim3((p.C + 31) / 32, 2), 256, 0, s>>>(p, ctas);
+    return cudaGetLastError();
+}
+
+}  // namespace sdtw

@@ -308,6 +308,100 @@ void sdtw_debug_set_clusters(int max_cluster);
  * within 2 ulp of the correctly rounded value; 0 for x < -125. */
 sdtw_status sdtw_debug_exp2_neg(const float* x, float* out, int n, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the sequence encoder whose outputs the loss aligns: layer norm,
+ * rotary positions and attention, each with its gradient. A model that is trained
+ * on the Soft-DTW loss, or that encodes a growing series sample by sample, runs
+ * them next to the entry points above.
+ *
+ * Conventions, where they differ from those above:
+ *  - Elements are fp32, bf16 or fp16 (sdtw_dtype). All sums, statistics and
+ *    probabilities are formed in fp32 and results are rounded once; the 16-bit
+ *    tensor-core paths of attention round the probabilities and their gradients to
+ *    the element type before the products that consume them.
+ *  - Outputs and gradients are overwritten, never accumulated; every result has the
+ *    same bits on every call (no atomics).
+ *  - A wait inside a kernel that runs out of time leaves NaN in the rows concerned
+ *    and sets a status word of the device, read by sdtw_encoder_status.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { SDTW_F32 = 0, SDTW_BF16 = 1, SDTW_F16 = 2 } sdtw_dtype;
+
+/* Layer norm of `rows` rows of C elements (contiguous):
+ *   mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps), y = (x - mean) rstd weight + bias.
+ * x and y have type `dtype`, weight and bias (C,) type `wdtype`; weight may be NULL (ones),
+ * bias may be NULL (zeros). mean and rstd (rows,) fp32 are kept for the backward pass and may be
+ * NULL (both) when there is none. */
+sdtw_status sdtw_layernorm_forward(const void* x, const void* weight, const void* bias, long long rows, int C,
+                                   float eps, int dtype, int wdtype, void* y, float* mean, float* rstd,
+                                   void* stream);
+
+/* Bytes of workspace of sdtw_layernorm_backward; 0 when the arguments are invalid. Pure host
+ * function but for the SM count of the current device. */
+size_t sdtw_layernorm_workspace_bytes(long long rows, int C);
+
+/* Gradients of sdtw_layernorm_forward from dy (like y), x, weight and the kept mean and rstd. dx (like
+ * x), dweight and dbias ((C,), type `wdtype`) may be NULL individually; the workspace is needed for
+ * dweight and dbias only. */
+sdtw_status sdtw_layernorm_backward(const void* dy, const void* x, const void* weight, const float* mean,
+                                    const float* rstd, long long rows, int C, int dtype, int wdtype, void* dx,
+                                    void* dweight, void* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* Rotary positions: the first R features of every head of q (B, N, Hq, D) and k (B, N, Hkv, D) are
+ * turned in pairs, (a, b) -> (a cos - b sin, b cos + a sin), by the angles of their position; the
+ * features from R on are copied. R is even and at most D. interleaved: pairs are neighbours (2i, 2i + 1);
+ * otherwise (i, i + R/2). table is (length, R / 2, 2) fp32: cos and sin of every position and pair
+ * (8-byte aligned). positions is a DEVICE int array (B, N) (pos_stride_b = N) or (N,) (pos_stride_b = 0),
+ * or NULL for 0 .. N-1; a position outside [0, length) gives NaN in the turned features. inverse
+ * non-zero turns backwards: the gradient of the turned tensor. q_stride and k_stride are the strides of
+ * batch, position and head in elements (features are contiguous); outputs are contiguous. k and k_out may be
+ * NULL. Inputs and outputs must not overlap. */
+sdtw_status sdtw_rotary(const void* q, const long long* q_stride, const void* k, const long long* k_stride, int B,
+                        int N, int Hq, int Hkv, int D, int R, const float* table, int length,
+                        const int* positions, long long pos_stride_b, int interleaved, int inverse, int dtype,
+                        void* q_out, void* k_out, void* stream);
+
+/* An attention problem: q (B, N, Hq, D), k and v (B, M, Hkv, D), Hq a multiple of Hkv (query head h reads
+ * key head h / (Hq / Hkv)), D <= 128. Strides of batch, position and head in elements; features are
+ * contiguous.
+ * Batch element b has n_b = q_lengths[b] query rows and m_b = k_lengths[b] keys (DEVICE int arrays (B,),
+ * clamped to [0, N] and [0, M]; NULL: N and M). Row n stands at key n + (m_b - n_b), the last row at the last
+ * key, and sees the keys from window_left before that to window_right after it (-1: without limit), so
+ * window_right = 0 is a causal mask. Rows from n_b on and rows that see no key give 0 and the lse -inf, and
+ * take no part in any gradient. What lies beyond the lengths may hold anything, NaN included. */
+typedef struct {
+    const void *q, *k, *v;
+    long long q_stride[3], k_stride[3], v_stride[3];
+    const int *q_lengths, *k_lengths;
+    int B, N, M, Hq, Hkv, D;
+    int dtype;
+    int window_left, window_right;
+    float scale;   /* of the scores, > 0 */
+} sdtw_attention;
+
+/* Bytes of workspace of sdtw_attention_forward (backward == 0; may be 0) or of sdtw_attention_backward
+ * (backward != 0). 0 also when the arguments are invalid. */
+size_t sdtw_attention_workspace_bytes(const sdtw_attention* a, int backward);
+
+/* out (B, N, Hq, D) contiguous = softmax(scale q k^T over the visible keys) v. For the backward pass, each may
+ * be NULL: out_rest, like out, what the rounding of out left, rounded in turn (16-bit types; 0 for fp32); lse
+ * (B, Hq, N) fp32, the logarithm of the sum of exp(scale q k^T). A few rows over many
+ * keys (a single new sample over a cache) are split over the key axis. */
+sdtw_status sdtw_attention_forward(const sdtw_attention* a, void* out, void* out_rest, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Gradients of sdtw_attention_forward from its out, out_rest (may be NULL: taken as 0, which costs dq and dk
+ * accuracy in 16-bit types) and lse and dout (B, N, Hq, D), all contiguous. dq
+ * (B, N, Hq, D), dk and dv (B, M, Hkv, D) are contiguous; dq may be NULL, and dk and dv may be NULL
+ * together. The probabilities are computed again from lse. */
+sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, const void* out_rest,
+                                    const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* Synchronizes `stream`, then reports (and clears) the current device's status word of the encoder
+ * operators: SDTW_OK, or SDTW_ERR_TIMEOUT when an attention kernel gave up a wait. */
+sdtw_status sdtw_encoder_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
