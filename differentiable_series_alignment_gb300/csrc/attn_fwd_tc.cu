@@ -1,0 +1,381 @@
+// attn_fwd_tc.cu -- attention's forward pass on the tensor cores (bf16 and fp16).
+//
+// One CTA takes two tiles of up to 128 packed rows and walks the visible keys in tiles of
+// 128. Warp 9 issues S_w = Q_w K^T and O_w += P_w V for the two row tiles w in turn, so that the
+// tensor cores work on one tile while the other's softmax runs; warps 0-3 and 4-7 are the two
+// softmaxes, a thread a row; warp 8 feeds a ring of K and V tiles by TMA. Tensor memory
+// holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all 512 columns.
+//
+// The running maximum is renewed only when a row's scores rise by more than 2^8 over it, so
+// that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
+// then at most 2^8, which fp32 sums and 16-bit operands take as well as 1.
+#include "attn_tc.cuh"
+
+namespace sdtw {
+namespace atc {
+namespace {
+
+__device__ int g_status;
+
+constexpr int kThreadsF = 320;
+constexpr float kLazy = 8.f;   // log2 of how far scores may rise over the maximum in use
+
+template <int DP> struct FwdShape {
+    static constexpr uint32_t tile = (DP / 64) * kBox;   // bytes of a row or key tile
+    static constexpr int slots = DP == 128 ? 5 : 10;     // K and V tiles in flight: 160 KB
+    static constexpr uint32_t smem = 2 * tile + slots * tile + 1024;
+};
+
+// fp16 cannot hold small probabilities in full: 2^7 more of them, up to 2^15 in all.
+template <typename T> struct Lift { static constexpr float v = 0.f; };
+template <> struct Lift<__half> { static constexpr float v = 7.f; };
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+{
+    using Sh = FwdShape<DP>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2], s_o[2], s_end;
+    __shared__ uint32_t s_tmem;
+    const sdtw_attention& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int RT = p.tile_rows;
+    // the last rows see the most keys under a causal mask: they start first
+    const int pairs = (p.rows + 2 * RT - 1) / (2 * RT);
+    const int r00 = (pairs - 1 - (int)(blockIdx.x / heads)) * 2 * RT;
+    const RowRange rr(a, b);
+    Tiles t0(rr, r00, min(r00 + RT, p.rows), p.G), t1(rr, r00 + RT, min(r00 + 2 * RT, p.rows), p.G);
+    int T0 = t0.hi == 0 ? t1.lo : t1.hi == 0 ? t0.lo : min(t0.lo, t1.lo), T1 = max(t0.hi, t1.hi);
+    if (p.splits > 1) {   // this CTA's share of the key tiles
+        const int per = (T1 - T0 + p.splits - 1) / p.splits;
+        T0 = min(T0 + per * (int)blockIdx.y, T1);
+        T1 = min(T0 + per, T1);
+        t0.lo = max(t0.lo, T0), t0.hi = min(t0.hi, T1);
+        t1.lo = max(t1.lo, T0), t1.hi = min(t1.hi, T1);
+    }
+    const bool any0 = t0.lo < t0.hi, any1 = t1.lo < t1.hi;
+    if (!any0 && !any1) T1 = T0;
+
+    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t q_img = base, ring = base + 2 * Sh::tile;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&s_q[w]), 1);
+            mbar_init(smem_u32(&s_s[w]), 1);
+            mbar_init(smem_u32(&s_p[w]), 4);
+            mbar_init(smem_u32(&s_o[w]), 1);
+        }
+        for (int e = 0; e < Sh::slots; ++e) {
+            mbar_init(smem_u32(&s_full[e]), 1);
+            mbar_init(smem_u32(&s_empty[e]), 1);
+        }
+        mbar_init(smem_u32(&s_end), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0 && !p.skip) {
+            const uint32_t row_bytes = (uint32_t)RT * 128 * (DP / 64);
+            const int n0 = r00 / p.G;
+            if (any0) {
+                mbar_expect_tx(smem_u32(&s_q[0]), row_bytes);
+                load_rows<DP>(q_img, &maps.q, n0, hk, b, smem_u32(&s_q[0]));
+            }
+            const int total = 2 * (T1 - T0);
+            int issued = 0;
+            for (int i = 0; i < total && ok; ++i) {
+                const int e = i % Sh::slots;
+                if (i >= Sh::slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::slots - 1) & 1), p.wait_ns, &g_status);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&s_full[e]);
+                mbar_expect_tx(bar, Sh::tile);
+                load_keys<DP>(ring + e * Sh::tile, (i & 1) ? &maps.v : &maps.k, (T0 + (i >> 1)) * kKeys, hk, b, bar);
+                issued = i + 1;
+                if (i == 0 && any1) {
+                    mbar_expect_tx(smem_u32(&s_q[1]), row_bytes);
+                    load_rows<DP>(q_img + Sh::tile, &maps.q, n0 + RT / p.G, hk, b, smem_u32(&s_q[1]));
+                }
+            }
+            // no copy may be writing shared memory when the CTA ends
+            bool drained = true;
+            for (int i = max(0, issued - Sh::slots); i < issued; ++i)
+                wait_for(drained, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
+            if (any0) wait_for(drained, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
+            if (any1 && issued > 0) wait_for(drained, smem_u32(&s_q[1]), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const int steps = (a.D + 15) / 16;
+        const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
+        for (int j = T0 - 1; j < T1; ++j) {
+            const int iv = 2 * (j - T0) + 1, ik = iv + 1;   // ring entries of V(j) and K(j + 1)
+            const uint32_t vimg = ring + (uint32_t)((iv + 2 * Sh::slots) % Sh::slots) * Sh::tile;
+            const uint32_t kimg = ring + (uint32_t)(ik % Sh::slots) * Sh::tile;
+            bool have_v = false, have_k = false;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const Tiles& t = w ? t1 : t0;
+                const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128;
+                if (j >= t.lo && j < t.hi) {
+                    if (!have_v) {
+                        wait_warp(ok, smem_u32(&s_full[iv % Sh::slots]), (uint32_t)((iv / Sh::slots) & 1), p.wait_ns, &g_status);
+                        have_v = true;
+                        const int tail = rr.m_b - j * kKeys;
+                        if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(vimg, tail, lane);
+                    }
+                    wait_warp(ok, smem_u32(&s_p[w]), (uint32_t)((j - t.lo) & 1), p.wait_ns, &g_status);
+                    fence_after_sync();
+                    if (ok && lane == 0) {
+#pragma unroll
+                        for (int s = 0; s < kKeys / 16; ++s)
+                            mma_ts(o_col, s_col + s * 8, sdesc_mn(vimg + s * 2048), id_o, (j > t.lo || s > 0) ? 1u : 0u);
+                        if (j == t.hi - 1) mma_commit(smem_u32(&s_o[w]));
+                    }
+                    __syncwarp();
+                }
+                if (j + 1 >= t.lo && j + 1 < t.hi) {
+                    if (!have_k) {
+                        wait_warp(ok, smem_u32(&s_full[ik % Sh::slots]), (uint32_t)((ik / Sh::slots) & 1), p.wait_ns, &g_status);
+                        have_k = true;
+                    }
+                    if (j + 1 == t.lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
+                    fence_after_sync();
+                    if (ok && lane == 0) {
+                        mma_features(s_col, q_img + w * Sh::tile, kimg, steps, id_s);
+                        mma_commit(smem_u32(&s_s[w]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (ok && lane == 0) {
+                if (j >= T0) mma_commit(smem_u32(&s_empty[iv % Sh::slots]));
+                if (j + 1 < T1) mma_commit(smem_u32(&s_empty[ik % Sh::slots]));
+            }
+            __syncwarp();
+        }
+        // every MMA has read its operands and written its result before the CTA ends
+        if (lane == 0) {
+            mma_commit(smem_u32(&s_end));
+            bool fin = true;
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else {
+        const int w = warp >> 2, quarter = warp & 3;
+        const Tiles t = w ? t1 : t0;
+        const int r = r00 + w * RT + quarter * 32 + lane;
+        const bool mine = quarter * 32 + lane < RT && r < p.rows;
+        const int n = mine ? r / p.G : 0, h = hk * p.G + (mine ? r % p.G : 0);
+        const bool live = mine && n < rr.n_b;
+        const int klo = live ? rr.lo(n) : 0, khi = live ? max(klo, rr.hi(n)) : 0;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + 256 + w * 128;
+        const float s2 = a.scale * kLog2e;
+        const int o_cols = (a.D + 31) / 32 * 32;
+        float m = -INFINITY, top = -INFINITY, off = 0.f, l = 0.f;   // maximum in use, its trigger, its base
+        for (int j = t.lo; j < t.hi && ok; ++j) {
+            wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)((j - t.lo) & 1), p.wait_ns, &g_status);
+            if (!ok) break;
+            fence_after_sync();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_col + c * 32, s + c * 32);
+            tmem_wait_ld();
+            const int j0 = j * kKeys;
+            if (__any_sync(0xffffffffu, live && (j0 < klo || j0 + kKeys > khi))) {
+                const int first = klo - j0, count = khi - klo;
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if ((unsigned)(c - first) >= (unsigned)count) s[c] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 128; c += 4)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], s[c + q]);
+            const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (__any_sync(0xffffffffu, live && now > top)) {
+                const float old = m;
+                m = fmaxf(m, now);
+                const float keep = m == old ? 1.f : ex2((old - m) * s2);
+                l *= keep;
+                off = (m == -INFINITY ? 0.f : m * s2) - Lift<T>::v;
+                top = m + kLazy / s2;
+                if (j > t.lo) {
+                    for (int c = 0; c < o_cols; c += 16) {
+                        float o[16];
+                        tmem_ld16(o_col + c, o);
+                        uint32_t u[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(o[q] * keep);
+                        tmem_st16(o_col + c, u);
+                    }
+                }
+            }
+            const unsigned long long mul = pk2(s2, s2), sub = pk2(-off, -off);
+            unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t u[16];
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                    float e[4];
+                    upk2(fma2(pk2(s[c + q], s[c + q + 1]), mul, sub), e[0], e[1]);
+                    upk2(fma2(pk2(s[c + q + 2], s[c + q + 3]), mul, sub), e[2], e[3]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
+                    sum0 = add2(sum0, pk2(e[0], e[1]));
+                    sum1 = add2(sum1, pk2(e[2], e[3]));
+                    u[q / 2] = pack2<T>(e[0], e[1]);
+                    u[q / 2 + 1] = pack2<T>(e[2], e[3]);
+                }
+                tmem_st16(s_col + c / 2, u);
+            }
+            float x, y;
+            upk2(add2(sum0, sum1), x, y);
+            l += x + y;
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_p[w]));
+        }
+        if (t.lo < t.hi) {
+            wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);
+            fence_after_sync();
+        }
+        const bool seen = live && t.lo < t.hi && l != 0.f;
+        const float inv = !ok ? NAN : seen ? 1.f / l : 0.f;
+        const float lse2 = !ok ? NAN : seen ? off + log2f(l) : -INFINITY;
+        const long long row = p.splits > 1 ? (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r
+                                           : ((long long)b * a.N + n) * a.Hq + h;
+        for (int c = 0; c < o_cols; c += 16) {
+            float o[16];
+            if (t.lo < t.hi && ok) {
+                tmem_ld16(o_col + c, o);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = 0.f;
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int q = 0; q < 16; q += 8) {
+                if (c + q >= a.D) continue;
+                const long long at = row * a.D + c + q;
+                if (!seen && ok) {
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) o[q + z] = 0.f;   // what a row that sees nothing accumulated
+                }
+                if (p.splits > 1) {
+#pragma unroll
+                    for (int z = 0; z < 8; z += 4)
+                        *reinterpret_cast<float4*>(p.part_o + at + z) =
+                            make_float4(o[q + z] * inv, o[q + z + 1] * inv, o[q + z + 2] * inv, o[q + z + 3] * inv);
+                } else {
+                    store8<T>(static_cast<T*>(p.out) + at, p.out_rest ? static_cast<T*>(p.out_rest) + at : nullptr, o + q, inv);
+                }
+            }
+        }
+        if (mine) {
+            if (p.splits > 1) p.part_lse[row] = lse2 * kLn2;
+            else if (p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int DP> cudaError_t run_fwd(const AttnParams& p, const Maps& m, cudaStream_t s)
+{
+    auto kern = attn_fwd_tc_kernel<T, DP>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdShape<DP>::smem);
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = (unsigned)((p.rows + 2 * p.tile_rows - 1) / (2 * p.tile_rows));
+    kern<<<dim3(pairs * p.a.B * p.a.Hkv, p.splits), kThreadsF, FwdShape<DP>::smem, s>>>(p, m);
+    return cudaGetLastError();
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box)
+{
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    const EncodeFn fn = encode_fn();
+    return fn && fn(m, dtype == SDTW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                    const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A dimension of one element is never stepped along: its stride need only be valid.
+cuuint64_t step(long long stride, int size) { return size > 1 ? (cuuint64_t)stride * 2 : 16; }
+
+}  // namespace
+
+bool map_rows(CUtensorMap* m, const void* p, const long long* stride, const sdtw_attention& a, int G, int RT)
+{
+    const cuuint64_t dims[5] = {(cuuint64_t)a.D, (cuuint64_t)G, (cuuint64_t)a.Hkv, (cuuint64_t)a.N, (cuuint64_t)a.B};
+    const cuuint64_t st[4] = {step(stride[2], G), step(stride[2] * G, a.Hkv), step(stride[1], a.N), step(stride[0], a.B)};
+    const cuuint32_t box[5] = {64, (cuuint32_t)G, 1, (cuuint32_t)(RT / G), 1};
+    return encode(m, a.dtype, 5, p, dims, st, box);
+}
+
+bool map_keys(CUtensorMap* m, const void* p, const long long* stride, const sdtw_attention& a)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.M, (cuuint64_t)a.Hkv, (cuuint64_t)a.B};
+    const cuuint64_t st[3] = {step(stride[1], a.M), step(stride[2], a.Hkv), step(stride[0], a.B)};
+    const cuuint32_t box[4] = {64, kKeys, 1, 1};
+    return encode(m, a.dtype, 4, p, dims, st, box);
+}
+
+}  // namespace atc
+
+cudaError_t launch_attn_forward_tc(const AttnParams& p, cudaStream_t s)
+{
+    atc::Maps m{};
+    const sdtw_attention& a = p.a;
+    if (!atc::map_rows(&m.q, a.q, a.q_stride, a, p.G, p.tile_rows) || !atc::map_keys(&m.k, a.k, a.k_stride, a) ||
+        !atc::map_keys(&m.v, a.v, a.v_stride, a))
+        return cudaErrorInvalidValue;
+    if (a.dtype == SDTW_BF16)
+        return a.D <= 64 ? atc::run_fwd<__nv_bfloat16, 64>(p, m, s) : atc::run_fwd<__nv_bfloat16, 128>(p, m, s);
+    return a.D <= 64 ? atc::run_fwd<__half, 64>(p, m, s) : atc::run_fwd<__half, 128>(p, m, s);
+}
+
+cudaError_t attn_forward_take_status(int* out, cudaStream_t s)
+{
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, atc::g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(atc::g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
+
+}  // namespace sdtw

@@ -1,0 +1,204 @@
+// attn_tc.cuh -- what the tensor-core attention kernels share: tensor maps of packed
+// rows and of keys, operand descriptors, bounded waits, and packed 16-bit conversions.
+//
+// Operands sit in shared memory as TMA writes them: boxes of 64 features (128 bytes,
+// 128-byte swizzle) by up to 128 rows, 16 KB apart. One image serves both ways round: as a
+// K-major operand of a product over the features, and as an MN-major operand (features
+// along N) of a product over the rows. Probabilities are A operands from tensor memory.
+#pragma once
+
+#include <cuda.h>
+
+#include "encoder.h"
+#include "tc.cuh"
+
+namespace sdtw {
+namespace atc {
+
+using namespace tc;
+
+constexpr int kKeys = 128;            // keys per tile
+constexpr uint32_t kBox = 128 * 128;  // bytes of a 128-row box of 64 16-bit features
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---- instruction and operand descriptors (kind::f16, fp32 accumulation)
+template <typename T> struct Fmt;
+template <> struct Fmt<__half> { static constexpr uint32_t v = 0; };
+template <> struct Fmt<__nv_bfloat16> { static constexpr uint32_t v = 1; };
+
+template <typename T> __device__ __forceinline__ uint32_t idesc(int M, int N, bool b_mn) {
+    return (1u << 4) | (Fmt<T>::v << 7) | (Fmt<T>::v << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// MN-major, 128-byte swizzle: 64-element groups along N a box apart, 8-row groups along
+// K 1 KiB apart. sdesc (tc.cuh) is the K-major form of the same image.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(kBox >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    mma_bf16(d, a, b, id, acc);   // kind::f16: the types are in the instruction descriptor
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+
+// D[128 x N] = A[128 x features] B[N x features]^T over `steps` steps of 16 features, both
+// K-major images; N of id.
+__device__ __forceinline__ void mma_features(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t id) {
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t o = (uint32_t)(s >> 2) * kBox + (uint32_t)(s & 3) * 32;
+        mma_ss(d, sdesc(a + o), sdesc(b + o), id, s > 0 ? 1u : 0u);
+    }
+}
+
+// ---- TMA
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4,
+                                     uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+template <int DP>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, int n0, int hk, int b, uint32_t bar) {
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) tma5(dst + c * kBox, m, c * 64, 0, hk, n0, b, bar);
+}
+template <int DP>
+__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* m, int j0, int hk, int b, uint32_t bar) {
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) tma4(dst + c * kBox, m, c * 64, j0, hk, b, bar);
+}
+
+// One warp clears rows [from, 128) of an image that a product over its rows is about to
+// read: what lies beyond a sequence's length may be NaN, and 0 * NaN is not 0.
+template <int DP> __device__ __forceinline__ void clear_rows(uint32_t img, int from, int lane) {
+    for (int c = 0; c < DP / 64; ++c)
+        for (uint32_t o = (uint32_t)from * 128 + lane * 16; o < kBox; o += 512)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(img + c * kBox + o), "r"(0) : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// ---- waits: bounded; after one that ran out the caller waits no more and the kernel
+// ends with NaN in its rows and the status word set.
+__device__ __forceinline__ void wait_for(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, int* status) {
+    if (!ok || mbar_test(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_test(bar, parity)) {
+        if (global_ns() - t0 > limit_ns) {
+            atomicOr(status, kStatusTimeout);
+            ok = false;
+            return;
+        }
+    }
+}
+
+// The same by a whole warp, which learns one answer.
+__device__ __forceinline__ void wait_warp(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, int* status) {
+    wait_for(ok, bar, parity, limit_ns, status);
+    ok = __all_sync(0xffffffffu, ok);
+}
+
+// ---- tensor memory
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two fp32 values rounded to 16 bits each, lo in the low half
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Writes 8 consecutive features of a result row (16 bytes), and what their rounding left.
+template <typename T> __device__ __forceinline__ void store8(T* out, T* rest, const float* v, float mul) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = pack2<T>(v[2 * q] * mul, v[2 * q + 1] * mul);
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (rest) {
+        const T* r = reinterpret_cast<const T*>(w);
+        uint32_t z[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            z[q] = pack2<T>(v[2 * q] * mul - to_f32(r[2 * q]), v[2 * q + 1] * mul - to_f32(r[2 * q + 1]));
+        *reinterpret_cast<uint4*>(rest) = make_uint4(z[0], z[1], z[2], z[3]);
+    }
+}
+
+// Key tiles [lo, hi) that the packed rows [r0, r1) see.
+struct Tiles {
+    int lo, hi;
+    __device__ __forceinline__ Tiles(const RowRange& rr, int r0, int r1, int G) : lo(0), hi(0) {
+        const int n0 = r0 / G, n1 = min((r1 - 1) / G, rr.n_b - 1);
+        if (r0 >= r1 || n0 > n1) return;
+        const int a = rr.lo(n0), b = rr.hi(n1);
+        if (a >= b) return;
+        lo = a / kKeys;
+        hi = (b + kKeys - 1) / kKeys;
+    }
+};
+
+// ---- host: tensor maps
+struct Maps {
+    CUtensorMap q, k, v, dout;
+};
+
+// Packed rows of a (B, N, Hq, D) tensor: (features, head in group, key head, position, batch).
+// RT rows per load.
+bool map_rows(CUtensorMap* m, const void* p, const long long* stride, const sdtw_attention& a, int G, int RT);
+// Keys of a (B, M, Hkv, D) tensor: (features, position, key head, batch).
+bool map_keys(CUtensorMap* m, const void* p, const long long* stride, const sdtw_attention& a);
+
+}  // namespace atc
+}  // namespace sdtw

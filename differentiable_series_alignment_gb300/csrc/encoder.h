@@ -84,7 +84,15 @@ struct AttnParams {
     int grad_shift;
     float* row_delta;         // [B][Hkv][rows_pad]: sum_d do * o
     int rows_pad;             // rows rounded up to 128
+    // tensor-core kernels
+    bool tc;                  // taken by them (attn_tc_fits)
+    int tile_rows;            // packed rows of a tile: whole positions, up to 128
+    unsigned long long wait_ns;
+    int skip;                 // test hook: nothing is loaded, so that every wait runs out
 };
+bool attn_tc_fits(const sdtw_attention& a);
+cudaError_t launch_attn_forward_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t attn_forward_take_status(int* out, cudaStream_t s);
 cudaError_t launch_attn_forward_simt(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_rowinfo(const AttnParams& p, cudaStream_t s);

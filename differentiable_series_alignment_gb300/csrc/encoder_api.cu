@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "encoder.h"
+#include "kernels.h"
 
 using namespace sdtw;
 
@@ -75,8 +76,11 @@ AttnParams attn_params(const sdtw_attention* a)
     p.G = a->Hq / a->Hkv;
     p.rows = a->N * p.G;
     p.rows_pad = (p.rows + 127) / 128 * 128;
-    p.splits = key_splits(p, 64, 64, 2);
+    p.tc = attn_tc_fits(*a);
+    p.tile_rows = p.tc ? 128 / p.G * p.G : 64;
+    p.splits = p.tc ? key_splits(p, 2 * p.tile_rows, 128, 4) : key_splits(p, 64, 64, 2);
     p.grad_shift = 32;
+    p.wait_ns = debug_wait_ns();
     return p;
 }
 
@@ -99,6 +103,28 @@ size_t carve_backward(AttnParams& p, void* ws)
     p.row_delta = reinterpret_cast<float*>(base + rows);
     return 2 * rows;
 }
+
+}  // namespace
+
+namespace sdtw {
+
+// The tensor-core kernels take 16-bit elements whose rows TMA can load: 16-byte
+// addresses and strides, none of them 0 (broadcast), and a group of heads within one tile.
+bool attn_tc_fits(const sdtw_attention& a)
+{
+    if (a.dtype == SDTW_F32 || a.D % 8 || a.Hq / a.Hkv > 128) return false;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v)) return false;
+    const int qs[3] = {a.B, a.N, a.Hq}, ks[3] = {a.B, a.M, a.Hkv};
+    for (int i = 0; i < 3; ++i) {
+        if (qs[i] > 1 && (a.q_stride[i] <= 0 || a.q_stride[i] % 8)) return false;
+        if (ks[i] > 1 && (a.k_stride[i] <= 0 || a.k_stride[i] % 8 || a.v_stride[i] <= 0 || a.v_stride[i] % 8)) return false;
+    }
+    return true;
+}
+
+}  // namespace sdtw
+
+namespace {
 
 #define ENC_CUDA(call)                                 \
     do {                                               \
@@ -187,7 +213,8 @@ sdtw_status sdtw_attention_forward(const sdtw_attention* a, void* out, void* out
     if (sdtw_status s = check_ws(ws, ws_bytes, carve_forward(p, ws))) return s;
     p.out = out, p.out_rest = out_rest, p.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    ENC_CUDA(launch_attn_forward_simt(p, st));
+    if (p.tc) p.skip = debug_take_skip_publish();
+    ENC_CUDA(p.tc ? launch_attn_forward_tc(p, st) : launch_attn_forward_simt(p, st));
     if (p.splits > 1) ENC_CUDA(launch_attn_combine(p, st));
     return SDTW_OK;
 }
@@ -210,8 +237,9 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
 
 sdtw_status sdtw_encoder_status(void* stream)
 {
-    ENC_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
-    return SDTW_OK;
+    int word = 0;
+    ENC_CUDA(attn_forward_take_status(&word, static_cast<cudaStream_t>(stream)));
+    return word ? SDTW_ERR_TIMEOUT : SDTW_OK;
 }
 
 }  // extern "C"

@@ -426,6 +426,21 @@ def test_attention_on_another_stream_and_in_a_graph(package):
     assert package.sdtw_encoder_status() == 0
 
 
+def test_a_wait_that_runs_out_is_reported(package):
+    """Nothing is loaded (a test hook; no fault is involved), so every wait of the kernel runs out."""
+    gen = generator(17)
+    q, k, v = (randn(gen, 1, 200, 2, 64, dtype=BF16) for _ in range(3))
+    want = package.attention(q, k, v)
+    try:
+        package.sdtw_debug_set_wait(0.02, skip_publish=True)
+        assert torch.isnan(package.attention(q, k, v)).all()
+        assert package.sdtw_encoder_status() == 7                  # SDTW_ERR_TIMEOUT
+    finally:
+        package.sdtw_debug_set_wait(0.0, skip_publish=False)
+    assert package.sdtw_encoder_status() == 0
+    assert torch.equal(package.attention(q, k, v), want)
+
+
 def test_empty_inputs_give_empty_or_zero_results(package):
     q = torch.randn(2, 3, 4, 16, device="cuda", requires_grad=True)
     k = torch.randn(2, 0, 2, 16, device="cuda", requires_grad=True)
