@@ -279,33 +279,74 @@ template <typename T> __global__ void __launch_bounds__(128) attn_combine_kernel
 // difference dP - delta cancels where one key has most of a row, so o is taken with what
 // its rounding to 16 bits left; with the rounded o alone dq and dk were up to 5 times
 // further from their 64-bit values than a plain fp32 pass on short fp16 sequences.
-// One warp per packed row, in packed order and padded to whole tiles.
-template <typename T> __global__ void __launch_bounds__(256) attn_rowinfo_kernel(const AttnParams p)
+// Eight lanes per packed row, 32 rows per CTA, in packed order and padded to whole tiles;
+// VEC elements per load. For fp16 on the tensor cores also the largest squared norm of do
+// of the CTA's rows, and in further CTAs of v of 32 keys.
+template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowinfo_kernel(const AttnParams p)
 {
+    __shared__ float most[8];
     const sdtw_attention& a = p.a;
-    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (at >= (long long)a.B * a.Hkv * p.rows_pad) return;
-    const int r = (int)(at % p.rows_pad);
-    const int hk = (int)(at / p.rows_pad % a.Hkv), b = (int)(at / p.rows_pad / a.Hkv);
-    const int n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
-    const int n = r / p.G, h = hk * p.G + r % p.G;
-    float lse = -INFINITY, delta = 0.f;
-    if (r < p.rows && n < n_b) {
-        lse = p.lse_in[((long long)b * a.Hq + h) * a.N + n];
-        const long long o = (((long long)b * a.N + n) * a.Hq + h) * a.D;
-        const T* x = static_cast<const T*>(p.out) + o;
-        const T* rest = p.out_rest ? static_cast<const T*>(p.out_rest) + o : nullptr;
-        const T* g = static_cast<const T*>(p.dout) + o;
-        for (int d = lane; d < a.D; d += 32)
-            delta = fmaf(to_f32(x[d]) + (rest ? to_f32(rest[d]) : 0.f), to_f32(g[d]), delta);
+    const int sub = threadIdx.x & 7;
+    const long long row_ctas = (long long)a.B * a.Hkv * (p.rows_pad / 32);
+    float norm = 0.f;
+    using P = Pack<T, VEC>;
+    if (blockIdx.x < row_ctas) {
+        const long long at = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+        const int r = (int)(at % p.rows_pad);
+        const int hk = (int)(at / p.rows_pad % a.Hkv), b = (int)(at / p.rows_pad / a.Hkv);
+        const int n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
+        const int n = r / p.G, h = hk * p.G + r % p.G;
+        float lse = -INFINITY, delta = 0.f;
+        if (r < p.rows && n < n_b) {
+            lse = p.lse_in[((long long)b * a.Hq + h) * a.N + n];
+            const long long o = (((long long)b * a.N + n) * a.Hq + h) * a.D;
+            const T* x = static_cast<const T*>(p.out) + o;
+            const T* rest = p.out_rest ? static_cast<const T*>(p.out_rest) + o : nullptr;
+            const T* g = static_cast<const T*>(p.dout) + o;
+            for (int d = sub * VEC; d < a.D; d += 8 * VEC) {
+                const P xv = *reinterpret_cast<const P*>(x + d), gv = *reinterpret_cast<const P*>(g + d);
+                P rv;
+                if (rest) rv = *reinterpret_cast<const P*>(rest + d);
 #pragma unroll
-        for (int q = 16; q > 0; q >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, q);
+                for (int e = 0; e < VEC; ++e) {
+                    const float gf = to_f32(gv.e[e]);
+                    delta = fmaf(to_f32(xv.e[e]) + (rest ? to_f32(rv.e[e]) : 0.f), gf, delta);
+                    norm = fmaf(gf, gf, norm);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 4; q > 0; q >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, q);
+        if (sub == 0) {
+            const bool none = lse == -INFINITY;
+            p.row_lse[at] = none ? INFINITY : lse * kLog2e - (float)p.grad_shift;
+            p.row_delta[at] = none ? 0.f : delta;
+        }
+    } else {
+        const int per = (a.M + 31) / 32;
+        const int c = (int)(blockIdx.x - row_ctas), bh = c / per, b = bh / a.Hkv;
+        const int m_b = a.k_lengths ? min(max(a.k_lengths[b], 0), a.M) : a.M;
+        const int j = c % per * 32 + (threadIdx.x >> 3);
+        if (j < m_b) {
+            const T* v = static_cast<const T*>(a.v) + b * a.v_stride[0] + j * a.v_stride[1] + bh % a.Hkv * a.v_stride[2];
+            for (int d = sub * VEC; d < a.D; d += 8 * VEC) {
+                const P vv = *reinterpret_cast<const P*>(v + d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) norm = fmaf(to_f32(vv.e[e]), to_f32(vv.e[e]), norm);
+            }
+        }
     }
-    if (lane == 0) {
-        const bool none = lse == -INFINITY;
-        p.row_lse[at] = none ? INFINITY : lse * kLog2e - (float)p.grad_shift;
-        p.row_delta[at] = none ? 0.f : delta;
+    if (!p.norm_rows) return;
+#pragma unroll
+    for (int q = 4; q > 0; q >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, q);
+#pragma unroll
+    for (int q = 16; q > 4; q >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xffffffffu, norm, q));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = norm;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) norm = fmaxf(norm, most[w]);
+        if (blockIdx.x < row_ctas) p.norm_rows[blockIdx.x] = norm;
+        else p.norm_keys[blockIdx.x - row_ctas] = norm;
     }
 }
 
@@ -546,13 +587,23 @@ cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <typename T> static cudaError_t rowinfo_typed(const AttnParams& p, cudaStream_t s)
+{
+    long long grid = (long long)p.a.B * p.a.Hkv * (p.rows_pad / 32);
+    if (p.norm_rows) grid += (long long)p.a.B * p.a.Hkv * ((p.a.M + 31) / 32);
+    constexpr int VEC = 16 / sizeof(T);
+    bool packed = p.a.D % VEC == 0 && aligned16(p.out) && aligned16(p.out_rest) && aligned16(p.dout);
+    if (p.norm_rows) packed = packed && p.tc;   // whose v has 16-byte rows
+    if (packed) attn_rowinfo_kernel<T, VEC><<<(unsigned)grid, 256, 0, s>>>(p);
+    else attn_rowinfo_kernel<T, 1><<<(unsigned)grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_rowinfo(const AttnParams& p, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(((long long)p.a.B * p.a.Hkv * p.rows_pad + 7) / 8);
-    if (p.a.dtype == SDTW_F32) attn_rowinfo_kernel<float><<<grid, 256, 0, s>>>(p);
-    else if (p.a.dtype == SDTW_BF16) attn_rowinfo_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else attn_rowinfo_kernel<__half><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.a.dtype == SDTW_F32) return rowinfo_typed<float>(p, s);
+    if (p.a.dtype == SDTW_BF16) return rowinfo_typed<__nv_bfloat16>(p, s);
+    return rowinfo_typed<__half>(p, s);
 }
 
 }  // namespace sdtw

@@ -1,0 +1,560 @@
+// attn_bwd_tc.cu -- attention's backward pass on the tensor cores (bf16 and fp16).
+//
+// Two kernels, each computing P = exp(S - lse) and dS = P (dP - delta) again from q, k, v, do
+// and the row's lse and delta:
+//   attn_dkv_tc_kernel: a CTA holds 128 keys and walks the packed rows that see them;
+//     S^T = K Q^T and dP^T = V dO^T go to tensor memory, P^T and dS^T come back there as
+//     16-bit A operands, dV += P^T dO and dK += dS^T Q;
+//   attn_dq_tc_kernel: a CTA holds a tile of packed rows and walks their keys;
+//     S = Q K^T, dP = dO V^T, dQ += dS K.
+// That is 7 products where one kernel would need 5, but no result is summed across CTAs:
+// no atomics, no partial dQ in memory, the same bits every time. The gradients of heads
+// that share keys are summed in the accumulator, as rows of one problem.
+// Warps 0-7 turn scores into probabilities (two warpgroups, half of the columns each),
+// warp 8 loads by TMA, warp 9 issues the products. While the tensor cores run dV and the next
+// S^T, the warps compute dS^T; while they run dK and the next dP^T, the next P^T.
+#include "attn_tc.cuh"
+
+namespace sdtw {
+namespace atc {
+namespace {
+
+__device__ int g_status;
+
+constexpr int kThreadsB = 320;
+constexpr int kWork = 256;   // threads of warps 0-7
+
+template <int DP> struct BwdShape {
+    static constexpr uint32_t tile = (DP / 64) * kBox;
+    static constexpr int stages = DP == 128 ? 2 : 4;   // dkv: (Q, dO) pairs in flight, 128 KB
+    static constexpr int slots = DP == 128 ? 5 : 10;   // dq: K and V tiles in flight, 160 KB
+    static constexpr uint32_t smem_dkv = 2 * tile + 2 * stages * tile + 1024;
+    static constexpr uint32_t smem_dq = 2 * tile + slots * tile + 1024;
+};
+
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// fp16 operands: dS is scaled by the power of two that keeps |dP - delta| <= 2 |do| |v| below 1
+// for the largest row of do and of v, so that neither small upstream gradients nor large ones
+// leave the format's range. bf16 has the range of fp32: 1.
+template <typename T> __device__ __forceinline__ float grad_scale(const AttnParams&, int, int) { return 1.f; }
+template <> __device__ __forceinline__ float grad_scale<__half>(const AttnParams& p, int bh, int lane) {
+    const int nr = p.rows_pad / 32, nk = (p.a.M + 31) / 32;
+    float g = 0.f, v = 0.f;
+    for (int i = lane; i < nr; i += 32) g = fmaxf(g, p.norm_rows[(long long)bh * nr + i]);
+    for (int i = lane; i < nk; i += 32) v = fmaxf(v, p.norm_keys[(long long)bh * nk + i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    }
+    const float most = 2.f * sqrtf(g) * sqrtf(v);
+    if (!(most > 0.f) || isinf(most)) return 1.f;
+    int e;
+    frexpf(most, &e);
+    return ldexpf(1.f, -min(max(e, -100), 100));
+}
+
+// A row of 64 probabilities' or gradients' 16-bit pairs into 32 tensor-memory columns.
+__device__ __forceinline__ void st64(uint32_t col, const uint32_t* u) {
+    tmem_st16(col, u);
+    tmem_st16(col + 16, u + 16);
+}
+
+// dV/dK/dQ += A[128 x 128 from tensor memory] B, B an image read over its rows. A's columns 0-63
+// are at a, 64-127 at a + 64 (each half lies over the half of the scores it came from).
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t img, uint32_t id, bool first) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, sdesc_mn(img + s * 2048), id, (!first || s > 0) ? 1u : 0u);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+{
+    using Sh = BwdShape<DP>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint64_t s_kv, s_full[Sh::stages], s_empty[Sh::stages], s_s, s_p, s_dp, s_ds, s_end;
+    __shared__ uint32_t s_tmem;
+    __shared__ __align__(16) float s_row[2][2][128];   // -lse and -delta of the tile's rows, two tiles
+    const sdtw_attention& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int RT = p.tile_rows, G = p.G;
+    const int j0 = (int)(blockIdx.x / heads) * kKeys;   // the first keys are seen by the most rows
+    const RowRange rr(a, b);
+    const int j_last = min(j0 + kKeys, rr.m_b) - 1;
+    int t_lo = 0, t_hi = 0;   // tiles of packed rows that see a key of this CTA
+    if (j0 <= j_last) {
+        const int lo = rr.row_lo(j0), hi = rr.row_hi(j_last);
+        if (lo < hi) {
+            t_lo = lo * G / RT;
+            t_hi = (hi * G + RT - 1) / RT;
+        }
+    }
+    const int tiles = t_hi - t_lo;
+
+    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t k_img = base, v_img = base + Sh::tile, ring = base + 2 * Sh::tile;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&s_kv), 1);
+        for (int e = 0; e < Sh::stages; ++e) {
+            mbar_init(smem_u32(&s_full[e]), 1);
+            mbar_init(smem_u32(&s_empty[e]), 1);
+        }
+        mbar_init(smem_u32(&s_s), 1);
+        mbar_init(smem_u32(&s_p), 8);
+        mbar_init(smem_u32(&s_dp), 1);
+        mbar_init(smem_u32(&s_ds), 8);
+        mbar_init(smem_u32(&s_end), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (RT < 128 && warp < 8)   // rows that no load writes, but the products over the rows read
+        for (int i = warp; i < 2 * Sh::stages; i += 8) clear_rows<DP>(ring + i * Sh::tile, RT, lane);
+    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    const uint32_t c_s = tmem, c_dp = tmem + 128, c_dv = tmem + 256, c_dk = tmem + 384;
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0 && tiles > 0) {
+            mbar_expect_tx(smem_u32(&s_kv), 2 * Sh::tile);
+            load_keys<DP>(k_img, &maps.k, j0, hk, b, smem_u32(&s_kv));
+            load_keys<DP>(v_img, &maps.v, j0, hk, b, smem_u32(&s_kv));
+            const uint32_t bytes = 2u * RT * 128 * (DP / 64);
+            int issued = 0;
+            for (int i = 0; i < tiles && ok; ++i) {
+                const int e = i % Sh::stages;
+                if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, &g_status);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&s_full[e]), dst = ring + e * 2 * Sh::tile;
+                const int n0 = (t_lo + i) * (RT / G);
+                mbar_expect_tx(bar, bytes);
+                load_rows<DP>(dst, &maps.q, n0, hk, b, bar);
+                load_rows<DP>(dst + Sh::tile, &maps.dout, n0, hk, b, bar);
+                issued = i + 1;
+            }
+            bool drained = true;   // no copy may be writing shared memory when the CTA ends
+            for (int i = max(0, issued - Sh::stages); i < issued; ++i)
+                wait_for(drained, smem_u32(&s_full[i % Sh::stages]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, &g_status);
+            wait_for(drained, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const int steps = (a.D + 15) / 16;
+        const uint32_t id_s = idesc<T>(128, 128, false), id_o = idesc<T>(128, steps * 16, true);
+        const int rows_b = rr.n_b * G;   // rows from here on hold anything
+        if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
+        for (int i = -1; i < tiles; ++i) {
+            const uint32_t q_img = ring + (uint32_t)(i < 0 ? 0 : i % Sh::stages) * 2 * Sh::tile, g_img = q_img + Sh::tile;
+            const int nx = i + 1;
+            const uint32_t q_nxt = ring + (uint32_t)(nx % Sh::stages) * 2 * Sh::tile, g_nxt = q_nxt + Sh::tile;
+            if (i >= 0) {
+                wait_warp(ok, smem_u32(&s_p), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                fence_after_sync();
+                if (ok && lane == 0) mma_rows(c_dv, c_s, g_img, id_o, i == 0);
+                __syncwarp();
+            }
+            if (nx < tiles) {
+                wait_warp(ok, smem_u32(&s_full[nx % Sh::stages]), (uint32_t)((nx / Sh::stages) & 1), p.wait_ns, &g_status);
+                const int tail = rows_b - (t_lo + nx) * RT;
+                if (ok && tail < RT && rr.n_b < a.N) {
+                    clear_rows<DP>(q_nxt, tail, lane);
+                    clear_rows<DP>(g_nxt, tail, lane);
+                }
+                fence_after_sync();
+                if (ok && lane == 0) {
+                    mma_features(c_s, k_img, q_nxt, steps, id_s);
+                    mma_commit(smem_u32(&s_s));
+                }
+                __syncwarp();
+            }
+            if (i >= 0) {
+                wait_warp(ok, smem_u32(&s_ds), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                fence_after_sync();
+                if (ok && lane == 0) {
+                    mma_rows(c_dk, c_dp, q_img, id_o, i == 0);
+                    mma_commit(smem_u32(&s_empty[i % Sh::stages]));
+                }
+                __syncwarp();
+            }
+            if (nx < tiles && ok && lane == 0) {
+                mma_features(c_dp, v_img, g_nxt, steps, id_s);
+                mma_commit(smem_u32(&s_dp));
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            mma_commit(smem_u32(&s_end));
+            bool fin = true;
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2, quarter = warp & 3;
+        const int key = j0 + quarter * 32 + lane;
+        const bool live = key < rr.m_b;
+        // packed rows that see this key
+        const int rlo = live ? rr.row_lo(key) * G : 0, rhi = live ? max(rlo, rr.row_hi(key) * G) : 0;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const float s2 = a.scale * kLog2e;
+        const float gs = grad_scale<T>(p, bh, lane);
+        const unsigned long long mul = pk2(s2, s2), gmul = pk2(gs, gs);
+        const long long info = (long long)bh * p.rows_pad;
+        const int mine = threadIdx.x & 127, which = threadIdx.x >> 7;
+        // this thread's entry of the next tile's row values, one tile ahead
+        auto fetch = [&](int i) -> float {
+            const int r = (t_lo + i) * RT + mine;
+            const bool valid = i < tiles && mine < RT && r < p.rows;
+            if (which) return valid ? -gs * p.row_delta[info + r] : 0.f;
+            return valid ? -p.row_lse[info + r] : -INFINITY;
+        };
+        s_row[0][which][mine] = fetch(0);
+        float next = fetch(1);
+        // a wait that ran out does not end the loop: the other warps would wait at the barrier
+        for (int i = 0; i < tiles; ++i) {
+            work_sync();
+            s_row[(i + 1) & 1][which][mine] = next;
+            next = fetch(i + 2);
+            const float4* lse4 = reinterpret_cast<const float4*>(s_row[i & 1][0] + half * 64);
+            const float4* del4 = reinterpret_cast<const float4*>(s_row[i & 1][1] + half * 64);
+            const int r0 = (t_lo + i) * RT + half * 64;
+            wait_warp(ok, smem_u32(&s_s), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            fence_after_sync();
+            float s[64];
+            tmem_ld32_nowait(c_s + lanes + half * 64, s);
+            tmem_ld32_nowait(c_s + lanes + half * 64 + 32, s + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                const float4 l = lse4[c / 4];
+                upk2(fma2(pk2(s[c], s[c + 1]), mul, pk2(l.x, l.y)), s[c], s[c + 1]);
+                upk2(fma2(pk2(s[c + 2], s[c + 3]), mul, pk2(l.z, l.w)), s[c + 2], s[c + 3]);
+            }
+            if (__any_sync(0xffffffffu, live && (r0 < rlo || r0 + 64 > rhi))) {
+                const int first = rlo - r0, count = rhi - rlo;
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if ((unsigned)(c - first) >= (unsigned)count) s[c] = -INFINITY;
+            }
+            uint32_t u[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                s[c] = ex2(s[c]);
+                s[c + 1] = ex2(s[c + 1]);
+                u[c / 2] = pack2<T>(s[c], s[c + 1]);
+            }
+            st64(c_s + lanes + half * 64, u);
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_p));
+
+            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            fence_after_sync();
+            float d[64];
+            tmem_ld32_nowait(c_dp + lanes + half * 64, d);
+            tmem_ld32_nowait(c_dp + lanes + half * 64 + 32, d + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                const float4 e = del4[c / 4];
+                float x, y;
+                upk2(mul2(pk2(s[c], s[c + 1]), fma2(pk2(d[c], d[c + 1]), gmul, pk2(e.x, e.y))), x, y);
+                u[c / 2] = pack2<T>(x, y);
+                upk2(mul2(pk2(s[c + 2], s[c + 3]), fma2(pk2(d[c + 2], d[c + 3]), gmul, pk2(e.z, e.w))), x, y);
+                u[c / 2 + 1] = pack2<T>(x, y);
+            }
+            st64(c_dp + lanes + half * 64, u);
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_ds));
+        }
+        if (tiles > 0) {
+            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            fence_after_sync();
+        }
+        // warps 0-3 write dV, 4-7 dK, a thread a key
+        const float unlift = ex2(-(float)p.grad_shift), more = half ? a.scale / gs : 1.f;
+        T* out = static_cast<T*>(half ? p.dk : p.dv) + (((long long)b * a.M + key) * a.Hkv + hk) * a.D;
+        const bool some = tiles > 0 && live;
+        for (int c = 0; c < (a.D + 31) / 32 * 32; c += 16) {
+            float o[16];
+            if (tiles > 0 && ok) {
+                tmem_ld16((half ? c_dk : c_dv) + lanes + c, o);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = 0.f;
+            }
+            if (key >= a.M) continue;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = !ok ? NAN : some ? o[q] * unlift : 0.f;
+#pragma unroll
+            for (int q = 0; q < 16; q += 8)
+                if (c + q < a.D) store8<T>(out + c + q, nullptr, o + q, more);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+{
+    using Sh = BwdShape<DP>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_dp, s_ds, s_end;
+    __shared__ uint32_t s_tmem;
+    const sdtw_attention& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int RT = p.tile_rows, G = p.G;
+    const int row_tiles = (p.rows + RT - 1) / RT;
+    const int r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * RT;
+    const RowRange rr(a, b);
+    const Tiles t(rr, r0, min(r0 + RT, p.rows), G);
+    const int tiles = t.hi - t.lo;
+
+    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t q_img = base, g_img = base + Sh::tile, ring = base + 2 * Sh::tile;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&s_q), 1);
+        for (int e = 0; e < Sh::slots; ++e) {
+            mbar_init(smem_u32(&s_full[e]), 1);
+            mbar_init(smem_u32(&s_empty[e]), 1);
+        }
+        mbar_init(smem_u32(&s_s[0]), 1);
+        mbar_init(smem_u32(&s_s[1]), 1);
+        mbar_init(smem_u32(&s_dp), 1);
+        mbar_init(smem_u32(&s_ds), 8);
+        mbar_init(smem_u32(&s_end), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    const uint32_t c_s = tmem, c_dp = tmem + 256, c_dq = tmem + 384;   // two S tiles
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0 && tiles > 0) {
+            mbar_expect_tx(smem_u32(&s_q), 2u * RT * 128 * (DP / 64));
+            load_rows<DP>(q_img, &maps.q, r0 / G, hk, b, smem_u32(&s_q));
+            load_rows<DP>(g_img, &maps.dout, r0 / G, hk, b, smem_u32(&s_q));
+            int issued = 0;
+            for (int i = 0; i < 2 * tiles && ok; ++i) {
+                const int e = i % Sh::slots;
+                if (i >= Sh::slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::slots - 1) & 1), p.wait_ns, &g_status);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&s_full[e]);
+                mbar_expect_tx(bar, Sh::tile);
+                load_keys<DP>(ring + e * Sh::tile, (i & 1) ? &maps.v : &maps.k, (t.lo + (i >> 1)) * kKeys, hk, b, bar);
+                issued = i + 1;
+            }
+            bool drained = true;
+            for (int i = max(0, issued - Sh::slots); i < issued; ++i)
+                wait_for(drained, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
+            wait_for(drained, smem_u32(&s_q), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const int steps = (a.D + 15) / 16;
+        const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
+        auto img = [&](int i) { return ring + (uint32_t)(i % Sh::slots) * Sh::tile; };
+        auto arrived = [&](int i) {
+            wait_warp(ok, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
+        };
+        // S(j) reads K(j) (ring entry 2j), dP(j) reads V(j) (entry 2j + 1)
+        auto scores = [&](int j) {
+            if (j >= tiles) return;
+            arrived(2 * j);
+            const int tail = rr.m_b - (t.lo + j) * kKeys;
+            if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(img(2 * j), tail, lane);
+            fence_after_sync();
+            if (ok && lane == 0) {
+                mma_features(c_s + (j & 1) * 128, q_img, img(2 * j), steps, id_s);
+                mma_commit(smem_u32(&s_s[j & 1]));
+            }
+            __syncwarp();
+        };
+        auto upstream = [&](int j) {
+            if (j >= tiles) return;
+            arrived(2 * j + 1);
+            if (ok && lane == 0) {
+                mma_features(c_dp, g_img, img(2 * j + 1), steps, id_s);
+                mma_commit(smem_u32(&s_dp));
+                mma_commit(smem_u32(&s_empty[(2 * j + 1) % Sh::slots]));
+            }
+            __syncwarp();
+        };
+        if (tiles > 0) {
+            wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, &g_status);
+            scores(0);
+            upstream(0);
+            scores(1);
+        }
+        for (int j = 0; j < tiles; ++j) {
+            wait_warp(ok, smem_u32(&s_ds), (uint32_t)(j & 1), p.wait_ns, &g_status);
+            fence_after_sync();
+            if (ok && lane == 0) {
+                mma_rows(c_dq, c_dp, img(2 * j), id_o, j == 0);
+                mma_commit(smem_u32(&s_empty[(2 * j) % Sh::slots]));
+            }
+            __syncwarp();
+            upstream(j + 1);
+            scores(j + 2);
+        }
+        if (lane == 0) {
+            mma_commit(smem_u32(&s_end));
+            bool fin = true;
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2, quarter = warp & 3;
+        const int r = r0 + quarter * 32 + lane;
+        const bool mine = quarter * 32 + lane < RT && r < p.rows;
+        const int n = mine ? r / G : 0, h = hk * G + (mine ? r % G : 0);
+        const bool live = mine && n < rr.n_b;
+        const int klo = live ? rr.lo(n) : 0, khi = live ? max(klo, rr.hi(n)) : 0;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const float s2 = a.scale * kLog2e;
+        const float gs = grad_scale<T>(p, bh, lane);
+        const long long info = (long long)bh * p.rows_pad + r;
+        const float nlse = live ? -p.row_lse[info] : -INFINITY, ndel = live ? -gs * p.row_delta[info] : 0.f;
+        const unsigned long long mul = pk2(s2, s2), sub = pk2(nlse, nlse), gmul = pk2(gs, gs), gsub = pk2(ndel, ndel);
+        for (int j = 0; j < tiles; ++j) {
+            const int j0 = (t.lo + j) * kKeys + half * 64;
+            wait_warp(ok, smem_u32(&s_s[j & 1]), (uint32_t)((j >> 1) & 1), p.wait_ns, &g_status);
+            fence_after_sync();
+            float s[64];
+            const uint32_t sc = c_s + (j & 1) * 128 + lanes + half * 64;
+            tmem_ld32_nowait(sc, s);
+            tmem_ld32_nowait(sc + 32, s + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) upk2(fma2(pk2(s[c], s[c + 1]), mul, sub), s[c], s[c + 1]);
+            const bool edge = __any_sync(0xffffffffu, live && (j0 < klo || j0 + 64 > khi));
+            const int first = klo - j0, count = khi - klo;
+            if (edge) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if ((unsigned)(c - first) >= (unsigned)count) s[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = ex2(s[c]);
+            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(j & 1), p.wait_ns, &g_status);
+            fence_after_sync();
+            float d[64];
+            tmem_ld32_nowait(c_dp + lanes + half * 64, d);
+            tmem_ld32_nowait(c_dp + lanes + half * 64 + 32, d + 32);
+            tmem_wait_ld();
+            if (edge) {   // dP of a key beyond the length may be NaN
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if ((unsigned)(c - first) >= (unsigned)count) d[c] = 0.f;
+            }
+            uint32_t u[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                float x, y;
+                upk2(mul2(pk2(s[c], s[c + 1]), fma2(pk2(d[c], d[c + 1]), gmul, gsub)), x, y);
+                u[c / 2] = pack2<T>(x, y);
+            }
+            st64(c_dp + lanes + half * 64, u);
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_ds));
+        }
+        if (tiles > 0) {
+            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            fence_after_sync();
+        }
+        // each warpgroup writes half of the features
+        const float unlift = ex2(-(float)p.grad_shift), more = a.scale / gs;
+        T* out = static_cast<T*>(p.dq) + (((long long)b * a.N + n) * a.Hq + h) * a.D;
+        for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 16) {
+            if (c >= a.D) break;
+            float o[16];
+            if (tiles > 0 && ok) {
+                tmem_ld16(c_dq + lanes + c, o);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = 0.f;
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = !ok ? NAN : live && tiles > 0 ? o[q] * unlift : 0.f;
+#pragma unroll
+            for (int q = 0; q < 16; q += 8)
+                if (c + q < a.D) store8<T>(out + c + q, nullptr, o + q, more);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int DP> cudaError_t run_bwd(const AttnParams& p, const Maps& m, cudaStream_t s)
+{
+    using Sh = BwdShape<DP>;
+    const unsigned heads = (unsigned)(p.a.B * p.a.Hkv);
+    if (p.dk) {
+        auto kern = attn_dkv_tc_kernel<T, DP>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem_dkv);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)((p.a.M + kKeys - 1) / kKeys) * heads, kThreadsB, Sh::smem_dkv, s>>>(p, m);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (p.dq) {
+        auto kern = attn_dq_tc_kernel<T, DP>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem_dq);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)((p.rows + p.tile_rows - 1) / p.tile_rows) * heads, kThreadsB, Sh::smem_dq, s>>>(p, m);
+        return cudaGetLastError();
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace atc
+
+cudaError_t launch_attn_backward_tc(const AttnParams& p, cudaStream_t s)
+{
+    atc::Maps m{};
+    const sdtw_attention& a = p.a;
+    const long long flat[3] = {(long long)a.N * a.Hq * a.D, (long long)a.Hq * a.D, a.D};
+    if (!atc::map_rows(&m.q, a.q, a.q_stride, a, p.G, p.tile_rows) || !atc::map_rows(&m.dout, p.dout, flat, a, p.G, p.tile_rows) ||
+        !atc::map_keys(&m.k, a.k, a.k_stride, a) || !atc::map_keys(&m.v, a.v, a.v_stride, a))
+        return cudaErrorInvalidValue;
+    if (a.dtype == SDTW_BF16)
+        return a.D <= 64 ? atc::run_bwd<__nv_bfloat16, 64>(p, m, s) : atc::run_bwd<__nv_bfloat16, 128>(p, m, s);
+    return a.D <= 64 ? atc::run_bwd<__half, 64>(p, m, s) : atc::run_bwd<__half, 128>(p, m, s);
+}
+
+cudaError_t attn_backward_take_status(int* out, cudaStream_t s)
+{
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, atc::g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(atc::g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
+
+}  // namespace sdtw

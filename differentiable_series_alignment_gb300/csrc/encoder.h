@@ -82,6 +82,9 @@ struct AttnParams {
     // bottom of the format's range reach the products instead of being flushed to 0.
     float* row_lse;
     int grad_shift;
+    // fp16 on the tensor cores: the largest squared norm of do in every 32 packed rows
+    // ([B][Hkv][rows_pad / 32]) and of v in every 32 keys ([B][Hkv][ceil(M / 32)])
+    float *norm_rows, *norm_keys;
     float* row_delta;         // [B][Hkv][rows_pad]: sum_d do * o
     int rows_pad;             // rows rounded up to 128
     // tensor-core kernels
@@ -92,6 +95,8 @@ struct AttnParams {
 };
 bool attn_tc_fits(const sdtw_attention& a);
 cudaError_t launch_attn_forward_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_backward_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t attn_backward_take_status(int* out, cudaStream_t s);
 cudaError_t attn_forward_take_status(int* out, cudaStream_t s);
 cudaError_t launch_attn_forward_simt(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s);

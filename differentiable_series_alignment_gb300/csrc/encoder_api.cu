@@ -101,7 +101,16 @@ size_t carve_backward(AttnParams& p, void* ws)
     char* base = static_cast<char*>(ws);
     p.row_lse = reinterpret_cast<float*>(base);
     p.row_delta = reinterpret_cast<float*>(base + rows);
-    return 2 * rows;
+    size_t o = 2 * rows;
+    if (p.tc && p.a.dtype == SDTW_F16) {
+        const size_t heads = (size_t)p.a.B * p.a.Hkv;
+        p.norm_rows = reinterpret_cast<float*>(base + o);
+        o += align_up(heads * (p.rows_pad / 32) * sizeof(float));
+        p.norm_keys = reinterpret_cast<float*>(base + o);
+        o += align_up(heads * ((p.a.M + 31) / 32) * sizeof(float));
+        p.grad_shift = 15;
+    }
+    return o;
 }
 
 }  // namespace
@@ -212,6 +221,7 @@ sdtw_status sdtw_attention_forward(const sdtw_attention* a, void* out, void* out
     AttnParams p = attn_params(a);
     if (sdtw_status s = check_ws(ws, ws_bytes, carve_forward(p, ws))) return s;
     p.out = out, p.out_rest = out_rest, p.lse = lse;
+    if (p.tc && !(aligned16(out) && aligned16(out_rest))) p.tc = false;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p.tc) p.skip = debug_take_skip_publish();
     ENC_CUDA(p.tc ? launch_attn_forward_tc(p, st) : launch_attn_forward_simt(p, st));
@@ -230,16 +240,23 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
     if (sdtw_status s = check_ws(ws, ws_bytes, carve_backward(p, ws))) return s;
     p.out = const_cast<void*>(out), p.out_rest = const_cast<void*>(out_rest), p.lse_in = lse, p.dout = dout, p.dq = dq, p.dk = dk, p.dv = dv;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // results of another alignment than torch's go the general way
+    if (p.tc && !(aligned16(out) && aligned16(dout) && aligned16(dq) && aligned16(dk) && aligned16(dv))) {
+        p.tc = false;
+        p.norm_rows = p.norm_keys = nullptr;
+        p.grad_shift = 32;
+    }
     ENC_CUDA(launch_attn_rowinfo(p, st));
-    ENC_CUDA(launch_attn_backward_simt(p, st));
+    ENC_CUDA(p.tc ? launch_attn_backward_tc(p, st) : launch_attn_backward_simt(p, st));
     return SDTW_OK;
 }
 
 sdtw_status sdtw_encoder_status(void* stream)
 {
-    int word = 0;
-    ENC_CUDA(attn_forward_take_status(&word, static_cast<cudaStream_t>(stream)));
-    return word ? SDTW_ERR_TIMEOUT : SDTW_OK;
+    int forward = 0, backward = 0;
+    ENC_CUDA(attn_forward_take_status(&forward, static_cast<cudaStream_t>(stream)));
+    ENC_CUDA(attn_backward_take_status(&backward, static_cast<cudaStream_t>(stream)));
+    return forward || backward ? SDTW_ERR_TIMEOUT : SDTW_OK;
 }
 
 }  // extern "C"
