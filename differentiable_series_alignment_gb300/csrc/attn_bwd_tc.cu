@@ -10,9 +10,10 @@
 // That is 7 products where one kernel would need 5, but no result is summed across CTAs:
 // no atomics, no partial dQ in memory, the same bits every time. The gradients of heads
 // that share keys are summed in the accumulator, as rows of one problem.
-// Warps 0-7 turn scores into probabilities (two warpgroups, half of the columns each),
-// warp 8 loads by TMA, warp 9 issues the products. While the tensor cores run dV and the next
-// S^T, the warps compute dS^T; while they run dK and the next dP^T, the next P^T.
+// Warps 0-7 turn scores into probabilities (two warpgroups, half of the columns each), warp 8
+// loads by TMA, warps 9 and 10 issue the products: one S and what P enters, the other dP and
+// what dS enters. While the tensor cores run dV and the next S^T, the warps compute dS^T; while
+// they run dK and the next dP^T, the next P^T.
 #include "attn_tc.cuh"
 
 namespace sdtw {
@@ -21,7 +22,7 @@ namespace {
 
 __device__ int g_status;
 
-constexpr int kThreadsB = 320;
+constexpr int kThreadsB = 352;
 constexpr int kWork = 256;   // threads of warps 0-7
 
 template <int DP> struct BwdShape {
@@ -64,9 +65,10 @@ __device__ __forceinline__ void st64(uint32_t col, const uint32_t* u) {
 // dV/dK/dQ += A[128 x 128 from tensor memory] B, B an image read over its rows. A's columns 0-63
 // are at a, 64-127 at a + 64 (each half lies over the half of the scores it came from).
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t img, uint32_t id, bool first) {
+    const uint64_t bd = sdesc_mn(img);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-        mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, sdesc_mn(img + s * 2048), id, (!first || s > 0) ? 1u : 0u);
+        mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, bd + s * 128, id, (!first || s > 0) ? 1u : 0u);
 }
 
 template <typename T, int DP>
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_row[2][2][128];   // -lse and -delta of the tile's rows, two tiles
     const sdtw_attention& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows, G = p.G;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
             t_hi = (hi * G + RT - 1) / RT;
         }
     }
+    t_lo = uniform(t_lo), t_hi = uniform(t_hi);
     const int tiles = t_hi - t_lo;
 
     const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
@@ -101,13 +104,13 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
         mbar_init(smem_u32(&s_kv), 1);
         for (int e = 0; e < Sh::stages; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
-            mbar_init(smem_u32(&s_empty[e]), 1);
+            mbar_init(smem_u32(&s_empty[e]), 2);   // both issuing warps
         }
         mbar_init(smem_u32(&s_s), 1);
         mbar_init(smem_u32(&s_p), 8);
         mbar_init(smem_u32(&s_dp), 1);
         mbar_init(smem_u32(&s_ds), 8);
-        mbar_init(smem_u32(&s_end), 1);
+        mbar_init(smem_u32(&s_end), 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (RT < 128 && warp < 8)   // rows that no load writes, but the products over the rows read
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
     const uint32_t c_s = tmem, c_dp = tmem + 128, c_dv = tmem + 256, c_dk = tmem + 384;
     bool ok = true;
 
@@ -144,49 +147,45 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
             wait_for(drained, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp >= 9) {
+        // warp 9: S^T, then dV += P^T dO; warp 10: dP^T, then dK += dS^T Q
+        const bool grad = warp == 10;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, 128, false), id_o = idesc<T>(128, steps * 16, true);
+        const uint32_t col = grad ? c_dp : c_s, acc = grad ? c_dk : c_dv, key_img = grad ? v_img : k_img;
+        const uint32_t made = smem_u32(grad ? &s_dp : &s_s), ready = smem_u32(grad ? &s_ds : &s_p);
         const int rows_b = rr.n_b * G;   // rows from here on hold anything
         if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
-        for (int i = -1; i < tiles; ++i) {
-            const uint32_t q_img = ring + (uint32_t)(i < 0 ? 0 : i % Sh::stages) * 2 * Sh::tile, g_img = q_img + Sh::tile;
-            const int nx = i + 1;
-            const uint32_t q_nxt = ring + (uint32_t)(nx % Sh::stages) * 2 * Sh::tile, g_nxt = q_nxt + Sh::tile;
+        uint32_t ph = 0;
+        for (int i = -1, e = 0, pe = 0; i < tiles; ++i) {   // ring entries of tiles i + 1 and i
             if (i >= 0) {
-                wait_warp(ok, smem_u32(&s_p), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                // dV takes dO, dK takes Q
+                const uint32_t rows_img = ring + (uint32_t)pe * 2 * Sh::tile + (grad ? 0 : Sh::tile);
+                wait_warp(ok, ready, (uint32_t)(i & 1), p.wait_ns, &g_status);
                 fence_after_sync();
-                if (ok && lane == 0) mma_rows(c_dv, c_s, g_img, id_o, i == 0);
-                __syncwarp();
-            }
-            if (nx < tiles) {
-                wait_warp(ok, smem_u32(&s_full[nx % Sh::stages]), (uint32_t)((nx / Sh::stages) & 1), p.wait_ns, &g_status);
-                const int tail = rows_b - (t_lo + nx) * RT;
-                if (ok && tail < RT && rr.n_b < a.N) {
-                    clear_rows<DP>(q_nxt, tail, lane);
-                    clear_rows<DP>(g_nxt, tail, lane);
-                }
-                fence_after_sync();
-                if (ok && lane == 0) {
-                    mma_features(c_s, k_img, q_nxt, steps, id_s);
-                    mma_commit(smem_u32(&s_s));
+                if (ok && elect_one()) {
+                    mma_rows(acc, col, rows_img, id_o, i == 0);
+                    mma_commit(smem_u32(&s_empty[pe]));
                 }
                 __syncwarp();
             }
-            if (i >= 0) {
-                wait_warp(ok, smem_u32(&s_ds), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            if (i + 1 < tiles) {
+                const uint32_t img = ring + (uint32_t)e * 2 * Sh::tile;
+                wait_warp(ok, smem_u32(&s_full[e]), ph, p.wait_ns, &g_status);
+                const int tail = rows_b - (t_lo + i + 1) * RT;
+                if (ok && tail < RT && rr.n_b < a.N) {   // both warps: the same zeros
+                    clear_rows<DP>(img, tail, lane);
+                    clear_rows<DP>(img + Sh::tile, tail, lane);
+                }
                 fence_after_sync();
-                if (ok && lane == 0) {
-                    mma_rows(c_dk, c_dp, q_img, id_o, i == 0);
-                    mma_commit(smem_u32(&s_empty[i % Sh::stages]));
+                if (ok && elect_one()) {
+                    mma_features<DP / 16>(col, key_img, img + (grad ? Sh::tile : 0), steps, id_s);
+                    mma_commit(made);
                 }
                 __syncwarp();
             }
-            if (nx < tiles && ok && lane == 0) {
-                mma_features(c_dp, v_img, g_nxt, steps, id_s);
-                mma_commit(smem_u32(&s_dp));
-            }
-            __syncwarp();
+            pe = e;
+            if (++e == Sh::stages) e = 0, ph ^= 1;
         }
         if (lane == 0) {
             mma_commit(smem_u32(&s_end));
@@ -312,17 +311,18 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
 {
     using Sh = BwdShape<DP>;
     extern __shared__ unsigned char dyn[];
-    __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_dp, s_ds, s_end;
+    __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_free[2], s_dp, s_ds, s_end;
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows, G = p.G;
     const int row_tiles = (p.rows + RT - 1) / RT;
     const int r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * RT;
     const RowRange rr(a, b);
-    const Tiles t(rr, r0, min(r0 + RT, p.rows), G);
+    Tiles t(rr, r0, min(r0 + RT, p.rows), G);
+    t.lo = uniform(t.lo), t.hi = uniform(t.hi);
     const int tiles = t.hi - t.lo;
 
     const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
@@ -335,16 +335,18 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
         }
         mbar_init(smem_u32(&s_s[0]), 1);
         mbar_init(smem_u32(&s_s[1]), 1);
+        mbar_init(smem_u32(&s_free[0]), 8);
+        mbar_init(smem_u32(&s_free[1]), 8);
         mbar_init(smem_u32(&s_dp), 1);
         mbar_init(smem_u32(&s_ds), 8);
-        mbar_init(smem_u32(&s_end), 1);
+        mbar_init(smem_u32(&s_end), 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) tmem_alloc(&s_tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
     const uint32_t c_s = tmem, c_dp = tmem + 256, c_dq = tmem + 384;   // two S tiles
     bool ok = true;
 
@@ -369,52 +371,61 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
             wait_for(drained, smem_u32(&s_q), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp >= 9) {
+        // warp 9: S(j), two tiles ahead; warp 10: dP(j), then dQ += dS K
+        const bool grad = warp == 10;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
-        auto img = [&](int i) { return ring + (uint32_t)(i % Sh::slots) * Sh::tile; };
-        auto arrived = [&](int i) {
-            wait_warp(ok, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
-        };
-        // S(j) reads K(j) (ring entry 2j), dP(j) reads V(j) (entry 2j + 1)
-        auto scores = [&](int j) {
-            if (j >= tiles) return;
-            arrived(2 * j);
+        if (tiles > 0) wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, &g_status);
+        auto clear_tail = [&](int j, uint32_t kimg) {   // both warps: the same zeros
             const int tail = rr.m_b - (t.lo + j) * kKeys;
-            if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(img(2 * j), tail, lane);
-            fence_after_sync();
-            if (ok && lane == 0) {
-                mma_features(c_s + (j & 1) * 128, q_img, img(2 * j), steps, id_s);
-                mma_commit(smem_u32(&s_s[j & 1]));
-            }
-            __syncwarp();
+            if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(kimg, tail, lane);
         };
-        auto upstream = [&](int j) {
-            if (j >= tiles) return;
-            arrived(2 * j + 1);
-            if (ok && lane == 0) {
-                mma_features(c_dp, g_img, img(2 * j + 1), steps, id_s);
-                mma_commit(smem_u32(&s_dp));
-                mma_commit(smem_u32(&s_empty[(2 * j + 1) % Sh::slots]));
+        int e_k = 0, e_v = 1;   // ring entries of K(j) and V(j), and the parities of their arrivals
+        uint32_t ph_k = 0, ph_v = 0;
+        if (!grad) {
+            for (int j = 0; j < tiles; ++j) {
+                // the scores of tile j - 2 have been read
+                if (j >= 2) wait_warp(ok, smem_u32(&s_free[j & 1]), (uint32_t)(((j >> 1) - 1) & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
+                const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
+                clear_tail(j, kimg);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    mma_features<DP / 16>(c_s + (j & 1) * 128, q_img, kimg, steps, id_s);
+                    mma_commit(smem_u32(&s_s[j & 1]));
+                }
+                __syncwarp();
+                if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots, ph_k ^= 1;
             }
-            __syncwarp();
-        };
-        if (tiles > 0) {
-            wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, &g_status);
-            scores(0);
-            upstream(0);
-            scores(1);
-        }
-        for (int j = 0; j < tiles; ++j) {
-            wait_warp(ok, smem_u32(&s_ds), (uint32_t)(j & 1), p.wait_ns, &g_status);
-            fence_after_sync();
-            if (ok && lane == 0) {
-                mma_rows(c_dq, c_dp, img(2 * j), id_o, j == 0);
-                mma_commit(smem_u32(&s_empty[(2 * j) % Sh::slots]));
+        } else {
+            int e_p = 0;   // entry of K(j - 1)
+            for (int j = 0; j <= tiles; ++j) {
+                if (j > 0) {
+                    const uint32_t kimg = ring + (uint32_t)e_p * Sh::tile;
+                    wait_warp(ok, smem_u32(&s_ds), (uint32_t)((j - 1) & 1), p.wait_ns, &g_status);
+                    clear_tail(j - 1, kimg);
+                    fence_after_sync();
+                    if (ok && elect_one()) {
+                        mma_rows(c_dq, c_dp, kimg, id_o, j == 1);
+                        mma_commit(smem_u32(&s_empty[e_p]));   // S(j - 1) was done before dS(j - 1)
+                    }
+                    __syncwarp();
+                }
+                if (j < tiles) {
+                    wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+                    fence_after_sync();
+                    if (ok && elect_one()) {
+                        mma_features<DP / 16>(c_dp, g_img, ring + (uint32_t)e_v * Sh::tile, steps, id_s);
+                        mma_commit(smem_u32(&s_dp));
+                        mma_commit(smem_u32(&s_empty[e_v]));
+                    }
+                    __syncwarp();
+                }
+                e_p = e_k;
+                if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots;
+                if ((e_v += 2) >= Sh::slots) e_v -= Sh::slots, ph_v ^= 1;
             }
-            __syncwarp();
-            upstream(j + 1);
-            scores(j + 2);
         }
         if (lane == 0) {
             mma_commit(smem_u32(&s_end));
@@ -444,6 +455,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
             tmem_ld32_nowait(sc, s);
             tmem_ld32_nowait(sc + 32, s + 32);
             tmem_wait_ld();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_free[j & 1]));
 #pragma unroll
             for (int c = 0; c < 64; c += 2) upk2(fma2(pk2(s[c], s[c + 1]), mul, sub), s[c], s[c + 1]);
             const bool edge = __any_sync(0xffffffffu, live && (j0 < klo || j0 + 64 > khi));

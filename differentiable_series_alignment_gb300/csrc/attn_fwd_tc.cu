@@ -1,10 +1,11 @@
 // attn_fwd_tc.cu -- attention's forward pass on the tensor cores (bf16 and fp16).
 //
 // One CTA takes two tiles of up to 128 packed rows and walks the visible keys in tiles of
-// 128. Warp 9 issues S_w = Q_w K^T and O_w += P_w V for the two row tiles w in turn, so that the
-// tensor cores work on one tile while the other's softmax runs; warps 0-3 and 4-7 are the two
-// softmaxes, a thread a row; warp 8 feeds a ring of K and V tiles by TMA. Tensor memory
-// holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all 512 columns.
+// 128. Warps 9 and 10 issue S_w = Q_w K^T and O_w += P_w V, a warp a row tile w, so that the tensor
+// cores work on one tile while the other's softmax runs and its issuing warp waits; warps 0-3 and
+// 4-7 are the two softmaxes, a thread a row; warp 8 feeds a ring of K and V tiles by TMA. Tensor
+// memory holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all 512 columns. O_w takes
+// the first 64 keys of a tile while the softmax is still at the others.
 //
 // The running maximum is renewed only when a row's scores rise by more than 2^8 over it, so
 // that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
@@ -17,7 +18,7 @@ namespace {
 
 __device__ int g_status;
 
-constexpr int kThreadsF = 320;
+constexpr int kThreadsF = 352;
 constexpr float kLazy = 8.f;   // log2 of how far scores may rise over the maximum in use
 
 template <int DP> struct FwdShape {
@@ -35,10 +36,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
 {
     using Sh = FwdShape<DP>;
     extern __shared__ unsigned char dyn[];
-    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2], s_o[2], s_end;
+    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2][2], s_o[2], s_end[2];
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows;
@@ -57,6 +58,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
     }
     const bool any0 = t0.lo < t0.hi, any1 = t1.lo < t1.hi;
     if (!any0 && !any1) T1 = T0;
+    T0 = uniform(T0), T1 = uniform(T1);
+    t0.lo = uniform(t0.lo), t0.hi = uniform(t0.hi), t1.lo = uniform(t1.lo), t1.hi = uniform(t1.hi);
 
     const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
     const uint32_t q_img = base, ring = base + 2 * Sh::tile;
@@ -64,21 +67,22 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_q[w]), 1);
             mbar_init(smem_u32(&s_s[w]), 1);
-            mbar_init(smem_u32(&s_p[w]), 4);
+            mbar_init(smem_u32(&s_p[w][0]), 4);
+            mbar_init(smem_u32(&s_p[w][1]), 4);
             mbar_init(smem_u32(&s_o[w]), 1);
+            mbar_init(smem_u32(&s_end[w]), 1);
         }
         for (int e = 0; e < Sh::slots; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
-            mbar_init(smem_u32(&s_empty[e]), 1);
+            mbar_init(smem_u32(&s_empty[e]), 2);   // both issuing warps
         }
-        mbar_init(smem_u32(&s_end), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) tmem_alloc(&s_tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
     bool ok = true;
 
     if (warp == 8) {
@@ -112,60 +116,60 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             if (any1 && issued > 0) wait_for(drained, smem_u32(&s_q[1]), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp >= 9) {
+        const int w = warp - 9;
+        const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
+        const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128, q = q_img + w * Sh::tile;
+        int e_v = Sh::slots - 1, e_k = 0;   // ring entries of V(j) and K(j + 1)
+        uint32_t ph_v = 1, ph_k = 0;        // and the parities of their arrivals
         for (int j = T0 - 1; j < T1; ++j) {
-            const int iv = 2 * (j - T0) + 1, ik = iv + 1;   // ring entries of V(j) and K(j + 1)
-            const uint32_t vimg = ring + (uint32_t)((iv + 2 * Sh::slots) % Sh::slots) * Sh::tile;
-            const uint32_t kimg = ring + (uint32_t)(ik % Sh::slots) * Sh::tile;
-            bool have_v = false, have_k = false;
+            // a warp gives every entry back once it is there, also those that its tile does not see:
+            // one that ran ahead would give back an entry's next use for its last
+            if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+            if (j >= lo && j < hi) {
+                const uint32_t vimg = ring + (uint32_t)e_v * Sh::tile;
+                const int tail = rr.m_b - j * kKeys;
+                if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(vimg, tail, lane);   // both warps: the same zeros
+                const uint64_t vd = sdesc_mn(vimg);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const Tiles& t = w ? t1 : t0;
-                const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128;
-                if (j >= t.lo && j < t.hi) {
-                    if (!have_v) {
-                        wait_warp(ok, smem_u32(&s_full[iv % Sh::slots]), (uint32_t)((iv / Sh::slots) & 1), p.wait_ns, &g_status);
-                        have_v = true;
-                        const int tail = rr.m_b - j * kKeys;
-                        if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(vimg, tail, lane);
-                    }
-                    wait_warp(ok, smem_u32(&s_p[w]), (uint32_t)((j - t.lo) & 1), p.wait_ns, &g_status);
+                for (int part = 0; part < 2; ++part) {
+                    wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)((j - lo) & 1), p.wait_ns, &g_status);
                     fence_after_sync();
-                    if (ok && lane == 0) {
+                    if (ok && elect_one()) {
 #pragma unroll
-                        for (int s = 0; s < kKeys / 16; ++s)
-                            mma_ts(o_col, s_col + s * 8, sdesc_mn(vimg + s * 2048), id_o, (j > t.lo || s > 0) ? 1u : 0u);
-                        if (j == t.hi - 1) mma_commit(smem_u32(&s_o[w]));
-                    }
-                    __syncwarp();
-                }
-                if (j + 1 >= t.lo && j + 1 < t.hi) {
-                    if (!have_k) {
-                        wait_warp(ok, smem_u32(&s_full[ik % Sh::slots]), (uint32_t)((ik / Sh::slots) & 1), p.wait_ns, &g_status);
-                        have_k = true;
-                    }
-                    if (j + 1 == t.lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
-                    fence_after_sync();
-                    if (ok && lane == 0) {
-                        mma_features(s_col, q_img + w * Sh::tile, kimg, steps, id_s);
-                        mma_commit(smem_u32(&s_s[w]));
+                        for (int s = 4 * part; s < 4 * part + 4; ++s)
+                            mma_ts(o_col, s_col + s * 8, vd + s * 128, id_o, (j > lo || s > 0) ? 1u : 0u);
+                        if (part == 1 && j == hi - 1) mma_commit(smem_u32(&s_o[w]));
                     }
                     __syncwarp();
                 }
             }
-            if (ok && lane == 0) {
-                if (j >= T0) mma_commit(smem_u32(&s_empty[iv % Sh::slots]));
-                if (j + 1 < T1) mma_commit(smem_u32(&s_empty[ik % Sh::slots]));
+            if (j + 1 < T1) wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
+            if (j + 1 >= lo && j + 1 < hi) {
+                if (j + 1 == lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    mma_features<DP / 16>(s_col, q, ring + (uint32_t)e_k * Sh::tile, steps, id_s);
+                    mma_commit(smem_u32(&s_s[w]));
+                }
+                __syncwarp();
+            }
+            if (ok && elect_one()) {
+                if (j >= T0) mma_commit(smem_u32(&s_empty[e_v]));
+                if (j + 1 < T1) mma_commit(smem_u32(&s_empty[e_k]));
             }
             __syncwarp();
+            // entries alternate: V(j + 1) follows K(j + 1), K(j + 2) follows it
+            if ((e_v += 2) >= Sh::slots) e_v -= Sh::slots, ph_v ^= 1;
+            if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots, ph_k ^= 1;
         }
         // every MMA has read its operands and written its result before the CTA ends
         if (lane == 0) {
-            mma_commit(smem_u32(&s_end));
+            mma_commit(smem_u32(&s_end[w]));
             bool fin = true;
-            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            wait_for(fin, smem_u32(&s_end[w]), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
     } else {
@@ -238,6 +242,12 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                     u[q / 2 + 1] = pack2<T>(e[2], e[3]);
                 }
                 tmem_st16(s_col + c / 2, u);
+                if (c == 32) {   // the first 64 keys are there
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
+                }
             }
             float x, y;
             upk2(add2(sum0, sum1), x, y);
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_p[w]));
+            if (lane == 0) mbar_arrive(smem_u32(&s_p[w][1]));
         }
         if (t.lo < t.hi) {
             wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);

@@ -52,12 +52,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, 
         "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
 }
 
-// D[128 x N] = A[128 x features] B[N x features]^T over `steps` steps of 16 features, both
+// One thread of a converged warp. The compiler knows that elect.sync leaves one thread, and
+// keeps the operands of the products that it issues in uniform registers; behind a
+// comparison of lane numbers every product cost about 150 cycles to issue, more than the 64
+// that it takes to run.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+
+// A value that every lane of the warp holds alike, made known as such to the compiler: what
+// the issuing warp computes with then stays in uniform registers, as its products' operands
+// have to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// D[128 x N] = A[128 x features] B[N x features]^T over `steps` <= MAX steps of 16 features, both
 // K-major images; N of id.
+template <int MAX>
 __device__ __forceinline__ void mma_features(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t id) {
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t o = (uint32_t)(s >> 2) * kBox + (uint32_t)(s & 3) * 32;
-        mma_ss(d, sdesc(a + o), sdesc(b + o), id, s > 0 ? 1u : 0u);
+    const uint64_t ad = sdesc(a), bd = sdesc(b);
+#pragma unroll
+    for (int s = 0; s < MAX; ++s) {
+        const uint32_t o = ((uint32_t)(s >> 2) * kBox + (uint32_t)(s & 3) * 32) >> 4;   // the address field counts 16 bytes
+        if (s < steps) mma_ss(d, ad + o, bd + o, id, s > 0 ? 1u : 0u);
     }
 }
 
