@@ -278,25 +278,15 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
             wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        // warps 0-3 write dV, 4-7 dK, a thread a key
+        // warps 0-3 write dV, 4-7 dK, through the image of V or K
         const float unlift = ex2(-(float)p.grad_shift), more = half ? a.scale / gs : 1.f;
-        T* out = static_cast<T*>(half ? p.dk : p.dv) + (((long long)b * a.M + key) * a.Hkv + hk) * a.D;
         const bool some = tiles > 0 && live;
-        for (int c = 0; c < (a.D + 31) / 32 * 32; c += 16) {
-            float o[16];
-            if (tiles > 0 && ok) {
-                tmem_ld16((half ? c_dk : c_dv) + lanes + c, o);
-            } else {
+        const long long at = key < a.M ? (((long long)b * a.M + key) * a.Hkv + hk) * a.D : -1;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = 0.f;
-            }
-            if (key >= a.M) continue;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = !ok ? NAN : some ? o[q] * unlift : 0.f;
-#pragma unroll
-            for (int q = 0; q < 16; q += 8)
-                if (c + q < a.D) store8<T>(out + c + q, nullptr, o + q, more);
-        }
+        for (int f = 0; f < DP; f += 64)
+            write_rows<T, 64>(base + (uint32_t)(half * 4 + quarter) * 32 * 128, (half ? c_dk : c_dv) + lanes + f, tiles > 0 && ok,
+                              ok && !some, ok ? unlift : NAN, more, false, half ? p.dk : p.dv, at < 0 ? at : at + f,
+                              min(64, a.D - f) / 8, lane);
     }
     fence_before_sync();
     __syncthreads();
@@ -497,25 +487,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
             wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        // each warpgroup writes half of the features
+        // each warpgroup writes half of the features, through Q's and dO's images
         const float unlift = ex2(-(float)p.grad_shift), more = a.scale / gs;
-        T* out = static_cast<T*>(p.dq) + (((long long)b * a.N + n) * a.Hq + h) * a.D;
-        for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 16) {
-            if (c >= a.D) break;
-            float o[16];
-            if (tiles > 0 && ok) {
-                tmem_ld16(c_dq + lanes + c, o);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = 0.f;
-            }
-            if (!mine) continue;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = !ok ? NAN : live && tiles > 0 ? o[q] * unlift : 0.f;
-#pragma unroll
-            for (int q = 0; q < 16; q += 8)
-                if (c + q < a.D) store8<T>(out + c + q, nullptr, o + q, more);
-        }
+        constexpr int F = DP / 2;
+        const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + half * F : -1;
+        write_rows<T, F>(base + (uint32_t)(half * 4 + quarter) * 32 * F * 2, c_dq + lanes + half * F, tiles > 0 && ok,
+                         ok && !(live && tiles > 0), ok ? unlift : NAN, more, false, p.dq, at, min(F, a.D - half * F) / 8, lane);
     }
     fence_before_sync();
     __syncthreads();

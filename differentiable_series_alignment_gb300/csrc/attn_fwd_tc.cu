@@ -1,11 +1,11 @@
 // attn_fwd_tc.cu -- attention's forward pass on the tensor cores (bf16 and fp16).
 //
 // One CTA takes two tiles of up to 128 packed rows and walks the visible keys in tiles of
-// 128. Warps 9 and 10 issue S_w = Q_w K^T and O_w += P_w V, a warp a row tile w, so that the tensor
-// cores work on one tile while the other's softmax runs and its issuing warp waits; warps 0-3 and
-// 4-7 are the two softmaxes, a thread a row; warp 8 feeds a ring of K and V tiles by TMA. Tensor
-// memory holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all 512 columns. O_w takes
-// the first 64 keys of a tile while the softmax is still at the others.
+// 128. Two warps issue S_w = Q_w K^T and O_w += P_w V, a warp a row tile w, so that the tensor
+// cores work on one tile while the other's softmax runs and its issuing warp waits. Four
+// warps are a tile's softmax, a thread a row; one more warp feeds a ring of K and V tiles by
+// TMA. Tensor memory holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all
+// 512 columns. O_w takes the first 64 keys of a tile while the softmax is still at the others.
 //
 // The running maximum is renewed only when a row's scores rise by more than 2^8 over it, so
 // that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
@@ -18,13 +18,15 @@ namespace {
 
 __device__ int g_status;
 
-constexpr int kThreadsF = 352;
+constexpr int kThreadsF = 352;   // 8 softmax warps, one that loads, two that issue
+constexpr int kLoader = 8, kIssuer = 9;
 constexpr float kLazy = 8.f;   // log2 of how far scores may rise over the maximum in use
 
 template <int DP> struct FwdShape {
     static constexpr uint32_t tile = (DP / 64) * kBox;   // bytes of a row or key tile
     static constexpr int slots = DP == 128 ? 5 : 10;     // K and V tiles in flight: 160 KB
-    static constexpr uint32_t smem = 2 * tile + slots * tile + 1024;
+    // with the static arrays, rounded up to 1 KB, all of the 227 KB that a CTA can have
+    static constexpr uint32_t smem = 2 * tile + slots * tile;
 };
 
 // fp16 cannot hold small probabilities in full: 2^7 more of them, up to 2^15 in all.
@@ -35,8 +37,8 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
 {
     using Sh = FwdShape<DP>;
-    extern __shared__ unsigned char dyn[];
-    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2][2], s_o[2], s_end[2];
+    extern __shared__ __align__(1024) unsigned char dyn[];   // as the swizzle of the images asks
+    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2][2], s_o[2], s_end[2], s_turn[2];
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -61,9 +63,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
     T0 = uniform(T0), T1 = uniform(T1);
     t0.lo = uniform(t0.lo), t0.hi = uniform(t0.hi), t1.lo = uniform(t1.lo), t1.hi = uniform(t1.hi);
 
-    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-    const uint32_t q_img = base, ring = base + 2 * Sh::tile;
-    if (threadIdx.x == 0) {
+    const uint32_t q_img = smem_u32(dyn), ring = q_img + 2 * Sh::tile;
+    // the loader makes the barriers and sends for the first tiles before the CTA has met
+    const uint32_t row_bytes = (uint32_t)RT * 128 * (DP / 64);
+    if (warp == kLoader && lane == 0) {
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_q[w]), 1);
             mbar_init(smem_u32(&s_s[w]), 1);
@@ -71,28 +74,28 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             mbar_init(smem_u32(&s_p[w][1]), 4);
             mbar_init(smem_u32(&s_o[w]), 1);
             mbar_init(smem_u32(&s_end[w]), 1);
+            mbar_init(smem_u32(&s_turn[w]), 1);
         }
         for (int e = 0; e < Sh::slots; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
             mbar_init(smem_u32(&s_empty[e]), 2);   // both issuing warps
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (!p.skip && any0) {
+            mbar_expect_tx(smem_u32(&s_q[0]), row_bytes);
+            load_rows<DP>(q_img, &maps.q, r00 / p.G, hk, b, smem_u32(&s_q[0]));
+        }
     }
-    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    if (warp == kIssuer) tmem_alloc(&s_tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
     bool ok = true;
 
-    if (warp == 8) {
+    if (warp == kLoader) {
         if (lane == 0 && !p.skip) {
-            const uint32_t row_bytes = (uint32_t)RT * 128 * (DP / 64);
             const int n0 = r00 / p.G;
-            if (any0) {
-                mbar_expect_tx(smem_u32(&s_q[0]), row_bytes);
-                load_rows<DP>(q_img, &maps.q, n0, hk, b, smem_u32(&s_q[0]));
-            }
             const int total = 2 * (T1 - T0);
             int issued = 0;
             for (int i = 0; i < total && ok; ++i) {
@@ -116,14 +119,21 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             if (any1 && issued > 0) wait_for(drained, smem_u32(&s_q[1]), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp >= 9) {
-        const int w = warp - 9;
+    } else if (warp == kIssuer || warp == kIssuer + 1) {
+        const int w = warp - kIssuer;
         const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
         const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128, q = q_img + w * Sh::tile;
         int e_v = Sh::slots - 1, e_k = 0;   // ring entries of V(j) and K(j + 1)
         uint32_t ph_v = 1, ph_k = 0;        // and the parities of their arrivals
+        // The two warps take turns, O_w of a tile and S_w of the next at a time. Left to themselves
+        // their products interleave, both tiles' scores come late and together, and so do both
+        // softmaxes, with the tensor cores idle meanwhile.
+        auto take_turn = [&](int j) {
+            const int k = j - (T0 - 1) - (w == 0);   // the other's k-th pass; the first turn is tile 0's
+            if (k >= 0) wait_warp(ok, smem_u32(&s_turn[w]), (uint32_t)(k & 1), p.wait_ns, &g_status);
+        };
         for (int j = T0 - 1; j < T1; ++j) {
             // a warp gives every entry back once it is there, also those that its tile does not see:
             // one that ran ahead would give back an entry's next use for its last
@@ -136,6 +146,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)((j - lo) & 1), p.wait_ns, &g_status);
+                    if (part == 0) take_turn(j);
                     fence_after_sync();
                     if (ok && elect_one()) {
 #pragma unroll
@@ -148,6 +159,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             if (j + 1 < T1) wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
             if (j + 1 >= lo && j + 1 < hi) {
+                if (!(j >= lo && j < hi)) take_turn(j);
                 if (j + 1 == lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
                 fence_after_sync();
                 if (ok && elect_one()) {
@@ -156,7 +168,9 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                 }
                 __syncwarp();
             }
+            if (!(j >= lo && j < hi) && !(j + 1 >= lo && j + 1 < hi)) take_turn(j);
             if (ok && elect_one()) {
+                mbar_arrive(smem_u32(&s_turn[w ^ 1]));
                 if (j >= T0) mma_commit(smem_u32(&s_empty[e_v]));
                 if (j + 1 < T1) mma_commit(smem_u32(&s_empty[e_k]));
             }
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             wait_for(fin, smem_u32(&s_end[w]), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else {
+    } else if (warp < kLoader) {
         const int w = warp >> 2, quarter = warp & 3;
         const Tiles t = w ? t1 : t0;
         const int r = r00 + w * RT + quarter * 32 + lane;
@@ -183,11 +197,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + 256 + w * 128;
         const float s2 = a.scale * kLog2e;
-        const int o_cols = (a.D + 31) / 32 * 32;
+        const int o_cols = (a.D + 15) / 16 * 16;
         float m = -INFINITY, top = -INFINITY, off = 0.f, l = 0.f;   // maximum in use, its trigger, its base
-        for (int j = t.lo; j < t.hi && ok; ++j) {
+        for (int j = t.lo; j < t.hi; ++j) {
             wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)((j - t.lo) & 1), p.wait_ns, &g_status);
-            if (!ok) break;
             fence_after_sync();
             float s[128];
 #pragma unroll
@@ -202,10 +215,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < 128; c += 4)
+            for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], s[c + q]);
-            const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], s[c + q], s[c + 4 + q]);
+            const float now = max3(max3(mx[0], s[124], s[125]), max3(mx[1], s[126], s[127]), fmaxf(mx[2], mx[3]));
             if (__any_sync(0xffffffffu, live && now > top)) {
                 const float old = m;
                 m = fmaxf(m, now);
@@ -264,43 +277,29 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         const bool seen = live && t.lo < t.hi && l != 0.f;
         const float inv = !ok ? NAN : seen ? 1.f / l : 0.f;
         const float lse2 = !ok ? NAN : seen ? off + log2f(l) : -INFINITY;
-        const long long row = p.splits > 1 ? (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r
-                                           : ((long long)b * a.N + n) * a.Hq + h;
-        for (int c = 0; c < o_cols; c += 16) {
-            float o[16];
-            if (t.lo < t.hi && ok) {
-                tmem_ld16(o_col + c, o);
-            } else {
+        const bool read = t.lo < t.hi && ok;
+        // through the rows' part of Q's image
+        const uint32_t area = q_img + w * Sh::tile + (uint32_t)(quarter * 32 * DP * 2);
+        if (p.splits > 1) {
+            const long long place = mine ? ((((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r) : -1;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = 0.f;
-            }
-            if (!mine) continue;
+            for (int f = 0; f < DP; f += 32)
+                write_rows_f32<32>(area, o_col + f, read, ok && !seen, inv, p.part_o, mine ? place * a.D + f : -1,
+                                   min(32, a.D - f) / 4, lane);
+            if (mine) p.part_lse[place] = lse2 * kLn2;
+        } else {
+            const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D : -1;
+            for (int pass = 0; pass < (p.out_rest ? 2 : 1); ++pass)
 #pragma unroll
-            for (int q = 0; q < 16; q += 8) {
-                if (c + q >= a.D) continue;
-                const long long at = row * a.D + c + q;
-                if (!seen && ok) {
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) o[q + z] = 0.f;   // what a row that sees nothing accumulated
-                }
-                if (p.splits > 1) {
-#pragma unroll
-                    for (int z = 0; z < 8; z += 4)
-                        *reinterpret_cast<float4*>(p.part_o + at + z) =
-                            make_float4(o[q + z] * inv, o[q + z + 1] * inv, o[q + z + 2] * inv, o[q + z + 3] * inv);
-                } else {
-                    store8<T>(static_cast<T*>(p.out) + at, p.out_rest ? static_cast<T*>(p.out_rest) + at : nullptr, o + q, inv);
-                }
-            }
-        }
-        if (mine) {
-            if (p.splits > 1) p.part_lse[row] = lse2 * kLn2;
-            else if (p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
+                for (int f = 0; f < DP; f += 64)
+                    write_rows<T, 64>(area, o_col + f, read, ok && !seen, inv, 1.f, pass == 1, pass ? p.out_rest : p.out,
+                                      mine ? at + f : -1, min(64, a.D - f) / 8, lane);
+            if (mine && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
         }
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         fence_after_sync();
         tmem_dealloc(tmem, 512);
     }

@@ -178,20 +178,92 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
     return r;
 }
 
-// Writes 8 consecutive features of a result row (16 bytes), and what their rounding left.
-template <typename T> __device__ __forceinline__ void store8(T* out, T* rest, const float* v, float mul) {
-    uint32_t w[4];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 32 rows of F features (a lane a row) through shared memory to their places in global
+// memory, a whole row's 16-byte pieces by neighbouring lanes: stored straight from the lanes
+// that hold them, 32 rows at a time, results took 7000 cycles of a CTA's end. `area` is
+// 32 * F * 2 bytes of the warp's own; `at` is the row's place in elements, or < 0.
+template <int F> __device__ __forceinline__ uint32_t stage_at(uint32_t area, int row, int piece) {
+    return area + row * (F * 2) + ((piece ^ (F == 64 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+template <int F> __device__ __forceinline__ void stage_out(uint32_t area, void* out, long long at, int pieces, int lane) {
+    constexpr int PER = F / 8;
+    __syncwarp();
+    const int c = lane % PER;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = pack2<T>(v[2 * q] * mul, v[2 * q + 1] * mul);
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (rest) {
-        const T* r = reinterpret_cast<const T*>(w);
-        uint32_t z[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            z[q] = pack2<T>(v[2 * q] * mul - to_f32(r[2 * q]), v[2 * q + 1] * mul - to_f32(r[2 * q + 1]));
-        *reinterpret_cast<uint4*>(rest) = make_uint4(z[0], z[1], z[2], z[3]);
+    for (int i = 0; i < PER; ++i) {
+        const int row = i * (32 / PER) + lane / PER;
+        const long long o = __shfl_sync(0xffffffffu, at, row);
+        if (o < 0 || c >= pieces) continue;
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(stage_at<F>(area, row, c)));
+        reinterpret_cast<uint4*>(static_cast<unsigned char*>(out) + o * 2)[c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __syncwarp();
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+// F features of an accumulator in tensor memory (this lane's row, from column col), times mul
+// and more (apart, so that neither overflows), rounded into out; `zero`: the row is 0 whatever
+// the accumulator holds. rest: what that rounding leaves instead.
+template <typename T, int F>
+__device__ __forceinline__ void write_rows(uint32_t area, uint32_t col, bool read, bool zero, float mul, float more, bool rest,
+                                           void* out, long long at, int pieces, int lane) {
+#pragma unroll
+    for (int f = 0; f < F; f += 16) {
+        float o[16];
+        if (read) {
+            tmem_ld16(col + f, o);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 16; q += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float x = zero ? 0.f : o[q + 2 * z] * mul * more, y = zero ? 0.f : o[q + 2 * z + 1] * mul * more;
+                w[z] = pack2<T>(x, y);
+                if (rest) {
+                    const T* r = reinterpret_cast<const T*>(&w[z]);
+                    w[z] = pack2<T>(x - to_f32(r[0]), y - to_f32(r[1]));
+                }
+            }
+            st_shared16(stage_at<F>(area, lane, (f + q) / 8), w);
+        }
+    }
+    stage_out<F>(area, out, at, pieces, lane);
+}
+// The same in fp32, F features of 4 bytes in an area of 32 * F * 4 bytes: F / 2 16-bit places.
+template <int F>
+__device__ __forceinline__ void write_rows_f32(uint32_t area, uint32_t col, bool read, bool zero, float mul, float* out,
+                                               long long at, int pieces, int lane) {
+#pragma unroll
+    for (int f = 0; f < F; f += 16) {
+        float o[16];
+        if (read) {
+            tmem_ld16(col + f, o);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 16; q += 4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = __float_as_uint(zero ? 0.f : o[q + z] * mul);
+            st_shared16(stage_at<2 * F>(area, lane, (f + q) / 4), w);
+        }
+    }
+    stage_out<2 * F>(area, out, at < 0 ? at : 2 * at, pieces, lane);
 }
 
 // Key tiles [lo, hi) that the packed rows [r0, r1) see.
