@@ -238,9 +238,11 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
 }
 
 // o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp lse_s: the shares of the key axis
-// joined, one warp per packed row.
-template <typename T> __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p)
+// joined, one warp per packed row. There are at most 128 shares; four shares' rows
+// are in flight at a time. V: consecutive features per lane and load.
+template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p)
 {
+    __shared__ float weight[4][128];
     const sdtw_attention& a = p.a;
     const long long all = (long long)a.B * a.Hkv * p.rows;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -249,27 +251,52 @@ template <typename T> __global__ void __launch_bounds__(128) attn_combine_kernel
     const int r = (int)(row % p.rows);
     const int hk = (int)(row / p.rows % a.Hkv), b = (int)(row / p.rows / a.Hkv);
     const int n = r / p.G, h = hk * p.G + r % p.G;
-    float m = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + row]);
+    float w[4], m = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < p.splits; ++s) {
-        const float w = ex2((p.part_lse[s * all + row] - base) * kLog2e);
-        total += w;
-        const float* src = p.part_o + (s * all + row) * a.D;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (lane + 32 * q < a.D) acc[q] = fmaf(w, src[lane + 32 * q], acc[q]);
+    for (int q = 0; q < 4; ++q) {
+        w[q] = lane + 32 * q < p.splits ? p.part_lse[(lane + 32 * q) * all + row] : -INFINITY;
+        m = w[q] > m || isnan(w[q]) ? w[q] : m;   // NaN, from a row of NaN, stays
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const long long at = (((long long)b * a.N + n) * a.Hq + h) * a.D + lane;
-    T* out = static_cast<T*>(p.out) + at;
-    T* rest = p.out_rest ? static_cast<T*>(p.out_rest) + at : nullptr;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (lane + 32 * q < a.D) store_rounded(out + 32 * q, rest ? rest + 32 * q : nullptr, acc[q] * inv);
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, m, o);
+        m = x > m || isnan(x) ? x : m;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    float total = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) total += w[q] = ex2((w[q] - base) * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    float* ws = weight[threadIdx.x >> 5];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ws[lane + 32 * q] = w[q] * inv;
+    __syncwarp();
+    const long long at = (((long long)b * a.N + n) * a.Hq + h) * a.D;
+    using P = Pack<float, V>;
+    for (int d = lane * V; d < a.D; d += 32 * V) {
+        float acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        const float* src = p.part_o + row * a.D + d;
+        for (int s0 = 0; s0 < p.splits; s0 += 4) {
+            P v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (s0 + q < p.splits) v[q] = *reinterpret_cast<const P*>(src + (s0 + q) * all * a.D);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (s0 + q < p.splits)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(ws[s0 + q], v[q].e[e], acc[e]);
+        }
+        Pack<T, V> o, rest;
+#pragma unroll
+        for (int e = 0; e < V; ++e) store_rounded(&o.e[e], &rest.e[e], acc[e]);
+        *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.out) + at + d) = o;
+        if (p.out_rest) *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.out_rest) + at + d) = rest;
+    }
     if (lane == 0 && p.lse)
         p.lse[((long long)b * a.Hq + h) * a.N + n] = total == 0.f ? -INFINITY : m + logf(total);
 }
@@ -578,13 +605,19 @@ cudaError_t launch_attn_backward_simt(const AttnParams& p, cudaStream_t s)
     return bwd_typed<__half>(p, s);
 }
 
-cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s)
+template <typename T> static cudaError_t combine_typed(const AttnParams& p, cudaStream_t s)
 {
     const unsigned grid = (unsigned)(((long long)p.a.B * p.a.Hkv * p.rows + 3) / 4);
-    if (p.a.dtype == SDTW_F32) attn_combine_kernel<float><<<grid, 128, 0, s>>>(p);
-    else if (p.a.dtype == SDTW_BF16) attn_combine_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p);
-    else attn_combine_kernel<__half><<<grid, 128, 0, s>>>(p);
+    if (p.a.D % 4 == 0 && aligned16(p.out) && aligned16(p.out_rest)) attn_combine_kernel<T, 4><<<grid, 128, 0, s>>>(p);
+    else attn_combine_kernel<T, 1><<<grid, 128, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s)
+{
+    if (p.a.dtype == SDTW_F32) return combine_typed<float>(p, s);
+    if (p.a.dtype == SDTW_BF16) return combine_typed<__nv_bfloat16>(p, s);
+    return combine_typed<__half>(p, s);
 }
 
 template <typename T> static cudaError_t rowinfo_typed(const AttnParams& p, cudaStream_t s)

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
 #pragma unroll
         for (int f = 0; f < DP; f += 64)
             write_rows<T, 64>(base + (uint32_t)(half * 4 + quarter) * 32 * 128, (half ? c_dk : c_dv) + lanes + f, tiles > 0 && ok,
-                              ok && !some, ok ? unlift : NAN, more, false, half ? p.dk : p.dv, at < 0 ? at : at + f,
+                              false, ok && !some, ok ? unlift : NAN, 0.f, more, false, half ? p.dk : p.dv, at < 0 ? at : at + f,
                               min(64, a.D - f) / 8, lane);
     }
     fence_before_sync();
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
         constexpr int F = DP / 2;
         const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + half * F : -1;
         write_rows<T, F>(base + (uint32_t)(half * 4 + quarter) * 32 * F * 2, c_dq + lanes + half * F, tiles > 0 && ok,
-                         ok && !(live && tiles > 0), ok ? unlift : NAN, more, false, p.dq, at, min(F, a.D - half * F) / 8, lane);
+                         false, ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, false, p.dq, at, min(F, a.D - half * F) / 8, lane);
     }
     fence_before_sync();
     __syncthreads();

@@ -7,6 +7,11 @@
 // TMA. Tensor memory holds S_0, S_1 (P_w over S_w, as a 16-bit A operand) and O_0, O_1: all
 // 512 columns. O_w takes the first 64 keys of a tile while the softmax is still at the others.
 //
+// A single tile of rows (new samples over a cache) takes both halves of the machine: its key
+// tiles alternate between them, each with a maximum, a sum and an O of its own, which are
+// joined at the end. Every tile's way through scores, softmax and product is a chain of some
+// 2700 cycles, longer than its K and V take to arrive.
+//
 // The running maximum is renewed only when a row's scores rise by more than 2^8 over it, so
 // that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
 // then at most 2^8, which fp32 sums and 16-bit operands take as well as 1.
@@ -39,6 +44,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
     using Sh = FwdShape<DP>;
     extern __shared__ __align__(1024) unsigned char dyn[];   // as the swizzle of the images asks
     __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2][2], s_o[2], s_end[2], s_turn[2];
+    __shared__ float s_join[2][128];
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -59,6 +65,11 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         t1.lo = max(t1.lo, T0), t1.hi = min(t1.hi, T1);
     }
     const bool any0 = t0.lo < t0.hi, any1 = t1.lo < t1.hi;
+    const bool alternate = p.rows <= RT;   // one tile of rows: key tiles T0, T0 + 2, .. and T0 + 1, T0 + 3, ..
+    // Ring entries in use. K and V of a tile are neighbours, so with a multiple of four of them an
+    // entry always serves the same half: a warp that saw only every other phase of an entry's
+    // barrier would take the phase before last for the one it waits for.
+    const int slots = alternate ? Sh::slots / 4 * 4 : Sh::slots;
     if (!any0 && !any1) T1 = T0;
     T0 = uniform(T0), T1 = uniform(T1);
     t0.lo = uniform(t0.lo), t0.hi = uniform(t0.hi), t1.lo = uniform(t1.lo), t1.hi = uniform(t1.hi);
@@ -78,7 +89,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         }
         for (int e = 0; e < Sh::slots; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
-            mbar_init(smem_u32(&s_empty[e]), 2);   // both issuing warps
+            mbar_init(smem_u32(&s_empty[e]), alternate ? 1 : 2);   // issuing warps that read it
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (!p.skip && any0) {
@@ -99,8 +110,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             const int total = 2 * (T1 - T0);
             int issued = 0;
             for (int i = 0; i < total && ok; ++i) {
-                const int e = i % Sh::slots;
-                if (i >= Sh::slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::slots - 1) & 1), p.wait_ns, &g_status);
+                const int e = i % slots;
+                if (i >= slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / slots - 1) & 1), p.wait_ns, &g_status);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[e]);
                 mbar_expect_tx(bar, Sh::tile);
@@ -113,8 +124,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             // no copy may be writing shared memory when the CTA ends
             bool drained = true;
-            for (int i = max(0, issued - Sh::slots); i < issued; ++i)
-                wait_for(drained, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
+            for (int i = max(0, issued - slots); i < issued; ++i)
+                wait_for(drained, smem_u32(&s_full[i % slots]), (uint32_t)((i / slots) & 1), p.wait_ns, &g_status);
             if (any0) wait_for(drained, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
             if (any1 && issued > 0) wait_for(drained, smem_u32(&s_q[1]), 0, p.wait_ns, &g_status);
         }
@@ -124,9 +135,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
-        const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128, q = q_img + w * Sh::tile;
-        int e_v = Sh::slots - 1, e_k = 0;   // ring entries of V(j) and K(j + 1)
-        uint32_t ph_v = 1, ph_k = 0;        // and the parities of their arrivals
+        const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128, q = q_img + (alternate ? 0 : w) * Sh::tile;
         // The two warps take turns, O_w of a tile and S_w of the next at a time. Left to themselves
         // their products interleave, both tiles' scores come late and together, and so do both
         // softmaxes, with the tensor cores idle meanwhile.
@@ -134,39 +143,66 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             const int k = j - (T0 - 1) - (w == 0);   // the other's k-th pass; the first turn is tile 0's
             if (k >= 0) wait_warp(ok, smem_u32(&s_turn[w]), (uint32_t)(k & 1), p.wait_ns, &g_status);
         };
-        for (int j = T0 - 1; j < T1; ++j) {
-            // a warp gives every entry back once it is there, also those that its tile does not see:
-            // one that ran ahead would give back an entry's next use for its last
-            if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
-            if (j >= lo && j < hi) {
-                const uint32_t vimg = ring + (uint32_t)e_v * Sh::tile;
-                const int tail = rr.m_b - j * kKeys;
-                if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(vimg, tail, lane);   // both warps: the same zeros
-                const uint64_t vd = sdesc_mn(vimg);
+        // a warp's own tiles in turn: O of one, then the scores of the next
+        auto products = [&](uint32_t vimg, int j, int i, bool last) {
+            const int tail = rr.m_b - j * kKeys;
+            if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(vimg, tail, lane);   // both warps: the same zeros
+            const uint64_t vd = sdesc_mn(vimg);
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)((j - lo) & 1), p.wait_ns, &g_status);
-                    if (part == 0) take_turn(j);
-                    fence_after_sync();
-                    if (ok && elect_one()) {
+            for (int part = 0; part < 2; ++part) {
+                wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                if (part == 0 && !alternate) take_turn(j);
+                fence_after_sync();
+                if (ok && elect_one()) {
 #pragma unroll
-                        for (int s = 4 * part; s < 4 * part + 4; ++s)
-                            mma_ts(o_col, s_col + s * 8, vd + s * 128, id_o, (j > lo || s > 0) ? 1u : 0u);
-                        if (part == 1 && j == hi - 1) mma_commit(smem_u32(&s_o[w]));
-                    }
+                    for (int s = 4 * part; s < 4 * part + 4; ++s)
+                        mma_ts(o_col, s_col + s * 8, vd + s * 128, id_o, (i > 0 || s > 0) ? 1u : 0u);
+                    if (part == 1 && last) mma_commit(smem_u32(&s_o[w]));
+                }
+                __syncwarp();
+            }
+        };
+        auto scores = [&](uint32_t kimg) {
+            fence_after_sync();
+            if (ok && elect_one()) {
+                mma_features<DP / 16>(s_col, q, kimg, steps, id_s);
+                mma_commit(smem_u32(&s_s[w]));
+            }
+            __syncwarp();
+        };
+        if (alternate) {
+            const int own = (T1 - T0 + 1 - w) / 2;
+            for (int i = -1; i < own; ++i) {
+                const int iv = 2 * (2 * i + w) + 1, ik = 2 * (2 * (i + 1) + w);   // ring entries
+                if (i >= 0) {
+                    const int e = iv % slots;
+                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((iv / slots) & 1), p.wait_ns, &g_status);
+                    products(ring + (uint32_t)e * Sh::tile, T0 + 2 * i + w, i, i == own - 1);
+                    if (ok && elect_one()) mma_commit(smem_u32(&s_empty[e]));
+                    __syncwarp();
+                }
+                if (i + 1 < own) {
+                    const int e = ik % slots;
+                    if (i < 0) wait_warp(ok, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
+                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((ik / slots) & 1), p.wait_ns, &g_status);
+                    scores(ring + (uint32_t)e * Sh::tile);
+                    if (ok && elect_one()) mma_commit(smem_u32(&s_empty[e]));
                     __syncwarp();
                 }
             }
+        }
+        int e_v = slots - 1, e_k = 0;   // ring entries of V(j) and K(j + 1)
+        uint32_t ph_v = 1, ph_k = 0;        // and the parities of their arrivals
+        for (int j = T0 - 1; j < T1 && !alternate; ++j) {
+            // a warp gives every entry back once it is there, also those that its tile does not see:
+            // one that ran ahead would give back an entry's next use for its last
+            if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+            if (j >= lo && j < hi) products(ring + (uint32_t)e_v * Sh::tile, j, j - lo, j == hi - 1);
             if (j + 1 < T1) wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
             if (j + 1 >= lo && j + 1 < hi) {
                 if (!(j >= lo && j < hi)) take_turn(j);
                 if (j + 1 == lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
-                fence_after_sync();
-                if (ok && elect_one()) {
-                    mma_features<DP / 16>(s_col, q, ring + (uint32_t)e_k * Sh::tile, steps, id_s);
-                    mma_commit(smem_u32(&s_s[w]));
-                }
-                __syncwarp();
+                scores(ring + (uint32_t)e_k * Sh::tile);
             }
             if (!(j >= lo && j < hi) && !(j + 1 >= lo && j + 1 < hi)) take_turn(j);
             if (ok && elect_one()) {
@@ -176,8 +212,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             __syncwarp();
             // entries alternate: V(j + 1) follows K(j + 1), K(j + 2) follows it
-            if ((e_v += 2) >= Sh::slots) e_v -= Sh::slots, ph_v ^= 1;
-            if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots, ph_k ^= 1;
+            if ((e_v += 2) >= slots) e_v -= slots, ph_v ^= 1;
+            if ((e_k += 2) >= slots) e_k -= slots, ph_k ^= 1;
         }
         // every MMA has read its operands and written its result before the CTA ends
         if (lane == 0) {
@@ -188,8 +224,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         __syncwarp();
     } else if (warp < kLoader) {
         const int w = warp >> 2, quarter = warp & 3;
-        const Tiles t = w ? t1 : t0;
-        const int r = r00 + w * RT + quarter * 32 + lane;
+        const int step = alternate ? 2 : 1, lo = alternate ? T0 + w : w ? t1.lo : t0.lo, hi = alternate ? T1 : w ? t1.hi : t0.hi;
+        const int r = r00 + (alternate ? 0 : w) * RT + quarter * 32 + lane;
         const bool mine = quarter * 32 + lane < RT && r < p.rows;
         const int n = mine ? r / p.G : 0, h = hk * p.G + (mine ? r % p.G : 0);
         const bool live = mine && n < rr.n_b;
@@ -199,8 +235,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         const float s2 = a.scale * kLog2e;
         const int o_cols = (a.D + 15) / 16 * 16;
         float m = -INFINITY, top = -INFINITY, off = 0.f, l = 0.f;   // maximum in use, its trigger, its base
-        for (int j = t.lo; j < t.hi; ++j) {
-            wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)((j - t.lo) & 1), p.wait_ns, &g_status);
+        for (int j = lo, i = 0; j < hi; j += step, ++i) {
+            wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)(i & 1), p.wait_ns, &g_status);
             fence_after_sync();
             float s[128];
 #pragma unroll
@@ -226,7 +262,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                 l *= keep;
                 off = (m == -INFINITY ? 0.f : m * s2) - Lift<T>::v;
                 top = m + kLazy / s2;
-                if (j > t.lo) {
+                if (i > 0) {
                     for (int c = 0; c < o_cols; c += 16) {
                         float o[16];
                         tmem_ld16(o_col + c, o);
@@ -270,31 +306,54 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s_p[w][1]));
         }
-        if (t.lo < t.hi) {
+        bool read = lo < hi, other = false;
+        if (read) {
             wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        const bool seen = live && t.lo < t.hi && l != 0.f;
-        const float inv = !ok ? NAN : seen ? 1.f / l : 0.f;
-        const float lse2 = !ok ? NAN : seen ? off + log2f(l) : -INFINITY;
-        const bool read = t.lo < t.hi && ok;
-        // through the rows' part of Q's image
-        const uint32_t area = q_img + w * Sh::tile + (uint32_t)(quarter * 32 * DP * 2);
-        if (p.splits > 1) {
-            const long long place = mine ? ((((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r) : -1;
-#pragma unroll
-            for (int f = 0; f < DP; f += 32)
-                write_rows_f32<32>(area, o_col + f, read, ok && !seen, inv, p.part_o, mine ? place * a.D + f : -1,
-                                   min(32, a.D - f) / 4, lane);
-            if (mine) p.part_lse[place] = lse2 * kLn2;
+        float mul = 0.f, mul1 = 0.f, total = l;
+        if (alternate) {   // warps 0-3 join the two; a lane's row lies in the same lane of O_0 and O_1
+            const int row = quarter * 32 + lane;
+            if (w == 1) s_join[0][row] = l == 0.f ? -INFINITY : off, s_join[1][row] = l;
+            fence_before_sync();
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            fence_after_sync();
+            other = T1 - T0 > 1;
+            const float off1 = s_join[0][row], l1 = s_join[1][row];
+            const float both = fmaxf(l == 0.f ? -INFINITY : off, off1);
+            mul = l == 0.f ? 0.f : ex2(off - both);
+            mul1 = off1 == -INFINITY ? 0.f : ex2(off1 - both);
+            total = l * mul + l1 * mul1;
+            off = both;
         } else {
-            const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D : -1;
-            for (int pass = 0; pass < (p.out_rest ? 2 : 1); ++pass)
+            mul = 1.f;
+        }
+        if (!(alternate && w == 1)) {
+            const bool seen = live && read && total != 0.f;
+            const float inv = !ok ? NAN : seen ? 1.f / total : 0.f;
+            const float lse2 = !ok ? NAN : seen ? off + log2f(total) : -INFINITY;
+            read = read && ok;
+            other = other && ok;
+            mul = ok ? mul * inv : NAN;
+            mul1 *= inv;
+            // through the rows' part of Q's image
+            const uint32_t area = q_img + w * Sh::tile + (uint32_t)(quarter * 32 * DP * 2);
+            if (p.splits > 1) {
+                const long long place = mine ? ((((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r) : -1;
 #pragma unroll
-                for (int f = 0; f < DP; f += 64)
-                    write_rows<T, 64>(area, o_col + f, read, ok && !seen, inv, 1.f, pass == 1, pass ? p.out_rest : p.out,
-                                      mine ? at + f : -1, min(64, a.D - f) / 8, lane);
-            if (mine && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
+                for (int f = 0; f < DP; f += 32)
+                    write_rows_f32<32>(area, o_col + f, read, other, ok && !seen, mul, mul1, p.part_o,
+                                       mine ? place * a.D + f : -1, min(32, a.D - f) / 4, lane);
+                if (mine) p.part_lse[place] = lse2 * kLn2;
+            } else {
+                const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D : -1;
+                for (int pass = 0; pass < (p.out_rest ? 2 : 1); ++pass)
+#pragma unroll
+                    for (int f = 0; f < DP; f += 64)
+                        write_rows<T, 64>(area, o_col + f, read, other, ok && !seen, mul, mul1, 1.f, pass == 1,
+                                          pass ? p.out_rest : p.out, mine ? at + f : -1, min(64, a.D - f) / 8, lane);
+                if (mine && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
+            }
         }
     }
     fence_before_sync();

@@ -210,27 +210,40 @@ template <int F> __device__ __forceinline__ void stage_out(uint32_t area, void* 
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
-// F features of an accumulator in tensor memory (this lane's row, from column col), times mul
-// and more (apart, so that neither overflows), rounded into out; `zero`: the row is 0 whatever
-// the accumulator holds. rest: what that rounding leaves instead.
+// 16 columns of an accumulator in tensor memory from `col`, times mul, and (other) of the one 128
+// columns on, times mul1.
+__device__ __forceinline__ void read_acc(uint32_t col, bool read, bool other, float mul, float mul1, float (&o)[16]) {
+    if (read) {
+        tmem_ld16(col, o);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) o[q] *= mul;
+    if (other) {
+        float x[16];
+        tmem_ld16(col + 128, x);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = fmaf(x[q], mul1, o[q]);
+    }
+}
+// F features of an accumulator (this lane's row, from column col) times mul, and more (apart, so
+// that neither overflows), rounded into out; `zero`: the row is 0 whatever the accumulator
+// holds. rest: what that rounding leaves instead.
 template <typename T, int F>
-__device__ __forceinline__ void write_rows(uint32_t area, uint32_t col, bool read, bool zero, float mul, float more, bool rest,
-                                           void* out, long long at, int pieces, int lane) {
+__device__ __forceinline__ void write_rows(uint32_t area, uint32_t col, bool read, bool other, bool zero, float mul, float mul1,
+                                           float more, bool rest, void* out, long long at, int pieces, int lane) {
 #pragma unroll
     for (int f = 0; f < F; f += 16) {
         float o[16];
-        if (read) {
-            tmem_ld16(col + f, o);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = 0.f;
-        }
+        read_acc(col + f, read, other, mul, mul1, o);
 #pragma unroll
         for (int q = 0; q < 16; q += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                const float x = zero ? 0.f : o[q + 2 * z] * mul * more, y = zero ? 0.f : o[q + 2 * z + 1] * mul * more;
+                const float x = zero ? 0.f : o[q + 2 * z] * more, y = zero ? 0.f : o[q + 2 * z + 1] * more;
                 w[z] = pack2<T>(x, y);
                 if (rest) {
                     const T* r = reinterpret_cast<const T*>(&w[z]);
@@ -244,22 +257,17 @@ __device__ __forceinline__ void write_rows(uint32_t area, uint32_t col, bool rea
 }
 // The same in fp32, F features of 4 bytes in an area of 32 * F * 4 bytes: F / 2 16-bit places.
 template <int F>
-__device__ __forceinline__ void write_rows_f32(uint32_t area, uint32_t col, bool read, bool zero, float mul, float* out,
+__device__ __forceinline__ void write_rows_f32(uint32_t area, uint32_t col, bool read, bool other, bool zero, float mul, float mul1, float* out,
                                                long long at, int pieces, int lane) {
 #pragma unroll
     for (int f = 0; f < F; f += 16) {
         float o[16];
-        if (read) {
-            tmem_ld16(col + f, o);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = 0.f;
-        }
+        read_acc(col + f, read, other, mul, mul1, o);
 #pragma unroll
         for (int q = 0; q < 16; q += 4) {
             uint32_t w[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) w[z] = __float_as_uint(zero ? 0.f : o[q + z] * mul);
+            for (int z = 0; z < 4; ++z) w[z] = __float_as_uint(zero ? 0.f : o[q + z]);
             st_shared16(stage_at<2 * F>(area, lane, (f + q) / 4), w);
         }
     }

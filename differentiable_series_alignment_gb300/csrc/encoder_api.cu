@@ -54,16 +54,31 @@ sdtw_status check_attention(const sdtw_attention* a)
     return SDTW_OK;
 }
 
-// Rows that alone would leave SMs idle share them along the key axis, in parts of
-// at least one tile of `keys`, as many as give every SM `waves` CTAs.
-int key_splits(const AttnParams& p, int tile_rows, int keys, int waves)
+// Shares of the key axis. Row tiles that alone would leave SMs idle are split along their
+// keys, and the shares joined by a second launch. A CTA takes `fixed` us and `tile` us a key
+// tile, `waves` of them follow one another on an SM; joining takes a launch and the shares'
+// fp32 rows twice through memory. The least sum of these is taken.
+int key_splits(const AttnParams& p, int tile_rows, int tile_keys, int resident, double fixed, double tile)
 {
-    const long long ctas = (long long)((p.rows + tile_rows - 1) / tile_rows) * p.a.B * p.a.Hkv;
-    const long long sms = device_sms(), tiles = (p.a.M + keys - 1) / keys;
-    if (ctas >= sms) return 1;
-    long long s = (waves * sms + ctas - 1) / ctas;
-    if (s > tiles) s = tiles;
-    return (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+    const sdtw_attention& a = p.a;
+    const long long ctas = (long long)((p.rows + tile_rows - 1) / tile_rows) * a.B * a.Hkv;
+    const long long slots = (long long)device_sms() * resident;
+    if (ctas >= slots) return 1;
+    long long keys = a.M;   // that a tile of rows sees at the most
+    if (p.a.window_left >= 0 && p.a.window_right >= 0) {
+        const long long span = (long long)p.a.window_left + p.a.window_right + (tile_rows - 1) / p.G + 1 + tile_keys;
+        if (span < keys) keys = span;
+    }
+    const int tiles = (int)((keys + tile_keys - 1) / tile_keys);
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= tiles && s <= 128; ++s) {
+        const double rounds = (double)((ctas * s + slots - 1) / slots);
+        const double join = s == 1 ? 0. : 5. + 1e-6 * 2. * s * (double)(a.B * (long long)a.Hkv * p.rows) * a.D * 4. / 5.;
+        const double cost = rounds * (fixed + tile * ((tiles + s - 1) / s)) + join;
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
 }
 
 AttnParams attn_params(const sdtw_attention* a)
@@ -78,7 +93,9 @@ AttnParams attn_params(const sdtw_attention* a)
     p.rows_pad = (p.rows + 127) / 128 * 128;
     p.tc = attn_tc_fits(*a);
     p.tile_rows = p.tc ? 128 / p.G * p.G : 64;
-    p.splits = p.tc ? key_splits(p, 2 * p.tile_rows, 128, 4) : key_splits(p, 64, 64, 2);
+    // a single row tile has its key tiles done two at a time
+    p.splits = p.tc ? key_splits(p, p.rows <= p.tile_rows ? p.tile_rows : 2 * p.tile_rows, p.rows <= p.tile_rows ? 256 : 128, 1, 5., 1.5)
+                    : key_splits(p, 64, 64, 2, 3., 2.);
     p.grad_shift = 32;
     p.wait_ns = debug_wait_ns();
     return p;

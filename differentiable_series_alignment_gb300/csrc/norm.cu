@@ -35,14 +35,34 @@ template <int L> __device__ __forceinline__ float row_sum(float v, float* red) {
     return s;
 }
 
-template <typename W> __device__ __forceinline__ float wload(const void* p, int c) {
-    return to_f32(static_cast<const W*>(p)[c]);
-}
 __device__ __forceinline__ float wval(const void* p, int c, int wdtype, float none) {
     if (p == nullptr) return none;
     if (wdtype == SDTW_F32) return static_cast<const float*>(p)[c];
-    if (wdtype == SDTW_BF16) return wload<__nv_bfloat16>(p, c);
-    return wload<__half>(p, c);
+    if (wdtype == SDTW_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[c]);
+    return to_f32(static_cast<const __half*>(p)[c]);
+}
+template <typename W, int VEC> __device__ __forceinline__ void wload(const void* p, int c0, float (&out)[VEC]) {
+    constexpr int N = VEC * sizeof(W) > 16 ? 16 / sizeof(W) : VEC;   // elements of one load
+#pragma unroll
+    for (int k = 0; k < VEC; k += N) {
+        const Pack<W, N> v = *reinterpret_cast<const Pack<W, N>*>(static_cast<const W*>(p) + c0 + k);
+#pragma unroll
+        for (int e = 0; e < N; ++e) out[k + e] = to_f32(v.e[e]);
+    }
+}
+// VEC weights from c0; with VEC > 1 the array is 16-byte aligned. Read from the cache for every
+// row: held in registers they would take the place of rows in flight.
+template <int VEC> __device__ __forceinline__ void weights(const void* p, int c0, int wdtype, float none, float (&out)[VEC]) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = none;
+    } else if (wdtype == SDTW_F32) {
+        wload<float, VEC>(p, c0, out);
+    } else if (wdtype == SDTW_BF16) {
+        wload<__nv_bfloat16, VEC>(p, c0, out);
+    } else {
+        wload<__half, VEC>(p, c0, out);
+    }
 }
 __device__ __forceinline__ void wstore(void* p, int c, int wdtype, float v) {
     if (wdtype == SDTW_F32) static_cast<float*>(p)[c] = v;
@@ -62,14 +82,22 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormParams p)
     const float inv_c = 1.f / (float)p.C;
     // every thread of a warp (of the CTA, for long rows) makes the same number of rounds:
     // the sums below are collective
-    for (long long r0 = (long long)blockIdx.x * (kThreads / L); r0 < p.rows; r0 += step) {
-        const long long r = r0 + threadIdx.x / L;
-        const bool live = r < p.rows;
-        const P* src = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + (live ? r : 0) * p.C);
-        P v[K];
+    auto fetch = [&](long long r, P (&v)[K]) {
+        const P* src = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.C);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (lane + k * L < packs) v[k] = src[lane + k * L];
+    };
+    long long r0 = (long long)blockIdx.x * (kThreads / L);
+    P next[K];
+    fetch(r0 + threadIdx.x / L, next);
+    for (; r0 < p.rows; r0 += step) {
+        const long long r = r0 + threadIdx.x / L;
+        const bool live = r < p.rows;
+        P v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = next[k];
+        if (r0 + step < p.rows) fetch(r + step, next);   // one row ahead of the sums
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -93,11 +121,11 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormParams p)
             for (int k = 0; k < K; ++k)
                 if (lane + k * L < packs) {
                     P o;
-                    const int c0 = (lane + k * L) * VEC;
+                    float w[VEC], b[VEC];
+                    weights<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
+                    weights<VEC>(p.bias, (lane + k * L) * VEC, p.wdtype, 0.f, b);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        o.e[e] = from_f32<T>(fmaf((to_f32(v[k].e[e]) - mu) * rs, wval(p.weight, c0 + e, p.wdtype, 1.f),
-                                                  wval(p.bias, c0 + e, p.wdtype, 0.f)));
+                    for (int e = 0; e < VEC; ++e) o.e[e] = from_f32<T>(fmaf((to_f32(v[k].e[e]) - mu) * rs, w[e], b[e]));
                     dst[lane + k * L] = o;
                 }
             if (lane == 0 && p.mean) {
@@ -150,28 +178,41 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormParams p)
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
-    for (long long r0 = (long long)blockIdx.x * (kThreads / L); r0 < p.rows; r0 += step) {
-        const long long r = r0 + group;
-        const bool live = r < p.rows;
-        const long long at = (live ? r : 0) * p.C;
+    auto fetch = [&](long long r, P (&xv)[K], P (&gv)[K], float& mu, float& rs) {
+        const long long at = (r < p.rows ? r : 0) * p.C;
         const P* xs = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + at);
         const P* gs = reinterpret_cast<const P*>(static_cast<const T*>(p.dy) + at);
-        P xv[K], gv[K];
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (lane + k * L < packs) {
                 xv[k] = xs[lane + k * L];
                 gv[k] = gs[lane + k * L];
             }
-        const float mu = p.mean[live ? r : 0], rs = p.rstd[live ? r : 0];
+        mu = p.mean[r < p.rows ? r : 0];
+        rs = p.rstd[r < p.rows ? r : 0];
+    };
+    long long r0 = (long long)blockIdx.x * (kThreads / L);
+    P xn[K], gn[K];
+    float mun, rsn;
+    fetch(r0 + group, xn, gn, mun, rsn);
+    for (; r0 < p.rows; r0 += step) {
+        const long long r = r0 + group;
+        const bool live = r < p.rows;
+        P xv[K], gv[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) xv[k] = xn[k], gv[k] = gn[k];
+        const float mu = mun, rs = rsn;
+        if (r0 + step < p.rows) fetch(r + step, xn, gn, mun, rsn);   // one row ahead of the sums
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (lane + k * L < packs)
+            if (lane + k * L < packs) {
+                float w[VEC];
+                weights<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float xh = (to_f32(xv[k].e[e]) - mu) * rs, dy = to_f32(gv[k].e[e]);
-                    const float g = dy * wval(p.weight, (lane + k * L) * VEC + e, p.wdtype, 1.f);
+                    const float g = dy * w[e];
                     s1 += g;
                     s2 = fmaf(g, xh, s2);
                     if (live) {
@@ -179,19 +220,21 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormParams p)
                         db[k][e] += dy;
                     }
                 }
+            }
         s1 = row_sum<L>(s1, red) * inv_c;
         s2 = row_sum<L>(s2, red) * inv_c;
         if (live && p.dx) {
-            P* dst = reinterpret_cast<P*>(static_cast<T*>(p.dx) + at);
+            P* dst = reinterpret_cast<P*>(static_cast<T*>(p.dx) + r * p.C);
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (lane + k * L < packs) {
                     P o;
+                    float w[VEC];
+                    weights<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const float xh = (to_f32(xv[k].e[e]) - mu) * rs;
-                        const float g = to_f32(gv[k].e[e]) * wval(p.weight, (lane + k * L) * VEC + e, p.wdtype, 1.f);
-                        o.e[e] = from_f32<T>(rs * (g - s1 - xh * s2));
+                        o.e[e] = from_f32<T>(rs * (to_f32(gv[k].e[e]) * w[e] - s1 - xh * s2));
                     }
                     dst[lane + k * L] = o;
                 }
@@ -262,23 +305,27 @@ template <typename T> __global__ void __launch_bounds__(kThreads) norm_bwd_long_
     }
 }
 
-// dw, db: the CTAs' partial rows added in a fixed order. 32 columns by 8 row lanes.
-__global__ void __launch_bounds__(256) norm_fold_kernel(const NormParams p, int ctas)
+// dw, db: the CTAs' partial rows added in a fixed order. 32 columns by 32 row lanes, four
+// rows in flight each.
+__global__ void __launch_bounds__(1024) norm_fold_kernel(const NormParams p, int ctas)
 {
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     const float* src = p.partial + (long long)blockIdx.y * ctas * p.C;
-    float s = 0.f;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < p.C)
-        for (int t = lane; t < ctas; t += 8) s += src[(long long)t * p.C + c];
-    part[lane][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (lane == 0 && c < p.C) {
+        for (int t = lane; t < ctas; t += 128) {
 #pragma unroll
-        for (int g = 1; g < 8; ++g) s += part[g][threadIdx.x & 31];
-        void* dst = blockIdx.y ? p.dbias : p.dweight;
-        if (dst) wstore(dst, c, p.wdtype, s);
-    }
+            for (int q = 0; q < 4; ++q)
+                if (t + 32 * q < ctas) s[q] += src[(long long)(t + 32 * q) * p.C + c];
+        }
+    part[lane][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    // transposed: a warp adds one column's 32 lanes
+    const float v = group_sum<32>(part[threadIdx.x & 31][lane]);
+    const int col = blockIdx.x * 32 + lane;
+    void* dst = blockIdx.y ? p.dbias : p.dweight;
+    if ((threadIdx.x & 31) == 0 && col < p.C && dst) wstore(dst, col, p.wdtype, v);
 }
 
 int device_sms()
@@ -343,7 +390,7 @@ cudaError_t pick_norm(const NormParams& p, bool backward, int ctas, cudaStream_t
 template <typename T> cudaError_t norm_typed(const NormParams& p, bool backward, int ctas, cudaStream_t s)
 {
     constexpr int VEC = 16 / sizeof(T);
-    const bool packed = p.C % VEC == 0 && aligned16(p.x) &&
+    const bool packed = p.C % VEC == 0 && aligned16(p.x) && aligned16(p.weight) && aligned16(p.bias) &&
                         (backward ? aligned16(p.dy) && aligned16(p.dx) : aligned16(p.y));
     return packed ? pick_norm<T, VEC>(p, backward, ctas, s) : pick_norm<T, 1>(p, backward, ctas, s);
 }
@@ -371,7 +418,7 @@ cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s)
 {
     cudaError_t e = norm_any(p, true, ctas, s);
     if (e != cudaSuccess || !p.partial) return e;
-    norm_fold_kernel<<<dim3((p.C + 31) / 32, 2), 256, 0, s>>>(p, ctas);
+    norm_fold_kernel<<<dim3((p.C + 31) / 32, 2), 1024, 0, s>>>(p, ctas);
     return cudaGetLastError();
 }
 

@@ -25,15 +25,22 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     const int turns = p.interleaved ? p.R / VEC : half / VEC;
     const int units = turns + (p.D - p.R) / VEC;
     const int heads = p.H[0] + (p.in[1] ? p.H[1] : 0);
-    const int groups = (heads + HEADS - 1) / HEADS;
-    const long long items = (long long)p.B * p.N * groups * units;
+    const long long items = (long long)p.B * p.N * units;
     for (long long it = (long long)blockIdx.x * kRotThreads + threadIdx.x; it < items;
-         it += (long long)gridDim.x * kRotThreads) {
-        const int u = (int)(it % units);
-        long long t = it / units;
-        const int g = (int)(t % groups);
-        t /= groups;
-        const int n = (int)(t % p.N), b = (int)(t / p.N);
+         it += (long long)gridDim.x * kRotThreads)
+      for (int g = blockIdx.y; g * HEADS < heads; g += gridDim.y) {
+        // 32-bit division wherever the sizes allow it: two of 64 bits cost more than the turns
+        long long token;
+        int u;
+        if (items <= 0x7fffffff) {
+            token = (unsigned)it / (unsigned)units;
+            u = (int)((unsigned)it - (unsigned)token * (unsigned)units);
+        } else {
+            token = it / units;
+            u = (int)(it - token * units);
+        }
+        const int b = token <= 0x7fffffff ? (int)((unsigned)token / (unsigned)p.N) : (int)(token / p.N);
+        const int n = (int)(token - (long long)b * p.N);
         const bool turn = u < turns;
         const int c0 = turn ? u * VEC : p.R + (u - turns) * VEC;   // first feature of the unit
         const bool two = turn && !p.interleaved;                    // its partners are half further on
@@ -132,11 +139,12 @@ template <typename T, int VEC> cudaError_t run_rotary(const RotaryParams& p, cud
     const long long one = (long long)p.B * p.N * units;
     // four heads a thread reuse its cosines; one a thread where that would leave SMs idle
     const bool many = one * ((heads + 3) / 4) >= 152ll * 4 * kRotThreads;
-    const long long items = one * (many ? (heads + 3) / 4 : heads);
-    long long grid = (items + kRotThreads - 1) / kRotThreads;
-    if (grid > 152ll * 64) grid = 152ll * 64;
-    if (many) rotary_kernel<T, VEC, 4><<<(unsigned)grid, kRotThreads, 0, s>>>(p);
-    else rotary_kernel<T, VEC, 1><<<(unsigned)grid, kRotThreads, 0, s>>>(p);
+    long long x = (one + kRotThreads - 1) / kRotThreads;
+    if (x > 1 << 24) x = 1 << 24;
+    const int groups = many ? (heads + 3) / 4 : heads;
+    const dim3 grid((unsigned)x, (unsigned)(groups < 65535 ? groups : 65535));
+    if (many) rotary_kernel<T, VEC, 4><<<grid, kRotThreads, 0, s>>>(p);
+    else rotary_kernel<T, VEC, 1><<<grid, kRotThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -332,6 +332,19 @@ def test_attention_of_padded_batches(package, N, M, D, causal, window, dtype):
     check_attention(package, q, k, v, do, dtype, causal, window, ql, kl)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("N,G,M", [(1, 1, 3001), (1, 4, 2048), (3, 3, 1300), (2, 8, 1111)])
+def test_attention_of_few_rows_over_long_caches(package, N, G, M, D, dtype):
+    """New samples over caches of many key tiles, full, odd and empty."""
+    gen = generator(M + D)
+    q, do = randn(gen, 3, N, 2 * G, D, dtype=dtype, std=1.5), randn(gen, 3, N, 2 * G, D, dtype=dtype, std=0.3)
+    k, v = randn(gen, 3, M, 2, D, dtype=dtype, std=1.5), randn(gen, 3, M, 2, D, dtype=dtype)
+    kl = torch.tensor([M, 0, M // 2 + 1], device="cuda", dtype=torch.int32)
+    for args in (dict(causal=True, kl=kl), dict(), dict(causal=True, window=700)):
+        check_attention(package, q, k, v, do, dtype, **args)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_of_slices_and_of_unaligned_heads(package, dtype):
     gen = generator(11)
