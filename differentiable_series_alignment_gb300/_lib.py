@@ -7,6 +7,7 @@ the method happens in Python: a missing library raises, there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -14,6 +15,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsdtw.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 UNFUSED, FUSED = 0, 1
 EXTENDED = 2   # precision flag OR-ed into the mode (double-float forward state)
@@ -57,7 +59,6 @@ class SdtwError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
-_quick = None   # the encoder operators' entry points, called without releasing the GIL
 
 
 def _bind_encoder(lib):
@@ -83,7 +84,7 @@ def _bind_encoder(lib):
 
 def load(path: str = LIB_PATH):
     """Load libsdtw.so (built in-tree); raises if it is missing."""
-    global _lib, _quick
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -139,18 +140,22 @@ def load(path: str = LIB_PATH):
         lib.sdtw_debug_set_wait.argtypes = [ctypes.c_double, i]
         lib.sdtw_debug_set_wait.restype = None
         _bind_encoder(lib)
-        # The encoder operators only enqueue work, in a few microseconds. A call that gives up the GIL
-        # for that lets autograd's thread in, which the caller then waits for: 240 instead of 150
-        # microseconds for a small layer norm's forward and backward.
-        _quick = ctypes.PyDLL(path)
-        _bind_encoder(_quick)
         _lib = lib
         return lib
 
 
-def quick():
-    """The encoder operators' entry points, for calls that only enqueue work."""
-    return _quick if _quick is not None else (load(), _quick)[1]
+_binding = None
+
+
+def binding():
+    """_binding.so: the encoder operators as autograd functions; raises if it is missing."""
+    global _binding
+    if _binding is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with `python -m differentiable_series_alignment_gb300.build`")
+        _binding = importlib.import_module("._binding", __package__)
+    return _binding
 
 
 def status_string(code: int) -> str:
