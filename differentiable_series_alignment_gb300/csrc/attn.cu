@@ -27,43 +27,68 @@ constexpr int kThr = 256;
 constexpr int kPitchP = kT + 4;   // pitch of a 64 x 64 tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Rows [0, kT) of a tile: row_ptr(i) is the row's first element or null (zeros).
+// Rows [0, kT) of a tile: row_ptr(i) is the row's first element or null (zeros). packed: rows
+// begin at boundaries of four elements and D is a multiple of four. All loads of a thread
+// go out before its stores.
 template <typename T, int DP, typename F>
-__device__ __forceinline__ void load_tile(float* dst, int D, F row_ptr)
+__device__ __forceinline__ void load_tile(float* dst, int D, bool packed, F row_ptr)
 {
-    constexpr int LD = DP + 4;
-    for (int e = threadIdx.x; e < kT * (DP / 4); e += kThr) {
-        const int r = e / (DP / 4), c = (e % (DP / 4)) * 4;
-        const T* src = row_ptr(r);
-        float v[4];
+    constexpr int LD = DP + 4, N = kT * (DP / 4) / kThr;
+    float4 v[N];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = (src && c + q < D) ? to_f32(src[c + q]) : 0.f;
-        *reinterpret_cast<float4*>(dst + r * LD + c) = make_float4(v[0], v[1], v[2], v[3]);
+    for (int k = 0; k < N; ++k) {
+        const int e = threadIdx.x + k * kThr, r = e / (DP / 4), c = (e % (DP / 4)) * 4;
+        const T* src = row_ptr(r);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src == nullptr || c >= D) continue;
+        if (packed) {
+            const Pack<T, 4> x = *reinterpret_cast<const Pack<T, 4>*>(src + c);
+            v[k] = make_float4(to_f32(x.e[0]), to_f32(x.e[1]), to_f32(x.e[2]), to_f32(x.e[3]));
+        } else {
+            v[k].x = to_f32(src[c]);
+            if (c + 1 < D) v[k].y = to_f32(src[c + 1]);
+            if (c + 2 < D) v[k].z = to_f32(src[c + 2]);
+            if (c + 3 < D) v[k].w = to_f32(src[c + 3]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int e = threadIdx.x + k * kThr;
+        *reinterpret_cast<float4*>(dst + e / (DP / 4) * LD + (e % (DP / 4)) * 4) = v[k];
     }
 }
 
-// acc[i][j] = sum_d a[ty + 16 i][d] * b[tx + 16 j][d]
+// acc[i][j] = sum_d a[ty + 16 i][d] * b[tx + 16 j][d], even and odd d apart in packed pairs
+// (one instruction for two products).
 template <int DP>
 __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx)
 {
     constexpr int LD = DP + 4;
+    unsigned long long s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[i][j] = pk2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < DP; d += 4) {
-        float4 x[4], y[4];
+        ulonglong2 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * LD + d);
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * i) * LD + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LD + d);
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * LD + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+            for (int j = 0; j < 4; ++j) s[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, s[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            upk2(s[i][j], lo, hi);
+            acc[i][j] = lo + hi;
+        }
 }
 
 // out[i][c] += sum_k p[ty + 16 i][k] * v[k][column c of this thread]; columns tx * 4 + 64 cc
@@ -74,8 +99,8 @@ template <int DP> struct Cols {
     static __device__ __forceinline__ int at(int tx, int cc, int w) { return tx * W + 64 * cc + w; }
 };
 template <int DP>
-__device__ __forceinline__ void mul_tile(float (&out)[4][Cols<DP>::N * Cols<DP>::W], const float* p, const float* v, int ty,
-                                         int tx)
+__device__ __forceinline__ void mul_tile(unsigned long long (&out)[4][Cols<DP>::N * Cols<DP>::W / 2], const float* p, const float* v,
+                                         int ty, int tx)
 {
     constexpr int LD = DP + 4, W = Cols<DP>::W, NC = Cols<DP>::N;
 #pragma unroll 2
@@ -84,25 +109,38 @@ __device__ __forceinline__ void mul_tile(float (&out)[4][Cols<DP>::N * Cols<DP>:
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPitchP + k);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+            unsigned long long a[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = q == 0 ? x[i].x : q == 1 ? x[i].y : q == 2 ? x[i].z : x[i].w;
+                a[i] = pk2(e, e);
+            }
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc) {
-                float y[W];
                 const float* src = v + (k + q) * LD + Cols<DP>::at(tx, cc, 0);
-                if (W == 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(src);
-                    y[0] = t.x, y[1] = t.y, y[W - 2] = t.z, y[W - 1] = t.w;
-                } else {
-                    const float2 t = *reinterpret_cast<const float2*>(src);
+                unsigned long long y[W / 2];
+                if constexpr (W == 4) {
+                    const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(src);
                     y[0] = t.x, y[1] = t.y;
+                } else {
+                    y[0] = *reinterpret_cast<const unsigned long long*>(src);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = q == 0 ? x[i].x : q == 1 ? x[i].y : q == 2 ? x[i].z : x[i].w;
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int w = 0; w < W; ++w) out[i][cc * W + w] = fmaf(a, y[w], out[i][cc * W + w]);
-                }
+                    for (int w = 0; w < W / 2; ++w) out[i][cc * (W / 2) + w] = fma2(a[i], y[w], out[i][cc * (W / 2) + w]);
             }
+        }
+    }
+}
+// the two halves of a packed accumulator, scaled
+template <int NP> __device__ __forceinline__ void unpack(const unsigned long long (&acc)[NP], float mul, float (&out)[2 * NP]) {
+#pragma unroll
+    for (int c = 0; c < NP; ++c) {
+        upk2(acc[c], out[2 * c], out[2 * c + 1]);
+        out[2 * c] *= mul;
+        out[2 * c + 1] *= mul;
     }
 }
 
@@ -118,7 +156,7 @@ __device__ __forceinline__ float sum16(float v) {
     return v;
 }
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_simt(const AttnParams p)
+template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 ? 1 : 2) attn_fwd_simt(const AttnParams p)
 {
     extern __shared__ float sm[];
     constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
@@ -150,7 +188,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
     const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
     const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
-    load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+    load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
         const int r = r0 + i;
         if (r >= p.rows) return nullptr;
         const int n = r / p.G;
@@ -158,7 +196,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
         return q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2];
     });
     int klo[4], khi[4];   // visible keys of this thread's rows
-    float m[4], l[4], o[4][NC];
+    float m[4], l[4];
+    unsigned long long o[4][NC / 2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty + 16 * i;
@@ -169,14 +208,14 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+        for (int c = 0; c < NC / 2; ++c) o[i][c] = pk2(0.f, 0.f);
     }
     const float s2 = a.scale * kLog2e;
     for (int t = t_lo; t < t_hi; ++t) {
         const int j0 = t * kT;
         __syncthreads();
-        load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
-        load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+        load_tile<T, DP>(K, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+        load_tile<T, DP>(V, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
         __syncthreads();
         float s[4][4];
         dot_tile<DP>(s, Q, K, ty, tx);
@@ -202,7 +241,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
             }
             l[i] = l[i] * keep + sum;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[i][c] *= keep;
+            for (int c = 0; c < NC / 2; ++c) o[i][c] = fma2(o[i][c], pk2(keep, keep), pk2(0.f, 0.f));
         }
         __syncthreads();
         mul_tile<DP>(o, P, V, ty, tx);
@@ -214,13 +253,15 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
         if (r >= p.rows) continue;
         const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
         const float lse = total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
+        float res[NC];
+        unpack(o[i], inv, res);
         const int n = r / p.G, h = hk * p.G + r % p.G;
         if (p.splits > 1) {
             const long long row = (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
-                if (d < a.D) p.part_o[row * a.D + d] = o[i][c] * inv;
+                if (d < a.D) p.part_o[row * a.D + d] = res[c];
             }
             if (tx == 0) p.part_lse[row] = lse;
         } else {
@@ -230,7 +271,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_fwd_s
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
-                if (d < a.D) store_rounded(out + d, rest ? rest + d : nullptr, o[i][c] * inv);
+                if (d < a.D) store_rounded(out + d, rest ? rest + d : nullptr, res[c]);
             }
             if (tx == 0 && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse;
         }
@@ -319,8 +360,9 @@ template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowin
     using P = Pack<T, VEC>;
     if (blockIdx.x < row_ctas) {
         const long long at = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
-        const int r = (int)(at % p.rows_pad);
-        const int hk = (int)(at / p.rows_pad % a.Hkv), b = (int)(at / p.rows_pad / a.Hkv);
+        const unsigned per = (unsigned)p.rows_pad / 32, bh = blockIdx.x / per;
+        const int r = (int)(blockIdx.x - bh * per) * 32 + (threadIdx.x >> 3);
+        const int b = (int)(bh / (unsigned)a.Hkv), hk = (int)(bh - (unsigned)b * a.Hkv);
         const int n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
         const int n = r / p.G, h = hk * p.G + r % p.G;
         float lse = -INFINITY, delta = 0.f;
@@ -378,9 +420,8 @@ template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowin
 }
 
 // dq of 64 packed rows: S and dP = do v^T per key tile, dq += dS k.
-template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_simt(const AttnParams p)
+template <typename T, int DP> __device__ __forceinline__ void dq_cta(const AttnParams& p, const int block, float* sm)
 {
-    extern __shared__ float sm[];
     constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
     float* Q = sm;
     float* G = Q + kT * LD;
@@ -389,9 +430,9 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_si
     float* S = V + kT * LD;
     const sdtw_attention& a = p.a;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int heads = a.B * a.Hkv, bh = block % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int r0 = (((p.rows + kT - 1) / kT) - 1 - (int)(blockIdx.x / heads)) * kT;
+    const int r0 = (((p.rows + kT - 1) / kT) - 1 - block / heads) * kT;
     const int last = min(r0 + kT, p.rows) - 1;
     const RowRange rr(a, b);
     const int n_first = r0 / p.G, n_last = min(last / p.G, rr.n_b - 1);
@@ -404,18 +445,19 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_si
     const T* dout = static_cast<const T*>(p.dout);
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
     const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
-    load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+    load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
         const int r = r0 + i;
         const int n = r / p.G;
         return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
     });
-    load_tile<T, DP>(G, a.D, [&](int i) -> const T* {
+    load_tile<T, DP>(G, a.D, p.packed, [&](int i) -> const T* {
         const int r = r0 + i;
         const int n = r / p.G;
         return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
     });
     int klo[4], khi[4];
-    float lse[4], delta[4], dq[4][NC];
+    float lse[4], delta[4];
+    unsigned long long dq[4][NC / 2];
     const long long info = ((long long)b * a.Hkv + hk) * p.rows_pad;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -427,13 +469,13 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_si
         lse[i] = p.row_lse[info + r];
         delta[i] = p.row_delta[info + r];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) dq[i][c] = 0.f;
+        for (int c = 0; c < NC / 2; ++c) dq[i][c] = pk2(0.f, 0.f);
     }
     const float s2 = a.scale * kLog2e, back = ex2(-(float)p.grad_shift);
     for (int j0 = lo / kT * kT; j0 < hi; j0 += kT) {
         __syncthreads();
-        load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
-        load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+        load_tile<T, DP>(K, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+        load_tile<T, DP>(V, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
         __syncthreads();
         float s[4][4], dp[4][4];
         dot_tile<DP>(s, Q, K, ty, tx);
@@ -454,19 +496,20 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dq_si
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty + 16 * i;
         if (r >= p.rows) continue;
+        float res[NC];
+        unpack(dq[i], back, res);
         T* out = static_cast<T*>(p.dq) + (((long long)b * a.N + r / p.G) * a.Hq + hk * p.G + r % p.G) * a.D;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
-            if (d < a.D) out[d] = from_f32<T>(dq[i][c] * back * a.scale);
+            if (d < a.D) out[d] = from_f32<T>(res[c] * a.scale);
         }
     }
 }
 
 // dk and dv of 64 keys: S^T and dP^T per tile of packed rows, dv += P^T do, dk += dS^T q.
-template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dkv_simt(const AttnParams p)
+template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const AttnParams& p, const int block, float* sm)
 {
-    extern __shared__ float sm[];
     constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
     float* K = sm;
     float* V = K + kT * LD;
@@ -476,9 +519,9 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dkv_s
     float* S = P + kT * kPitchP;
     const sdtw_attention& a = p.a;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int heads = a.B * a.Hkv, bh = block % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int j0 = (int)(blockIdx.x / heads) * kT;   // the first keys are seen by the most rows
+    const int j0 = block / heads * kT;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
     // rows that see any key of the tile
     const int j_last = min(j0 + kT, rr.m_b) - 1;
@@ -491,23 +534,23 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dkv_s
     const T* dout = static_cast<const T*>(p.dout);
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
     const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
-    load_tile<T, DP>(K, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
-    load_tile<T, DP>(V, a.D, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
-    float dk[4][NC], dv[4][NC];
+    load_tile<T, DP>(K, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
+    load_tile<T, DP>(V, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
+    unsigned long long dk[4][NC / 2], dv[4][NC / 2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) dk[i][c] = dv[i][c] = 0.f;
+        for (int c = 0; c < NC / 2; ++c) dk[i][c] = dv[i][c] = pk2(0.f, 0.f);
     const float s2 = a.scale * kLog2e, back = ex2(-(float)p.grad_shift);
     const long long info = ((long long)b * a.Hkv + hk) * p.rows_pad;
     for (int r0 = row_lo / kT * kT; r0 < row_hi; r0 += kT) {
         __syncthreads();
-        load_tile<T, DP>(Q, a.D, [&](int i) -> const T* {
+        load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
             return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
         });
-        load_tile<T, DP>(G, a.D, [&](int i) -> const T* {
+        load_tile<T, DP>(G, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
             return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
@@ -541,43 +584,47 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr) attn_dkv_s
         const int j = j0 + ty + 16 * i;
         if (j >= a.M) continue;
         const long long o = (((long long)b * a.M + j) * a.Hkv + hk) * a.D;
+        float rk[NC], rv[NC];
+        unpack(dk[i], back, rk);
+        unpack(dv[i], back, rv);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = Cols<DP>::at(tx, c / Cols<DP>::W, c % Cols<DP>::W);
             if (d < a.D) {
-                if (p.dk) static_cast<T*>(p.dk)[o + d] = from_f32<T>(dk[i][c] * back * a.scale);
-                if (p.dv) static_cast<T*>(p.dv)[o + d] = from_f32<T>(dv[i][c] * back);
+                if (p.dk) static_cast<T*>(p.dk)[o + d] = from_f32<T>(rk[c] * a.scale);
+                if (p.dv) static_cast<T*>(p.dv)[o + d] = from_f32<T>(rv[c]);
             }
         }
     }
 }
 
-template <typename K> cudaError_t launch(K kernel, dim3 grid, size_t smem, const AttnParams& p, cudaStream_t s)
+// Both kinds of CTAs in one launch, the ones that take longer first.
+template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 ? 1 : 2) attn_bwd_simt(const AttnParams p, const int dkv)
 {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThr, smem, s>>>(p);
-    return cudaGetLastError();
+    extern __shared__ float sm[];
+    if ((int)blockIdx.x < dkv) dkv_cta<T, DP>(p, (int)blockIdx.x, sm);
+    else dq_cta<T, DP>(p, (int)blockIdx.x - dkv, sm);
 }
 
 template <typename T, int DP> cudaError_t fwd_simt(const AttnParams& p, cudaStream_t s)
 {
+    constexpr size_t smem = sizeof(float) * (3 * kT * (DP + 4) + kT * kPitchP);
+    const cudaError_t e = allow_smem<attn_fwd_simt<T, DP>>(smem);
+    if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((p.rows + kT - 1) / kT);
-    const size_t smem = sizeof(float) * (3 * kT * (DP + 4) + kT * kPitchP);
-    return launch(attn_fwd_simt<T, DP>, dim3(tiles * p.a.B * p.a.Hkv, p.splits), smem, p, s);
+    attn_fwd_simt<T, DP><<<dim3(tiles * p.a.B * p.a.Hkv, p.splits), kThr, smem, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int DP> cudaError_t bwd_simt(const AttnParams& p, cudaStream_t s)
 {
-    const size_t tile = sizeof(float) * kT * (DP + 4), sq = sizeof(float) * kT * kPitchP;
-    if (p.dq) {
-        const unsigned tiles = (unsigned)((p.rows + kT - 1) / kT);
-        cudaError_t e = launch(attn_dq_simt<T, DP>, dim3(tiles * p.a.B * p.a.Hkv), 4 * tile + sq, p, s);
-        if (e != cudaSuccess) return e;
-    }
-    if (p.dk || p.dv)
-        return launch(attn_dkv_simt<T, DP>, dim3((unsigned)((p.a.M + kT - 1) / kT) * p.a.B * p.a.Hkv), 4 * tile + 2 * sq, p, s);
-    return cudaSuccess;
+    constexpr size_t smem = sizeof(float) * (4 * kT * (DP + 4) + 2 * kT * kPitchP);
+    const cudaError_t e = allow_smem<attn_bwd_simt<T, DP>>(smem);
+    if (e != cudaSuccess) return e;
+    const int heads = p.a.B * p.a.Hkv;
+    const int dkv = p.dk ? (p.a.M + kT - 1) / kT * heads : 0, dq = p.dq ? (p.rows + kT - 1) / kT * heads : 0;
+    attn_bwd_simt<T, DP><<<(unsigned)(dkv + dq), kThr, smem, s>>>(p, dkv);
+    return cudaGetLastError();
 }
 
 template <typename T> cudaError_t fwd_typed(const AttnParams& p, cudaStream_t s)

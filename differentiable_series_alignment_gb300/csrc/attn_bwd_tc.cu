@@ -1,15 +1,16 @@
 // attn_bwd_tc.cu -- attention's backward pass on the tensor cores (bf16 and fp16).
 //
-// Two kernels, each computing P = exp(S - lse) and dS = P (dP - delta) again from q, k, v, do
-// and the row's lse and delta:
-//   attn_dkv_tc_kernel: a CTA holds 128 keys and walks the packed rows that see them;
+// CTAs of two kinds, each computing P = exp(S - lse) and dS = P (dP - delta) again from q, k, v,
+// do and the row's lse and delta:
+//   dkv: a CTA holds 128 keys and walks the packed rows that see them;
 //     S^T = K Q^T and dP^T = V dO^T go to tensor memory, P^T and dS^T come back there as
 //     16-bit A operands, dV += P^T dO and dK += dS^T Q;
-//   attn_dq_tc_kernel: a CTA holds a tile of packed rows and walks their keys;
+//   dq: a CTA holds a tile of packed rows and walks their keys;
 //     S = Q K^T, dP = dO V^T, dQ += dS K.
 // That is 7 products where one kernel would need 5, but no result is summed across CTAs:
 // no atomics, no partial dQ in memory, the same bits every time. The gradients of heads
-// that share keys are summed in the accumulator, as rows of one problem.
+// that share keys are summed in the accumulator, as rows of one problem. Both kinds are one
+// launch: the dkv CTAs, few and long, start first and the dq CTAs fill the SMs that they leave.
 // Warps 0-7 turn scores into probabilities (two warpgroups, half of the columns each), warp 8
 // loads by TMA, warps 9 and 10 issue the products: one S and what P enters, the other dP and
 // what dS enters. While the tensor cores run dV and the next S^T, the warps compute dS^T; while
@@ -29,8 +30,8 @@ template <int DP> struct BwdShape {
     static constexpr uint32_t tile = (DP / 64) * kBox;
     static constexpr int stages = DP == 128 ? 2 : 4;   // dkv: (Q, dO) pairs in flight, 128 KB
     static constexpr int slots = DP == 128 ? 5 : 10;   // dq: K and V tiles in flight, 160 KB
-    static constexpr uint32_t smem_dkv = 2 * tile + 2 * stages * tile + 1024;
-    static constexpr uint32_t smem_dq = 2 * tile + slots * tile + 1024;
+    // with the static arrays, rounded up to 1 KB, all of the 227 KB that a CTA can have
+    static constexpr uint32_t smem_dkv = 2 * tile + 2 * stages * tile, smem_dq = 2 * tile + slots * tile;
 };
 
 __device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -72,19 +73,18 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t img, u
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+__device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, const int block, unsigned char* dyn)
 {
     using Sh = BwdShape<DP>;
-    extern __shared__ unsigned char dyn[];
     __shared__ uint64_t s_kv, s_full[Sh::stages], s_empty[Sh::stages], s_s, s_p, s_dp, s_ds, s_end;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_row[2][2][128];   // -lse and -delta of the tile's rows, two tiles
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int heads = a.B * a.Hkv, bh = block % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows, G = p.G;
-    const int j0 = (int)(blockIdx.x / heads) * kKeys;   // the first keys are seen by the most rows
+    const int j0 = block / heads * kKeys;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
     const int j_last = min(j0 + kKeys, rr.m_b) - 1;
     int t_lo = 0, t_hi = 0;   // tiles of packed rows that see a key of this CTA
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
     t_lo = uniform(t_lo), t_hi = uniform(t_hi);
     const int tiles = t_hi - t_lo;
 
-    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t base = smem_u32(dyn);
     const uint32_t k_img = base, v_img = base + Sh::tile, ring = base + 2 * Sh::tile;
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&s_kv), 1);
@@ -297,25 +297,24 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dkv_tc_kernel(const AttnPar
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+__device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, const int block, unsigned char* dyn)
 {
     using Sh = BwdShape<DP>;
-    extern __shared__ unsigned char dyn[];
     __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_free[2], s_dp, s_ds, s_end;
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
+    const int heads = a.B * a.Hkv, bh = block % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows, G = p.G;
     const int row_tiles = (p.rows + RT - 1) / RT;
-    const int r0 = (row_tiles - 1 - (int)(blockIdx.x / heads)) * RT;
+    const int r0 = (row_tiles - 1 - block / heads) * RT;
     const RowRange rr(a, b);
     Tiles t(rr, r0, min(r0 + RT, p.rows), G);
     t.lo = uniform(t.lo), t.hi = uniform(t.hi);
     const int tiles = t.hi - t.lo;
 
-    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t base = smem_u32(dyn);
     const uint32_t q_img = base, g_img = base + Sh::tile, ring = base + 2 * Sh::tile;
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&s_q), 1);
@@ -502,25 +501,25 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_dq_tc_kernel(const AttnPara
     }
 }
 
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps, const int dkv)
+{
+    extern __shared__ __align__(1024) unsigned char dyn[];   // as the swizzle of the images asks
+    if ((int)blockIdx.x < dkv) dkv_cta<T, DP>(p, maps, (int)blockIdx.x, dyn);
+    else dq_cta<T, DP>(p, maps, (int)blockIdx.x - dkv, dyn);
+}
+
 template <typename T, int DP> cudaError_t run_bwd(const AttnParams& p, const Maps& m, cudaStream_t s)
 {
     using Sh = BwdShape<DP>;
-    const unsigned heads = (unsigned)(p.a.B * p.a.Hkv);
-    if (p.dk) {
-        auto kern = attn_dkv_tc_kernel<T, DP>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem_dkv);
-        if (e != cudaSuccess) return e;
-        kern<<<(unsigned)((p.a.M + kKeys - 1) / kKeys) * heads, kThreadsB, Sh::smem_dkv, s>>>(p, m);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (p.dq) {
-        auto kern = attn_dq_tc_kernel<T, DP>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem_dq);
-        if (e != cudaSuccess) return e;
-        kern<<<(unsigned)((p.rows + p.tile_rows - 1) / p.tile_rows) * heads, kThreadsB, Sh::smem_dq, s>>>(p, m);
-        return cudaGetLastError();
-    }
-    return cudaSuccess;
+    constexpr uint32_t smem = Sh::smem_dkv > Sh::smem_dq ? Sh::smem_dkv : Sh::smem_dq;
+    const cudaError_t e = allow_smem<attn_bwd_tc_kernel<T, DP>>(smem);
+    if (e != cudaSuccess) return e;
+    const int heads = p.a.B * p.a.Hkv;
+    const int dkv = p.dk ? (p.a.M + kKeys - 1) / kKeys * heads : 0;
+    const int dq = p.dq ? (p.rows + p.tile_rows - 1) / p.tile_rows * heads : 0;
+    attn_bwd_tc_kernel<T, DP><<<(unsigned)(dkv + dq), kThreadsB, smem, s>>>(p, m, dkv);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
 template <typename T, int DP> cudaError_t run_fwd(const AttnParams& p, const Maps& m, cudaStream_t s)
 {
     auto kern = attn_fwd_tc_kernel<T, DP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdShape<DP>::smem);
+    cudaError_t e = allow_smem<attn_fwd_tc_kernel<T, DP>>(FwdShape<DP>::smem);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)((p.rows + 2 * p.tile_rows - 1) / (2 * p.tile_rows));
     kern<<<dim3(pairs * p.a.B * p.a.Hkv, p.splits), kThreadsF, FwdShape<DP>::smem, s>>>(p, m);

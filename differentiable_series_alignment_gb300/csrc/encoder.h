@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/sdtw.h"
@@ -33,6 +34,19 @@ template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack {
 
 inline int dtype_size(int dtype) { return dtype == SDTW_F32 ? 4 : 2; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Allows a kernel its dynamic shared memory, once per device.
+template <auto Kernel> cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 struct NormParams {
     const void *x, *weight, *bias, *dy;
@@ -87,6 +101,7 @@ struct AttnParams {
     float *norm_rows, *norm_keys;
     float* row_delta;         // [B][Hkv][rows_pad]: sum_d do * o
     int rows_pad;             // rows rounded up to 128
+    bool packed;              // rows of four-element packs: D, strides and addresses allow them
     // tensor-core kernels
     bool tc;                  // taken by them (attn_tc_fits)
     int tile_rows;            // packed rows of a tile: whole positions, up to 128

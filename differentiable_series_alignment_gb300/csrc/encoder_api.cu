@@ -47,7 +47,7 @@ sdtw_status check_attention(const sdtw_attention* a)
     if (a->window_left < -1 || a->window_right < -1) return SDTW_ERR_ARG;
     if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return SDTW_ERR_ARG;
     // 32-bit positions, packed rows and grids (of at least 64-row tiles)
-    const long long G = a->Hq / a->Hkv, heads = (long long)a->B * a->Hkv, most = 1ll << 28;
+    const long long G = a->Hq / a->Hkv, heads = (long long)a->B * a->Hkv, most = 1ll << 27;
     if (a->D > 128 || a->N * G > most || a->M > most || heads > most || ((a->N * G + 63) / 64) * heads > most || ((a->M + 63ll) / 64) * heads > most ||
         (a->N * G + 127) / 8 * heads > most)
         return SDTW_ERR_TOO_LARGE;
@@ -92,6 +92,8 @@ AttnParams attn_params(const sdtw_attention* a)
     p.rows = a->N * p.G;
     p.rows_pad = (p.rows + 127) / 128 * 128;
     p.tc = attn_tc_fits(*a);
+    p.packed = a->D % 4 == 0 && aligned16(a->q) && aligned16(a->k) && aligned16(a->v);
+    for (int i = 0; i < 3; ++i) p.packed = p.packed && a->q_stride[i] % 4 == 0 && a->k_stride[i] % 4 == 0 && a->v_stride[i] % 4 == 0;
     p.tile_rows = p.tc ? 128 / p.G * p.G : 64;
     // a single row tile has its key tiles done two at a time
     p.splits = p.tc ? key_splits(p, p.rows <= p.tile_rows ? p.tile_rows : 2 * p.tile_rows, p.rows <= p.tile_rows ? 256 : 128, 1, 5., 1.5)
@@ -263,6 +265,7 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
         p.norm_rows = p.norm_keys = nullptr;
         p.grad_shift = 32;
     }
+    p.packed = p.packed && aligned16(dout);
     ENC_CUDA(launch_attn_rowinfo(p, st));
     ENC_CUDA(p.tc ? launch_attn_backward_tc(p, st) : launch_attn_backward_simt(p, st));
     return SDTW_OK;

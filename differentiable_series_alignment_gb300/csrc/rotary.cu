@@ -15,10 +15,25 @@ namespace {
 
 constexpr int kRotThreads = 256;
 
+// n pairs' cosines and sines, two pairs a load where they come in pairs
+template <int N> __device__ __forceinline__ void turns_of(const float2* row, float2 (&cs)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float4 t = *reinterpret_cast<const float4*>(row + e);
+            cs[e] = make_float2(t.x, t.y), cs[e + 1] = make_float2(t.z, t.w);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) cs[e] = row[e];
+    }
+}
+
 // A unit is 16 bytes of one feature row (VEC features): for halves it is VEC pairs, that
-// is VEC features of each half; the units after them copy the features from R on.
+// is VEC features of each half; the units after them copy the features from R on. A thread
+// has one unit of one token and goes through heads HEADS at a time, its cosines in registers.
 template <typename T, int VEC, int HEADS>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p)
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryParams p)
 {
     using P = Pack<T, VEC>;
     const int half = p.R / 2;
@@ -27,8 +42,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     const int heads = p.H[0] + (p.in[1] ? p.H[1] : 0);
     const long long items = (long long)p.B * p.N * units;
     for (long long it = (long long)blockIdx.x * kRotThreads + threadIdx.x; it < items;
-         it += (long long)gridDim.x * kRotThreads)
-      for (int g = blockIdx.y; g * HEADS < heads; g += gridDim.y) {
+         it += (long long)gridDim.x * kRotThreads) {
         // 32-bit division wherever the sizes allow it: two of 64 bits cost more than the turns
         long long token;
         int u;
@@ -44,90 +58,72 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
         const bool turn = u < turns;
         const int c0 = turn ? u * VEC : p.R + (u - turns) * VEC;   // first feature of the unit
         const bool two = turn && !p.interleaved;                    // its partners are half further on
-        const T* src[HEADS];
-        T* dst[HEADS];
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            const int head = g * HEADS + h;
-            const int w = head >= p.H[0];
-            const int hh = head - (w ? p.H[0] : 0);
-            const bool live = head < heads;
-            src[h] = live ? static_cast<const T*>(p.in[w]) + (b * p.stride[w][0] + n * p.stride[w][1] + hh * p.stride[w][2]) + c0
-                          : nullptr;
-            dst[h] = live ? static_cast<T*>(p.out[w]) + (((long long)b * p.N + n) * p.H[w] + hh) * p.D + c0 : nullptr;
-        }
-        P va[HEADS], vb[HEADS];
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            if (src[h]) {
-                va[h] = *reinterpret_cast<const P*>(src[h]);
-                if (two) vb[h] = *reinterpret_cast<const P*>(src[h] + half);
-            }
+        // cosines and sines of the unit's pairs; a lone feature (VEC 1) has its neighbour's
+        float2 cs[VEC];
+        int mate = 0;   // VEC 1, interleaved: where the partner is
         if (turn) {
             const int pos = p.positions ? p.positions[b * p.pos_stride_b + n] : n;
             // a position outside the table has no angle: its features become NaN
             const bool known = pos >= 0 && pos < p.length;
             const float2* row = reinterpret_cast<const float2*>(p.table) + (long long)(known ? pos : 0) * half;
-            const float nan = __int_as_float(0x7fffffff);
+            constexpr int PAIRS = VEC >= 2 ? VEC / 2 : 1;
             if (p.interleaved) {
-                if (VEC >= 2) {
-                    constexpr int PAIRS = VEC >= 2 ? VEC / 2 : 1;
-                    float2 cs[PAIRS];
+                float2 few[PAIRS];
+                turns_of<PAIRS>(row + c0 / 2, few);
 #pragma unroll
-                    for (int e = 0; e < PAIRS; ++e) {
-                        cs[e] = row[c0 / 2 + e];
-                        if (p.inverse) cs[e].y = -cs[e].y;
-                        if (!known) cs[e] = make_float2(nan, nan);
-                    }
-#pragma unroll
-                    for (int h = 0; h < HEADS; ++h)
-                        if (src[h]) {
-#pragma unroll
-                            for (int e = 0; e < PAIRS; ++e) {
-                                const float a = to_f32(va[h].e[(2 * e) % VEC]), c = to_f32(va[h].e[(2 * e + 1) % VEC]);
-                                va[h].e[(2 * e) % VEC] = from_f32<T>(a * cs[e].x - c * cs[e].y);
-                                va[h].e[(2 * e + 1) % VEC] = from_f32<T>(c * cs[e].x + a * cs[e].y);
-                            }
-                            *reinterpret_cast<P*>(dst[h]) = va[h];
-                        }
-                } else {
-                    // one feature: its partner is its neighbour
-                    float2 cs = row[c0 / 2];
-                    if (p.inverse) cs.y = -cs.y;
-                    if (!known) cs = make_float2(nan, nan);
-                    const int mate = (c0 & 1) ? -1 : 1;
-#pragma unroll
-                    for (int h = 0; h < HEADS; ++h)
-                        if (src[h]) {
-                            const float a = to_f32(va[h].e[0]), c = to_f32(src[h][mate]);
-                            dst[h][0] = from_f32<T>(a * cs.x - (float)mate * c * cs.y);
-                        }
-                }
+                for (int e = 0; e < PAIRS; ++e) cs[e] = few[e];
+                if (VEC == 1) mate = (c0 & 1) ? -1 : 1;
             } else {
-                float2 cs[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    cs[e] = row[c0 + e];
-                    if (p.inverse) cs[e].y = -cs[e].y;
-                    if (!known) cs[e] = make_float2(nan, nan);
-                }
-#pragma unroll
-                for (int h = 0; h < HEADS; ++h)
-                    if (src[h]) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float a = to_f32(va[h].e[e]), c = to_f32(vb[h].e[e]);
-                            va[h].e[e] = from_f32<T>(a * cs[e].x - c * cs[e].y);
-                            vb[h].e[e] = from_f32<T>(c * cs[e].x + a * cs[e].y);
-                        }
-                        *reinterpret_cast<P*>(dst[h]) = va[h];
-                        *reinterpret_cast<P*>(dst[h] + half) = vb[h];
-                    }
+                turns_of<VEC>(row + c0, cs);
             }
-        } else {
+            const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-                if (src[h]) *reinterpret_cast<P*>(dst[h]) = va[h];
+            for (int e = 0; e < VEC; ++e) {
+                if (p.inverse) cs[e].y = -cs[e].y;
+                if (!known) cs[e] = make_float2(nan, nan);
+            }
+        }
+        const long long in0 = b * p.stride[0][0] + n * p.stride[0][1] + c0, in1 = b * p.stride[1][0] + n * p.stride[1][1] + c0;
+        const long long out0 = token * p.H[0] * p.D + c0, out1 = token * p.H[1] * p.D + c0;
+        for (int h0 = blockIdx.y * HEADS; h0 < heads; h0 += gridDim.y * HEADS) {
+            const T* src[HEADS];
+            T* dst[HEADS];
+            P va[HEADS], vb[HEADS];
+#pragma unroll
+            for (int q = 0; q < HEADS; ++q) {
+                const int h = h0 + q, w = h >= p.H[0], hh = w ? h - p.H[0] : h;
+                if (h >= heads) continue;
+                src[q] = w ? static_cast<const T*>(p.in[1]) + in1 + hh * p.stride[1][2]
+                           : static_cast<const T*>(p.in[0]) + in0 + hh * p.stride[0][2];
+                dst[q] = w ? static_cast<T*>(p.out[1]) + out1 + (long long)hh * p.D : static_cast<T*>(p.out[0]) + out0 + (long long)hh * p.D;
+                va[q] = *reinterpret_cast<const P*>(src[q]);
+                if (two) vb[q] = *reinterpret_cast<const P*>(src[q] + half);
+                else if (VEC == 1 && turn) vb[q].e[0] = src[q][mate];
+            }
+#pragma unroll
+            for (int q = 0; q < HEADS; ++q) {
+                if (h0 + q >= heads) continue;
+                if (two) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float x = to_f32(va[q].e[e]), y = to_f32(vb[q].e[e]);
+                        va[q].e[e] = from_f32<T>(x * cs[e].x - y * cs[e].y);
+                        vb[q].e[e] = from_f32<T>(y * cs[e].x + x * cs[e].y);
+                    }
+                    *reinterpret_cast<P*>(dst[q] + half) = vb[q];
+                } else if (turn && VEC == 1) {
+                    const float x = to_f32(va[q].e[0]), y = to_f32(vb[q].e[0]);
+                    va[q].e[0] = from_f32<T>(x * cs[0].x - (float)mate * y * cs[0].y);
+                } else if (turn) {
+#pragma unroll
+                    for (int e = 0; e + 1 < VEC; e += 2) {
+                        const float x = to_f32(va[q].e[e]), y = to_f32(va[q].e[e + 1]);
+                        va[q].e[e] = from_f32<T>(x * cs[e / 2].x - y * cs[e / 2].y);
+                        va[q].e[e + 1] = from_f32<T>(y * cs[e / 2].x + x * cs[e / 2].y);
+                    }
+                }
+                *reinterpret_cast<P*>(dst[q]) = va[q];
+            }
         }
     }
 }
@@ -137,13 +133,18 @@ template <typename T, int VEC> cudaError_t run_rotary(const RotaryParams& p, cud
     const int heads = p.H[0] + (p.in[1] ? p.H[1] : 0);
     const int units = (p.interleaved ? p.R : p.R / 2) / VEC + (p.D - p.R) / VEC;
     const long long one = (long long)p.B * p.N * units;
-    // four heads a thread reuse its cosines; one a thread where that would leave SMs idle
-    const bool many = one * ((heads + 3) / 4) >= 152ll * 4 * kRotThreads;
     long long x = (one + kRotThreads - 1) / kRotThreads;
     if (x > 1 << 24) x = 1 << 24;
-    const int groups = many ? (heads + 3) / 4 : heads;
-    const dim3 grid((unsigned)x, (unsigned)(groups < 65535 ? groups : 65535));
-    if (many) rotary_kernel<T, VEC, 4><<<grid, kRotThreads, 0, s>>>(p);
+    // the heads are shared out over as many CTAs as fill the SMs twice over (three are resident);
+    // a thread takes two heads at a time, one where there is too little work for that
+    const long long full = 152ll * 6;
+    const bool pairs = x * ((heads + 1) / 2) >= full;
+    const long long steps = pairs ? (heads + 1) / 2 : heads;
+    long long y = (full + x - 1) / x;
+    y = y > steps ? steps : y;
+    y = y > 65535 ? 65535 : y;
+    const dim3 grid((unsigned)x, (unsigned)y);
+    if (pairs) rotary_kernel<T, VEC, 2><<<grid, kRotThreads, 0, s>>>(p);
     else rotary_kernel<T, VEC, 1><<<grid, kRotThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -152,7 +153,7 @@ template <typename T> cudaError_t rotary_typed(const RotaryParams& p, cudaStream
 {
     constexpr int VEC = 16 / sizeof(T);
     bool packed = p.D % VEC == 0 && (p.interleaved ? p.R : p.R / 2) % VEC == 0 && (p.D - p.R) % VEC == 0 &&
-                  (reinterpret_cast<uintptr_t>(p.table) & 7) == 0;
+                  aligned16(p.table) && p.R % 4 == 0;
     for (int w = 0; w < 2; ++w)
         if (p.in[w]) {
             packed = packed && aligned16(p.in[w]) && aligned16(p.out[w]);
