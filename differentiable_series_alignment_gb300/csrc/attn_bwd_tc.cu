@@ -282,10 +282,10 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         const float unlift = ex2(-(float)p.grad_shift), more = half ? a.scale / gs : 1.f;
         const bool some = tiles > 0 && live;
         const long long at = key < a.M ? (((long long)b * a.M + key) * a.Hkv + hk) * a.D : -1;
-#pragma unroll
+#pragma unroll 1
         for (int f = 0; f < DP; f += 64)
             write_rows<T, 64>(base + (uint32_t)(half * 4 + quarter) * 32 * 128, (half ? c_dk : c_dv) + lanes + f, tiles > 0 && ok,
-                              false, ok && !some, ok ? unlift : NAN, 0.f, more, false, half ? p.dk : p.dv, at < 0 ? at : at + f,
+                              false, ok && !some, ok ? unlift : NAN, 0.f, more, half ? p.dk : p.dv, nullptr, at < 0 ? at : at + f,
                               min(64, a.D - f) / 8, lane);
     }
     fence_before_sync();
@@ -491,7 +491,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         constexpr int F = DP / 2;
         const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + half * F : -1;
         write_rows<T, F>(base + (uint32_t)(half * 4 + quarter) * 32 * F * 2, c_dq + lanes + half * F, tiles > 0 && ok,
-                         false, ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, false, p.dq, at, min(F, a.D - half * F) / 8, lane);
+                         false, ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, p.dq, nullptr, at, min(F, a.D - half * F) / 8, lane);
     }
     fence_before_sync();
     __syncthreads();
@@ -505,6 +505,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps, const int dkv)
 {
     extern __shared__ __align__(1024) unsigned char dyn[];   // as the swizzle of the images asks
+    if (threadIdx.x == kWork) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v), prefetch_map(&maps.dout);
     if ((int)blockIdx.x < dkv) dkv_cta<T, DP>(p, maps, (int)blockIdx.x, dyn);
     else dq_cta<T, DP>(p, maps, (int)blockIdx.x - dkv, dyn);
 }

@@ -1,6 +1,6 @@
 // attn_fwd_tc.cu -- attention's forward pass on the tensor cores (bf16 and fp16).
 //
-// One CTA takes two tiles of up to 128 packed rows and walks the visible keys in tiles of
+// One CTA takes NT = 2 tiles of up to 128 packed rows and walks the visible keys in tiles of
 // 128. Two warps issue S_w = Q_w K^T and O_w += P_w V, a warp a row tile w, so that the tensor
 // cores work on one tile while the other's softmax runs and its issuing warp waits. Four
 // warps are a tile's softmax, a thread a row; one more warp feeds a ring of K and V tiles by
@@ -12,9 +12,21 @@
 // joined at the end. Every tile's way through scores, softmax and product is a chain of some
 // 2700 cycles, longer than its K and V take to arrive.
 //
+// NT = 1 is the same with one tile of rows, half of the tensor memory and less than half of the
+// shared memory: for heads of up to 64 two such CTAs share an SM and one's start and end go
+// under the other's products (32 x 512 samples, 8 heads of 64: 47 us with NT = 2), and wider
+// heads take it where there are too few tiles for every SM.
+//
 // The running maximum is renewed only when a row's scores rise by more than 2^8 over it, so
 // that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
 // then at most 2^8, which fp32 sums and 16-bit operands take as well as 1.
+//
+// Probabilities are rounded to 16 bits for their product with V. Where a backward pass will
+// follow, O is divided by the sum of the rounded ones: their errors then enter delta = do . o only
+// by how they differ from key to key, as those of dS itself do. Divided by the exact sum, which
+// lse keeps, dq was up to 1.9 times as far from its 64-bit value as a plain fp32 pass.
+#include <type_traits>
+
 #include "attn_tc.cuh"
 
 namespace sdtw {
@@ -23,39 +35,43 @@ namespace {
 
 __device__ int g_status;
 
-constexpr int kThreadsF = 352;   // 8 softmax warps, one that loads, two that issue
-constexpr int kLoader = 8, kIssuer = 9;
 constexpr float kLazy = 8.f;   // log2 of how far scores may rise over the maximum in use
 
-template <int DP> struct FwdShape {
+template <int DP, int NT> struct FwdShape {
+    static constexpr int loader = 4 * NT, issuer = loader + 1;   // warps: 4 a tile for its softmax, then these
+    static constexpr int threads = 32 * (issuer + NT);
     static constexpr uint32_t tile = (DP / 64) * kBox;   // bytes of a row or key tile
-    static constexpr int slots = DP == 128 ? 5 : 10;     // K and V tiles in flight: 160 KB
-    // with the static arrays, rounded up to 1 KB, all of the 227 KB that a CTA can have
-    static constexpr uint32_t smem = 2 * tile + slots * tile;
+    static constexpr int slots = DP == 128 || NT == 1 ? 5 : 10;   // K and V tiles in flight: 160 KB, 80 of two CTAs
+    // two tiles of 128 features: with the static arrays, rounded up to 1 KB, all of the 227 KB
+    // that a CTA can have
+    static constexpr uint32_t smem = NT * tile + slots * tile;
+    static constexpr int columns = 256 * NT;             // of tensor memory: S, then O
 };
 
 // fp16 cannot hold small probabilities in full: 2^7 more of them, up to 2^15 in all.
 template <typename T> struct Lift { static constexpr float v = 0.f; };
 template <> struct Lift<__half> { static constexpr float v = 7.f; };
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
+template <typename T, int DP, int NT>
+__global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) attn_fwd_tc_kernel(const AttnParams p, const __grid_constant__ Maps maps)
 {
-    using Sh = FwdShape<DP>;
+    using Sh = FwdShape<DP, NT>;
+    constexpr int kLoader = Sh::loader, kIssuer = Sh::issuer;
     extern __shared__ __align__(1024) unsigned char dyn[];   // as the swizzle of the images asks
-    __shared__ uint64_t s_q[2], s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_p[2][2], s_o[2], s_end[2], s_turn[2];
-    __shared__ float s_join[2][128];
+    __shared__ uint64_t s_q[NT], s_full[Sh::slots], s_empty[Sh::slots], s_s[NT], s_p[NT][2], s_o[NT], s_end[NT], s_turn[NT];
+    __shared__ float s_join[3][128];
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (warp == kLoader && lane == 0) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v);
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int RT = p.tile_rows;
     // the last rows see the most keys under a causal mask: they start first
-    const int pairs = (p.rows + 2 * RT - 1) / (2 * RT);
-    const int r00 = (pairs - 1 - (int)(blockIdx.x / heads)) * 2 * RT;
+    const int groups = (p.rows + NT * RT - 1) / (NT * RT);
+    const int r00 = (groups - 1 - (int)(blockIdx.x / heads)) * NT * RT;
     const RowRange rr(a, b);
-    Tiles t0(rr, r00, min(r00 + RT, p.rows), p.G), t1(rr, r00 + RT, min(r00 + 2 * RT, p.rows), p.G);
+    Tiles t0(rr, r00, min(r00 + RT, p.rows), p.G), t1(rr, r00 + RT, min(r00 + NT * RT, p.rows), p.G);   // NT 1: t1 is empty
     int T0 = t0.hi == 0 ? t1.lo : t1.hi == 0 ? t0.lo : min(t0.lo, t1.lo), T1 = max(t0.hi, t1.hi);
     if (p.splits > 1) {   // this CTA's share of the key tiles
         const int per = (T1 - T0 + p.splits - 1) / p.splits;
@@ -65,7 +81,8 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         t1.lo = max(t1.lo, T0), t1.hi = min(t1.hi, T1);
     }
     const bool any0 = t0.lo < t0.hi, any1 = t1.lo < t1.hi;
-    const bool alternate = p.rows <= RT;   // one tile of rows: key tiles T0, T0 + 2, .. and T0 + 1, T0 + 3, ..
+    const bool alternate = NT == 2 && p.rows <= RT;   // one tile of rows: key tiles T0, T0 + 2, .. and T0 + 1, T0 + 3, ..
+    const bool solo = NT == 1 || alternate;           // no entry of the ring is read by two warps
     // Ring entries in use. K and V of a tile are neighbours, so with a multiple of four of them an
     // entry always serves the same half: a warp that saw only every other phase of an entry's
     // barrier would take the phase before last for the one it waits for.
@@ -74,11 +91,11 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
     T0 = uniform(T0), T1 = uniform(T1);
     t0.lo = uniform(t0.lo), t0.hi = uniform(t0.hi), t1.lo = uniform(t1.lo), t1.hi = uniform(t1.hi);
 
-    const uint32_t q_img = smem_u32(dyn), ring = q_img + 2 * Sh::tile;
+    const uint32_t q_img = smem_u32(dyn), ring = q_img + NT * Sh::tile;
     // the loader makes the barriers and sends for the first tiles before the CTA has met
     const uint32_t row_bytes = (uint32_t)RT * 128 * (DP / 64);
     if (warp == kLoader && lane == 0) {
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NT; ++w) {
             mbar_init(smem_u32(&s_q[w]), 1);
             mbar_init(smem_u32(&s_s[w]), 1);
             mbar_init(smem_u32(&s_p[w][0]), 4);
@@ -89,7 +106,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         }
         for (int e = 0; e < Sh::slots; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
-            mbar_init(smem_u32(&s_empty[e]), alternate ? 1 : 2);   // issuing warps that read it
+            mbar_init(smem_u32(&s_empty[e]), solo ? 1 : 2);   // issuing warps that read it
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         if (!p.skip && any0) {
@@ -97,7 +114,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             load_rows<DP>(q_img, &maps.q, r00 / p.G, hk, b, smem_u32(&s_q[0]));
         }
     }
-    if (warp == kIssuer) tmem_alloc(&s_tmem, 512);
+    if (warp == kIssuer) tmem_alloc(&s_tmem, Sh::columns);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -117,9 +134,9 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                 mbar_expect_tx(bar, Sh::tile);
                 load_keys<DP>(ring + e * Sh::tile, (i & 1) ? &maps.v : &maps.k, (T0 + (i >> 1)) * kKeys, hk, b, bar);
                 issued = i + 1;
-                if (i == 0 && any1) {
-                    mbar_expect_tx(smem_u32(&s_q[1]), row_bytes);
-                    load_rows<DP>(q_img + Sh::tile, &maps.q, n0 + RT / p.G, hk, b, smem_u32(&s_q[1]));
+                if (NT == 2 && i == 0 && any1) {
+                    mbar_expect_tx(smem_u32(&s_q[NT - 1]), row_bytes);
+                    load_rows<DP>(q_img + Sh::tile, &maps.q, n0 + RT / p.G, hk, b, smem_u32(&s_q[NT - 1]));
                 }
             }
             // no copy may be writing shared memory when the CTA ends
@@ -127,15 +144,15 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             for (int i = max(0, issued - slots); i < issued; ++i)
                 wait_for(drained, smem_u32(&s_full[i % slots]), (uint32_t)((i / slots) & 1), p.wait_ns, &g_status);
             if (any0) wait_for(drained, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
-            if (any1 && issued > 0) wait_for(drained, smem_u32(&s_q[1]), 0, p.wait_ns, &g_status);
+            if (NT == 2 && any1 && issued > 0) wait_for(drained, smem_u32(&s_q[NT - 1]), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp == kIssuer || warp == kIssuer + 1) {
+    } else if (warp >= kIssuer) {
         const int w = warp - kIssuer;
         const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
-        const uint32_t s_col = tmem + w * 128, o_col = tmem + 256 + w * 128, q = q_img + (alternate ? 0 : w) * Sh::tile;
+        const uint32_t s_col = tmem + w * 128, o_col = tmem + NT * 128 + w * 128, q = q_img + (alternate ? 0 : w) * Sh::tile;
         // The two warps take turns, O_w of a tile and S_w of the next at a time. Left to themselves
         // their products interleave, both tiles' scores come late and together, and so do both
         // softmaxes, with the tensor cores idle meanwhile.
@@ -151,7 +168,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
                 wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)(i & 1), p.wait_ns, &g_status);
-                if (part == 0 && !alternate) take_turn(j);
+                if (part == 0 && !solo) take_turn(j);
                 fence_after_sync();
                 if (ok && elect_one()) {
 #pragma unroll
@@ -170,14 +187,14 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             __syncwarp();
         };
-        if (alternate) {
-            const int own = (T1 - T0 + 1 - w) / 2;
+        if (solo) {
+            const int step = NT == 1 ? 1 : 2, own = (T1 - T0 - w + step - 1) / step;
             for (int i = -1; i < own; ++i) {
-                const int iv = 2 * (2 * i + w) + 1, ik = 2 * (2 * (i + 1) + w);   // ring entries
+                const int iv = 2 * (step * i + w) + 1, ik = 2 * (step * (i + 1) + w);   // ring entries
                 if (i >= 0) {
                     const int e = iv % slots;
                     wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((iv / slots) & 1), p.wait_ns, &g_status);
-                    products(ring + (uint32_t)e * Sh::tile, T0 + 2 * i + w, i, i == own - 1);
+                    products(ring + (uint32_t)e * Sh::tile, T0 + step * i + w, i, i == own - 1);
                     if (ok && elect_one()) mma_commit(smem_u32(&s_empty[e]));
                     __syncwarp();
                 }
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         }
         int e_v = slots - 1, e_k = 0;   // ring entries of V(j) and K(j + 1)
         uint32_t ph_v = 1, ph_k = 0;        // and the parities of their arrivals
-        for (int j = T0 - 1; j < T1 && !alternate; ++j) {
+        for (int j = T0 - 1; j < T1 && !solo; ++j) {
             // a warp gives every entry back once it is there, also those that its tile does not see:
             // one that ran ahead would give back an entry's next use for its last
             if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
@@ -206,7 +223,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             }
             if (!(j >= lo && j < hi) && !(j + 1 >= lo && j + 1 < hi)) take_turn(j);
             if (ok && elect_one()) {
-                mbar_arrive(smem_u32(&s_turn[w ^ 1]));
+                mbar_arrive(smem_u32(&s_turn[(w + 1) % NT]));
                 if (j >= T0) mma_commit(smem_u32(&s_empty[e_v]));
                 if (j + 1 < T1) mma_commit(smem_u32(&s_empty[e_k]));
             }
@@ -231,10 +248,11 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
         const bool live = mine && n < rr.n_b;
         const int klo = live ? rr.lo(n) : 0, khi = live ? max(klo, rr.hi(n)) : 0;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + 256 + w * 128;
+        const uint32_t s_col = tmem + lanes + w * 128, o_col = tmem + lanes + NT * 128 + w * 128;
         const float s2 = a.scale * kLog2e;
         const int o_cols = (a.D + 15) / 16 * 16;
-        float m = -INFINITY, top = -INFINITY, off = 0.f, l = 0.f;   // maximum in use, its trigger, its base
+        float m = -INFINITY, top = -INFINITY, off = 0.f;   // maximum in use, its trigger, its base
+        float l = 0.f, lr = 0.f;                           // sums of the probabilities, exact and rounded
         for (int j = lo, i = 0; j < hi; j += step, ++i) {
             wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)(i & 1), p.wait_ns, &g_status);
             fence_after_sync();
@@ -260,6 +278,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                 m = fmaxf(m, now);
                 const float keep = m == old ? 1.f : ex2((old - m) * s2);
                 l *= keep;
+                lr *= keep;
                 off = (m == -INFINITY ? 0.f : m * s2) - Lift<T>::v;
                 top = m + kLazy / s2;
                 if (i > 0) {
@@ -274,31 +293,41 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
                 }
             }
             const unsigned long long mul = pk2(s2, s2), sub = pk2(-off, -off);
-            unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
+            unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f), seen2 = pk2(0.f, 0.f);
+            auto exps = [&](auto train) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t u[16];
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t u[16];
 #pragma unroll
-                for (int q = 0; q < 32; q += 4) {
-                    float e[4];
-                    upk2(fma2(pk2(s[c + q], s[c + q + 1]), mul, sub), e[0], e[1]);
-                    upk2(fma2(pk2(s[c + q + 2], s[c + q + 3]), mul, sub), e[2], e[3]);
+                    for (int q = 0; q < 32; q += 4) {
+                        float e[4];
+                        upk2(fma2(pk2(s[c + q], s[c + q + 1]), mul, sub), e[0], e[1]);
+                        upk2(fma2(pk2(s[c + q + 2], s[c + q + 3]), mul, sub), e[2], e[3]);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
-                    sum0 = add2(sum0, pk2(e[0], e[1]));
-                    sum1 = add2(sum1, pk2(e[2], e[3]));
-                    u[q / 2] = pack2<T>(e[0], e[1]);
-                    u[q / 2 + 1] = pack2<T>(e[2], e[3]);
+                        for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
+                        sum0 = add2(sum0, pk2(e[0], e[1]));
+                        sum1 = add2(sum1, pk2(e[2], e[3]));
+                        u[q / 2] = pack2<T>(e[0], e[1]);
+                        u[q / 2 + 1] = pack2<T>(e[2], e[3]);
+                        if (train) seen2 = add2(seen2, add2(unpack2<T>(u[q / 2]), unpack2<T>(u[q / 2 + 1])));
+                    }
+                    tmem_st16(s_col + c / 2, u);
+                    if (c == 32) {   // the first 64 keys are there
+                        tmem_wait_st();
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
+                    }
                 }
-                tmem_st16(s_col + c / 2, u);
-                if (c == 32) {   // the first 64 keys are there
-                    tmem_wait_st();
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
-                }
-            }
+            };
             float x, y;
+            if (p.out_rest) {
+                exps(std::true_type{});
+                upk2(seen2, x, y);
+                lr += x + y;
+            } else {
+                exps(std::false_type{});
+            }
             upk2(add2(sum0, sum1), x, y);
             l += x + y;
             tmem_wait_st();
@@ -311,10 +340,11 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        float mul = 0.f, mul1 = 0.f, total = l;
-        if (alternate) {   // warps 0-3 join the two; a lane's row lies in the same lane of O_0 and O_1
+        if (!p.out_rest) lr = l;
+        float mul = 0.f, mul1 = 0.f, total = l, by = lr;
+        if (NT == 2 && alternate) {   // warps 0-3 join the two; a lane's row lies in the same lane of O_0 and O_1
             const int row = quarter * 32 + lane;
-            if (w == 1) s_join[0][row] = l == 0.f ? -INFINITY : off, s_join[1][row] = l;
+            if (w == 1) s_join[0][row] = l == 0.f ? -INFINITY : off, s_join[1][row] = l, s_join[2][row] = lr;
             fence_before_sync();
             asm volatile("bar.sync 1, 256;" ::: "memory");
             fence_after_sync();
@@ -324,13 +354,14 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             mul = l == 0.f ? 0.f : ex2(off - both);
             mul1 = off1 == -INFINITY ? 0.f : ex2(off1 - both);
             total = l * mul + l1 * mul1;
+            by = lr * mul + s_join[2][row] * mul1;
             off = both;
         } else {
             mul = 1.f;
         }
         if (!(alternate && w == 1)) {
             const bool seen = live && read && total != 0.f;
-            const float inv = !ok ? NAN : seen ? 1.f / total : 0.f;
+            const float inv = !ok ? NAN : seen ? 1.f / by : 0.f;
             const float lse2 = !ok ? NAN : seen ? off + log2f(total) : -INFINITY;
             read = read && ok;
             other = other && ok;
@@ -340,18 +371,18 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
             const uint32_t area = q_img + w * Sh::tile + (uint32_t)(quarter * 32 * DP * 2);
             if (p.splits > 1) {
                 const long long place = mine ? ((((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r) : -1;
-#pragma unroll
+#pragma unroll 1
                 for (int f = 0; f < DP; f += 32)
                     write_rows_f32<32>(area, o_col + f, read, other, ok && !seen, mul, mul1, p.part_o,
                                        mine ? place * a.D + f : -1, min(32, a.D - f) / 4, lane);
                 if (mine) p.part_lse[place] = lse2 * kLn2;
             } else {
                 const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D : -1;
-                for (int pass = 0; pass < (p.out_rest ? 2 : 1); ++pass)
-#pragma unroll
-                    for (int f = 0; f < DP; f += 64)
-                        write_rows<T, 64>(area, o_col + f, read, other, ok && !seen, mul, mul1, 1.f, pass == 1,
-                                          pass ? p.out_rest : p.out, mine ? at + f : -1, min(64, a.D - f) / 8, lane);
+                constexpr int F = DP / 2;   // at a time: the area holds them and what their rounding leaves
+#pragma unroll 1
+                for (int f = 0; f < DP; f += F)
+                    write_rows<T, F>(area, o_col + f, read, other, ok && !seen, mul, mul1, 1.f, p.out, p.out_rest,
+                                     mine ? at + f : -1, min(F, a.D - f) / 8, lane);
                 if (mine && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse2 * kLn2;
             }
         }
@@ -360,18 +391,23 @@ __global__ void __launch_bounds__(kThreadsF, 1) attn_fwd_tc_kernel(const AttnPar
     __syncthreads();
     if (warp == kIssuer) {
         fence_after_sync();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, Sh::columns);
     }
 }
 
-template <typename T, int DP> cudaError_t run_fwd(const AttnParams& p, const Maps& m, cudaStream_t s)
+template <typename T, int DP, int NT> cudaError_t run_fwd(const AttnParams& p, const Maps& m, cudaStream_t s)
 {
-    auto kern = attn_fwd_tc_kernel<T, DP>;
-    cudaError_t e = allow_smem<attn_fwd_tc_kernel<T, DP>>(FwdShape<DP>::smem);
+    using Sh = FwdShape<DP, NT>;
+    const cudaError_t e = allow_smem<attn_fwd_tc_kernel<T, DP, NT>>(Sh::smem);
     if (e != cudaSuccess) return e;
-    const unsigned pairs = (unsigned)((p.rows + 2 * p.tile_rows - 1) / (2 * p.tile_rows));
-    kern<<<dim3(pairs * p.a.B * p.a.Hkv, p.splits), kThreadsF, FwdShape<DP>::smem, s>>>(p, m);
+    const unsigned groups = (unsigned)((p.rows + NT * p.tile_rows - 1) / (NT * p.tile_rows));
+    attn_fwd_tc_kernel<T, DP, NT><<<dim3(groups * p.a.B * p.a.Hkv, p.splits), Sh::threads, Sh::smem, s>>>(p, m);
     return cudaGetLastError();
+}
+template <typename T> cudaError_t pick_fwd(const AttnParams& p, const Maps& m, cudaStream_t s)
+{
+    if (p.row_tiles == 1) return p.a.D <= 64 ? run_fwd<T, 64, 1>(p, m, s) : run_fwd<T, 128, 1>(p, m, s);
+    return p.a.D <= 64 ? run_fwd<T, 64, 2>(p, m, s) : run_fwd<T, 128, 2>(p, m, s);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -432,9 +468,7 @@ cudaError_t launch_attn_forward_tc(const AttnParams& p, cudaStream_t s)
     if (!atc::map_rows(&m.q, a.q, a.q_stride, a, p.G, p.tile_rows) || !atc::map_keys(&m.k, a.k, a.k_stride, a) ||
         !atc::map_keys(&m.v, a.v, a.v_stride, a))
         return cudaErrorInvalidValue;
-    if (a.dtype == SDTW_BF16)
-        return a.D <= 64 ? atc::run_fwd<__nv_bfloat16, 64>(p, m, s) : atc::run_fwd<__nv_bfloat16, 128>(p, m, s);
-    return a.D <= 64 ? atc::run_fwd<__half, 64>(p, m, s) : atc::run_fwd<__half, 128>(p, m, s);
+    return a.dtype == SDTW_BF16 ? atc::pick_fwd<__nv_bfloat16>(p, m, s) : atc::pick_fwd<__half>(p, m, s);
 }
 
 cudaError_t attn_forward_take_status(int* out, cudaStream_t s)

@@ -104,6 +104,10 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* m, in
     for (int c = 0; c < DP / 64; ++c) tma4(dst + c * kBox, m, c * 64, j0, hk, b, bar);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // One warp clears rows [from, 128) of an image that a product over its rows is about to
 // read: what lies beyond a sequence's length may be NaN, and 0 * NaN is not 0.
 template <int DP> __device__ __forceinline__ void clear_rows(uint32_t img, int from, int lane) {
@@ -167,6 +171,14 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// the values that pack2 made, as a packed fp32 pair
+template <typename T> __device__ __forceinline__ unsigned long long unpack2(uint32_t v) {
+    const T* h = reinterpret_cast<const T*>(&v);
+    return pk2(to_f32(h[0]), to_f32(h[1]));
+}
+template <> __device__ __forceinline__ unsigned long long unpack2<__nv_bfloat16>(uint32_t v) {
+    return pk2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
 __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -195,7 +207,7 @@ template <int F> __device__ __forceinline__ void stage_out(uint32_t area, void* 
     constexpr int PER = F / 8;
     __syncwarp();
     const int c = lane % PER;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < PER; ++i) {
         const int row = i * (32 / PER) + lane / PER;
         const long long o = __shfl_sync(0xffffffffu, at, row);
@@ -229,37 +241,40 @@ __device__ __forceinline__ void read_acc(uint32_t col, bool read, bool other, fl
     }
 }
 // F features of an accumulator (this lane's row, from column col) times mul, and more (apart, so
-// that neither overflows), rounded into out; `zero`: the row is 0 whatever the accumulator
-// holds. rest: what that rounding leaves instead.
+// that neither overflows), rounded into out and, where it is wanted, what the rounding left into
+// rest; `zero`: the row is 0 whatever the accumulator holds. area: 32 * F * 2 bytes, twice that
+// with rest.
 template <typename T, int F>
 __device__ __forceinline__ void write_rows(uint32_t area, uint32_t col, bool read, bool other, bool zero, float mul, float mul1,
-                                           float more, bool rest, void* out, long long at, int pieces, int lane) {
-#pragma unroll
+                                           float more, void* out, void* rest, long long at, int pieces, int lane) {
+#pragma unroll 1   // run once a CTA: what counts is how much code there is to fetch
     for (int f = 0; f < F; f += 16) {
         float o[16];
         read_acc(col + f, read, other, mul, mul1, o);
 #pragma unroll
         for (int q = 0; q < 16; q += 8) {
-            uint32_t w[4];
+            uint32_t w[4], z[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const float x = zero ? 0.f : o[q + 2 * z] * more, y = zero ? 0.f : o[q + 2 * z + 1] * more;
-                w[z] = pack2<T>(x, y);
+            for (int k = 0; k < 4; ++k) {
+                const float x = zero ? 0.f : o[q + 2 * k] * more, y = zero ? 0.f : o[q + 2 * k + 1] * more;
+                w[k] = pack2<T>(x, y);
                 if (rest) {
-                    const T* r = reinterpret_cast<const T*>(&w[z]);
-                    w[z] = pack2<T>(x - to_f32(r[0]), y - to_f32(r[1]));
+                    const T* r = reinterpret_cast<const T*>(&w[k]);
+                    z[k] = pack2<T>(x - to_f32(r[0]), y - to_f32(r[1]));
                 }
             }
             st_shared16(stage_at<F>(area, lane, (f + q) / 8), w);
+            if (rest) st_shared16(stage_at<F>(area + 32 * F * 2, lane, (f + q) / 8), z);
         }
     }
     stage_out<F>(area, out, at, pieces, lane);
+    if (rest) stage_out<F>(area + 32 * F * 2, rest, at, pieces, lane);
 }
 // The same in fp32, F features of 4 bytes in an area of 32 * F * 4 bytes: F / 2 16-bit places.
 template <int F>
 __device__ __forceinline__ void write_rows_f32(uint32_t area, uint32_t col, bool read, bool other, bool zero, float mul, float mul1, float* out,
                                                long long at, int pieces, int lane) {
-#pragma unroll
+#pragma unroll 1
     for (int f = 0; f < F; f += 16) {
         float o[16];
         read_acc(col + f, read, other, mul, mul1, o);

@@ -105,6 +105,7 @@ struct AttnParams {
     // tensor-core kernels
     bool tc;                  // taken by them (attn_tc_fits)
     int tile_rows;            // packed rows of a tile: whole positions, up to 128
+    int row_tiles;            // forward: row tiles of a CTA, 1 or 2
     unsigned long long wait_ns;
     int skip;                 // test hook: nothing is loaded, so that every wait runs out
 };

@@ -95,9 +95,14 @@ AttnParams attn_params(const sdtw_attention* a)
     p.packed = a->D % 4 == 0 && aligned16(a->q) && aligned16(a->k) && aligned16(a->v);
     for (int i = 0; i < 3; ++i) p.packed = p.packed && a->q_stride[i] % 4 == 0 && a->k_stride[i] % 4 == 0 && a->v_stride[i] % 4 == 0;
     p.tile_rows = p.tc ? 128 / p.G * p.G : 64;
-    // a single row tile has its key tiles done two at a time
-    p.splits = p.tc ? key_splits(p, p.rows <= p.tile_rows ? p.tile_rows : 2 * p.tile_rows, p.rows <= p.tile_rows ? 256 : 128, 1, 5., 1.5)
-                    : key_splits(p, 64, 64, 2, 3., 2.);
+    // Row tiles of a tensor-core CTA: see attn_fwd_tc.cu. A single row tile (new samples over a
+    // cache) has its key tiles done two at a time.
+    const bool single = p.rows <= p.tile_rows;
+    const long long tiles = (long long)((p.rows + p.tile_rows - 1) / p.tile_rows) * a->B * a->Hkv;
+    p.row_tiles = single ? (a->M > 128 ? 2 : 1) : a->D <= 64 || tiles < 2ll * device_sms() ? 1 : 2;
+    if (!p.tc) p.splits = key_splits(p, 64, 64, 2, 3., 2.);
+    else if (single && p.row_tiles == 2) p.splits = key_splits(p, p.tile_rows, 256, 1, 5., 1.5);
+    else p.splits = key_splits(p, p.row_tiles * p.tile_rows, 128, p.row_tiles == 1 && a->D <= 64 ? 2 : 1, 5., 1.5);
     p.grad_shift = 32;
     p.wait_ns = debug_wait_ns();
     return p;
