@@ -11,10 +11,14 @@
 // no atomics, no partial dQ in memory, the same bits every time. The gradients of heads
 // that share keys are summed in the accumulator, as rows of one problem. Both kinds are one
 // launch: the dkv CTAs, few and long, start first and the dq CTAs fill the SMs that they leave.
-// Warps 0-7 turn scores into probabilities (two warpgroups, half of the columns each), warp 8
-// loads by TMA, warps 9 and 10 issue the products: one S and what P enters, the other dP and
-// what dS enters. While the tensor cores run dV and the next S^T, the warps compute dS^T; while
-// they run dK and the next dP^T, the next P^T.
+// Sixteen warps turn scores into probabilities (four warpgroups, 32 of the 128 columns each: with
+// 64 each, eight warps were too few to hide the latencies of the chain through them), one more
+// loads by TMA, two issue the products: one S and what P enters, the other dP and what dS
+// enters.
+// The 16-bit operands have tensor memory of their own where it is large enough (dq; dkv of heads of
+// up to 64): the next scores are then made as soon as the last ones have been read. The dkv CTAs
+// of wider heads have P^T over S^T and dS^T over dP^T: while the tensor cores run dV and the next S^T, the warps compute dS^T; while they run dK
+// and the next dP^T, the next P^T.
 #include "attn_tc.cuh"
 
 namespace sdtw {
@@ -23,8 +27,11 @@ namespace {
 
 __device__ int g_status;
 
-constexpr int kThreadsB = 352;
-constexpr int kWork = 256;   // threads of warps 0-7
+constexpr int kWorkers = 16;             // warps
+constexpr int kWork = 32 * kWorkers;     // threads
+constexpr int kLoader = kWorkers, kIssuer = kWorkers + 1;
+constexpr int kThreadsB = kWork + 96;
+constexpr int kCols = 32;                // of a tile's 128 columns, per warp
 
 template <int DP> struct BwdShape {
     static constexpr uint32_t tile = (DP / 64) * kBox;
@@ -34,7 +41,13 @@ template <int DP> struct BwdShape {
     static constexpr uint32_t smem_dkv = 2 * tile + 2 * stages * tile, smem_dq = 2 * tile + slots * tile;
 };
 
-__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A warp's tensor-memory accesses are done: one of the barrier's arrivals.
+__device__ __forceinline__ void done(uint64_t& bar) {
+    fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+}
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 // fp16 operands: dS is scaled by the power of two that keeps |dP - delta| <= 2 |do| |v| below 1
 // for the largest row of do and of v, so that neither small upstream gradients nor large ones
@@ -57,19 +70,15 @@ template <> __device__ __forceinline__ float grad_scale<__half>(const AttnParams
     return ldexpf(1.f, -min(max(e, -100), 100));
 }
 
-// A row of 64 probabilities' or gradients' 16-bit pairs into 32 tensor-memory columns.
-__device__ __forceinline__ void st64(uint32_t col, const uint32_t* u) {
-    tmem_st16(col, u);
-    tmem_st16(col + 16, u + 16);
-}
-
-// dV/dK/dQ += A[128 x 128 from tensor memory] B, B an image read over its rows. A's columns 0-63
-// are at a, 64-127 at a + 64 (each half lies over the half of the scores it came from).
+// dV/dK/dQ += A[128 x 128 from tensor memory] B, B an image read over its rows. A is in 64 columns of
+// its own (APART), or its pairs of 16 lie over the first half of the 32 scores that they came from.
+template <bool APART> __device__ __forceinline__ uint32_t a_col(int part) { return part * (APART ? kCols / 2 : kCols); }
+template <bool APART>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t img, uint32_t id, bool first) {
     const uint64_t bd = sdesc_mn(img);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-        mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, bd + s * 128, id, (!first || s > 0) ? 1u : 0u);
+        mma_ts(d, a + a_col<APART>(s >> 1) + (s & 1) * 8, bd + s * 128, id, (!first || s > 0) ? 1u : 0u);
 }
 
 template <typename T, int DP>
@@ -77,6 +86,9 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
 {
     using Sh = BwdShape<DP>;
     __shared__ uint64_t s_kv, s_full[Sh::stages], s_empty[Sh::stages], s_s, s_p, s_dp, s_ds, s_end;
+    __shared__ uint64_t s_read[2], s_free[2];   // APART: S^T and dP^T read, P^T and dS^T used
+    __shared__ volatile int s_issued;           // else: S^T tiles issued after the first
+    constexpr bool APART = DP == 64;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_row[2][2][128];   // -lse and -delta of the tile's rows, two tiles
     const sdtw_attention& a = p.a;
@@ -107,23 +119,29 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             mbar_init(smem_u32(&s_empty[e]), 2);   // both issuing warps
         }
         mbar_init(smem_u32(&s_s), 1);
-        mbar_init(smem_u32(&s_p), 8);
+        mbar_init(smem_u32(&s_p), kWorkers);
         mbar_init(smem_u32(&s_dp), 1);
-        mbar_init(smem_u32(&s_ds), 8);
+        mbar_init(smem_u32(&s_ds), kWorkers);
         mbar_init(smem_u32(&s_end), 2);
+        s_issued = 0;
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(smem_u32(&s_read[k]), kWorkers);
+            mbar_init(smem_u32(&s_free[k]), 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (RT < 128 && warp < 8)   // rows that no load writes, but the products over the rows read
-        for (int i = warp; i < 2 * Sh::stages; i += 8) clear_rows<DP>(ring + i * Sh::tile, RT, lane);
-    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    if (RT < 128 && warp < kWorkers)   // rows that no load writes, but the products over the rows read
+        for (int i = warp; i < 2 * Sh::stages; i += kWorkers) clear_rows<DP>(ring + i * Sh::tile, RT, lane);
+    if (warp == kIssuer) tmem_alloc(&s_tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
-    const uint32_t c_s = tmem, c_dp = tmem + 128, c_dv = tmem + 256, c_dk = tmem + 384;
+    const uint32_t c_s = tmem, c_dp = tmem + 128, c_dv = tmem + 256, c_dk = c_dv + DP;
+    const uint32_t c_p = APART ? tmem + 384 : c_s, c_ds = APART ? tmem + 448 : c_dp;   // 16-bit operands
     bool ok = true;
 
-    if (warp == 8) {
+    if (warp == kLoader) {
         if (lane == 0 && tiles > 0) {
             mbar_expect_tx(smem_u32(&s_kv), 2 * Sh::tile);
             load_keys<DP>(k_img, &maps.k, j0, hk, b, smem_u32(&s_kv));
@@ -147,45 +165,57 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             wait_for(drained, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp >= 9) {
-        // warp 9: S^T, then dV += P^T dO; warp 10: dP^T, then dK += dS^T Q
-        const bool grad = warp == 10;
+    } else if (warp >= kIssuer) {
+        // one warp: S^T, then dV += P^T dO; the other: dP^T, then dK += dS^T Q
+        const bool grad = warp == kIssuer + 1;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, 128, false), id_o = idesc<T>(128, steps * 16, true);
         const uint32_t col = grad ? c_dp : c_s, acc = grad ? c_dk : c_dv, key_img = grad ? v_img : k_img;
         const uint32_t made = smem_u32(grad ? &s_dp : &s_s), ready = smem_u32(grad ? &s_ds : &s_p);
         const int rows_b = rr.n_b * G;   // rows from here on hold anything
         if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
+        const uint32_t operand = grad ? c_ds : c_p;
+        int e = 0, pe = 0;   // ring entries of the next scores and of the next product with rows
         uint32_t ph = 0;
-        for (int i = -1, e = 0, pe = 0; i < tiles; ++i) {   // ring entries of tiles i + 1 and i
-            if (i >= 0) {
-                // dV takes dO, dK takes Q
-                const uint32_t rows_img = ring + (uint32_t)pe * 2 * Sh::tile + (grad ? 0 : Sh::tile);
-                wait_warp(ok, ready, (uint32_t)(i & 1), p.wait_ns, &g_status);
-                fence_after_sync();
-                if (ok && elect_one()) {
-                    mma_rows(acc, col, rows_img, id_o, i == 0);
-                    mma_commit(smem_u32(&s_empty[pe]));
-                }
-                __syncwarp();
+        auto scores = [&](int i) {
+            const uint32_t img = ring + (uint32_t)e * 2 * Sh::tile;
+            wait_warp(ok, smem_u32(&s_full[e]), ph, p.wait_ns, &g_status);
+            const int tail = rows_b - (t_lo + i) * RT;
+            if (ok && tail < RT && rr.n_b < a.N) {   // both warps: the same zeros
+                clear_rows<DP>(img, tail, lane);
+                clear_rows<DP>(img + Sh::tile, tail, lane);
             }
-            if (i + 1 < tiles) {
-                const uint32_t img = ring + (uint32_t)e * 2 * Sh::tile;
-                wait_warp(ok, smem_u32(&s_full[e]), ph, p.wait_ns, &g_status);
-                const int tail = rows_b - (t_lo + i + 1) * RT;
-                if (ok && tail < RT && rr.n_b < a.N) {   // both warps: the same zeros
-                    clear_rows<DP>(img, tail, lane);
-                    clear_rows<DP>(img + Sh::tile, tail, lane);
-                }
-                fence_after_sync();
-                if (ok && elect_one()) {
-                    mma_features<DP / 16>(col, key_img, img + (grad ? Sh::tile : 0), steps, id_s);
-                    mma_commit(made);
-                }
-                __syncwarp();
+            fence_after_sync();
+            if (ok && elect_one()) {
+                mma_features<DP / 16>(col, key_img, img + (grad ? Sh::tile : 0), steps, id_s);
+                mma_commit(made);
             }
-            pe = e;
+            __syncwarp();
             if (++e == Sh::stages) e = 0, ph ^= 1;
+        };
+        if (tiles > 0) scores(0);
+        for (int i = 0; i < tiles; ++i) {
+            if (APART && i + 1 < tiles) {
+                wait_warp(ok, smem_u32(&s_read[grad]), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                scores(i + 1);
+            }
+            // dV takes dO, dK takes Q
+            const uint32_t rows_img = ring + (uint32_t)pe * 2 * Sh::tile + (grad ? 0 : Sh::tile);
+            wait_warp(ok, ready, (uint32_t)(i & 1), p.wait_ns, &g_status);
+            // dK and the next dP^T would interleave with the next S^T, which the warps wait for first. Only
+            // the order in the queue hangs on this, so it waits a while and no longer.
+            if (!APART && grad && i + 1 < tiles)
+                for (int k = 0; k < 1000 && s_issued <= i; ++k) __nanosleep(20);
+            fence_after_sync();
+            if (ok && elect_one()) {
+                mma_rows<APART>(acc, operand, rows_img, id_o, i == 0);
+                mma_commit(smem_u32(&s_empty[pe]));
+                if (APART) mma_commit(smem_u32(&s_free[grad]));
+            }
+            __syncwarp();
+            if (++pe == Sh::stages) pe = 0;
+            if (!APART && i + 1 < tiles) scores(i + 1);
+            if (!APART && !grad && lane == 0) s_issued = i + 1;
         }
         if (lane == 0) {
             mma_commit(smem_u32(&s_end));
@@ -194,7 +224,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         }
         __syncwarp();
     } else {
-        const int half = warp >> 2, quarter = warp & 3;
+        const int part = warp >> 2, quarter = warp & 3;   // columns and rows of a tile
         const int key = j0 + quarter * 32 + lane;
         const bool live = key < rr.m_b;
         // packed rows that see this key
@@ -204,63 +234,70 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         const float gs = grad_scale<T>(p, bh, lane);
         const unsigned long long mul = pk2(s2, s2), gmul = pk2(gs, gs);
         const long long info = (long long)bh * p.rows_pad;
-        const int mine = threadIdx.x & 127, which = threadIdx.x >> 7;
-        // this thread's entry of the next tile's row values, one tile ahead
-        auto fetch = [&](int i) -> float {
-            const int r = (t_lo + i) * RT + mine;
-            const bool valid = i < tiles && mine < RT && r < p.rows;
-            if (which) return valid ? -gs * p.row_delta[info + r] : 0.f;
-            return valid ? -p.row_lse[info + r] : -INFINITY;
-        };
-        s_row[0][which][mine] = fetch(0);
-        float next = fetch(1);
+        const int mine = threadIdx.x & 127, which = (threadIdx.x >> 7) & 1;
+        // this thread's entry of a tile's row values, fetched two tiles ahead by 256 threads. The value
+        // is only touched when it is put: an iteration waited 450 cycles for a negation of it
+        const float* values = (which ? p.row_delta : p.row_lse) + info;
+        auto valid = [&](int i) { return i < tiles && mine < RT && (t_lo + i) * RT + mine < p.rows; };
+        auto fetch = [&](int i) { return valid(i) ? values[(t_lo + i) * RT + mine] : 0.f; };
+        auto put = [&](int i, float v) { s_row[i & 1][which][mine] = which ? -gs * v : valid(i) ? -v : -INFINITY; };
+        float next = 0.f;
+        if (part < 2) {
+            const float first = fetch(0);
+            next = fetch(1);
+            put(0, first);
+        }
         // a wait that ran out does not end the loop: the other warps would wait at the barrier
         for (int i = 0; i < tiles; ++i) {
             work_sync();
-            s_row[(i + 1) & 1][which][mine] = next;
-            next = fetch(i + 2);
-            const float4* lse4 = reinterpret_cast<const float4*>(s_row[i & 1][0] + half * 64);
-            const float4* del4 = reinterpret_cast<const float4*>(s_row[i & 1][1] + half * 64);
-            const int r0 = (t_lo + i) * RT + half * 64;
+            if (part < 2) {
+                put(i + 1, next);
+                next = fetch(i + 2);
+            }
+            const float4* lse4 = reinterpret_cast<const float4*>(s_row[i & 1][0] + part * kCols);
+            const float4* del4 = reinterpret_cast<const float4*>(s_row[i & 1][1] + part * kCols);
+            const int r0 = (t_lo + i) * RT + part * kCols;
             wait_warp(ok, smem_u32(&s_s), (uint32_t)(i & 1), p.wait_ns, &g_status);
             fence_after_sync();
-            float s[64];
-            tmem_ld32_nowait(c_s + lanes + half * 64, s);
-            tmem_ld32_nowait(c_s + lanes + half * 64 + 32, s + 32);
+            float s[kCols];
+            tmem_ld32_nowait(c_s + lanes + part * kCols, s);
             tmem_wait_ld();
+            if (APART) done(s_read[0]);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kCols; c += 4) {
                 const float4 l = lse4[c / 4];
                 upk2(fma2(pk2(s[c], s[c + 1]), mul, pk2(l.x, l.y)), s[c], s[c + 1]);
                 upk2(fma2(pk2(s[c + 2], s[c + 3]), mul, pk2(l.z, l.w)), s[c + 2], s[c + 3]);
             }
-            if (__any_sync(0xffffffffu, live && (r0 < rlo || r0 + 64 > rhi))) {
+            if (__any_sync(0xffffffffu, live && (r0 < rlo || r0 + kCols > rhi))) {
                 const int first = rlo - r0, count = rhi - rlo;
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < kCols; ++c)
                     if ((unsigned)(c - first) >= (unsigned)count) s[c] = -INFINITY;
             }
-            uint32_t u[32];
+            uint32_t u[kCols / 2];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < kCols; c += 2) {
                 s[c] = ex2(s[c]);
                 s[c + 1] = ex2(s[c + 1]);
                 u[c / 2] = pack2<T>(s[c], s[c + 1]);
             }
-            st64(c_s + lanes + half * 64, u);
+            if (APART && i > 0) {   // dV has taken the last probabilities
+                wait_warp(ok, smem_u32(&s_free[0]), (uint32_t)((i - 1) & 1), p.wait_ns, &g_status);
+                fence_after_sync();
+            }
+            tmem_st16(c_p + lanes + a_col<APART>(part), u);
             tmem_wait_st();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_p));
+            done(s_p);
 
             wait_warp(ok, smem_u32(&s_dp), (uint32_t)(i & 1), p.wait_ns, &g_status);
             fence_after_sync();
-            float d[64];
-            tmem_ld32_nowait(c_dp + lanes + half * 64, d);
-            tmem_ld32_nowait(c_dp + lanes + half * 64 + 32, d + 32);
+            float d[kCols];
+            tmem_ld32_nowait(c_dp + lanes + part * kCols, d);
             tmem_wait_ld();
+            if (APART) done(s_read[1]);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kCols; c += 4) {
                 const float4 e = del4[c / 4];
                 float x, y;
                 upk2(mul2(pk2(s[c], s[c + 1]), fma2(pk2(d[c], d[c + 1]), gmul, pk2(e.x, e.y))), x, y);
@@ -268,29 +305,32 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
                 upk2(mul2(pk2(s[c + 2], s[c + 3]), fma2(pk2(d[c + 2], d[c + 3]), gmul, pk2(e.z, e.w))), x, y);
                 u[c / 2 + 1] = pack2<T>(x, y);
             }
-            st64(c_dp + lanes + half * 64, u);
+            if (APART && i > 0) {   // dK has taken the last gradients
+                wait_warp(ok, smem_u32(&s_free[1]), (uint32_t)((i - 1) & 1), p.wait_ns, &g_status);
+                fence_after_sync();
+            }
+            tmem_st16(c_ds + lanes + a_col<APART>(part), u);
             tmem_wait_st();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_ds));
+            done(s_ds);
         }
         if (tiles > 0) {
             wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        // warps 0-3 write dV, 4-7 dK, through the image of V or K
-        const float unlift = ex2(-(float)p.grad_shift), more = half ? a.scale / gs : 1.f;
+        // half of the warpgroups write dV, half dK, each half of the features, through the images of K
+        // and V
+        constexpr int F = DP / 2;
+        const bool is_k = part & 1;
+        const int f0 = (part >> 1) * F;
+        const float unlift = ex2(-(float)p.grad_shift), more = is_k ? a.scale / gs : 1.f;
         const bool some = tiles > 0 && live;
-        const long long at = key < a.M ? (((long long)b * a.M + key) * a.Hkv + hk) * a.D : -1;
-#pragma unroll 1
-        for (int f = 0; f < DP; f += 64)
-            write_rows<T, 64>(base + (uint32_t)(half * 4 + quarter) * 32 * 128, (half ? c_dk : c_dv) + lanes + f, tiles > 0 && ok,
-                              false, ok && !some, ok ? unlift : NAN, 0.f, more, half ? p.dk : p.dv, nullptr, at < 0 ? at : at + f,
-                              min(64, a.D - f) / 8, lane);
+        const long long at = key < a.M ? (((long long)b * a.M + key) * a.Hkv + hk) * a.D + f0 : -1;
+        write_rows<T, F>(base + (uint32_t)warp * 32 * F * 2, (is_k ? c_dk : c_dv) + lanes + f0, tiles > 0 && ok, false, ok && !some,
+                         ok ? unlift : NAN, 0.f, more, is_k ? p.dk : p.dv, nullptr, at, min(F, a.D - f0) / 8, lane);
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
@@ -300,7 +340,7 @@ template <typename T, int DP>
 __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, const int block, unsigned char* dyn)
 {
     using Sh = BwdShape<DP>;
-    __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s[2], s_free[2], s_dp, s_ds, s_end;
+    __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s, s_sread, s_dp, s_dpread, s_ds[2], s_dsfree[2], s_end;
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -322,24 +362,28 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             mbar_init(smem_u32(&s_full[e]), 1);
             mbar_init(smem_u32(&s_empty[e]), 1);
         }
-        mbar_init(smem_u32(&s_s[0]), 1);
-        mbar_init(smem_u32(&s_s[1]), 1);
-        mbar_init(smem_u32(&s_free[0]), 8);
-        mbar_init(smem_u32(&s_free[1]), 8);
+        mbar_init(smem_u32(&s_s), 1);
+        mbar_init(smem_u32(&s_sread), kWorkers);
         mbar_init(smem_u32(&s_dp), 1);
-        mbar_init(smem_u32(&s_ds), 8);
+        mbar_init(smem_u32(&s_dpread), kWorkers);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(smem_u32(&s_ds[k]), kWorkers);
+            mbar_init(smem_u32(&s_dsfree[k]), 1);
+        }
         mbar_init(smem_u32(&s_end), 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    if (warp == kIssuer) tmem_alloc(&s_tmem, 512);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
-    const uint32_t c_s = tmem, c_dp = tmem + 256, c_dq = tmem + 384;   // two S tiles
+    // scores are read at once and dS has columns of its own, twice: the next S and dP are made
+    // meanwhile, and the next dS need not wait for the product with the last one
+    const uint32_t c_s = tmem, c_dp = tmem + 128, c_ds = tmem + 256, c_dq = tmem + 384;
     bool ok = true;
 
-    if (warp == 8) {
+    if (warp == kLoader) {
         if (lane == 0 && tiles > 0) {
             mbar_expect_tx(smem_u32(&s_q), 2u * RT * 128 * (DP / 64));
             load_rows<DP>(q_img, &maps.q, r0 / G, hk, b, smem_u32(&s_q));
@@ -360,9 +404,9 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             wait_for(drained, smem_u32(&s_q), 0, p.wait_ns, &g_status);
         }
         __syncwarp();
-    } else if (warp >= 9) {
-        // warp 9: S(j), two tiles ahead; warp 10: dP(j), then dQ += dS K
-        const bool grad = warp == 10;
+    } else if (warp >= kIssuer) {
+        // one warp: S(j); the other: dP(j), then dQ += dS K
+        const bool grad = warp == kIssuer + 1;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
         if (tiles > 0) wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, &g_status);
@@ -374,46 +418,47 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         uint32_t ph_k = 0, ph_v = 0;
         if (!grad) {
             for (int j = 0; j < tiles; ++j) {
-                // the scores of tile j - 2 have been read
-                if (j >= 2) wait_warp(ok, smem_u32(&s_free[j & 1]), (uint32_t)(((j >> 1) - 1) & 1), p.wait_ns, &g_status);
+                if (j > 0) wait_warp(ok, smem_u32(&s_sread), (uint32_t)((j - 1) & 1), p.wait_ns, &g_status);
                 wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
                 const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
                 clear_tail(j, kimg);
                 fence_after_sync();
                 if (ok && elect_one()) {
-                    mma_features<DP / 16>(c_s + (j & 1) * 128, q_img, kimg, steps, id_s);
-                    mma_commit(smem_u32(&s_s[j & 1]));
+                    mma_features<DP / 16>(c_s, q_img, kimg, steps, id_s);
+                    mma_commit(smem_u32(&s_s));
                 }
                 __syncwarp();
                 if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots, ph_k ^= 1;
             }
         } else {
-            int e_p = 0;   // entry of K(j - 1)
-            for (int j = 0; j <= tiles; ++j) {
-                if (j > 0) {
-                    const uint32_t kimg = ring + (uint32_t)e_p * Sh::tile;
-                    wait_warp(ok, smem_u32(&s_ds), (uint32_t)((j - 1) & 1), p.wait_ns, &g_status);
-                    clear_tail(j - 1, kimg);
-                    fence_after_sync();
-                    if (ok && elect_one()) {
-                        mma_rows(c_dq, c_dp, kimg, id_o, j == 1);
-                        mma_commit(smem_u32(&s_empty[e_p]));   // S(j - 1) was done before dS(j - 1)
-                    }
-                    __syncwarp();
+            auto upstream = [&]() {
+                wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    mma_features<DP / 16>(c_dp, g_img, ring + (uint32_t)e_v * Sh::tile, steps, id_s);
+                    mma_commit(smem_u32(&s_dp));
+                    mma_commit(smem_u32(&s_empty[e_v]));
                 }
-                if (j < tiles) {
-                    wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
-                    fence_after_sync();
-                    if (ok && elect_one()) {
-                        mma_features<DP / 16>(c_dp, g_img, ring + (uint32_t)e_v * Sh::tile, steps, id_s);
-                        mma_commit(smem_u32(&s_dp));
-                        mma_commit(smem_u32(&s_empty[e_v]));
-                    }
-                    __syncwarp();
-                }
-                e_p = e_k;
-                if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots;
+                __syncwarp();
                 if ((e_v += 2) >= Sh::slots) e_v -= Sh::slots, ph_v ^= 1;
+            };
+            if (tiles > 0) upstream();
+            for (int j = 0; j < tiles; ++j) {
+                if (j + 1 < tiles) {
+                    wait_warp(ok, smem_u32(&s_dpread), (uint32_t)(j & 1), p.wait_ns, &g_status);
+                    upstream();
+                }
+                const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
+                wait_warp(ok, smem_u32(&s_ds[j & 1]), (uint32_t)((j >> 1) & 1), p.wait_ns, &g_status);
+                clear_tail(j, kimg);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    mma_rows<true>(c_dq, c_ds + (j & 1) * 64, kimg, id_o, j == 0);
+                    mma_commit(smem_u32(&s_empty[e_k]));   // S(j) was done before dS(j)
+                    mma_commit(smem_u32(&s_dsfree[j & 1]));
+                }
+                __syncwarp();
+                if ((e_k += 2) >= Sh::slots) e_k -= Sh::slots;
             }
         }
         if (lane == 0) {
@@ -423,7 +468,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         }
         __syncwarp();
     } else {
-        const int half = warp >> 2, quarter = warp & 3;
+        const int part = warp >> 2, quarter = warp & 3;   // columns and rows of a tile
         const int r = r0 + quarter * 32 + lane;
         const bool mine = quarter * 32 + lane < RT && r < p.rows;
         const int n = mine ? r / G : 0, h = hk * G + (mine ? r % G : 0);
@@ -436,66 +481,66 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         const float nlse = live ? -p.row_lse[info] : -INFINITY, ndel = live ? -gs * p.row_delta[info] : 0.f;
         const unsigned long long mul = pk2(s2, s2), sub = pk2(nlse, nlse), gmul = pk2(gs, gs), gsub = pk2(ndel, ndel);
         for (int j = 0; j < tiles; ++j) {
-            const int j0 = (t.lo + j) * kKeys + half * 64;
-            wait_warp(ok, smem_u32(&s_s[j & 1]), (uint32_t)((j >> 1) & 1), p.wait_ns, &g_status);
+            const int j0 = (t.lo + j) * kKeys + part * kCols;
+            wait_warp(ok, smem_u32(&s_s), (uint32_t)(j & 1), p.wait_ns, &g_status);
             fence_after_sync();
-            float s[64];
-            const uint32_t sc = c_s + (j & 1) * 128 + lanes + half * 64;
-            tmem_ld32_nowait(sc, s);
-            tmem_ld32_nowait(sc + 32, s + 32);
+            float s[kCols];
+            tmem_ld32_nowait(c_s + lanes + part * kCols, s);
             tmem_wait_ld();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_free[j & 1]));
+            done(s_sread);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) upk2(fma2(pk2(s[c], s[c + 1]), mul, sub), s[c], s[c + 1]);
-            const bool edge = __any_sync(0xffffffffu, live && (j0 < klo || j0 + 64 > khi));
+            for (int c = 0; c < kCols; c += 2) upk2(fma2(pk2(s[c], s[c + 1]), mul, sub), s[c], s[c + 1]);
+            const bool edge = __any_sync(0xffffffffu, live && (j0 < klo || j0 + kCols > khi));
             const int first = klo - j0, count = khi - klo;
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < kCols; ++c)
                     if ((unsigned)(c - first) >= (unsigned)count) s[c] = -INFINITY;
             }
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = ex2(s[c]);
+            for (int c = 0; c < kCols; ++c) s[c] = ex2(s[c]);
             wait_warp(ok, smem_u32(&s_dp), (uint32_t)(j & 1), p.wait_ns, &g_status);
             fence_after_sync();
-            float d[64];
-            tmem_ld32_nowait(c_dp + lanes + half * 64, d);
-            tmem_ld32_nowait(c_dp + lanes + half * 64 + 32, d + 32);
+            float d[kCols];
+            tmem_ld32_nowait(c_dp + lanes + part * kCols, d);
             tmem_wait_ld();
+            done(s_dpread);
             if (edge) {   // dP of a key beyond the length may be NaN
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < kCols; ++c)
                     if ((unsigned)(c - first) >= (unsigned)count) d[c] = 0.f;
             }
-            uint32_t u[32];
+            uint32_t u[kCols / 2];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < kCols; c += 2) {
                 float x, y;
                 upk2(mul2(pk2(s[c], s[c + 1]), fma2(pk2(d[c], d[c + 1]), gmul, gsub)), x, y);
                 u[c / 2] = pack2<T>(x, y);
             }
-            st64(c_dp + lanes + half * 64, u);
+            if (j > 1) {   // dQ has taken the gradients before the last
+                wait_warp(ok, smem_u32(&s_dsfree[j & 1]), (uint32_t)(((j >> 1) - 1) & 1), p.wait_ns, &g_status);
+                fence_after_sync();
+            }
+            tmem_st16(c_ds + (j & 1) * 64 + lanes + a_col<true>(part), u);
             tmem_wait_st();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_ds));
+            done(s_ds[j & 1]);
         }
         if (tiles > 0) {
             wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        // each warpgroup writes half of the features, through Q's and dO's images
+        // a warpgroup writes 32 features, through the images of Q and dO
         const float unlift = ex2(-(float)p.grad_shift), more = a.scale / gs;
-        constexpr int F = DP / 2;
-        const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + half * F : -1;
-        write_rows<T, F>(base + (uint32_t)(half * 4 + quarter) * 32 * F * 2, c_dq + lanes + half * F, tiles > 0 && ok,
-                         false, ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, p.dq, nullptr, at, min(F, a.D - half * F) / 8, lane);
+        const int f0 = part * 32;
+        if (f0 < DP) {
+            const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + f0 : -1;
+            write_rows<T, 32>(base + (uint32_t)warp * 32 * 64, c_dq + lanes + f0, tiles > 0 && ok, false,
+                              ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, p.dq, nullptr, at, min(32, a.D - f0) / 8, lane);
+        }
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         fence_after_sync();
         tmem_dealloc(tmem, 512);
     }

@@ -21,12 +21,10 @@
 // that the accumulator in tensor memory is rarely read back for rescaling: probabilities are
 // then at most 2^8, which fp32 sums and 16-bit operands take as well as 1.
 //
-// Probabilities are rounded to 16 bits for their product with V. Where a backward pass will
-// follow, O is divided by the sum of the rounded ones: their errors then enter delta = do . o only
-// by how they differ from key to key, as those of dS itself do. Divided by the exact sum, which
-// lse keeps, dq was up to 1.9 times as far from its 64-bit value as a plain fp32 pass.
-#include <type_traits>
-
+// Probabilities are rounded to 16 bits for their product with V, and O is divided by the sum of
+// the rounded ones: in the backward pass their errors then enter delta = do . o only by how they
+// differ from key to key, as those of dS itself do. Divided by the exact sum, which lse keeps,
+// dq was up to 1.9 times as far from its 64-bit value as a plain fp32 pass.
 #include "attn_tc.cuh"
 
 namespace sdtw {
@@ -294,40 +292,33 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
             }
             const unsigned long long mul = pk2(s2, s2), sub = pk2(-off, -off);
             unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f), seen2 = pk2(0.f, 0.f);
-            auto exps = [&](auto train) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t u[16];
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t u[16];
 #pragma unroll
-                    for (int q = 0; q < 32; q += 4) {
-                        float e[4];
-                        upk2(fma2(pk2(s[c + q], s[c + q + 1]), mul, sub), e[0], e[1]);
-                        upk2(fma2(pk2(s[c + q + 2], s[c + q + 3]), mul, sub), e[2], e[3]);
+                for (int q = 0; q < 32; q += 4) {
+                    float e[4];
+                    upk2(fma2(pk2(s[c + q], s[c + q + 1]), mul, sub), e[0], e[1]);
+                    upk2(fma2(pk2(s[c + q + 2], s[c + q + 3]), mul, sub), e[2], e[3]);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
-                        sum0 = add2(sum0, pk2(e[0], e[1]));
-                        sum1 = add2(sum1, pk2(e[2], e[3]));
-                        u[q / 2] = pack2<T>(e[0], e[1]);
-                        u[q / 2 + 1] = pack2<T>(e[2], e[3]);
-                        if (train) seen2 = add2(seen2, add2(unpack2<T>(u[q / 2]), unpack2<T>(u[q / 2 + 1])));
-                    }
-                    tmem_st16(s_col + c / 2, u);
-                    if (c == 32) {   // the first 64 keys are there
-                        tmem_wait_st();
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
-                    }
+                    for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
+                    sum0 = add2(sum0, pk2(e[0], e[1]));
+                    sum1 = add2(sum1, pk2(e[2], e[3]));
+                    u[q / 2] = pack2<T>(e[0], e[1]);
+                    u[q / 2 + 1] = pack2<T>(e[2], e[3]);
+                    seen2 = add2(seen2, add2(unpack2<T>(u[q / 2]), unpack2<T>(u[q / 2 + 1])));
                 }
-            };
-            float x, y;
-            if (p.out_rest) {
-                exps(std::true_type{});
-                upk2(seen2, x, y);
-                lr += x + y;
-            } else {
-                exps(std::false_type{});
+                tmem_st16(s_col + c / 2, u);
+                if (c == 32) {   // the first 64 keys are there
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
+                }
             }
+            float x, y;
+            upk2(seen2, x, y);
+            lr += x + y;
             upk2(add2(sum0, sum1), x, y);
             l += x + y;
             tmem_wait_st();
@@ -340,7 +331,6 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
             wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);
             fence_after_sync();
         }
-        if (!p.out_rest) lr = l;
         float mul = 0.f, mul1 = 0.f, total = l, by = lr;
         if (NT == 2 && alternate) {   // warps 0-3 join the two; a lane's row lies in the same lane of O_0 and O_1
             const int row = quarter * 32 + lane;
