@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
                 }
             }
             const unsigned long long mul = pk2(s2, s2), sub = pk2(-off, -off);
-            unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f), seen2 = pk2(0.f, 0.f);
+            unsigned long long sum0 = pk2(0.f, 0.f), sum1 = pk2(0.f, 0.f);
+            float seen[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 uint32_t u[16];
@@ -306,7 +307,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
                     sum1 = add2(sum1, pk2(e[2], e[3]));
                     u[q / 2] = pack2<T>(e[0], e[1]);
                     u[q / 2 + 1] = pack2<T>(e[2], e[3]);
-                    seen2 = add2(seen2, add2(unpack2<T>(u[q / 2]), unpack2<T>(u[q / 2 + 1])));
+                    add_pair<T>(seen[0], seen[1], u[q / 2]);
+                    add_pair<T>(seen[2], seen[3], u[q / 2 + 1]);
                 }
                 tmem_st16(s_col + c / 2, u);
                 if (c == 32) {   // the first 64 keys are there
@@ -316,9 +318,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
                     if (lane == 0) mbar_arrive(smem_u32(&s_p[w][0]));
                 }
             }
+            lr += (seen[0] + seen[1]) + (seen[2] + seen[3]);
             float x, y;
-            upk2(seen2, x, y);
-            lr += x + y;
             upk2(add2(sum0, sum1), x, y);
             l += x + y;
             tmem_wait_st();

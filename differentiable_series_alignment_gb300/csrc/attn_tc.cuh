@@ -171,13 +171,19 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// the values that pack2 made, as a packed fp32 pair
-template <typename T> __device__ __forceinline__ unsigned long long unpack2(uint32_t v) {
-    const T* h = reinterpret_cast<const T*>(&v);
-    return pk2(to_f32(h[0]), to_f32(h[1]));
+// The two values that pack2 made, added to x and y. The instruction takes a 16-bit operand as it
+// is: 1.1 cycles a value and warp, where unpacking them for packed fp32 adds took 4 (shifts and
+// masks run at half rate).
+template <typename T> __device__ __forceinline__ void add_pair(float& x, float& y, uint32_t v);
+template <> __device__ __forceinline__ void add_pair<__nv_bfloat16>(float& x, float& y, uint32_t v) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(x), "+f"(y) : "r"(v));
 }
-template <> __device__ __forceinline__ unsigned long long unpack2<__nv_bfloat16>(uint32_t v) {
-    return pk2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+template <> __device__ __forceinline__ void add_pair<__half>(float& x, float& y, uint32_t v) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
+        : "+f"(x), "+f"(y) : "r"(v));
 }
 __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
     unsigned long long r;

@@ -345,6 +345,19 @@ def test_attention_of_few_rows_over_long_caches(package, N, G, M, D, dtype):
         check_attention(package, q, k, v, do, dtype, **args)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("N,M,Hq,Hkv,D", [(1100, 1100, 2, 1, 128), (1300, 2050, 2, 2, 64), (2049, 1153, 3, 1, 128), (600, 1500, 3, 3, 40),
+                                          (1024, 1024, 4, 1, 96), (1537, 1537, 6, 2, 64)])
+@pytest.mark.parametrize("causal,window,ragged", [(True, None, False), (False, None, True), (True, 600, False), (False, 900, True)])
+def test_attention_of_long_sequences(package, N, M, Hq, Hkv, D, causal, window, ragged, dtype):
+    """Long enough that neighbouring tiles share their loads."""
+    gen = generator(N + M + D)
+    q, do = randn(gen, 2, N, Hq, D, dtype=dtype, std=1.5), randn(gen, 2, N, Hq, D, dtype=dtype, std=0.3)
+    k, v = randn(gen, 2, M, Hkv, D, dtype=dtype, std=1.5), randn(gen, 2, M, Hkv, D, dtype=dtype)
+    lengths = lambda n: torch.tensor([n - 3, n // 3], device="cuda", dtype=torch.int32) if ragged else None  # noqa: E731
+    check_attention(package, q, k, v, do, dtype, causal, window, lengths(N), lengths(M))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_of_slices_and_of_unaligned_heads(package, dtype):
     gen = generator(11)
