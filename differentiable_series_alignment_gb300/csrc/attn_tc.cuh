@@ -10,6 +10,7 @@
 #include <cuda.h>
 
 #include "encoder.h"
+#include "packed.cuh"
 #include "tc.cuh"
 
 namespace sdtw {
@@ -158,43 +159,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// two fp32 values rounded to 16 bits each, lo in the low half
-template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// The two values that pack2 made, added to x and y. The instruction takes a 16-bit operand as it
-// is: 1.1 cycles a value and warp, where unpacking them for packed fp32 adds took 4 (shifts and
-// masks run at half rate).
-template <typename T> __device__ __forceinline__ void add_pair(float& x, float& y, uint32_t v);
-template <> __device__ __forceinline__ void add_pair<__nv_bfloat16>(float& x, float& y, uint32_t v) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
-        : "+f"(x), "+f"(y) : "r"(v));
-}
-template <> __device__ __forceinline__ void add_pair<__half>(float& x, float& y, uint32_t v) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
-        : "+f"(x), "+f"(y) : "r"(v));
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;

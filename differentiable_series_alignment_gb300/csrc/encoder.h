@@ -57,7 +57,7 @@ struct NormParams {
     int C, dtype, wdtype;
     float eps;
 };
-int norm_partial_ctas(long long rows, int C, int sms);   // CTAs of the backward = partial rows
+int norm_partial_ctas(long long rows, int sms);   // CTAs of the backward = partial rows, at most
 cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s);
 

@@ -183,7 +183,7 @@ sdtw_status sdtw_layernorm_forward(const void* x, const void* weight, const void
 size_t sdtw_layernorm_workspace_bytes(long long rows, int C)
 {
     if (check_norm(rows, C, SDTW_F32, SDTW_F32) != SDTW_OK) return 0;
-    return align_up(2 * sizeof(float) * (size_t)norm_partial_ctas(rows, C, device_sms()) * C);
+    return align_up(2 * sizeof(float) * (size_t)norm_partial_ctas(rows, device_sms()) * C);
 }
 
 sdtw_status sdtw_layernorm_backward(const void* dy, const void* x, const void* weight, const float* mean,
@@ -201,7 +201,7 @@ sdtw_status sdtw_layernorm_backward(const void* dy, const void* x, const void* w
     p.dy = dy, p.x = x, p.weight = weight, p.mean = const_cast<float*>(mean), p.rstd = const_cast<float*>(rstd);
     p.dx = dx, p.dweight = dweight, p.dbias = dbias;
     p.rows = rows, p.C = C, p.dtype = dtype, p.wdtype = wdtype;
-    ENC_CUDA(launch_norm_backward(p, norm_partial_ctas(rows, C, device_sms()), static_cast<cudaStream_t>(stream)));
+    ENC_CUDA(launch_norm_backward(p, norm_partial_ctas(rows, device_sms()), static_cast<cudaStream_t>(stream)));
     return SDTW_OK;
 }
 

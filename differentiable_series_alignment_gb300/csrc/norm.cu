@@ -9,12 +9,25 @@
 // again from the cache. The weights' gradients are summed in registers over the rows
 // that a CTA takes (a column stays with its thread), then over the CTAs by a second
 // launch in a fixed order: no atomics, the same bits every time.
+//
+// Memory bounds it, and next to it the instructions of 16-bit rows: elements are taken into fp32 by
+// mixed-precision adds and worked on in pairs, which halved the instructions of both directions
+// (the backward issued 69 % of the time before), and coming rows are on their way to shared memory
+// meanwhile. 65535 rows of 1024 with fp32 weights: bf16 forward 51 us (5.2 TB/s), backward 80 us
+// (5.1 TB/s) and 6 for the fold; fp32 forward 108 us (5.0), backward 138 (5.9). A plain copy of as
+// many bytes runs at 5.6 TB/s. Without the rows ahead fp32 took 149 and 164.
+#include <algorithm>
+
 #include "encoder.h"
+#include "packed.cuh"
 
 namespace sdtw {
 namespace {
 
 constexpr int kThreads = 256;
+// Backward CTAs per SM, by packs a thread. With four of one pack (64 registers) the sums of the weights'
+// gradients spilled: 65535 rows of 1024 bf16 took 99 us where three take 83.
+template <int K> constexpr int kBwdCtas = K == 1 ? 3 : K == 2 ? 2 : 1;
 
 template <int W> __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
@@ -90,58 +103,182 @@ __device__ __forceinline__ void wstore(void* p, int c, int wdtype, float v) {
     else static_cast<__half*>(p)[c] = from_f32<__half>(v);
 }
 
+// VEC elements as fp32 pairs; a lone one has a zero beside it.
+template <int VEC> constexpr int kPairs = (VEC + 1) / 2;
+using Pair = unsigned long long;
+template <int VEC> __device__ __forceinline__ void pairs_of(const float (&v)[VEC], Pair (&out)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) out[q] = pk2(v[2 * q], VEC == 1 ? 0.f : v[2 * q + 1]);
+}
+template <int VEC> __device__ __forceinline__ void weight_pairs(const void* p, int c0, int wdtype, float none, Pair (&out)[kPairs<VEC>]) {
+    float w[VEC];
+    weights<VEC>(p, c0, wdtype, none, w);
+    pairs_of<VEC>(w, out);
+}
+// v + c
+template <typename T, int VEC> __device__ __forceinline__ void plus(const Pack<T, VEC>& v, float c, Pair (&out)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        if constexpr (VEC == 1) {
+            out[q] = pk2(to_f32(v.e[0]) + c, 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            out[q] = add2(pk2(v.e[2 * q], v.e[2 * q + 1]), pk2(c, c));
+        } else {
+            float x = c, y = c;
+            add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+            out[q] = pk2(x, y);
+        }
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> rounded(const Pair (&v)[kPairs<VEC>]) {
+    Pack<T, VEC> o;
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        float x, y;
+        upk2(v[q], x, y);
+        if constexpr (VEC == 1) o.e[0] = from_f32<T>(x);
+        else if constexpr (sizeof(T) == 4) o.e[2 * q] = x, o.e[2 * q + 1] = y;
+        else *reinterpret_cast<uint32_t*>(&o.e[2 * q]) = pack2<T>(x, y);
+    }
+    return o;
+}
+// s + v, the even elements in one half and the odd ones in the other
+template <typename T, int VEC> __device__ __forceinline__ Pair sum_onto(Pair s, const Pack<T, VEC>& v) {
+    float x, y;
+    upk2(s, x, y);
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        if constexpr (VEC == 1) x += to_f32(v.e[0]);
+        else if constexpr (sizeof(T) == 4) x += v.e[2 * q], y += v.e[2 * q + 1];
+        else add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+    }
+    return pk2(x, y);
+}
+__device__ __forceinline__ float both(Pair v) {
+    float x, y;
+    upk2(v, x, y);
+    return x + y;
+}
+
+// Packs on their way from memory: a thread copies its own packs of coming rounds to shared memory
+// and reads back only those, so that nobody waits for anybody. An SM then has some 100 KB in flight
+// whatever its threads are busy with, where loads to registers leave it idle from a round's sums
+// to its stores.
+__device__ __forceinline__ void fetch16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch_mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
 // L threads per row, K packs of VEC elements per thread, R rows at a time (their sums run side by
 // side, and weights that are not kept in registers are read once for all); C is a multiple of VEC.
-template <typename T, int VEC, int K, int L, int R>
+// AHEAD rounds of rows are on their way while one is worked on (0: a round loads its own).
+template <typename T, int VEC, int K, int L, int R, int AHEAD>
 __global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormParams p)
 {
     __shared__ float2 red[2 * kThreads / 32];
+    extern __shared__ __align__(16) unsigned char ring[];   // [AHEAD + 1][R][K][kThreads] packs
     int turn = 0;
     using P = Pack<T, VEC>;
     const int lane = threadIdx.x % L;
     const long long step = (long long)gridDim.x * (kThreads / L) * R;
     const int packs = p.C / VEC;
     const float inv_c = 1.f / (float)p.C;
-    float w1[VEC], b1[VEC];   // one pack a thread: its weights stay in registers
+    constexpr int Q = kPairs<VEC>;
+    Pair w1[Q], b1[Q];   // one pack a thread: its weights stay in registers
     if (K == 1 && lane < packs) {
-        weights<VEC>(p.weight, lane * VEC, p.wdtype, 1.f, w1);
-        weights<VEC>(p.bias, lane * VEC, p.wdtype, 0.f, b1);
+        weight_pairs<VEC>(p.weight, lane * VEC, p.wdtype, 1.f, w1);
+        weight_pairs<VEC>(p.bias, lane * VEC, p.wdtype, 0.f, b1);
     }
+    // A warp with a whole row has them in shared memory, in pieces of 16 bytes that neighbouring lanes
+    // find side by side. Read from the cache for every row, at strides of 32 bytes, they kept it
+    // busier than x and y did (65535 rows of 1024 bf16: 65 us, L1 at 86 %; 53 us so).
+    constexpr bool HELD = K > 1 && L == 32 && VEC > 1;
+    constexpr int FOURS = HELD ? VEC / 4 : 1;
+    __shared__ float4 held[2 * FOURS][HELD ? K * L : 1];
+    if constexpr (HELD) {
+        for (int c = threadIdx.x; c < packs; c += kThreads)
+#pragma unroll
+            for (int h = 0; h < FOURS; ++h) {
+                float w[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = wval(p.weight, c * VEC + 4 * h + e, p.wdtype, 1.f);
+                    b[e] = wval(p.bias, c * VEC + 4 * h + e, p.wdtype, 0.f);
+                }
+                held[h][c] = make_float4(w[0], w[1], w[2], w[3]);
+                held[FOURS + h][c] = make_float4(b[0], b[1], b[2], b[3]);
+            }
+        __syncthreads();
+    }
+    auto row_weights = [&](int k, Pair (&w)[Q], Pair (&b)[Q]) {
+        if constexpr (K == 1) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) w[q] = w1[q], b[q] = b1[q];
+        } else if constexpr (HELD) {
+#pragma unroll
+            for (int h = 0; h < FOURS; ++h) {
+                const float4 x = held[h][lane + k * L], y = held[FOURS + h][lane + k * L];
+                w[2 * h] = pk2(x.x, x.y), w[2 * h + 1] = pk2(x.z, x.w);
+                b[2 * h] = pk2(y.x, y.y), b[2 * h + 1] = pk2(y.z, y.w);
+            }
+        } else {
+            weight_pairs<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
+            weight_pairs<VEC>(p.bias, (lane + k * L) * VEC, p.wdtype, 0.f, b);
+        }
+    };
     // every thread of a warp (of the CTA, for long rows) makes the same number of rounds: the sums
     // are collective
+    auto row = [&](long long r) { return reinterpret_cast<const P*>(static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.C); };
+    auto slot = [&](int stage, int i, int k) { return reinterpret_cast<P*>(ring) + ((stage * R + i) * K + k) * kThreads + threadIdx.x; };
+    auto send = [&](long long r, int stage) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (r + i < p.rows && lane + k * L < packs) fetch16(slot(stage, i, k), row(r + i) + lane + k * L);
+        fetch_mark();
+    };
+    const long long own = (long long)blockIdx.x * (kThreads / L) * R + threadIdx.x / L * R;
+    int stage = 0;
+    if constexpr (AHEAD > 0)
+        for (int s = 0; s < AHEAD; ++s) send(own + s * step, s);
     for (long long r0 = (long long)blockIdx.x * (kThreads / L) * R; r0 < p.rows; r0 += step) {
         const long long r = r0 + threadIdx.x / L * R;
         P v[R][K];
+        if constexpr (AHEAD > 0) {
+            send(r + AHEAD * step, stage == 0 ? AHEAD : stage - 1);   // where the last round's were: they are in use no more
+            fetch_wait<AHEAD>();
+        }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const P* src = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + (r + i < p.rows ? r + i : 0) * p.C);
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (lane + k * L < packs) v[i][k] = src[lane + k * L];
-        }
+                if (lane + k * L < packs) v[i][k] = AHEAD > 0 ? *slot(stage, i, k) : row(r + i)[lane + k * L];
+        stage = stage == AHEAD ? 0 : stage + 1;
         float mu[R], rs[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            mu[i] = 0.f;
+            Pair s = pk2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (lane + k * L < packs)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) mu[i] += to_f32(v[i][k].e[e]);
+                if (lane + k * L < packs) s = sum_onto(s, v[i][k]);
+            mu[i] = both(s);
         }
         all_sums<L, R>(mu, red, turn);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             mu[i] *= inv_c;
-            rs[i] = 0.f;
+            Pair s = pk2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (lane + k * L < packs)
+                if (lane + k * L < packs) {
+                    Pair d[Q];
+                    plus<T, VEC>(v[i][k], -mu[i], d);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float d = to_f32(v[i][k].e[e]) - mu[i];
-                        rs[i] = fmaf(d, d, rs[i]);
-                    }
+                    for (int q = 0; q < Q; ++q) s = fma2(d[q], d[q], s);
+                }
+            rs[i] = both(s);
         }
         all_sums<L, R>(rs, red, turn);
 #pragma unroll
@@ -155,21 +292,16 @@ __global__ void __launch_bounds__(kThreads, 4) norm_fwd_kernel(const NormParams 
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (lane + k * L < packs) {
-                float w[VEC], b[VEC];
-                if (K > 1) {
-                    weights<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
-                    weights<VEC>(p.bias, (lane + k * L) * VEC, p.wdtype, 0.f, b);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) w[e] = w1[e], b[e] = b1[e];
-                }
+                Pair w[Q], b[Q];
+                row_weights(k, w, b);
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     if (r + i < p.rows) {
-                        P o;
+                        Pair d[Q];
+                        plus<T, VEC>(v[i][k], -mu[i], d);
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) o.e[e] = from_f32<T>(fmaf((to_f32(v[i][k].e[e]) - mu[i]) * rs[i], w[e], b[e]));
-                        reinterpret_cast<P*>(static_cast<T*>(p.y) + (r + i) * p.C)[lane + k * L] = o;
+                        for (int q = 0; q < Q; ++q) d[q] = fma2(mul2(d[q], pk2(rs[i], rs[i])), w[q], b[q]);
+                        reinterpret_cast<P*>(static_cast<T*>(p.y) + (r + i) * p.C)[lane + k * L] = rounded<T, VEC>(d);
                     }
             }
     }
@@ -203,106 +335,115 @@ template <typename T> __global__ void __launch_bounds__(kThreads) norm_fwd_long_
     }
 }
 
-template <typename T, int VEC, int K, int L>
-__global__ void __launch_bounds__(kThreads, K == 1 ? 4 : K == 2 ? 2 : 1) norm_bwd_kernel(const NormParams p)
+template <typename T, int VEC, int K, int L, int AHEAD>
+__global__ void __launch_bounds__(kThreads, kBwdCtas<K>) norm_bwd_kernel(const NormParams p)
 {
     __shared__ float2 red[2 * kThreads / 32];
     int turn = 0;
-    extern __shared__ float fold[];   // L < kThreads: [kThreads / L][C] sums of one gradient at a time
+    extern __shared__ __align__(16) unsigned char ring[];   // [AHEAD + 1][K][x, dy][kThreads] packs
+    float* fold = reinterpret_cast<float*>(ring);           // at the end, L < kThreads: [kThreads / L][C] sums of one gradient at a time
     using P = Pack<T, VEC>;
     const int lane = threadIdx.x % L, group = threadIdx.x / L;
     const long long step = (long long)gridDim.x * (kThreads / L);
     const int packs = p.C / VEC;
     const float inv_c = 1.f / (float)p.C;
-    float dw[K][VEC], db[K][VEC];
+    constexpr int Q = kPairs<VEC>;
+    Pair dw[K][Q], db[K][Q];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
-    auto fetch = [&](long long r, P (&xv)[K], P (&gv)[K], float& mu, float& rs) {
-        const long long row = r < p.rows ? r : 0;
-        const P* xs = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + row * p.C);
-        const P* gs = reinterpret_cast<const P*>(static_cast<const T*>(p.dy) + row * p.C);
+        for (int q = 0; q < Q; ++q) dw[k][q] = db[k][q] = pk2(0.f, 0.f);
+    auto row = [&](const void* base, long long r) { return reinterpret_cast<const P*>(static_cast<const T*>(base) + (r < p.rows ? r : 0) * p.C); };
+    auto slot = [&](int stage, int k, int which) { return reinterpret_cast<P*>(ring) + ((stage * K + k) * 2 + which) * kThreads + threadIdx.x; };
+    auto send = [&](long long r, int stage) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (lane + k * L < packs) {
-                xv[k] = xs[lane + k * L];
-                gv[k] = gs[lane + k * L];
+            if (r < p.rows && lane + k * L < packs) {
+                fetch16(slot(stage, k, 0), row(p.x, r) + lane + k * L);
+                fetch16(slot(stage, k, 1), row(p.dy, r) + lane + k * L);
             }
-        mu = p.mean[row];
-        rs = p.rstd[row];
+        fetch_mark();
     };
-    float w1[VEC];   // one pack a thread: its weights stay in registers
-    if (K == 1 && lane < packs) weights<VEC>(p.weight, lane * VEC, p.wdtype, 1.f, w1);
-    auto row_weights = [&](int k, float (&w)[VEC]) {
-        if (K > 1) {
-            weights<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = w1[e];
-        }
-    };
+    Pair w1[Q];   // one pack a thread: its weights stay in registers
+    if (K == 1 && lane < packs) weight_pairs<VEC>(p.weight, lane * VEC, p.wdtype, 1.f, w1);
+    const long long own = (long long)blockIdx.x * (kThreads / L) + group;
+    int stage = 0;
+    if constexpr (AHEAD > 0)
+        for (int s = 0; s < AHEAD; ++s) send(own + s * step, s);
+    float mu_next = p.mean[own < p.rows ? own : 0], rs_next = p.rstd[own < p.rows ? own : 0];
     for (long long r0 = (long long)blockIdx.x * (kThreads / L); r0 < p.rows; r0 += step) {
         const long long r = r0 + group;
         const bool live = r < p.rows;
         P xv[K], gv[K];
-        float mu, rs;
-        fetch(r, xv, gv, mu, rs);
-        float s1 = 0.f, s2 = 0.f;
+        const float mu = mu_next, rs = rs_next;
+        const long long next = r + step < p.rows ? r + step : 0;
+        mu_next = p.mean[next], rs_next = p.rstd[next];
+        if constexpr (AHEAD > 0) {
+            send(r + AHEAD * step, stage == 0 ? AHEAD : stage - 1);   // where the last round's were: they are in use no more
+            fetch_wait<AHEAD>();
+        }
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (lane + k * L < packs) {
-                float w[VEC];
-                row_weights(k, w);
+                xv[k] = AHEAD > 0 ? *slot(stage, k, 0) : row(p.x, r)[lane + k * L];
+                gv[k] = AHEAD > 0 ? *slot(stage, k, 1) : row(p.dy, r)[lane + k * L];
+            }
+        stage = stage == AHEAD ? 0 : stage + 1;
+        Pair xh[K][Q], g[K][Q], s1 = pk2(0.f, 0.f), s2 = pk2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float xh = (to_f32(xv[k].e[e]) - mu) * rs, dy = to_f32(gv[k].e[e]);
-                    const float g = dy * w[e];
-                    s1 += g;
-                    s2 = fmaf(g, xh, s2);
-                    if (live) {
-                        dw[k][e] = fmaf(dy, xh, dw[k][e]);
-                        db[k][e] += dy;
-                    }
+        for (int k = 0; k < K; ++k)
+            if (live && lane + k * L < packs) {
+                Pair w[Q];
+                if (K > 1) weight_pairs<VEC>(p.weight, (lane + k * L) * VEC, p.wdtype, 1.f, w);
+                plus<T, VEC>(xv[k], -mu, xh[k]);
+                plus<T, VEC>(gv[k], 0.f, g[k]);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    xh[k][q] = mul2(xh[k][q], pk2(rs, rs));
+                    dw[k][q] = fma2(g[k][q], xh[k][q], dw[k][q]);
+                    db[k][q] = add2(db[k][q], g[k][q]);
+                    g[k][q] = mul2(g[k][q], K == 1 ? w1[q] : w[q]);
+                    s1 = add2(s1, g[k][q]);
+                    s2 = fma2(g[k][q], xh[k][q], s2);
                 }
             }
-        const float2 sums = row_sums<L>(s1, s2, red, turn);
-        s1 = sums.x * inv_c;
-        s2 = sums.y * inv_c;
+        const float2 sums = row_sums<L>(both(s1), both(s2), red, turn);
+        const float m1 = -sums.x * inv_c, m2 = -sums.y * inv_c;
         if (live && p.dx) {
             P* dst = reinterpret_cast<P*>(static_cast<T*>(p.dx) + r * p.C);
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (lane + k * L < packs) {
-                    P o;
-                    float w[VEC];
-                    row_weights(k, w);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float xh = (to_f32(xv[k].e[e]) - mu) * rs;
-                        o.e[e] = from_f32<T>(rs * (to_f32(gv[k].e[e]) * w[e] - s1 - xh * s2));
-                    }
-                    dst[lane + k * L] = o;
+                    for (int q = 0; q < Q; ++q)
+                        g[k][q] = mul2(fma2(xh[k][q], pk2(m2, m2), add2(g[k][q], pk2(m1, m1))), pk2(rs, rs));
+                    dst[lane + k * L] = rounded<T, VEC>(g[k]);
                 }
         }
     }
     if (!p.partial) return;
+    auto put = [](float* dst, const Pair (&v)[Q]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            float x, y;
+            upk2(v[q], x, y);
+            dst[2 * q] = x;
+            if (VEC > 1) dst[2 * q + 1] = y;
+        }
+    };
     for (int which = 0; which < 2; ++which) {
         float* out = p.partial + ((long long)which * gridDim.x + blockIdx.x) * p.C;
         if (L == kThreads) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (lane + k * L < packs)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) out[(lane + k * L) * VEC + e] = which ? db[k][e] : dw[k][e];
+                    put(out + (lane + k * L) * VEC, which ? db[k] : dw[k]);
         } else {
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (lane + k * L < packs)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        fold[group * p.C + (lane + k * L) * VEC + e] = which ? db[k][e] : dw[k][e];
+                    put(fold + group * p.C + (lane + k * L) * VEC, which ? db[k] : dw[k]);
             __syncthreads();
             for (int c = threadIdx.x; c < p.C; c += kThreads) {
                 float s = 0.f;
@@ -353,21 +494,21 @@ template <typename T> __global__ void __launch_bounds__(kThreads) norm_bwd_long_
     }
 }
 
-// dw, db: the CTAs' partial rows added in a fixed order. 32 columns by 32 row lanes, four
-// rows in flight each.
+// dw, db: the CTAs' partial rows added in a fixed order. 32 columns by 32 row lanes, eight
+// rows in flight each: two waits for the cache at the most partial rows there are.
 __global__ void __launch_bounds__(1024) norm_fold_kernel(const NormParams p, int ctas)
 {
     __shared__ float part[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     const float* src = p.partial + (long long)blockIdx.y * ctas * p.C;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (c < p.C)
-        for (int t = lane; t < ctas; t += 128) {
+        for (int t = lane; t < ctas; t += 256) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 8; ++q)
                 if (t + 32 * q < ctas) s[q] += src[(long long)(t + 32 * q) * p.C + c];
         }
-    part[lane][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
+    part[lane][threadIdx.x & 31] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     // transposed: a warp adds one column's 32 lanes
     const float v = group_sum<32>(part[threadIdx.x & 31][lane]);
@@ -379,19 +520,29 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const NormParams p, int
 template <typename T, int VEC, int K, int L, int R = 1> cudaError_t run_fwd(const NormParams& p, cudaStream_t s)
 {
     constexpr int rows = kThreads / L * R;
-    const long long need = (p.rows + rows - 1) / rows, most = K == 1 ? 152 * 16 : 1ll << 30;
-    norm_fwd_kernel<T, VEC, K, L, R><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(p);
+    constexpr int AHEAD = VEC == 1 ? 0 : R * K == 4 ? 1 : 2;
+    constexpr size_t smem = AHEAD ? (AHEAD + 1) * R * K * kThreads * 16 : 0;
+    const long long need = (p.rows + rows - 1) / rows, most = AHEAD ? 152 * 4 : K == 1 ? 152 * 16 : 1ll << 30;
+    if constexpr (AHEAD > 0)
+        if (const cudaError_t e = allow_smem<norm_fwd_kernel<T, VEC, K, L, R, AHEAD>>(smem); e != cudaSuccess) return e;
+    norm_fwd_kernel<T, VEC, K, L, R, AHEAD><<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int VEC, int K, int L> cudaError_t run_bwd(const NormParams& p, int ctas, cudaStream_t s)
+template <typename T, int VEC, int K, int L> cudaError_t run_bwd(const NormParams& p, int& ctas, cudaStream_t s)
 {
-    const size_t smem = L == kThreads ? 0 : (size_t)(kThreads / L) * p.C * sizeof(float);
-    norm_bwd_kernel<T, VEC, K, L><<<ctas, kThreads, smem, s>>>(p);
+    ctas = std::min(ctas, 152 * kBwdCtas<K>);
+    constexpr int AHEAD = VEC == 1 ? 0 : K == 1 ? 2 : 1;
+    constexpr size_t ring = AHEAD ? (AHEAD + 1) * K * 2 * kThreads * 16 : 0;
+    const size_t fold = L == kThreads ? 0 : (size_t)(kThreads / L) * p.C * sizeof(float), smem = ring > fold ? ring : fold;
+    if constexpr (AHEAD > 0)
+        if (const cudaError_t e = allow_smem<norm_bwd_kernel<T, VEC, K, L, AHEAD>>(ring); e != cudaSuccess) return e;
+    norm_bwd_kernel<T, VEC, K, L, AHEAD><<<ctas, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
 // Threads per row. Forward: up to 32 lanes hold a row in up to 4 packs each, so that its sums
-// need no barrier. Backward: a pack a thread as far as the CTA goes, since two sums are kept per
+// need no barrier (65535 rows of 1024 bf16: 51 us, 75 with 128 threads a row), where there are rows
+// for all the warps. Backward: a pack a thread as far as the CTA goes, since two sums are kept per
 // element besides the two rows: 65535 rows of 1024 bf16 took 132 us with 4 packs a lane (224
 // registers, one CTA per SM).
 template <typename T, int VEC> cudaError_t pick_fwd(const NormParams& p, cudaStream_t s)
@@ -409,7 +560,7 @@ template <typename T, int VEC> cudaError_t pick_fwd(const NormParams& p, cudaStr
     norm_fwd_long_kernel<T><<<(unsigned)(p.rows < (1 << 30) ? p.rows : 1 << 30), kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int VEC> cudaError_t pick_bwd(const NormParams& p, int ctas, cudaStream_t s)
+template <typename T, int VEC> cudaError_t pick_bwd(const NormParams& p, int& ctas, cudaStream_t s)
 {
     const int packs = p.C / VEC;
     if (packs <= 4) return run_bwd<T, VEC, 1, 4>(p, ctas, s);
@@ -425,7 +576,7 @@ template <typename T, int VEC> cudaError_t pick_bwd(const NormParams& p, int cta
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t norm_typed(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+template <typename T> cudaError_t norm_typed(const NormParams& p, bool backward, int& ctas, cudaStream_t s)
 {
     constexpr int VEC = 16 / sizeof(T);
     const bool packed = p.C % VEC == 0 && aligned16(p.x) && aligned16(p.weight) && aligned16(p.bias) &&
@@ -434,7 +585,7 @@ template <typename T> cudaError_t norm_typed(const NormParams& p, bool backward,
     return packed ? pick_fwd<T, VEC>(p, s) : pick_fwd<T, 1>(p, s);
 }
 
-cudaError_t norm_any(const NormParams& p, bool backward, int ctas, cudaStream_t s)
+cudaError_t norm_any(const NormParams& p, bool backward, int& ctas, cudaStream_t s)
 {
     if (p.dtype == SDTW_F32) return norm_typed<float>(p, backward, ctas, s);
     if (p.dtype == SDTW_BF16) return norm_typed<__nv_bfloat16>(p, backward, ctas, s);
@@ -443,16 +594,18 @@ cudaError_t norm_any(const NormParams& p, bool backward, int ctas, cudaStream_t 
 
 }  // namespace
 
-// Four CTAs per SM (as many as are resident where a thread has one pack); fewer where there
-// are few rows, which are then not worth another partial row.
-int norm_partial_ctas(long long rows, int C, int sms)
+// At most as many CTAs as are resident, and their partial rows; fewer where there are few rows, which
+// are then not worth another partial row.
+int norm_partial_ctas(long long rows, int sms)
 {
-    (void)C;
-    const long long most = 4ll * sms, need = (rows + 7) / 8;
+    const long long most = (long long)kBwdCtas<1> * sms, need = (rows + 7) / 8;
     return (int)(need < most ? (need < 1 ? 1 : need) : most);
 }
 
-cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t s) { return norm_any(p, false, 0, s); }
+cudaError_t launch_norm_forward(const NormParams& p, cudaStream_t s) {
+    int none = 0;
+    return norm_any(p, false, none, s);
+}
 
 cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s)
 {
