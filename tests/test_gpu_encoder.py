@@ -11,7 +11,9 @@ Tolerances are bounds, element by element, of what the arithmetic of the operato
 and a 16-bit result, or a probability rounded to 16 bits before the product that consumes it, adds ut of
 itself. fp16 adds its smallest step (2^-24) to every rounding that can be subnormal.
 """
+import importlib.util
 import math
+import os
 
 import pytest
 
@@ -22,6 +24,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U32 = 2.0 ** -24
 UT = {F32: 2.0 ** -24, BF16: 2.0 ** -8, F16: 2.0 ** -11}
 TINY = {F32: 2.0 ** -126, BF16: 2.0 ** -126, F16: 2.0 ** -24}
@@ -504,3 +507,16 @@ def test_refusals(package):
                 lambda: package.layer_norm(x, w, w.bfloat16())):
         with pytest.raises(TypeError):
             bad()
+
+
+# The operators together: a few training steps through Soft-DTW, then a stream over the cache against the
+# whole causal encoding. The two differ by their roundings alone: some 20 of the type's along a feature's
+# way through two layers, each at most half a unit in the last place, against the features' norm.
+@pytest.mark.parametrize("dtype,bound", [("fp32", 20 * 2.0 ** -23), ("bf16", 20 * 2.0 ** -8), ("fp16", 20 * 2.0 ** -11)])
+def test_example_trains_and_streams(package, capsys, dtype, bound):
+    spec = importlib.util.spec_from_file_location("encoder_alignment", os.path.join(ROOT, "examples", "encoder_alignment.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    first, last, off = example.main(["--steps", "3", "--dtype", dtype, "--length", "70"])
+    assert math.isfinite(first) and math.isfinite(last)
+    assert off < bound
