@@ -159,6 +159,7 @@ __device__ __forceinline__ float sum16(float v) {
 template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 ? 1 : 2) attn_fwd_simt(const AttnParams p)
 {
     extern __shared__ float sm[];
+    if (p.splits > 1) let_next_come();
     constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
     float* Q = sm;
     float* K = Q + kT * LD;
@@ -284,6 +285,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
 template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p)
 {
     __shared__ float weight[4][128];
+    after_previous();
     const sdtw_attention& a = p.a;
     const long long all = (long long)a.B * a.Hkv * p.rows;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -655,9 +657,8 @@ cudaError_t launch_attn_backward_simt(const AttnParams& p, cudaStream_t s)
 template <typename T> static cudaError_t combine_typed(const AttnParams& p, cudaStream_t s)
 {
     const unsigned grid = (unsigned)(((long long)p.a.B * p.a.Hkv * p.rows + 3) / 4);
-    if (p.a.D % 4 == 0 && aligned16(p.out) && aligned16(p.out_rest)) attn_combine_kernel<T, 4><<<grid, 128, 0, s>>>(p);
-    else attn_combine_kernel<T, 1><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError();
+    if (p.a.D % 4 == 0 && aligned16(p.out) && aligned16(p.out_rest)) return launch_behind(attn_combine_kernel<T, 4>, grid, 128, s, p);
+    return launch_behind(attn_combine_kernel<T, 1>, grid, 128, s, p);
 }
 
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s)

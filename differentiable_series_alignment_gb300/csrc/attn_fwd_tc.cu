@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
     __shared__ uint32_t s_tmem;
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (p.splits > 1) let_next_come();
     if (warp == kLoader && lane == 0) prefetch_map(&maps.q), prefetch_map(&maps.k), prefetch_map(&maps.v);
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;

@@ -48,6 +48,24 @@ template <auto Kernel> cudaError_t allow_smem(size_t bytes) {
     return e;
 }
 
+// Launches a kernel that reads what the one before it in the stream writes, and begins with
+// after_previous(): its CTAs come while the other's last ones run, which hides what a launch takes
+// (2 us of the 16 of a small call that joins the shares of a key axis).
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = grid, c.blockDim = dim3(threads), c.stream = s, c.attrs = &at, c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+// Returns when the kernels before this one are complete and their results visible.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel behind this one come as soon as all CTAs have said so; it waits for them in after_previous().
+__device__ __forceinline__ void let_next_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct NormParams {
     const void *x, *weight, *bias, *dy;
     void *y, *dx, *dweight, *dbias;

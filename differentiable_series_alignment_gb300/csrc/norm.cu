@@ -499,6 +499,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) norm_bwd_long_
 __global__ void __launch_bounds__(1024) norm_fold_kernel(const NormParams p, int ctas)
 {
     __shared__ float part[32][33];
+    after_previous();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     const float* src = p.partial + (long long)blockIdx.y * ctas * p.C;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -611,8 +612,7 @@ cudaError_t launch_norm_backward(const NormParams& p, int ctas, cudaStream_t s)
 {
     cudaError_t e = norm_any(p, true, ctas, s);
     if (e != cudaSuccess || !p.partial) return e;
-    norm_fold_kernel<<<dim3((p.C + 31) / 32, 2), 1024, 0, s>>>(p, ctas);
-    return cudaGetLastError();
+    return launch_behind(norm_fold_kernel, dim3((p.C + 31) / 32, 2), 1024, s, p, ctas);
 }
 
 }  // namespace sdtw

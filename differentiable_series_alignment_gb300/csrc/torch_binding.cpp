@@ -47,6 +47,12 @@ void once_only()
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 Tensor like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }   // contiguous
+// Conversions that have nothing to do cost a call of the dispatcher each, a third of a small operator's time.
+Tensor packed(const Tensor& t) { return t.is_contiguous() ? t : t.contiguous(); }
+Tensor as_int(const Tensor& t, const Tensor& beside)
+{
+    return packed(t.scalar_type() == at::kInt && t.device() == beside.device() ? t : t.to(beside.device(), at::kInt));
+}
 Tensor workspace(size_t n, const Tensor& t)
 {
     return n ? at::empty({static_cast<int64_t>(n)}, t.options().dtype(at::kByte)) : Tensor();
@@ -104,7 +110,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
         if (want & 4) db = rows ? like(b) : at::zeros_like(b);
         if (rows) {
             if (want & 6) ws = workspace(sdtw_layernorm_workspace_bytes(rows, static_cast<int>(C)), x);
-            const Tensor dy = grads[0].contiguous();
+            const Tensor dy = packed(grads[0]);
             const Tensor& any = w.defined() ? w : b;
             float* mean = stats.data_ptr<float>();
             check_status(sdtw_layernorm_backward(ptr(dy), ptr(x), ptr(w), mean, mean + rows, rows, static_cast<int>(C),
@@ -133,9 +139,9 @@ Tensor layer_norm(const Tensor& x_, const Maybe& weight, const Maybe& bias, doub
         TORCH_CHECK_VALUE(t.device() == x_.device(), name, " must be on x's device");
     }
     TORCH_CHECK_TYPE(!w.defined() || !b.defined() || w.scalar_type() == b.scalar_type(), "weight and bias must be of one type");
-    const Tensor x = x_.contiguous();
-    if (w.defined()) w = w.contiguous();
-    if (b.defined()) b = b.contiguous();
+    const Tensor x = packed(x_);
+    if (w.defined()) w = packed(w);
+    if (b.defined()) b = packed(b);
     if (recording({x, w, b})) return LayerNorm::apply(x, given(w), given(b), eps);
     return norm_forward(x, w, b, eps, Tensor());
 }
@@ -206,11 +212,11 @@ variable_list rotary(const Tensor& q, const Maybe& k_, const Tensor& table_, con
                               ((positions.dim() == 2 && positions.size(0) == q.size(0) && positions.size(1) == q.size(1)) ||
                                (positions.dim() == 1 && positions.size(0) == q.size(1))),
                           "positions must be (B, N) or (N,) integers");
-        positions = positions.to(q.device(), at::kInt).contiguous();
+        positions = as_int(positions, q);
     } else {
         TORCH_CHECK_VALUE(q.size(1) <= table_.size(0), "the table has fewer positions than q");
     }
-    const Tensor table = table_.detach().contiguous();
+    const Tensor table = packed(table_.requires_grad() ? table_.detach() : table_);
     if (recording({q, k})) return Rotary::apply(q, given(k), table, given(positions), interleaved);
     return rotate(q, k, table, positions, interleaved, false);
 }
@@ -286,7 +292,7 @@ struct Attention : torch::autograd::Function<Attention> {
         } else if (want) {
             const sdtw_attention a = problem(q, k, v, m);
             const Tensor ws = workspace(sdtw_attention_workspace_bytes(&a, 1), q);
-            const Tensor dout = grads[0].contiguous();
+            const Tensor dout = packed(grads[0]);
             check_status(sdtw_attention_backward(&a, ptr(out), ptr(rest), static_cast<float*>(ptr(lse)), ptr(dout), ptr(dq), ptr(dk),
                                                  ptr(dv), ptr(ws), bytes(ws), stream()),
                          "sdtw_attention_backward");
@@ -300,7 +306,7 @@ Tensor lengths_of(const Maybe& t, const Tensor& q, const char* name)
     if (!t.has_value() || !t->defined()) return Tensor();
     TORCH_CHECK_VALUE(at::isIntegralType(t->scalar_type(), false) && t->dim() == 1 && t->size(0) == q.size(0), name,
                       " must be a (B,) integer tensor");
-    return t->to(q.device(), at::kInt).contiguous();
+    return as_int(*t, q);
 }
 
 // (out,) or (out, lse)
