@@ -6,7 +6,7 @@
 //   dq = scale dS k, dk = scale dS^T q, dv = P^T do
 //
 // Forward: one CTA per 64 packed rows (rows of the heads that share a key head, see
-// encoder.h) walks the keys in tiles of 64 with the running maximum and sum of the
+// encoder.h; 16 where there are no more, and another kernel below for up to 12) walks the keys in tiles of 64 with the running maximum and sum of the
 // softmax; S never leaves the SM. Backward: P is computed again from lse. One kernel
 // walks the keys for a tile of rows and gives dq, another walks the rows for a tile of
 // keys and gives dk and dv, summed over the heads that share them: no atomics, the same
@@ -14,6 +14,11 @@
 // 256 threads hold 4 x 4 of every 64 x 64 product (rows ty + 16 i, columns tx + 16 j), so
 // that a step of four features costs 8 16-byte shared loads for 64 FMAs; row pitches of
 // D + 4 floats keep those loads free of bank conflicts.
+// 8 x 512 samples, 4 heads of 64, fp32: forward 75 us (29 TFLOP/s), backward 229 (33 TFLOP/s) of the pipe's
+// 74. The 16-byte loads of a product's operands return four times what they read (each value goes to 16
+// threads), which keeps the load unit busy 82 % of the time, and 256 CTAs fill 304 places unevenly.
+// With 8 x 4 products a thread, half the threads and a third fewer loads, the latency of each warp's chain
+// took its place: 78 and 221 us.
 #include <cfloat>
 
 #include "common.cuh"
@@ -27,18 +32,18 @@ constexpr int kThr = 256;
 constexpr int kPitchP = kT + 4;   // pitch of a 64 x 64 tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Rows [0, kT) of a tile: row_ptr(i) is the row's first element or null (zeros). packed: rows
+// Rows [0, ROWS) of a tile: row_ptr(i) is the row's first element or null (zeros). packed: rows
 // begin at boundaries of four elements and D is a multiple of four. All loads of a thread
 // go out before its stores.
-template <typename T, int DP, typename F>
+template <typename T, int DP, int ROWS = kT, typename F>
 __device__ __forceinline__ void load_tile(float* dst, int D, bool packed, F row_ptr)
 {
-    constexpr int LD = DP + 4, N = kT * (DP / 4) / kThr;
+    constexpr int LD = DP + 4, ALL = ROWS * (DP / 4), N = (ALL + kThr - 1) / kThr;
     float4 v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int e = threadIdx.x + k * kThr, r = e / (DP / 4), c = (e % (DP / 4)) * 4;
-        const T* src = row_ptr(r);
+        const T* src = e < ALL ? row_ptr(r) : nullptr;
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (src == nullptr || c >= D) continue;
         if (packed) {
@@ -54,35 +59,35 @@ __device__ __forceinline__ void load_tile(float* dst, int D, bool packed, F row_
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int e = threadIdx.x + k * kThr;
-        *reinterpret_cast<float4*>(dst + e / (DP / 4) * LD + (e % (DP / 4)) * 4) = v[k];
+        if (e < ALL) *reinterpret_cast<float4*>(dst + e / (DP / 4) * LD + (e % (DP / 4)) * 4) = v[k];
     }
 }
 
 // acc[i][j] = sum_d a[ty + 16 i][d] * b[tx + 16 j][d], even and odd d apart in packed pairs
 // (one instruction for two products).
-template <int DP>
-__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, const float* b, int ty, int tx)
+template <int DP, int R>
+__device__ __forceinline__ void dot_tile(float (&acc)[R][4], const float* a, const float* b, int ty, int tx)
 {
     constexpr int LD = DP + 4;
-    unsigned long long s[4][4];
+    unsigned long long s[R][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = pk2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < DP; d += 4) {
-        ulonglong2 x[4], y[4];
+        ulonglong2 x[R], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * i) * LD + d);
+        for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * i) * LD + d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * j) * LD + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, s[i][j]));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float lo, hi;
@@ -98,21 +103,21 @@ template <int DP> struct Cols {
     static constexpr int N = DP >= 64 ? DP / 64 : 1;
     static __device__ __forceinline__ int at(int tx, int cc, int w) { return tx * W + 64 * cc + w; }
 };
-template <int DP>
-__device__ __forceinline__ void mul_tile(unsigned long long (&out)[4][Cols<DP>::N * Cols<DP>::W / 2], const float* p, const float* v,
+template <int DP, int R>
+__device__ __forceinline__ void mul_tile(unsigned long long (&out)[R][Cols<DP>::N * Cols<DP>::W / 2], const float* p, const float* v,
                                          int ty, int tx)
 {
     constexpr int LD = DP + 4, W = Cols<DP>::W, NC = Cols<DP>::N;
 #pragma unroll 2
     for (int k = 0; k < kT; k += 4) {
-        float4 x[4];
+        float4 x[R];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPitchP + k);
+        for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPitchP + k);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            unsigned long long a[4];
+            unsigned long long a[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
                 const float e = q == 0 ? x[i].x : q == 1 ? x[i].y : q == 2 ? x[i].z : x[i].w;
                 a[i] = pk2(e, e);
             }
@@ -127,7 +132,7 @@ __device__ __forceinline__ void mul_tile(unsigned long long (&out)[4][Cols<DP>::
                     y[0] = *reinterpret_cast<const unsigned long long*>(src);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int w = 0; w < W / 2; ++w) out[i][cc * (W / 2) + w] = fma2(a[i], y[w], out[i][cc * (W / 2) + w]);
             }
@@ -156,13 +161,15 @@ __device__ __forceinline__ float sum16(float v) {
     return v;
 }
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 ? 1 : 2) attn_fwd_simt(const AttnParams p)
+// R rows a thread: tiles of 64 rows, or of 16 where there are no more, which have a quarter of the
+// products: 8 rows, B = 16, 4 key heads of 128, 8000 keys 326 us, 537 with tiles of 64.
+template <typename T, int DP, int R> __global__ void __launch_bounds__(kThr, DP == 128 && R > 1 ? 1 : 2) attn_fwd_simt(const AttnParams p)
 {
     extern __shared__ float sm[];
     if (p.splits > 1) let_next_come();
-    constexpr int LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
+    constexpr int TR = 16 * R, LD = DP + 4, NC = Cols<DP>::N * Cols<DP>::W;
     float* Q = sm;
-    float* K = Q + kT * LD;
+    float* K = Q + TR * LD;
     float* V = K + kT * LD;
     float* P = V + kT * LD;
     const sdtw_attention& a = p.a;
@@ -170,8 +177,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
     const int heads = a.B * a.Hkv, bh = blockIdx.x % heads;
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     // the last rows see the most keys under a causal mask: they start first
-    const int r0 = (((p.rows + kT - 1) / kT) - 1 - (int)(blockIdx.x / heads)) * kT;
-    const int last = min(r0 + kT, p.rows) - 1;
+    const int r0 = (((p.rows + TR - 1) / TR) - 1 - (int)(blockIdx.x / heads)) * TR;
+    const int last = min(r0 + TR, p.rows) - 1;
     const RowRange rr(a, b);
     const int n_first = r0 / p.G, n_last = min(last / p.G, rr.n_b - 1);
     int lo = 0, hi = 0;
@@ -189,18 +196,18 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
     const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
     const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
-    load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
+    load_tile<T, DP, TR>(Q, a.D, p.packed, [&](int i) -> const T* {
         const int r = r0 + i;
         if (r >= p.rows) return nullptr;
         const int n = r / p.G;
         if (n >= rr.n_b) return nullptr;
         return q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2];
     });
-    int klo[4], khi[4];   // visible keys of this thread's rows
-    float m[4], l[4];
-    unsigned long long o[4][NC / 2];
+    int klo[R], khi[R];   // visible keys of this thread's rows
+    float m[R], l[R];
+    unsigned long long o[R][NC / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int r = r0 + ty + 16 * i;
         const int n = r / p.G;
         const bool live = r < p.rows && n < rr.n_b;
@@ -218,10 +225,10 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
         load_tile<T, DP>(K, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? kk + (j0 + j) * a.k_stride[1] : nullptr; });
         load_tile<T, DP>(V, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
         __syncthreads();
-        float s[4][4];
-        dot_tile<DP>(s, Q, K, ty, tx);
+        float s[R][4];
+        dot_tile<DP, R>(s, Q, K, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             float mx = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -245,10 +252,10 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
             for (int c = 0; c < NC / 2; ++c) o[i][c] = fma2(o[i][c], pk2(keep, keep), pk2(0.f, 0.f));
         }
         __syncthreads();
-        mul_tile<DP>(o, P, V, ty, tx);
+        mul_tile<DP, R>(o, P, V, ty, tx);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const int r = r0 + ty + 16 * i;
         const float total = sum16(l[i]);
         if (r >= p.rows) continue;
@@ -279,8 +286,183 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
     }
 }
 
+// R packed rows a CTA over a long key axis (new samples over a cache): K and V go straight into
+// registers, once for every R rows, and that bounds it. Eight lanes have a key, DP / 8 of its features each, and a
+// running maximum, sum and output of their own for every row, so that nothing is exchanged but the three
+// shuffles of a score; 16 packs of 4 features a lane are on their way at a time. The 32 groups of
+// eight lanes are joined at the end. Measured against tiles of 16 rows in shared memory, fp32: one row,
+// B = 8, 4 heads of 64, 4000 keys 23 us (2.9 TB/s) and 55; 8 rows, B = 16, 4 key heads of 128, 8000 keys 225 us
+// and 326; 12 rows, B = 8, 2 key heads of 64, 3000 keys 29 us and 31; 16 rows, 4 key heads of 64, 6000 keys
+// 104 us and 82: it takes up to 12 rows.
+template <typename T, int DP, int R> __global__ void __launch_bounds__(kThr, R == 1 ? 2 : 1) attn_fwd_few(const AttnParams p)
+{
+    constexpr int F = DP / 32, U = 8 / F, kGroups = kThr / 8, kWarps = kThr / 32;
+    __shared__ __align__(16) float s_o[kWarps][R][DP];
+    __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+    if (p.splits > 1) let_next_come();
+    const sdtw_attention& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, group = threadIdx.x >> 3;
+    const int b = blockIdx.x / a.Hkv, hk = blockIdx.x % a.Hkv;
+    const RowRange rr(a, b);
+    const int r0 = blockIdx.z * R, n_first = r0 / p.G, n_last = min((min(r0 + R, p.rows) - 1) / p.G, rr.n_b - 1);
+    const int lo = n_first <= n_last ? rr.lo(n_first) : 0, hi = n_first <= n_last ? rr.hi(n_last) : 0;
+    // this CTA's share, in the key tiles that the shares are counted in
+    int t_lo = lo / kT, t_hi = hi > lo ? (hi + kT - 1) / kT : t_lo;
+    if (p.splits > 1) {
+        const int per = (t_hi - t_lo + p.splits - 1) / p.splits;
+        t_lo = min(t_lo + per * (int)blockIdx.y, t_hi);
+        t_hi = min(t_lo + per, t_hi);
+    }
+    const int first = max(lo, t_lo * kT), end = min(hi, t_hi * kT);
+    using P4 = Pack<T, 4>;
+    auto pairs = [](const P4& v, unsigned long long (&out)[2]) {
+        out[0] = pk2(to_f32(v.e[0]), to_f32(v.e[1]));
+        out[1] = pk2(to_f32(v.e[2]), to_f32(v.e[3]));
+    };
+    int klo[R], khi[R];
+    float m[R], l[R];
+    unsigned long long q[R][F][2], o[R][F][2];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = r0 + i, n = r / p.G;
+        const bool live = r < p.rows && n < rr.n_b;
+        klo[i] = live ? rr.lo(n) : 0;
+        khi[i] = live ? rr.hi(n) : 0;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        const T* src = static_cast<const T*>(a.q) + b * a.q_stride[0] + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int c = (sub + 8 * f) * 4;
+            q[i][f][0] = q[i][f][1] = o[i][f][0] = o[i][f][1] = pk2(0.f, 0.f);
+            if (live && c < a.D) pairs(*reinterpret_cast<const P4*>(src + c), q[i][f]);
+        }
+    }
+    const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
+    const T* vv = static_cast<const T*>(a.v) + b * a.v_stride[0] + hk * a.v_stride[2];
+    const float s2 = a.scale * kLog2e;
+    for (int j0 = first; j0 < end; j0 += kGroups * U) {
+        P4 kx[U][F], vx[U][F];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kGroups + group;
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int c = (sub + 8 * f) * 4;
+                kx[u][f] = vx[u][f] = P4{};
+                if (j < end && c < a.D) {
+                    kx[u][f] = *reinterpret_cast<const P4*>(kk + j * a.k_stride[1] + c);
+                    vx[u][f] = *reinterpret_cast<const P4*>(vv + j * a.v_stride[1] + c);
+                }
+            }
+        }
+        float e[R][U];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                unsigned long long s = pk2(0.f, 0.f);
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    unsigned long long x[2];
+                    pairs(kx[u][f], x);
+                    s = fma2(q[i][f][1], x[1], fma2(q[i][f][0], x[0], s));
+                }
+                float x, y;
+                upk2(s, x, y);
+                x += y;
+#pragma unroll
+                for (int w = 4; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+                const int j = j0 + u * kGroups + group;
+                e[i][u] = j < end && j >= klo[i] && j < khi[i] ? x * s2 : -INFINITY;
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int u = 0; u < U; ++u) mx = fmaxf(mx, e[i][u]);
+            const float base = mx == -INFINITY ? 0.f : mx;   // nothing seen yet: every term is 0
+            const float keep = ex2(m[i] - base);
+            m[i] = mx;
+            l[i] *= keep;
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) o[i][f][h] = fma2(o[i][f][h], pk2(keep, keep), pk2(0.f, 0.f));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * kGroups + group;
+                if (j >= end || j < klo[i] || j >= khi[i]) continue;   // what is hidden is not touched, NaN or not
+                const float x = ex2(e[i][u] - base);
+                l[i] += x;
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    unsigned long long y[2];
+                    pairs(vx[u][f], y);
+                    o[i][f][0] = fma2(pk2(x, x), y[0], o[i][f][0]);
+                    o[i][f][1] = fma2(pk2(x, x), y[1], o[i][f][1]);
+                }
+            }
+        }
+    }
+    // the warp's four groups, then the warps
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+        for (int w = 8; w < 32; w <<= 1) {
+            const float m1 = __shfl_xor_sync(0xffffffffu, m[i], w), l1 = __shfl_xor_sync(0xffffffffu, l[i], w);
+            const float mx = fmaxf(m[i], m1), base = mx == -INFINITY ? 0.f : mx;
+            const float k0 = ex2(m[i] - base), k1 = ex2(m1 - base);
+            m[i] = mx;
+            l[i] = l[i] * k0 + l1 * k1;
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    o[i][f][h] = fma2(__shfl_xor_sync(0xffffffffu, o[i][f][h], w), pk2(k1, k1),
+                                      fma2(o[i][f][h], pk2(k0, k0), pk2(0.f, 0.f)));
+        }
+        if (lane < 8) {
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                ulonglong2 x;
+                x.x = o[i][f][0], x.y = o[i][f][1];
+                *reinterpret_cast<ulonglong2*>(&s_o[warp][i][(sub + 8 * f) * 4]) = x;
+            }
+            if (lane == 0) s_m[warp][i] = m[i], s_l[warp][i] = l[i];
+        }
+    }
+    __syncthreads();
+    for (int at = threadIdx.x; at < R * DP; at += kThr) {
+        const int i = at / DP, d = at % DP, r = r0 + i;
+        if (r >= p.rows || d >= a.D) continue;
+        float mx = -INFINITY, total = 0.f, res = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][i]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float x = ex2(s_m[w][i] - base);
+            total = fmaf(s_l[w][i], x, total);
+            res = fmaf(s_o[w][i][d], x, res);
+        }
+        res *= total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+        const float lse = total == 0.f ? -INFINITY : (mx + log2f(total)) * kLn2;
+        const int n = r / p.G, h = hk * p.G + r % p.G;
+        if (p.splits > 1) {
+            const long long row = (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r;
+            p.part_o[row * a.D + d] = res;
+            if (d == 0) p.part_lse[row] = lse;
+        } else {
+            const long long o_at = (((long long)b * a.N + n) * a.Hq + h) * a.D + d;
+            store_rounded(static_cast<T*>(p.out) + o_at, p.out_rest ? static_cast<T*>(p.out_rest) + o_at : nullptr, res);
+            if (d == 0 && p.lse) p.lse[((long long)b * a.Hq + h) * a.N + n] = lse;
+        }
+    }
+}
+
 // o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp lse_s: the shares of the key axis
-// joined, one warp per packed row. There are at most 128 shares; four shares' rows
+// joined, one warp per packed row. There are at most 128 shares; eight shares' rows
 // are in flight at a time. V: consecutive features per lane and load.
 template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p)
 {
@@ -323,13 +505,13 @@ template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
         const float* src = p.part_o + row * a.D + d;
-        for (int s0 = 0; s0 < p.splits; s0 += 4) {
-            P v[4];
+        for (int s0 = 0; s0 < p.splits; s0 += 8) {
+            P v[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 8; ++q)
                 if (s0 + q < p.splits) v[q] = *reinterpret_cast<const P*>(src + (s0 + q) * all * a.D);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 8; ++q)
                 if (s0 + q < p.splits)
 #pragma unroll
                     for (int e = 0; e < V; ++e) acc[e] = fmaf(ws[s0 + q], v[q].e[e], acc[e]);
@@ -349,6 +531,7 @@ template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine
 // difference dP - delta cancels where one key has most of a row, so o is taken with what
 // its rounding to 16 bits left; with the rounded o alone dq and dk were up to 5 times
 // further from their 64-bit values than a plain fp32 pass on short fp16 sequences.
+// One read of o, its rest and do bounds it: 2 x 4096 samples, 16 heads of 128, bf16 20 us, 5.0 TB/s.
 // Eight lanes per packed row, 32 rows per CTA, in packed order and padded to whole tiles;
 // VEC elements per load. For fp16 on the tensor cores also the largest squared norm of do
 // of the CTA's rows, and in further CTAs of v of 32 keys.
@@ -480,8 +663,8 @@ template <typename T, int DP> __device__ __forceinline__ void dq_cta(const AttnP
         load_tile<T, DP>(V, a.D, p.packed, [&](int j) -> const T* { return j0 + j < rr.m_b ? vv + (j0 + j) * a.v_stride[1] : nullptr; });
         __syncthreads();
         float s[4][4], dp[4][4];
-        dot_tile<DP>(s, Q, K, ty, tx);
-        dot_tile<DP>(dp, G, V, ty, tx);
+        dot_tile<DP, 4>(s, Q, K, ty, tx);
+        dot_tile<DP, 4>(dp, G, V, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -492,7 +675,7 @@ template <typename T, int DP> __device__ __forceinline__ void dq_cta(const AttnP
                     see ? ex2(fmaf(s[i][j], s2, -lse[i])) * (dp[i][j] - delta[i]) : 0.f;
             }
         __syncthreads();
-        mul_tile<DP>(dq, S, K, ty, tx);
+        mul_tile<DP, 4>(dq, S, K, ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -559,8 +742,8 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
         });
         __syncthreads();
         float s[4][4], dp[4][4];
-        dot_tile<DP>(s, K, Q, ty, tx);
-        dot_tile<DP>(dp, V, G, ty, tx);
+        dot_tile<DP, 4>(s, K, Q, ty, tx);
+        dot_tile<DP, 4>(dp, V, G, ty, tx);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = r0 + tx + 16 * j;
@@ -578,8 +761,8 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
             }
         }
         __syncthreads();
-        mul_tile<DP>(dv, P, G, ty, tx);
-        mul_tile<DP>(dk, S, Q, ty, tx);
+        mul_tile<DP, 4>(dv, P, G, ty, tx);
+        mul_tile<DP, 4>(dk, S, Q, ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -608,14 +791,25 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThr, DP == 128 
     else dq_cta<T, DP>(p, (int)blockIdx.x - dkv, sm);
 }
 
+template <typename T, int DP, int R> cudaError_t fwd_simt(const AttnParams& p, cudaStream_t s)
+{
+    constexpr size_t smem = sizeof(float) * ((16 * R + 2 * kT) * (DP + 4) + 16 * R * kPitchP);
+    const cudaError_t e = allow_smem<attn_fwd_simt<T, DP, R>>(smem);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = (unsigned)((p.rows + 16 * R - 1) / (16 * R));
+    attn_fwd_simt<T, DP, R><<<dim3(tiles * p.a.B * p.a.Hkv, p.splits), kThr, smem, s>>>(p);
+    return cudaGetLastError();
+}
 template <typename T, int DP> cudaError_t fwd_simt(const AttnParams& p, cudaStream_t s)
 {
-    constexpr size_t smem = sizeof(float) * (3 * kT * (DP + 4) + kT * kPitchP);
-    const cudaError_t e = allow_smem<attn_fwd_simt<T, DP>>(smem);
-    if (e != cudaSuccess) return e;
-    const unsigned tiles = (unsigned)((p.rows + kT - 1) / kT);
-    attn_fwd_simt<T, DP><<<dim3(tiles * p.a.B * p.a.Hkv, p.splits), kThr, smem, s>>>(p);
-    return cudaGetLastError();
+    if (p.few) {
+        const dim3 grid((unsigned)(p.a.B * p.a.Hkv), p.splits, (p.rows + 3) / 4);
+        if (p.rows == 1) attn_fwd_few<T, DP, 1><<<grid, kThr, 0, s>>>(p);
+        else if (p.rows == 2) attn_fwd_few<T, DP, 2><<<grid, kThr, 0, s>>>(p);
+        else attn_fwd_few<T, DP, 4><<<grid, kThr, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    return p.rows <= 16 ? fwd_simt<T, DP, 1>(p, s) : fwd_simt<T, DP, 4>(p, s);
 }
 
 template <typename T, int DP> cudaError_t bwd_simt(const AttnParams& p, cudaStream_t s)

@@ -11,14 +11,17 @@
 // no atomics, no partial dQ in memory, the same bits every time. The gradients of heads
 // that share keys are summed in the accumulator, as rows of one problem. Both kinds are one
 // launch: the dkv CTAs, few and long, start first and the dq CTAs fill the SMs that they leave.
-// Sixteen warps turn scores into probabilities (four warpgroups, 32 of the 128 columns each: with
-// 64 each, eight warps were too few to hide the latencies of the chain through them), one more
-// loads by TMA, two issue the products: one S and what P enters, the other dP and what dS
-// enters.
+// Sixteen warps turn scores into probabilities (four warpgroups, 32 of the 128 columns each; eight
+// warps of 64 columns were as fast: the products set the pace, not the warps), one more loads by
+// TMA, two issue the products: one S and what P enters, the other dP and what dS enters.
 // The 16-bit operands have tensor memory of their own where it is large enough (dq; dkv of heads of
 // up to 64): the next scores are then made as soon as the last ones have been read. The dkv CTAs
 // of wider heads have P^T over S^T and dS^T over dP^T: while the tensor cores run dV and the next S^T, the warps compute dS^T; while they run dK
 // and the next dP^T, the next P^T.
+// 2 x 4096 samples, causal, 16 heads of 128 over 4 key heads: 353 us for the 7 products of the visible
+// tiles, 1370 TFLOP/s, with the card near its power limit (a plain bf16 product sustains 1717).
+// 32 x 512 samples, 8 heads of 64, padded: 104 us: the products are
+// half as long as for 128 features, the exponentials, loads and hand-overs of a tile as many.
 #include "attn_tc.cuh"
 
 namespace sdtw {

@@ -25,6 +25,12 @@
 // the rounded ones: in the backward pass their errors then enter delta = do . o only by how they
 // differ from key to key, as those of dS itself do. Divided by the exact sum, which lse keeps,
 // dq was up to 1.9 times as far from its 64-bit value as a plain fp32 pass.
+//
+// 4 x 4096 samples, causal, 16 heads of 128 over 4 key heads: 224 us, 1230 TFLOP/s. A tile's chain of
+// scores, maximum, exponentials and product takes some 3600 cycles, the products of two tiles 2048 of
+// them: latency bounds it, next to the power limit (1365 of 1400 W). Clusters of two CTAs that share
+// the loads of K and V, and 16 softmax warps, made it no faster. One new sample of 16
+// streams over 8192 keys, 32 heads of 128 over 8: 76 us, 5.0 TB/s of K and V.
 #include "attn_tc.cuh"
 
 namespace sdtw {

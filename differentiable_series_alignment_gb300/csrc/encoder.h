@@ -114,6 +114,7 @@ struct AttnParams {
     // bottom of the format's range reach the products instead of being flushed to 0.
     float* row_lse;
     int grad_shift;
+    bool few;        // at most 12 rows, read in packs: the kernel for new samples over a cache
     // fp16 on the tensor cores: the largest squared norm of do in every 32 packed rows
     // ([B][Hkv][rows_pad / 32]) and of v in every 32 keys ([B][Hkv][ceil(M / 32)])
     float *norm_rows, *norm_keys;

@@ -100,7 +100,8 @@ AttnParams attn_params(const sdtw_attention* a)
     const bool single = p.rows <= p.tile_rows;
     const long long tiles = (long long)((p.rows + p.tile_rows - 1) / p.tile_rows) * a->B * a->Hkv;
     p.row_tiles = single ? (a->M > 128 ? 2 : 1) : a->D <= 64 || tiles < 2ll * device_sms() ? 1 : 2;
-    if (!p.tc) p.splits = key_splits(p, 64, 64, 2, 3., 2.);
+    p.few = !p.tc && p.packed && p.rows <= 12;   // see attn.cu
+    if (!p.tc) p.splits = p.few ? key_splits(p, 4, 64, p.rows == 1 ? 2 : 1, 3., 0.5) : key_splits(p, 64, 64, 2, 3., 2.);
     else if (single && p.row_tiles == 2) p.splits = key_splits(p, p.tile_rows, 256, 1, 5., 1.5);
     else p.splits = key_splits(p, p.row_tiles * p.tile_rows, 128, p.row_tiles == 1 && a->D <= 64 ? 2 : 1, 5., 1.5);
     p.grad_shift = 32;

@@ -353,12 +353,42 @@ def test_attention_of_few_rows_over_long_caches(package, N, G, M, D, dtype):
                                           (1024, 1024, 4, 1, 96), (1537, 1537, 6, 2, 64)])
 @pytest.mark.parametrize("causal,window,ragged", [(True, None, False), (False, None, True), (True, 600, False), (False, 900, True)])
 def test_attention_of_long_sequences(package, N, M, Hq, Hkv, D, causal, window, ragged, dtype):
-    """Long enough that neighbouring tiles share their loads."""
+    """More tiles of rows and keys than a CTA has in flight, in every order of masks."""
     gen = generator(N + M + D)
     q, do = randn(gen, 2, N, Hq, D, dtype=dtype, std=1.5), randn(gen, 2, N, Hq, D, dtype=dtype, std=0.3)
     k, v = randn(gen, 2, M, Hkv, D, dtype=dtype, std=1.5), randn(gen, 2, M, Hkv, D, dtype=dtype)
     lengths = lambda n: torch.tensor([n - 3, n // 3], device="cuda", dtype=torch.int32) if ragged else None  # noqa: E731
     check_attention(package, q, k, v, do, dtype, causal, window, lengths(N), lengths(M))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("N,G,M,D", [(1, 1, 1, 4), (1, 2, 70, 32), (2, 1, 300, 60), (1, 3, 513, 124), (3, 1, 65, 20), (4, 1, 1000, 36),
+                                     (2, 2, 31, 100), (5, 1, 200, 28), (2, 8, 90, 52), (17, 1, 90, 52)])
+def test_attention_of_one_to_seventeen_rows(package, N, G, M, D, dtype):
+    """Heads in packs of four features: of 16 bits, they do not fit the tensor cores."""
+    gen = generator(N + G + M + D)
+    q, do = randn(gen, 3, N, 2 * G, D, dtype=dtype, std=1.5), randn(gen, 3, N, 2 * G, D, dtype=dtype, std=0.3)
+    k, v = randn(gen, 3, M, 2, D, dtype=dtype, std=1.5), randn(gen, 3, M, 2, D, dtype=dtype)
+    kl = torch.tensor([M, 0, M // 2 + 1], device="cuda", dtype=torch.int32)
+    ql = torch.tensor([N, N, max(N - 1, 0)], device="cuda", dtype=torch.int32)
+    for args in (dict(causal=True, kl=kl), dict(), dict(window=9), dict(causal=True, window=40, ql=ql, kl=kl)):
+        check_attention(package, q, k, v, do, dtype, **args)
+
+
+@pytest.mark.parametrize("N,G", [(1, 1), (2, 1), (1, 4), (2, 8), (40, 2)])
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 63), (BF16, 60), (BF16, 64)])
+def test_what_no_row_sees_may_be_nan(package, N, G, dtype, D):
+    """Keys and values past the lengths or out of every row's window leave no trace, NaN or not."""
+    gen = generator(N * G + D)
+    q = randn(gen, 2, N, 2 * G, D, dtype=dtype)
+    k, v = randn(gen, 2, 700, 2, D, dtype=dtype), randn(gen, 2, 700, 2, D, dtype=dtype)
+    kl = torch.tensor([650, 333], device="cuda", dtype=torch.int32)
+    want = package.attention(q, k, v, causal=True, window=128, k_lengths=kl)
+    for t in (k, v):
+        for b, m in enumerate((650, 333)):
+            t[b, m:] = float("nan")
+            t[b, :(m - N - 127) // 256 * 256] = float("nan")    # whole tiles before the first row's window
+    assert torch.equal(package.attention(q, k, v, causal=True, window=128, k_lengths=kl), want)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
