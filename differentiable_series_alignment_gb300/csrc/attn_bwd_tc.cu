@@ -16,8 +16,8 @@
 // TMA, two issue the products: one S and what P enters, the other dP and what dS enters.
 // The 16-bit operands have tensor memory of their own where it is large enough (dq; dkv of heads of
 // up to 64): the next scores are then made as soon as the last ones have been read. The dkv CTAs
-// of wider heads have P^T over S^T and dS^T over dP^T: while the tensor cores run dV and the next S^T, the warps compute dS^T; while they run dK
-// and the next dP^T, the next P^T.
+// of wider heads have P^T over S^T and dS^T over dP^T: while the tensor cores run dV and the next S^T, the
+// warps compute dS^T; while they run dK and the next dP^T, the next P^T.
 // 2 x 4096 samples, causal, 16 heads of 128 over 4 key heads: 353 us for the 7 products of the visible
 // tiles, 1370 TFLOP/s, with the card near its power limit (a plain bf16 product sustains 1717).
 // 32 x 512 samples, 8 heads of 64, padded: 104 us: the products are

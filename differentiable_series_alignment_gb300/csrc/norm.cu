@@ -14,8 +14,8 @@
 // mixed-precision adds and worked on in pairs, which halved the instructions of both directions
 // (the backward issued 69 % of the time before), and coming rows are on their way to shared memory
 // meanwhile. 65535 rows of 1024 with fp32 weights: bf16 forward 51 us (5.2 TB/s), backward 80 us
-// (5.1 TB/s) and 6 for the fold; fp32 forward 108 us (5.0), backward 138 (5.9). A plain copy of as
-// many bytes runs at 5.6 TB/s. Without the rows ahead fp32 took 149 and 164.
+// (5.1 TB/s) and 6 for the fold, caches flushed before; fp32 forward 108 us (5.0), backward
+// 138 (5.9). A plain copy of as many bytes runs at 5.6 TB/s. Without the rows ahead fp32 took 149 and 164.
 #include <algorithm>
 
 #include "encoder.h"

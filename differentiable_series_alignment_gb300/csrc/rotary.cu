@@ -7,8 +7,8 @@
 // the program makes once, rounded once from 64 bits: an angle formed in fp32 would be
 // off by position * 2^-24 radians. One read and one write of q and k bound it; both
 // tensors are turned by one launch, and a thread turns the same features of several
-// heads with the cosines it holds in registers. 4 x 4096 samples, 16 + 4 heads of 128, bf16: 36 us a
-// direction, 4.6 TB/s of the 5.6 of a plain copy of as many bytes.
+// heads with the cosines it holds in registers. 4 x 4096 samples, 16 + 4 heads of 128, bf16: 34 us a
+// direction, 4.9 TB/s of the 5.6 of a plain copy of as many bytes.
 #include "encoder.h"
 
 namespace sdtw {
@@ -136,9 +136,10 @@ template <typename T, int VEC> cudaError_t run_rotary(const RotaryParams& p, cud
     const long long one = (long long)p.B * p.N * units;
     long long x = (one + kRotThreads - 1) / kRotThreads;
     if (x > 1 << 24) x = 1 << 24;
-    // the heads are shared out over as many CTAs as fill the SMs twice over (three are resident);
+    // the heads are shared out over as many CTAs as fill the SMs three times over (three are resident):
+    // 8 x 4096 samples, 16 heads of 64, fp32 49 us, 51 with two times, where the last ones are fewer;
     // a thread takes two heads at a time, one where there is too little work for that
-    const long long full = 152ll * 6;
+    const long long full = 152ll * 9;
     const bool pairs = x * ((heads + 1) / 2) >= full;
     const long long steps = pairs ? (heads + 1) / 2 : heads;
     long long y = (full + x - 1) / x;
