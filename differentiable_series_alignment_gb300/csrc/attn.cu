@@ -708,13 +708,7 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int j0 = block / heads * kT;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
-    // rows that see any key of the tile
-    const int j_last = min(j0 + kT, rr.m_b) - 1;
-    int row_lo = 0, row_hi = 0;
-    if (j0 <= j_last) {
-        row_lo = rr.row_lo(j0) * p.G;
-        row_hi = rr.row_hi(j_last) * p.G;
-    }
+    const RowRange::Rows rows = rr.seeing(j0, j0 + kT, p.G);
     const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
     const T* dout = static_cast<const T*>(p.dout);
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
@@ -728,7 +722,7 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
         for (int c = 0; c < NC / 2; ++c) dk[i][c] = dv[i][c] = pk2(0.f, 0.f);
     const float s2 = a.scale * kLog2e, back = ex2(-(float)p.grad_shift);
     const long long info = ((long long)b * a.Hkv + hk) * p.rows_pad;
-    for (int r0 = row_lo / kT * kT; r0 < row_hi; r0 += kT) {
+    for (int r0 = rows.lo / kT * kT; r0 < rows.hi; r0 += kT) {
         __syncthreads();
         load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;

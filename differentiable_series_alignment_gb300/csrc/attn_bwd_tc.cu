@@ -101,15 +101,9 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
     const int RT = p.tile_rows, G = p.G;
     const int j0 = block / heads * kKeys;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
-    const int j_last = min(j0 + kKeys, rr.m_b) - 1;
-    int t_lo = 0, t_hi = 0;   // tiles of packed rows that see a key of this CTA
-    if (j0 <= j_last) {
-        const int lo = rr.row_lo(j0), hi = rr.row_hi(j_last);
-        if (lo < hi) {
-            t_lo = lo * G / RT;
-            t_hi = (hi * G + RT - 1) / RT;
-        }
-    }
+    // tiles of packed rows that see a key of this CTA
+    const RowRange::Rows rows = rr.seeing(j0, j0 + kKeys, G);
+    int t_lo = rows.lo / RT, t_hi = (rows.hi + RT - 1) / RT;
     t_lo = uniform(t_lo), t_hi = uniform(t_hi);
     const int tiles = t_hi - t_lo;
 

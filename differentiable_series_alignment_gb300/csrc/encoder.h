@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/sdtw.h"
+#include "attn_range.h"
 
 namespace sdtw {
 
@@ -137,23 +138,5 @@ cudaError_t launch_attn_forward_simt(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_rowinfo(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_backward_simt(const AttnParams& p, cudaStream_t s);
-
-// Keys that packed row r of batch element b sees: [lo, hi), empty where lo >= hi.
-// Row n of n_b stands at key n + (m_b - n_b): the last row at the last key.
-struct RowRange {
-    int n_b, m_b, shift, left, right;
-    __device__ __forceinline__ RowRange(const sdtw_attention& a, int b) {
-        n_b = a.q_lengths ? min(max(a.q_lengths[b], 0), a.N) : a.N;
-        m_b = a.k_lengths ? min(max(a.k_lengths[b], 0), a.M) : a.M;
-        shift = m_b - n_b;
-        left = a.window_left;
-        right = a.window_right;
-    }
-    __device__ __forceinline__ int lo(int n) const { return left < 0 ? 0 : max(0, n + shift - left); }
-    __device__ __forceinline__ int hi(int n) const { return right < 0 ? m_b : min(m_b, n + shift + right + 1); }
-    // rows that see key j: [row_lo, row_hi)
-    __device__ __forceinline__ int row_lo(int j) const { return right < 0 ? 0 : max(0, j - shift - right); }
-    __device__ __forceinline__ int row_hi(int j) const { return left < 0 ? n_b : min(n_b, j - shift + left + 1); }
-};
 
 }  // namespace sdtw
