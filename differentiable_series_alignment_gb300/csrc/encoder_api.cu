@@ -214,6 +214,7 @@ sdtw_status sdtw_rotary(const void* q, const long long* q_stride, const void* k,
     if (B < 1 || N < 1 || Hq < 1 || D < 1 || length < 1 || (k && Hkv < 1)) return SDTW_ERR_EMPTY;
     if (!q || !q_stride || !q_out || !table || !good_dtype(dtype) || (!k != !k_out) || (k && !k_stride))
         return SDTW_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(table) & 7) return SDTW_ERR_ARG;   // a pair's cosine and sine are one load
     if (R < 2 || R % 2 || R > D) return SDTW_ERR_SHAPE;
     if (positions ? (pos_stride_b != 0 && pos_stride_b < N) : N > length) return SDTW_ERR_SHAPE;
     if (D > (1 << 20) || Hq > (1 << 20) || (k && Hkv > (1 << 20))) return SDTW_ERR_TOO_LARGE;

@@ -216,7 +216,8 @@ variable_list rotary(const Tensor& q, const Maybe& k_, const Tensor& table_, con
     } else {
         TORCH_CHECK_VALUE(q.size(1) <= table_.size(0), "the table has fewer positions than q");
     }
-    const Tensor table = packed(table_.requires_grad() ? table_.detach() : table_);
+    Tensor table = packed(table_.requires_grad() ? table_.detach() : table_);
+    if (reinterpret_cast<uintptr_t>(table.data_ptr()) & 7) table = table.clone();   // a pair's cosine and sine are one load
     if (recording({q, k})) return Rotary::apply(q, given(k), table, given(positions), interleaved);
     return rotate(q, k, table, positions, interleaved, false);
 }

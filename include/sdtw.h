@@ -351,7 +351,7 @@ sdtw_status sdtw_layernorm_backward(const void* dy, const void* x, const void* w
  * turned in pairs, (a, b) -> (a cos - b sin, b cos + a sin), by the angles of their position; the
  * features from R on are copied. R is even and at most D. interleaved: pairs are neighbours (2i, 2i + 1);
  * otherwise (i, i + R/2). table is (length, R / 2, 2) fp32: cos and sin of every position and pair
- * (8-byte aligned). positions is a DEVICE int array (B, N) (pos_stride_b = N) or (N,) (pos_stride_b = 0),
+ * (8-byte aligned, otherwise SDTW_ERR_ARG). positions is a DEVICE int array (B, N) (pos_stride_b = N) or (N,) (pos_stride_b = 0),
  * or NULL for 0 .. N-1; a position outside [0, length) gives NaN in the turned features. inverse
  * non-zero turns backwards: the gradient of the turned tensor. q_stride and k_stride are the strides of
  * batch, position and head in elements (features are contiguous); outputs are contiguous. k and k_out may be
