@@ -49,8 +49,13 @@ void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 Tensor like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }   // contiguous
 // Conversions that have nothing to do cost a call of the dispatcher each, a third of a small operator's time.
 Tensor packed(const Tensor& t) { return t.is_contiguous() ? t : t.contiguous(); }
-Tensor as_int(const Tensor& t, const Tensor& beside)
+// Integers as the kernels take them. What lies outside 32 bits becomes the nearest end of their range, which is
+// outside any table and beyond any length too.
+Tensor as_int(Tensor t, const Tensor& beside)
 {
+    constexpr int64_t low = std::numeric_limits<int>::min(), high = std::numeric_limits<int>::max();
+    if (t.scalar_type() == at::kUInt64) t = t.to(at::kDouble).clamp(0, static_cast<double>(high));
+    if (t.scalar_type() == at::kLong || t.scalar_type() == at::kUInt32) t = t.to(at::kLong).clamp(low, high);
     return packed(t.scalar_type() == at::kInt && t.device() == beside.device() ? t : t.to(beside.device(), at::kInt));
 }
 Tensor workspace(size_t n, const Tensor& t)

@@ -46,3 +46,31 @@ def test_a_rotary_table_may_begin_anywhere(package, offset, interleaved, dtype):
     got, want = (package.rotary(q, table=t, interleaved=interleaved) for t in (view, table))
     assert torch.equal(got, want)
     assert torch.equal(*(torch.autograd.grad(y, q, up)[0] for y in (got, want)))
+
+
+@pytest.mark.parametrize("wide", [torch.int64, torch.uint32])
+def test_positions_past_32_bits_are_outside_the_table(package, wide):
+    table = package.rotary_table(16, 4)
+    x = randn(generator(2), 1, 5, 2, 6)
+    far = [2 ** 32 + 3, 2 ** 31, -2 ** 32 + 1, -2 ** 63] if wide == torch.int64 else [2 ** 31, 2 ** 32 - 1, 2 ** 31 + 3, 16]
+    positions = torch.tensor([3] + far, dtype=wide, device="cuda")
+    got = package.rotary(x, table=table, positions=positions)
+    assert torch.isnan(got[:, 1:, :, :4]).all()
+    assert torch.equal(got[:, :1], package.rotary(x[:, :1], table=table, positions=torch.tensor([3], device="cuda", dtype=torch.int32)))
+    assert torch.equal(got[..., 4:], x[..., 4:])
+
+
+# --- attention ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("place", ["cuda", "cpu"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_lengths_past_32_bits_are_all_there_is(package, dtype, place):
+    gen = generator(3)
+    B, N, M = 6, 9, 70
+    q, k, v = randn(gen, B, N, 2, 32, dtype=dtype), randn(gen, B, M, 2, 32, dtype=dtype), randn(gen, B, M, 2, 32, dtype=dtype)
+    far = torch.tensor([2 ** 63 - 1, 2 ** 31, 2 ** 32 + 5, -2 ** 40, -2 ** 63, 8], device=place)
+    near = lambda n: torch.tensor([n, n, n, 0, 0, 8], dtype=torch.int32, device="cuda")  # noqa: E731
+    got = package.attention(q, k, v, causal=True, q_lengths=far, k_lengths=far, return_lse=True)
+    want = package.attention(q, k, v, causal=True, q_lengths=near(N), k_lengths=near(M), return_lse=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
