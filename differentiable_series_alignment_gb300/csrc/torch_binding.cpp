@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <cmath>
 #include <limits>
 #include <optional>
@@ -35,6 +36,11 @@ void check_cuda(const Tensor& t, const char* name)
 {
     TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor");
     dtype_of(t, name);
+}
+void check_sizes(const Tensor& t, const char* name)
+{
+    for (const int64_t n : t.sizes())
+        TORCH_CHECK_VALUE(n <= std::numeric_limits<int>::max(), name, " has a dimension of ", n, ", more than 32 bits count");
 }
 void check_status(sdtw_status s, const char* where)
 {
@@ -165,9 +171,11 @@ variable_list rotate(const Tensor& q_, const Tensor& k_, const Tensor& table, co
         long long ks[3] = {0, 0, 0};
         if (k.defined()) ks[0] = k.stride(0), ks[1] = k.stride(1), ks[2] = k.stride(2);
         const int N = static_cast<int>(q.size(1));
+        // positions are 32 bits: what a longer table has beyond is out of their reach
+        const int length = static_cast<int>(std::min<int64_t>(table.size(0), std::numeric_limits<int>::max()));
         check_status(sdtw_rotary(ptr(q), qs, ptr(k), ks, static_cast<int>(q.size(0)), N, static_cast<int>(q.size(2)),
                                  k.defined() ? static_cast<int>(k.size(2)) : 0, static_cast<int>(q.size(3)),
-                                 static_cast<int>(2 * table.size(1)), table.data_ptr<float>(), static_cast<int>(table.size(0)),
+                                 static_cast<int>(2 * table.size(1)), table.data_ptr<float>(), length,
                                  positions.defined() ? positions.data_ptr<int>() : nullptr,
                                  positions.defined() && positions.dim() == 2 ? N : 0, interleaved, inverse, dtype_of(q, "q"),
                                  ptr(qo), ptr(ko), stream()),
@@ -200,6 +208,7 @@ variable_list rotary(const Tensor& q, const Maybe& k_, const Tensor& table_, con
 {
     check_cuda(q, "q");
     TORCH_CHECK_VALUE(q.dim() == 4, "q must be (B, N, H, D)");
+    check_sizes(q, "q");
     const Tensor k = value(k_);
     if (k.defined()) {
         check_cuda(k, "k");
@@ -207,6 +216,7 @@ variable_list rotary(const Tensor& q, const Maybe& k_, const Tensor& table_, con
         TORCH_CHECK_VALUE(k.dim() == 4 && k.size(0) == q.size(0) && k.size(1) == q.size(1) && k.size(3) == q.size(3) &&
                               k.device() == q.device(),
                           "k must be (B, N, H, D) with q's batch, positions and features, on q's device");
+        check_sizes(k, "k");
     }
     TORCH_CHECK_VALUE(table_.dim() == 3 && table_.size(2) == 2 && table_.scalar_type() == at::kFloat && table_.device() == q.device(),
                       "table must be a (length, R / 2, 2) float32 tensor on q's device, as rotary_table gives");
@@ -325,6 +335,7 @@ variable_list attention(const Tensor& q_, const Tensor& k_, const Tensor& v_, bo
         check_cuda(*in[i], names[i]);
         TORCH_CHECK_TYPE(in[i]->scalar_type() == q_.scalar_type(), names[i], " must be of q's type");
         TORCH_CHECK_VALUE(in[i]->dim() == 4 && in[i]->device() == q_.device(), names[i], " must be (B, L, H, D), on q's device");
+        check_sizes(*in[i], names[i]);
     }
     TORCH_CHECK_VALUE(k_.sizes() == v_.sizes() && k_.size(0) == q_.size(0) && k_.size(3) == q_.size(3),
                       "k and v must both be (B, M, Hkv, D) with q's batch and features");

@@ -74,3 +74,32 @@ def test_lengths_past_32_bits_are_all_there_is(package, dtype, place):
     want = package.attention(q, k, v, causal=True, q_lengths=near(N), k_lengths=near(M), return_lse=True)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# --- sizes --------------------------------------------------------------------------------------
+
+def test_dimensions_past_32_bits_are_refused(package):
+    """Views whose strides are 0 have any size for a few bytes: none of it may be cut to 32 bits."""
+    table = package.rotary_table(8, 4)
+    one = torch.zeros(1, 1, 1, 8, device="cuda")
+    for shape in ((2 ** 32 + 2, 1, 1, 8), (1, 2 ** 32 + 2, 1, 8), (1, 1, 2 ** 32 + 2, 8), (1, 2 ** 31, 1, 8)):
+        long = one.expand(shape)
+        with pytest.raises(ValueError):
+            package.rotary(long, table=table, positions=torch.zeros((), dtype=torch.int32, device="cuda").expand(shape[:2]))
+        with pytest.raises(ValueError):
+            package.attention(long, one.expand(shape[0], 1, 1, 8), one.expand(shape[0], 1, 1, 8))
+    with pytest.raises(ValueError):
+        package.rotary(one, one.expand(1, 1, 2 ** 32 + 2, 8), table=table)
+    for shape in ((1, 2 ** 32 + 5, 1, 8), (1, 1, 2 ** 32 + 1, 8)):
+        long = one.expand(shape)
+        with pytest.raises(ValueError):
+            package.attention(one.expand(1, 1, shape[2], 8), long, long)
+
+
+def test_a_table_may_have_more_positions_than_32_bits_count(package):
+    """17 GB, of which a call reads a few lines."""
+    table = torch.zeros(2 ** 31 + 8, 1, 2, device="cuda")
+    table[7, 0, 0] = 1.0
+    x = randn(generator(4), 1, 2, 1, 2)
+    got = package.rotary(x, table=table, positions=torch.tensor([7, -1], device="cuda"))
+    assert torch.equal(got[:, 0], x[:, 0]) and torch.isnan(got[:, 1]).all()
