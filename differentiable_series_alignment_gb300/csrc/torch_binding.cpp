@@ -13,6 +13,7 @@
 #include <cmath>
 #include <limits>
 #include <optional>
+#include <utility>
 
 #include "../../include/sdtw.h"
 
@@ -166,19 +167,25 @@ variable_list rotate(const Tensor& q_, const Tensor& k_, const Tensor& table, co
     const c10::cuda::CUDAGuard guard(q_.device());
     const Tensor q = with_features(q_), k = k_.defined() ? with_features(k_) : Tensor();
     Tensor qo = like(q), ko = k.defined() ? like(k) : Tensor();
-    if (q.numel()) {
-        const long long qs[3] = {q.stride(0), q.stride(1), q.stride(2)};
-        long long ks[3] = {0, 0, 0};
-        if (k.defined()) ks[0] = k.stride(0), ks[1] = k.stride(1), ks[2] = k.stride(2);
+    // those that have something to turn; one of the two may have no heads
+    const Tensor* in[2] = {nullptr, nullptr};
+    void* out[2] = {nullptr, nullptr};
+    long long stride[2][3] = {};
+    int heads[2] = {0, 0}, count = 0;
+    for (const auto& [t, o] : {std::pair(&q, &qo), std::pair(&k, &ko)}) {
+        if (!t->defined() || t->numel() == 0) continue;
+        for (int i = 0; i < 3; ++i) stride[count][i] = t->stride(i);
+        in[count] = t, out[count] = ptr(*o), heads[count] = static_cast<int>(t->size(2)), ++count;
+    }
+    if (count) {
         const int N = static_cast<int>(q.size(1));
         // positions are 32 bits: what a longer table has beyond is out of their reach
         const int length = static_cast<int>(std::min<int64_t>(table.size(0), std::numeric_limits<int>::max()));
-        check_status(sdtw_rotary(ptr(q), qs, ptr(k), ks, static_cast<int>(q.size(0)), N, static_cast<int>(q.size(2)),
-                                 k.defined() ? static_cast<int>(k.size(2)) : 0, static_cast<int>(q.size(3)),
-                                 static_cast<int>(2 * table.size(1)), table.data_ptr<float>(), length,
-                                 positions.defined() ? positions.data_ptr<int>() : nullptr,
-                                 positions.defined() && positions.dim() == 2 ? N : 0, interleaved, inverse, dtype_of(q, "q"),
-                                 ptr(qo), ptr(ko), stream()),
+        check_status(sdtw_rotary(ptr(*in[0]), stride[0], count > 1 ? ptr(*in[1]) : nullptr, stride[1], static_cast<int>(q.size(0)), N,
+                                 heads[0], heads[1], static_cast<int>(q.size(3)), static_cast<int>(2 * table.size(1)),
+                                 table.data_ptr<float>(), length, positions.defined() ? positions.data_ptr<int>() : nullptr,
+                                 positions.defined() && positions.dim() == 2 ? N : 0, interleaved, inverse, dtype_of(q, "q"), out[0],
+                                 out[1], stream()),
                      "sdtw_rotary");
     }
     if (ko.defined()) return {qo, ko};

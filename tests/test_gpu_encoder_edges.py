@@ -103,3 +103,25 @@ def test_a_table_may_have_more_positions_than_32_bits_count(package):
     x = randn(generator(4), 1, 2, 1, 2)
     got = package.rotary(x, table=table, positions=torch.tensor([7, -1], device="cuda"))
     assert torch.equal(got[:, 0], x[:, 0]) and torch.isnan(got[:, 1]).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rotary_of_no_heads_beside_some(package, dtype, interleaved):
+    """Slices of a projection that leave q or k without a head: the other one is turned as it is alone."""
+    gen = generator(5)
+    table = package.rotary_table(16, 8)
+    some, none = randn(gen, 2, 5, 3, 16, dtype=dtype), randn(gen, 2, 5, 0, 16, dtype=dtype)
+    up = randn(gen, 2, 5, 3, 16, dtype=dtype)
+    alone = some.clone().requires_grad_()
+    want = package.rotary(alone, table=table, interleaved=interleaved)
+    gradient, = torch.autograd.grad(want, alone, up)
+    for first in (True, False):
+        torch.full((2, 5, 3, 16), math.nan, device="cuda", dtype=dtype)      # what the allocator gives next holds NaN
+        leaf = some.clone().requires_grad_()
+        out = package.rotary(*((leaf, none) if first else (none, leaf)), table=table, interleaved=interleaved)
+        got, empty = out if first else out[::-1]
+        assert torch.equal(got, want) and empty.shape == none.shape
+        assert torch.equal(torch.autograd.grad(got, leaf, up)[0], gradient)
+    assert package.rotary(none, table=table).shape == none.shape
+    assert [t.shape for t in package.rotary(none, none, table=table)] == [none.shape] * 2
