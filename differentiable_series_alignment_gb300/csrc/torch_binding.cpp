@@ -4,6 +4,7 @@
 // thread of its own, where every line of Python costs two or three times as much: the
 // forward and backward of a small layer norm took 200 us that way and half of that here.
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
@@ -73,8 +74,13 @@ size_t bytes(const Tensor& ws) { return ws.defined() ? static_cast<size_t>(ws.nu
 Maybe given(const Tensor& t) { return t.defined() ? Maybe(t) : std::nullopt; }   // autograd takes no undefined inputs
 Tensor value(const Maybe& t) { return t.has_value() ? *t : Tensor(); }
 bool wants(const Tensor& t) { return t.defined() && t.requires_grad(); }
+// Whether autograd records a call of these tensors. Tangents of forward mode would be lost: a tensor may carry one
+// without requiring a gradient.
 bool recording(std::initializer_list<Tensor> ts)
 {
+    const bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    for (const Tensor& t : ts)
+        TORCH_CHECK_NOT_IMPLEMENTED(!tangents || !t.defined() || !t._fw_grad(0).defined(), "the encoder operators have no forward-mode derivative");
     if (!at::GradMode::is_enabled()) return false;
     for (const Tensor& t : ts)
         if (wants(t)) return true;

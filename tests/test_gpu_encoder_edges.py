@@ -125,3 +125,31 @@ def test_rotary_of_no_heads_beside_some(package, dtype, interleaved):
         assert torch.equal(torch.autograd.grad(got, leaf, up)[0], gradient)
     assert package.rotary(none, table=table).shape == none.shape
     assert [t.shape for t in package.rotary(none, none, table=table)] == [none.shape] * 2
+
+
+# --- derivatives --------------------------------------------------------------------------------
+
+def test_forward_mode_tangents_are_refused(package):
+    """There is no forward-mode derivative; a result without a tangent would stand for a derivative of zero."""
+    fwd = torch.autograd.forward_ad
+    gen = generator(6)
+    x, w, q, k = randn(gen, 4, 8), randn(gen, 8), randn(gen, 1, 5, 2, 8), randn(gen, 1, 7, 2, 8)
+    table = package.rotary_table(8, 8)
+    calls = [(package.layer_norm, (x, w, w)), (lambda a, b: package.rotary(a, b, table=table), (q, q.clone())),
+             (package.attention, (q, k, k.clone()))]
+    for call, args in calls:
+        for grad in (False, True):
+            leaves = [t.clone().requires_grad_(grad) for t in args]
+            call(*leaves)
+            for at in range(len(args)):
+                with fwd.dual_level():
+                    dual = [fwd.make_dual(t, torch.ones_like(t)) if n == at else t for n, t in enumerate(leaves)]
+                    with pytest.raises(RuntimeError):          # NotImplementedError is one
+                        call(*dual)
+                    with torch.no_grad(), pytest.raises(RuntimeError):
+                        call(*dual)
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        with fwd._set_fwd_grad_enabled(False):                 # as in a function that brings its own rule
+            got = package.layer_norm(dual, w, w)
+        assert torch.equal(got, package.layer_norm(x, w, w))
