@@ -30,6 +30,11 @@ template <int N> __device__ __forceinline__ void turns_of(const float2* row, flo
     }
 }
 
+// The turned pair (a, b), the first product of each sum unrounded. Written out, so that packs and single
+// elements, whichever the alignment allows, give the same bits.
+__device__ __forceinline__ float turned_a(float a, float b, float2 t) { return fmaf(a, t.x, -(b * t.y)); }
+__device__ __forceinline__ float turned_b(float a, float b, float2 t) { return fmaf(b, t.x, a * t.y); }
+
 // A unit is 16 bytes of one feature row (VEC features): for halves it is VEC pairs, that
 // is VEC features of each half; the units after them copy the features from R on. A thread
 // has one unit of one token and goes through heads HEADS at a time, its cosines in registers.
@@ -108,19 +113,19 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryPara
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const float x = to_f32(va[q].e[e]), y = to_f32(vb[q].e[e]);
-                        va[q].e[e] = from_f32<T>(x * cs[e].x - y * cs[e].y);
-                        vb[q].e[e] = from_f32<T>(y * cs[e].x + x * cs[e].y);
+                        va[q].e[e] = from_f32<T>(turned_a(x, y, cs[e]));
+                        vb[q].e[e] = from_f32<T>(turned_b(x, y, cs[e]));
                     }
                     *reinterpret_cast<P*>(dst[q] + half) = vb[q];
                 } else if (turn && VEC == 1) {
                     const float x = to_f32(va[q].e[0]), y = to_f32(vb[q].e[0]);
-                    va[q].e[0] = from_f32<T>(x * cs[0].x - (float)mate * y * cs[0].y);
+                    va[q].e[0] = from_f32<T>(mate > 0 ? turned_a(x, y, cs[0]) : turned_b(y, x, cs[0]));
                 } else if (turn) {
 #pragma unroll
                     for (int e = 0; e + 1 < VEC; e += 2) {
                         const float x = to_f32(va[q].e[e]), y = to_f32(va[q].e[e + 1]);
-                        va[q].e[e] = from_f32<T>(x * cs[e / 2].x - y * cs[e / 2].y);
-                        va[q].e[e + 1] = from_f32<T>(y * cs[e / 2].x + x * cs[e / 2].y);
+                        va[q].e[e] = from_f32<T>(turned_a(x, y, cs[e / 2]));
+                        va[q].e[e + 1] = from_f32<T>(turned_b(x, y, cs[e / 2]));
                     }
                 }
                 *reinterpret_cast<P*>(dst[q]) = va[q];
