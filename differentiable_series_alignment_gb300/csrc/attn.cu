@@ -263,6 +263,9 @@ template <typename T, int DP, int R> __global__ void __launch_bounds__(kThr, DP 
         const float lse = total == 0.f ? -INFINITY : (m[i] + log2f(total)) * kLn2;
         float res[NC];
         unpack(o[i], inv, res);
+        if (total == 0.f)   // 0 whatever the keys hold that other rows of the tile see
+#pragma unroll
+            for (int c = 0; c < NC; ++c) res[c] = 0.f;
         const int n = r / p.G, h = hk * p.G + r % p.G;
         if (p.splits > 1) {
             const long long row = (((long long)blockIdx.y * a.B + b) * a.Hkv + hk) * p.rows + r;
@@ -534,7 +537,8 @@ template <typename T, int V> __global__ void __launch_bounds__(128) attn_combine
 // One read of o, its rest and do bounds it: 2 x 4096 samples, 16 heads of 128, bf16 20 us, 5.0 TB/s.
 // Eight lanes per packed row, 32 rows per CTA, in packed order and padded to whole tiles;
 // VEC elements per load. For fp16 on the tensor cores also the largest squared norm of do
-// of the CTA's rows, and in further CTAs of v of 32 keys.
+// of the CTA's rows, and in further CTAs of v of 32 keys; rows that see no key and keys that no row
+// sees have none.
 template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowinfo_kernel(const AttnParams p)
 {
     __shared__ float most[8];
@@ -557,7 +561,7 @@ template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowin
             const T* x = static_cast<const T*>(p.out) + o;
             const T* rest = p.out_rest ? static_cast<const T*>(p.out_rest) + o : nullptr;
             const T* g = static_cast<const T*>(p.dout) + o;
-            for (int d = sub * VEC; d < a.D; d += 8 * VEC) {
+            for (int d = sub * VEC; d < a.D && lse != -INFINITY; d += 8 * VEC) {
                 const P xv = *reinterpret_cast<const P*>(x + d), gv = *reinterpret_cast<const P*>(g + d);
                 P rv;
                 if (rest) rv = *reinterpret_cast<const P*>(rest + d);
@@ -579,9 +583,9 @@ template <typename T, int VEC> __global__ void __launch_bounds__(256) attn_rowin
     } else {
         const int per = (a.M + 31) / 32;
         const int c = (int)(blockIdx.x - row_ctas), bh = c / per, b = bh / a.Hkv;
-        const int m_b = a.k_lengths ? min(max(a.k_lengths[b], 0), a.M) : a.M;
+        const RowRange rr(a, b);
         const int j = c % per * 32 + (threadIdx.x >> 3);
-        if (j < m_b) {
+        if (j < rr.m_b && rr.row_lo(j) < rr.row_hi(j)) {
             const T* v = static_cast<const T*>(a.v) + b * a.v_stride[0] + j * a.v_stride[1] + bh % a.Hkv * a.v_stride[2];
             for (int d = sub * VEC; d < a.D; d += 8 * VEC) {
                 const P vv = *reinterpret_cast<const P*>(v + d);
@@ -683,6 +687,9 @@ template <typename T, int DP> __device__ __forceinline__ void dq_cta(const AttnP
         if (r >= p.rows) continue;
         float res[NC];
         unpack(dq[i], back, res);
+        if (klo[i] >= khi[i])   // 0 whatever the keys hold that other rows of the tile see
+#pragma unroll
+            for (int c = 0; c < NC; ++c) res[c] = 0.f;
         T* out = static_cast<T*>(p.dq) + (((long long)b * a.N + r / p.G) * a.Hq + hk * p.G + r % p.G) * a.D;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -709,6 +716,7 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
     const int j0 = block / heads * kT;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
     const RowRange::Rows rows = rr.seeing(j0, j0 + kT, p.G);
+    const int blind = rr.first_row();   // rows before see no key: they are left out, since 0 * NaN is not 0
     const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
     const T* dout = static_cast<const T*>(p.dout);
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
@@ -727,12 +735,12 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
         load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
-            return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
+            return r < p.rows && n < rr.n_b && n >= blind ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
         });
         load_tile<T, DP>(G, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
-            return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
+            return r < p.rows && n < rr.n_b && n >= blind ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
         });
         __syncthreads();
         float s[4][4], dp[4][4];

@@ -169,7 +169,8 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         const uint32_t id_s = idesc<T>(128, 128, false), id_o = idesc<T>(128, steps * 16, true);
         const uint32_t col = grad ? c_dp : c_s, acc = grad ? c_dk : c_dv, key_img = grad ? v_img : k_img;
         const uint32_t made = smem_u32(grad ? &s_dp : &s_s), ready = smem_u32(grad ? &s_ds : &s_p);
-        const int rows_b = rr.n_b * G;   // rows from here on hold anything
+        // rows of the first tile before `head`, which see no key, and rows from `rows_b` on hold anything
+        const int head = rr.first_row() * G - t_lo * RT, rows_b = rr.n_b * G;
         if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
         const uint32_t operand = grad ? c_ds : c_p;
         int e = 0, pe = 0;   // ring entries of the next scores and of the next product with rows
@@ -181,6 +182,10 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             if (ok && tail < RT && rr.n_b < a.N) {   // both warps: the same zeros
                 clear_rows<DP>(img, tail, lane);
                 clear_rows<DP>(img + Sh::tile, tail, lane);
+            }
+            if (ok && i == 0 && head > 0) {
+                clear_rows<DP>(img, 0, lane, head);
+                clear_rows<DP>(img + Sh::tile, 0, lane, head);
             }
             fence_after_sync();
             if (ok && elect_one()) {
@@ -532,7 +537,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         if (f0 < DP) {
             const long long at = mine ? (((long long)b * a.N + n) * a.Hq + h) * a.D + f0 : -1;
             write_rows<T, 32>(base + (uint32_t)warp * 32 * 64, c_dq + lanes + f0, tiles > 0 && ok, false,
-                              ok && !(live && tiles > 0), ok ? unlift : NAN, 0.f, more, p.dq, nullptr, at, min(32, a.D - f0) / 8, lane);
+                              ok && !(live && klo < khi && tiles > 0), ok ? unlift : NAN, 0.f, more, p.dq, nullptr, at, min(32, a.D - f0) / 8, lane);
         }
     }
     fence_before_sync();

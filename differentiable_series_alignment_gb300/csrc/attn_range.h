@@ -30,6 +30,9 @@ struct RowRange {
     // G times as many, fit 32 bits as N * G does: old keys of a long cache are up to M rows out of a window's reach.
     SDTW_BOTH int row_lo(int j) const { return right < 0 ? 0 : least(n_b, most(0, j - shift - right)); }
     SDTW_BOTH int row_hi(int j) const { return left < 0 ? n_b : most(0, least(n_b, j - shift + left + 1)); }
+    // Rows before this one stand before the first key and see none. Those from it on, up to n_b, each see one: a window
+    // takes in a row's own place, and the last row stands at the last key.
+    SDTW_BOTH int first_row() const { return m_b > 0 ? row_lo(0) : n_b; }
     // packed rows (G a position) that see any of the keys [j0, j1): [lo, hi), both 0 where there is none
     struct Rows {
         int lo, hi;

@@ -109,11 +109,11 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-// One warp clears rows [from, 128) of an image that a product over its rows is about to
-// read: what lies beyond a sequence's length may be NaN, and 0 * NaN is not 0.
-template <int DP> __device__ __forceinline__ void clear_rows(uint32_t img, int from, int lane) {
+// One warp clears rows [from, to) of an image that a product over its rows is about to read: what lies
+// beyond a sequence's length, or in rows that see no key, may be NaN, and 0 * NaN is not 0.
+template <int DP> __device__ __forceinline__ void clear_rows(uint32_t img, int from, int lane, int to = 128) {
     for (int c = 0; c < DP / 64; ++c)
-        for (uint32_t o = (uint32_t)from * 128 + lane * 16; o < kBox; o += 512)
+        for (uint32_t o = (uint32_t)from * 128 + lane * 16; o < (uint32_t)to * 128; o += 512)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(img + c * kBox + o), "r"(0) : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();

@@ -17,7 +17,7 @@ extern "C" void seeing(const sdtw_attention* a, int b, int j0, int j1, int G, in
 {
     const sdtw::RowRange r(*a, b);
     const auto rows = r.seeing(j0, j1, G);
-    out[0] = rows.lo, out[1] = rows.hi, out[2] = r.row_lo(j0), out[3] = r.row_hi(j0);
+    out[0] = rows.lo, out[1] = rows.hi, out[2] = r.row_lo(j0), out[3] = r.row_hi(j0), out[4] = r.first_row();
 }
 """
 
@@ -39,7 +39,7 @@ def seeing(tmp_path_factory):
         ql, kl = (ctypes.c_int * 1)(n), (ctypes.c_int * 1)(m)
         a = Attention(q_lengths=ctypes.addressof(ql), k_lengths=ctypes.addressof(kl), B=1, N=N, M=M, Hq=G, Hkv=1, D=8, window_left=left,
                       window_right=right, scale=1.0)
-        out = (ctypes.c_int * 4)()
+        out = (ctypes.c_int * 5)()
         lib.seeing(ctypes.byref(a), 0, j0, j1, G, out)
         return tuple(out)
     return call
@@ -64,9 +64,11 @@ def test_against_an_enumeration(seeing):
         j0 = rng.randrange(0, M)
         rows = [i for i in range(n)
                 if any((left < 0 or j >= i + m - n - left) and (right < 0 or j <= i + m - n + right) for j in range(j0, min(j0 + tile, m)))]
-        lo, hi, one_lo, one_hi = seeing(N, M, G, left, right, n, m, j0, j0 + tile)
+        lo, hi, one_lo, one_hi, first = seeing(N, M, G, left, right, n, m, j0, j0 + tile)
         assert list(range(lo, hi)) == [i * G + g for i in rows for g in range(G)]
         assert 0 <= one_lo <= n and 0 <= one_hi <= n
+        blind = [i for i in range(n) if not any((left < 0 or j >= i + m - n - left) and (right < 0 or j <= i + m - n + right) for j in range(m))]
+        assert blind == list(range(first))
 
 
 @pytest.mark.parametrize("M", [16778216, 1 << 25, 1 << 26, 1 << 27])
@@ -78,9 +80,9 @@ def test_the_largest_sizes_stay_within_the_rows(seeing, N, G, M):
             n, m = rng.choice([N, N // 2, 0, rng.randint(0, N)]), rng.choice([M, M // 2 + 1, 0, rng.randint(0, M)])
             left, right = rng.choice([-1, 0, 64, M, M + N - 1]), rng.choice([-1, 0, 64, M, M + N - 1])
             j0 = rng.choice([0, M // 2, M - 1, rng.randrange(M)]) // tile * tile
-            lo, hi, one_lo, one_hi = seeing(N, M, G, left, right, n, m, j0, j0 + tile)
+            lo, hi, one_lo, one_hi, first = seeing(N, M, G, left, right, n, m, j0, j0 + tile)
             assert (lo, hi) == expected(n, m, G, left, right, j0, j0 + tile)
-            assert 0 <= one_lo <= n and 0 <= one_hi <= n
+            assert 0 <= one_lo <= n and 0 <= one_hi <= n and 0 <= first <= n
 
 
 def test_old_keys_of_a_long_cache_are_seen_by_no_row(seeing):

@@ -153,3 +153,48 @@ def test_forward_mode_tangents_are_refused(package):
         with fwd._set_fwd_grad_enabled(False):                 # as in a function that brings its own rule
             got = package.layer_norm(dual, w, w)
         assert torch.equal(got, package.layer_norm(x, w, w))
+
+
+# --- rows that see no key -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 63), (F32, 128), (BF16, 64), (BF16, 128), (BF16, 36), (F16, 40), (F16, 128)])
+@pytest.mark.parametrize("N,M,Hq,Hkv", [(200, 90, 2, 2), (130, 5, 4, 2), (70, 69, 3, 1), (300, 40, 8, 2), (9, 3, 2, 1)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_rows_that_see_no_key_leave_no_trace(package, N, M, Hq, Hkv, padded, dtype, D):
+    """More rows than keys under a causal mask: the first rows stand before every key. Their output is 0, so what follows
+    may well give them a gradient of NaN (a division by their norm), and their queries may hold anything."""
+    gen = generator(N + M + D)
+    B = 3
+    ql = torch.tensor([N, N - 2, N], dtype=torch.int32, device="cuda") if padded else None
+    kl = torch.tensor([M, M - 1, 0], dtype=torch.int32, device="cuda") if padded else None
+    n, m = (t.tolist() if padded else [e] * B for t, e in ((ql, N), (kl, M)))
+    q, do = randn(gen, B, N, Hq, D, dtype=dtype, std=1.5), randn(gen, B, N, Hq, D, dtype=dtype, std=0.3)
+    k, v = randn(gen, B, M, Hkv, D, dtype=dtype, std=1.5), randn(gen, B, M, Hkv, D, dtype=dtype)
+    blind = [range(n[b] if m[b] == 0 else max(0, n[b] - m[b])) for b in range(B)]
+    for window in (None, 30):
+        results = []
+        for anything in (0.0, math.nan, math.inf, 6e4):
+            for b in range(B):
+                q[b, blind[b]], do[b, blind[b]] = anything, anything
+            leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+            out = package.attention(*leaves, causal=True, window=window, q_lengths=ql, k_lengths=kl)
+            results.append((out.detach(), *torch.autograd.grad(out, leaves, do)))
+        for b in range(B):
+            assert (results[0][0][b, blind[b]] == 0).all() and (results[0][1][b, blind[b]] == 0).all()
+        for other in results[1:]:
+            for a, b in zip(results[0], other):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (BF16, 64), (BF16, 128), (F16, 36)])
+def test_rows_that_see_no_key_are_0_beside_rows_of_nan(package, dtype, D):
+    """Keys that other rows see may be NaN: the rows that see none are 0 all the same, and so is their gradient."""
+    gen = generator(D)
+    q, k, v = (randn(gen, 1, n, 2, D, dtype=dtype) for n in (40, 10, 10))
+    do = randn(gen, 1, 40, 2, D, dtype=dtype)
+    k[:, 4], v[:, 4] = math.nan, math.inf
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    out = package.attention(*leaves, causal=True)
+    dq, = torch.autograd.grad(out, leaves[:1], do)
+    assert (out[:, :30] == 0).all() and (dq[:, :30] == 0).all()
+    assert torch.isnan(out[:, 34:]).all() and torch.isnan(dq[:, 34:]).all()
