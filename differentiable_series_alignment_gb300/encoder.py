@@ -57,7 +57,8 @@ def rotary_table(length: int, dim: int, base: float = 10000.0, scaling: str | No
             raise ValueError("scaling='yarn' needs original_length")
         # the pair that turns `turns` times over the original length
         at = lambda turns: dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
-        first, last = max(0, math.floor(at(beta_fast))), min(dim // 2 - 1, math.ceil(at(beta_slow)))
+        # either end of the ramp may lie beyond the pairs that there are
+        first, last = math.floor(at(beta_fast)), math.ceil(at(beta_slow))
         slow = ((pair - first) / max(last - first, 1e-3)).clamp(0, 1)
         freq = freq * (1 - slow) + freq / factor * slow
         magnitude = 0.1 * math.log(factor) + 1.0

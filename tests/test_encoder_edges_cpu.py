@@ -1,6 +1,7 @@
 """The encoder operators at the edges of their arguments, without a GPU: refusals of the C entry points before any launch, and the
 rotary tables where their scalings begin and end."""
 import ctypes
+import math
 
 import pytest
 
@@ -25,3 +26,27 @@ def test_rotary_refuses_a_table_off_eight_bytes(lib, table):
     vp, stride = ctypes.c_void_p, (ctypes.c_longlong * 3)(64, 64, 64)
     assert lib.load().sdtw_rotary(vp(0x1000), stride, None, None, 1, 4, 2, 0, 16, 8, vp(table), 8, None, 0, 0, 0, 0, vp(0x5000), None,
                                   None) == ARG
+
+
+@pytest.mark.parametrize("dim,base,original", [(128, 1e4, 131072), (64, 1e4, 2048), (64, 1e4, 64), (64, 1e4, 4), (128, 5e5, 8192),
+                                               (32, 1e4, 1 << 20)])
+def test_yarn_divides_the_slow_pairs_alone(dim, base, original):
+    """Pair by pair: how often it turns over the original length decides, wherever the ramp begins and ends."""
+    from differentiable_series_alignment_gb300 import rotary_table
+    factor, length = 4.0, 9
+    plain = lambda i: base ** (-2.0 * i / dim)  # noqa: E731
+    # real pair indices that turn beta_fast and beta_slow times
+    fast, slow = (dim * math.log(original / (t * 2 * math.pi)) / (2 * math.log(base)) for t in (32.0, 1.0))
+    first, last = math.floor(fast), math.ceil(slow)
+    magnitude = 0.1 * math.log(factor) + 1.0
+    table = rotary_table(length, dim, base=base, scaling="yarn", factor=factor, original_length=original, device="cpu")
+    for i in range(dim // 2):
+        turns = original * plain(i) / (2 * math.pi)
+        part = min(1.0, max(0.0, (i - first) / (last - first)))
+        assert turns <= 32.0 or part == 0.0
+        assert turns >= 1.0 or part == 1.0
+        freq = plain(i) * (1 - part) + plain(i) / factor * part
+        for p in range(length):
+            # one rounding to fp32 of a value of at most `magnitude`
+            assert float(table[p, i, 0]) == pytest.approx(magnitude * math.cos(p * freq), abs=2.0 ** -24 * magnitude + 1e-12)
+            assert float(table[p, i, 1]) == pytest.approx(magnitude * math.sin(p * freq), abs=2.0 ** -24 * magnitude + 1e-12)
