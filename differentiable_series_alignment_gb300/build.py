@@ -6,13 +6,14 @@ encoder operators as torch autograd functions, host code only).
 Every .cu file under csrc/ is compiled in parallel with nvcc
 (-gencode arch=compute_103a,code=sm_103a) and linked into
 differentiable_series_alignment_gb300/libsdtw.so next to this file; csrc/torch_binding.cpp
-is compiled with g++ against torch's headers and linked to it.
+is compiled with g++ against torch's headers and linked to it, where torch is installed.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -48,10 +49,15 @@ def _deps():
                                + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB, BINDING] if _has_torch() else [LIB]
+    if not all(os.path.exists(m) for m in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -102,17 +108,20 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
+    # the library first: it needs nvcc alone, whatever becomes of the binding
     with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
-        binding = ex.submit(_binding_object, cc)
+        binding = ex.submit(_binding_object, cc) if _has_torch() else None
         objs = list(ex.map(compile_one, srcs))
-        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC", "-Xlinker", "-soname=libsdtw.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    if binding is None:
+        print("torch is not installed: _binding.so, its side of the encoder operators, is left out", file=sys.stderr)
+    else:
+        _link_binding(binding.result())
     return LIB
 
 
