@@ -83,7 +83,9 @@ def _link_binding(obj: str):
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+    # the library by its name alone, found beside the binding. It has no soname, so that programs linked to it by
+    # path find it there.
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
            "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -113,7 +115,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         binding = ex.submit(_binding_object, cc) if _has_torch() else None
         objs = list(ex.map(compile_one, srcs))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC", "-Xlinker", "-soname=libsdtw.so"]
+    cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
