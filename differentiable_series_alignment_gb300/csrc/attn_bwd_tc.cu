@@ -93,6 +93,8 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
     __shared__ volatile int s_issued;           // else: S^T tiles issued after the first
     constexpr bool APART = DP == 64;
     __shared__ uint32_t s_tmem;
+    __shared__ int s_late;
+    const Late late{&g_status, &s_late};
     __shared__ __align__(16) float s_row[2][2][128];   // -lse and -delta of the tile's rows, two tiles
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -110,6 +112,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
     const uint32_t base = smem_u32(dyn);
     const uint32_t k_img = base, v_img = base + Sh::tile, ring = base + 2 * Sh::tile;
     if (threadIdx.x == 0) {
+        s_late = 0;
         mbar_init(smem_u32(&s_kv), 1);
         for (int e = 0; e < Sh::stages; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
@@ -139,7 +142,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
     bool ok = true;
 
     if (warp == kLoader) {
-        if (lane == 0 && tiles > 0) {
+        if (lane == 0 && tiles > 0 && p.skip != 1) {
             mbar_expect_tx(smem_u32(&s_kv), 2 * Sh::tile);
             load_keys<DP>(k_img, &maps.k, j0, hk, b, smem_u32(&s_kv));
             load_keys<DP>(v_img, &maps.v, j0, hk, b, smem_u32(&s_kv));
@@ -147,7 +150,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             int issued = 0;
             for (int i = 0; i < tiles && ok; ++i) {
                 const int e = i % Sh::stages;
-                if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, &g_status);
+                if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, late);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[e]), dst = ring + e * 2 * Sh::tile;
                 const int n0 = (t_lo + i) * (RT / G);
@@ -158,8 +161,8 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             }
             bool drained = true;   // no copy may be writing shared memory when the CTA ends
             for (int i = max(0, issued - Sh::stages); i < issued; ++i)
-                wait_for(drained, smem_u32(&s_full[i % Sh::stages]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, &g_status);
-            wait_for(drained, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
+                wait_for(drained, smem_u32(&s_full[i % Sh::stages]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, late);
+            wait_for(drained, smem_u32(&s_kv), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else if (warp >= kIssuer) {
@@ -171,13 +174,13 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         const uint32_t made = smem_u32(grad ? &s_dp : &s_s), ready = smem_u32(grad ? &s_ds : &s_p);
         // rows of the first tile before `head`, which see no key, and rows from `rows_b` on hold anything
         const int head = rr.first_row() * G - t_lo * RT, rows_b = rr.n_b * G;
-        if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, &g_status);
+        if (tiles > 0) wait_warp(ok, smem_u32(&s_kv), 0, p.wait_ns, late);
         const uint32_t operand = grad ? c_ds : c_p;
         int e = 0, pe = 0;   // ring entries of the next scores and of the next product with rows
         uint32_t ph = 0;
         auto scores = [&](int i) {
             const uint32_t img = ring + (uint32_t)e * 2 * Sh::tile;
-            wait_warp(ok, smem_u32(&s_full[e]), ph, p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_full[e]), ph, p.wait_ns, late);
             const int tail = rows_b - (t_lo + i) * RT;
             if (ok && tail < RT && rr.n_b < a.N) {   // both warps: the same zeros
                 clear_rows<DP>(img, tail, lane);
@@ -198,12 +201,12 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         if (tiles > 0) scores(0);
         for (int i = 0; i < tiles; ++i) {
             if (APART && i + 1 < tiles) {
-                wait_warp(ok, smem_u32(&s_read[grad]), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_read[grad]), (uint32_t)(i & 1), p.wait_ns, late);
                 scores(i + 1);
             }
             // dV takes dO, dK takes Q
             const uint32_t rows_img = ring + (uint32_t)pe * 2 * Sh::tile + (grad ? 0 : Sh::tile);
-            wait_warp(ok, ready, (uint32_t)(i & 1), p.wait_ns, &g_status);
+            wait_warp(ok, ready, (uint32_t)(i & 1), p.skip == 2 && i + 1 == tiles ? 0 : p.wait_ns, late);   // (test hook)
             // dK and the next dP^T would interleave with the next S^T, which the warps wait for first. Only
             // the order in the queue hangs on this, so it waits a while and no longer.
             if (!APART && grad && i + 1 < tiles)
@@ -222,7 +225,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
         if (lane == 0) {
             mma_commit(smem_u32(&s_end));
             bool fin = true;
-            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else {
@@ -259,7 +262,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             const float4* lse4 = reinterpret_cast<const float4*>(s_row[i & 1][0] + part * kCols);
             const float4* del4 = reinterpret_cast<const float4*>(s_row[i & 1][1] + part * kCols);
             const int r0 = (t_lo + i) * RT + part * kCols;
-            wait_warp(ok, smem_u32(&s_s), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_s), (uint32_t)(i & 1), p.wait_ns, late);
             fence_after_sync();
             float s[kCols];
             tmem_ld32_nowait(c_s + lanes + part * kCols, s);
@@ -285,14 +288,14 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
                 u[c / 2] = pack2<T>(s[c], s[c + 1]);
             }
             if (APART && i > 0) {   // dV has taken the last probabilities
-                wait_warp(ok, smem_u32(&s_free[0]), (uint32_t)((i - 1) & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_free[0]), (uint32_t)((i - 1) & 1), p.wait_ns, late);
                 fence_after_sync();
             }
             tmem_st16(c_p + lanes + a_col<APART>(part), u);
             tmem_wait_st();
             done(s_p);
 
-            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(i & 1), p.wait_ns, late);
             fence_after_sync();
             float d[kCols];
             tmem_ld32_nowait(c_dp + lanes + part * kCols, d);
@@ -308,7 +311,7 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
                 u[c / 2 + 1] = pack2<T>(x, y);
             }
             if (APART && i > 0) {   // dK has taken the last gradients
-                wait_warp(ok, smem_u32(&s_free[1]), (uint32_t)((i - 1) & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_free[1]), (uint32_t)((i - 1) & 1), p.wait_ns, late);
                 fence_after_sync();
             }
             tmem_st16(c_ds + lanes + a_col<APART>(part), u);
@@ -316,9 +319,10 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             done(s_ds);
         }
         if (tiles > 0) {
-            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, late);
             fence_after_sync();
         }
+        ok = ok && !late.any();
         // half of the warpgroups write dV, half dK, each half of the features, through the images of K
         // and V
         constexpr int F = DP / 2;
@@ -344,6 +348,8 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
     using Sh = BwdShape<DP>;
     __shared__ uint64_t s_q, s_full[Sh::slots], s_empty[Sh::slots], s_s, s_sread, s_dp, s_dpread, s_ds[2], s_dsfree[2], s_end;
     __shared__ uint32_t s_tmem;
+    __shared__ int s_late;
+    const Late late{&g_status, &s_late};
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int heads = a.B * a.Hkv, bh = block % heads;
@@ -359,6 +365,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
     const uint32_t base = smem_u32(dyn);
     const uint32_t q_img = base, g_img = base + Sh::tile, ring = base + 2 * Sh::tile;
     if (threadIdx.x == 0) {
+        s_late = 0;
         mbar_init(smem_u32(&s_q), 1);
         for (int e = 0; e < Sh::slots; ++e) {
             mbar_init(smem_u32(&s_full[e]), 1);
@@ -386,14 +393,14 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
     bool ok = true;
 
     if (warp == kLoader) {
-        if (lane == 0 && tiles > 0) {
+        if (lane == 0 && tiles > 0 && p.skip != 1) {
             mbar_expect_tx(smem_u32(&s_q), 2u * RT * 128 * (DP / 64));
             load_rows<DP>(q_img, &maps.q, r0 / G, hk, b, smem_u32(&s_q));
             load_rows<DP>(g_img, &maps.dout, r0 / G, hk, b, smem_u32(&s_q));
             int issued = 0;
             for (int i = 0; i < 2 * tiles && ok; ++i) {
                 const int e = i % Sh::slots;
-                if (i >= Sh::slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::slots - 1) & 1), p.wait_ns, &g_status);
+                if (i >= Sh::slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::slots - 1) & 1), p.wait_ns, late);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[e]);
                 mbar_expect_tx(bar, Sh::tile);
@@ -402,8 +409,8 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             }
             bool drained = true;
             for (int i = max(0, issued - Sh::slots); i < issued; ++i)
-                wait_for(drained, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, &g_status);
-            wait_for(drained, smem_u32(&s_q), 0, p.wait_ns, &g_status);
+                wait_for(drained, smem_u32(&s_full[i % Sh::slots]), (uint32_t)((i / Sh::slots) & 1), p.wait_ns, late);
+            wait_for(drained, smem_u32(&s_q), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else if (warp >= kIssuer) {
@@ -411,7 +418,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         const bool grad = warp == kIssuer + 1;
         const int steps = (a.D + 15) / 16;
         const uint32_t id_s = idesc<T>(128, kKeys, false), id_o = idesc<T>(128, steps * 16, true);
-        if (tiles > 0) wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, &g_status);
+        if (tiles > 0) wait_warp(ok, smem_u32(&s_q), 0, p.wait_ns, late);
         auto clear_tail = [&](int j, uint32_t kimg) {   // both warps: the same zeros
             const int tail = rr.m_b - (t.lo + j) * kKeys;
             if (ok && tail < kKeys && rr.m_b < a.M) clear_rows<DP>(kimg, tail, lane);
@@ -420,8 +427,8 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         uint32_t ph_k = 0, ph_v = 0;
         if (!grad) {
             for (int j = 0; j < tiles; ++j) {
-                if (j > 0) wait_warp(ok, smem_u32(&s_sread), (uint32_t)((j - 1) & 1), p.wait_ns, &g_status);
-                wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
+                if (j > 0) wait_warp(ok, smem_u32(&s_sread), (uint32_t)((j - 1) & 1), p.wait_ns, late);
+                wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, late);
                 const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
                 clear_tail(j, kimg);
                 fence_after_sync();
@@ -434,7 +441,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             }
         } else {
             auto upstream = [&]() {
-                wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, late);
                 fence_after_sync();
                 if (ok && elect_one()) {
                     mma_features<DP / 16>(c_dp, g_img, ring + (uint32_t)e_v * Sh::tile, steps, id_s);
@@ -447,11 +454,11 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             if (tiles > 0) upstream();
             for (int j = 0; j < tiles; ++j) {
                 if (j + 1 < tiles) {
-                    wait_warp(ok, smem_u32(&s_dpread), (uint32_t)(j & 1), p.wait_ns, &g_status);
+                    wait_warp(ok, smem_u32(&s_dpread), (uint32_t)(j & 1), p.wait_ns, late);
                     upstream();
                 }
                 const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
-                wait_warp(ok, smem_u32(&s_ds[j & 1]), (uint32_t)((j >> 1) & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_ds[j & 1]), (uint32_t)((j >> 1) & 1), p.skip == 2 && j + 1 == tiles ? 0 : p.wait_ns, late);
                 clear_tail(j, kimg);
                 fence_after_sync();
                 if (ok && elect_one()) {
@@ -466,7 +473,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         if (lane == 0) {
             mma_commit(smem_u32(&s_end));
             bool fin = true;
-            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else {
@@ -484,7 +491,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
         const unsigned long long mul = pk2(s2, s2), sub = pk2(nlse, nlse), gmul = pk2(gs, gs), gsub = pk2(ndel, ndel);
         for (int j = 0; j < tiles; ++j) {
             const int j0 = (t.lo + j) * kKeys + part * kCols;
-            wait_warp(ok, smem_u32(&s_s), (uint32_t)(j & 1), p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_s), (uint32_t)(j & 1), p.wait_ns, late);
             fence_after_sync();
             float s[kCols];
             tmem_ld32_nowait(c_s + lanes + part * kCols, s);
@@ -501,7 +508,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             }
 #pragma unroll
             for (int c = 0; c < kCols; ++c) s[c] = ex2(s[c]);
-            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(j & 1), p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_dp), (uint32_t)(j & 1), p.wait_ns, late);
             fence_after_sync();
             float d[kCols];
             tmem_ld32_nowait(c_dp + lanes + part * kCols, d);
@@ -520,7 +527,7 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
                 u[c / 2] = pack2<T>(x, y);
             }
             if (j > 1) {   // dQ has taken the gradients before the last
-                wait_warp(ok, smem_u32(&s_dsfree[j & 1]), (uint32_t)(((j >> 1) - 1) & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_dsfree[j & 1]), (uint32_t)(((j >> 1) - 1) & 1), p.wait_ns, late);
                 fence_after_sync();
             }
             tmem_st16(c_ds + (j & 1) * 64 + lanes + a_col<true>(part), u);
@@ -528,9 +535,10 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
             done(s_ds[j & 1]);
         }
         if (tiles > 0) {
-            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_end), 0, p.wait_ns, late);
             fence_after_sync();
         }
+        ok = ok && !late.any();
         // a warpgroup writes 32 features, through the images of Q and dO
         const float unlift = ex2(-(float)p.grad_shift), more = a.scale / gs;
         const int f0 = part * 32;

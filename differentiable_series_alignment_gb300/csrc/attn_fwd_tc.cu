@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
     __shared__ uint64_t s_q[NT], s_full[Sh::slots], s_empty[Sh::slots], s_s[NT], s_p[NT][2], s_o[NT], s_end[NT], s_turn[NT];
     __shared__ float s_join[3][128];
     __shared__ uint32_t s_tmem;
+    __shared__ int s_late;
+    const Late late{&g_status, &s_late};
     const sdtw_attention& a = p.a;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (p.splits > 1) let_next_come();
@@ -100,6 +102,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
     // the loader makes the barriers and sends for the first tiles before the CTA has met
     const uint32_t row_bytes = (uint32_t)RT * 128 * (DP / 64);
     if (warp == kLoader && lane == 0) {
+        s_late = 0;
         for (int w = 0; w < NT; ++w) {
             mbar_init(smem_u32(&s_q[w]), 1);
             mbar_init(smem_u32(&s_s[w]), 1);
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
             mbar_init(smem_u32(&s_empty[e]), solo ? 1 : 2);   // issuing warps that read it
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (!p.skip && any0) {
+        if (p.skip != 1 && any0) {
             mbar_expect_tx(smem_u32(&s_q[0]), row_bytes);
             load_rows<DP>(q_img, &maps.q, r00 / p.G, hk, b, smem_u32(&s_q[0]));
         }
@@ -127,13 +130,15 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
     bool ok = true;
 
     if (warp == kLoader) {
-        if (lane == 0 && !p.skip) {
+        if (lane == 0 && p.skip != 1) {
             const int n0 = r00 / p.G;
             const int total = 2 * (T1 - T0);
             int issued = 0;
+            auto left_out = [&](int i) { return p.skip == 2 && ((T0 + (i >> 1)) & 1); };   // test hook: every second key tile
             for (int i = 0; i < total && ok; ++i) {
+                if (left_out(i)) continue;
                 const int e = i % slots;
-                if (i >= slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / slots - 1) & 1), p.wait_ns, &g_status);
+                if (i >= slots) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / slots - 1) & 1), p.wait_ns, late);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&s_full[e]);
                 mbar_expect_tx(bar, Sh::tile);
@@ -147,9 +152,9 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
             // no copy may be writing shared memory when the CTA ends
             bool drained = true;
             for (int i = max(0, issued - slots); i < issued; ++i)
-                wait_for(drained, smem_u32(&s_full[i % slots]), (uint32_t)((i / slots) & 1), p.wait_ns, &g_status);
-            if (any0) wait_for(drained, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
-            if (NT == 2 && any1 && issued > 0) wait_for(drained, smem_u32(&s_q[NT - 1]), 0, p.wait_ns, &g_status);
+                if (!left_out(i)) wait_for(drained, smem_u32(&s_full[i % slots]), (uint32_t)((i / slots) & 1), p.wait_ns, late);
+            if (any0) wait_for(drained, smem_u32(&s_q[0]), 0, p.wait_ns, late);
+            if (NT == 2 && any1 && issued > 0) wait_for(drained, smem_u32(&s_q[NT - 1]), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else if (warp >= kIssuer) {
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         // softmaxes, with the tensor cores idle meanwhile.
         auto take_turn = [&](int j) {
             const int k = j - (T0 - 1) - (w == 0);   // the other's k-th pass; the first turn is tile 0's
-            if (k >= 0) wait_warp(ok, smem_u32(&s_turn[w]), (uint32_t)(k & 1), p.wait_ns, &g_status);
+            if (k >= 0) wait_warp(ok, smem_u32(&s_turn[w]), (uint32_t)(k & 1), p.wait_ns, late);
         };
         // a warp's own tiles in turn: O of one, then the scores of the next
         auto products = [&](uint32_t vimg, int j, int i, bool last) {
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
             const uint64_t vd = sdesc_mn(vimg);
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)(i & 1), p.wait_ns, &g_status);
+                wait_warp(ok, smem_u32(&s_p[w][part]), (uint32_t)(i & 1), p.wait_ns, late);
                 if (part == 0 && !solo) take_turn(j);
                 fence_after_sync();
                 if (ok && elect_one()) {
@@ -198,15 +203,15 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
                 const int iv = 2 * (step * i + w) + 1, ik = 2 * (step * (i + 1) + w);   // ring entries
                 if (i >= 0) {
                     const int e = iv % slots;
-                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((iv / slots) & 1), p.wait_ns, &g_status);
+                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((iv / slots) & 1), p.wait_ns, late);
                     products(ring + (uint32_t)e * Sh::tile, T0 + step * i + w, i, i == own - 1);
                     if (ok && elect_one()) mma_commit(smem_u32(&s_empty[e]));
                     __syncwarp();
                 }
                 if (i + 1 < own) {
                     const int e = ik % slots;
-                    if (i < 0) wait_warp(ok, smem_u32(&s_q[0]), 0, p.wait_ns, &g_status);
-                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((ik / slots) & 1), p.wait_ns, &g_status);
+                    if (i < 0) wait_warp(ok, smem_u32(&s_q[0]), 0, p.wait_ns, late);
+                    wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((ik / slots) & 1), p.wait_ns, late);
                     scores(ring + (uint32_t)e * Sh::tile);
                     if (ok && elect_one()) mma_commit(smem_u32(&s_empty[e]));
                     __syncwarp();
@@ -218,12 +223,12 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         for (int j = T0 - 1; j < T1 && !solo; ++j) {
             // a warp gives every entry back once it is there, also those that its tile does not see:
             // one that ran ahead would give back an entry's next use for its last
-            if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, &g_status);
+            if (j >= T0) wait_warp(ok, smem_u32(&s_full[e_v]), ph_v, p.wait_ns, late);
             if (j >= lo && j < hi) products(ring + (uint32_t)e_v * Sh::tile, j, j - lo, j == hi - 1);
-            if (j + 1 < T1) wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, &g_status);
+            if (j + 1 < T1) wait_warp(ok, smem_u32(&s_full[e_k]), ph_k, p.wait_ns, late);
             if (j + 1 >= lo && j + 1 < hi) {
                 if (!(j >= lo && j < hi)) take_turn(j);
-                if (j + 1 == lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, &g_status);
+                if (j + 1 == lo) wait_warp(ok, smem_u32(&s_q[w]), 0, p.wait_ns, late);
                 scores(ring + (uint32_t)e_k * Sh::tile);
             }
             if (!(j >= lo && j < hi) && !(j + 1 >= lo && j + 1 < hi)) take_turn(j);
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         if (lane == 0) {
             mma_commit(smem_u32(&s_end[w]));
             bool fin = true;
-            wait_for(fin, smem_u32(&s_end[w]), 0, p.wait_ns, &g_status);
+            wait_for(fin, smem_u32(&s_end[w]), 0, p.wait_ns, late);
         }
         __syncwarp();
     } else if (warp < kLoader) {
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         float m = -INFINITY, top = -INFINITY, off = 0.f;   // maximum in use, its trigger, its base
         float l = 0.f, lr = 0.f;                           // sums of the probabilities, exact and rounded
         for (int j = lo, i = 0; j < hi; j += step, ++i) {
-            wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)(i & 1), p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_s[w]), (uint32_t)(i & 1), p.wait_ns, late);
             fence_after_sync();
             float s[128];
 #pragma unroll
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         }
         bool read = lo < hi, other = false;
         if (read) {
-            wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, &g_status);
+            wait_warp(ok, smem_u32(&s_o[w]), 0, p.wait_ns, late);
             fence_after_sync();
         }
         float mul = 0.f, mul1 = 0.f, total = l, by = lr;
@@ -357,6 +362,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::threads, NT == 1 ? 2 : 1) at
         } else {
             mul = 1.f;
         }
+        ok = ok && !late.any();
         if (!(alternate && w == 1)) {
             const bool seen = live && read && total != 0.f;
             const float inv = !ok ? NAN : seen ? 1.f / by : 0.f;

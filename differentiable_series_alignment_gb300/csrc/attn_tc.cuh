@@ -119,14 +119,27 @@ template <int DP> __device__ __forceinline__ void clear_rows(uint32_t img, int f
     __syncwarp();
 }
 
-// ---- waits: bounded; after one that ran out the caller waits no more and the kernel
-// ends with NaN in its rows and the status word set.
-__device__ __forceinline__ void wait_for(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, int* status) {
+// ---- waits: bounded. After one that ran out the caller waits no more, and since it may then give others what is not
+// there, or not yet, the whole CTA's results become NaN: whoever writes them asks `cta` when its own last
+// wait is over. The status word is set too.
+struct Late {
+    int* status;   // of the device
+    int* cta;      // shared memory, 0 at first
+    __device__ __forceinline__ void set() const {
+        atomicOr(status, kStatusTimeout);
+        *static_cast<volatile int*>(cta) = 1;
+        __threadfence_block();
+    }
+    // by a whole warp
+    __device__ __forceinline__ bool any() const { return __any_sync(0xffffffffu, *static_cast<volatile int*>(cta) != 0); }
+};
+
+__device__ __forceinline__ void wait_for(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, const Late& late) {
     if (!ok || mbar_test(bar, parity)) return;
     const unsigned long long t0 = global_ns();
     while (!mbar_test(bar, parity)) {
         if (global_ns() - t0 > limit_ns) {
-            atomicOr(status, kStatusTimeout);
+            late.set();
             ok = false;
             return;
         }
@@ -134,8 +147,8 @@ __device__ __forceinline__ void wait_for(bool& ok, uint32_t bar, uint32_t parity
 }
 
 // The same by a whole warp, which learns one answer.
-__device__ __forceinline__ void wait_warp(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, int* status) {
-    wait_for(ok, bar, parity, limit_ns, status);
+__device__ __forceinline__ void wait_warp(bool& ok, uint32_t bar, uint32_t parity, unsigned long long limit_ns, const Late& late) {
+    wait_for(ok, bar, parity, limit_ns, late);
     ok = __all_sync(0xffffffffu, ok);
 }
 

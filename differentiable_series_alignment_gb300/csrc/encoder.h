@@ -127,7 +127,9 @@ struct AttnParams {
     int tile_rows;            // packed rows of a tile: whole positions, up to 128
     int row_tiles;            // forward: row tiles of a CTA, 1 or 2
     unsigned long long wait_ns;
-    int skip;                 // test hook: nothing is loaded, so that every wait runs out
+    // test hook. 1: nothing is loaded, so that every wait runs out; 2: one chain of waits alone does, in the forward
+    // pass for want of every second key tile, in the backward pass before the last product of a sum
+    int skip;
 };
 bool attn_tc_fits(const sdtw_attention& a);
 cudaError_t launch_attn_forward_tc(const AttnParams& p, cudaStream_t s);

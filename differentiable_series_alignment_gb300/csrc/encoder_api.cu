@@ -273,6 +273,7 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
         p.grad_shift = 32;
     }
     p.packed = p.packed && aligned16(dout);
+    if (p.tc) p.skip = debug_take_skip_publish();
     ENC_CUDA(launch_attn_rowinfo(p, st));
     ENC_CUDA(p.tc ? launch_attn_backward_tc(p, st) : launch_attn_backward_simt(p, st));
     return SDTW_OK;

@@ -279,7 +279,9 @@ const char* sdtw_status_string(sdtw_status s);
  * restores the default of 2 s) and, when `skip_publish` is non-zero, makes the
  * next sdtw_forward withhold the ready flags of the first strip so that waiting
  * tiles run out of time and the call reports SDTW_ERR_TIMEOUT through
- * sdtw_last_device_status. No GPU fault is involved. Process-wide. */
+ * sdtw_last_device_status. The next attention on the tensor cores takes it too: 1
+ * withholds all that its kernel would load, 2 lets a single chain of waits run out,
+ * reported by sdtw_encoder_status. No GPU fault is involved. Process-wide. */
 void sdtw_debug_set_wait(double seconds, int skip_publish);
 
 /* Testing hook. Forces choices the library otherwise makes itself, so that tests

@@ -198,3 +198,35 @@ def test_rows_that_see_no_key_are_0_beside_rows_of_nan(package, dtype, D):
     dq, = torch.autograd.grad(out, leaves[:1], do)
     assert (out[:, :30] == 0).all() and (dq[:, :30] == 0).all()
     assert torch.isnan(out[:, 34:]).all() and torch.isnan(dq[:, 34:]).all()
+
+
+# --- waits that run out -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("how", [1, 2])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("N,M,D", [(1, 256, 128), (3, 250, 64), (200, 500, 64), (200, 500, 128)])
+def test_a_wait_that_runs_out_leaves_nan_in_all_that_hangs_on_it(package, N, M, D, dtype, how):
+    """The loads are withheld, all of them or those of one chain of waits (a test hook; no fault is involved): whatever
+    the others of the CTA have computed by then, no row keeps a number that the missing part should have entered."""
+    gen = generator(M)
+    leaves = [randn(gen, 1, n, 2, D, dtype=dtype).requires_grad_() for n in (N, M, M)]
+    do = randn(gen, 1, N, 2, D, dtype=dtype)
+    out = package.attention(*leaves)
+    want = (out.detach(), *torch.autograd.grad(out, leaves, do, retain_graph=True))
+    debug, late = package.load().sdtw_debug_set_wait, 7            # SDTW_ERR_TIMEOUT
+    assert package.sdtw_encoder_status() == 0
+    try:
+        debug(0.02, how)
+        assert torch.isnan(package.attention(*leaves).detach()).all()
+        assert package.sdtw_encoder_status() == late
+        debug(0.02, how)
+        grads = torch.autograd.grad(out, leaves, do, retain_graph=True)
+        assert package.sdtw_encoder_status() == late
+        for g in grads:
+            assert torch.isnan(g).all()
+    finally:
+        debug(0.0, 0)
+    again = package.attention(*leaves)
+    for a, b in zip((again.detach(), *torch.autograd.grad(again, leaves, do)), want):
+        assert torch.equal(a, b)
+    assert package.sdtw_encoder_status() == 0
