@@ -144,7 +144,7 @@ Tensor layer_norm(const Tensor& x_, const Maybe& weight, const Maybe& bias, doub
 {
     check_cuda(x_, "x");
     TORCH_CHECK_VALUE(x_.dim() >= 1 && x_.size(-1) >= 1, "x must have a last dimension of at least 1");
-    TORCH_CHECK_VALUE(eps >= 0 && std::isfinite(eps), "eps must be finite and >= 0");
+    TORCH_CHECK_VALUE(eps >= 0 && std::isfinite(static_cast<float>(eps)), "eps must be >= 0 and finite in float32");
     Tensor w = value(weight), b = value(bias);
     for (int k = 0; k < 2; ++k) {
         const Tensor& t = k ? b : w;
@@ -357,7 +357,7 @@ variable_list attention(const Tensor& q_, const Tensor& k_, const Tensor& v_, bo
     TORCH_CHECK_VALUE(Hkv >= 1 && Hq >= 1 && Hq % Hkv == 0, "the query heads must be a multiple of the key heads");
     TORCH_CHECK_VALUE(!window || *window >= 1, "window must be >= 1");
     const double scale = scale_ ? *scale_ : 1.0 / std::sqrt(static_cast<double>(D));
-    TORCH_CHECK_VALUE(scale > 0 && std::isfinite(scale), "scale must be finite and > 0");
+    TORCH_CHECK_VALUE(static_cast<float>(scale) > 0 && std::isfinite(static_cast<float>(scale)), "scale must be > 0 and finite in float32");
     const int64_t left = window ? std::min<int64_t>(*window - 1, std::numeric_limits<int>::max() - 1) : -1;
     const int64_t right = causal ? 0 : left;
     const Tensor ql = lengths_of(q_lengths, q_, "q_lengths"), kl = lengths_of(k_lengths, q_, "k_lengths");

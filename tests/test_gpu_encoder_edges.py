@@ -230,3 +230,16 @@ def test_a_wait_that_runs_out_leaves_nan_in_all_that_hangs_on_it(package, N, M, 
     for a, b in zip((again.detach(), *torch.autograd.grad(again, leaves, do)), want):
         assert torch.equal(a, b)
     assert package.sdtw_encoder_status() == 0
+
+
+# --- refusals -----------------------------------------------------------------------------------
+
+def test_values_outside_fp32_are_refused_like_other_wrong_values(package):
+    x, q = torch.ones(2, 8, device="cuda"), torch.ones(1, 2, 1, 8, device="cuda")
+    for eps in (1e39, 1e300):
+        with pytest.raises(ValueError):
+            package.layer_norm(x, eps=eps)
+    for scale in (1e-60, 1e39, 1e300):
+        with pytest.raises(ValueError):
+            package.attention(q, q, q, scale=scale)
+    assert torch.isfinite(package.attention(q, q, q, scale=1e-30)).all()
