@@ -43,7 +43,7 @@ def rotary_table(length: int, dim: int, base: float = 10000.0, scaling: str | No
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     if not (base > 1 and factor >= 1):
         raise ValueError("base must be > 1 and factor >= 1")
-    pair = torch.arange(dim // 2, dtype=torch.float64, device=device or "cuda")
+    pair = torch.arange(dim // 2, dtype=torch.float64, device="cuda" if device is None else device)
     magnitude = 1.0
     if scaling == "ntk":
         if dim < 4:

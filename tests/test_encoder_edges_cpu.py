@@ -50,3 +50,19 @@ def test_yarn_divides_the_slow_pairs_alone(dim, base, original):
             # one rounding to fp32 of a value of at most `magnitude`
             assert float(table[p, i, 0]) == pytest.approx(magnitude * math.cos(p * freq), abs=2.0 ** -24 * magnitude + 1e-12)
             assert float(table[p, i, 1]) == pytest.approx(magnitude * math.sin(p * freq), abs=2.0 ** -24 * magnitude + 1e-12)
+
+
+def test_rotary_table_goes_where_it_is_told(monkeypatch):
+    """Device 0 by its number is a device, not the lack of one."""
+    from differentiable_series_alignment_gb300 import encoder
+    asked = []
+
+    def arange(*args, device=None, **kwargs):
+        asked.append(device)
+        return real(*args, device="cpu", **kwargs)
+    real = torch.arange
+    monkeypatch.setattr(encoder.torch, "arange", arange)
+    for device, want in ((0, 0), (None, "cuda"), ("cpu", "cpu")):
+        asked.clear()
+        encoder.rotary_table(4, 4, device=device)
+        assert asked[0] == want
