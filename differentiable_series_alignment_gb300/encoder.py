@@ -41,8 +41,8 @@ def rotary_table(length: int, dim: int, base: float = 10000.0, scaling: str | No
         raise ValueError("length must be >= 1 and dim even and >= 2")
     if scaling not in (None, "linear", "ntk", "yarn"):
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
-    if not (base > 1 and factor >= 1):
-        raise ValueError("base must be > 1 and factor >= 1")
+    if not (1 < base < math.inf and 1 <= factor < math.inf):
+        raise ValueError("base must be > 1 and factor >= 1, both finite")
     pair = torch.arange(dim // 2, dtype=torch.float64, device="cuda" if device is None else device)
     magnitude = 1.0
     if scaling == "ntk":
@@ -55,11 +55,13 @@ def rotary_table(length: int, dim: int, base: float = 10000.0, scaling: str | No
     elif scaling == "yarn":
         if original_length is None or original_length < 1:
             raise ValueError("scaling='yarn' needs original_length")
+        if not 0 < beta_slow < beta_fast < math.inf:
+            raise ValueError("scaling='yarn' needs 0 < beta_slow < beta_fast")
         # the pair that turns `turns` times over the original length
         at = lambda turns: dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
         # either end of the ramp may lie beyond the pairs that there are
         first, last = math.floor(at(beta_fast)), math.ceil(at(beta_slow))
-        slow = ((pair - first) / max(last - first, 1e-3)).clamp(0, 1)
+        slow = ((pair - first) / max(last - first, 1)).clamp(0, 1)
         freq = freq * (1 - slow) + freq / factor * slow
         magnitude = 0.1 * math.log(factor) + 1.0
     angle = torch.arange(length, dtype=torch.float64, device=pair.device)[:, None] * freq

@@ -66,3 +66,13 @@ def test_rotary_table_goes_where_it_is_told(monkeypatch):
         asked.clear()
         encoder.rotary_table(4, 4, device=device)
         assert asked[0] == want
+
+
+def test_rotary_table_refuses_ramps_that_go_nowhere():
+    from differentiable_series_alignment_gb300 import rotary_table
+    for fast, slow in ((1.0, 1.0), (1.0, 32.0), (32.0, 0.0), (32.0, -1.0), (math.nan, 1.0), (32.0, math.nan), (math.inf, 1.0)):
+        with pytest.raises(ValueError, match="beta"):
+            rotary_table(4, 8, scaling="yarn", factor=2.0, original_length=64, beta_fast=fast, beta_slow=slow, device="cpu")
+    for bad in (dict(base=math.inf), dict(scaling="ntk", factor=math.inf), dict(scaling="linear", factor=math.nan)):
+        with pytest.raises(ValueError):
+            rotary_table(4, 8, device="cpu", **bad)
