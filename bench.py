@@ -10,6 +10,9 @@ fused mode, i.e. 2*B*N*M DP cells. Metric: DP cells per second (B*N*M per
 forward+backward). Inputs are resident in HBM before the timed region; the L2 is
 flushed (a 256 MiB write) between timed steps, outside the per-step events.
 
+One JSON line goes to stdout. The figures behind it (per mode, roofline, the other
+workloads, the host's) go to stderr in a line that begins with "detail:".
+
 --impl reference times the fp64 CPU oracle on the host cores on a bounded sample
 of the same workload (the method has no runnable reference implementation).
 """
@@ -90,6 +93,20 @@ def time_max_over_ranks(total_ms, device=None):
 def job_value(world, steps, cells_per_step, total_ms):
     """Whole-job cells/s: every rank runs `steps` steps of its own batch (weak scaling)."""
     return world * steps * cells_per_step / (total_ms * 1e-3)
+
+
+def headline(line):
+    """`line` as it is printed: whole in a log's last few kilobytes. Figures beside the contract's are cut to six
+    digits, and what explains them or belongs to other workloads is left to the detail."""
+    def six(v):
+        return float(f"{v:.6g}") if isinstance(v, float) else v
+    keep = ("fwd_ms", "bwd_wavefront_ms", "fwd_bwd_ms", "peak_MB", "workspace_MB")
+    short = {k: v for k, v in line.items() if k != "per_config"}
+    short["per_mode"] = {m: {k: six(v[k]) for k in keep if k in v} for m, v in line["per_mode"].items()}
+    short["roofline"] = {k: six(line["roofline"].get(k)) for k in ("bound", "achieved", "peak", "unit", "frac", "traffic", "kernel")}
+    cpu = line.get("cpu_baseline") or {}
+    short["cpu_baseline"] = {k: six(cpu[k]) for k in ("value", "unit", "cores", "kind") if k in cpu}
+    return short
 
 
 def run_reference(args):
@@ -658,7 +675,8 @@ def run_ours(args):
         "clocks": clocks,
         "wall_s_timed": t_wall,
     }
-    print(json.dumps(line), flush=True)
+    log("detail: " + json.dumps({k: line[k] for k in ("per_mode", "roofline", "per_config", "cpu_baseline")}))
+    print(json.dumps(headline(line)), flush=True)
     if world > 1:
         dist.destroy_process_group()
     return 0
