@@ -716,7 +716,6 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
     const int j0 = block / heads * kT;   // the first keys are seen by the most rows
     const RowRange rr(a, b);
     const RowRange::Rows rows = rr.seeing(j0, j0 + kT, p.G);
-    const int blind = rr.first_row();   // rows before see no key: they are left out, since 0 * NaN is not 0
     const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0];
     const T* dout = static_cast<const T*>(p.dout);
     const T* kk = static_cast<const T*>(a.k) + b * a.k_stride[0] + hk * a.k_stride[2];
@@ -735,14 +734,19 @@ template <typename T, int DP> __device__ __forceinline__ void dkv_cta(const Attn
         load_tile<T, DP>(Q, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
-            return r < p.rows && n < rr.n_b && n >= blind ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
+            return r < p.rows && n < rr.n_b ? q + n * a.q_stride[1] + (hk * p.G + r % p.G) * a.q_stride[2] : nullptr;
         });
         load_tile<T, DP>(G, a.D, p.packed, [&](int i) -> const T* {
             const int r = r0 + i;
             const int n = r / p.G;
-            return r < p.rows && n < rr.n_b && n >= blind ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
+            return r < p.rows && n < rr.n_b ? dout + (((long long)b * a.N + n) * a.Hq + hk * p.G + r % p.G) * a.D : nullptr;
         });
         __syncthreads();
+        // rows that see no key, which stand before the first, are cleared: 0 * NaN is not 0
+        if (const int blind = min(rr.first_row() * p.G - r0, kT) * LD; blind > 0) {
+            for (int e = threadIdx.x; e < blind; e += kThr) Q[e] = G[e] = 0.f;
+            __syncthreads();
+        }
         float s[4][4], dp[4][4];
         dot_tile<DP, 4>(s, K, Q, ty, tx);
         dot_tile<DP, 4>(dp, V, G, ty, tx);
