@@ -18,6 +18,10 @@
 // up to 64): the next scores are then made as soon as the last ones have been read. The dkv CTAs
 // of wider heads have P^T over S^T and dS^T over dP^T: while the tensor cores run dV and the next S^T, the
 // warps compute dS^T; while they run dK and the next dP^T, the next P^T.
+// P and dS are rounded to the operands' 16 bits. Next to a result's own rounding that of dS is as large again, in squares, for dq
+// and dk, that of P for dv, and what the forward pass's rounded P leaves in delta comes on top for dq and dk: up to 1.5
+// times the error of a plain fp32 pass. dS as two 16-bit parts, each with a product of its own, would bring dq and dk to 1.02 to
+// 1.14 (a model in 64 bits) and took the case below from 379 to 475 us with flushed caches: not kept.
 // 2 x 4096 samples, causal, 16 heads of 128 over 4 key heads: 353 us for the 7 products of the visible
 // tiles, 1370 TFLOP/s, with the card near its power limit (a plain bf16 product sustains 1717).
 // 32 x 512 samples, 8 heads of 64, padded: 104 us: the products are

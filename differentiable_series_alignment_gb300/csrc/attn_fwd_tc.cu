@@ -29,8 +29,8 @@
 // 4 x 4096 samples, causal, 16 heads of 128 over 4 key heads: 224 us, 1230 TFLOP/s. A tile's chain of
 // scores, maximum, exponentials and product takes some 3600 cycles, the products of two tiles 2048 of
 // them: latency bounds it, next to the power limit (1365 of 1400 W). Clusters of two CTAs that share
-// the loads of K and V, and 16 softmax warps, made it no faster. One new sample of 16
-// streams over 8192 keys, 32 heads of 128 over 8: 76 us, 5.0 TB/s of K and V.
+// the loads of K and V, and 16 softmax warps, made it no faster. A softmax thread holds 128 scores and spills 88
+// bytes at 168 registers. One new sample of 16 streams over 8192 keys, 32 heads of 128 over 8: 76 us, 5.0 TB/s of K and V.
 #include "attn_tc.cuh"
 
 namespace sdtw {

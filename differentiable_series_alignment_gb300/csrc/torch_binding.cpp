@@ -2,7 +2,7 @@
 // torch's memory and streams, and calls of the C entry points of include/sdtw.h, nothing
 // more. Compiled rather than written in Python because autograd runs a backward pass in a
 // thread of its own, where every line of Python costs two or three times as much: the
-// forward and backward of a small layer norm took 200 us that way and half of that here.
+// forward and backward of a layer norm of 16384 x 64 took some 300 us that way and 130 here.
 #include <ATen/ATen.h>
 #include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>

@@ -6,7 +6,7 @@
 
 Tensors are fp32, bf16 or fp16 on a CUDA device; every step of the operators runs
 in libsdtw.so's kernels, on the current stream of the tensors' device. Wrong shapes and
-values raise ValueError, wrong types TypeError.
+values raise ValueError, wrong types TypeError, tangents of forward-mode differentiation NotImplementedError.
 """
 from __future__ import annotations
 
@@ -73,7 +73,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None = None, *, table: torch.Tenso
     """q (B, N, Hq, D) and, where given, k (B, N, Hkv, D) with the first 2 * table.shape[1]
     features of every head turned by their position's angles, differentiable in q and k. Returns the
     turned q, or (q, k). Pairs are neighbouring features (interleaved) or (i, i + R/2). positions (B, N) or
-    (N,) integers index the table; None stands for 0 .. N-1. A position outside the table gives NaN."""
+    (N,) integers of any width index the table; None stands for 0 .. N-1. A position outside the table gives NaN."""
     out = _lib.binding().rotary(q, k, table, positions, interleaved)
     return out[0] if k is None else tuple(out)
 
@@ -87,10 +87,14 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
     head h // (Hq // Hkv). D is at most 128; scale defaults to 1 / sqrt(D). Any strides do where features
     are contiguous (slices of one projection, a cache longer than what is filled of it).
 
-    q_lengths and k_lengths (B,) make a padded batch: element b has n_b rows and m_b keys, and what lies
-    beyond them is not used. Row n stands at key n + (m_b - n_b), so the newest row stands at the newest
+    q_lengths and k_lengths (B,), bounded by N and M, make a padded batch: element b has n_b rows and m_b keys, and
+    what lies beyond them is not used. Row n stands at key n + (m_b - n_b), so the newest row stands at the newest
     key: causal hides the keys after a row's own, window=w the keys w or more away from it. Rows without a
     visible key, and rows from n_b on, are 0 and pass no gradient.
+
+    Scores, sums and accumulators are fp32. In bf16 and fp16 the tensor cores take the probabilities and, in the
+    backward pass, the gradients of the scores rounded to the type: results are some 1.2 (out), 1.4 (dk, dv) and 1.5
+    (dq) times as far from exact as their own rounding. float32 rounds results alone.
 
     N = 1 over a cache of M keys is the step of a growing series; the key axis is then split over the SMs.
     return_lse gives (out, lse): the logarithm (B, Hq, N) of each row's sum of exp(score), fp32, not

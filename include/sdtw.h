@@ -320,10 +320,11 @@ sdtw_status sdtw_debug_exp2_neg(const float* x, float* out, int n, void* stream)
  *  - Elements are fp32, bf16 or fp16 (sdtw_dtype). All sums, statistics and
  *    probabilities are formed in fp32 and results are rounded once; the 16-bit
  *    tensor-core paths of attention round the probabilities and their gradients to
- *    the element type before the products that consume them.
+ *    the element type before the products that consume them (results are then 1.2 to 1.5
+ *    times as far from exact as their own rounding).
  *  - Outputs and gradients are overwritten, never accumulated; every result has the
  *    same bits on every call (no atomics).
- *  - A wait inside a kernel that runs out of time leaves NaN in the rows concerned
+ *  - A wait inside a kernel that runs out of time leaves NaN in all that its CTA computes
  *    and sets a status word of the device, read by sdtw_encoder_status.
  * ------------------------------------------------------------------------- */
 
