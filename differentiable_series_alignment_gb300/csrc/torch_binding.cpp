@@ -14,12 +14,15 @@
 #include <cmath>
 #include <limits>
 #include <optional>
+#include <stdexcept>
+#include <string>
 #include <utility>
 
 #include "../../include/sdtw.h"
 
 namespace {
 
+namespace py = pybind11;
 using at::Tensor;
 using torch::autograd::AutogradContext;
 using torch::autograd::variable_list;
@@ -44,9 +47,16 @@ void check_sizes(const Tensor& t, const char* name)
     for (const int64_t n : t.sizes())
         TORCH_CHECK_VALUE(n <= std::numeric_limits<int>::max(), name, " has a dimension of ", n, ", more than 32 bits count");
 }
+// A status of a C entry point. It leaves a call as the package's SdtwError; autograd makes a RuntimeError of the same
+// words of one from a backward pass.
+struct StatusError : std::runtime_error {
+    sdtw_status status;
+    const char* where;
+    StatusError(sdtw_status s, const char* w) : std::runtime_error(std::string(w) + ": " + sdtw_status_string(s)), status(s), where(w) {}
+};
 void check_status(sdtw_status s, const char* where)
 {
-    TORCH_CHECK(s == SDTW_OK, where, ": ", sdtw_status_string(s));
+    if (s != SDTW_OK) throw StatusError(s, where);
 }
 void once_only()
 {
@@ -376,6 +386,14 @@ variable_list attention(const Tensor& q_, const Tensor& k_, const Tensor& v_, bo
 
 PYBIND11_MODULE(_binding, m)
 {
+    py::register_local_exception_translator([](std::exception_ptr p) {
+        try {
+            if (p) std::rethrow_exception(p);
+        } catch (const StatusError& e) {
+            const py::object error = py::module_::import("differentiable_series_alignment_gb300._lib").attr("SdtwError");
+            PyErr_SetObject(error.ptr(), error(static_cast<int>(e.status), e.where).ptr());
+        }
+    });
     m.def("layer_norm", &layer_norm);
     m.def("rotary", &rotary);
     m.def("attention", &attention);

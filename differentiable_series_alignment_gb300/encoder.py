@@ -6,7 +6,8 @@
 
 Tensors are fp32, bf16 or fp16 on a CUDA device; every step of the operators runs
 in libsdtw.so's kernels, on the current stream of the tensors' device. Wrong shapes and
-values raise ValueError, wrong types TypeError, tangents of forward-mode differentiation NotImplementedError.
+values raise ValueError, wrong types TypeError, tangents of forward-mode differentiation NotImplementedError,
+and what the library itself refuses (sizes beyond its limits) SdtwError, as every other entry.
 """
 from __future__ import annotations
 

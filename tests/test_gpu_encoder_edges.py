@@ -243,3 +243,14 @@ def test_values_outside_fp32_are_refused_like_other_wrong_values(package):
         with pytest.raises(ValueError):
             package.attention(q, q, q, scale=scale)
     assert torch.isfinite(package.attention(q, q, q, scale=1e-30)).all()
+
+
+def test_what_the_library_refuses_is_the_package_s_own_error(package):
+    """Sizes that only the C entry knows the limits of: the same error as from every other entry, with its status."""
+    x = torch.zeros(1, (1 << 24) + 1, device="cuda")
+    q = torch.zeros(1, 1, 1, 1, device="cuda")
+    rows = q.expand(1, (1 << 27) + 1, 1, 1)
+    for call in (lambda: package.layer_norm(x), lambda: package.attention(q, rows, rows), lambda: package.layer_norm(x.requires_grad_())):
+        with pytest.raises(package.SdtwError) as e:
+            call()
+        assert e.value.code == 8 and "SDTW_ERR_TOO_LARGE" in str(e.value)
