@@ -13,7 +13,9 @@ README ("Usage", "Fused Mode", "Normalization", "Time Series Barycenters"):
 
 Operators of the sequence encoder whose outputs are aligned (encoder.py), differentiable:
     layer_norm(x, weight, bias), rotary(q, k, table=rotary_table(length, dim)),
-    attention(q, k, v, causal=False, window=None, q_lengths=None, k_lengths=None)
+    attention(q, k, v, causal=False, window=None, q_lengths=None, k_lengths=None),
+    group_norm(x, groups, weight, bias, activation=None), gated_recurrence(x, gate, state=None),
+    gated_linear(x, gate_weight, up_weight, activation="silu")
 
 PyTorch supplies device memory and streams only; every step of the method runs
 in libsdtw.so's kernels.
@@ -33,8 +35,11 @@ from ._lib import (CHECKPOINT, EXTENDED, FUSED, OP_BARYCENTER, OP_COST, OP_FWD_B
                    sdtw_workspace_bytes, workspace, host_workspace, sdtw_host_workspace_bytes,
                    sdtw_value_and_grad_host, Attention, attention_problem, sdtw_attention_backward,
                    sdtw_attention_forward, sdtw_attention_workspace_bytes, sdtw_encoder_status,
-                   sdtw_layernorm_backward, sdtw_layernorm_forward, sdtw_layernorm_workspace_bytes, sdtw_rotary)
-from .encoder import attention, layer_norm, rotary, rotary_table
+                   sdtw_layernorm_backward, sdtw_layernorm_forward, sdtw_layernorm_workspace_bytes, sdtw_rotary,
+                   Gated, Recurrence, gated_problem, recurrence_problem, sdtw_gated_backward, sdtw_gated_forward,
+                   sdtw_gated_workspace_bytes, sdtw_groupnorm_backward, sdtw_groupnorm_forward,
+                   sdtw_groupnorm_workspace_bytes, sdtw_recurrence_backward, sdtw_recurrence_forward)
+from .encoder import attention, gated_linear, gated_recurrence, group_norm, layer_norm, rotary, rotary_table
 
 __all__ = [
     "SoftDTW", "soft_dtw_cost", "softdtw_barycenter", "SdtwError", "load", "workspace",
@@ -48,6 +53,9 @@ __all__ = [
     "layer_norm", "rotary", "rotary_table", "attention", "Attention", "attention_problem",
     "sdtw_attention_forward", "sdtw_attention_backward", "sdtw_attention_workspace_bytes", "sdtw_encoder_status",
     "sdtw_layernorm_forward", "sdtw_layernorm_backward", "sdtw_layernorm_workspace_bytes", "sdtw_rotary",
+    "group_norm", "gated_recurrence", "gated_linear", "Recurrence", "recurrence_problem", "Gated", "gated_problem",
+    "sdtw_groupnorm_forward", "sdtw_groupnorm_backward", "sdtw_groupnorm_workspace_bytes", "sdtw_recurrence_forward",
+    "sdtw_recurrence_backward", "sdtw_gated_forward", "sdtw_gated_backward", "sdtw_gated_workspace_bytes",
 ]
 
 

@@ -36,9 +36,14 @@ EXPORTS = ("sdtw_workspace_bytes", "sdtw_distance", "sdtw_forward", "sdtw_backwa
            "sdtw_debug_set_options", "sdtw_debug_set_clusters", "sdtw_debug_exp2_neg",
            "sdtw_layernorm_forward", "sdtw_layernorm_workspace_bytes", "sdtw_layernorm_backward", "sdtw_rotary",
            "sdtw_attention_workspace_bytes", "sdtw_attention_forward", "sdtw_attention_backward",
+           "sdtw_groupnorm_workspace_bytes", "sdtw_groupnorm_forward", "sdtw_groupnorm_backward",
+           "sdtw_recurrence_forward", "sdtw_recurrence_backward",
+           "sdtw_gated_workspace_bytes", "sdtw_gated_forward", "sdtw_gated_backward",
            "sdtw_encoder_status")
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # sdtw_dtype
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "relu": 3, "sigmoid": 4}   # sdtw_activation
+RECURRENCE_STEP = 64   # SDTW_RECURRENCE_STEP
 
 
 class Attention(ctypes.Structure):
@@ -49,6 +54,22 @@ class Attention(ctypes.Structure):
                 ("B", ctypes.c_int), ("N", ctypes.c_int), ("M", ctypes.c_int), ("Hq", ctypes.c_int),
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("window_left", ctypes.c_int),
                 ("window_right", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Recurrence(ctypes.Structure):
+    """sdtw_recurrence of include/sdtw.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("x_stride", ctypes.c_longlong * 2),
+                ("gate_stride", ctypes.c_longlong * 2), ("state", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("N", ctypes.c_int), ("C", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("reverse", ctypes.c_int), ("tied", ctypes.c_int)]
+
+
+class Gated(ctypes.Structure):
+    """sdtw_gated of include/sdtw.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("gate_weight", ctypes.c_void_p), ("up_weight", ctypes.c_void_p),
+                ("gate_bias", ctypes.c_void_p), ("up_bias", ctypes.c_void_p), ("x_stride", ctypes.c_longlong),
+                ("gate_stride", ctypes.c_longlong), ("up_stride", ctypes.c_longlong), ("R", ctypes.c_longlong),
+                ("K", ctypes.c_int), ("F", ctypes.c_int), ("dtype", ctypes.c_int), ("activation", ctypes.c_int)]
 
 
 class SdtwError(RuntimeError):
@@ -78,6 +99,23 @@ def _bind_encoder(lib):
     lib.sdtw_attention_forward.restype = i
     lib.sdtw_attention_backward.argtypes = [at, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.sdtw_attention_backward.restype = i
+    lib.sdtw_groupnorm_workspace_bytes.argtypes = [i] * 6
+    lib.sdtw_groupnorm_workspace_bytes.restype = sz
+    lib.sdtw_groupnorm_forward.argtypes = [vp, vp, vp, vp, i, i, i, i, f, i, i, i, vp, vp, vp, vp, sz, vp]
+    lib.sdtw_groupnorm_forward.restype = i
+    lib.sdtw_groupnorm_backward.argtypes = [vp] * 7 + [i] * 7 + [vp, vp, vp, vp, sz, vp]
+    lib.sdtw_groupnorm_backward.restype = i
+    rp, gp = ctypes.POINTER(Recurrence), ctypes.POINTER(Gated)
+    lib.sdtw_recurrence_forward.argtypes = [rp, vp, vp, vp, vp]
+    lib.sdtw_recurrence_forward.restype = i
+    lib.sdtw_recurrence_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sdtw_recurrence_backward.restype = i
+    lib.sdtw_gated_workspace_bytes.argtypes = [gp, i]
+    lib.sdtw_gated_workspace_bytes.restype = sz
+    lib.sdtw_gated_forward.argtypes = [gp, vp, vp, sz, vp]
+    lib.sdtw_gated_forward.restype = i
+    lib.sdtw_gated_backward.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.sdtw_gated_backward.restype = i
     lib.sdtw_encoder_status.argtypes = [vp]
     lib.sdtw_encoder_status.restype = i
 
@@ -493,6 +531,68 @@ def sdtw_attention_backward(problem: Attention, out, out_rest, lse, dout, dq, dk
     _check(load().sdtw_attention_backward(ctypes.byref(problem), _ptr(out), _ptr(out_rest), _f32(lse, "lse"),
                                           _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
                                           0 if ws is None else ws.numel(), _stream(stream)), "sdtw_attention_backward")
+
+
+def sdtw_groupnorm_workspace_bytes(B, S, G, C, dtype, backward=False) -> int:
+    return int(load().sdtw_groupnorm_workspace_bytes(B, S, G, C, DTYPES[dtype], 1 if backward else 0))
+
+
+def sdtw_groupnorm_forward(x, weight, bias, lengths, groups, eps, activation, y, mean, rstd, ws, stream=None):
+    B, S, C = x.shape
+    w = weight if weight is not None else bias
+    _check(load().sdtw_groupnorm_forward(_ptr(x), _ptr(weight), _ptr(bias), _i32(lengths, "lengths"), B, S, groups, C, float(eps),
+                                         ACTIVATIONS[activation], _dtype(x, "x"), 0 if w is None else _dtype(w, "weight"), _ptr(y),
+                                         _ptr(mean), _ptr(rstd), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
+           "sdtw_groupnorm_forward")
+
+
+def sdtw_groupnorm_backward(dy, x, weight, bias, lengths, mean, rstd, groups, activation, dx, dweight, dbias, ws, stream=None):
+    B, S, C = x.shape
+    w = next((t for t in (weight, bias, dweight, dbias) if t is not None), None)
+    _check(load().sdtw_groupnorm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _i32(lengths, "lengths"), _ptr(mean),
+                                          _ptr(rstd), B, S, groups, C, ACTIVATIONS[activation], _dtype(x, "x"),
+                                          0 if w is None else _dtype(w, "weight"), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(stream)), "sdtw_groupnorm_backward")
+
+
+def recurrence_problem(x, gate, state=None, lengths=None, reverse=False, tied=True) -> Recurrence:
+    """The sdtw_recurrence of these tensors, which the caller keeps alive while it is in use."""
+    B, N, C = x.shape
+    stride = ctypes.c_longlong * 2
+    return Recurrence(x.data_ptr(), gate.data_ptr(), stride(x.stride(0), x.stride(1)), stride(gate.stride(0), gate.stride(1)),
+                      _ptr(state), _i32(lengths, "lengths"), B, N, C, _dtype(x, "x"), int(reverse), int(tied))
+
+
+def sdtw_recurrence_forward(problem: Recurrence, h, last, kept, stream=None):
+    _check(load().sdtw_recurrence_forward(ctypes.byref(problem), _ptr(h), _ptr(last), _ptr(kept), _stream(stream)),
+           "sdtw_recurrence_forward")
+
+
+def sdtw_recurrence_backward(problem: Recurrence, kept, dh, dlast, dx, dgate, dstate, stream=None):
+    _check(load().sdtw_recurrence_backward(ctypes.byref(problem), _ptr(kept), _ptr(dh), _ptr(dlast), _ptr(dx), _ptr(dgate),
+                                           _ptr(dstate), _stream(stream)), "sdtw_recurrence_backward")
+
+
+def gated_problem(x, gate_weight, up_weight, gate_bias=None, up_bias=None, activation="silu") -> Gated:
+    """The sdtw_gated of these tensors (x (R, K)), which the caller keeps alive while it is in use."""
+    return Gated(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), _ptr(gate_bias), _ptr(up_bias), x.stride(0),
+                 gate_weight.stride(0), up_weight.stride(0), x.shape[0], x.shape[1], gate_weight.shape[0], _dtype(x, "x"),
+                 ACTIVATIONS[activation])
+
+
+def sdtw_gated_workspace_bytes(problem: Gated, backward: bool = False) -> int:
+    return int(load().sdtw_gated_workspace_bytes(ctypes.byref(problem), 1 if backward else 0))
+
+
+def sdtw_gated_forward(problem: Gated, h, ws, stream=None):
+    _check(load().sdtw_gated_forward(ctypes.byref(problem), _ptr(h), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
+           "sdtw_gated_forward")
+
+
+def sdtw_gated_backward(problem: Gated, dh, dx, dgate_weight, dup_weight, dgate_bias, dup_bias, ws, stream=None):
+    _check(load().sdtw_gated_backward(ctypes.byref(problem), _ptr(dh), _ptr(dx), _ptr(dgate_weight), _ptr(dup_weight),
+                                      _ptr(dgate_bias), _ptr(dup_bias), _ptr(ws), 0 if ws is None else ws.numel(),
+                                      _stream(stream)), "sdtw_gated_backward")
 
 
 def sdtw_encoder_status(stream=None) -> int:

@@ -1,0 +1,48 @@
+// activation.cuh -- the activations of group norm and of gated linear units, and their derivatives.
+#pragma once
+#include "common.cuh"
+#include "encoder.h"
+
+namespace sdtw {
+
+// 1 / (1 + exp(-z)). EXACT, for results of 32 bits, takes expf: ex2 alone makes the rounding of its argument, up to
+// |z| 2^-24, a relative error of the exponential; 16 bits do not show it.
+template <bool EXACT> __device__ __forceinline__ float sigmoid(float z) {
+    return __fdividef(1.f, 1.f + (EXACT ? expf(-z) : ex2(-1.4426950408889634f * z)));
+}
+
+// act(z), and with SLOPE its derivative.
+template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ float activate(float z, float& slope) {
+    if constexpr (ACT == SDTW_ACT_SILU) {
+        const float s = sigmoid<EXACT>(z);
+        if (SLOPE) slope = fmaf(z * s, 1.f - s, s);
+        return z * s;
+    } else if constexpr (ACT == SDTW_ACT_GELU) {
+        const float c = fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f);
+        if (SLOPE) slope = fmaf(z * 0.39894228040143268f, EXACT ? expf(-0.5f * z * z) : ex2(-0.72134752044448170f * z * z), c);
+        return z * c;
+    } else if constexpr (ACT == SDTW_ACT_RELU) {
+        if (SLOPE) slope = z > 0.f ? 1.f : 0.f;
+        return z < 0.f ? 0.f : z;   // NaN stays
+    } else if constexpr (ACT == SDTW_ACT_SIGMOID) {
+        const float s = sigmoid<EXACT>(z);
+        if (SLOPE) slope = s * (1.f - s);
+        return s;
+    } else {
+        if (SLOPE) slope = 1.f;
+        return z;
+    }
+}
+
+// f(std::integral_constant<int, activation>)
+template <typename F> auto with_activation(int activation, F f) {
+    switch (activation) {
+        case SDTW_ACT_SILU: return f(std::integral_constant<int, SDTW_ACT_SILU>());
+        case SDTW_ACT_GELU: return f(std::integral_constant<int, SDTW_ACT_GELU>());
+        case SDTW_ACT_RELU: return f(std::integral_constant<int, SDTW_ACT_RELU>());
+        case SDTW_ACT_SIGMOID: return f(std::integral_constant<int, SDTW_ACT_SIGMOID>());
+        default: return f(std::integral_constant<int, SDTW_ACT_NONE>());
+    }
+}
+
+}  // namespace sdtw

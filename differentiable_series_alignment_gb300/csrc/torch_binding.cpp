@@ -17,6 +17,7 @@
 #include <stdexcept>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/sdtw.h"
 
@@ -382,6 +383,286 @@ variable_list attention(const Tensor& q_, const Tensor& k_, const Tensor& v_, bo
     return {got[0]};
 }
 
+// ---- group norm
+Tensor group_forward(const Tensor& x, const Tensor& w, const Tensor& b, const Tensor& lengths, int64_t groups, double eps, int64_t activation,
+                     const Tensor& stats)
+{
+    const c10::cuda::CUDAGuard guard(x.device());
+    Tensor y = like(x);
+    if (x.numel() == 0) return y;
+    const int B = static_cast<int>(x.size(0)), C = static_cast<int>(x.size(-1)), S = static_cast<int>(x.numel() / x.size(0) / C);
+    const Tensor& any = w.defined() ? w : b;
+    float* mean = stats.defined() ? stats.data_ptr<float>() : nullptr;
+    const Tensor ws = workspace(sdtw_groupnorm_workspace_bytes(B, S, static_cast<int>(groups), C, dtype_of(x, "x"), 0), x);
+    check_status(sdtw_groupnorm_forward(ptr(x), ptr(w), ptr(b), static_cast<int*>(ptr(lengths)), B, S, static_cast<int>(groups), C,
+                                        static_cast<float>(eps), static_cast<int>(activation), dtype_of(x, "x"),
+                                        any.defined() ? dtype_of(any, "weight") : SDTW_F32, ptr(y), mean,
+                                        mean ? mean + B * groups : nullptr, ptr(ws), bytes(ws), stream()),
+                 "sdtw_groupnorm_forward");
+    return y;
+}
+
+struct GroupNorm : torch::autograd::Function<GroupNorm> {
+    static Tensor forward(AutogradContext* ctx, const Tensor& x, const Maybe& weight, const Maybe& bias, const Maybe& lengths_,
+                          int64_t groups, double eps, int64_t activation)
+    {
+        const Tensor w = value(weight), b = value(bias), lengths = value(lengths_);
+        const Tensor stats = at::empty({2, x.size(0), groups}, x.options().dtype(at::kFloat));
+        Tensor y = group_forward(x, w, b, lengths, groups, eps, activation, stats);
+        ctx->save_for_backward({x, w, b, lengths, stats});
+        ctx->saved_data["groups"] = groups;
+        ctx->saved_data["activation"] = activation;
+        ctx->saved_data["want"] = (wants(x) ? 1 : 0) | (wants(w) ? 2 : 0) | (wants(b) ? 4 : 0);
+        return y;
+    }
+    static variable_list backward(AutogradContext* ctx, variable_list grads)
+    {
+        once_only();
+        const variable_list saved = ctx->get_saved_variables();
+        const Tensor &x = saved[0], &w = saved[1], &b = saved[2], &lengths = saved[3], &stats = saved[4];
+        const int groups = static_cast<int>(ctx->saved_data["groups"].toInt());
+        const int64_t want = ctx->saved_data["want"].toInt();
+        const c10::cuda::CUDAGuard guard(x.device());
+        const bool some = x.numel() != 0;
+        Tensor dx, dw, db;
+        if (want & 1) dx = like(x);
+        if (want & 2) dw = some ? like(w) : at::zeros_like(w);
+        if (want & 4) db = some ? like(b) : at::zeros_like(b);
+        if (some) {
+            const int B = static_cast<int>(x.size(0)), C = static_cast<int>(x.size(-1)), S = static_cast<int>(x.numel() / x.size(0) / C);
+            const Tensor ws = workspace(sdtw_groupnorm_workspace_bytes(B, S, groups, C, dtype_of(x, "x"), 1), x);
+            const Tensor dy = packed(grads[0]);
+            const Tensor& any = w.defined() ? w : b;
+            float* mean = stats.data_ptr<float>();
+            check_status(sdtw_groupnorm_backward(ptr(dy), ptr(x), ptr(w), ptr(b), static_cast<int*>(ptr(lengths)), mean,
+                                                 mean + static_cast<int64_t>(B) * groups, B, S, groups, C,
+                                                 static_cast<int>(ctx->saved_data["activation"].toInt()), dtype_of(x, "x"),
+                                                 any.defined() ? dtype_of(any, "weight") : SDTW_F32, ptr(dx), ptr(dw), ptr(db),
+                                                 ptr(ws), bytes(ws), stream()),
+                         "sdtw_groupnorm_backward");
+        }
+        return {dx, dw, db, Tensor(), Tensor(), Tensor(), Tensor()};
+    }
+};
+
+Tensor group_norm(const Tensor& x_, int64_t groups, const Maybe& weight, const Maybe& bias, double eps, int64_t activation,
+                  const Maybe& lengths_)
+{
+    check_cuda(x_, "x");
+    TORCH_CHECK_VALUE(x_.dim() >= 2 && x_.size(-1) >= 1, "x must be (B, ..., C) with at least one channel");
+    check_sizes(x_, "x");
+    TORCH_CHECK_VALUE(groups >= 1 && x_.size(-1) % groups == 0, "groups must divide the channels, ", x_.size(-1));
+    TORCH_CHECK_VALUE(eps >= 0 && std::isfinite(static_cast<float>(eps)), "eps must be >= 0 and finite in float32");
+    TORCH_CHECK_VALUE(x_.numel() == 0 || x_.numel() / x_.size(0) / x_.size(-1) <= std::numeric_limits<int>::max(),
+                      "x has more positions than 32 bits count");
+    Tensor w = value(weight), b = value(bias);
+    for (int k = 0; k < 2; ++k) {
+        const Tensor& t = k ? b : w;
+        const char* name = k ? "bias" : "weight";
+        if (!t.defined()) continue;
+        check_cuda(t, name);
+        TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == x_.size(-1), name, " must be (", x_.size(-1), ",)");
+        TORCH_CHECK_TYPE(t.scalar_type() == x_.scalar_type() || t.scalar_type() == at::kFloat, name,
+                         " must be float32 or of x's type");
+        TORCH_CHECK_VALUE(t.device() == x_.device(), name, " must be on x's device");
+    }
+    TORCH_CHECK_TYPE(!w.defined() || !b.defined() || w.scalar_type() == b.scalar_type(), "weight and bias must be of one type");
+    const Tensor lengths = lengths_of(lengths_, x_, "lengths");
+    TORCH_CHECK_VALUE(!lengths.defined() || x_.dim() == 3, "lengths needs x of (B, N, C)");
+    const Tensor x = packed(x_);
+    if (w.defined()) w = packed(w);
+    if (b.defined()) b = packed(b);
+    if (recording({x, w, b})) return GroupNorm::apply(x, given(w), given(b), given(lengths), groups, eps, activation);
+    return group_forward(x, w, b, lengths, groups, eps, activation, Tensor());
+}
+
+// ---- gated recurrence
+Tensor with_channels(const Tensor& t) { return t.stride(2) == 1 || t.size(2) == 1 ? t : t.contiguous(); }
+
+sdtw_recurrence recurrence(const Tensor& x, const Tensor& gate, const Tensor& state, const Tensor& lengths, bool reverse, bool tied)
+{
+    sdtw_recurrence a{};
+    a.x = ptr(x), a.gate = ptr(gate), a.state = static_cast<float*>(ptr(state)), a.lengths = static_cast<int*>(ptr(lengths));
+    for (int i = 0; i < 2; ++i) a.x_stride[i] = x.stride(i), a.gate_stride[i] = gate.stride(i);
+    a.B = static_cast<int>(x.size(0)), a.N = static_cast<int>(x.size(1)), a.C = static_cast<int>(x.size(2));
+    a.dtype = dtype_of(x, "x"), a.reverse = reverse, a.tied = tied;
+    return a;
+}
+
+// h, last (want_last) and the states for the backward pass (keep)
+std::array<Tensor, 3> recur(const Tensor& x, const Tensor& gate, const Tensor& state, const Tensor& lengths, bool reverse, bool tied,
+                            bool want_last, bool keep)
+{
+    const c10::cuda::CUDAGuard guard(x.device());
+    const auto f32 = x.options().dtype(at::kFloat);
+    Tensor h = like(x), last, kept;
+    if (want_last) last = at::empty({x.size(0), x.size(2)}, f32);
+    if (x.numel() == 0) {
+        if (want_last) state.defined() ? last.copy_(state) : last.zero_();
+        return {h, last, kept};
+    }
+    if (keep) kept = at::empty({x.size(0), (x.size(1) + SDTW_RECURRENCE_STEP - 1) / SDTW_RECURRENCE_STEP, x.size(2)}, f32);
+    const sdtw_recurrence a = recurrence(x, gate, state, lengths, reverse, tied);
+    check_status(sdtw_recurrence_forward(&a, ptr(h), static_cast<float*>(ptr(last)), static_cast<float*>(ptr(kept)), stream()),
+                 "sdtw_recurrence_forward");
+    return {h, last, kept};
+}
+
+struct Recurrence : torch::autograd::Function<Recurrence> {
+    static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& gate, const Maybe& state_, const Maybe& lengths_,
+                                 bool reverse, bool tied)
+    {
+        const Tensor state = value(state_), lengths = value(lengths_);
+        const auto got = recur(x, gate, state, lengths, reverse, tied, true, true);
+        ctx->save_for_backward({x, gate, state, lengths, got[2]});
+        ctx->saved_data["reverse"] = reverse;
+        ctx->saved_data["tied"] = tied;
+        ctx->saved_data["want"] = (wants(x) ? 1 : 0) | (wants(gate) ? 2 : 0) | (wants(state) ? 4 : 0);
+        ctx->set_materialize_grads(false);   // an output that the loss does not use costs nothing
+        return {got[0], got[1]};
+    }
+    static variable_list backward(AutogradContext* ctx, variable_list grads)
+    {
+        once_only();
+        const variable_list s = ctx->get_saved_variables();
+        const Tensor &x = s[0], &gate = s[1], &state = s[2], &lengths = s[3], &kept = s[4];
+        const int64_t want = ctx->saved_data["want"].toInt();
+        if (!grads[0].defined() && !grads[1].defined()) return variable_list(6);
+        const c10::cuda::CUDAGuard guard(x.device());
+        Tensor dx = like(x), dgate = like(x), dstate;
+        if (want & 4) dstate = like(state);
+        if (x.numel() == 0) {
+            if (want & 4) grads[1].defined() ? dstate.copy_(grads[1]) : dstate.zero_();
+        } else {
+            const sdtw_recurrence a = recurrence(x, gate, state, lengths, ctx->saved_data["reverse"].toBool(), ctx->saved_data["tied"].toBool());
+            const Tensor dh = grads[0].defined() ? packed(grads[0]) : Tensor(), dlast = grads[1].defined() ? packed(grads[1]) : Tensor();
+            check_status(sdtw_recurrence_backward(&a, kept.data_ptr<float>(), ptr(dh), static_cast<float*>(ptr(dlast)), ptr(dx), ptr(dgate),
+                                                  static_cast<float*>(ptr(dstate)), stream()),
+                         "sdtw_recurrence_backward");
+        }
+        return {want & 1 ? dx : Tensor(), want & 2 ? dgate : Tensor(), dstate, Tensor(), Tensor(), Tensor()};
+    }
+};
+
+// (h,) or (h, last)
+variable_list gated_recurrence(const Tensor& x_, const Tensor& gate_, const Maybe& state_, const Maybe& lengths_, bool reverse, bool tied,
+                               bool return_state)
+{
+    check_cuda(x_, "x");
+    check_cuda(gate_, "gate");
+    TORCH_CHECK_VALUE(x_.dim() == 3, "x must be (B, N, C)");
+    check_sizes(x_, "x");
+    TORCH_CHECK_TYPE(gate_.scalar_type() == x_.scalar_type(), "gate must be of x's type");
+    TORCH_CHECK_VALUE(gate_.sizes() == x_.sizes() && gate_.device() == x_.device(), "gate must have x's shape, on x's device");
+    Tensor state = value(state_);
+    if (state.defined()) {
+        TORCH_CHECK_TYPE(state.scalar_type() == at::kFloat, "state must be float32");
+        TORCH_CHECK_VALUE(state.dim() == 2 && state.size(0) == x_.size(0) && state.size(1) == x_.size(2) && state.device() == x_.device(),
+                          "state must be (B, C), on x's device");
+        state = packed(state);
+    }
+    const Tensor lengths = lengths_of(lengths_, x_, "lengths");
+    const Tensor x = with_channels(x_), gate = with_channels(gate_);
+    if (recording({x, gate, state})) {
+        variable_list r = Recurrence::apply(x, gate, given(state), given(lengths), reverse, tied);
+        if (!return_state) r.resize(1);
+        return r;
+    }
+    const auto got = recur(x, gate, state, lengths, reverse, tied, return_state, false);
+    if (return_state) return {got[0], got[1]};
+    return {got[0]};
+}
+
+// ---- gated linear units
+sdtw_gated gated(const Tensor& x, const Tensor& wg, const Tensor& wu, const Tensor& bg, const Tensor& bu, int64_t activation)
+{
+    sdtw_gated a{};
+    a.x = ptr(x), a.gate_weight = ptr(wg), a.up_weight = ptr(wu), a.gate_bias = ptr(bg), a.up_bias = ptr(bu);
+    a.x_stride = x.stride(0), a.gate_stride = wg.stride(0), a.up_stride = wu.stride(0);
+    a.R = x.size(0), a.K = static_cast<int>(x.size(1)), a.F = static_cast<int>(wg.size(0));
+    a.dtype = dtype_of(x, "x"), a.activation = static_cast<int>(activation);
+    return a;
+}
+
+Tensor gate_forward(const Tensor& x, const Tensor& wg, const Tensor& wu, const Tensor& bg, const Tensor& bu, int64_t activation)
+{
+    const c10::cuda::CUDAGuard guard(x.device());
+    Tensor h = at::empty({x.size(0), wg.size(0)}, x.options());
+    if (x.size(0) == 0) return h;
+    const sdtw_gated a = gated(x, wg, wu, bg, bu, activation);
+    const Tensor ws = workspace(sdtw_gated_workspace_bytes(&a, 0), x);
+    check_status(sdtw_gated_forward(&a, ptr(h), ptr(ws), bytes(ws), stream()), "sdtw_gated_forward");
+    return h;
+}
+
+struct GatedLinear : torch::autograd::Function<GatedLinear> {
+    static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& wg, const Tensor& wu, const Maybe& bg_, const Maybe& bu_,
+                          int64_t activation)
+    {
+        const Tensor bg = value(bg_), bu = value(bu_);
+        ctx->save_for_backward({x, wg, wu, bg, bu});
+        ctx->saved_data["activation"] = activation;
+        ctx->saved_data["want"] = (wants(x) ? 1 : 0) | (wants(wg) ? 2 : 0) | (wants(wu) ? 4 : 0) | (wants(bg) ? 8 : 0) | (wants(bu) ? 16 : 0);
+        return gate_forward(x, wg, wu, bg, bu, activation);
+    }
+    static variable_list backward(AutogradContext* ctx, variable_list grads)
+    {
+        once_only();
+        const variable_list s = ctx->get_saved_variables();
+        const Tensor& x = s[0];
+        const int64_t want = ctx->saved_data["want"].toInt();
+        const c10::cuda::CUDAGuard guard(x.device());
+        variable_list d(6);
+        const bool some = x.size(0) != 0;
+        for (int i = 0; i < 5; ++i)
+            if (want >> i & 1) d[i] = some ? like(s[i]) : at::zeros(s[i].sizes(), s[i].options());
+        if (some && want) {
+            const sdtw_gated a = gated(x, s[1], s[2], s[3], s[4], ctx->saved_data["activation"].toInt());
+            const Tensor ws = workspace(sdtw_gated_workspace_bytes(&a, 1), x);
+            const Tensor dh = packed(grads[0]);
+            check_status(sdtw_gated_backward(&a, ptr(dh), ptr(d[0]), ptr(d[1]), ptr(d[2]), ptr(d[3]), ptr(d[4]), ptr(ws), bytes(ws), stream()),
+                         "sdtw_gated_backward");
+        }
+        return d;
+    }
+};
+
+Tensor gated_linear(const Tensor& x_, const Tensor& wg_, const Tensor& wu_, const Maybe& bg_, const Maybe& bu_, int64_t activation)
+{
+    check_cuda(x_, "x");
+    TORCH_CHECK_VALUE(x_.dim() >= 1 && x_.size(-1) >= 1, "x must have a last dimension of at least 1");
+    const int64_t K = x_.size(-1);
+    const Tensor* weights[2] = {&wg_, &wu_};
+    const char* names[4] = {"gate_weight", "up_weight", "gate_bias", "up_bias"};
+    for (int i = 0; i < 2; ++i) {
+        check_cuda(*weights[i], names[i]);
+        TORCH_CHECK_TYPE(weights[i]->scalar_type() == x_.scalar_type(), names[i], " must be of x's type");
+        TORCH_CHECK_VALUE(weights[i]->dim() == 2 && weights[i]->size(1) == K && weights[i]->size(0) == wg_.size(0) && wg_.size(0) >= 1 &&
+                              weights[i]->device() == x_.device(),
+                          names[i], " must be (F, ", K, ") as the other weight, with F >= 1, on x's device");
+        check_sizes(*weights[i], names[i]);
+    }
+    Tensor bg = value(bg_), bu = value(bu_);
+    for (int i = 0; i < 2; ++i) {
+        const Tensor& t = i ? bu : bg;
+        if (!t.defined()) continue;
+        check_cuda(t, names[2 + i]);
+        TORCH_CHECK_TYPE(t.scalar_type() == x_.scalar_type(), names[2 + i], " must be of x's type");
+        TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == wg_.size(0) && t.device() == x_.device(), names[2 + i], " must be (F,), on x's device");
+    }
+    // rows of any stride where features are contiguous; what does not flatten to that is copied
+    auto rows = [](const Tensor& t) { return t.stride(1) == 1 || t.size(1) == 1 ? t : t.contiguous(); };
+    const Tensor x = rows(x_.reshape({x_.numel() / K, K})), wg = rows(wg_), wu = rows(wu_);
+    if (bg.defined()) bg = packed(bg);
+    if (bu.defined()) bu = packed(bu);
+    const Tensor h = recording({x, wg, wu, bg, bu}) ? GatedLinear::apply(x, wg, wu, given(bg), given(bu), activation)
+                                                    : gate_forward(x, wg, wu, bg, bu, activation);
+    if (x_.dim() == 2) return h;
+    std::vector<int64_t> shape(x_.sizes().begin(), x_.sizes().end());
+    shape.back() = wg.size(0);
+    return h.view(shape);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m)
@@ -397,4 +678,7 @@ PYBIND11_MODULE(_binding, m)
     m.def("layer_norm", &layer_norm);
     m.def("rotary", &rotary);
     m.def("attention", &attention);
+    m.def("group_norm", &group_norm);
+    m.def("gated_recurrence", &gated_recurrence);
+    m.def("gated_linear", &gated_linear);
 }

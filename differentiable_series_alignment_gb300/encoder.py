@@ -3,6 +3,9 @@
     layer_norm(x, weight, bias, eps=1e-5)
     rotary_table(length, dim, ...), rotary(q, k, table=..., positions=None, interleaved=False)
     attention(q, k, v, causal=False, window=None, q_lengths=None, k_lengths=None, scale=None)
+    group_norm(x, groups, weight, bias, eps=1e-5, activation=None, lengths=None)
+    gated_recurrence(x, gate, state=None, lengths=None, reverse=False, tied=True)
+    gated_linear(x, gate_weight, up_weight, gate_bias=None, up_bias=None, activation="silu")
 
 Tensors are fp32, bf16 or fp16 on a CUDA device; every step of the operators runs
 in libsdtw.so's kernels, on the current stream of the tensors' device. Wrong shapes and
@@ -102,3 +105,49 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
     differentiable, -inf for rows that see nothing."""
     out = _lib.binding().attention(q, k, v, causal, window, q_lengths, k_lengths, scale, return_lse)
     return tuple(out) if return_lse else out[0]
+
+
+def _activation(name: str | None, known: tuple) -> int:
+    if name not in known:
+        raise ValueError(f"activation must be one of {', '.join(map(repr, known))}")
+    return _lib.ACTIVATIONS[name]
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+               eps: float = 1e-5, activation: str | None = None, lengths: torch.Tensor | None = None) -> torch.Tensor:
+    """activation((x - mean) / sqrt(var + eps) * weight + bias) of x (B, ..., C), channels last, differentiable in x, weight
+    and bias. The C channels are `groups` groups of neighbours; mean and variance are those of a batch element's group
+    over all its positions. groups = C normalises every channel by itself, and x (rows, C) every row by itself.
+
+    activation is None, "silu", "gelu" (with erf) or "relu". weight and bias (C,) are of x's type or fp32, both alike.
+    lengths (B,), bounded by N, makes x (B, N, C) a padded batch: positions from lengths[b] on may hold anything, take no
+    part, and are 0 in the result and in x's gradient. Statistics and sums are fp32."""
+    code = _activation(activation, (None, "silu", "gelu", "relu"))
+    return _lib.binding().group_norm(x, groups, weight, bias, eps, code, lengths)
+
+
+def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor | None = None, *,
+                     lengths: torch.Tensor | None = None, reverse: bool = False, tied: bool = True,
+                     return_state: bool = False):
+    """h (B, N, C) of the linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t, a_t = sigmoid(gate_t), each channel by itself;
+    with tied=False the input enters whole, h_t = a_t h_{t-1} + x_t. Differentiable in x, gate and state.
+
+    x and gate are (B, N, C) of one type, of any strides where channels are contiguous (halves of one projection). state
+    (B, C) fp32 is h before the first position, None: zeros. return_state gives (h, state after the last position), fp32:
+    a series goes on from it, sample by sample (N = 1) or in pieces of any length. lengths (B,), bounded by N, makes a
+    padded batch: positions from lengths[b] on may hold anything, take no part, and are 0 in h and in the gradients.
+    reverse runs from an element's last position to its first. The recurrence is carried in fp32."""
+    out = _lib.binding().gated_recurrence(x, gate, state, lengths, reverse, tied, return_state)
+    return tuple(out) if return_state else out[0]
+
+
+def gated_linear(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Tensor, gate_bias: torch.Tensor | None = None,
+                 up_bias: torch.Tensor | None = None, *, activation: str = "silu") -> torch.Tensor:
+    """activation(x gate_weight^T + gate_bias) * (x up_weight^T + up_bias), (..., F), the first half of a gated
+    feed-forward block, differentiable in all five. x is (..., K), the weights (F, K), the biases (F,) or None, all of one
+    type; activation is "silu", "gelu" (with erf), "relu" or "sigmoid". Weights may be slices of one matrix.
+
+    Neither product is stored: the backward pass computes both again. Sums are fp32; in bf16 and fp16 the
+    gradients of the two products are rounded to the type before the products that consume them."""
+    code = _activation(activation, ("silu", "gelu", "relu", "sigmoid"))
+    return _lib.binding().gated_linear(x, gate_weight, up_weight, gate_bias, up_bias, code)

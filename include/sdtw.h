@@ -401,8 +401,89 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
                                     const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
                                     size_t ws_bytes, void* stream);
 
+/* Activations of sdtw_groupnorm_* (NONE, SILU, GELU, RELU) and sdtw_gated_* (SILU, GELU, RELU, SIGMOID): z,
+ * z / (1 + exp(-z)), z (1 + erf(z / sqrt 2)) / 2, max(z, 0) (derivative 0 at 0), 1 / (1 + exp(-z)). */
+typedef enum { SDTW_ACT_NONE = 0, SDTW_ACT_SILU = 1, SDTW_ACT_GELU = 2, SDTW_ACT_RELU = 3, SDTW_ACT_SIGMOID = 4 } sdtw_activation;
+
+/* Group norm with an activation, channels last: x is (B, S, C) contiguous, its C channels are G groups of C / G
+ * neighbours. Over the S positions and C / G channels of a batch element's group
+ *   mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps), y = act((x - mean) rstd weight + bias).
+ * lengths (DEVICE int array (B,), clamped to [0, S]; NULL: S) makes a padded batch: positions from lengths[b] on may hold
+ * anything, take no part, and are 0 in y and dx. x and y have type `dtype`, weight and bias (C,) type `wdtype`, each
+ * may be NULL (ones, zeros). mean and rstd (B, G) fp32 are kept for the backward pass and may be NULL (both) when there
+ * is none. */
+sdtw_status sdtw_groupnorm_forward(const void* x, const void* weight, const void* bias, const int* lengths, int B, int S,
+                                   int G, int C, float eps, int activation, int dtype, int wdtype, void* y, float* mean,
+                                   float* rstd, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of sdtw_groupnorm_forward (backward == 0) or of sdtw_groupnorm_backward (backward != 0); either may
+ * need none. 0 also when the arguments are invalid. Pure host function but for the SM count of the current device. */
+size_t sdtw_groupnorm_workspace_bytes(int B, int S, int G, int C, int dtype, int backward);
+
+/* Gradients of sdtw_groupnorm_forward from dy (like y), x, weight, bias and the kept mean and rstd. dx (like x),
+ * dweight and dbias ((C,), type `wdtype`) may be NULL individually. */
+sdtw_status sdtw_groupnorm_backward(const void* dy, const void* x, const void* weight, const void* bias, const int* lengths,
+                                    const float* mean, const float* rstd, int B, int S, int G, int C, int activation,
+                                    int dtype, int wdtype, void* dx, void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* A gated linear recurrence along the positions of x and gate (B, N, C), each channel by itself:
+ *   a_t = 1 / (1 + exp(-gate_t)), h_t = a_t h_{t-1} + (1 - a_t) x_t (tied != 0) or a_t h_{t-1} + x_t (tied == 0)
+ * Strides of batch and position in elements; channels are contiguous. state (B, C) fp32 contiguous is h before the first
+ * position, NULL: zeros. lengths (DEVICE int array (B,), clamped to [0, N]; NULL: N) makes a padded batch: positions
+ * from lengths[b] on may hold anything and take no part. reverse != 0 runs from the last of an element's positions to
+ * the first. States are carried in fp32. */
+typedef struct {
+    const void *x, *gate;
+    long long x_stride[2], gate_stride[2];
+    const float* state;
+    const int* lengths;
+    int B, N, C;
+    int dtype;
+    int reverse, tied;
+} sdtw_recurrence;
+
+/* Positions between two of the states that the forward pass keeps for the backward pass. */
+#define SDTW_RECURRENCE_STEP 64
+
+/* h (B, N, C) contiguous, 0 from lengths[b] on; last (B, C) fp32, may be NULL: the state after the last position (the
+ * given state where there is none); kept (B, ceil(N / SDTW_RECURRENCE_STEP), C) fp32, may be NULL: the states before every
+ * SDTW_RECURRENCE_STEP-th position in the order of the recurrence, for sdtw_recurrence_backward. */
+sdtw_status sdtw_recurrence_forward(const sdtw_recurrence* a, void* h, float* last, float* kept, void* stream);
+
+/* Gradients of sdtw_recurrence_forward from its kept states, dh (like h, contiguous; NULL: zeros) and dlast (like
+ * last; NULL: zeros): dx and dgate (B, N, C) contiguous, 0 from lengths[b] on, and dstate (B, C) fp32, NULL if not wanted. */
+sdtw_status sdtw_recurrence_backward(const sdtw_recurrence* a, const float* kept, const void* dh, const float* dlast, void* dx,
+                                     void* dgate, float* dstate, void* stream);
+
+/* A gated linear unit, the first half of a gated feed-forward block: x (R, K), gate_weight and up_weight (F, K) with
+ * contiguous features and any row strides (in elements), gate_bias and up_bias (F,) or NULL, all of type `dtype`,
+ *   h = act(x gate_weight^T + gate_bias) * (x up_weight^T + up_bias)   (R, F).
+ * activation is SILU, GELU, RELU or SIGMOID. */
+typedef struct {
+    const void *x, *gate_weight, *up_weight, *gate_bias, *up_bias;
+    long long x_stride, gate_stride, up_stride;
+    long long R;
+    int K, F;
+    int dtype;
+    int activation;
+} sdtw_gated;
+
+/* Bytes of workspace of sdtw_gated_forward (backward == 0) or of sdtw_gated_backward (backward != 0); either may need
+ * none. 0 also when the arguments are invalid. Pure host function but for the SM count of the current device. */
+size_t sdtw_gated_workspace_bytes(const sdtw_gated* a, int backward);
+
+/* h (R, F) contiguous. */
+sdtw_status sdtw_gated_forward(const sdtw_gated* a, void* h, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients from dh (like h, contiguous): dx (R, K), dgate_weight and dup_weight (F, K), dgate_bias and dup_bias (F,),
+ * all contiguous, of type `dtype`, NULL if not wanted. Both products are computed again from x. In 16-bit types the
+ * gradients of the two products are rounded to the type before the products that consume them. */
+sdtw_status sdtw_gated_backward(const sdtw_gated* a, const void* dh, void* dx, void* dgate_weight, void* dup_weight,
+                                void* dgate_bias, void* dup_bias, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reports (and clears) the current device's status word of the encoder
- * operators: SDTW_OK, or SDTW_ERR_TIMEOUT when an attention kernel gave up a wait. */
+ * operators: SDTW_OK, or SDTW_ERR_TIMEOUT when a kernel on the tensor cores gave up a wait. */
 sdtw_status sdtw_encoder_status(void* stream);
 
 #ifdef __cplusplus
