@@ -431,6 +431,8 @@ EncodeFn encode_fn()
     return fn;
 }
 
+}  // namespace
+
 bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box)
 {
@@ -441,6 +443,8 @@ bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // A dimension of one element is never stepped along: its stride need only be valid.
 cuuint64_t step(long long stride, int size) { return size > 1 ? (cuuint64_t)stride * 2 : 16; }

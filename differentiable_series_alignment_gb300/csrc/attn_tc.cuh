@@ -286,6 +286,9 @@ struct Tiles {
 };
 
 // ---- host: tensor maps
+// A map of 16-bit elements with the 128-byte swizzle; strides in bytes, of all dimensions but the first.
+bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box);
 struct Maps {
     CUtensorMap q, k, v, dout;
 };

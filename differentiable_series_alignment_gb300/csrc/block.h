@@ -37,10 +37,16 @@ struct GatedParams {
     void* h;
     const void* dh;
     void *dx, *dgate_weight, *dup_weight, *dgate_bias, *dup_bias;
-    float* grads;   // backward: (R, 2 F) gradients of the two products
+    unsigned long long wait_ns;   // of a wait on the tensor cores
+    int skip;                     // test hook: the next kernel on the tensor cores loads nothing
 };
 size_t gated_workspace(const GatedParams& p, bool backward, int sms);
+bool gated_is_few(const GatedParams& p);   // a forward pass that stays off the tensor cores
 cudaError_t launch_gated_forward(const GatedParams& p, void* ws, int sms, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaStream_t s);
+cudaError_t gated_fwd_take_status(int* out, cudaStream_t s);
+cudaError_t gated_grad_take_status(int* out, cudaStream_t s);
+cudaError_t gated_dx_take_status(int* out, cudaStream_t s);
+cudaError_t gated_dw_take_status(int* out, cudaStream_t s);
 
 }  // namespace sdtw

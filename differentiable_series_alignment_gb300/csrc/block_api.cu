@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "block.h"
+#include "kernels.h"
 
 using namespace sdtw;
 
@@ -146,7 +147,8 @@ sdtw_status sdtw_gated_forward(const sdtw_gated* a, void* h, void* ws, size_t ws
     if (!h) return SDTW_ERR_ARG;
     if (sdtw_status s = check_ws(ws, ws_bytes, sdtw_gated_workspace_bytes(a, 0))) return s;
     GatedParams p{};
-    p.a = *a, p.h = h;
+    p.a = *a, p.h = h, p.wait_ns = debug_wait_ns();
+    if (!gated_is_few(p)) p.skip = debug_take_skip_publish();
     BLOCK_CUDA(launch_gated_forward(p, ws, device_sms(), static_cast<cudaStream_t>(stream)));
     return SDTW_OK;
 }
@@ -161,6 +163,7 @@ sdtw_status sdtw_gated_backward(const sdtw_gated* a, const void* dh, void* dx, v
     GatedParams p{};
     p.a = *a, p.dh = dh, p.dx = dx, p.dgate_weight = dgate_weight, p.dup_weight = dup_weight;
     p.dgate_bias = dgate_bias, p.dup_bias = dup_bias;
+    p.wait_ns = debug_wait_ns(), p.skip = debug_take_skip_publish();
     BLOCK_CUDA(launch_gated_backward(p, ws, device_sms(), static_cast<cudaStream_t>(stream)));
     return SDTW_OK;
 }

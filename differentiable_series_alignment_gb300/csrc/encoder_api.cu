@@ -1,8 +1,9 @@
 // encoder_api.cu -- the C ABI of the sequence-encoder operators: validation on the host
 // before any launch, workspace carving and launches on the caller's stream.
 #include <cmath>
+#include <initializer_list>
 
-#include "encoder.h"
+#include "block.h"
 #include "kernels.h"
 
 using namespace sdtw;
@@ -281,10 +282,14 @@ sdtw_status sdtw_attention_backward(const sdtw_attention* a, const void* out, co
 
 sdtw_status sdtw_encoder_status(void* stream)
 {
-    int forward = 0, backward = 0;
-    ENC_CUDA(attn_forward_take_status(&forward, static_cast<cudaStream_t>(stream)));
-    ENC_CUDA(attn_backward_take_status(&backward, static_cast<cudaStream_t>(stream)));
-    return forward || backward ? SDTW_ERR_TIMEOUT : SDTW_OK;
+    int any = 0;
+    for (const auto take : {attn_forward_take_status, attn_backward_take_status, gated_fwd_take_status, gated_grad_take_status, gated_dx_take_status,
+                            gated_dw_take_status}) {
+        int one = 0;
+        ENC_CUDA(take(&one, static_cast<cudaStream_t>(stream)));
+        any |= one;
+    }
+    return any ? SDTW_ERR_TIMEOUT : SDTW_OK;
 }
 
 }  // extern "C"

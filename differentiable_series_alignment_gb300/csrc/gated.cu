@@ -3,124 +3,209 @@
 //   g = x Wg^T + bg, u = x Wu^T + bu, h = act(g) u
 //   dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dbg, dbu = column sums
 //
-// Products of any strides by tiles of 64 x 64 on the FP32 pipe.
+// The products run on the tensor cores (gated_tc.cuh). Here are the kernels around them: operands brought into the form that
+// TMA loads, few rows, sums over row tiles and over shares of a sum, and the order of it all.
+#include <algorithm>
 #include <type_traits>
 
-#include "activation.cuh"
-#include "block.h"
+#include "gated_tc.cuh"
 
 namespace sdtw {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+using gtc::kParts;
 
-template <typename T> struct Matrix {   // element (i, k)
-    const T* p;
-    long long si, sk, rows;
-    __device__ __forceinline__ float at(long long i, long long k, long long depth) const {
-        return i < rows && k < depth ? to_f32(p[i * si + k * sk]) : 0.f;
-    }
-};
+// ---- few rows: the weights are read once, straight into the registers of m16n8k16 products. A CTA has 16 features of both
+// weights; its eight warps share the sum, 32 of it at a time. In those a lane holds 8 neighbours of its row for both
+// operands, and takes them as the fragments of two products: which of the sum's terms a position stands for does not
+// matter as long as both operands agree. Tiles of 128 rows on the tensor cores would be empty but for these.
+template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
+template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <> __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-// acc += A(i0 .. i0 + 63, :) B(j0 .. j0 + 63, :)^T; a thread of 256 has 4 x 4 of it
-template <typename A, typename B>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], const Matrix<A>& a, const Matrix<B>& b, long long i0, long long j0, long long depth)
-{
-    __shared__ float as[kDepth][kTile + 1], bs[kDepth][kTile + 1];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (long long k0 = 0; k0 < depth; k0 += kDepth) {
-        __syncthreads();
-        for (int q = threadIdx.x; q < kTile * kDepth; q += 256) {
-            as[q % kDepth][q / kDepth] = a.at(i0 + q / kDepth, k0 + q % kDepth, depth);
-            bs[q % kDepth][q / kDepth] = b.at(j0 + q / kDepth, k0 + q % kDepth, depth);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(as[k][ty * 4 + r], bs[k][tx * 4 + c], acc[r][c]);
+constexpr int kFew = 32;   // rows at the most
+
+__device__ __forceinline__ float activate_by(int activation, bool exact, float z) {
+    float none;
+    switch (activation) {
+        case SDTW_ACT_SILU: return exact ? activate<SDTW_ACT_SILU, true, false>(z, none) : activate<SDTW_ACT_SILU, false, false>(z, none);
+        case SDTW_ACT_GELU: return activate<SDTW_ACT_GELU, true, false>(z, none);
+        case SDTW_ACT_RELU: return activate<SDTW_ACT_RELU, true, false>(z, none);
+        default: return exact ? activate<SDTW_ACT_SIGMOID, true, false>(z, none) : activate<SDTW_ACT_SIGMOID, false, false>(z, none);
     }
 }
 
-// h, or with GRADS the gradients of both products
-template <typename T, int ACT, bool GRADS> __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p)
+template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_kernel(const GatedParams p)
+{
+    constexpr int N = 8 * NT;
+    __shared__ float part[8][2][16][N + 1];
+    const sdtw_gated& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, at = (lane & 3) * 8, f0 = blockIdx.x * 16;
+    const int R = (int)a.R;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load = [&](const void* base, long long stride, int r, int rows, int k) {
+        return r < rows && k < a.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + r * stride + k) : zero;
+    };
+    float acc[2][NT][4] = {};
+#pragma unroll 4
+    for (int k0 = warp * 32; k0 < a.K; k0 += 256) {
+        const int k = k0 + at;
+        uint4 w[2][2], x[NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[0][h] = load(a.gate_weight, a.gate_stride, f0 + row + 8 * h, a.F, k);
+            w[1][h] = load(a.up_weight, a.up_stride, f0 + row + 8 * h, a.F, k);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t] = load(a.x, a.x_stride, t * 8 + row, R, k);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mma16816<T>(acc[m][t], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[t].x, x[t].y);
+                mma16816<T>(acc[m][t], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[t].z, x[t].w);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) part[warp][m][row + 8 * (q >> 1)][t * 8 + (lane & 3) * 2 + (q & 1)] = acc[m][t][q];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * N; i += 256) {
+        const int f = f0 + i % 16, r = i / 16;
+        if (f >= a.F || r >= R) continue;
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) g += part[w][0][i % 16][r], u += part[w][1][i % 16][r];
+        if (a.gate_bias) g += to_f32(static_cast<const T*>(a.gate_bias)[f]);
+        if (a.up_bias) u += to_f32(static_cast<const T*>(a.up_bias)[f]);
+        static_cast<T*>(p.h)[(long long)r * a.F + f] = from_f32<T>(activate_by(a.activation, false, g) * u);
+    }
+}
+
+// Few rows of fp32, or of any stride and address: a warp a feature, eight rows at a time, element by element.
+template <typename T> __global__ void __launch_bounds__(256) gated_dot_kernel(const GatedParams p)
 {
     const sdtw_gated& a = p.a;
-    const long long i0 = (long long)blockIdx.x * kTile, j0 = (long long)blockIdx.y * kTile;
-    const Matrix<T> x{static_cast<const T*>(a.x), a.x_stride, 1, a.R}, wg{static_cast<const T*>(a.gate_weight), a.gate_stride, 1, a.F},
-        wu{static_cast<const T*>(a.up_weight), a.up_stride, 1, a.F};
-    float g[4][4] = {}, u[4][4] = {};
-    tile_product(g, x, wg, i0, j0, a.K);
-    tile_product(u, x, wu, i0, j0, a.K);
-    for (int r = 0; r < 4; ++r)
-        for (int c = 0; c < 4; ++c) {
-            const long long i = i0 + threadIdx.x / 16 * 4 + r, j = j0 + threadIdx.x % 16 * 4 + c;
-            if (i >= a.R || j >= a.F) continue;
-            const float gv = g[r][c] + (a.gate_bias ? to_f32(static_cast<const T*>(a.gate_bias)[j]) : 0.f);
-            const float uv = u[r][c] + (a.up_bias ? to_f32(static_cast<const T*>(a.up_bias)[j]) : 0.f);
-            float slope;
-            const float v = activate<ACT, sizeof(T) == 4, GRADS>(gv, slope);
-            if (GRADS) {
-                const float d = to_f32(static_cast<const T*>(p.dh)[i * a.F + j]);
-                p.grads[i * 2 * a.F + j] = d * uv * slope;
-                p.grads[i * 2 * a.F + a.F + j] = d * v;
-            } else {
-                static_cast<T*>(p.h)[i * a.F + j] = from_f32<T>(v * uv);
+    const int lane = threadIdx.x & 31, f = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (f >= a.F) return;
+    const T* wg = static_cast<const T*>(a.gate_weight) + f * a.gate_stride;
+    const T* wu = static_cast<const T*>(a.up_weight) + f * a.up_stride;
+    const float bg = a.gate_bias ? to_f32(static_cast<const T*>(a.gate_bias)[f]) : 0.f;
+    const float bu = a.up_bias ? to_f32(static_cast<const T*>(a.up_bias)[f]) : 0.f;
+    for (int r0 = 0; r0 < a.R; r0 += 8) {
+        const T* x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = static_cast<const T*>(a.x) + min((long long)r0 + r, a.R - 1) * a.x_stride;
+        float g[8] = {}, u[8] = {};
+#pragma unroll 4
+        for (int k = lane; k < a.K; k += 32) {
+            const float vg = to_f32(wg[k]), vu = to_f32(wu[k]);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float xv = to_f32(x[r][k]);
+                g[r] = fmaf(vg, xv, g[r]);
+                u[r] = fmaf(vu, xv, u[r]);
             }
         }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                g[r] += __shfl_xor_sync(0xffffffffu, g[r], o);
+                u[r] += __shfl_xor_sync(0xffffffffu, u[r], o);
+            }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (lane == r && r0 + r < a.R)
+                static_cast<T*>(p.h)[(r0 + r) * (long long)a.F + f] = from_f32<T>(activate_by(a.activation, sizeof(T) == 4, g[r] + bg) * (u[r] + bu));
+    }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) gated_dx_kernel(const GatedParams p)
+// ---- operands that TMA cannot load as they are: rows copied to a pitch of whole 16 bytes, fp32 as its three bf16 parts
+struct PackJob {
+    const void* from[3];
+    uint16_t* to[3];
+    long long stride[3], rows[3];
+    int first[4];    // CTAs of a job; a CTA has 8 rows
+    int cols, pitch;
+};
+template <typename T> __global__ void __launch_bounds__(256) gated_pack_kernel(const PackJob j)
 {
-    const sdtw_gated& a = p.a;
-    const long long i0 = (long long)blockIdx.x * kTile, j0 = (long long)blockIdx.y * kTile;
-    const Matrix<float> dg{p.grads, 2ll * a.F, 1, a.R}, du{p.grads + a.F, 2ll * a.F, 1, a.R};
-    const Matrix<T> wg{static_cast<const T*>(a.gate_weight), 1, a.gate_stride, a.K}, wu{static_cast<const T*>(a.up_weight), 1, a.up_stride, a.K};
-    float acc[4][4] = {};
-    tile_product(acc, dg, wg, i0, j0, a.F);
-    tile_product(acc, du, wu, i0, j0, a.F);
-    for (int r = 0; r < 4; ++r)
-        for (int c = 0; c < 4; ++c) {
-            const long long i = i0 + threadIdx.x / 16 * 4 + r, j = j0 + threadIdx.x % 16 * 4 + c;
-            if (i < a.R && j < a.K) static_cast<T*>(p.dx)[i * a.K + j] = from_f32<T>(acc[r][c]);
+    using O = typename gtc::Operand<T>::type;
+    int w = 0;
+    while (w < 2 && (int)blockIdx.x >= j.first[w + 1]) ++w;
+    const long long r = (long long)(blockIdx.x - j.first[w]) * 8 + (threadIdx.x >> 5);
+    if (r >= j.rows[w]) return;
+    const T* from = static_cast<const T*>(j.from[w]) + r * j.stride[w];
+    const long long part = j.rows[w] * j.pitch;
+    O* to = reinterpret_cast<O*>(j.to[w]) + r * j.pitch;
+    for (int c = (threadIdx.x & 31) * 2; c < j.cols; c += 64) {   // the pitch is even
+        float x = to_f32(from[c]), y = c + 1 < j.cols ? to_f32(from[c + 1]) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kParts<T>; ++k) {
+            const uint32_t v = pack2<O>(x, y);
+            *reinterpret_cast<uint32_t*>(to + k * part + c) = v;
+            const O* e = reinterpret_cast<const O*>(&v);
+            x -= to_f32(e[0]), y -= to_f32(e[1]);
         }
+    }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) gated_dw_kernel(const GatedParams p)
+// ---- fp16: dg and du are kept times a power of two that brings the largest |dh| to [1/4, 1/2), so that small upstream
+// gradients do not end among fp16's subnormal numbers. The maximum of bit patterns does not depend on their order.
+__global__ void __launch_bounds__(256) gated_top_kernel(const __half* dh, long long n, unsigned* top)
 {
-    const sdtw_gated& a = p.a;
-    void* out = blockIdx.z ? p.dup_weight : p.dgate_weight;
-    if (!out) return;
-    const long long i0 = (long long)blockIdx.x * kTile, j0 = (long long)blockIdx.y * kTile;
-    const Matrix<float> d{p.grads + blockIdx.z * a.F, 1, 2ll * a.F, a.F};
-    const Matrix<T> x{static_cast<const T*>(a.x), 1, a.x_stride, a.K};
-    float acc[4][4] = {};
-    tile_product(acc, d, x, i0, j0, a.R);
-    for (int r = 0; r < 4; ++r)
-        for (int c = 0; c < 4; ++c) {
-            const long long i = i0 + threadIdx.x / 16 * 4 + r, j = j0 + threadIdx.x % 16 * 4 + c;
-            if (i < a.F && j < a.K) static_cast<T*>(out)[i * a.K + j] = from_f32<T>(acc[r][c]);
+    unsigned m = 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
+        m = max(m, (unsigned)(__half_as_ushort(dh[i]) & 0x7fff));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(top, m);
+}
+__global__ void gated_scale_kernel(const unsigned* top, float* scale)
+{
+    const float m = __half2float(__ushort_as_half((unsigned short)*top));
+    int e = 0;
+    if (m > 0.f && m < INFINITY) frexpf(m, &e);   // m = f 2^e, 1/2 <= f < 1
+    scale[0] = m > 0.f && m < INFINITY ? exp2f((float)(-1 - e)) : 1.f;
+    scale[1] = 1.f / scale[0];
+}
+
+// ---- column sums of row tiles, and shares of a sum, added in a fixed order
+template <typename T> __global__ void __launch_bounds__(1024) gated_bias_kernel(const float* sums, long long n, int F, T* dgate, T* dup)
+{
+    __shared__ float part[32][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+    float s[4] = {};
+    if (c < 2 * F)
+        for (long long t = lane; t < n; t += 128) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (t + 32 * q < n) s[q] += sums[(t + 32 * q) * 2 * F + c];
         }
-}
-
-template <typename T> __global__ void __launch_bounds__(256) gated_db_kernel(const GatedParams p)
-{
-    __shared__ float part[8][32];
-    const sdtw_gated& a = p.a;
-    void* out = blockIdx.y ? p.dup_bias : p.dgate_bias;
-    if (!out) return;
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32;
-    float s = 0.f;
-    if (c < a.F)
-        for (long long i = lane; i < a.R; i += 8) s += p.grads[i * 2 * a.F + blockIdx.y * a.F + c];
-    part[lane][threadIdx.x % 32] = s;
+    part[lane][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
-    if (lane == 0 && c < a.F) {
-        s = 0.f;
-        for (int w = 0; w < 8; ++w) s += part[w][threadIdx.x];
-        static_cast<T*>(out)[c] = from_f32<T>(s);
+    float v = part[threadIdx.x & 31][lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int col = blockIdx.x * 32 + lane;
+    T* dst = col < F ? dgate : dup;
+    if ((threadIdx.x & 31) == 0 && col < 2 * F && dst) dst[col < F ? col : col - F] = from_f32<T>(v);
+}
+template <typename T> __global__ void __launch_bounds__(256) gated_join_kernel(const float* shares, int splits, long long n, int sets, T* out0, T* out1)
+{
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n * sets; i += (long long)gridDim.x * 256) {
+        float s = 0.f;
+        for (int k = 0; k < splits; ++k) s += shares[k * n * sets + i];
+        (i < n ? out0 : out1)[i < n ? i : i - n] = from_f32<T>(s);
     }
 }
 
@@ -129,37 +214,227 @@ template <typename F> cudaError_t with_type(int dtype, F f) {
     if (dtype == SDTW_BF16) return f(__nv_bfloat16());
     return f(__half());
 }
-unsigned tiles(long long n) { return (unsigned)((n + kTile - 1) / kTile); }
 
-}  // namespace
+size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+bool loadable(const void* p, long long stride, long long rows, int dtype) {
+    return dtype != SDTW_F32 && aligned16(p) && (rows == 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 38)));
+}
 
-size_t gated_workspace(const GatedParams& p, bool backward, int) { return backward ? sizeof(float) * 2 * p.a.R * p.a.F : 0; }
+// A 16-bit operand: (parts, rows, cols) of a pitch.
+struct Image {
+    const void* p;
+    long long pitch, rows;
+    int cols, parts;
+    bool map(CUtensorMap* m, int dtype, int box_cols, int box_rows) const {
+        const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+        const long long row = rows > 1 ? pitch * 2 : 16;
+        const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)(parts > 1 ? pitch * 2 * rows : 16)};
+        const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+        return atc::encode(m, dtype == SDTW_F32 ? SDTW_BF16 : dtype, 3, p, dims, strides, box);
+    }
+};
 
-cudaError_t launch_gated_forward(const GatedParams& p, void*, int, cudaStream_t s)
+struct Plan {
+    Image x, w[2], grads;
+    PackJob pack;
+    int pack_ctas = 0;
+    float *sums = nullptr, *shares = nullptr, *scale = nullptr;
+    int dw_nb = 256, dw_splits = 1;
+    size_t bytes = 0;
+};
+
+int tiles_of(long long n, int tile) { return (int)((n + tile - 1) / tile); }
+
+// Columns of an accumulator: as many as there are results for, fewer where wide tiles would leave SMs without one.
+int pick_nb(long long rows, long long cols, long long others, int sms, bool pair)
 {
+    for (int nb = 256; nb > 64; nb /= 2) {
+        const int width = pair ? nb / 2 : nb;
+        if (cols > width / 2 && (long long)tiles_of(rows, 128) * tiles_of(cols, width) * others >= sms) return nb;
+    }
+    return 64;
+}
+
+// Shares of the weights' sum over the rows: tiles that alone would leave SMs idle, or many of them in the last round, share
+// theirs. A block of the sum takes `block` us, a tile 1.5 besides; shares go through memory twice, at 4 TB/s.
+int pick_splits(long long tiles, long long blocks, int nb, double result_bytes, int sms)
+{
+    const double block = 0.34 * nb / 256;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 64 && s <= blocks; ++s) {
+        const double rounds = (double)((tiles * s + sms - 1) / sms);
+        const double cost = rounds * (1.5 + block * (double)((blocks + s - 1) / s)) + (s == 1 ? 0. : 4. + 2e-6 * s * result_bytes / 4.);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+
+Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
+{
+    const sdtw_gated& a = p.a;
+    Plan plan;
+    char* base = static_cast<char*>(ws);
+    auto carve = [&](size_t n) {
+        char* at = base + plan.bytes;
+        plan.bytes += align_up(n);
+        return at;
+    };
+    const int parts = a.dtype == SDTW_F32 ? 3 : 1;
+    PackJob& j = plan.pack;
+    j = PackJob{};
+    j.cols = a.K, j.pitch = (a.K + 7) / 8 * 8;
+    int jobs = 0;
+    auto operand = [&](const void* from, long long stride, long long rows) {
+        if (loadable(from, stride, rows, a.dtype)) return Image{from, stride, rows, a.K, 1};
+        uint16_t* to = reinterpret_cast<uint16_t*>(carve((size_t)parts * rows * j.pitch * 2));
+        j.from[jobs] = from, j.to[jobs] = to, j.stride[jobs] = stride, j.rows[jobs] = rows;
+        j.first[jobs] = plan.pack_ctas;
+        plan.pack_ctas += (int)((rows + 7) / 8);
+        for (int k = ++jobs; k < 4; ++k) j.first[k] = plan.pack_ctas;
+        return Image{to, j.pitch, rows, a.K, parts};
+    };
+    plan.x = operand(a.x, a.x_stride, a.R);
+    plan.w[0] = operand(a.gate_weight, a.gate_stride, a.F);
+    plan.w[1] = operand(a.up_weight, a.up_stride, a.F);
+    if (!backward) return plan;
+    const long long pitch = (a.F + 7) / 8 * 8;
+    plan.grads = Image{carve((size_t)2 * parts * a.R * pitch * 2), pitch, a.R, a.F, 2 * parts};
+    plan.sums = reinterpret_cast<float*>(carve((size_t)4 * tiles_of(a.R, 128) * 2 * a.F * sizeof(float)));
+    plan.scale = reinterpret_cast<float*>(carve(256));
+    plan.dw_nb = pick_nb(a.F, a.K, 1 << 20, sms, false);
+    plan.dw_splits = pick_splits(2ll * tiles_of(a.F, 128) * tiles_of(a.K, plan.dw_nb), (parts == 3 ? 6ll : 1ll) * tiles_of(a.R, 64), plan.dw_nb,
+                                 8. * a.F * a.K, sms);
+    if (plan.dw_splits > 1) plan.shares = reinterpret_cast<float*>(carve((size_t)plan.dw_splits * 2 * a.F * a.K * sizeof(float)));
+    return plan;
+}
+
+// The pieces of a sum: pairs of parts, smallest products first.
+constexpr unsigned char kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+void set_segs(gtc::Params& g, int parts, bool both)
+{
+    g.segs = 0;
+    for (int k = parts == 3 ? 0 : 5; k < 6; ++k)
+        for (int m = 0; m < (both ? 2 : 1); ++m) g.seg[g.segs++] = gtc::Seg{(unsigned char)(kPairs[k][0] + m * parts), (unsigned char)m, kPairs[k][1]};
+}
+
+cudaError_t pack_operands(const GatedParams& p, const Plan& plan, cudaStream_t s)
+{
+    if (!plan.pack_ctas) return cudaSuccess;
     return with_type(p.a.dtype, [&](auto t) {
-        return with_activation(p.a.activation, [&](auto act) {
-            gated_kernel<decltype(t), act(), false><<<dim3(tiles(p.a.R), tiles(p.a.F)), 256, 0, s>>>(p);
-            return cudaGetLastError();
-        });
+        gated_pack_kernel<decltype(t)><<<plan.pack_ctas, 256, 0, s>>>(plan.pack);
+        return cudaGetLastError();
     });
 }
 
-cudaError_t launch_gated_backward(const GatedParams& p0, void* ws, int, cudaStream_t s)
+// Both products, side by side.
+cudaError_t products(const GatedParams& p, const Plan& plan, bool grads, bool want_sums, int sms, cudaStream_t s)
 {
-    GatedParams p = p0;
-    p.grads = static_cast<float*>(ws);
-    return with_type(p.a.dtype, [&](auto t) {
-        using T = decltype(t);
-        with_activation(p.a.activation, [&](auto act) {
-            gated_kernel<T, act(), true><<<dim3(tiles(p.a.R), tiles(p.a.F)), 256, 0, s>>>(p);
-            return cudaSuccess;
+    const sdtw_gated& a = p.a;
+    gtc::Params g{};
+    const int nb = pick_nb(a.R, a.F, 1, sms, true), width = nb / 2;
+    if (!plan.x.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, width) || !plan.w[1].map(&g.b[1], a.dtype, 64, width))
+        return cudaErrorInvalidValue;
+    set_segs(g, plan.x.parts, false);
+    g.blocks = tiles_of(a.K, 64);
+    g.tiles_m = tiles_of(a.R, 128), g.tiles_n = tiles_of(a.F, width), g.sets = g.splits = 1;
+    g.M = a.R, g.N = g.F = a.F, g.activation = a.activation;
+    g.out[0] = p.h, g.bias[0] = a.gate_bias, g.bias[1] = a.up_bias, g.dh = p.dh;
+    g.grads = static_cast<uint16_t*>(const_cast<void*>(plan.grads.p)), g.ld = plan.grads.pitch;
+    g.sums = want_sums ? plan.sums : nullptr;
+    g.scale = grads && a.dtype == SDTW_F16 ? plan.scale : nullptr;
+    g.wait_ns = p.wait_ns, g.skip = p.skip;
+    return grads ? gtc::run_grad(g, a.dtype, nb, sms, s) : gtc::run_fwd(g, a.dtype, nb, sms, s);
+}
+
+}  // namespace
+
+bool gated_is_few(const GatedParams& p) { return p.a.R <= kFew; }
+
+size_t gated_workspace(const GatedParams& p, bool backward, int sms)
+{
+    return !backward && gated_is_few(p) ? 0 : make_plan(p, nullptr, backward, sms).bytes;
+}
+
+cudaError_t launch_gated_forward(const GatedParams& p, void* ws, int sms, cudaStream_t s)
+{
+    const sdtw_gated& a = p.a;
+    if (gated_is_few(p))
+        return with_type(a.dtype, [&](auto t) {
+            using T = decltype(t);
+            if constexpr (sizeof(T) == 2)
+                if (a.K % 8 == 0 && loadable(a.x, a.x_stride, a.R, a.dtype) && loadable(a.gate_weight, a.gate_stride, a.F, a.dtype) &&
+                    loadable(a.up_weight, a.up_stride, a.F, a.dtype)) {
+                    const unsigned grid = (unsigned)tiles_of(a.F, 16);
+                    if (a.R <= 8) gated_few_kernel<T, 1><<<grid, 256, 0, s>>>(p);
+                    else if (a.R <= 16) gated_few_kernel<T, 2><<<grid, 256, 0, s>>>(p);
+                    else gated_few_kernel<T, 4><<<grid, 256, 0, s>>>(p);
+                    return cudaGetLastError();
+                }
+            gated_dot_kernel<T><<<tiles_of(a.F, 8), 256, 0, s>>>(p);
+            return cudaGetLastError();
         });
-        if (p.dx) gated_dx_kernel<T><<<dim3(tiles(p.a.R), tiles(p.a.K)), 256, 0, s>>>(p);
-        if (p.dgate_weight || p.dup_weight) gated_dw_kernel<T><<<dim3(tiles(p.a.F), tiles(p.a.K), 2), 256, 0, s>>>(p);
-        if (p.dgate_bias || p.dup_bias) gated_db_kernel<T><<<dim3((p.a.F + 31) / 32, 2), 256, 0, s>>>(p);
-        return cudaGetLastError();
-    });
+    const Plan plan = make_plan(p, ws, false, sms);
+    if (const cudaError_t e = pack_operands(p, plan, s); e != cudaSuccess) return e;
+    return products(p, plan, false, false, sms, s);
+}
+
+cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaStream_t s)
+{
+    const sdtw_gated& a = p.a;
+    const Plan plan = make_plan(p, ws, true, sms);
+    const int parts = plan.x.parts;
+    cudaError_t e = pack_operands(p, plan, s);
+    if (e != cudaSuccess) return e;
+    if (a.dtype == SDTW_F16) {
+        unsigned* top = reinterpret_cast<unsigned*>(plan.scale + 2);
+        if ((e = cudaMemsetAsync(top, 0, sizeof(unsigned), s)) != cudaSuccess) return e;
+        gated_top_kernel<<<(unsigned)std::min(a.R * a.F / 2048 + 1, (long long)sms * 8), 256, 0, s>>>(static_cast<const __half*>(p.dh), a.R * a.F, top);
+        gated_scale_kernel<<<1, 1, 0, s>>>(top, plan.scale);
+    }
+    const bool biases = p.dgate_bias || p.dup_bias;
+    if ((e = products(p, plan, true, biases, sms, s)) != cudaSuccess) return e;
+    gtc::Params g{};
+    g.scale = a.dtype == SDTW_F16 ? plan.scale : nullptr;
+    g.wait_ns = p.wait_ns;
+    if (p.dx) {
+        const int nb = pick_nb(a.R, a.K, 1, sms, false);
+        if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, 64) || !plan.w[1].map(&g.b[1], a.dtype, 64, 64))
+            return cudaErrorInvalidValue;
+        set_segs(g, parts, true);
+        g.blocks = tiles_of(a.F, 64);
+        g.tiles_m = tiles_of(a.R, 128), g.tiles_n = tiles_of(a.K, nb), g.sets = g.splits = 1, g.set0 = 0;
+        g.M = a.R, g.N = a.K, g.out[0] = p.dx;
+        if ((e = gtc::run_dx(g, a.dtype, nb, sms, s)) != cudaSuccess) return e;
+    }
+    if (p.dgate_weight || p.dup_weight) {
+        if (!plan.grads.map(&g.a, a.dtype, 64, 64) || !plan.x.map(&g.b[0], a.dtype, 64, 64)) return cudaErrorInvalidValue;
+        g.b[1] = g.b[0];
+        set_segs(g, parts, false);
+        g.blocks = tiles_of(a.R, 64);
+        g.tiles_m = tiles_of(a.F, 128), g.tiles_n = tiles_of(a.K, plan.dw_nb);
+        g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1, g.splits = plan.dw_splits;
+        g.M = a.F, g.N = a.K, g.out[0] = p.dgate_weight, g.out[1] = p.dup_weight, g.shares = plan.shares;
+        if ((e = gtc::run_dw(g, a.dtype, plan.dw_nb, sms, s)) != cudaSuccess) return e;
+        if (g.splits > 1) {
+            const long long n = (long long)a.F * a.K;
+            e = with_type(a.dtype, [&](auto t) {
+                using T = decltype(t);
+                gated_join_kernel<T><<<(unsigned)std::min(n * g.sets / 256 + 1, (long long)sms * 8), 256, 0, s>>>(
+                    plan.shares, g.splits, n, g.sets, static_cast<T*>(g.out[g.set0]), static_cast<T*>(g.out[1]));
+                return cudaGetLastError();
+            });
+            if (e != cudaSuccess) return e;
+        }
+    }
+    if (biases)
+        e = with_type(a.dtype, [&](auto t) {
+            using T = decltype(t);
+            gated_bias_kernel<T><<<(2 * a.F + 31) / 32, 1024, 0, s>>>(plan.sums, tiles_of(a.R, 32), a.F, static_cast<T*>(p.dgate_bias),
+                                                                     static_cast<T*>(p.dup_bias));
+            return cudaGetLastError();
+        });
+    return e;
 }
 
 }  // namespace sdtw

@@ -1,0 +1,488 @@
+// gated_tc.cuh -- the products of gated linear units on the tensor cores (tcgen05), one kernel for all of them:
+//
+//   FWD   h = act(x Wg^T + bg) * (x Wu^T + bu)       rows of x by features f, both products side by side in one tile
+//   GRAD  the same two products again, and from them and dh: dg and du, rounded to the operands' type
+//   DX    dx = dg Wg + du Wu                          one sum over the features f of both
+//   DW    dWg = dg^T x, dWu = du^T x                  sums over the rows
+//
+// Operands are 16 bits. They come by TMA in blocks of 64 along the sum, 128 bytes a row with the 128-byte swizzle; what
+// a tensor map leaves out (rows, features, the tail of the sum) arrives as zeros. x, dg and W lie along their rows, so
+// that a sum over features has K-major operands and a sum over rows MN-major ones: no operand is transposed in memory.
+// fp32 operands are split into three bf16 parts, v = v0 + v1 + v2 to 24 bits, and a product is the sum of the six part products
+// above 2^-24 of it, (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first, as one longer sum.
+//
+// A persistent CTA: a loading warp, an issuing warp, and eight warps that turn a finished accumulator into results while
+// the next one is summed (two accumulators in tensor memory).
+#pragma once
+#include "activation.cuh"
+#include "attn_tc.cuh"
+#include "block.h"
+
+namespace sdtw {
+namespace gtc {
+
+using namespace atc;
+
+enum Kind { FWD, GRAD, DX, DW };
+
+constexpr int kRows = 128, kBlock = 64;               // rows of a tile; length of a block of the sum
+constexpr uint32_t kABytes = kRows * kBlock * 2;
+
+// One piece of the sum: part of A, map and part of B.
+struct Seg {
+    unsigned char a, map, b;
+};
+
+struct alignas(64) Params {
+    CUtensorMap a, b[2];
+    Seg seg[12];
+    int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks
+    int tiles_m, tiles_n, set0, sets, splits, tiles;   // sets: DW's weights, from set0 on; splits: shares of the sum, none empty
+    long long M;                                       // rows and columns of the result
+    int N, F, activation;
+    void* out[2];                                      // FWD h; DX dx; DW both weights' gradients
+    const void *bias[2], *dh;
+    // GRAD: dg and du, rounded, as parts 0 .. parts - 1 and parts .. 2 parts - 1 of (2 parts, M, ld)
+    uint16_t* grads;
+    long long ld;
+    float* sums;                                       // GRAD, with biases: [4 tiles_m][2 F] column sums of 32 rows
+    float* shares;                                     // DW with splits: [splits][sets][M][N]
+    const float* scale;                                // fp16: what dg and du are multiplied by, and its inverse
+    unsigned long long wait_ns;
+    int skip;                                          // test hook: nothing is loaded
+};
+
+// the operands' type
+template <typename T> struct Operand { using type = T; };
+template <> struct Operand<float> { using type = __nv_bfloat16; };
+template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+
+template <int NB> struct Shape {
+    static constexpr uint32_t b_bytes = NB * kBlock * 2, stage = kABytes + b_bytes;
+    static constexpr uint32_t area = 4096;             // of shared memory, a warp's own
+    static constexpr int stages = NB == 256 ? 4 : NB == 128 ? 6 : 7;
+    static constexpr uint32_t smem = stages * stage + 8 * area;
+    static constexpr int columns = 2 * NB < 32 ? 32 : 2 * NB;
+};
+
+constexpr int kLoad = 8, kIssue = 9, kThreadsG = 320;
+
+static __device__ int g_status;   // of this file's kernels
+
+__device__ __forceinline__ bool aligned16_dev(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// MN-major blocks of 64 rows: groups of 64 elements 8 KB apart
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((kBlock * 128) >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+template <typename T> __device__ __forceinline__ uint32_t idesc2(int M, int N, bool a_mn, bool b_mn) {
+    return idesc<T>(M, N, b_mn) | ((a_mn ? 1u : 0u) << 15);
+}
+
+// A tile's place. Tiles of a column follow one another in groups of 16 rows of tiles, so that those in work at a time
+// share their operands in the cache.
+struct Tile {
+    int m, n, set, split, first, last;   // blocks [first, last) of the sum
+    __device__ __forceinline__ Tile(const Params& p, int t) {
+        const int per = p.tiles_m * p.tiles_n;
+        split = t / (per * p.sets);
+        t %= per * p.sets;
+        set = p.set0 + t / per;
+        t %= per;
+        constexpr int G = 16;
+        const int group = t / (G * p.tiles_n), rows = min(G, p.tiles_m - group * G), in = t - group * G * p.tiles_n;
+        m = group * G + in % rows;
+        n = in / rows;
+        const int total = p.segs * p.blocks;
+        first = (int)((long long)total * split / p.splits);
+        last = (int)((long long)total * (split + 1) / p.splits);
+    }
+};
+
+// ---- 32 rows by 32 columns between a warp's registers (a lane a row) and memory, through its own shared memory, so that
+// neighbouring lanes read and write neighbouring addresses
+template <typename O> __device__ __forceinline__ uint32_t chunk_at(uint32_t area, int row, int piece) {
+    if constexpr (sizeof(O) == 4) return area + row * 128 + ((piece ^ (row & 7)) << 4);
+    else return area + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+template <typename O> __device__ __forceinline__ uint32_t element_at(uint32_t area, int row, int c) {
+    constexpr int E = 16 / sizeof(O);
+    return chunk_at<O>(area, row, c / E) + (c % E) * sizeof(O);
+}
+template <typename O> __device__ __forceinline__ void words_of(const float* v, uint32_t (&w)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(O) == 4) w[k] = __float_as_uint(v[k]);
+        else w[k] = pack2<O>(v[2 * k], v[2 * k + 1]);
+    }
+}
+// rows and cols: how many of either there are; vec: 16-byte accesses are aligned
+template <typename O>
+__device__ __forceinline__ void put_chunk(uint32_t area, const float (&v)[32], O* out, long long ld, int rows, int cols, bool vec, int lane)
+{
+    constexpr int E = 16 / sizeof(O), P = 32 / E;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        uint32_t w[4];
+        words_of<O>(v + q * E, w);
+        st_shared16(chunk_at<O>(area, lane, q), w);
+    }
+    __syncwarp();
+    if (vec && cols % E == 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int row = i * (32 / P) + lane / P, q = lane % P;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(chunk_at<O>(area, row, q)));
+            if (row < rows && q * E < cols) *reinterpret_cast<uint4*>(out + row * ld + q * E) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        for (int row = 0; row < rows; ++row)
+            if (lane < cols) {
+                if constexpr (sizeof(O) == 4) {
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(element_at<O>(area, row, lane)));
+                    out[row * ld + lane] = __uint_as_float(w);
+                } else {
+                    uint16_t w;
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(element_at<O>(area, row, lane)));
+                    reinterpret_cast<uint16_t*>(out)[row * ld + lane] = w;
+                }
+            }
+    }
+}
+// what is not there is 0
+template <typename O>
+__device__ __forceinline__ void get_chunk(uint32_t area, float (&v)[32], const O* in, long long ld, int rows, int cols, bool vec, int lane)
+{
+    constexpr int E = 16 / sizeof(O), P = 32 / E;
+    __syncwarp();
+    if (vec && cols % E == 0) {
+        uint4 w[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int row = i * (32 / P) + lane / P, q = lane % P;
+            w[i] = row < rows && q * E < cols ? *reinterpret_cast<const uint4*>(in + row * ld + q * E) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            st_shared16(chunk_at<O>(area, i * (32 / P) + lane / P, lane % P), u);
+        }
+    } else {
+        for (int row = 0; row < 32; ++row) {
+            const bool there = row < rows && lane < cols;
+            if constexpr (sizeof(O) == 4) {
+                const uint32_t w = there ? __float_as_uint(in[row * ld + lane]) : 0u;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(element_at<O>(area, row, lane)), "r"(w) : "memory");
+            } else {
+                const uint16_t w = there ? reinterpret_cast<const uint16_t*>(in)[row * ld + lane] : (uint16_t)0;
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(element_at<O>(area, row, lane)), "h"(w) : "memory");
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(chunk_at<O>(area, lane, q)));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(O) == 4) {
+                v[q * E + k] = __uint_as_float(w[k]);
+            } else {
+                const O* e = reinterpret_cast<const O*>(&w[k]);
+                v[q * E + 2 * k] = to_f32(e[0]);
+                v[q * E + 2 * k + 1] = to_f32(e[1]);
+            }
+        }
+    }
+}
+// Sums over the 32 lanes of each of v's entries; lane l receives that of entry l. 31 shuffles in a fixed order.
+__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const bool up = lane & o;
+            const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + o], o);
+            v[j] = (up ? v[j + o] : v[j]) + other;
+        }
+    return v[0];
+}
+
+template <typename T> __device__ __forceinline__ void add_bias(float (&v)[32], const void* bias, int f0, int cols) {
+    if (!bias) return;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < cols) v[j] += to_f32(static_cast<const T*>(bias)[f0 + j]);
+}
+
+// h in place of g, or with dh the gradients of g and u in their places
+template <int ACT, bool EXACT, bool GRADS> __device__ __forceinline__ void gate32(float (&g)[32], float (&u)[32], const float (&d)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float slope;
+        const float v = activate<ACT, EXACT, GRADS>(g[j], slope);
+        if (GRADS) {
+            g[j] = d[j] * u[j] * slope;
+            u[j] = d[j] * v;
+        } else {
+            g[j] = v * u[j];
+        }
+    }
+}
+template <bool EXACT, bool GRADS> __device__ __forceinline__ void gate_by(int activation, float (&g)[32], float (&u)[32], const float (&d)[32]) {
+    switch (activation) {
+        case SDTW_ACT_SILU: gate32<SDTW_ACT_SILU, EXACT, GRADS>(g, u, d); break;
+        case SDTW_ACT_GELU: gate32<SDTW_ACT_GELU, EXACT, GRADS>(g, u, d); break;
+        case SDTW_ACT_RELU: gate32<SDTW_ACT_RELU, EXACT, GRADS>(g, u, d); break;
+        default: gate32<SDTW_ACT_SIGMOID, EXACT, GRADS>(g, u, d); break;
+    }
+}
+
+// T: the call's type. NB: columns of the accumulator; FWD and GRAD have NB / 2 features of either product in them.
+template <int KIND, typename T, int NB>
+__global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_constant__ Params p)
+{
+    using Sh = Shape<NB>;
+    using O = typename Operand<T>::type;
+    constexpr bool PAIR = KIND == FWD || KIND == GRAD, A_MN = KIND == DW, B_MN = KIND == DX || KIND == DW;
+    constexpr int WIDTH = PAIR ? NB / 2 : NB;             // columns of a tile's result
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    __shared__ uint64_t s_full[Sh::stages], s_empty[Sh::stages], s_done[2], s_free[2], s_end;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_late;
+    const Late late{&g_status, &s_late};
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (warp == kLoad && lane == 0) {
+        prefetch_map(&p.a), prefetch_map(&p.b[0]), prefetch_map(&p.b[1]);
+        s_late = 0;
+        for (int e = 0; e < Sh::stages; ++e) mbar_init(smem_u32(&s_full[e]), 1), mbar_init(smem_u32(&s_empty[e]), 1);
+        for (int e = 0; e < 2; ++e) mbar_init(smem_u32(&s_done[e]), 1), mbar_init(smem_u32(&s_free[e]), 8);
+        mbar_init(smem_u32(&s_end), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kIssue) tmem_alloc(&s_tmem, Sh::columns);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = (uint32_t)uniform((int)s_tmem), ring = smem_u32(dyn);
+    bool ok = true;
+
+    if (warp == kLoad) {
+        if (lane == 0 && !p.skip) {
+            int i = 0;   // blocks sent for
+            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+                const Tile tile(p, t);
+                for (int k = tile.first; k < tile.last; ++k, ++i) {
+                    const int e = i % Sh::stages;
+                    if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, late);
+                    if (!ok) break;
+                    const Seg sg = p.seg[k / p.blocks];
+                    const int at = k % p.blocks * kBlock;
+                    const uint32_t bar = smem_u32(&s_full[e]), a = ring + e * Sh::stage, b = a + kABytes;
+                    mbar_expect_tx(bar, Sh::stage);
+                    if constexpr (A_MN) {
+#pragma unroll
+                        for (int c = 0; c < kRows / 64; ++c)
+                            tma3(a + c * kBlock * 128, &p.a, tile.m * kRows + c * 64, at, sg.a + tile.set * kParts<T>, bar);
+                    } else {
+                        tma3(a, &p.a, at, tile.m * kRows, sg.a, bar);
+                    }
+                    if constexpr (PAIR) {
+                        tma3(b, &p.b[0], at, tile.n * WIDTH, sg.b, bar);
+                        tma3(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, sg.b, bar);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < NB / 64; ++c) tma3(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + c * 64, at, sg.b, bar);
+                    }
+                }
+            }
+            // no copy may be writing shared memory when the CTA ends
+            bool drained = true;
+            for (int k = max(0, i - Sh::stages); k < i; ++k)
+                wait_for(drained, smem_u32(&s_full[k % Sh::stages]), (uint32_t)((k / Sh::stages) & 1), p.wait_ns, late);
+        }
+        __syncwarp();
+    } else if (warp == kIssue) {
+        const uint32_t id = idesc2<O>(kRows, NB, A_MN, B_MN);
+        int i = 0, n = 0;
+        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++n) {
+            const Tile tile(p, t);
+            const int first = uniform(tile.first), last = uniform(tile.last);
+            const uint32_t d = tmem + (n & 1) * NB;
+            if (n >= 2) wait_warp(ok, smem_u32(&s_free[n & 1]), (uint32_t)((n / 2 - 1) & 1), p.wait_ns, late);
+            fence_after_sync();
+            for (int k = first; k < last; ++k, ++i) {
+                const int e = i % Sh::stages;
+                wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, late);
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    const uint32_t a = ring + e * Sh::stage, b = a + kABytes;
+                    const uint64_t ad = A_MN ? desc_mn(a) : sdesc(a), bd = B_MN ? desc_mn(b) : sdesc(b);
+#pragma unroll
+                    for (int s = 0; s < kBlock / 16; ++s)   // 16 of the sum: 32 bytes along a row, or 16 rows
+                        mma_ss(d, ad + s * (A_MN ? 128 : 2), bd + s * (B_MN ? 128 : 2), id, k > first || s > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&s_empty[e]));
+                    if (k == last - 1) mma_commit(smem_u32(&s_done[n & 1]));
+                }
+                __syncwarp();
+            }
+        }
+        // every MMA has read its operands and written its result before the CTA ends
+        if (lane == 0) {
+            mma_commit(smem_u32(&s_end));
+            bool fin = true;
+            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, late);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
+        const float up = p.scale ? p.scale[0] : 1.f, down = p.scale ? p.scale[1] : 1.f;
+        int n = 0;
+        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
+            const Tile tile(p, t);
+            const long long row0 = (long long)tile.m * kRows + quarter * 32;
+            const int rows = (int)min(32ll, p.M - row0);
+            const int limit = PAIR ? p.F : p.N;
+            wait_warp(ok, smem_u32(&s_done[n & 1]), (uint32_t)((n / 2) & 1), p.wait_ns, late);
+            fence_after_sync();
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * NB;
+#pragma unroll 1
+            for (int c = half; c < WIDTH / 32; c += 2) {
+                const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
+                float g[32], u[32], dh[32];
+                const bool some = rows > 0 && cols > 0;
+                if constexpr (KIND == GRAD)
+                    if (some) {
+                        const T* src = static_cast<const T*>(p.dh) + row0 * p.F + col;
+                        get_chunk<T>(area, dh, src, p.F, rows, cols, p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh), lane);
+                    }
+                tmem_ld32_nowait(acc + c * 32, g);
+                if constexpr (PAIR) tmem_ld32_nowait(acc + WIDTH + c * 32, u);
+                tmem_wait_ld();
+                if (c + 2 >= WIDTH / 32) {   // the accumulator has been read
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_free[n & 1]));
+                }
+                if (!some) continue;
+                if constexpr (PAIR) {
+                    add_bias<T>(g, p.bias[0], col, cols);
+                    add_bias<T>(u, p.bias[1], col, cols);
+                }
+                const bool bad = !ok || late.any();
+                if constexpr (KIND == FWD) {
+                    gate_by<sizeof(T) == 4, false>(p.activation, g, u, g);
+                } else if constexpr (KIND == GRAD) {
+                    gate_by<sizeof(T) == 4, true>(p.activation, g, u, dh);
+                    if (lane >= rows) {   // rows that are not there: 0 by a NaN bias is not 0
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = u[j] = 0.f;
+                    }
+                } else if constexpr (KIND == DX || KIND == DW) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) g[j] *= down;
+                }
+                if (bad) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) g[j] = __int_as_float(0x7fffffff), u[j] = g[j];
+                }
+                if constexpr (KIND == GRAD) {
+#pragma unroll 1
+                    for (int which = 0; which < 2; ++which) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = which ? u[j] : g[j];
+#pragma unroll 1
+                        for (int part = 0; part < kParts<T>; ++part) {
+                            float r[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                r[j] = v[j] * up;
+                                if (kParts<T> > 1) v[j] -= to_f32(from_f32<O>(v[j]));   // exact: what the parts so far leave
+                            }
+                            put_chunk<O>(area, r, reinterpret_cast<O*>(p.grads) + ((which * kParts<T> + part) * p.M + row0) * p.ld + col, p.ld, rows,
+                                         cols, true, lane);
+                        }
+                        if (p.sums) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = which ? u[j] : g[j];
+                            const float s = column_sums(v, lane);
+                            if (lane < cols) p.sums[((long long)tile.m * 4 + quarter) * 2 * p.F + which * p.F + col + lane] = s;
+                        }
+                    }
+                } else if (KIND == DW && p.splits > 1) {
+                    float* out = p.shares + (((long long)tile.split * p.sets + tile.set - p.set0) * p.M + row0) * p.N + col;
+                    put_chunk<float>(area, g, out, p.N, rows, cols, p.N % 4 == 0, lane);
+                } else {
+                    T* base = static_cast<T*>(p.out[KIND == DW ? tile.set : 0]);
+                    if (base) put_chunk<T>(area, g, base + row0 * limit + col, limit, rows, cols, limit % (16 / (int)sizeof(T)) == 0 && aligned16_dev(base), lane);
+                }
+            }
+            if (half >= WIDTH / 32) {   // narrow tiles leave nothing for the other warps
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_free[n & 1]));
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == kIssue) {
+        fence_after_sync();
+        tmem_dealloc(tmem, Sh::columns);
+    }
+}
+
+template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cudaStream_t s)
+{
+    using Sh = Shape<NB>;
+    if (const cudaError_t e = allow_smem<gated_tc_kernel<KIND, T, NB>>(Sh::smem); e != cudaSuccess) return e;
+    p.tiles = p.tiles_m * p.tiles_n * p.sets * p.splits;
+    gated_tc_kernel<KIND, T, NB><<<p.tiles < sms ? p.tiles : sms, kThreadsG, Sh::smem, s>>>(p);
+    return cudaGetLastError();
+}
+template <int KIND, typename T> cudaError_t run_nb(Params& p, int NB, int sms, cudaStream_t s)
+{
+    return NB == 256 ? run<KIND, T, 256>(p, sms, s) : NB == 128 ? run<KIND, T, 128>(p, sms, s) : run<KIND, T, 64>(p, sms, s);
+}
+template <int KIND> cudaError_t run_kind(Params& p, int dtype, int NB, int sms, cudaStream_t s)
+{
+    if (dtype == SDTW_F32) return run_nb<KIND, float>(p, NB, sms, s);
+    if (dtype == SDTW_BF16) return run_nb<KIND, __nv_bfloat16>(p, NB, sms, s);
+    return run_nb<KIND, __half>(p, NB, sms, s);
+}
+static cudaError_t take_status_of_file(int* out, cudaStream_t s)
+{
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
+
+// one file each, compiled side by side; NB is 256, 128 or 64
+cudaError_t run_fwd(Params& p, int dtype, int NB, int sms, cudaStream_t s);
+cudaError_t run_grad(Params& p, int dtype, int NB, int sms, cudaStream_t s);
+cudaError_t run_dx(Params& p, int dtype, int NB, int sms, cudaStream_t s);
+cudaError_t run_dw(Params& p, int dtype, int NB, int sms, cudaStream_t s);
+
+}  // namespace gtc
+}  // namespace sdtw
