@@ -38,6 +38,11 @@ template <typename T> __device__ __forceinline__ uint32_t open_bits() {
 }
 __device__ __forceinline__ void set_raw(uint32_t& r, uint32_t v) { r = v; }
 __device__ __forceinline__ void set_raw(Pair& r, uint32_t v) { r = (Pair)v << 32 | v; }
+template <typename T, int VEC> __device__ __forceinline__ void load(typename Raw<T, VEC>::type& r, const T* p) {
+    if constexpr (sizeof(T) * VEC == 8) asm volatile("ld.global.b64 %0, [%1];" : "=l"(r) : "l"(p));
+    else if constexpr (sizeof(T) * VEC == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p));
+    else asm volatile("ld.global.u16 %0, [%1];" : "=r"(r) : "l"(p));
+}
 template <typename T, int VEC> __device__ __forceinline__ void load_if(typename Raw<T, VEC>::type& r, const T* p, bool there) {
     if constexpr (sizeof(T) * VEC == 8)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.b64 %0, [%1];\n\t}" : "+l"(r) : "l"(p), "r"((int)there));
@@ -73,20 +78,39 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
     else *reinterpret_cast<Pair*>(p) = v;
 }
 
-// a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. From e = 2^120 on
-// a is 0 and b is 1. A NaN stays.
-template <bool EXACT> __device__ __forceinline__ void gate_of(float z, float& a, float& b) {
-    const float t = -1.4426950408889634f * z, e = EXACT ? expf(-z) : ex2(t);
-    const bool closed = t > 120.f;
-    a = closed ? 0.f : __fdividef(1.f, 1.f + e);
-    b = closed ? 1.f : e * a;
+// a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. EXACT, for
+// results of 32 bits: a is 0 and b 1 from e = 2^120 on; otherwise e ends at 2^126, which 16 bits of either do not show. A
+// NaN stays.
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float v, float most) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
+    return r;
 }
 template <bool EXACT, int VEC> __device__ __forceinline__ void gates(Pair z, Pair& a, Pair& b) {
-    float z0, z1, a0, a1 = 0.f, b0, b1 = 0.f;
-    upk2(z, z0, z1);
-    gate_of<EXACT>(z0, a0, b0);
-    if (VEC > 1) gate_of<EXACT>(z1, a1, b1);
-    a = pk2(a0, a1), b = pk2(b0, b1);
+    if constexpr (EXACT) {
+        float g[2], f[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
+        upk2(z, g[0], g[1]);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const float e = expf(-g[k]);
+            const bool closed = g[k] < -83.f;
+            f[k] = closed ? 0.f : reciprocal(1.f + e);
+            o[k] = closed ? 1.f : e * f[k];
+        }
+        a = pk2(f[0], f[1]), b = pk2(o[0], o[1]);
+    } else {
+        float t0, t1;
+        upk2(mul2(z, pair(-1.4426950408889634f)), t0, t1);
+        const Pair e = pk2(ex2(min_nan(t0, 126.f)), VEC > 1 ? ex2(min_nan(t1, 126.f)) : 0.f);
+        upk2(add2(e, pair(1.f)), t0, t1);
+        a = pk2(reciprocal(t0), VEC > 1 ? reciprocal(t1) : 1.f);
+        b = mul2(e, a);
+    }
 }
 
 // A batch element's positions, in the order of the recurrence
@@ -117,13 +141,18 @@ struct alignas(16) Run {   // h -> a h + h0
 };
 
 // Rows [t, t + ROWS) of a run, in the recurrence's order: `there` of them are within the element's length, `none` stands
-// for the others.
+// for the others. A row's offset is within 32 bits.
 template <typename T, int VEC, int ROWS>
-__device__ __forceinline__ void fetch(typename Raw<T, VEC>::type (&out)[ROWS], const T* first, long long step, int there, uint32_t none) {
+__device__ __forceinline__ void fetch(typename Raw<T, VEC>::type (&out)[ROWS], const T* first, int step, int there, uint32_t none) {
+    if (there >= ROWS) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        set_raw(out[i], none);
-        load_if<T, VEC>(out[i], first + i * step, i < there);
+        for (int i = 0; i < ROWS; ++i) load<T, VEC>(out[i], first + i * step);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            set_raw(out[i], none);
+            load_if<T, VEC>(out[i], first + i * step, i < there);
+        }
     }
 }
 
@@ -145,7 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
     const long long bc = (long long)b * a.C + c;
     const int per = ctas * kWarps * ROWS;                 // positions that the cluster takes at a time
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
-    const long long xs = el.reverse ? -a.x_stride[1] : a.x_stride[1], gs = el.reverse ? -a.gate_stride[1] : a.gate_stride[1];
+    const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
     const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0] + c;
     const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c;
     T* out = static_cast<T*>(p.h) + (long long)b * a.N * a.C + c;
@@ -202,13 +231,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
         if (p.kept && t % kStep == 0 && t < a.N) store_f32<VEC>(p.kept + ((long long)b * steps + t / kStep) * a.C + c, h);
         const long long r = el.row(t);
         T* dst = out + r * a.C;
-        const long long step = el.reverse ? -(long long)a.C : a.C;
+        if (there >= ROWS) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            h = fma2(f[i], h, u[i]);
-            if (i < there) store<T, VEC>(dst + i * step, h);
+            for (int i = 0; i < ROWS; ++i) {
+                h = fma2(f[i], h, u[i]);
+                store<T, VEC>(dst + i * step, h);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                h = fma2(f[i], h, u[i]);
+                if (i < there) store<T, VEC>(dst + i * step, h);
+            }
+            clear<T, VEC>(out, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
         }
-        if (there < ROWS) clear<T, VEC>(out, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
     }
     if (!on) return;
     clear<T, VEC>(out, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
@@ -230,7 +266,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
     const long long bc = (long long)b * a.C + c, base = (long long)b * a.N * a.C + c;
     const int per = ctas * kStep;
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
-    const int turn_sign = el.reverse ? -1 : 1;
+    const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
     const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0] + c;
     const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c;
     const T* dh = p.dh ? static_cast<const T*>(p.dh) + base : nullptr;
@@ -243,9 +279,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
     auto get = [&](int at) {
         const int there = on ? el.len - at : 0;
         const long long r = el.row(at);
-        fetch<T, VEC, ROWS>(xr, x + r * a.x_stride[1], turn_sign * a.x_stride[1], there, 0);
-        fetch<T, VEC, ROWS>(gr, gate + r * a.gate_stride[1], turn_sign * a.gate_stride[1], there, open_bits<T>());
-        fetch<T, VEC, ROWS>(dr, dh + r * a.C, turn_sign * (long long)a.C, dh ? there : 0, 0);
+        fetch<T, VEC, ROWS>(xr, x + r * a.x_stride[1], xs, there, 0);
+        fetch<T, VEC, ROWS>(gr, gate + r * a.gate_stride[1], gs, there, open_bits<T>());
+        fetch<T, VEC, ROWS>(dr, dh + r * a.C, step, dh ? there : 0, 0);
         state = there > 0 ? load_f32<VEC>(p.kept_in + ((long long)b * steps + at / kStep) * a.C + c) : pair(0.f);
     };
     if (rounds > 0) get(t);
@@ -300,22 +336,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
         }
         r = fma2(behind.a, r, behind.h);
         if (!on) continue;
-        const long long row = el.row(t), step = turn_sign * (long long)a.C;
+        const long long row = (long long)el.row(t) * a.C;
         Pair before[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             before[i] = a.tied ? fma2(v[i], pair(-1.f), h) : h;
             h = fma2(f[i], h, a.tied ? mul2(o[i], v[i]) : v[i]);
         }
+        auto go = [&](bool every) {
 #pragma unroll
-        for (int i = ROWS - 1; i >= 0; --i) {
-            const Pair e = add2(d[i], r), g = mul2(o[i], e);
-            r = mul2(f[i], e);
-            if (i < there) {
-                store<T, VEC>(dx + row * a.C + i * step, a.tied ? g : e);
-                store<T, VEC>(dgate + row * a.C + i * step, mul2(mul2(g, f[i]), before[i]));
+            for (int i = ROWS - 1; i >= 0; --i) {
+                const Pair e = add2(d[i], r), g = mul2(o[i], e);
+                r = mul2(f[i], e);
+                if (every || i < there) {
+                    store<T, VEC>(dx + row + i * step, a.tied ? g : e);
+                    store<T, VEC>(dgate + row + i * step, mul2(mul2(g, f[i]), before[i]));
+                }
             }
-        }
+        };
+        if (there >= ROWS) go(true);
+        else go(false);
         if (there < ROWS) {
             clear<T, VEC>(dx, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
             clear<T, VEC>(dgate, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
@@ -338,9 +378,9 @@ template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) 
     const Element el(a, b);
     const long long bc = (long long)b * a.C + c, r = el.row(0), base = (long long)b * a.N * a.C + c;
     typename Raw<T, VEC>::type xr[ROWS], gr[ROWS];
-    const int turn_sign = el.reverse ? -1 : 1;
-    fetch<T, VEC, ROWS>(xr, static_cast<const T*>(a.x) + b * a.x_stride[0] + c + r * a.x_stride[1], turn_sign * a.x_stride[1], el.len, 0);
-    fetch<T, VEC, ROWS>(gr, static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c + r * a.gate_stride[1], turn_sign * a.gate_stride[1], el.len, open_bits<T>());
+    const int sign = el.reverse ? -1 : 1;
+    fetch<T, VEC, ROWS>(xr, static_cast<const T*>(a.x) + b * a.x_stride[0] + c + r * a.x_stride[1], sign * (int)a.x_stride[1], el.len, 0);
+    fetch<T, VEC, ROWS>(gr, static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c + r * a.gate_stride[1], sign * (int)a.gate_stride[1], el.len, open_bits<T>());
     Pair h = a.state ? load_f32<VEC>(a.state + bc) : pair(0.f);
     if (p.kept) store_f32<VEC>(p.kept + bc, h);
     T* out = static_cast<T*>(p.h) + base;
