@@ -28,9 +28,12 @@ struct RecurrenceParams {
     const float* dlast;
     void *dx, *dgate;
     float* dstate;
+    unsigned long long wait_ns;   // of a wait within a cluster
+    int skip;                     // test hook: a cluster's first CTA sends nothing
 };
 cudaError_t launch_recurrence_forward(const RecurrenceParams& p, int sms, cudaStream_t s);
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, int sms, cudaStream_t s);
+cudaError_t recurrence_take_status(int* out, cudaStream_t s);
 
 struct GatedParams {
     sdtw_gated a;

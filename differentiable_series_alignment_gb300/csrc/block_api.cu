@@ -43,8 +43,8 @@ sdtw_status check_recurrence(const sdtw_recurrence* a)
     if (!a) return SDTW_ERR_ARG;
     if (a->B < 1 || a->N < 1 || a->C < 1) return SDTW_ERR_EMPTY;
     if (!a->x || !a->gate || !good_dtype(a->dtype)) return SDTW_ERR_ARG;
-    // 32-bit positions and grids, and offsets of a run of 16 positions
-    if (a->N >= (1 << 30) || a->C > (1 << 26) || std::llabs(a->x_stride[1]) > (1 << 26) || std::llabs(a->gate_stride[1]) > (1 << 26) || (long long)a->B * ((a->C + 31ll) / 32) > 0x7fffffffll) return SDTW_ERR_TOO_LARGE;
+    // 32-bit positions and grids, and offsets of 128 positions
+    if (a->N >= (1 << 30) || a->C > (1 << 23) || std::llabs(a->x_stride[1]) > (1 << 23) || std::llabs(a->gate_stride[1]) > (1 << 23) || (long long)a->B * ((a->C + 31ll) / 32) > 0x7fffffffll) return SDTW_ERR_TOO_LARGE;
     return SDTW_OK;
 }
 
@@ -119,6 +119,7 @@ sdtw_status sdtw_recurrence_forward(const sdtw_recurrence* a, void* h, float* la
     if (!h) return SDTW_ERR_ARG;
     RecurrenceParams p{};
     p.a = *a, p.h = h, p.last = last, p.kept = kept;
+    p.wait_ns = debug_wait_ns(), p.skip = debug_take_skip_publish();
     BLOCK_CUDA(launch_recurrence_forward(p, device_sms(), static_cast<cudaStream_t>(stream)));
     return SDTW_OK;
 }
@@ -130,6 +131,7 @@ sdtw_status sdtw_recurrence_backward(const sdtw_recurrence* a, const float* kept
     if (!kept || !dx || !dgate) return SDTW_ERR_ARG;
     RecurrenceParams p{};
     p.a = *a, p.kept_in = kept, p.dh = dh, p.dlast = dlast, p.dx = dx, p.dgate = dgate, p.dstate = dstate;
+    p.wait_ns = debug_wait_ns(), p.skip = debug_take_skip_publish();
     BLOCK_CUDA(launch_recurrence_backward(p, device_sms(), static_cast<cudaStream_t>(stream)));
     return SDTW_OK;
 }

@@ -284,7 +284,7 @@ sdtw_status sdtw_encoder_status(void* stream)
 {
     int any = 0;
     for (const auto take : {attn_forward_take_status, attn_backward_take_status, gated_fwd_take_status, gated_grad_take_status, gated_dx_take_status,
-                            gated_dw_take_status}) {
+                            gated_dw_take_status, recurrence_take_status}) {
         int one = 0;
         ENC_CUDA(take(&one, static_cast<cudaStream_t>(stream)));
         any |= one;

@@ -4,12 +4,16 @@
 //   e_t = dh_t + r_{t+1}, r_t = a_t e_t, dx_t = (1 - a_t) e_t or e_t, dgate_t = e_t (h_{t-1} - x_t or h_{t-1}) a_t (1 - a_t)
 //
 // Steps h -> a h + u compose: the steps of a run of positions are one pair (A, H), h -> A h + H, and those of the
-// gradient one pair (A, R) with the same A. A warp has a run of ROWS positions of 32 lanes' channels, a lane two of
-// them (one where sizes are odd): it loads its run into registers and composes it, the CTA's warps and then the CTAs of a cluster
+// gradient one pair (A, R) with the same A, R = sum_i a_1 .. a_i dh_i. A warp has a run of ROWS positions of 32 lanes' channels,
+// a lane two of them (one where sizes are odd): it composes its run, the CTA's warps and then the CTAs of a cluster
 // exchange their pairs through shared memory, and each goes over its run again from the state before it. A cluster so takes
 // CTAs x warps x ROWS positions at a time, and carries the state to the next. The order of all sums is fixed by the sizes:
 // the same bits every time. The backward pass computes the states again from those that the forward pass kept, one in
 // SDTW_RECURRENCE_STEP positions: 3 reads and 2 writes where stored states would be another read.
+//
+// Coming positions are on their way to shared memory meanwhile (cp.async, rows of 16-byte pieces; sizes and addresses that
+// do not allow them are loaded by the lanes that use them). Pairs go between CTAs by stores that report to the receiver's
+// mbarrier: a cluster's own barrier also waits for the results that are on their way to memory.
 #include "activation.cuh"
 #include "block.h"
 #include "packed.cuh"
@@ -20,7 +24,8 @@ namespace sdtw {
 namespace {
 
 constexpr int kStep = SDTW_RECURRENCE_STEP;
-constexpr int kWarps = 8, kMostCtas = 8;   // of a CTA; of a cluster
+constexpr int kWarps = 8, kMostCtas = 16;   // of a CTA; of a cluster
+constexpr int kStages = 3;                  // of the forward pass's ring
 using Pair = unsigned long long;           // two channels' fp32 values
 
 __device__ __forceinline__ Pair pair(float v) { return pk2(v, v); }
@@ -38,11 +43,6 @@ template <typename T> __device__ __forceinline__ uint32_t open_bits() {
 }
 __device__ __forceinline__ void set_raw(uint32_t& r, uint32_t v) { r = v; }
 __device__ __forceinline__ void set_raw(Pair& r, uint32_t v) { r = (Pair)v << 32 | v; }
-template <typename T, int VEC> __device__ __forceinline__ void load(typename Raw<T, VEC>::type& r, const T* p) {
-    if constexpr (sizeof(T) * VEC == 8) asm volatile("ld.global.b64 %0, [%1];" : "=l"(r) : "l"(p));
-    else if constexpr (sizeof(T) * VEC == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p));
-    else asm volatile("ld.global.u16 %0, [%1];" : "=r"(r) : "l"(p));
-}
 template <typename T, int VEC> __device__ __forceinline__ void load_if(typename Raw<T, VEC>::type& r, const T* p, bool there) {
     if constexpr (sizeof(T) * VEC == 8)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.b64 %0, [%1];\n\t}" : "+l"(r) : "l"(p), "r"((int)there));
@@ -122,18 +122,41 @@ struct Element {
 };
 
 // ---- clusters
-__device__ __forceinline__ void cluster_arrive() {
+__device__ int g_status;
+
+__device__ __forceinline__ void cluster_sync() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ uint32_t in_cta(uint32_t mine, int cta) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(cta));
+    return there;
 }
-__device__ __forceinline__ void store_remote(const void* mine, int cta, Pair x, Pair y) {
-    uint32_t at = (uint32_t)__cvta_generic_to_shared(mine), there;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
-    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(there), "l"(x), "l"(y) : "memory");
+// 16 bytes to another CTA's shared memory, reported to its barrier
+__device__ __forceinline__ void send_pairs(uint32_t there, uint32_t bar, Pair x, Pair y) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(there), "l"(x), "l"(y), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded: false, and the status word set, when it ran out.
+__device__ __forceinline__ bool wait_arrived(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    if (arrived(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!arrived(bar, parity))
+        if (global_ns() - t0 > limit_ns) {
+            atomicOr(&g_status, kStatusTimeout);
+            return false;
+        }
+    return true;
 }
 
 struct alignas(16) Run {   // h -> a h + h0
@@ -141,18 +164,13 @@ struct alignas(16) Run {   // h -> a h + h0
 };
 
 // Rows [t, t + ROWS) of a run, in the recurrence's order: `there` of them are within the element's length, `none` stands
-// for the others. A row's offset is within 32 bits.
+// for the others.
 template <typename T, int VEC, int ROWS>
 __device__ __forceinline__ void fetch(typename Raw<T, VEC>::type (&out)[ROWS], const T* first, int step, int there, uint32_t none) {
-    if (there >= ROWS) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) load<T, VEC>(out[i], first + i * step);
-    } else {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            set_raw(out[i], none);
-            load_if<T, VEC>(out[i], first + i * step, i < there);
-        }
+    for (int i = 0; i < ROWS; ++i) {
+        set_raw(out[i], none);
+        load_if<T, VEC>(out[i], first + i * step, i < there);
     }
 }
 
@@ -161,66 +179,121 @@ template <typename T, int VEC> __device__ __forceinline__ void clear(T* base, lo
     for (t += warp; t < N; t += warps) store<T, VEC>(base + t * C, pair(0.f));
 }
 
+// The CTA's positions of one array, as they lie in memory: by cp.async in a ring of stages, or in the lanes' registers.
+template <typename T, int VEC, int ROWS, bool RING> struct Rows {
+    typename Raw<T, VEC>::type raw[ROWS];
+    __device__ __forceinline__ Pair at(int i, const unsigned char*) const { return value<T, VEC>(raw[i]); }
+};
+template <typename T, int VEC, int ROWS> struct Rows<T, VEC, ROWS, true> {
+    __device__ __forceinline__ Pair at(int i, const unsigned char* mine) const {
+        return value<T, VEC>(*reinterpret_cast<const typename Raw<T, VEC>::type*>(mine + i * 32 * VEC * (int)sizeof(T)));
+    }
+};
+// [t0, t0 + kWarps ROWS) of an array into a stage: 16-byte pieces, `none` where there is nothing.
 template <typename T, int VEC, int ROWS>
+__device__ __forceinline__ void send_rows(unsigned char* stage, const T* first, int step, int there, int channels, uint32_t none) {
+    constexpr int bytes = 32 * VEC * sizeof(T), pieces = bytes / 16, per = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < kWarps * ROWS * pieces / (kWarps * 32); ++q) {
+        const int j = threadIdx.x + q * kWarps * 32, row = j / pieces, piece = j % pieces;
+        unsigned char* to = stage + j * 16;
+        if (row < there && piece * per < channels)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(first + row * step + piece * per) : "memory");
+        else
+            *reinterpret_cast<uint4*>(to) = make_uint4(none, none, none, none);
+    }
+}
+__device__ __forceinline__ void mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// TIED: 1, 0, or -1: as the call says.
+template <typename T, int VEC, int ROWS, bool RING, int TIED>
 __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const RecurrenceParams p, int ctas)
 {
-    __shared__ Run run[2][kWarps][32], total[2][kMostCtas][32];
+    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? kWarps * ROWS * bytes : 0;
+    constexpr int turns = RING ? 1 : 2;                   // with a ring, all threads meet once more in a round
+    __shared__ Run run[turns][kWarps][32];
+    __shared__ uint64_t s_bar[2];
+    extern __shared__ __align__(16) unsigned char ring[];   // [kStages][x, gate][kWarps ROWS][32 VEC], then [2][ctas][32] Runs
+    Run* total = reinterpret_cast<Run*>(ring + kStages * 2 * image);
     const sdtw_recurrence& a = p.a;
+    const bool tied = TIED < 0 ? a.tied != 0 : TIED != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x % ctas;
     const int columns = (a.C + 32 * VEC - 1) / (32 * VEC), id = blockIdx.x / ctas, b = id / columns;
-    const int c = (id % columns * 32 + lane) * VEC;
+    const int c0 = id % columns * 32 * VEC, c = c0 + lane * VEC;
     const bool on = c < a.C;
     const Element el(a, b);
     const long long bc = (long long)b * a.C + c;
     const int per = ctas * kWarps * ROWS;                 // positions that the cluster takes at a time
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
     const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
-    const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0] + c;
-    const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c;
+    const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0];
+    const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0];
     T* out = static_cast<T*>(p.h) + (long long)b * a.N * a.C + c;
-    if (ctas > 1) cluster_arrive();
+    const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
+    if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = a.state && on ? load_f32<VEC>(a.state + bc) : pair(0.f);
-    typename Raw<T, VEC>::type xr[ROWS], gr[ROWS];
-    int t = (rank * kWarps + warp) * ROWS;
-    auto get = [&](int at) {
-        const int there = on ? el.len - at : 0;
+    const int t0 = rank * kWarps * ROWS;                  // the CTA's first position
+    int t = t0 + warp * ROWS;
+    auto send = [&](int round) {
+        const int at = t0 + round * per;
+        unsigned char* stage = ring + round % kStages * 2 * image;
         const long long r = el.row(at);
-        fetch<T, VEC, ROWS>(xr, x + r * a.x_stride[1], xs, there, 0);
-        fetch<T, VEC, ROWS>(gr, gate + r * a.gate_stride[1], gs, there, open_bits<T>());
+        if (round < rounds) {
+            send_rows<T, VEC, ROWS>(stage, x + r * a.x_stride[1] + c0, xs, el.len - at, a.C - c0, 0);
+            send_rows<T, VEC, ROWS>(stage + image, gate + r * a.gate_stride[1] + c0, gs, el.len - at, a.C - c0, open_bits<T>());
+        }
+        mark();
     };
-    get(t);
-    if (ctas > 1) cluster_wait();                         // the others have begun
+    if constexpr (RING)
+        for (int k = 0; k < kStages - 1; ++k) send(k);
+    if (ctas > 1) cluster_sync();                         // the others have begun, with barriers
+    bool ok = true;
     for (int round = 0; round < rounds; ++round, t += per) {
         const int there = el.len - t, turn = round & 1;
+        Rows<T, VEC, ROWS, RING> xr, gr;
+        const unsigned char* mine = ring + round % kStages * 2 * image + warp * ROWS * bytes + lane * VEC * sizeof(T);
+        if constexpr (RING) {
+            landed<kStages - 2>();
+            __syncthreads();                              // everyone's pieces; and the stage before this one is read no more
+            send(round + kStages - 1);
+        } else {
+            const long long r = el.row(t);
+            fetch<T, VEC, ROWS>(xr.raw, x + r * a.x_stride[1] + c, xs, on ? there : 0, 0);
+            fetch<T, VEC, ROWS>(gr.raw, gate + r * a.gate_stride[1] + c, gs, on ? there : 0, open_bits<T>());
+        }
         Pair f[ROWS], u[ROWS];
         Run own{pair(1.f), pair(0.f)};
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             Pair o;
-            gates<sizeof(T) == 4, VEC>(value<T, VEC>(gr[i]), f[i], o);
-            u[i] = a.tied ? mul2(o, value<T, VEC>(xr[i])) : value<T, VEC>(xr[i]);
+            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image), f[i], o);
+            u[i] = tied ? mul2(o, xr.at(i, mine)) : xr.at(i, mine);
             own.a = mul2(own.a, f[i]);
             own.h = fma2(f[i], own.h, u[i]);
         }
-        if (round + 1 < rounds) get(t + per);
-        run[turn][warp][lane] = own;
+        run[turn % turns][warp][lane] = own;
         __syncthreads();
         Run all{pair(1.f), pair(0.f)}, before = all;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w == warp) before = all;
-            const Run r = run[turn][w][lane];
+            const Run r = run[turn % turns][w][lane];
             all.h = fma2(r.a, all.h, r.h);
             all.a = mul2(all.a, r.a);
         }
         Pair h = carry;
         if (ctas > 1) {
-            for (int k = warp; k < ctas; k += kWarps) store_remote(&total[turn][rank][lane], k, all.a, all.h);
-            cluster_arrive();
-            cluster_wait();
+            const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
+            if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
+            if (!(p.skip && rank == 0))
+                for (int k = warp; k < ctas; k += kWarps) send_pairs(in_cta(slot, k), in_cta(bar, k), all.a, all.h);
+            if (ok) ok = wait_arrived(bar, (uint32_t)(round >> 1) & 1, p.wait_ns);
+            if (!ok) carry = pair(__int_as_float(0x7fffffff));
             for (int k = 0; k < ctas; ++k) {
                 if (k == rank) h = carry;
-                const Run r = total[turn][k][lane];
+                const Run r = total[(turn * ctas + k) * 32 + lane];
                 carry = fma2(r.a, carry, r.h);
             }
         } else {
@@ -229,8 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
         h = fma2(before.a, h, before.h);
         if (!on) continue;
         if (p.kept && t % kStep == 0 && t < a.N) store_f32<VEC>(p.kept + ((long long)b * steps + t / kStep) * a.C + c, h);
-        const long long r = el.row(t);
-        T* dst = out + r * a.C;
+        T* dst = out + (long long)el.row(t) * a.C;
         if (there >= ROWS) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
@@ -246,121 +318,153 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
             clear<T, VEC>(out, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
         }
     }
+    if (ctas > 1) cluster_sync();                         // no store may come to a CTA that has ended
     if (!on) return;
     clear<T, VEC>(out, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
     if (p.last && rank == 0 && warp == 0) store_f32<VEC>(p.last + bc, carry);
 }
 
-template <typename T, int VEC, int ROWS>
+template <typename T, int VEC, int ROWS, bool RING, int TIED>
 __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const RecurrenceParams p, int ctas)
 {
-    __shared__ Run run[2][kWarps][32], total[2][kMostCtas][32];
-    __shared__ Pair back[2][kWarps][32];
-    static_assert(kWarps * ROWS == kStep, "a CTA's run begins with a kept state");
+    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? kWarps * ROWS * bytes : 0;
+    constexpr int turns = RING ? 1 : 2;
+    __shared__ Run run[turns][kWarps][32];
+    __shared__ Pair back[turns][kWarps][32];
+    __shared__ uint64_t s_bar[2];
+    extern __shared__ __align__(16) unsigned char ring[];   // [2][x, gate, dh][kWarps ROWS][32 VEC], then [2][ctas][32] Runs
+    Run* total = reinterpret_cast<Run*>(ring + 2 * 3 * image);
+    static_assert(kWarps * ROWS % kStep == 0 || kStep % (kWarps * ROWS) == 0, "kept states at CTAs' first positions");
     const sdtw_recurrence& a = p.a;
+    const bool tied = TIED < 0 ? a.tied != 0 : TIED != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x % ctas;
     const int columns = (a.C + 32 * VEC - 1) / (32 * VEC), id = blockIdx.x / ctas, b = id / columns;
-    const int c = (id % columns * 32 + lane) * VEC;
+    const int c0 = id % columns * 32 * VEC, c = c0 + lane * VEC;
     const bool on = c < a.C;
     const Element el(a, b);
-    const long long bc = (long long)b * a.C + c, base = (long long)b * a.N * a.C + c;
-    const int per = ctas * kStep;
+    const long long bc = (long long)b * a.C + c, base = (long long)b * a.N * a.C;
+    const int per = ctas * kWarps * ROWS;
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
     const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
-    const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0] + c;
-    const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0] + c;
-    const T* dh = p.dh ? static_cast<const T*>(p.dh) + base : nullptr;
-    T *dx = static_cast<T*>(p.dx) + base, *dgate = static_cast<T*>(p.dgate) + base;
-    if (ctas > 1) cluster_arrive();
+    const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0];
+    const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0];
+    const T* dh = static_cast<const T*>(p.dh) + base;
+    T *dx = static_cast<T*>(p.dx) + base + c, *dgate = static_cast<T*>(p.dgate) + base + c;
+    const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
+    if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = p.dlast && on ? load_f32<VEC>(p.dlast + bc) : pair(0.f);
-    typename Raw<T, VEC>::type xr[ROWS], gr[ROWS], dr[ROWS];
-    Pair state = pair(0.f);
-    int t = (rounds - 1) * per + (rank * kWarps + warp) * ROWS;
-    auto get = [&](int at) {
-        const int there = on ? el.len - at : 0;
+    const int t0 = rank * kWarps * ROWS;
+    auto send = [&](int round) {
+        const int at = t0 + round * per;
+        unsigned char* stage = ring + (round & 1) * 3 * image;
         const long long r = el.row(at);
-        fetch<T, VEC, ROWS>(xr, x + r * a.x_stride[1], xs, there, 0);
-        fetch<T, VEC, ROWS>(gr, gate + r * a.gate_stride[1], gs, there, open_bits<T>());
-        fetch<T, VEC, ROWS>(dr, dh + r * a.C, step, dh ? there : 0, 0);
-        state = there > 0 ? load_f32<VEC>(p.kept_in + ((long long)b * steps + at / kStep) * a.C + c) : pair(0.f);
+        if (round >= 0) {
+            send_rows<T, VEC, ROWS>(stage, x + r * a.x_stride[1] + c0, xs, el.len - at, a.C - c0, 0);
+            send_rows<T, VEC, ROWS>(stage + image, gate + r * a.gate_stride[1] + c0, gs, el.len - at, a.C - c0, open_bits<T>());
+            send_rows<T, VEC, ROWS>(stage + 2 * image, dh + r * a.C + c0, step, p.dh ? el.len - at : 0, a.C - c0, 0);
+        }
+        mark();
     };
-    if (rounds > 0) get(t);
-    if (ctas > 1) cluster_wait();
-    for (int round = rounds - 1; round >= 0; --round, t -= per) {
-        const int there = on ? el.len - t : 0, turn = round & 1;
-        Pair f[ROWS], o[ROWS], v[ROWS], d[ROWS], h = state;
+    auto kept = [&](int round) {   // the state before the CTA's first position
+        const int at = t0 + round * per;
+        return on && round >= 0 && at < el.len ? load_f32<VEC>(p.kept_in + ((long long)b * steps + at / kStep) * a.C + c) : pair(0.f);
+    };
+    if constexpr (RING) send(rounds - 1);
+    Pair state = kept(rounds - 1);
+    if (ctas > 1) cluster_sync();
+    bool ok = true;
+    int turn = 0, phase = 0;
+    for (int round = rounds - 1; round >= 0; --round) {
+        const int t = t0 + round * per + warp * ROWS, there = on ? el.len - t : 0;
+        Rows<T, VEC, ROWS, RING> xr, gr, dr;
+        const unsigned char* mine = ring + (round & 1) * 3 * image + warp * ROWS * bytes + lane * VEC * sizeof(T);
+        if constexpr (RING) {
+            landed<0>();
+            __syncthreads();
+            send(round - 1);
+        } else {
+            const long long r = el.row(t);
+            fetch<T, VEC, ROWS>(xr.raw, x + r * a.x_stride[1] + c, xs, there, 0);
+            fetch<T, VEC, ROWS>(gr.raw, gate + r * a.gate_stride[1] + c, gs, there, open_bits<T>());
+            fetch<T, VEC, ROWS>(dr.raw, dh + r * a.C + c, step, p.dh ? there : 0, 0);
+        }
+        Pair f[ROWS], o[ROWS], h = state, r = pair(0.f);
         Run own{pair(1.f), pair(0.f)};
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            gates<sizeof(T) == 4, VEC>(value<T, VEC>(gr[i]), f[i], o[i]);
-            v[i] = value<T, VEC>(xr[i]);
-            d[i] = value<T, VEC>(dr[i]);
+            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image), f[i], o[i]);
+            const Pair v = xr.at(i, mine);
             own.a = mul2(own.a, f[i]);
-            own.h = fma2(f[i], own.h, a.tied ? mul2(o[i], v[i]) : v[i]);
+            own.h = fma2(f[i], own.h, tied ? mul2(o[i], v) : v);
+            r = fma2(own.a, dr.at(i, mine + 2 * image), r);
         }
-        Pair r = pair(0.f);
-#pragma unroll
-        for (int i = ROWS - 1; i >= 0; --i) r = mul2(f[i], add2(d[i], r));
-        if (round > 0) get(t - per);
-        run[turn][warp][lane] = own;
-        back[turn][warp][lane] = r;
+        run[turn % turns][warp][lane] = own;
+        back[turn % turns][warp][lane] = r;
+        state = kept(round - 1);
         __syncthreads();
-        // states before the run, and what the later runs of the CTA hand back
+        // the state before the run, and what the later runs of the CTA hand back
         Run behind{pair(1.f), pair(0.f)};
         Pair all_a = pair(1.f), all_r = pair(0.f);
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w) {
             if (w == warp) behind = Run{all_a, all_r};
-            const Pair wa = run[turn][w][lane].a;
-            all_r = fma2(wa, all_r, back[turn][w][lane]);
+            const Pair wa = run[turn % turns][w][lane].a;
+            all_r = fma2(wa, all_r, back[turn % turns][w][lane]);
             all_a = mul2(all_a, wa);
         }
-#pragma unroll
-        for (int w = 0; w < kWarps - 1; ++w)
-            if (w < warp) {
-                const Run q = run[turn][w][lane];
-                h = fma2(q.a, h, q.h);
-            }
+        for (int w = 0; w < warp; ++w) {
+            const Run q = run[turn % turns][w][lane];
+            h = fma2(q.a, h, q.h);
+        }
         r = carry;
         if (ctas > 1) {
-            for (int k = warp; k < ctas; k += kWarps) store_remote(&total[turn][rank][lane], k, all_a, all_r);
-            cluster_arrive();
-            cluster_wait();
+            const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
+            if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
+            if (!(p.skip && rank == 0))
+                for (int k = warp; k < ctas; k += kWarps) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
+            if (ok) ok = wait_arrived(bar, (uint32_t)phase, p.wait_ns);
+            if (!ok) carry = pair(__int_as_float(0x7fffffff));
             for (int k = ctas - 1; k >= 0; --k) {
                 if (k == rank) r = carry;
-                const Run q = total[turn][k][lane];
+                const Run q = total[(turn * ctas + k) * 32 + lane];
                 carry = fma2(q.a, carry, q.h);
             }
         } else {
             carry = fma2(all_a, carry, all_r);
         }
+        phase ^= turn;   // every second round
+        turn ^= 1;
         r = fma2(behind.a, r, behind.h);
         if (!on) continue;
         const long long row = (long long)el.row(t) * a.C;
-        Pair before[ROWS];
+        Pair w[ROWS];   // dgate_t / e_t
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            before[i] = a.tied ? fma2(v[i], pair(-1.f), h) : h;
-            h = fma2(f[i], h, a.tied ? mul2(o[i], v[i]) : v[i]);
+            const Pair v = xr.at(i, mine);
+            w[i] = mul2(mul2(f[i], o[i]), tied ? fma2(v, pair(-1.f), h) : h);
+            h = fma2(f[i], h, tied ? mul2(o[i], v) : v);
         }
         auto go = [&](bool every) {
 #pragma unroll
             for (int i = ROWS - 1; i >= 0; --i) {
-                const Pair e = add2(d[i], r), g = mul2(o[i], e);
+                const Pair e = add2(dr.at(i, mine + 2 * image), r);
                 r = mul2(f[i], e);
                 if (every || i < there) {
-                    store<T, VEC>(dx + row + i * step, a.tied ? g : e);
-                    store<T, VEC>(dgate + row + i * step, mul2(mul2(g, f[i]), before[i]));
+                    store<T, VEC>(dx + row + i * step, tied ? mul2(o[i], e) : e);
+                    store<T, VEC>(dgate + row + i * step, mul2(w[i], e));
                 }
             }
         };
-        if (there >= ROWS) go(true);
-        else go(false);
-        if (there < ROWS) {
+        if (there >= ROWS) {
+            go(true);
+        } else {
+            go(false);
             clear<T, VEC>(dx, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
             clear<T, VEC>(dgate, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
         }
     }
+    if (ctas > 1) cluster_sync();
     if (!on) return;
     clear<T, VEC>(dx, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
     clear<T, VEC>(dgate, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
@@ -398,14 +502,18 @@ template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) 
     if (p.last) store_f32<VEC>(p.last + bc, h);
 }
 
-template <typename... P> cudaError_t launch_clusters(void (*kernel)(P...), long long clusters, int ctas, cudaStream_t s, const RecurrenceParams& p)
+template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas, size_t images, size_t totals, cudaStream_t s, const RecurrenceParams& p)
 {
+    if (const cudaError_t e = allow_smem<Kernel>(images + kMostCtas * totals); e != cudaSuccess) return e;
+    if (ctas > 8)
+        if (const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); e != cudaSuccess) return e;
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
     c.gridDim = dim3((unsigned)(clusters * ctas)), c.blockDim = dim3(kWarps * 32), c.stream = s, c.attrs = &at, c.numAttrs = ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&c, kernel, p, ctas);
+    c.dynamicSmemBytes = images + (ctas > 1 ? ctas * totals : 0);
+    return cudaLaunchKernelEx(&c, Kernel, p, ctas);
 }
 
 // CTAs of a cluster: as many as it takes to have two a SM, no more than there are runs.
@@ -418,31 +526,40 @@ int cluster_size(long long clusters, int N, int positions, int sms)
 
 constexpr int kFewRows = 8;
 
-template <typename T, int VEC> cudaError_t run_vec(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
+template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
-    constexpr int ROWS = sizeof(T) == 4 ? 8 : 16;   // forward: two arrays' rows in flight, and their gates
     const sdtw_recurrence& a = p.a;
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
-    if (backward) return launch_clusters(recurrence_bwd_kernel<T, VEC, kStep / kWarps>, clusters, cluster_size(clusters, a.N, kStep, sms), s, p);
-    if (a.N <= kFewRows) {
-        const long long threads = (long long)a.B * ((a.C + VEC - 1) / VEC);
-        if (a.N == 1) recurrence_few_kernel<T, VEC, 1><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(p);
-        else recurrence_few_kernel<T, VEC, kFewRows><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    return launch_clusters(recurrence_fwd_kernel<T, VEC, ROWS>, clusters, cluster_size(clusters, a.N, kWarps * ROWS, sms), s, p);
+    const int ctas = cluster_size(clusters, a.N, kWarps * ROWS, sms);
+    constexpr size_t image = RING ? kWarps * ROWS * 32 * VEC * sizeof(T) : 0;
+    const size_t images = (backward ? 2 * 3 : kStages * 2) * image, totals = sizeof(Run) * 2 * 32;   // of a CTA of the cluster
+    if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, RING, TIED>>(clusters, ctas, images, totals, s, p);
+    return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, RING, TIED>>(clusters, ctas, images, totals, s, p);
+}
+template <typename T, int VEC> cudaError_t run_few(const RecurrenceParams& p, cudaStream_t s)
+{
+    const long long threads = (long long)p.a.B * ((p.a.C + VEC - 1) / VEC);
+    if (p.a.N == 1) recurrence_few_kernel<T, VEC, 1><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(p);
+    else recurrence_few_kernel<T, VEC, kFewRows><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T> cudaError_t run(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
     const sdtw_recurrence& a = p.a;
-    constexpr uintptr_t mask = 2 * sizeof(T) - 1;
-    auto even = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & m) == 0; };
-    bool pairs = a.C % 2 == 0 && even(a.x, mask) && even(a.gate, mask) && even(a.state, 7);
-    for (int i = 0; i < 2; ++i) pairs = pairs && a.x_stride[i] % 2 == 0 && a.gate_stride[i] % 2 == 0;
-    pairs = pairs && (backward ? even(p.dh, mask) && even(p.dx, mask) && even(p.dgate, mask) && even(p.dlast, 7) && even(p.dstate, 7) && even(p.kept_in, 7)
-                               : even(p.h, mask) && even(p.last, 7) && even(p.kept, 7));
-    return pairs ? run_vec<T, 2>(p, backward, sms, s) : run_vec<T, 1>(p, backward, sms, s);
+    auto on = [](const void* q, uintptr_t n) { return (reinterpret_cast<uintptr_t>(q) & (n - 1)) == 0; };
+    auto strides = [&](int n) {
+        return a.C % n == 0 && a.x_stride[0] % n == 0 && a.x_stride[1] % n == 0 && a.gate_stride[0] % n == 0 && a.gate_stride[1] % n == 0;
+    };
+    constexpr int pack = 16 / sizeof(T);
+    bool pairs = strides(2) && on(a.x, 2 * sizeof(T)) && on(a.gate, 2 * sizeof(T)) && on(a.state, 8);
+    pairs = pairs && (backward ? on(p.dh, 2 * sizeof(T)) && on(p.dx, 2 * sizeof(T)) && on(p.dgate, 2 * sizeof(T)) && on(p.dlast, 8) && on(p.dstate, 8) && on(p.kept_in, 8)
+                               : on(p.h, 2 * sizeof(T)) && on(p.last, 8) && on(p.kept, 8));
+    if (!backward && a.N <= kFewRows) return pairs ? run_few<T, 2>(p, s) : run_few<T, 1>(p, s);
+    const bool ring = pairs && strides(pack) && on(a.x, 16) && on(a.gate, 16) && on(p.dh, 16);
+    if (!ring) return run_rows<T, 1, 8, false, -1>(p, backward, sms, s);
+    constexpr int ROWS = sizeof(T) == 4 ? 8 : 16;
+    return a.tied ? run_rows<T, 2, ROWS, true, 1>(p, backward, sms, s) : run_rows<T, 2, ROWS, true, 0>(p, backward, sms, s);
 }
 cudaError_t any(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
@@ -455,5 +572,14 @@ cudaError_t any(const RecurrenceParams& p, bool backward, int sms, cudaStream_t 
 
 cudaError_t launch_recurrence_forward(const RecurrenceParams& p, int sms, cudaStream_t s) { return any(p, false, sms, s); }
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, int sms, cudaStream_t s) { return any(p, true, sms, s); }
+
+cudaError_t recurrence_take_status(int* out, cudaStream_t s)
+{
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e;
+}
 
 }  // namespace sdtw

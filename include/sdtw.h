@@ -429,7 +429,7 @@ sdtw_status sdtw_groupnorm_backward(const void* dy, const void* x, const void* w
 
 /* A gated linear recurrence along the positions of x and gate (B, N, C), each channel by itself:
  *   a_t = 1 / (1 + exp(-gate_t)), h_t = a_t h_{t-1} + (1 - a_t) x_t (tied != 0) or a_t h_{t-1} + x_t (tied == 0)
- * Strides of batch and position (at most 2^26) in elements; channels are contiguous. state (B, C) fp32 contiguous is h before the first
+ * Strides of batch and position (at most 2^23) in elements; channels are contiguous. state (B, C) fp32 contiguous is h before the first
  * position, NULL: zeros. lengths (DEVICE int array (B,), clamped to [0, N]; NULL: N) makes a padded batch: positions
  * from lengths[b] on may hold anything and take no part. reverse != 0 runs from the last of an element's positions to
  * the first. States are carried in fp32. */
@@ -483,7 +483,7 @@ sdtw_status sdtw_gated_backward(const sdtw_gated* a, const void* dh, void* dx, v
                                 void* dgate_bias, void* dup_bias, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronizes `stream`, then reports (and clears) the current device's status word of the encoder
- * operators: SDTW_OK, or SDTW_ERR_TIMEOUT when a kernel on the tensor cores gave up a wait. */
+ * operators: SDTW_OK, or SDTW_ERR_TIMEOUT when a kernel gave up a wait. */
 sdtw_status sdtw_encoder_status(void* stream);
 
 #ifdef __cplusplus

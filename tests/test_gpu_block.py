@@ -639,3 +639,34 @@ def test_refusals(package):
         import torch.autograd.forward_ad as fwd
         with fwd.dual_level(), pytest.raises(NotImplementedError):
             call(fwd.make_dual(x, x))
+
+
+def test_waits_that_run_out(package):
+    """A kernel that gives up a wait leaves NaN, reports it, and the next call is right again."""
+    gen = generator(51)
+    x, gate = randn(gen, 1, 2000, 64, dtype=BF16), randn(gen, 1, 2000, 64, dtype=BF16, mean=1.0)
+    rows, w = randn(gen, 300, 64, dtype=BF16), randn(gen, 128, 64, dtype=BF16)
+    dh = randn(gen, 300, 128, dtype=BF16)
+    jobs = [lambda: package.gated_recurrence(x, gate), lambda: package.gated_linear(rows, w, w)]
+
+    def backward():
+        leaf = rows.detach().requires_grad_()
+        return torch.autograd.grad(package.gated_linear(leaf, w, w), leaf, dh)[0]
+
+    want = [f() for f in jobs] + [backward()]
+    assert package.sdtw_encoder_status() == 0
+    try:
+        for f, right in zip(jobs, want):
+            package.sdtw_debug_set_wait(0.05, 1)
+            got = f()
+            assert package.sdtw_encoder_status() == 7 and torch.isnan(got).any()
+            assert package.sdtw_encoder_status() == 0
+            assert torch.equal(f(), right)
+        leaf = rows.detach().requires_grad_()
+        h = package.gated_linear(leaf, w, w)
+        package.sdtw_debug_set_wait(0.05, 1)
+        (got,) = torch.autograd.grad(h, leaf, dh)
+        assert package.sdtw_encoder_status() == 7 and torch.isnan(got).all()
+    finally:
+        package.sdtw_debug_set_wait(0.0, 0)
+    assert torch.equal(backward(), want[2])
