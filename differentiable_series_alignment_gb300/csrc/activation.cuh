@@ -3,12 +3,19 @@
 #include "common.cuh"
 #include "encoder.h"
 
+#include <type_traits>
+
 namespace sdtw {
 
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 // 1 / (1 + exp(-z)). EXACT, for results of 32 bits, takes expf: ex2 alone makes the rounding of its argument, up to
 // |z| 2^-24, a relative error of the exponential; 16 bits do not show it.
 template <bool EXACT> __device__ __forceinline__ float sigmoid(float z) {
-    return __fdividef(1.f, 1.f + (EXACT ? expf(-z) : ex2(-1.4426950408889634f * z)));
+    return reciprocal(1.f + (EXACT ? expf(-z) : ex2(-1.4426950408889634f * z)));
 }
 
 // act(z), and with SLOPE its derivative.
@@ -35,7 +42,7 @@ template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ float acti
 }
 
 // f(std::integral_constant<int, activation>)
-template <typename F> auto with_activation(int activation, F f) {
+template <typename F> __host__ __device__ __forceinline__ auto with_activation(int activation, F f) {
     switch (activation) {
         case SDTW_ACT_SILU: return f(std::integral_constant<int, SDTW_ACT_SILU>());
         case SDTW_ACT_GELU: return f(std::integral_constant<int, SDTW_ACT_GELU>());

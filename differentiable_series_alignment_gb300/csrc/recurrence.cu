@@ -81,11 +81,6 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
 // a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. EXACT, for
 // results of 32 bits: a is 0 and b 1 from e = 2^120 on; otherwise e ends at 2^126, which 16 bits of either do not show. A
 // NaN stays.
-__device__ __forceinline__ float reciprocal(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 __device__ __forceinline__ float min_nan(float v, float most) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
