@@ -2,6 +2,7 @@
 #pragma once
 #include "common.cuh"
 #include "encoder.h"
+#include "packed.cuh"
 
 #include <type_traits>
 
@@ -38,6 +39,26 @@ template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ float acti
     } else {
         if (SLOPE) slope = 1.f;
         return z;
+    }
+}
+
+// Two values at a time: act of z, or its derivative.
+template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ Pair activate2(Pair z) {
+    float x, y, slope;
+    if constexpr (ACT == SDTW_ACT_NONE) {
+        return SLOPE ? pk2(1.f, 1.f) : z;
+    } else if constexpr (ACT == SDTW_ACT_SILU && !EXACT) {
+        upk2(mul2(z, pk2(-1.4426950408889634f, -1.4426950408889634f)), x, y);
+        upk2(add2(pk2(ex2(x), ex2(y)), pk2(1.f, 1.f)), x, y);
+        const Pair s = pk2(reciprocal(x), reciprocal(y)), v = mul2(z, s);
+        return SLOPE ? fma2(v, sub2(pk2(1.f, 1.f), s), s) : v;
+    } else {
+        upk2(z, x, y);
+        const float u = activate<ACT, EXACT, SLOPE>(x, slope);
+        x = SLOPE ? slope : u;
+        const float v = activate<ACT, EXACT, SLOPE>(y, slope);
+        y = SLOPE ? slope : v;
+        return pk2(x, y);
     }
 }
 

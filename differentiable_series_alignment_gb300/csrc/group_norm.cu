@@ -42,15 +42,11 @@ template <bool EXACT, bool SLOPE> __device__ __forceinline__ float activate_as(i
         default: return activate<SDTW_ACT_NONE, EXACT, SLOPE>(z, slope);
     }
 }
-// v[e] = activation of v[e], or its derivative
-template <bool EXACT, bool SLOPE, int VEC> __device__ __forceinline__ void activate_all(int activation, float (&v)[VEC]) {
+// z = activation of z, or its derivative
+template <bool EXACT, bool SLOPE, int Q> __device__ __forceinline__ void activate_all(int activation, Pair (&z)[Q]) {
     auto each = [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float slope;
-            const float y = activate<act(), EXACT, SLOPE>(v[e], slope);
-            v[e] = SLOPE ? slope : y;
-        }
+        for (int q = 0; q < Q; ++q) z[q] = activate2<act(), EXACT, SLOPE>(z[q]);
     };
     switch (activation) {
         case SDTW_ACT_SILU: each(std::integral_constant<int, SDTW_ACT_SILU>()); break;
@@ -65,6 +61,7 @@ template <bool EXACT, bool SLOPE, int VEC> __device__ __forceinline__ void activ
 // clusters.
 struct Layout {
     bool fits;               // else the kernels of any size take it
+    bool small;              // groups within a warp: lanes of a group, packs of a lane (items)
     bool held;               // in shared memory
     int vec, width, packs;   // elements of a pack; channels and packs of a slab
     int slabs, items, lanes, rounds;   // rounds: rows of a thread
@@ -84,57 +81,75 @@ __device__ __forceinline__ void store_remote(const float* mine, int cta, float v
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
-// Sums of the CTA's (and the cluster's) groups. `v` are a thread's sums of its channels, red holds those of all threads, one
-// row of threads after the other; a warp adds up a group, then the CTAs' sums of it are exchanged. Every thread finds the sum of
-// group `g` of its item in sums[item * groups + g]. `parts`: [ctas][items * groups], of this call alone.
-template <int VEC>
-__device__ __forceinline__ void group_sums(const float (&v)[VEC], float* red, float* parts, float* sums, const Layout& L, int cg, int rank)
+// Sums of the CTA's (and the cluster's) groups, NV of them side by side. `v` are a thread's sums of its channels; where a pack lies
+// within a group they are one. red holds those of all threads, one row of threads after the other; a warp adds up a
+// group, then the CTAs' sums of it are exchanged. parts: [ctas][NV][items * groups], of this call alone. What becomes of a group's
+// sum is done once, by the thread that calls finish(which, item * groups + group, sum).
+template <int VEC, int NV, typename F>
+__device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], float* red, float* parts, const Layout& L, int cg, int rank, F finish)
 {
     const int groups = L.width / cg, all = L.items * groups, rows = L.lanes, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)threadIdx.x < L.items * rows * L.packs) {
+    const bool within = cg % VEC == 0;
+    const int across = within ? L.packs : L.width, n = within ? cg / VEC : cg;   // entries of a row, of a group's row
+    const bool mine = (int)threadIdx.x < L.items * rows * L.packs;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) red[threadIdx.x * VEC + e] = v[e];
+    for (int w = 0; w < NV; ++w) {
+        float* to = red + w * kThreads * VEC;
+        if (mine && within) {
+            Pair t = v[w][0];
+#pragma unroll
+            for (int q = 1; q < kPairs<VEC>; ++q) t = add2(t, v[w][q]);
+            to[threadIdx.x] = both(t);
+        } else if (mine) {
+#pragma unroll
+            for (int q = 0; q < kPairs<VEC>; ++q) {
+                float x, y;
+                upk2(v[w][q], x, y);
+                to[threadIdx.x * VEC + 2 * q] = x;
+                if (VEC > 1) to[threadIdx.x * VEC + 2 * q + 1] = y;
+            }
+        }
     }
     __syncthreads();
-    const int n = rows * cg;
-    for (int k = warp; k < all; k += kWarpsG) {
-        const float* first = red + k / groups * rows * L.width + k % groups * cg;
+    const int side = n < 32 ? 32 / n : 1;                   // rows of a group that a warp has side by side
+    const int r0 = n < 32 ? lane / n : 0, c0 = n < 32 ? lane % n : lane;
+    for (int k = warp; k < NV * all; k += kWarpsG) {
+        const int w = NV > 1 && k >= all ? 1 : 0, j = k - w * all, item = L.items > 1 ? j / groups : 0;
+        const float* first = red + w * kThreads * VEC + item * rows * across + (j - item * groups) * n;
         float s = 0.f;
-        for (int i = lane; i < n; i += 32) s += first[i / cg * L.width + i % cg];
+        if (r0 < side)
+            for (int r = r0; r < rows; r += side)
+                for (int c = c0; c < n; c += 32) s += first[r * across + c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (L.ctas == 1) {
-            if (lane == 0) sums[k] = s;
+            if (lane == 0) finish(w, j, s);
         } else if (lane < L.ctas) {
-            store_remote(parts + rank * all + k, lane, s);
+            store_remote(parts + rank * NV * all + k, lane, s);
         }
     }
     if (L.ctas > 1) {
         cluster_sync_g();
-        for (int k = threadIdx.x; k < all; k += kThreads) {
+        for (int k = threadIdx.x; k < NV * all; k += kThreads) {
             float s = 0.f;
-            for (int c = 0; c < L.ctas; ++c) s += parts[c * all + k];
-            sums[k] = s;
+            for (int c = 0; c < L.ctas; ++c) s += parts[c * NV * all + k];
+            finish(NV > 1 && k >= all ? 1 : 0, NV > 1 && k >= all ? k - all : k, s);
         }
     }
     __syncthreads();
 }
-
-template <typename T, int VEC> __device__ __forceinline__ void unpack(const Pack<T, VEC>& p, float (&v)[VEC]) {
+// A thread's channels' entries of a group's [groups]
+template <int VEC> __device__ __forceinline__ void of_channels(const float* from, int c0, int cg, Pair (&v)[kPairs<VEC>]) {
+    if (cg % VEC == 0) {
+        const float x = from[c0 / cg];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = to_f32(p.e[e]);
-}
-template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> packed_of(const float (&v)[VEC]) {
-    Pack<T, VEC> p;
-    if constexpr (VEC > 1 && sizeof(T) == 2) {
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) *reinterpret_cast<uint32_t*>(&p.e[e]) = pack2<T>(v[e], v[e + 1]);
+        for (int q = 0; q < kPairs<VEC>; ++q) v[q] = pk2(x, x);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) p.e[e] = from_f32<T>(v[e]);
+        for (int q = 0; q < kPairs<VEC>; ++q) v[q] = pk2(from[(c0 + 2 * q) / cg], VEC > 1 ? from[(c0 + 2 * q + 1) / cg] : 0.f);
     }
-    return p;
 }
+
 __device__ __forceinline__ void fetch16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
@@ -158,164 +173,212 @@ struct Place {
     }
 };
 
-template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThreads, 2) group_fwd_kernel(const GroupNormParams p, const Layout L)
+// The slab's weights in shared memory, as fp32: [width] of either
+__device__ __forceinline__ void take_weights(float* to, const GroupNormParams& p, const Layout& L, int slab) {
+    for (int c = threadIdx.x; c < L.width; c += kThreads) {
+        to[c] = wval(p.weight, slab * L.width + c, p.wdtype, 1.f);
+        to[L.width + c] = wval(p.bias, slab * L.width + c, p.wdtype, 0.f);
+    }
+}
+// VEC weights, all on their way at once
+template <int VEC> __device__ __forceinline__ void read_weights(const void* p, int c, int wdtype, float none, float (&v)[VEC]) {
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = none;
+    } else if (wdtype == SDTW_F32) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = static_cast<const float*>(p)[c + e];
+    } else if (wdtype == SDTW_BF16) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = to_f32(static_cast<const __nv_bfloat16*>(p)[c + e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = to_f32(static_cast<const __half*>(p)[c + e]);
+    }
+}
+__device__ __forceinline__ float length_of(const GroupNormParams& p, int b) {
+    return (float)(b >= p.B ? 0 : p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S);
+}
+template <int VEC> __device__ __forceinline__ void read_floats(const float* from, Pair (&v)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) v[q] = VEC > 1 ? *reinterpret_cast<const Pair*>(from + 2 * q) : pk2(from[0], 0.f);
+}
+
+template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThreads, 3) group_fwd_kernel(const GroupNormParams p, const Layout L)
 {
-    extern __shared__ __align__(16) unsigned char held[];   // [rounds][kThreads] packs, then the sums
+    extern __shared__ __align__(16) unsigned char held[];   // [rounds][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
+    constexpr int Q = kPairs<VEC>;
     const int slab = blockIdx.x / L.ctas % L.slabs, rank = blockIdx.x % L.ctas, groups = L.width / p.cg, all = L.items * groups;
-    float* red = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * kThreads * 16 : 0));
-    float* sums = red + kThreads * VEC;                     // of values, of squares
-    float* parts = sums + 2 * all;                          // likewise
+    float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * kThreads * 16 : 0));
+    float* red = weights + 2 * L.width;
+    float* stats = red + kThreads * VEC;                    // mean, 1 / deviation
+    float* parts = stats + 2 * all;
     const T* x = static_cast<const T*>(p.x);
     T* y = static_cast<T*>(p.y);
-    float w[VEC], bias[VEC];
-    int group[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        const int c = threadIdx.x % L.packs * VEC + e;
-        group[e] = c / p.cg;
-        w[e] = wval(p.weight, slab * L.width + c, p.wdtype, 1.f);
-        bias[e] = wval(p.bias, slab * L.width + c, p.wdtype, 0.f);
-    }
+    take_weights(weights, p, L, slab);
     if (L.ctas > 1) cluster_sync_g();                       // the others have begun
     const long long step = (long long)L.lanes * p.C;
+    const int c0 = threadIdx.x % L.packs * VEC;
     for (int b0 = blockIdx.x / (L.ctas * L.slabs) * L.items; b0 < p.B; b0 += L.columns * L.items) {
         const Place at(p, L, slab, b0, rank);
         const int there = min(at.last, at.len);             // rows that take part
         P* mine = reinterpret_cast<P*>(held) + threadIdx.x;
-        auto value = [&](int k) { return HELD ? mine[k * kThreads] : *reinterpret_cast<const P*>(x + at.at + k * step); };
+        const T* src = x + at.at;
+        auto value = [&](int k) { return HELD ? mine[k * kThreads] : *reinterpret_cast<const P*>(src + k * step); };
         if constexpr (HELD) {
-            for (int k = 0, s = at.first; s < there; ++k, s += L.lanes) fetch16(mine + k * kThreads, x + at.at + k * step);
+            const T* q = src;
+            P* to = mine;
+#pragma unroll 4
+            for (int s = at.first; s < there; s += L.lanes, q += step, to += kThreads) fetch16(to, q);
             fetched();
         }
-        float s[VEC] = {};
+        Pair s[1][Q], mu[Q], rw[Q], bias[Q], d[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[0][q] = mu[q] = pk2(0.f, 0.f);
+#pragma unroll 2
         for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            float v[VEC];
-            unpack<T, VEC>(value(k), v);
+            minus<T, VEC>(value(k), mu, d);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[e] += v[e];
+            for (int q = 0; q < Q; ++q) s[0][q] = add2(s[0][q], d[q]);
         }
-        group_sums<VEC>(s, red, parts, sums, L, p.cg, rank);
-        const float n = (float)at.len * (float)p.cg, inv = at.len ? 1.f / n : 0.f;
-        float mu[VEC], rw[VEC];
-        const int g0 = at.item < L.items ? at.item * groups : 0;
+        auto count = [&](int k) { return length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg; };
+        group_sums<VEC, 1>(s, red, parts, L, p.cg, rank, [&](int, int k, float sum) { stats[k] = count(k) > 0.f ? sum / count(k) : 0.f; });
+        const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
+        of_channels<VEC>(mine_stats, c0, p.cg, mu);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) mu[e] = sums[g0 + group[e]] * inv, s[e] = 0.f;
+        for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
+#pragma unroll 2
         for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            float v[VEC];
-            unpack<T, VEC>(value(k), v);
+            minus<T, VEC>(value(k), mu, d);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[e] = fmaf(v[e] - mu[e], v[e] - mu[e], s[e]);
+            for (int q = 0; q < Q; ++q) s[0][q] = fma2(d[q], d[q], s[0][q]);
         }
-        group_sums<VEC>(s, red, parts + L.ctas * all, sums + all, L, p.cg, rank);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float r = at.len ? 1.f / sqrtf(sums[all + g0 + group[e]] * inv + p.eps) : 0.f;
-            if (p.mean && rank == 0 && at.on && at.row == 0 && (at.pack * VEC + e) % p.cg == 0) {
-                const long long to = (long long)at.b * p.G + slab * groups + group[e];
-                p.mean[to] = mu[e], p.rstd[to] = r;
+        group_sums<VEC, 1>(s, red, parts + L.ctas * all, L, p.cg, rank, [&](int, int k, float sum) {
+            const float r = count(k) > 0.f ? 1.f / sqrtf(sum / count(k) + p.eps) : 0.f;
+            stats[all + k] = r;
+            if (p.mean && rank == 0 && b0 + k / groups < p.B) {
+                const long long to = (long long)(b0 + k / groups) * p.G + slab * groups + k % groups;
+                p.mean[to] = stats[k], p.rstd[to] = r;
             }
-            rw[e] = r * w[e];
-        }
-        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes) {
-            float v[VEC] = {};
+        });
+        read_floats<VEC>(weights + c0, rw);
+        read_floats<VEC>(weights + L.width + c0, bias);
+        of_channels<VEC>(mine_stats + all, c0, p.cg, d);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], d[q]);
+        T* dst = y + at.at;
+        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes, dst += step) {
             if (i < there) {
-                unpack<T, VEC>(value(k), v);
+                minus<T, VEC>(value(k), mu, d);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = fmaf(v[e] - mu[e], rw[e], bias[e]);
-                activate_all<sizeof(T) == 4, false, VEC>(p.activation, v);
+                for (int q = 0; q < Q; ++q) d[q] = fma2(d[q], rw[q], bias[q]);
+                activate_all<sizeof(T) == 4, false, Q>(p.activation, d);
+            } else {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) d[q] = pk2(0.f, 0.f);
             }
-            *reinterpret_cast<P*>(y + at.at + k * step) = packed_of<T, VEC>(v);
+            *reinterpret_cast<P*>(dst) = rounded<T, VEC>(d);
         }
     }
 }
 
 template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThreads, 2) group_bwd_kernel(const GroupNormParams p, const Layout L)
 {
-    extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the sums
+    extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
+    constexpr int Q = kPairs<VEC>;
     const int slab = blockIdx.x / L.ctas % L.slabs, rank = blockIdx.x % L.ctas, groups = L.width / p.cg, all = L.items * groups;
     const int column = blockIdx.x / (L.ctas * L.slabs);
-    float* red = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
-    float* sums = red + kThreads * VEC;
-    float* parts = sums + 2 * all;
+    float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
+    float* red = weights + 2 * L.width;
+    float* stats = red + 2 * kThreads * VEC;                // mean g, mean g xh
+    float* parts = stats + 2 * all;
     const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
     T* dx = static_cast<T*>(p.dx);
-    float w[VEC], bias[VEC], dw[VEC] = {}, db[VEC] = {};
-    int group[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        const int c = threadIdx.x % L.packs * VEC + e;
-        group[e] = c / p.cg;
-        w[e] = wval(p.weight, slab * L.width + c, p.wdtype, 1.f);
-        bias[e] = wval(p.bias, slab * L.width + c, p.wdtype, 0.f);
-    }
+    take_weights(weights, p, L, slab);
     if (L.ctas > 1) cluster_sync_g();
+    else __syncthreads();
     const long long step = (long long)L.lanes * p.C;
+    const int c0 = threadIdx.x % L.packs * VEC;
+    Pair w[Q], bias[Q], sum[2][Q];                          // of the weights' gradients
+    const Pair none[Q] = {};
+    read_floats<VEC>(weights + c0, w);
+    read_floats<VEC>(weights + L.width + c0, bias);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) sum[0][q] = sum[1][q] = pk2(0.f, 0.f);
     int turn = 0;
     for (int b0 = column * L.items; b0 < p.B; b0 += L.columns * L.items, turn ^= 1) {
         const Place at(p, L, slab, b0, rank);
         const int there = min(at.last, at.len);
         P* mine = reinterpret_cast<P*>(held) + threadIdx.x;
+        const T *sx = x + at.at, *sd = dy + at.at;
         auto value = [&](int k, int which) {
-            return HELD ? mine[(2 * k + which) * kThreads] : *reinterpret_cast<const P*>((which ? dy : x) + at.at + k * step);
+            return HELD ? mine[(2 * k + which) * kThreads] : *reinterpret_cast<const P*>((which ? sd : sx) + k * step);
         };
-        if constexpr (HELD)
-            for (int k = 0, s = at.first; s < there; ++k, s += L.lanes) {
-                fetch16(mine + 2 * k * kThreads, x + at.at + k * step);
-                fetch16(mine + (2 * k + 1) * kThreads, dy + at.at + k * step);
+        if constexpr (HELD) {
+            const T *q = sx, *d = sd;
+            P* to = mine;
+#pragma unroll 4
+            for (int s = at.first; s < there; s += L.lanes, q += step, d += step, to += 2 * kThreads) {
+                fetch16(to, q);
+                fetch16(to + kThreads, d);
             }
-        float mu[VEC], r[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const long long from = (long long)(at.on ? at.b : 0) * p.G + slab * groups + group[e];
-            mu[e] = p.mean[from], r[e] = p.rstd[from];
         }
+        Pair mu[Q], r[Q], s[2][Q];
+        const long long from = (long long)(at.on ? at.b : 0) * p.G + slab * groups;
+        of_channels<VEC>(p.mean + from, c0, p.cg, mu);
+        of_channels<VEC>(p.rstd + from, c0, p.cg, r);
         if constexpr (HELD) fetched();
         // xh and dz of a pack
-        auto both = [&](int k, float (&xh)[VEC], float (&dz)[VEC]) {
-            float z[VEC];
-            unpack<T, VEC>(value(k, 0), xh);
-            unpack<T, VEC>(value(k, 1), dz);
+        auto values = [&](int k, Pair (&xh)[Q], Pair (&dz)[Q]) {
+            Pair z[Q];
+            minus<T, VEC>(value(k, 0), mu, xh);
+            minus<T, VEC>(value(k, 1), none, dz);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                xh[e] = (xh[e] - mu[e]) * r[e];
-                z[e] = fmaf(xh[e], w[e], bias[e]);
+            for (int q = 0; q < Q; ++q) {
+                xh[q] = mul2(xh[q], r[q]);
+                z[q] = fma2(xh[q], w[q], bias[q]);
             }
-            activate_all<sizeof(T) == 4, true, VEC>(p.activation, z);
+            activate_all<sizeof(T) == 4, true, Q>(p.activation, z);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) dz[e] *= z[e];
+            for (int q = 0; q < Q; ++q) dz[q] = mul2(dz[q], z[q]);
         };
-        float s1[VEC] = {}, s2[VEC] = {};
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = pk2(0.f, 0.f);
         for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            float xh[VEC], dz[VEC];
-            both(k, xh, dz);
+            Pair xh[Q], dz[Q];
+            values(k, xh, dz);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                s1[e] += dz[e];
-                s2[e] = fmaf(dz[e], xh[e], s2[e]);
+            for (int q = 0; q < Q; ++q) {
+                s[0][q] = add2(s[0][q], dz[q]);
+                s[1][q] = fma2(dz[q], xh[q], s[1][q]);
             }
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            db[e] += s1[e], dw[e] += s2[e];
-            s1[e] *= w[e], s2[e] *= w[e];
-        }
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sum[k][q] = add2(sum[k][q], s[k][q]), s[k][q] = mul2(s[k][q], w[q]);
         if (!dx) continue;
-        group_sums<VEC>(s1, red, parts + 2 * turn * L.ctas * all, sums, L, p.cg, rank);
-        group_sums<VEC>(s2, red, parts + (2 * turn + 1) * L.ctas * all, sums + all, L, p.cg, rank);
-        const float inv = at.len ? 1.f / ((float)at.len * (float)p.cg) : 0.f;
-        const int g0 = at.item < L.items ? at.item * groups : 0;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s1[e] = sums[g0 + group[e]] * inv, s2[e] = sums[all + g0 + group[e]] * inv;
-        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes) {
-            float xh[VEC], dz[VEC] = {};
+        group_sums<VEC, 2>(s, red, parts + 2 * turn * L.ctas * all, L, p.cg, rank, [&](int which, int k, float t) {
+            const float n = length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg;
+            stats[which * all + k] = n > 0.f ? t / n : 0.f;
+        });
+        const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
+        of_channels<VEC>(mine_stats, c0, p.cg, s[0]);
+        of_channels<VEC>(mine_stats + all, c0, p.cg, s[1]);
+        T* dst = dx + at.at;
+        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes, dst += step) {
+            Pair xh[Q], dz[Q];
             if (i < there) {
-                both(k, xh, dz);
+                values(k, xh, dz);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) dz[e] = r[e] * (fmaf(dz[e], w[e], -s1[e]) - xh[e] * s2[e]);
+                for (int q = 0; q < Q; ++q) dz[q] = mul2(r[q], sub2(sub2(mul2(dz[q], w[q]), s[0][q]), mul2(xh[q], s[1][q])));
+            } else {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dz[q] = pk2(0.f, 0.f);
             }
-            *reinterpret_cast<P*>(dx + at.at + k * step) = packed_of<T, VEC>(dz);
+            *reinterpret_cast<P*>(dst) = rounded<T, VEC>(dz);
         }
     }
     if (!p.partial) return;
@@ -323,7 +386,12 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     for (int which = 0; which < 2; ++which) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) red[threadIdx.x * VEC + e] = which ? db[e] : dw[e];
+        for (int q = 0; q < Q; ++q) {
+            float u, v;
+            upk2(sum[1 - which][q], u, v);
+            red[threadIdx.x * VEC + 2 * q] = u;
+            if (VEC > 1) red[threadIdx.x * VEC + 2 * q + 1] = v;
+        }
         __syncthreads();
         float* out = p.partial + (((long long)column * L.ctas + rank) * 2 + which) * p.C + slab * L.width;
         for (int c = threadIdx.x; c < L.width; c += kThreads) {
@@ -331,6 +399,153 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
             for (int k = 0; k < L.items * L.lanes; ++k) s += red[k * L.width + c];
             out[c] = s;
         }
+    }
+}
+
+// ---- groups of a few positions (normalising row by row): a group is `lanes` lanes of a warp, at most two packs each, whose
+// sums need no barrier. A thread's group and channels stay the same over the batch elements that it takes, every
+// columns-th; the next one's packs are on their way meanwhile.
+__device__ __forceinline__ float lane_sum(float v, int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+constexpr int kSmallPacks = 2;
+
+template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds__(kThreads, (BWD ? 2 : 4) / K) group_small_kernel(const GroupNormParams p, const Layout L)
+{
+    using P = Pack<T, VEC>;
+    constexpr int Q = kPairs<VEC>;
+    const Pair none[Q] = {};
+    const long long id = ((long long)blockIdx.x * kThreads + threadIdx.x) / L.lanes;
+    const int lane = threadIdx.x % L.lanes, g = (int)(id % p.G), per = p.cg / VEC, packs = p.S * per;
+    const long long column = id / p.G, end = column < L.columns ? p.B : 0;   // the last CTA's threads may be too many
+    const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
+    T* out = static_cast<T*>(BWD ? p.dx : p.y);
+    int row[K], c[K];
+    Pair w[K][Q], bias[K][Q], dw[K][Q] = {}, db[K][Q] = {};
+    bool has[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int q = lane + k * L.lanes;
+        has[k] = q < packs;
+        row[k] = has[k] ? q / per : 0;
+        c[k] = g * p.cg + (has[k] ? q % per * VEC : 0);
+        float t[VEC];
+        read_weights<VEC>(p.weight, c[k], p.wdtype, 1.f, t);
+        pairs_of<VEC>(t, w[k]);
+        read_weights<VEC>(p.bias, c[k], p.wdtype, 0.f, t);
+        pairs_of<VEC>(t, bias[k]);
+    }
+    auto length = [&](long long b) { return b < end ? p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S : 0; };
+    uint4 xv[K], dv[K];   // not looked into before they are needed
+    float mean = 0.f, rstd = 0.f;
+    auto get = [&](long long b, int len) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (has[k] && row[k] < len) {
+                const long long at = (b * p.S + row[k]) * p.C + c[k];
+                xv[k] = *reinterpret_cast<const uint4*>(x + at);
+                if (BWD) dv[k] = *reinterpret_cast<const uint4*>(dy + at);
+            }
+        if (BWD && len > 0) mean = p.mean[b * p.G + g], rstd = p.rstd[b * p.G + g];
+    };
+    int len = length(column);
+    get(column, len);
+    // every lane of a warp makes the same number of rounds: the sums are collective
+    const long long most = (p.B + L.columns - 1) / L.columns;
+    for (long long turn = 0; turn < most; ++turn) {
+        const long long b = column + turn * L.columns;
+        Pair v[K][Q], d[K][Q], s1 = pk2(0.f, 0.f), s2 = s1;
+        bool in[K];
+        const float n = (float)len * (float)p.cg, inv = len ? 1.f / n : 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            in[k] = has[k] && row[k] < len;
+            if (in[k]) {
+                minus<T, VEC>(reinterpret_cast<const P&>(xv[k]), none, v[k]);
+                if (BWD) minus<T, VEC>(reinterpret_cast<const P&>(dv[k]), none, d[k]);
+            }
+        }
+        float mu = mean, r = rstd;
+        const int next = turn + 1 < most ? length(b + L.columns) : 0;
+        get(b + L.columns, next);
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in[k]) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) s1 = add2(s1, v[k][q]);
+                }
+            mu = lane_sum(both(s1), L.lanes) * inv;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in[k]) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        v[k][q] = sub2(v[k][q], pk2(mu, mu));
+                        s2 = fma2(v[k][q], v[k][q], s2);
+                    }
+                }
+            r = len ? 1.f / sqrtf(lane_sum(both(s2), L.lanes) * inv + p.eps) : 0.f;
+            if (p.mean && lane == 0 && b < end) p.mean[b * p.G + g] = mu, p.rstd[b * p.G + g] = r;
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (in[k]) {
+                    Pair z[Q];
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        v[k][q] = mul2(sub2(v[k][q], pk2(mu, mu)), pk2(r, r));
+                        z[q] = fma2(v[k][q], w[k][q], bias[k][q]);
+                    }
+                    activate_all<sizeof(T) == 4, true, Q>(p.activation, z);
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        d[k][q] = mul2(d[k][q], z[q]);
+                        db[k][q] = add2(db[k][q], d[k][q]);
+                        dw[k][q] = fma2(d[k][q], v[k][q], dw[k][q]);
+                        d[k][q] = mul2(d[k][q], w[k][q]);
+                        s1 = add2(s1, d[k][q]);
+                        s2 = fma2(d[k][q], v[k][q], s2);
+                    }
+                }
+            const float m1 = lane_sum(both(s1), L.lanes) * inv, m2 = lane_sum(both(s2), L.lanes) * inv;
+            s1 = pk2(m1, m1), s2 = pk2(m2, m2);
+        }
+        if (out && b < end) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (has[k]) {
+                    if (!in[k]) {
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) v[k][q] = pk2(0.f, 0.f);
+                    } else if constexpr (BWD) {
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) v[k][q] = mul2(pk2(r, r), sub2(sub2(d[k][q], s1), mul2(v[k][q], s2)));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) v[k][q] = fma2(mul2(v[k][q], pk2(r, r)), w[k][q], bias[k][q]);
+                        activate_all<sizeof(T) == 4, false, Q>(p.activation, v[k]);
+                    }
+                    *reinterpret_cast<P*>(out + (b * p.S + row[k]) * p.C + c[k]) = rounded<T, VEC>(v[k]);
+                }
+        }
+        len = next;
+    }
+    if (BWD && p.partial && column < L.columns) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (has[k]) {
+                float* to = p.partial + 2 * (column * p.S + row[k]) * p.C + c[k];
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    float u, v;
+                    upk2(dw[k][q], u, v);
+                    to[2 * q] = u, to[2 * q + 1] = v;
+                    upk2(db[k][q], u, v);
+                    to[p.C + 2 * q] = u, to[p.C + 2 * q + 1] = v;
+                }
+            }
     }
 }
 
@@ -427,17 +642,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads) group_bwd_any_
 }
 
 // dw, db: the partial rows added in a fixed order, 32 columns by 32 row lanes
-__global__ void __launch_bounds__(1024) group_fold_kernel(const GroupNormParams p, int rows)
+__global__ void __launch_bounds__(1024) group_fold_kernel(const GroupNormParams p, long long rows)
 {
     __shared__ float part[32][33];
     after_previous();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     float s[4] = {};
     if (c < p.C)
-        for (int t = lane; t < rows; t += 128) {
+        for (long long t = lane; t < rows; t += 128) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (t + 32 * q < rows) s[q] += p.partial[(2ll * (t + 32 * q) + blockIdx.y) * p.C + c];
+                if (t + 32 * q < rows) s[q] += p.partial[(2 * (t + 32 * q) + blockIdx.y) * p.C + c];
         }
     part[lane][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
@@ -463,6 +678,17 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     Layout L{};
     const int size = dtype_size(p.dtype);
     L.vec = packs && p.C % (16 / size) == 0 ? 16 / size : 1;
+    if (L.vec > 1 && p.cg % L.vec == 0 && (long long)p.S * (p.cg / L.vec) <= 32 * kSmallPacks) {
+        const int packs = p.S * (p.cg / L.vec);
+        L.small = L.fits = true;
+        L.lanes = 1;
+        while (L.lanes < 32 && L.lanes < packs) L.lanes *= 2;
+        L.items = packs > 32 ? 2 : 1;
+        // as many columns as fill the SMs
+        const long long most = std::max(1ll, (long long)sms * (backward ? 2 : 4) / L.items * kThreads / L.lanes / p.G);
+        L.columns = (int)std::min<long long>(most, p.B);
+        return L;
+    }
     const long long whole = p.cg / gcd(p.cg, L.vec) * L.vec;    // channels of whole groups and whole packs
     L.width = (int)whole;
     // at least 128 bytes a row, or all channels
@@ -482,7 +708,7 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     // few items are spread over the SMs
     while (L.items > 1 && (long long)((p.B + L.items - 1) / L.items) * L.slabs < sms) L.items = (L.items + 1) / 2;
     const int arrays = backward ? 2 : 1;
-    const size_t sums = ((size_t)kThreads * L.vec + 2 * L.items * (L.width / p.cg)) * sizeof(float);
+    const size_t sums = (2 * (size_t)L.width + (size_t)arrays * kThreads * L.vec + 2 * L.items * (L.width / p.cg)) * sizeof(float);
     auto bytes = [&](int ctas) {
         const size_t exchange = ctas > 1 ? (size_t)4 * ctas * (L.width / p.cg) * sizeof(float) : 0;
         const long long rounds = ((p.S + ctas - 1) / ctas + L.lanes - 1) / L.lanes;
@@ -520,15 +746,22 @@ template <auto Kernel> cudaError_t launch(const GroupNormParams& p, const Layout
 }
 
 bool packs(const GroupNormParams& p) { return aligned16(p.x) && aligned16(p.y) && aligned16(p.dy) && aligned16(p.dx); }
-int partial_rows(const GroupNormParams& p, const Layout& L) { return L.fits ? L.columns * L.ctas : p.B; }
+long long partial_rows(const GroupNormParams& p, const Layout& L) { return L.small ? (long long)L.columns * p.S : L.fits ? L.columns * L.ctas : p.B; }
+template <typename T, int VEC, bool BWD> cudaError_t run_small(const GroupNormParams& p, const Layout& L, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(((long long)L.columns * p.G * L.lanes + kThreads - 1) / kThreads);
+    if (L.items == 1) group_small_kernel<T, VEC, 1, BWD><<<grid, kThreads, 0, s>>>(p, L);
+    else group_small_kernel<T, VEC, 2, BWD><<<grid, kThreads, 0, s>>>(p, L);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
 size_t group_norm_workspace(const GroupNormParams& p, bool backward, int sms)
 {
     if (!backward) return 0;
-    const size_t rows = std::max(partial_rows(p, layout(p, true, true, sms)), partial_rows(p, layout(p, true, false, sms)));
-    return sizeof(float) * 2 * rows * p.C;
+    const long long rows = std::max(partial_rows(p, layout(p, true, true, sms)), partial_rows(p, layout(p, true, false, sms)));
+    return sizeof(float) * 2 * (size_t)rows * p.C;
 }
 
 cudaError_t launch_group_norm_forward(const GroupNormParams& p, int sms, cudaStream_t s)
@@ -537,6 +770,7 @@ cudaError_t launch_group_norm_forward(const GroupNormParams& p, int sms, cudaStr
     return with_type(p.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int VEC = 16 / sizeof(T);
+        if (L.small) return run_small<T, VEC, false>(p, L, s);
         if (L.fits) return L.vec == 1 ? launch<group_fwd_kernel<T, 1, false>>(p, L, s) : L.held ? launch<group_fwd_kernel<T, VEC, true>>(p, L, s)
                                                                                               : launch<group_fwd_kernel<T, VEC, false>>(p, L, s);
         group_fwd_any_kernel<T><<<p.B * p.G, kThreads, 0, s>>>(p);
@@ -552,6 +786,7 @@ cudaError_t launch_group_norm_backward(const GroupNormParams& p0, int sms, cudaS
     const cudaError_t e = with_type(p.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int VEC = 16 / sizeof(T);
+        if (L.small) return run_small<T, VEC, true>(p, L, s);
         if (L.fits) return L.vec == 1 ? launch<group_bwd_kernel<T, 1, false>>(p, L, s) : L.held ? launch<group_bwd_kernel<T, VEC, true>>(p, L, s)
                                                                                               : launch<group_bwd_kernel<T, VEC, false>>(p, L, s);
         group_bwd_any_kernel<T><<<p.B * p.G, kThreads, 0, s>>>(p);

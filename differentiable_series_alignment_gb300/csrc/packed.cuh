@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "encoder.h"
 
 namespace sdtw {
 
@@ -45,6 +46,75 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
     unsigned long long r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// VEC elements as fp32 pairs; a lone one has a zero beside it.
+template <int VEC> constexpr int kPairs = (VEC + 1) / 2;
+using Pair = unsigned long long;
+template <int VEC> __device__ __forceinline__ void pairs_of(const float (&v)[VEC], Pair (&out)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) out[q] = pk2(v[2 * q], VEC == 1 ? 0.f : v[2 * q + 1]);
+}
+// v + c
+template <typename T, int VEC> __device__ __forceinline__ void plus(const Pack<T, VEC>& v, float c, Pair (&out)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        if constexpr (VEC == 1) {
+            out[q] = pk2(to_f32(v.e[0]) + c, 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            out[q] = add2(pk2(v.e[2 * q], v.e[2 * q + 1]), pk2(c, c));
+        } else {
+            float x = c, y = c;
+            add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+            out[q] = pk2(x, y);
+        }
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> rounded(const Pair (&v)[kPairs<VEC>]) {
+    Pack<T, VEC> o;
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        float x, y;
+        upk2(v[q], x, y);
+        if constexpr (VEC == 1) o.e[0] = from_f32<T>(x);
+        else if constexpr (sizeof(T) == 4) o.e[2 * q] = x, o.e[2 * q + 1] = y;
+        else *reinterpret_cast<uint32_t*>(&o.e[2 * q]) = pack2<T>(x, y);
+    }
+    return o;
+}
+// s + v, the even elements in one half and the odd ones in the other
+template <typename T, int VEC> __device__ __forceinline__ Pair sum_onto(Pair s, const Pack<T, VEC>& v) {
+    float x, y;
+    upk2(s, x, y);
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        if constexpr (VEC == 1) x += to_f32(v.e[0]);
+        else if constexpr (sizeof(T) == 4) x += v.e[2 * q], y += v.e[2 * q + 1];
+        else add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+    }
+    return pk2(x, y);
+}
+__device__ __forceinline__ float both(Pair v) {
+    float x, y;
+    upk2(v, x, y);
+    return x + y;
+}
+// v - m, element by element
+template <typename T, int VEC> __device__ __forceinline__ void minus(const Pack<T, VEC>& v, const Pair (&m)[kPairs<VEC>], Pair (&out)[kPairs<VEC>]) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        float x, y;
+        upk2(m[q], x, y);
+        if constexpr (VEC == 1) {
+            out[q] = pk2(to_f32(v.e[0]) - x, 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            out[q] = sub2(pk2(v.e[2 * q], v.e[2 * q + 1]), m[q]);
+        } else {
+            x = -x, y = -y;
+            add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+            out[q] = pk2(x, y);
+        }
+    }
 }
 
 }  // namespace sdtw

@@ -26,7 +26,6 @@ namespace {
 constexpr int kStep = SDTW_RECURRENCE_STEP;
 constexpr int kWarps = 8, kMostCtas = 16;   // of a CTA; of a cluster
 constexpr int kStages = 3;                  // of the forward pass's ring
-using Pair = unsigned long long;           // two channels' fp32 values
 
 __device__ __forceinline__ Pair pair(float v) { return pk2(v, v); }
 
