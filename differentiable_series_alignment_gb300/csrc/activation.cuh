@@ -26,8 +26,20 @@ template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ float acti
         if (SLOPE) slope = fmaf(z * s, 1.f - s, s);
         return z * s;
     } else if constexpr (ACT == SDTW_ACT_GELU) {
-        const float c = fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f);
-        if (SLOPE) slope = fmaf(z * 0.39894228040143268f, EXACT ? expf(-0.5f * z * z) : ex2(-0.72134752044448170f * z * z), c);
+        float c, e = 0.f;
+        if constexpr (EXACT) {
+            c = fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f);
+            if (SLOPE) e = expf(-0.5f * z * z);
+        } else {
+            // Abramowitz and Stegun 7.1.26: erfc(x) = t poly(t) exp(-x^2) to 1.5e-7, whose exponential the derivative has
+            // use for too
+            const float t = reciprocal(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.f));
+            e = ex2(-0.72134752044448170f * z * z);
+            const float half = t * e * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f), 0.5f * -0.284496736f),
+                                            0.5f * 0.254829592f);
+            c = z < 0.f ? half : 1.f - half;
+        }
+        if (SLOPE) slope = fmaf(z * 0.39894228040143268f, e, c);
         return z * c;
     } else if constexpr (ACT == SDTW_ACT_RELU) {
         if (SLOPE) slope = z > 0.f ? 1.f : 0.f;

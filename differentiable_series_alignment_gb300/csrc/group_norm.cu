@@ -59,6 +59,11 @@ template <bool EXACT, bool SLOPE, int Q> __device__ __forceinline__ void activat
 // How a call is laid over the GPU. A CTA has `items` batch elements at a time, `lanes` rows of each in flight, `packs` packs
 // to a row of its slab; thread = (item * lanes + row) * packs + pack. With several items of a few positions there are no
 // clusters.
+struct Div {                 // by multiplication, of numbers below 2^16
+    unsigned mul;
+    int by;
+};
+__device__ __forceinline__ int operator/(int n, const Div& d) { return d.by == 1 ? n : (int)__umulhi((unsigned)n, d.mul); }
 struct Layout {
     bool fits;               // else the kernels of any size take it
     bool small;              // groups within a warp: lanes of a group, packs of a lane (items)
@@ -67,12 +72,25 @@ struct Layout {
     int slabs, items, lanes, rounds;   // rounds: rows of a thread
     int ctas, part;          // CTAs of a cluster, positions of each
     int columns;             // CTAs or clusters side by side that share the items of a slab
+    int groups;              // of a slab
+    int entries, side;       // sums of a group in a row of threads; rows of them that a warp adds up side by side
+    Div by_packs, by_lanes, by_cg, by_entries;
     size_t smem;
 };
 
 __device__ __forceinline__ void cluster_sync_g() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cta_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_id() {
+    int r;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ void store_remote(const float* mine, int cta, float v) {
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine);
@@ -88,9 +106,9 @@ __device__ __forceinline__ void store_remote(const float* mine, int cta, float v
 template <int VEC, int NV, typename F>
 __device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], float* red, float* parts, const Layout& L, int cg, int rank, F finish)
 {
-    const int groups = L.width / cg, all = L.items * groups, rows = L.lanes, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = L.groups, all = L.items * groups, rows = L.lanes, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool within = cg % VEC == 0;
-    const int across = within ? L.packs : L.width, n = within ? cg / VEC : cg;   // entries of a row, of a group's row
+    const int across = within ? L.packs : L.width, n = L.entries;   // entries of a row, of a group's row
     const bool mine = (int)threadIdx.x < L.items * rows * L.packs;
 #pragma unroll
     for (int w = 0; w < NV; ++w) {
@@ -111,8 +129,8 @@ __device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], flo
         }
     }
     __syncthreads();
-    const int side = n < 32 ? 32 / n : 1;                   // rows of a group that a warp has side by side
-    const int r0 = n < 32 ? lane / n : 0, c0 = n < 32 ? lane % n : lane;
+    const int side = L.side;                                // rows of a group that a warp has side by side
+    const int r0 = n < 32 ? lane / L.by_entries : 0, c0 = lane - r0 * n;
     for (int k = warp; k < NV * all; k += kWarpsG) {
         const int w = NV > 1 && k >= all ? 1 : 0, j = k - w * all, item = L.items > 1 ? j / groups : 0;
         const float* first = red + w * kThreads * VEC + item * rows * across + (j - item * groups) * n;
@@ -139,8 +157,8 @@ __device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], flo
     __syncthreads();
 }
 // A thread's channels' entries of a group's [groups]
-template <int VEC> __device__ __forceinline__ void of_channels(const float* from, int c0, int cg, Pair (&v)[kPairs<VEC>]) {
-    if (cg % VEC == 0) {
+template <int VEC> __device__ __forceinline__ void of_channels(const float* from, int c0, const Div& cg, Pair (&v)[kPairs<VEC>]) {
+    if (cg.by % VEC == 0) {
         const float x = from[c0 / cg];
 #pragma unroll
         for (int q = 0; q < kPairs<VEC>; ++q) v[q] = pk2(x, x);
@@ -153,6 +171,9 @@ template <int VEC> __device__ __forceinline__ void of_channels(const float* from
 __device__ __forceinline__ void fetch16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void fetch4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // What a thread has of a round of items: rows [first, first + rounds * lanes) of its batch element, every lanes-th.
@@ -161,9 +182,10 @@ struct Place {
     long long at;                               // of the first, in elements
     bool on;
     __device__ __forceinline__ Place(const GroupNormParams& p, const Layout& L, int slab, int b0, int rank) {
-        pack = threadIdx.x % L.packs;
-        row = threadIdx.x / L.packs % L.lanes;
-        item = threadIdx.x / (L.packs * L.lanes);
+        const int line = (int)threadIdx.x / L.by_packs;
+        pack = threadIdx.x - line * L.packs;
+        item = line / L.by_lanes;
+        row = line - item * L.lanes;
         b = b0 + item;
         on = item < L.items && b < p.B;
         len = !on ? 0 : p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S;
@@ -209,7 +231,8 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
     constexpr int Q = kPairs<VEC>;
-    const int slab = blockIdx.x / L.ctas % L.slabs, rank = blockIdx.x % L.ctas, groups = L.width / p.cg, all = L.items * groups;
+    const int slab = blockIdx.y, rank = L.ctas > 1 ? cta_rank() : 0, column = L.ctas > 1 ? cluster_id() : blockIdx.x;
+    const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * kThreads * 16 : 0));
     float* red = weights + 2 * L.width;
     float* stats = red + kThreads * VEC;                    // mean, 1 / deviation
@@ -219,8 +242,8 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     take_weights(weights, p, L, slab);
     if (L.ctas > 1) cluster_sync_g();                       // the others have begun
     const long long step = (long long)L.lanes * p.C;
-    const int c0 = threadIdx.x % L.packs * VEC;
-    for (int b0 = blockIdx.x / (L.ctas * L.slabs) * L.items; b0 < p.B; b0 += L.columns * L.items) {
+    const int c0 = ((int)threadIdx.x - (int)threadIdx.x / L.by_packs * L.packs) * VEC;
+    for (int b0 = column * L.items; b0 < p.B; b0 += L.columns * L.items) {
         const Place at(p, L, slab, b0, rank);
         const int there = min(at.last, at.len);             // rows that take part
         P* mine = reinterpret_cast<P*>(held) + threadIdx.x;
@@ -245,7 +268,7 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         auto count = [&](int k) { return length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg; };
         group_sums<VEC, 1>(s, red, parts, L, p.cg, rank, [&](int, int k, float sum) { stats[k] = count(k) > 0.f ? sum / count(k) : 0.f; });
         const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
-        of_channels<VEC>(mine_stats, c0, p.cg, mu);
+        of_channels<VEC>(mine_stats, c0, L.by_cg, mu);
 #pragma unroll
         for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
 #pragma unroll 2
@@ -264,7 +287,7 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         });
         read_floats<VEC>(weights + c0, rw);
         read_floats<VEC>(weights + L.width + c0, bias);
-        of_channels<VEC>(mine_stats + all, c0, p.cg, d);
+        of_channels<VEC>(mine_stats + all, c0, L.by_cg, d);
 #pragma unroll
         for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], d[q]);
         T* dst = y + at.at;
@@ -288,8 +311,8 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
     constexpr int Q = kPairs<VEC>;
-    const int slab = blockIdx.x / L.ctas % L.slabs, rank = blockIdx.x % L.ctas, groups = L.width / p.cg, all = L.items * groups;
-    const int column = blockIdx.x / (L.ctas * L.slabs);
+    const int slab = blockIdx.y, rank = L.ctas > 1 ? cta_rank() : 0, column = L.ctas > 1 ? cluster_id() : blockIdx.x;
+    const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
     float* red = weights + 2 * L.width;
     float* stats = red + 2 * kThreads * VEC;                // mean g, mean g xh
@@ -300,7 +323,7 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     if (L.ctas > 1) cluster_sync_g();
     else __syncthreads();
     const long long step = (long long)L.lanes * p.C;
-    const int c0 = threadIdx.x % L.packs * VEC;
+    const int c0 = ((int)threadIdx.x - (int)threadIdx.x / L.by_packs * L.packs) * VEC;
     Pair w[Q], bias[Q], sum[2][Q];                          // of the weights' gradients
     const Pair none[Q] = {};
     read_floats<VEC>(weights + c0, w);
@@ -327,8 +350,8 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         }
         Pair mu[Q], r[Q], s[2][Q];
         const long long from = (long long)(at.on ? at.b : 0) * p.G + slab * groups;
-        of_channels<VEC>(p.mean + from, c0, p.cg, mu);
-        of_channels<VEC>(p.rstd + from, c0, p.cg, r);
+        of_channels<VEC>(p.mean + from, c0, L.by_cg, mu);
+        of_channels<VEC>(p.rstd + from, c0, L.by_cg, r);
         if constexpr (HELD) fetched();
         // xh and dz of a pack
         auto values = [&](int k, Pair (&xh)[Q], Pair (&dz)[Q]) {
@@ -365,8 +388,8 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
             stats[which * all + k] = n > 0.f ? t / n : 0.f;
         });
         const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
-        of_channels<VEC>(mine_stats, c0, p.cg, s[0]);
-        of_channels<VEC>(mine_stats + all, c0, p.cg, s[1]);
+        of_channels<VEC>(mine_stats, c0, L.by_cg, s[0]);
+        of_channels<VEC>(mine_stats + all, c0, L.by_cg, s[1]);
         T* dst = dx + at.at;
         for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes, dst += step) {
             Pair xh[Q], dz[Q];
@@ -404,12 +427,12 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
 
 // ---- groups of a few positions (normalising row by row): a group is `lanes` lanes of a warp, at most two packs each, whose
 // sums need no barrier. A thread's group and channels stay the same over the batch elements that it takes, every
-// columns-th; the next one's packs are on their way meanwhile.
+// columns-th; the coming ones' packs are on their way to shared memory meanwhile, a thread's to places of its own.
 __device__ __forceinline__ float lane_sum(float v, int lanes) {
     for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-constexpr int kSmallPacks = 2;
+constexpr int kSmallPacks = 2, kAhead = 3;
 
 template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds__(kThreads, (BWD ? 2 : 4) / K) group_small_kernel(const GroupNormParams p, const Layout L)
 {
@@ -437,38 +460,49 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
         pairs_of<VEC>(t, bias[k]);
     }
     auto length = [&](long long b) { return b < end ? p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S : 0; };
-    uint4 xv[K], dv[K];   // not looked into before they are needed
-    float mean = 0.f, rstd = 0.f;
-    auto get = [&](long long b, int len) {
+    // [kAhead + 1][K][x, dy][kThreads] packs, and after them [kAhead + 1][mean, rstd][kThreads]
+    extern __shared__ __align__(16) unsigned char held[];
+    constexpr int N = BWD ? 2 : 1;
+    float* stat = reinterpret_cast<float*>(held + (kAhead + 1) * K * N * kThreads * 16);
+    auto slot = [&](int stage, int k, int which) { return reinterpret_cast<P*>(held) + ((stage * K + k) * N + which) * kThreads + threadIdx.x; };
+    auto send = [&](long long b, int stage) {
+        const int len = length(b);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (has[k] && row[k] < len) {
                 const long long at = (b * p.S + row[k]) * p.C + c[k];
-                xv[k] = *reinterpret_cast<const uint4*>(x + at);
-                if (BWD) dv[k] = *reinterpret_cast<const uint4*>(dy + at);
+                fetch16(slot(stage, k, 0), x + at);
+                if (BWD) fetch16(slot(stage, k, N - 1), dy + at);
             }
-        if (BWD && len > 0) mean = p.mean[b * p.G + g], rstd = p.rstd[b * p.G + g];
+        if (BWD && len > 0) {
+            fetch4(stat + 2 * stage * kThreads + threadIdx.x, p.mean + b * p.G + g);
+            fetch4(stat + (2 * stage + 1) * kThreads + threadIdx.x, p.rstd + b * p.G + g);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int len = length(column);
-    get(column, len);
+    for (int k = 0; k < kAhead; ++k) send(column + (long long)k * L.columns, k);
+    int stage = 0;
     // every lane of a warp makes the same number of rounds: the sums are collective
     const long long most = (p.B + L.columns - 1) / L.columns;
     for (long long turn = 0; turn < most; ++turn) {
         const long long b = column + turn * L.columns;
+        const int len = length(b);
         Pair v[K][Q], d[K][Q], s1 = pk2(0.f, 0.f), s2 = s1;
         bool in[K];
         const float n = (float)len * (float)p.cg, inv = len ? 1.f / n : 0.f;
+        send(b + (long long)kAhead * L.columns, stage == 0 ? kAhead : stage - 1);   // where the last round's were
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             in[k] = has[k] && row[k] < len;
             if (in[k]) {
-                minus<T, VEC>(reinterpret_cast<const P&>(xv[k]), none, v[k]);
-                if (BWD) minus<T, VEC>(reinterpret_cast<const P&>(dv[k]), none, d[k]);
+                minus<T, VEC>(*slot(stage, k, 0), none, v[k]);
+                if (BWD) minus<T, VEC>(*slot(stage, k, N - 1), none, d[k]);
             }
         }
-        float mu = mean, r = rstd;
-        const int next = turn + 1 < most ? length(b + L.columns) : 0;
-        get(b + L.columns, next);
+        float mu = 0.f, r = 0.f;
+        if (BWD && len > 0) mu = stat[2 * stage * kThreads + threadIdx.x], r = stat[(2 * stage + 1) * kThreads + threadIdx.x];
+        stage = stage == kAhead ? 0 : stage + 1;
         if constexpr (!BWD) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -530,7 +564,6 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
                     *reinterpret_cast<P*>(out + (b * p.S + row[k]) * p.C + c[k]) = rounded<T, VEC>(v[k]);
                 }
         }
-        len = next;
     }
     if (BWD && p.partial && column < L.columns) {
 #pragma unroll
@@ -670,6 +703,8 @@ template <typename F> cudaError_t with_type(int dtype, F f) {
     return f(__half());
 }
 
+Div div_by(int d) { return Div{(unsigned)((0x100000000ull + d - 1) / d), d}; }   // of 1: not multiplied by
+
 long long gcd(long long a, long long b) { return b ? gcd(b, a % b) : a; }
 
 // Both alignments' layouts are asked for by the size of the workspace, which so does not depend on addresses.
@@ -700,8 +735,9 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
         }
     L.packs = L.width / L.vec;
     if (L.packs > kThreads) return L;
-    L.fits = true;
     L.slabs = p.C / L.width;
+    if (L.slabs > 65535) return L;
+    L.fits = true;
     const int most = kThreads / L.packs;
     L.lanes = std::min(most, p.S);
     L.items = std::min(most / L.lanes, p.B);
@@ -718,13 +754,17 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
     while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes &&
-           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > 72 * 1024 || clusters * L.ctas < 2 * sms))
+           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > 75 * 1024 || clusters * L.ctas < 2 * sms))
         L.ctas *= 2;
     const auto need = bytes(L.ctas);
     L.part = (p.S + L.ctas - 1) / L.ctas;
     L.rounds = (L.part + L.lanes - 1) / L.lanes;
     L.held = L.vec > 1 && (long long)need.first + need.second <= 220 * 1024;
     L.smem = need.first + (L.held ? (size_t)need.second : 0);
+    L.groups = L.width / p.cg;
+    L.entries = p.cg % L.vec == 0 ? p.cg / L.vec : p.cg;
+    L.side = L.entries < 32 ? 32 / L.entries : 1;
+    L.by_packs = div_by(L.packs), L.by_lanes = div_by(L.lanes), L.by_cg = div_by(p.cg), L.by_entries = div_by(L.entries);
     // persistent where there are many small items
     const long long wanted = (p.B + L.items - 1) / L.items, per_sm = std::max<long long>(1, std::min<long long>(8, 220 * 1024 / (long long)L.smem));
     L.columns = (int)std::min(wanted, std::max(1ll, L.ctas > 1 ? wanted : (sms * per_sm + L.slabs - 1) / L.slabs));
@@ -740,7 +780,7 @@ template <auto Kernel> cudaError_t launch(const GroupNormParams& p, const Layout
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)L.ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.gridDim = dim3((unsigned)((long long)L.columns * L.slabs * L.ctas)), c.blockDim = dim3(kThreads), c.stream = s, c.attrs = &at;
+    c.gridDim = dim3((unsigned)(L.columns * L.ctas), (unsigned)L.slabs), c.blockDim = dim3(kThreads), c.stream = s, c.attrs = &at;
     c.numAttrs = L.ctas > 1 ? 1 : 0, c.dynamicSmemBytes = L.smem;
     return cudaLaunchKernelEx(&c, Kernel, p, L);
 }
@@ -750,9 +790,14 @@ long long partial_rows(const GroupNormParams& p, const Layout& L) { return L.sma
 template <typename T, int VEC, bool BWD> cudaError_t run_small(const GroupNormParams& p, const Layout& L, cudaStream_t s)
 {
     const unsigned grid = (unsigned)(((long long)L.columns * p.G * L.lanes + kThreads - 1) / kThreads);
-    if (L.items == 1) group_small_kernel<T, VEC, 1, BWD><<<grid, kThreads, 0, s>>>(p, L);
-    else group_small_kernel<T, VEC, 2, BWD><<<grid, kThreads, 0, s>>>(p, L);
-    return cudaGetLastError();
+    auto go = [&](auto k) {
+        constexpr size_t smem = (kAhead + 1) * kThreads * (k() * 16 + 4) * (BWD ? 2 : 1);
+        const cudaError_t e = allow_smem<group_small_kernel<T, VEC, k(), BWD>>(smem);
+        if (e != cudaSuccess) return e;
+        group_small_kernel<T, VEC, k(), BWD><<<grid, kThreads, smem, s>>>(p, L);
+        return cudaGetLastError();
+    };
+    return L.items == 1 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 2>());
 }
 
 }  // namespace
