@@ -438,10 +438,16 @@ bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t
 {
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     const EncodeFn fn = encode_fn();
-    return fn && fn(m, dtype == SDTW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-                    const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto go = [&] {
+        return fn(m, dtype == SDTW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                  const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (!fn) return false;
+    if (go() == CUDA_SUCCESS) return true;
+    // a thread whose first CUDA call this is (autograd's own, for one) has no context before it names its device
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && go() == CUDA_SUCCESS;
 }
 
 namespace {

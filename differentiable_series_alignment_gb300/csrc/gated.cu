@@ -246,25 +246,28 @@ struct Plan {
 int tiles_of(long long n, int tile) { return (int)((n + tile - 1) / tile); }
 
 // Columns of an accumulator: as many as there are results for, fewer where wide tiles would leave SMs without one.
-int pick_nb(long long rows, long long cols, long long others, int sms, bool pair)
+int pick_nb(long long rows, long long cols, long long others, int sms, bool pair, int dtype)
 {
-    for (int nb = 256; nb > 64; nb /= 2) {
+    for (int nb = dtype == SDTW_F32 ? 128 : 256; nb > 64; nb /= 2) {
         const int width = pair ? nb / 2 : nb;
-        if (cols > width / 2 && (long long)tiles_of(rows, 128) * tiles_of(cols, width) * others >= sms) return nb;
+        const int ctas = nb == 256 ? 2 : 1;   // 256 columns are a pair's tile, of 256 rows
+        if (cols > width / 2 && rows > 128 * (ctas - 1) && (long long)tiles_of(rows, 128 * ctas) * tiles_of(cols, width) * others * ctas >= sms) return nb;
     }
     return 64;
 }
 
 // Shares of the weights' sum over the rows: tiles that alone would leave SMs idle, or many of them in the last round, share
 // theirs. A block of the sum takes `block` us, a tile 1.5 besides; shares go through memory twice, at 4 TB/s.
-int pick_splits(long long tiles, long long blocks, int nb, double result_bytes, int sms)
+int pick_splits(long long rows, long long cols, int sets, long long blocks, int nb, int sms)
 {
+    const int ctas = nb == 256 ? 2 : 1, workers = sms / ctas;
+    const long long tiles = (long long)tiles_of(rows, 128 * ctas) * tiles_of(cols, nb) * sets;
     const double block = 0.34 * nb / 256;
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= 64 && s <= blocks; ++s) {
-        const double rounds = (double)((tiles * s + sms - 1) / sms);
-        const double cost = rounds * (1.5 + block * (double)((blocks + s - 1) / s)) + (s == 1 ? 0. : 4. + 2e-6 * s * result_bytes / 4.);
+        const double rounds = (double)((tiles * s + workers - 1) / workers);
+        const double cost = rounds * (1.5 + block * (double)((blocks + s - 1) / s)) + (s == 1 ? 0. : 4. + 2e-6 * s * 4. * rows * cols * sets / 4.);
         if (cost < least) least = cost, best = s;
     }
     return best;
@@ -300,11 +303,10 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
     if (!backward) return plan;
     const long long pitch = (a.F + 7) / 8 * 8;
     plan.grads = Image{carve((size_t)2 * parts * a.R * pitch * 2), pitch, a.R, a.F, 2 * parts};
-    plan.sums = reinterpret_cast<float*>(carve((size_t)4 * tiles_of(a.R, 128) * 2 * a.F * sizeof(float)));
+    plan.sums = reinterpret_cast<float*>(carve((size_t)tiles_of(a.R, 32) * 2 * a.F * sizeof(float)));
     plan.scale = reinterpret_cast<float*>(carve(256));
-    plan.dw_nb = pick_nb(a.F, a.K, 1 << 20, sms, false);
-    plan.dw_splits = pick_splits(2ll * tiles_of(a.F, 128) * tiles_of(a.K, plan.dw_nb), (parts == 3 ? 6ll : 1ll) * tiles_of(a.R, 64), plan.dw_nb,
-                                 8. * a.F * a.K, sms);
+    plan.dw_nb = pick_nb(a.F, a.K, 1 << 20, sms, false, a.dtype);
+    plan.dw_splits = pick_splits(a.F, a.K, 2, (parts == 3 ? 6ll : 1ll) * tiles_of(a.R, 64), plan.dw_nb, sms);
     if (plan.dw_splits > 1) plan.shares = reinterpret_cast<float*>(carve((size_t)plan.dw_splits * 2 * a.F * a.K * sizeof(float)));
     return plan;
 }
@@ -332,12 +334,12 @@ cudaError_t products(const GatedParams& p, const Plan& plan, bool grads, bool wa
 {
     const sdtw_gated& a = p.a;
     gtc::Params g{};
-    const int nb = pick_nb(a.R, a.F, 1, sms, true), width = nb / 2;
+    const int nb = pick_nb(a.R, a.F, 1, sms, true, a.dtype), width = nb / 2;
     if (!plan.x.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, width) || !plan.w[1].map(&g.b[1], a.dtype, 64, width))
         return cudaErrorInvalidValue;
     set_segs(g, plan.x.parts, false);
     g.blocks = tiles_of(a.K, 64);
-    g.tiles_m = tiles_of(a.R, 128), g.tiles_n = tiles_of(a.F, width), g.sets = g.splits = 1;
+    g.sets = g.splits = 1;
     g.M = a.R, g.N = g.F = a.F, g.activation = a.activation;
     g.out[0] = p.h, g.bias[0] = a.gate_bias, g.bias[1] = a.up_bias, g.dh = p.dh;
     g.grads = static_cast<uint16_t*>(const_cast<void*>(plan.grads.p)), g.ld = plan.grads.pitch;
@@ -398,12 +400,12 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
     g.scale = a.dtype == SDTW_F16 ? plan.scale : nullptr;
     g.wait_ns = p.wait_ns;
     if (p.dx) {
-        const int nb = pick_nb(a.R, a.K, 1, sms, false);
+        const int nb = pick_nb(a.R, a.K, 1, sms, false, a.dtype);
         if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, 64) || !plan.w[1].map(&g.b[1], a.dtype, 64, 64))
             return cudaErrorInvalidValue;
         set_segs(g, parts, true);
         g.blocks = tiles_of(a.F, 64);
-        g.tiles_m = tiles_of(a.R, 128), g.tiles_n = tiles_of(a.K, nb), g.sets = g.splits = 1, g.set0 = 0;
+        g.sets = g.splits = 1, g.set0 = 0;
         g.M = a.R, g.N = a.K, g.out[0] = p.dx;
         if ((e = gtc::run_dx(g, a.dtype, nb, sms, s)) != cudaSuccess) return e;
     }
@@ -412,7 +414,6 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
         g.b[1] = g.b[0];
         set_segs(g, parts, false);
         g.blocks = tiles_of(a.R, 64);
-        g.tiles_m = tiles_of(a.F, 128), g.tiles_n = tiles_of(a.K, plan.dw_nb);
         g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1, g.splits = plan.dw_splits;
         g.M = a.F, g.N = a.K, g.out[0] = p.dgate_weight, g.out[1] = p.dup_weight, g.shares = plan.shares;
         if ((e = gtc::run_dw(g, a.dtype, plan.dw_nb, sms, s)) != cudaSuccess) return e;

@@ -9,11 +9,17 @@
 // a tensor map leaves out (rows, features, the tail of the sum) arrives as zeros. x, dg and W lie along their rows, so
 // that a sum over features has K-major operands and a sum over rows MN-major ones: no operand is transposed in memory.
 // fp32 operands are split into three bf16 parts, v = v0 + v1 + v2 to 24 bits, and a product is the sum of the six part products
-// above 2^-24 of it, (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first, as one longer sum.
+// above 2^-24 of it, (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first, as one longer sum. The tensor cores cut off what an
+// addition leaves below the accumulator's last bit, always towards 0: over a sum of 6000 terms that came to 250 times the
+// result's own rounding. Sums of fp32 are so taken in runs of 256 terms, which are added up in registers, rounded to nearest.
 //
 // A persistent CTA: a loading warp, an issuing warp, and eight warps that turn a finished accumulator into results while
-// the next one is summed (two accumulators in tensor memory).
+// the next one is summed (two accumulators in tensor memory). Large calls take pairs of CTAs (cta_group::2) with 256 rows and 256
+// columns of accumulator to a tile: each CTA has 128 of the rows and loads half of the other operand, which both use. The
+// first of a pair issues for both.
 #pragma once
+#include <algorithm>
+
 #include "activation.cuh"
 #include "attn_tc.cuh"
 #include "block.h"
@@ -45,7 +51,7 @@ struct alignas(64) Params {
     // GRAD: dg and du, rounded, as parts 0 .. parts - 1 and parts .. 2 parts - 1 of (2 parts, M, ld)
     uint16_t* grads;
     long long ld;
-    float* sums;                                       // GRAD, with biases: [4 tiles_m][2 F] column sums of 32 rows
+    float* sums;                                       // GRAD, with biases: [M / 32][2 F] column sums of 32 rows
     float* shares;                                     // DW with splits: [splits][sets][M][N]
     const float* scale;                                // fp16: what dg and du are multiplied by, and its inverse
     unsigned long long wait_ns;
@@ -56,13 +62,16 @@ struct alignas(64) Params {
 template <typename T> struct Operand { using type = T; };
 template <> struct Operand<float> { using type = __nv_bfloat16; };
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+template <typename T> constexpr int kRun = sizeof(T) == 4 ? 4 : 1 << 30;   // blocks that one accumulator takes
 
 template <int NB> struct Shape {
-    static constexpr uint32_t b_bytes = NB * kBlock * 2, stage = kABytes + b_bytes;
+    static constexpr int ctas = NB == 256 ? 2 : 1;     // that share a tile
+    static constexpr uint32_t b_bytes = NB / ctas * kBlock * 2, stage = kABytes + b_bytes;   // of a CTA
     static constexpr uint32_t area = 4096;             // of shared memory, a warp's own
-    static constexpr int stages = NB == 256 ? 4 : NB == 128 ? 6 : 7;
+    static constexpr int stages = NB == 64 ? 7 : 6;
     static constexpr uint32_t smem = stages * stage + 8 * area;
-    static constexpr int columns = 2 * NB < 32 ? 32 : 2 * NB;
+    static constexpr int columns = 2 * NB;             // of tensor memory
+    static constexpr int rows = ctas * kRows;          // of a tile
 };
 
 constexpr int kLoad = 8, kIssue = 9, kThreadsG = 320;
@@ -76,6 +85,66 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* m, int c0,
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
+}
+// The same by a CTA of a pair, reported to the first one's barrier
+__device__ __forceinline__ void tma3_pair(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+template <int CTAS> __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+    if constexpr (CTAS == 2) tma3_pair(dst, m, c0, c1, c2, bar);
+    else tma3(dst, m, c0, c1, c2, bar);
+}
+template <int CTAS> __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(acc));
+    else mma_ss(d, a, b, id, acc);
+}
+// of a pair: reported to both
+template <int CTAS> __device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+                     : "memory");
+    else mma_commit(bar);
+}
+template <int CTAS> __device__ __forceinline__ void alloc(uint32_t* to, int columns) {
+    if constexpr (CTAS == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(to, columns);
+    }
+}
+template <int CTAS> __device__ __forceinline__ void dealloc(uint32_t tmem, int columns) {
+    if constexpr (CTAS == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+    else tmem_dealloc(tmem, columns);
+}
+// All threads of the CTA, or of the pair, have come here.
+template <int CTAS> __device__ __forceinline__ void meet() {
+    if constexpr (CTAS == 2) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t mine, int cta) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(cta));
+    return there;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {   // of this cluster
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ int cta_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 // MN-major blocks of 64 rows: groups of 64 elements 8 KB apart
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
@@ -268,18 +337,20 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     __shared__ uint32_t s_tmem;
     __shared__ int s_late;
     const Late late{&g_status, &s_late};
-    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    constexpr int CTAS = Sh::ctas;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, rank = CTAS == 2 ? uniform(cta_rank()) : 0;
+    const int worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
     if (warp == kLoad && lane == 0) {
         prefetch_map(&p.a), prefetch_map(&p.b[0]), prefetch_map(&p.b[1]);
         s_late = 0;
         for (int e = 0; e < Sh::stages; ++e) mbar_init(smem_u32(&s_full[e]), 1), mbar_init(smem_u32(&s_empty[e]), 1);
-        for (int e = 0; e < 2; ++e) mbar_init(smem_u32(&s_done[e]), 1), mbar_init(smem_u32(&s_free[e]), 8);
+        for (int e = 0; e < 2; ++e) mbar_init(smem_u32(&s_done[e]), 1), mbar_init(smem_u32(&s_free[e]), 8 * CTAS);
         mbar_init(smem_u32(&s_end), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kIssue) tmem_alloc(&s_tmem, Sh::columns);
+    if (warp == kIssue) alloc<CTAS>(&s_tmem, Sh::columns);
     fence_before_sync();
-    __syncthreads();
+    meet<CTAS>();
     fence_after_sync();
     const uint32_t tmem = (uint32_t)uniform((int)s_tmem), ring = smem_u32(dyn);
     bool ok = true;
@@ -287,48 +358,56 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     if (warp == kLoad) {
         if (lane == 0 && !p.skip) {
             int i = 0;   // blocks sent for
-            for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+            for (int t = worker; t < p.tiles && ok; t += workers) {
                 const Tile tile(p, t);
+                const int row = tile.m * Sh::rows + rank * kRows;
                 for (int k = tile.first; k < tile.last; ++k, ++i) {
                     const int e = i % Sh::stages;
                     if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, late);
                     if (!ok) break;
                     const Seg sg = p.seg[k / p.blocks];
                     const int at = k % p.blocks * kBlock;
-                    const uint32_t bar = smem_u32(&s_full[e]), a = ring + e * Sh::stage, b = a + kABytes;
-                    mbar_expect_tx(bar, Sh::stage);
+                    const uint32_t mine = smem_u32(&s_full[e]), a = ring + e * Sh::stage, b = a + kABytes;
+                    const uint32_t bar = CTAS == 2 ? in_cta(mine, 0) : mine;
+                    if (rank == 0) mbar_expect_tx(mine, CTAS * Sh::stage);
                     if constexpr (A_MN) {
 #pragma unroll
                         for (int c = 0; c < kRows / 64; ++c)
-                            tma3(a + c * kBlock * 128, &p.a, tile.m * kRows + c * 64, at, sg.a + tile.set * kParts<T>, bar);
+                            load3<CTAS>(a + c * kBlock * 128, &p.a, row + c * 64, at, sg.a + tile.set * kParts<T>, bar);
                     } else {
-                        tma3(a, &p.a, at, tile.m * kRows, sg.a, bar);
+                        load3<CTAS>(a, &p.a, at, row, sg.a, bar);
                     }
-                    if constexpr (PAIR) {
-                        tma3(b, &p.b[0], at, tile.n * WIDTH, sg.b, bar);
-                        tma3(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, sg.b, bar);
+                    if constexpr (PAIR && CTAS == 2) {   // the first CTA has the gate's weights, the second the others
+                        load3<CTAS>(b, &p.b[rank], at, tile.n * WIDTH, sg.b, bar);
+                    } else if constexpr (PAIR) {
+                        load3<CTAS>(b, &p.b[0], at, tile.n * WIDTH, sg.b, bar);
+                        load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, sg.b, bar);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < NB / 64; ++c) tma3(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + c * 64, at, sg.b, bar);
+                        for (int c = 0; c < NB / CTAS / 64; ++c)
+                            load3<CTAS>(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + rank * (NB / CTAS) + c * 64, at, sg.b, bar);
                     }
                 }
             }
             // no copy may be writing shared memory when the CTA ends
-            bool drained = true;
-            for (int k = max(0, i - Sh::stages); k < i; ++k)
+            bool drained = true;   // a pair's are all reported to the first CTA, for which the second waits at the end
+            for (int k = max(0, i - Sh::stages); k < i && rank == 0; ++k)
                 wait_for(drained, smem_u32(&s_full[k % Sh::stages]), (uint32_t)((k / Sh::stages) & 1), p.wait_ns, late);
         }
         __syncwarp();
     } else if (warp == kIssue) {
-        const uint32_t id = idesc2<O>(kRows, NB, A_MN, B_MN);
+        const uint32_t id = idesc2<O>(Sh::rows, NB, A_MN, B_MN);
         int i = 0, n = 0;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++n) {
+        for (int t = worker; t < p.tiles && ok && rank == 0; t += workers) {
             const Tile tile(p, t);
             const int first = uniform(tile.first), last = uniform(tile.last);
-            const uint32_t d = tmem + (n & 1) * NB;
-            if (n >= 2) wait_warp(ok, smem_u32(&s_free[n & 1]), (uint32_t)((n / 2 - 1) & 1), p.wait_ns, late);
-            fence_after_sync();
-            for (int k = first; k < last; ++k, ++i) {
+            for (int k = first, in = 0; k < last; ++k, ++i) {   // in: of the run
+                if (in == 0) {
+                    if (n >= 2) wait_warp(ok, smem_u32(&s_free[n & 1]), (uint32_t)((n / 2 - 1) & 1), p.wait_ns, late);
+                    fence_after_sync();
+                }
+                const uint32_t d = tmem + (n & 1) * NB;
+                const bool ends = k == last - 1 || in == kRun<T> - 1;
                 const int e = i % Sh::stages;
                 wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, late);
                 fence_after_sync();
@@ -337,16 +416,18 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                     const uint64_t ad = A_MN ? desc_mn(a) : sdesc(a), bd = B_MN ? desc_mn(b) : sdesc(b);
 #pragma unroll
                     for (int s = 0; s < kBlock / 16; ++s)   // 16 of the sum: 32 bytes along a row, or 16 rows
-                        mma_ss(d, ad + s * (A_MN ? 128 : 2), bd + s * (B_MN ? 128 : 2), id, k > first || s > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&s_empty[e]));
-                    if (k == last - 1) mma_commit(smem_u32(&s_done[n & 1]));
+                        mma<CTAS>(d, ad + s * (A_MN ? 128 : 2), bd + s * (B_MN ? 128 : 2), id, in > 0 || s > 0 ? 1u : 0u);
+                    commit<CTAS>(smem_u32(&s_empty[e]));
+                    if (ends) commit<CTAS>(smem_u32(&s_done[n & 1]));
                 }
                 __syncwarp();
+                in = ends ? 0 : in + 1;
+                n += ends;
             }
         }
         // every MMA has read its operands and written its result before the CTA ends
-        if (lane == 0) {
-            mma_commit(smem_u32(&s_end));
+        if (lane == 0 && rank == 0) {
+            commit<CTAS>(smem_u32(&s_end));
             bool fin = true;
             wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, late);
         }
@@ -355,34 +436,29 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
         const float up = p.scale ? p.scale[0] : 1.f, down = p.scale ? p.scale[1] : 1.f;
+        // the accumulator has been read by this warp
+        auto release = [&](int which) {
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (CTAS == 2) arrive_at(in_cta(smem_u32(&s_free[which]), 0));
+                else mbar_arrive(smem_u32(&s_free[which]));
+            }
+        };
         int n = 0;
-        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
+        for (int t = worker; t < p.tiles; t += workers) {
             const Tile tile(p, t);
-            const long long row0 = (long long)tile.m * kRows + quarter * 32;
+            const long long row0 = (long long)tile.m * Sh::rows + rank * kRows + quarter * 32;
             const int rows = (int)min(32ll, p.M - row0);
             const int limit = PAIR ? p.F : p.N;
-            wait_warp(ok, smem_u32(&s_done[n & 1]), (uint32_t)((n / 2) & 1), p.wait_ns, late);
-            fence_after_sync();
-            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * NB;
-#pragma unroll 1
-            for (int c = half; c < WIDTH / 32; c += 2) {
+            // 32 columns of the result from the accumulators
+            auto finish = [&](int c, float (&g)[32], float (&u)[32]) {
                 const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
-                float g[32], u[32], dh[32];
-                const bool some = rows > 0 && cols > 0;
+                if (rows <= 0 || cols <= 0) return;
+                float dh[32];
                 if constexpr (KIND == GRAD)
-                    if (some) {
-                        const T* src = static_cast<const T*>(p.dh) + row0 * p.F + col;
-                        get_chunk<T>(area, dh, src, p.F, rows, cols, p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh), lane);
-                    }
-                tmem_ld32_nowait(acc + c * 32, g);
-                if constexpr (PAIR) tmem_ld32_nowait(acc + WIDTH + c * 32, u);
-                tmem_wait_ld();
-                if (c + 2 >= WIDTH / 32) {   // the accumulator has been read
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_free[n & 1]));
-                }
-                if (!some) continue;
+                    get_chunk<T>(area, dh, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols,
+                                 p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh), lane);
                 if constexpr (PAIR) {
                     add_bias<T>(g, p.bias[0], col, cols);
                     add_bias<T>(u, p.bias[1], col, cols);
@@ -402,7 +478,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                 }
                 if (bad) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) g[j] = __int_as_float(0x7fffffff), u[j] = g[j];
+                    for (int j = 0; j < 32; ++j) {
+                        g[j] = __int_as_float(0x7fffffff);
+                        if (PAIR) u[j] = g[j];
+                    }
                 }
                 if constexpr (KIND == GRAD) {
 #pragma unroll 1
@@ -425,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] = which ? u[j] : g[j];
                             const float s = column_sums(v, lane);
-                            if (lane < cols) p.sums[((long long)tile.m * 4 + quarter) * 2 * p.F + which * p.F + col + lane] = s;
+                            if (lane < cols) p.sums[row0 / 32 * 2 * p.F + which * p.F + col + lane] = s;
                         }
                     }
                 } else if (KIND == DW && p.splits > 1) {
@@ -435,19 +514,58 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                     T* base = static_cast<T*>(p.out[KIND == DW ? tile.set : 0]);
                     if (base) put_chunk<T>(area, g, base + row0 * limit + col, limit, rows, cols, limit % (16 / (int)sizeof(T)) == 0 && aligned16_dev(base), lane);
                 }
-            }
-            if (half >= WIDTH / 32) {   // narrow tiles leave nothing for the other warps
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&s_free[n & 1]));
+            };
+            auto await = [&] {
+                wait_warp(ok, smem_u32(&s_done[n & 1]), (uint32_t)((n / 2) & 1), p.wait_ns, late);
+                fence_after_sync();
+                return tmem + ((uint32_t)(quarter * 32) << 16) + (n & 1) * NB;
+            };
+            if constexpr (sizeof(T) == 4) {
+                constexpr int C = (WIDTH / 32 + 1) / 2;   // times 32 columns of this warp, added up over the runs
+                float g[C][32], u[PAIR ? C : 1][32];
+                for (int k = tile.first; k < tile.last; k += kRun<T>, ++n) {
+                    const uint32_t acc = await();
+                    if (half < WIDTH / 32) {
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            float v[32];
+#pragma unroll
+                            for (int w = 0; w < (PAIR ? 2 : 1); ++w) {
+                                float (&to)[32] = w ? u[c] : g[c];
+                                tmem_ld32_nowait(acc + w * WIDTH + (half + 2 * c) * 32, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) to[j] = k == tile.first ? v[j] : to[j] + v[j];
+                            }
+                        }
+                    }
+                    release(n & 1);
+                }
+                if (half < WIDTH / 32) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) finish(half + 2 * c, g[c], PAIR ? u[c] : g[c]);
+                }
+            } else {
+                const uint32_t acc = await();
+#pragma unroll 1
+                for (int c = half; c < WIDTH / 32; c += 2) {
+                    float g[32], u[32];
+                    tmem_ld32_nowait(acc + c * 32, g);
+                    if constexpr (PAIR) tmem_ld32_nowait(acc + WIDTH + c * 32, u);
+                    tmem_wait_ld();
+                    if (c + 2 >= WIDTH / 32) release(n & 1);
+                    finish(c, g, u);
+                }
+                if (half >= WIDTH / 32) release(n & 1);   // narrow tiles leave nothing for the other warps
+                ++n;
             }
         }
     }
     fence_before_sync();
-    __syncthreads();
+    meet<CTAS>();
     if (warp == kIssue) {
         fence_after_sync();
-        tmem_dealloc(tmem, Sh::columns);
+        dealloc<CTAS>(tmem, Sh::columns);
     }
 }
 
@@ -455,13 +573,22 @@ template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cuda
 {
     using Sh = Shape<NB>;
     if (const cudaError_t e = allow_smem<gated_tc_kernel<KIND, T, NB>>(Sh::smem); e != cudaSuccess) return e;
+    p.tiles_m = (int)((p.M + Sh::rows - 1) / Sh::rows);
+    p.tiles_n = (p.N + (KIND == FWD || KIND == GRAD ? NB / 2 : NB) - 1) / (KIND == FWD || KIND == GRAD ? NB / 2 : NB);
     p.tiles = p.tiles_m * p.tiles_n * p.sets * p.splits;
-    gated_tc_kernel<KIND, T, NB><<<p.tiles < sms ? p.tiles : sms, kThreadsG, Sh::smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = Sh::ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.gridDim = dim3((unsigned)(std::min(p.tiles, sms / Sh::ctas) * Sh::ctas)), c.blockDim = dim3(kThreadsG), c.dynamicSmemBytes = Sh::smem;
+    c.stream = s, c.attrs = &at, c.numAttrs = Sh::ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&c, gated_tc_kernel<KIND, T, NB>, (const Params&)p);
 }
 template <int KIND, typename T> cudaError_t run_nb(Params& p, int NB, int sms, cudaStream_t s)
 {
-    return NB == 256 ? run<KIND, T, 256>(p, sms, s) : NB == 128 ? run<KIND, T, 128>(p, sms, s) : run<KIND, T, 64>(p, sms, s);
+    if constexpr (sizeof(T) == 2)   // fp32's sums are in registers: half as many columns
+        if (NB == 256) return run<KIND, T, 256>(p, sms, s);
+    return NB == 128 ? run<KIND, T, 128>(p, sms, s) : run<KIND, T, 64>(p, sms, s);
 }
 template <int KIND> cudaError_t run_kind(Params& p, int dtype, int NB, int sms, cudaStream_t s)
 {

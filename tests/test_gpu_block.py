@@ -670,3 +670,52 @@ def test_waits_that_run_out(package):
     finally:
         package.sdtw_debug_set_wait(0.0, 0)
     assert torch.equal(backward(), want[2])
+
+
+def test_first_call_of_a_thread(package):
+    """A thread that has made no other CUDA call yet has no context of its own; tensor maps need one."""
+    import subprocess
+    import sys
+    code = """if 1:
+        import threading, torch
+        from differentiable_series_alignment_gb300 import attention, gated_linear
+        q = torch.randn(1, 200, 2, 64, device="cuda", dtype=torch.bfloat16)
+        x, w = q.reshape(-1, 64), torch.randn(256, 64, device="cuda", dtype=torch.bfloat16)
+        want = attention(q, q, q), gated_linear(x, w, w)
+        del want
+        got = []
+        for f in (lambda: attention(q, q, q), lambda: gated_linear(x, w, w)):
+            t = threading.Thread(target=lambda: got.append(f()))
+            t.start()
+            t.join()
+        assert torch.equal(got[0], attention(q, q, q)) and torch.equal(got[1], gated_linear(x, w, w))
+        leaf = x.detach().requires_grad_()
+        torch.autograd.grad(gated_linear(leaf, w, w), leaf, torch.ones(400, 256, device="cuda", dtype=torch.bfloat16))
+        torch.cuda.synchronize()
+    """
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_large_products_against_64_bits(package, dtype):
+    """Tiles of two CTAs, shares of a sum, ragged last tiles: in quadratic mean against 64 bits, where a tile that is
+    missing, doubled or misplaced shows. fp32's sums of up to 8192 terms have errors of 64 roundings of a term at the least."""
+    gen = generator(24)
+    R, K, F = (2100, 300, 3001) if dtype == F32 else (5000, 520, 4100)
+    x, wg, wu = randn(gen, R, K, dtype=dtype), *(randn(gen, F, K, dtype=dtype, std=K ** -0.5) for _ in range(2))
+    bg, dh = randn(gen, F, dtype=dtype), randn(gen, R, F, dtype=dtype, std=1e-3)
+    leaves = [t.requires_grad_() for t in (x, wg, wu, bg)]
+    h = package.gated_linear(x, wg, wu, bg, activation="gelu")
+    grads = torch.autograd.grad(h, leaves, dh)
+    wide = [t.detach().double().requires_grad_() for t in leaves]
+    g = wide[0] @ wide[1].T + wide[3]
+    exact = g * 0.5 * torch.erfc(-g / math.sqrt(2)) * (wide[0] @ wide[2].T)
+    want = torch.autograd.grad(exact, wide, dh.double())
+    for got, right, what in zip((h, *grads), (exact, *want), ("h", "dx", "dwg", "dwu", "dbg")):
+        error = ((got.detach().double() - right) ** 2).mean().sqrt()
+        own = ((right.to(dtype).double() - right) ** 2).mean().sqrt()
+        assert error <= (64 if dtype == F32 else 1.02 if what in ("h", "dbg") else 1.6) * own, (what, float(error / own))
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(package.gated_linear(x, wg, wu, bg, activation="gelu"), leaves, dh), grads))
