@@ -6,6 +6,7 @@
 // The products run on the tensor cores (gated_tc.cuh). Here are the kernels around them: operands brought into the form that
 // TMA loads, few rows, sums over row tiles and over shares of a sum, and the order of it all.
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "gated_tc.cuh"
@@ -179,7 +180,7 @@ __global__ void gated_scale_kernel(const unsigned* top, float* scale)
     scale[1] = 1.f / scale[0];
 }
 
-// ---- column sums of row tiles, and shares of a sum, added in a fixed order
+// ---- column sums of row tiles, added in a fixed order
 template <typename T> __global__ void __launch_bounds__(1024) gated_bias_kernel(const float* sums, long long n, int F, T* dgate, T* dup)
 {
     __shared__ float part[32][33];
@@ -200,15 +201,6 @@ template <typename T> __global__ void __launch_bounds__(1024) gated_bias_kernel(
     T* dst = col < F ? dgate : dup;
     if ((threadIdx.x & 31) == 0 && col < 2 * F && dst) dst[col < F ? col : col - F] = from_f32<T>(v);
 }
-template <typename T> __global__ void __launch_bounds__(256) gated_join_kernel(const float* shares, int splits, long long n, int sets, T* out0, T* out1)
-{
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n * sets; i += (long long)gridDim.x * 256) {
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k) s += shares[k * n * sets + i];
-        (i < n ? out0 : out1)[i < n ? i : i - n] = from_f32<T>(s);
-    }
-}
-
 template <typename F> cudaError_t with_type(int dtype, F f) {
     if (dtype == SDTW_F32) return f(float());
     if (dtype == SDTW_BF16) return f(__nv_bfloat16());
@@ -239,7 +231,7 @@ struct Plan {
     PackJob pack;
     int pack_ctas = 0;
     float *sums = nullptr, *shares = nullptr, *scale = nullptr;
-    int dw_nb = 256, dw_splits = 1;
+    int dx_nb = 256, dw_nb = 256;
     size_t bytes = 0;
 };
 
@@ -254,23 +246,6 @@ int pick_nb(long long rows, long long cols, long long others, int sms, bool pair
         if (cols > width / 2 && rows > 128 * (ctas - 1) && (long long)tiles_of(rows, 128 * ctas) * tiles_of(cols, width) * others * ctas >= sms) return nb;
     }
     return 64;
-}
-
-// Shares of the weights' sum over the rows: tiles that alone would leave SMs idle, or many of them in the last round, share
-// theirs. A block of the sum takes `block` us, a tile 1.5 besides; shares go through memory twice, at 4 TB/s.
-int pick_splits(long long rows, long long cols, int sets, long long blocks, int nb, int sms)
-{
-    const int ctas = nb == 256 ? 2 : 1, workers = sms / ctas;
-    const long long tiles = (long long)tiles_of(rows, 128 * ctas) * tiles_of(cols, nb) * sets;
-    const double block = 0.34 * nb / 256;
-    int best = 1;
-    double least = 1e30;
-    for (int s = 1; s <= 64 && s <= blocks; ++s) {
-        const double rounds = (double)((tiles * s + workers - 1) / workers);
-        const double cost = rounds * (1.5 + block * (double)((blocks + s - 1) / s)) + (s == 1 ? 0. : 4. + 2e-6 * s * 4. * rows * cols * sets / 4.);
-        if (cost < least) least = cost, best = s;
-    }
-    return best;
 }
 
 Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
@@ -305,9 +280,32 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
     plan.grads = Image{carve((size_t)2 * parts * a.R * pitch * 2), pitch, a.R, a.F, 2 * parts};
     plan.sums = reinterpret_cast<float*>(carve((size_t)tiles_of(a.R, 32) * 2 * a.F * sizeof(float)));
     plan.scale = reinterpret_cast<float*>(carve(256));
-    plan.dw_nb = pick_nb(a.F, a.K, 1 << 20, sms, false, a.dtype);
-    plan.dw_splits = pick_splits(a.F, a.K, 2, (parts == 3 ? 6ll : 1ll) * tiles_of(a.R, 64), plan.dw_nb, sms);
-    if (plan.dw_splits > 1) plan.shares = reinterpret_cast<float*>(carve((size_t)plan.dw_splits * 2 * a.F * a.K * sizeof(float)));
+    // Columns of dx's and the weights' accumulators, by the least time, and room for their shares; one of the weights'
+    // gradients alone may share its sums otherwise than both.
+    size_t shares = 0;
+    auto time = [&](int sets, int nb, size_t& bytes) {   // sets 0: dx
+        const int ctas = nb == 256 ? 2 : 1;
+        gtc::Params g{};
+        g.segs = (parts == 3 ? 6 : 1) * (sets ? 1 : 2), g.blocks = sets ? tiles_of(a.R, 64) : tiles_of(a.F, 64);
+        g.sets = sets ? sets : 1, g.M = sets ? a.F : a.R, g.N = a.K;
+        const double t = gtc::share_out(g, 128 * ctas, nb, nb, sms / ctas, true);
+        bytes = gtc::share_bytes(g, 128 * ctas, nb);
+        return t;
+    };
+    for (int sets : {0, 2}) {
+        double least = 1e30;
+        for (int nb = a.dtype == SDTW_F32 ? 128 : 256; nb >= 64; nb /= 2) {
+            size_t bytes;
+            const double t = time(sets, nb, bytes);
+            if (t < least) least = t, (sets ? plan.dw_nb : plan.dx_nb) = nb;
+        }
+    }
+    for (int sets : {0, 1, 2}) {
+        size_t bytes;
+        time(sets, sets ? plan.dw_nb : plan.dx_nb, bytes);
+        shares = std::max(shares, bytes);
+    }
+    plan.shares = reinterpret_cast<float*>(carve(shares));
     return plan;
 }
 
@@ -339,7 +337,7 @@ cudaError_t products(const GatedParams& p, const Plan& plan, bool grads, bool wa
         return cudaErrorInvalidValue;
     set_segs(g, plan.x.parts, false);
     g.blocks = tiles_of(a.K, 64);
-    g.sets = g.splits = 1;
+    g.sets = 1;
     g.M = a.R, g.N = g.F = a.F, g.activation = a.activation;
     g.out[0] = p.h, g.bias[0] = a.gate_bias, g.bias[1] = a.up_bias, g.dh = p.dh;
     g.grads = static_cast<uint16_t*>(const_cast<void*>(plan.grads.p)), g.ld = plan.grads.pitch;
@@ -400,33 +398,22 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
     g.scale = a.dtype == SDTW_F16 ? plan.scale : nullptr;
     g.wait_ns = p.wait_ns;
     if (p.dx) {
-        const int nb = pick_nb(a.R, a.K, 1, sms, false, a.dtype);
         if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, 64) || !plan.w[1].map(&g.b[1], a.dtype, 64, 64))
             return cudaErrorInvalidValue;
         set_segs(g, parts, true);
         g.blocks = tiles_of(a.F, 64);
-        g.sets = g.splits = 1, g.set0 = 0;
-        g.M = a.R, g.N = a.K, g.out[0] = p.dx;
-        if ((e = gtc::run_dx(g, a.dtype, nb, sms, s)) != cudaSuccess) return e;
+        g.sets = 1, g.set0 = 0;
+        g.M = a.R, g.N = a.K, g.out[0] = p.dx, g.shares = plan.shares;
+        if ((e = gtc::run_dx(g, a.dtype, plan.dx_nb, sms, s)) != cudaSuccess) return e;
     }
     if (p.dgate_weight || p.dup_weight) {
         if (!plan.grads.map(&g.a, a.dtype, 64, 64) || !plan.x.map(&g.b[0], a.dtype, 64, 64)) return cudaErrorInvalidValue;
         g.b[1] = g.b[0];
         set_segs(g, parts, false);
         g.blocks = tiles_of(a.R, 64);
-        g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1, g.splits = plan.dw_splits;
+        g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1;
         g.M = a.F, g.N = a.K, g.out[0] = p.dgate_weight, g.out[1] = p.dup_weight, g.shares = plan.shares;
         if ((e = gtc::run_dw(g, a.dtype, plan.dw_nb, sms, s)) != cudaSuccess) return e;
-        if (g.splits > 1) {
-            const long long n = (long long)a.F * a.K;
-            e = with_type(a.dtype, [&](auto t) {
-                using T = decltype(t);
-                gated_join_kernel<T><<<(unsigned)std::min(n * g.sets / 256 + 1, (long long)sms * 8), 256, 0, s>>>(
-                    plan.shares, g.splits, n, g.sets, static_cast<T*>(g.out[g.set0]), static_cast<T*>(g.out[1]));
-                return cudaGetLastError();
-            });
-            if (e != cudaSuccess) return e;
-        }
     }
     if (biases)
         e = with_type(a.dtype, [&](auto t) {

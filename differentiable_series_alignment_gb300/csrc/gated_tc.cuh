@@ -43,7 +43,8 @@ struct alignas(64) Params {
     CUtensorMap a, b[2];
     Seg seg[12];
     int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks
-    int tiles_m, tiles_n, set0, sets, splits, tiles;   // sets: DW's weights, from set0 on; splits: shares of the sum, none empty
+    int tiles_m, tiles_n, group, set0, sets, tiles;    // sets: DW's weights, from set0 on
+    int whole, workers;                                // tiles summed whole; workers that share the others' sums (below)
     long long M;                                       // rows and columns of the result
     int N, F, activation;
     void* out[2];                                      // FWD h; DX dx; DW both weights' gradients
@@ -52,7 +53,7 @@ struct alignas(64) Params {
     uint16_t* grads;
     long long ld;
     float* sums;                                       // GRAD, with biases: [M / 32][2 F] column sums of 32 rows
-    float* shares;                                     // DW with splits: [splits][sets][M][N]
+    float* shares;                                     // DX, DW: [2 workers][rows of a tile][its columns]
     const float* scale;                                // fp16: what dg and du are multiplied by, and its inverse
     unsigned long long wait_ns;
     int skip;                                          // test hook: nothing is loaded
@@ -159,23 +160,50 @@ template <typename T> __device__ __forceinline__ uint32_t idesc2(int M, int N, b
     return idesc<T>(M, N, b_mn) | ((a_mn ? 1u : 0u) << 15);
 }
 
-// A tile's place. Tiles of a column follow one another in groups of 16 rows of tiles, so that those in work at a time
-// share their operands in the cache.
+// A tile's place. Tiles of a column follow one another in groups of some rows of tiles, so that those in work at a time are
+// a block of about nine columns, or all of fewer, and share their operands in the cache: 8192 x 2048 from 2 x 4096 features read
+// 397 MB from memory in groups of 16 rows, three times what there is.
 struct Tile {
-    int m, n, set, split, first, last;   // blocks [first, last) of the sum
-    __device__ __forceinline__ Tile(const Params& p, int t) {
+    int m, n, set, first, last;   // blocks [first, last) of the sum
+    int share;                    // where a part of a sum goes, or -1
+    __device__ __forceinline__ void place(const Params& p, int t) {
         const int per = p.tiles_m * p.tiles_n;
-        split = t / (per * p.sets);
-        t %= per * p.sets;
-        set = p.set0 + t / per;
-        t %= per;
-        constexpr int G = 16;
-        const int group = t / (G * p.tiles_n), rows = min(G, p.tiles_m - group * G), in = t - group * G * p.tiles_n;
-        m = group * G + in % rows;
+        set = t / per;
+        t -= set * per;
+        set += p.set0;
+        const int G = p.group, group = t / (G * p.tiles_n), rows = min(G, p.tiles_m - group * G), in = t - group * G * p.tiles_n;
         n = in / rows;
+        m = group * G + in - n * rows;
+    }
+};
+// What a worker (a CTA, or a pair) does: every workers-th of the whole tiles, as many as all have alike, and a part of the
+// blocks of those that are left, which all share evenly: the end of one tile's sum and the beginning of the next one's at the most.
+// Parts go to memory in fp32 and are added up, in the workers' order, by a launch of their own.
+struct Work {
+    const Params& p;
+    int t, stride, share;
+    long long u, end;
+    __device__ __forceinline__ Work(const Params& p_, int worker, int workers) : p(p_), t(worker), stride(workers), share(2 * worker), u(0), end(0) {
+        const long long units = (long long)(p.tiles - p.whole) * p.segs * p.blocks;
+        if (worker < p.workers) u = units * worker / p.workers, end = units * (worker + 1) / p.workers;
+    }
+    __device__ __forceinline__ bool next(Tile& tile) {
         const int total = p.segs * p.blocks;
-        first = (int)((long long)total * split / p.splits);
-        last = (int)((long long)total * (split + 1) / p.splits);
+        if (t < p.whole) {
+            tile.place(p, t);
+            tile.first = 0, tile.last = total, tile.share = -1;
+            t += stride;
+            return true;
+        }
+        if (u >= end) return false;
+        const int k = (int)(u / total);
+        tile.place(p, p.whole + k);
+        tile.first = (int)(u - (long long)k * total);
+        tile.last = (int)min((long long)total, tile.first + (end - u));
+        tile.share = tile.first == 0 && tile.last == total ? -1 : share;
+        ++share;
+        u += tile.last - tile.first;
+        return true;
     }
 };
 
@@ -281,6 +309,35 @@ __device__ __forceinline__ void get_chunk(uint32_t area, float (&v)[32], const O
         }
     }
 }
+// The same in two steps, 16-bit elements at aligned 16 bytes: on their way, and taken.
+template <typename O> __device__ __forceinline__ void ask_chunk(uint4 (&w)[4], const O* in, long long ld, int rows, int cols, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = i * 8 + lane / 4, q = lane % 4;
+        w[i] = row < rows && q * 8 < cols ? *reinterpret_cast<const uint4*>(in + row * ld + q * 8) : make_uint4(0, 0, 0, 0);
+    }
+}
+template <typename O> __device__ __forceinline__ void take_chunk(uint32_t area, const uint4 (&w)[4], float (&v)[32], int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        st_shared16(chunk_at<O>(area, i * 8 + lane / 4, lane % 4), u);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t u[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                     : "r"(chunk_at<O>(area, lane, q)));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const O* e = reinterpret_cast<const O*>(&u[k]);
+            v[q * 8 + 2 * k] = to_f32(e[0]);
+            v[q * 8 + 2 * k + 1] = to_f32(e[1]);
+        }
+    }
+}
 // Sums over the 32 lanes of each of v's entries; lane l receives that of entry l. 31 shuffles in a fixed order.
 __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 #pragma unroll
@@ -358,8 +415,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     if (warp == kLoad) {
         if (lane == 0 && !p.skip) {
             int i = 0;   // blocks sent for
-            for (int t = worker; t < p.tiles && ok; t += workers) {
-                const Tile tile(p, t);
+            Work work(p, worker, workers);
+            for (Tile tile; ok && work.next(tile);) {
                 const int row = tile.m * Sh::rows + rank * kRows;
                 for (int k = tile.first; k < tile.last; ++k, ++i) {
                     const int e = i % Sh::stages;
@@ -398,8 +455,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     } else if (warp == kIssue) {
         const uint32_t id = idesc2<O>(Sh::rows, NB, A_MN, B_MN);
         int i = 0, n = 0;
-        for (int t = worker; t < p.tiles && ok && rank == 0; t += workers) {
-            const Tile tile(p, t);
+        Work work(p, worker, workers);
+        for (Tile tile; ok && rank == 0 && work.next(tile);) {
             const int first = uniform(tile.first), last = uniform(tile.last);
             for (int k = first, in = 0; k < last; ++k, ++i) {   // in: of the run
                 if (in == 0) {
@@ -436,6 +493,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
         const float up = p.scale ? p.scale[0] : 1.f, down = p.scale ? p.scale[1] : 1.f;
+        const bool dh_packs = p.F % 8 == 0 && aligned16_dev(p.dh);
         // the accumulator has been read by this warp
         auto release = [&](int which) {
             fence_before_sync();
@@ -446,17 +504,29 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             }
         };
         int n = 0;
-        for (int t = worker; t < p.tiles; t += workers) {
-            const Tile tile(p, t);
+        Work work(p, worker, workers);
+        for (Tile tile; work.next(tile);) {
             const long long row0 = (long long)tile.m * Sh::rows + rank * kRows + quarter * 32;
             const int rows = (int)min(32ll, p.M - row0);
             const int limit = PAIR ? p.F : p.N;
+            // of dh, on its way before the accumulator is there
+            uint4 asked[4];
+            auto ask = [&](int c) {
+                const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
+                if constexpr (KIND == GRAD && sizeof(T) == 2)
+                    if (dh_packs && c < WIDTH / 32 && rows > 0 && cols > 0) ask_chunk<T>(asked, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols, lane);
+            };
             // 32 columns of the result from the accumulators
             auto finish = [&](int c, float (&g)[32], float (&u)[32]) {
                 const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
                 if (rows <= 0 || cols <= 0) return;
                 float dh[32];
-                if constexpr (KIND == GRAD)
+                if (KIND == GRAD && sizeof(T) == 2 && dh_packs) {
+                    if constexpr (sizeof(T) == 2) {
+                        take_chunk<T>(area, asked, dh, lane);
+                        ask(c + 2);
+                    }
+                } else if constexpr (KIND == GRAD)
                     get_chunk<T>(area, dh, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols,
                                  p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh), lane);
                 if constexpr (PAIR) {
@@ -507,9 +577,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                             if (lane < cols) p.sums[row0 / 32 * 2 * p.F + which * p.F + col + lane] = s;
                         }
                     }
-                } else if (KIND == DW && p.splits > 1) {
-                    float* out = p.shares + (((long long)tile.split * p.sets + tile.set - p.set0) * p.M + row0) * p.N + col;
-                    put_chunk<float>(area, g, out, p.N, rows, cols, p.N % 4 == 0, lane);
+                } else if ((KIND == DX || KIND == DW) && tile.share >= 0) {
+                    float* out = p.shares + ((long long)tile.share * Sh::rows + rank * kRows + quarter * 32) * NB + c * 32;
+                    put_chunk<float>(area, g, out, NB, rows, cols, true, lane);
                 } else {
                     T* base = static_cast<T*>(p.out[KIND == DW ? tile.set : 0]);
                     if (base) put_chunk<T>(area, g, base + row0 * limit + col, limit, rows, cols, limit % (16 / (int)sizeof(T)) == 0 && aligned16_dev(base), lane);
@@ -546,6 +616,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                     for (int c = 0; c < C; ++c) finish(half + 2 * c, g[c], PAIR ? u[c] : g[c]);
                 }
             } else {
+                ask(half);
                 const uint32_t acc = await();
 #pragma unroll 1
                 for (int c = half; c < WIDTH / 32; c += 2) {
@@ -569,20 +640,96 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     }
 }
 
+// dx, or a weight's gradient, of the tiles whose sums were shared
+template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_kernel(const __grid_constant__ Params p)
+{
+    after_previous();
+    constexpr int ROWS = Shape<NB>::rows, PIECES = ROWS * NB / 4 / 256;   // of four columns, a thread
+    Tile tile;
+    tile.place(p, p.whole + blockIdx.x);
+    T* out = static_cast<T*>(p.out[tile.set]);
+    if (!out) return;
+    const long long total = (long long)p.segs * p.blocks, units = (p.tiles - p.whole) * total, lo = blockIdx.x * total, hi = lo + total;
+    auto start = [&](long long w) { return units * w / p.workers; };
+    long long w0 = lo * p.workers / units, w1 = hi * p.workers / units;   // the first worker with a part of it, and the one behind the last
+    while (w0 > 0 && start(w0) > lo) --w0;
+    while (start(w0 + 1) <= lo) ++w0;
+    while (w1 > w0 + 1 && start(w1 - 1) >= hi) --w1;
+    while (w1 < p.workers && start(w1) < hi) ++w1;
+    if (w1 == w0 + 1 && start(w0) <= lo) return;           // it alone: written whole
+    // a worker's first part is of the tile that its range begins in
+    const float* first = p.shares + (2 * w0 + (start(w0) < lo ? 1 : 0)) * ROWS * NB;
+    const float* others = p.shares + 2 * (w0 + 1) * ROWS * NB;
+    const int count = (int)(w1 - w0 - 1);
+    const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0;
+    for (int k = blockIdx.y; k < PIECES; k += gridDim.y) {
+        const int e = (k * 256 + threadIdx.x) * 4, r = e / NB, c = e % NB;
+        const long long row = (long long)tile.m * ROWS + r;
+        const int col = tile.n * NB + c;
+        if (row >= p.M || col >= p.N) continue;
+        float4 s = *reinterpret_cast<const float4*>(first + e);
+#pragma unroll 8
+        for (int w = 0; w < count; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(others + 2ll * w * ROWS * NB + e);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        T* to = out + row * p.N + col;
+        if (vec) {
+            Pack<T, 4> v;
+            v.e[0] = from_f32<T>(s.x), v.e[1] = from_f32<T>(s.y), v.e[2] = from_f32<T>(s.z), v.e[3] = from_f32<T>(s.w);
+            *reinterpret_cast<Pack<T, 4>*>(to) = v;
+        } else {
+            const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < p.N) to[j] = from_f32<T>(v[j]);
+        }
+    }
+}
+
+// How many tiles there are and how they are shared out. Sharing pays where the blocks that it saves the last round take longer
+// than the shares' way through memory and another launch. Returns about how long it all takes, in us: a block takes 0.34 at 256
+// columns, 0.22 and 0.15 at 128 and 64 (loads bound these), a tile 1.5 besides.
+inline double share_out(Params& p, int rows, int width, int nb, int workers, bool share)
+{
+    p.tiles_m = (int)((p.M + rows - 1) / rows), p.tiles_n = (p.N + width - 1) / width;
+    const int side = std::min(p.tiles_n, 9);
+    p.group = (workers + side - 1) / side;
+    p.tiles = p.tiles_m * p.tiles_n * p.sets;
+    p.whole = p.tiles, p.workers = 0;
+    const int left = p.tiles % workers, rounds = p.tiles / workers;
+    const long long total = (long long)p.segs * p.blocks;
+    const double block = nb == 256 ? 0.34 : nb == 128 ? 0.22 : 0.15, whole = rounds * (1.5 + block * (double)total);
+    const double last = left ? 1.5 + block * (double)total : 0.;
+    if (!share || left == 0) return whole + last;
+    const int sharers = (int)std::max<long long>(left, std::min<long long>(workers, left * total / 4));   // four blocks at the least
+    const double shared = 1.5 + block * (double)((left * total + sharers - 1) / sharers) + 5. + 4e-6 * sharers * rows * width * sizeof(float) / 8.;
+    if (shared >= last) return whole + last;
+    p.whole = p.tiles - left, p.workers = sharers;
+    return whole + shared;
+}
+inline size_t share_bytes(const Params& p, int rows, int width) { return p.workers ? (size_t)2 * p.workers * rows * width * sizeof(float) : 0; }
+
 template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cudaStream_t s)
 {
     using Sh = Shape<NB>;
     if (const cudaError_t e = allow_smem<gated_tc_kernel<KIND, T, NB>>(Sh::smem); e != cudaSuccess) return e;
-    p.tiles_m = (int)((p.M + Sh::rows - 1) / Sh::rows);
-    p.tiles_n = (p.N + (KIND == FWD || KIND == GRAD ? NB / 2 : NB) - 1) / (KIND == FWD || KIND == GRAD ? NB / 2 : NB);
-    p.tiles = p.tiles_m * p.tiles_n * p.sets * p.splits;
+    const int workers = sms / Sh::ctas;
+    share_out(p, Sh::rows, KIND == FWD || KIND == GRAD ? NB / 2 : NB, NB, workers, KIND == DX || KIND == DW);
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = Sh::ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.gridDim = dim3((unsigned)(std::min(p.tiles, sms / Sh::ctas) * Sh::ctas)), c.blockDim = dim3(kThreadsG), c.dynamicSmemBytes = Sh::smem;
+    const int busy = p.whole ? std::max(std::min(p.whole, workers), p.workers) : p.workers;
+    c.gridDim = dim3((unsigned)(busy * Sh::ctas)), c.blockDim = dim3(kThreadsG), c.dynamicSmemBytes = Sh::smem;
     c.stream = s, c.attrs = &at, c.numAttrs = Sh::ctas > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&c, gated_tc_kernel<KIND, T, NB>, (const Params&)p);
+    const cudaError_t e = cudaLaunchKernelEx(&c, gated_tc_kernel<KIND, T, NB>, (const Params&)p);
+    if constexpr (KIND == DX || KIND == DW)
+        if (e == cudaSuccess && p.workers) {
+            const int tiles = p.tiles - p.whole, pieces = Sh::rows * NB / 4 / 256;
+            return launch_behind(gated_join_kernel<T, NB>, dim3((unsigned)tiles, (unsigned)std::min(pieces, std::max(1, 8 * sms / tiles))), 256, s, p);
+        }
+    return e;
 }
 template <int KIND, typename T> cudaError_t run_nb(Params& p, int NB, int sms, cudaStream_t s)
 {
