@@ -54,24 +54,29 @@ template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_k
         return r < rows && k < a.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + r * stride + k) : zero;
     };
     float acc[2][NT][4] = {};
-#pragma unroll 4
-    for (int k0 = warp * 32; k0 < a.K; k0 += 256) {
-        const int k = k0 + at;
-        uint4 w[2][2], x[NT];
+    constexpr int AHEAD = NT == 4 ? 2 : 4;   // pieces whose loads are all on their way before the first product
+    for (int k0 = warp * 32; k0 < a.K; k0 += 256 * AHEAD) {
+        uint4 w[AHEAD][2][2], x[AHEAD][NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[0][h] = load(a.gate_weight, a.gate_stride, f0 + row + 8 * h, a.F, k);
-            w[1][h] = load(a.up_weight, a.up_stride, f0 + row + 8 * h, a.F, k);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = k0 + i * 256 + at;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[i][0][h] = load(a.gate_weight, a.gate_stride, f0 + row + 8 * h, a.F, k);
+                w[i][1][h] = load(a.up_weight, a.up_stride, f0 + row + 8 * h, a.F, k);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[i][t] = load(a.x, a.x_stride, t * 8 + row, R, k);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = load(a.x, a.x_stride, t * 8 + row, R, k);
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma16816<T>(acc[m][t], w[m][0].x, w[m][1].x, w[m][0].y, w[m][1].y, x[t].x, x[t].y);
-                mma16816<T>(acc[m][t], w[m][0].z, w[m][1].z, w[m][0].w, w[m][1].w, x[t].z, x[t].w);
-            }
+                for (int t = 0; t < NT; ++t) {
+                    mma16816<T>(acc[m][t], w[i][m][0].x, w[i][m][1].x, w[i][m][0].y, w[i][m][1].y, x[i][t].x, x[i][t].y);
+                    mma16816<T>(acc[m][t], w[i][m][0].z, w[i][m][1].z, w[i][m][0].w, w[i][m][1].w, x[i][t].z, x[i][t].w);
+                }
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -136,33 +141,47 @@ struct PackJob {
     const void* from[3];
     uint16_t* to[3];
     long long stride[3], rows[3];
-    int first[4];    // CTAs of a job; a CTA has 8 rows
+    int first[4];    // CTAs of a job; a CTA has kPackQuads times four columns, one row after the other
+    bool quads[3];   // four columns are one aligned load
     int cols, pitch;
 };
+constexpr int kPackQuads = 1024;
 template <typename T> __global__ void __launch_bounds__(256) gated_pack_kernel(const PackJob j)
 {
     using O = typename gtc::Operand<T>::type;
     int w = 0;
     while (w < 2 && (int)blockIdx.x >= j.first[w + 1]) ++w;
-    const long long r = (long long)(blockIdx.x - j.first[w]) * 8 + (threadIdx.x >> 5);
-    if (r >= j.rows[w]) return;
-    const T* from = static_cast<const T*>(j.from[w]) + r * j.stride[w];
-    const long long part = j.rows[w] * j.pitch;
-    O* to = reinterpret_cast<O*>(j.to[w]) + r * j.pitch;
-    for (int c = (threadIdx.x & 31) * 2; c < j.cols; c += 64) {   // the pitch is even
-        float x = to_f32(from[c]), y = c + 1 < j.cols ? to_f32(from[c + 1]) : 0.f;
+    const int across = (j.cols + 3) / 4;
+    const long long part = j.rows[w] * j.pitch, quads = j.rows[w] * across;
+#pragma unroll
+    for (int i = 0; i < kPackQuads / 256; ++i) {
+        const long long q = (long long)(blockIdx.x - j.first[w]) * kPackQuads + i * 256 + threadIdx.x;
+        if (q >= quads) return;
+        const long long r = q / across;
+        const int c = (int)(q - r * across) * 4;
+        const T* from = static_cast<const T*>(j.from[w]) + r * j.stride[w] + c;
+        O* to = reinterpret_cast<O*>(j.to[w]) + r * j.pitch + c;   // the pitch is a multiple of eight: four are always there
+        float v[4];
+        if (j.quads[w]) {
+            const Pack<T, 4> p = *reinterpret_cast<const Pack<T, 4>*>(from);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = to_f32(p.e[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = c + e < j.cols ? to_f32(from[e]) : 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < kParts<T>; ++k) {
-            const uint32_t v = pack2<O>(x, y);
-            *reinterpret_cast<uint32_t*>(to + k * part + c) = v;
-            const O* e = reinterpret_cast<const O*>(&v);
-            x -= to_f32(e[0]), y -= to_f32(e[1]);
+            const uint2 u = make_uint2(pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3]));
+            *reinterpret_cast<uint2*>(to + k * part) = u;
+            const O* e = reinterpret_cast<const O*>(&u);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] -= to_f32(e[z]);
         }
     }
 }
 
-// ---- fp16: dg and du are kept times a power of two that brings the largest |dh| to [1/4, 1/2), so that small upstream
-// gradients do not end among fp16's subnormal numbers. The maximum of bit patterns does not depend on their order.
+// ---- fp16: the largest |dh|. The maximum of bit patterns does not depend on their order.
 __global__ void __launch_bounds__(256) gated_top_kernel(const __half* dh, long long n, unsigned* top)
 {
     unsigned m = 0;
@@ -171,15 +190,6 @@ __global__ void __launch_bounds__(256) gated_top_kernel(const __half* dh, long l
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) atomicMax(top, m);
 }
-__global__ void gated_scale_kernel(const unsigned* top, float* scale)
-{
-    const float m = __half2float(__ushort_as_half((unsigned short)*top));
-    int e = 0;
-    if (m > 0.f && m < INFINITY) frexpf(m, &e);   // m = f 2^e, 1/2 <= f < 1
-    scale[0] = m > 0.f && m < INFINITY ? exp2f((float)(-1 - e)) : 1.f;
-    scale[1] = 1.f / scale[0];
-}
-
 // ---- column sums of row tiles, added in a fixed order
 template <typename T> __global__ void __launch_bounds__(1024) gated_bias_kernel(const float* sums, long long n, int F, T* dgate, T* dup)
 {
@@ -230,7 +240,8 @@ struct Plan {
     Image x, w[2], grads;
     PackJob pack;
     int pack_ctas = 0;
-    float *sums = nullptr, *shares = nullptr, *scale = nullptr;
+    float *sums = nullptr, *shares = nullptr;
+    unsigned* top = nullptr;
     int dx_nb = 256, dw_nb = 256;
     size_t bytes = 0;
 };
@@ -268,7 +279,8 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
         uint16_t* to = reinterpret_cast<uint16_t*>(carve((size_t)parts * rows * j.pitch * 2));
         j.from[jobs] = from, j.to[jobs] = to, j.stride[jobs] = stride, j.rows[jobs] = rows;
         j.first[jobs] = plan.pack_ctas;
-        plan.pack_ctas += (int)((rows + 7) / 8);
+        j.quads[jobs] = a.K % 4 == 0 && stride % 4 == 0 && reinterpret_cast<uintptr_t>(from) % (4 * dtype_size(a.dtype)) == 0;
+        plan.pack_ctas += (int)((rows * ((a.K + 3) / 4) + kPackQuads - 1) / kPackQuads);
         for (int k = ++jobs; k < 4; ++k) j.first[k] = plan.pack_ctas;
         return Image{to, j.pitch, rows, a.K, parts};
     };
@@ -279,16 +291,16 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
     const long long pitch = (a.F + 7) / 8 * 8;
     plan.grads = Image{carve((size_t)2 * parts * a.R * pitch * 2), pitch, a.R, a.F, 2 * parts};
     plan.sums = reinterpret_cast<float*>(carve((size_t)tiles_of(a.R, 32) * 2 * a.F * sizeof(float)));
-    plan.scale = reinterpret_cast<float*>(carve(256));
+    plan.top = reinterpret_cast<unsigned*>(carve(sizeof(unsigned)));
     // Columns of dx's and the weights' accumulators, by the least time, and room for their shares; one of the weights'
     // gradients alone may share its sums otherwise than both.
     size_t shares = 0;
     auto time = [&](int sets, int nb, size_t& bytes) {   // sets 0: dx
         const int ctas = nb == 256 ? 2 : 1;
         gtc::Params g{};
-        g.segs = (parts == 3 ? 6 : 1) * (sets ? 1 : 2), g.blocks = sets ? tiles_of(a.R, 64) : tiles_of(a.F, 64);
+        g.segs = sets ? 1 : 2, g.blocks = sets ? tiles_of(a.R, 64) : tiles_of(a.F, 64);
         g.sets = sets ? sets : 1, g.M = sets ? a.F : a.R, g.N = a.K;
-        const double t = gtc::share_out(g, 128 * ctas, nb, nb, sms / ctas, true);
+        const double t = gtc::share_out(g, 128 * ctas, nb, nb, parts, sms / ctas, true);
         bytes = gtc::share_bytes(g, 128 * ctas, nb);
         return t;
     };
@@ -309,15 +321,6 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
     return plan;
 }
 
-// The pieces of a sum: pairs of parts, smallest products first.
-constexpr unsigned char kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
-void set_segs(gtc::Params& g, int parts, bool both)
-{
-    g.segs = 0;
-    for (int k = parts == 3 ? 0 : 5; k < 6; ++k)
-        for (int m = 0; m < (both ? 2 : 1); ++m) g.seg[g.segs++] = gtc::Seg{(unsigned char)(kPairs[k][0] + m * parts), (unsigned char)m, kPairs[k][1]};
-}
-
 cudaError_t pack_operands(const GatedParams& p, const Plan& plan, cudaStream_t s)
 {
     if (!plan.pack_ctas) return cudaSuccess;
@@ -335,14 +338,13 @@ cudaError_t products(const GatedParams& p, const Plan& plan, bool grads, bool wa
     const int nb = pick_nb(a.R, a.F, 1, sms, true, a.dtype), width = nb / 2;
     if (!plan.x.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, width) || !plan.w[1].map(&g.b[1], a.dtype, 64, width))
         return cudaErrorInvalidValue;
-    set_segs(g, plan.x.parts, false);
-    g.blocks = tiles_of(a.K, 64);
+    g.segs = 1, g.blocks = tiles_of(a.K, 64);
     g.sets = 1;
     g.M = a.R, g.N = g.F = a.F, g.activation = a.activation;
     g.out[0] = p.h, g.bias[0] = a.gate_bias, g.bias[1] = a.up_bias, g.dh = p.dh;
     g.grads = static_cast<uint16_t*>(const_cast<void*>(plan.grads.p)), g.ld = plan.grads.pitch;
     g.sums = want_sums ? plan.sums : nullptr;
-    g.scale = grads && a.dtype == SDTW_F16 ? plan.scale : nullptr;
+    g.top = grads && a.dtype == SDTW_F16 ? plan.top : nullptr;
     g.wait_ns = p.wait_ns, g.skip = p.skip;
     return grads ? gtc::run_grad(g, a.dtype, nb, sms, s) : gtc::run_fwd(g, a.dtype, nb, sms, s);
 }
@@ -387,21 +389,18 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
     cudaError_t e = pack_operands(p, plan, s);
     if (e != cudaSuccess) return e;
     if (a.dtype == SDTW_F16) {
-        unsigned* top = reinterpret_cast<unsigned*>(plan.scale + 2);
-        if ((e = cudaMemsetAsync(top, 0, sizeof(unsigned), s)) != cudaSuccess) return e;
-        gated_top_kernel<<<(unsigned)std::min(a.R * a.F / 2048 + 1, (long long)sms * 8), 256, 0, s>>>(static_cast<const __half*>(p.dh), a.R * a.F, top);
-        gated_scale_kernel<<<1, 1, 0, s>>>(top, plan.scale);
+        if ((e = cudaMemsetAsync(plan.top, 0, sizeof(unsigned), s)) != cudaSuccess) return e;
+        gated_top_kernel<<<(unsigned)std::min(a.R * a.F / 2048 + 1, (long long)sms * 8), 256, 0, s>>>(static_cast<const __half*>(p.dh), a.R * a.F, plan.top);
     }
     const bool biases = p.dgate_bias || p.dup_bias;
     if ((e = products(p, plan, true, biases, sms, s)) != cudaSuccess) return e;
     gtc::Params g{};
-    g.scale = a.dtype == SDTW_F16 ? plan.scale : nullptr;
+    g.top = a.dtype == SDTW_F16 ? plan.top : nullptr;
     g.wait_ns = p.wait_ns;
     if (p.dx) {
         if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, 64) || !plan.w[1].map(&g.b[1], a.dtype, 64, 64))
             return cudaErrorInvalidValue;
-        set_segs(g, parts, true);
-        g.blocks = tiles_of(a.F, 64);
+        g.segs = 2, g.seg[1] = gtc::Seg{(unsigned char)parts, 1}, g.blocks = tiles_of(a.F, 64);
         g.sets = 1, g.set0 = 0;
         g.M = a.R, g.N = a.K, g.out[0] = p.dx, g.shares = plan.shares;
         if ((e = gtc::run_dx(g, a.dtype, plan.dx_nb, sms, s)) != cudaSuccess) return e;
@@ -409,8 +408,7 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
     if (p.dgate_weight || p.dup_weight) {
         if (!plan.grads.map(&g.a, a.dtype, 64, 64) || !plan.x.map(&g.b[0], a.dtype, 64, 64)) return cudaErrorInvalidValue;
         g.b[1] = g.b[0];
-        set_segs(g, parts, false);
-        g.blocks = tiles_of(a.R, 64);
+        g.segs = 1, g.blocks = tiles_of(a.R, 64);
         g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1;
         g.M = a.F, g.N = a.K, g.out[0] = p.dgate_weight, g.out[1] = p.dup_weight, g.shares = plan.shares;
         if ((e = gtc::run_dw(g, a.dtype, plan.dw_nb, sms, s)) != cudaSuccess) return e;

@@ -9,9 +9,10 @@
 // a tensor map leaves out (rows, features, the tail of the sum) arrives as zeros. x, dg and W lie along their rows, so
 // that a sum over features has K-major operands and a sum over rows MN-major ones: no operand is transposed in memory.
 // fp32 operands are split into three bf16 parts, v = v0 + v1 + v2 to 24 bits, and a product is the sum of the six part products
-// above 2^-24 of it, (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first, as one longer sum. The tensor cores cut off what an
-// addition leaves below the accumulator's last bit, always towards 0: over a sum of 6000 terms that came to 250 times the
-// result's own rounding. Sums of fp32 are so taken in runs of 256 terms, which are added up in registers, rounded to nearest.
+// above 2^-24 of it, (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first. A block of either operand comes with all its parts. The
+// tensor cores cut off what an addition leaves below the accumulator's last bit, always towards 0: over a sum of 6000 terms
+// that came to 250 times the result's own rounding. Sums of fp32 so leave the accumulator after every block of 64 terms and
+// are added up in registers, rounded to nearest.
 //
 // A persistent CTA: a loading warp, an issuing warp, and eight warps that turn a finished accumulator into results while
 // the next one is summed (two accumulators in tensor memory). Large calls take pairs of CTAs (cta_group::2) with 256 rows and 256
@@ -19,6 +20,7 @@
 // first of a pair issues for both.
 #pragma once
 #include <algorithm>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "attn_tc.cuh"
@@ -34,14 +36,14 @@ enum Kind { FWD, GRAD, DX, DW };
 constexpr int kRows = 128, kBlock = 64;               // rows of a tile; length of a block of the sum
 constexpr uint32_t kABytes = kRows * kBlock * 2;
 
-// One piece of the sum: part of A, map and part of B.
+// One piece of the sum: the first part of A, and the map of B.
 struct Seg {
-    unsigned char a, map, b;
+    unsigned char a, map;
 };
 
 struct alignas(64) Params {
     CUtensorMap a, b[2];
-    Seg seg[12];
+    Seg seg[2];
     int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks
     int tiles_m, tiles_n, group, set0, sets, tiles;    // sets: DW's weights, from set0 on
     int whole, workers;                                // tiles summed whole; workers that share the others' sums (below)
@@ -54,7 +56,7 @@ struct alignas(64) Params {
     long long ld;
     float* sums;                                       // GRAD, with biases: [M / 32][2 F] column sums of 32 rows
     float* shares;                                     // DX, DW: [2 workers][rows of a tile][its columns]
-    const float* scale;                                // fp16: what dg and du are multiplied by, and its inverse
+    const unsigned* top;                               // fp16: bits of the largest |dh|, by which dg and du are scaled
     unsigned long long wait_ns;
     int skip;                                          // test hook: nothing is loaded
 };
@@ -63,13 +65,13 @@ struct alignas(64) Params {
 template <typename T> struct Operand { using type = T; };
 template <> struct Operand<float> { using type = __nv_bfloat16; };
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-template <typename T> constexpr int kRun = sizeof(T) == 4 ? 4 : 1 << 30;   // blocks that one accumulator takes
+template <typename T> constexpr int kRun = sizeof(T) == 4 ? 1 : 1 << 30;   // blocks that one accumulator takes
 
-template <int NB> struct Shape {
+template <int NB, int PARTS> struct Shape {
     static constexpr int ctas = NB == 256 ? 2 : 1;     // that share a tile
-    static constexpr uint32_t b_bytes = NB / ctas * kBlock * 2, stage = kABytes + b_bytes;   // of a CTA
+    static constexpr uint32_t b_bytes = NB / ctas * kBlock * 2, stage = PARTS * (kABytes + b_bytes);   // of a CTA
     static constexpr uint32_t area = 4096;             // of shared memory, a warp's own
-    static constexpr int stages = NB == 64 ? 7 : 6;
+    static constexpr int stages = PARTS > 1 ? 2 : NB == 64 ? 7 : 6;
     static constexpr uint32_t smem = stages * stage + 8 * area;
     static constexpr int columns = 2 * NB;             // of tensor memory
     static constexpr int rows = ctas * kRows;          // of a tile
@@ -385,7 +387,8 @@ template <bool EXACT, bool GRADS> __device__ __forceinline__ void gate_by(int ac
 template <int KIND, typename T, int NB>
 __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_constant__ Params p)
 {
-    using Sh = Shape<NB>;
+    constexpr int PARTS = kParts<T>;
+    using Sh = Shape<NB, PARTS>;
     using O = typename Operand<T>::type;
     constexpr bool PAIR = KIND == FWD || KIND == GRAD, A_MN = KIND == DW, B_MN = KIND == DX || KIND == DW;
     constexpr int WIDTH = PAIR ? NB / 2 : NB;             // columns of a tile's result
@@ -424,25 +427,29 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                     if (!ok) break;
                     const Seg sg = p.seg[k / p.blocks];
                     const int at = k % p.blocks * kBlock;
-                    const uint32_t mine = smem_u32(&s_full[e]), a = ring + e * Sh::stage, b = a + kABytes;
-                    const uint32_t bar = CTAS == 2 ? in_cta(mine, 0) : mine;
+                    const uint32_t mine = smem_u32(&s_full[e]), bar = CTAS == 2 ? in_cta(mine, 0) : mine;
                     if (rank == 0) mbar_expect_tx(mine, CTAS * Sh::stage);
-                    if constexpr (A_MN) {
 #pragma unroll
-                        for (int c = 0; c < kRows / 64; ++c)
-                            load3<CTAS>(a + c * kBlock * 128, &p.a, row + c * 64, at, sg.a + tile.set * kParts<T>, bar);
-                    } else {
-                        load3<CTAS>(a, &p.a, at, row, sg.a, bar);
-                    }
-                    if constexpr (PAIR && CTAS == 2) {   // the first CTA has the gate's weights, the second the others
-                        load3<CTAS>(b, &p.b[rank], at, tile.n * WIDTH, sg.b, bar);
-                    } else if constexpr (PAIR) {
-                        load3<CTAS>(b, &p.b[0], at, tile.n * WIDTH, sg.b, bar);
-                        load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, sg.b, bar);
-                    } else {
+                    for (int part = 0; part < PARTS; ++part) {
+                        const uint32_t a = ring + e * Sh::stage + part * kABytes;
+                        const uint32_t b = ring + e * Sh::stage + PARTS * kABytes + part * Sh::b_bytes;
+                        if constexpr (A_MN) {
 #pragma unroll
-                        for (int c = 0; c < NB / CTAS / 64; ++c)
-                            load3<CTAS>(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + rank * (NB / CTAS) + c * 64, at, sg.b, bar);
+                            for (int c = 0; c < kRows / 64; ++c)
+                                load3<CTAS>(a + c * kBlock * 128, &p.a, row + c * 64, at, sg.a + tile.set * PARTS + part, bar);
+                        } else {
+                            load3<CTAS>(a, &p.a, at, row, sg.a + part, bar);
+                        }
+                        if constexpr (PAIR && CTAS == 2) {   // the first CTA has the gate's weights, the second the others
+                            load3<CTAS>(b, &p.b[rank], at, tile.n * WIDTH, part, bar);
+                        } else if constexpr (PAIR) {
+                            load3<CTAS>(b, &p.b[0], at, tile.n * WIDTH, part, bar);
+                            load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, part, bar);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < NB / CTAS / 64; ++c)
+                                load3<CTAS>(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + rank * (NB / CTAS) + c * 64, at, part, bar);
+                        }
                     }
                 }
             }
@@ -469,11 +476,17 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                 wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, late);
                 fence_after_sync();
                 if (ok && elect_one()) {
-                    const uint32_t a = ring + e * Sh::stage, b = a + kABytes;
-                    const uint64_t ad = A_MN ? desc_mn(a) : sdesc(a), bd = B_MN ? desc_mn(b) : sdesc(b);
+                    // pairs of parts, the smallest products first
+                    constexpr int PAIRS = PARTS == 3 ? 6 : 1, PA[6] = {0, 2, 1, 0, 1, 0}, PB[6] = {2, 0, 1, 1, 0, 0};
 #pragma unroll
-                    for (int s = 0; s < kBlock / 16; ++s)   // 16 of the sum: 32 bytes along a row, or 16 rows
-                        mma<CTAS>(d, ad + s * (A_MN ? 128 : 2), bd + s * (B_MN ? 128 : 2), id, in > 0 || s > 0 ? 1u : 0u);
+                    for (int q = 0; q < PAIRS; ++q) {
+                        const uint32_t a = ring + e * Sh::stage + (PARTS == 3 ? PA[q] : 0) * kABytes;
+                        const uint32_t b = ring + e * Sh::stage + PARTS * kABytes + (PARTS == 3 ? PB[q] : 0) * Sh::b_bytes;
+                        const uint64_t ad = A_MN ? desc_mn(a) : sdesc(a), bd = B_MN ? desc_mn(b) : sdesc(b);
+#pragma unroll
+                        for (int s = 0; s < kBlock / 16; ++s)   // 16 of the sum: 32 bytes along a row, or 16 rows
+                            mma<CTAS>(d, ad + s * (A_MN ? 128 : 2), bd + s * (B_MN ? 128 : 2), id, in > 0 || q > 0 || s > 0 ? 1u : 0u);
+                    }
                     commit<CTAS>(smem_u32(&s_empty[e]));
                     if (ends) commit<CTAS>(smem_u32(&s_done[n & 1]));
                 }
@@ -492,7 +505,15 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     } else {
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
-        const float up = p.scale ? p.scale[0] : 1.f, down = p.scale ? p.scale[1] : 1.f;
+        // dg and du are kept times a power of two that brings the largest |dh| to [1/4, 1/2), so that small upstream gradients
+        // do not end among fp16's subnormal numbers
+        float up = 1.f;
+        if (std::is_same<T, __half>::value && p.top) {
+            const float top = __half2float(__ushort_as_half((unsigned short)*p.top));
+            int exponent = 0;
+            if (top > 0.f && top < INFINITY) frexpf(top, &exponent), up = ldexpf(1.f, -1 - exponent);
+        }
+        const float down = 1.f / up;
         const bool dh_packs = p.F % 8 == 0 && aligned16_dev(p.dh);
         // the accumulator has been read by this warp
         auto release = [&](int which) {
@@ -644,7 +665,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
 template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_kernel(const __grid_constant__ Params p)
 {
     after_previous();
-    constexpr int ROWS = Shape<NB>::rows, PIECES = ROWS * NB / 4 / 256;   // of four columns, a thread
+    constexpr int ROWS = Shape<NB, 1>::rows, PIECES = ROWS * NB / 4 / 64;   // of four columns, 64 at a time by four groups of threads
+    __shared__ float4 part[3][64];
+    const int group = threadIdx.x / 64, lane = threadIdx.x % 64;
     Tile tile;
     tile.place(p, p.whole + blockIdx.x);
     T* out = static_cast<T*>(p.out[tile.set]);
@@ -658,39 +681,47 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_
     while (w1 < p.workers && start(w1) < hi) ++w1;
     if (w1 == w0 + 1 && start(w0) <= lo) return;           // it alone: written whole
     // a worker's first part is of the tile that its range begins in
+    const int count = (int)(w1 - w0), per = (count + 3) / 4, from = min(group * per, count), to = min(from + per, count);
     const float* first = p.shares + (2 * w0 + (start(w0) < lo ? 1 : 0)) * ROWS * NB;
-    const float* others = p.shares + 2 * (w0 + 1) * ROWS * NB;
-    const int count = (int)(w1 - w0 - 1);
+    const float* parts = p.shares + 2 * w0 * ROWS * NB;
     const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0;
     for (int k = blockIdx.y; k < PIECES; k += gridDim.y) {
-        const int e = (k * 256 + threadIdx.x) * 4, r = e / NB, c = e % NB;
+        const int e = (k * 64 + lane) * 4, r = e / NB, c = e % NB;
         const long long row = (long long)tile.m * ROWS + r;
         const int col = tile.n * NB + c;
-        if (row >= p.M || col >= p.N) continue;
-        float4 s = *reinterpret_cast<const float4*>(first + e);
+        const bool in = row < p.M && col < p.N;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in) {
 #pragma unroll 8
-        for (int w = 0; w < count; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(others + 2ll * w * ROWS * NB + e);
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            for (int w = from; w < to; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>((w == 0 ? first : parts + 2ll * w * ROWS * NB) + e);
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
         }
-        T* to = out + row * p.N + col;
+        __syncthreads();
+        if (group > 0) part[group - 1][lane] = s;
+        __syncthreads();
+        if (group > 0 || !in) continue;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) s.x += part[g][lane].x, s.y += part[g][lane].y, s.z += part[g][lane].z, s.w += part[g][lane].w;
+        T* dst = out + row * p.N + col;
         if (vec) {
             Pack<T, 4> v;
             v.e[0] = from_f32<T>(s.x), v.e[1] = from_f32<T>(s.y), v.e[2] = from_f32<T>(s.z), v.e[3] = from_f32<T>(s.w);
-            *reinterpret_cast<Pack<T, 4>*>(to) = v;
+            *reinterpret_cast<Pack<T, 4>*>(dst) = v;
         } else {
             const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (col + j < p.N) to[j] = from_f32<T>(v[j]);
+                if (col + j < p.N) dst[j] = from_f32<T>(v[j]);
         }
     }
 }
 
 // How many tiles there are and how they are shared out. Sharing pays where the blocks that it saves the last round take longer
 // than the shares' way through memory and another launch. Returns about how long it all takes, in us: a block takes 0.34 at 256
-// columns, 0.22 and 0.15 at 128 and 64 (loads bound these), a tile 1.5 besides.
-inline double share_out(Params& p, int rows, int width, int nb, int workers, bool share)
+// columns, 0.22 and 0.15 at 128 and 64 (loads bound these), in three parts 1 and 0.7, a tile 1.5 besides.
+inline double share_out(Params& p, int rows, int width, int nb, int parts, int workers, bool share)
 {
     p.tiles_m = (int)((p.M + rows - 1) / rows), p.tiles_n = (p.N + width - 1) / width;
     const int side = std::min(p.tiles_n, 9);
@@ -699,10 +730,10 @@ inline double share_out(Params& p, int rows, int width, int nb, int workers, boo
     p.whole = p.tiles, p.workers = 0;
     const int left = p.tiles % workers, rounds = p.tiles / workers;
     const long long total = (long long)p.segs * p.blocks;
-    const double block = nb == 256 ? 0.34 : nb == 128 ? 0.22 : 0.15, whole = rounds * (1.5 + block * (double)total);
+    const double block = parts > 1 ? (nb == 128 ? 1. : 0.7) : nb == 256 ? 0.34 : nb == 128 ? 0.22 : 0.15, whole = rounds * (1.5 + block * (double)total);
     const double last = left ? 1.5 + block * (double)total : 0.;
     if (!share || left == 0) return whole + last;
-    const int sharers = (int)std::max<long long>(left, std::min<long long>(workers, left * total / 4));   // four blocks at the least
+    const int sharers = (int)std::max<long long>(left, std::min<long long>(workers, left * total / (parts > 1 ? 1 : 4)));   // four blocks at the least
     const double shared = 1.5 + block * (double)((left * total + sharers - 1) / sharers) + 5. + 4e-6 * sharers * rows * width * sizeof(float) / 8.;
     if (shared >= last) return whole + last;
     p.whole = p.tiles - left, p.workers = sharers;
@@ -712,10 +743,10 @@ inline size_t share_bytes(const Params& p, int rows, int width) { return p.worke
 
 template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cudaStream_t s)
 {
-    using Sh = Shape<NB>;
+    using Sh = Shape<NB, kParts<T>>;
     if (const cudaError_t e = allow_smem<gated_tc_kernel<KIND, T, NB>>(Sh::smem); e != cudaSuccess) return e;
     const int workers = sms / Sh::ctas;
-    share_out(p, Sh::rows, KIND == FWD || KIND == GRAD ? NB / 2 : NB, NB, workers, KIND == DX || KIND == DW);
+    share_out(p, Sh::rows, KIND == FWD || KIND == GRAD ? NB / 2 : NB, NB, kParts<T>, workers, KIND == DX || KIND == DW);
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -726,7 +757,7 @@ template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cuda
     const cudaError_t e = cudaLaunchKernelEx(&c, gated_tc_kernel<KIND, T, NB>, (const Params&)p);
     if constexpr (KIND == DX || KIND == DW)
         if (e == cudaSuccess && p.workers) {
-            const int tiles = p.tiles - p.whole, pieces = Sh::rows * NB / 4 / 256;
+            const int tiles = p.tiles - p.whole, pieces = Sh::rows * NB / 4 / 64;
             return launch_behind(gated_join_kernel<T, NB>, dim3((unsigned)tiles, (unsigned)std::min(pieces, std::max(1, 8 * sms / tiles))), 256, s, p);
         }
     return e;
