@@ -249,6 +249,7 @@ __device__ __forceinline__ void put_chunk(uint32_t area, const float (&v)[32], O
             if (row < rows && q * E < cols) *reinterpret_cast<uint4*>(out + row * ld + q * E) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
+#pragma unroll 4
         for (int row = 0; row < rows; ++row)
             if (lane < cols) {
                 if constexpr (sizeof(O) == 4) {
@@ -263,82 +264,63 @@ __device__ __forceinline__ void put_chunk(uint32_t area, const float (&v)[32], O
             }
     }
 }
-// what is not there is 0
-template <typename O>
-__device__ __forceinline__ void get_chunk(uint32_t area, float (&v)[32], const O* in, long long ld, int rows, int cols, bool vec, int lane)
-{
+// A lane's row
+template <typename O> __device__ __forceinline__ void read_chunk(uint32_t area, float (&v)[32], int lane) {
     constexpr int E = 16 / sizeof(O), P = 32 / E;
-    __syncwarp();
-    if (vec && cols % E == 0) {
-        uint4 w[P];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int row = i * (32 / P) + lane / P, q = lane % P;
-            w[i] = row < rows && q * E < cols ? *reinterpret_cast<const uint4*>(in + row * ld + q * E) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            st_shared16(chunk_at<O>(area, i * (32 / P) + lane / P, lane % P), u);
-        }
-    } else {
-        for (int row = 0; row < 32; ++row) {
-            const bool there = row < rows && lane < cols;
-            if constexpr (sizeof(O) == 4) {
-                const uint32_t w = there ? __float_as_uint(in[row * ld + lane]) : 0u;
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(element_at<O>(area, row, lane)), "r"(w) : "memory");
-            } else {
-                const uint16_t w = there ? reinterpret_cast<const uint16_t*>(in)[row * ld + lane] : (uint16_t)0;
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(element_at<O>(area, row, lane)), "h"(w) : "memory");
-            }
-        }
-    }
-    __syncwarp();
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+        uint32_t u[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
                      : "r"(chunk_at<O>(area, lane, q)));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if constexpr (sizeof(O) == 4) {
-                v[q * E + k] = __uint_as_float(w[k]);
+                v[q * E + k] = __uint_as_float(u[k]);
             } else {
-                const O* e = reinterpret_cast<const O*>(&w[k]);
+                const O* e = reinterpret_cast<const O*>(&u[k]);
                 v[q * E + 2 * k] = to_f32(e[0]);
                 v[q * E + 2 * k + 1] = to_f32(e[1]);
             }
         }
     }
 }
-// The same in two steps, 16-bit elements at aligned 16 bytes: on their way, and taken.
-template <typename O> __device__ __forceinline__ void ask_chunk(uint4 (&w)[4], const O* in, long long ld, int rows, int cols, int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = i * 8 + lane / 4, q = lane % 4;
-        w[i] = row < rows && q * 8 < cols ? *reinterpret_cast<const uint4*>(in + row * ld + q * 8) : make_uint4(0, 0, 0, 0);
-    }
-}
-template <typename O> __device__ __forceinline__ void take_chunk(uint32_t area, const uint4 (&w)[4], float (&v)[32], int lane) {
+// Element by element; what is not there is 0.
+template <typename O>
+__device__ __forceinline__ void get_chunk(uint32_t area, float (&v)[32], const O* in, long long ld, int rows, int cols, int lane)
+{
+    using Bits = typename std::conditional<sizeof(O) == 4, uint32_t, uint16_t>::type;
     __syncwarp();
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {   // eight rows on their way at a time
+        Bits w[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        st_shared16(chunk_at<O>(area, i * 8 + lane / 4, lane % 4), u);
-    }
-    __syncwarp();
+        for (int i = 0; i < 8; ++i) w[i] = r0 + i < rows && lane < cols ? reinterpret_cast<const Bits*>(in)[(r0 + i) * ld + lane] : Bits(0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t u[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                     : "r"(chunk_at<O>(area, lane, q)));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const O* e = reinterpret_cast<const O*>(&u[k]);
-            v[q * 8 + 2 * k] = to_f32(e[0]);
-            v[q * 8 + 2 * k + 1] = to_f32(e[1]);
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(O) == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(element_at<O>(area, r0 + i, lane)), "r"(w[i]) : "memory");
+            else asm volatile("st.shared.b16 [%0], %1;" ::"r"(element_at<O>(area, r0 + i, lane)), "h"(w[i]) : "memory");
         }
     }
+    __syncwarp();
+    read_chunk<O>(area, v, lane);
+}
+// The same of aligned 16 bytes, in two steps: on their way to the area, and taken from there.
+template <typename O> __device__ __forceinline__ void ask_chunk(uint32_t area, const O* in, long long ld, int rows, int cols, int lane) {
+    constexpr int E = 16 / sizeof(O), P = 32 / E;
+    __syncwarp();   // everyone has taken what was there
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int row = i * (32 / P) + lane / P, q = lane % P;
+        const bool there = row < rows && q * E < cols;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(chunk_at<O>(area, row, q)), "l"(there ? in + row * ld + q * E : in),
+                     "r"(there ? 16 : 0)
+                     : "memory");
+    }
+}
+template <typename O> __device__ __forceinline__ void take_chunk(uint32_t area, float (&v)[32], int lane) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    read_chunk<O>(area, v, lane);
 }
 // Sums over the 32 lanes of each of v's entries; lane l receives that of entry l. 31 shuffles in a fixed order.
 __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
@@ -353,11 +335,10 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
     return v[0];
 }
 
-template <typename T> __device__ __forceinline__ void add_bias(float (&v)[32], const void* bias, int f0, int cols) {
-    if (!bias) return;
+// Lane l has the bias of column l.
+__device__ __forceinline__ void add_bias(float (&v)[32], float bias) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < cols) v[j] += to_f32(static_cast<const T*>(bias)[f0 + j]);
+    for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
 }
 
 // h in place of g, or with dh the gradients of g and u in their places
@@ -514,7 +495,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             if (top > 0.f && top < INFINITY) frexpf(top, &exponent), up = ldexpf(1.f, -1 - exponent);
         }
         const float down = 1.f / up;
-        const bool dh_packs = p.F % 8 == 0 && aligned16_dev(p.dh);
+        // 16-bit pieces of dh have half of the area to themselves; fp32's are taken before results are put there
+        const uint32_t dh_area = sizeof(T) == 2 ? area + 2048 : area;
+        const bool dh_packs = p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh);
         // the accumulator has been read by this warp
         auto release = [&](int which) {
             fence_before_sync();
@@ -530,29 +513,31 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             const long long row0 = (long long)tile.m * Sh::rows + rank * kRows + quarter * 32;
             const int rows = (int)min(32ll, p.M - row0);
             const int limit = PAIR ? p.F : p.N;
-            // of dh, on its way before the accumulator is there
-            uint4 asked[4];
+            // what 32 columns take from memory, on its way before the accumulator is there
+            float bias[2] = {0.f, 0.f};
             auto ask = [&](int c) {
                 const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
-                if constexpr (KIND == GRAD && sizeof(T) == 2)
-                    if (dh_packs && c < WIDTH / 32 && rows > 0 && cols > 0) ask_chunk<T>(asked, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols, lane);
+                if (c >= WIDTH / 32 || rows <= 0 || cols <= 0) return;
+                if constexpr (PAIR)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+                        if (p.bias[w] && lane < cols) bias[w] = to_f32(static_cast<const T*>(p.bias[w])[col + lane]);
+                if constexpr (KIND == GRAD)
+                    if (dh_packs) ask_chunk<T>(dh_area, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols, lane);
             };
             // 32 columns of the result from the accumulators
             auto finish = [&](int c, float (&g)[32], float (&u)[32]) {
                 const int col = tile.n * WIDTH + c * 32, cols = min(32, limit - col);
                 if (rows <= 0 || cols <= 0) return;
                 float dh[32];
-                if (KIND == GRAD && sizeof(T) == 2 && dh_packs) {
-                    if constexpr (sizeof(T) == 2) {
-                        take_chunk<T>(area, asked, dh, lane);
-                        ask(c + 2);
-                    }
-                } else if constexpr (KIND == GRAD)
-                    get_chunk<T>(area, dh, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols,
-                                 p.F % (16 / (int)sizeof(T)) == 0 && aligned16_dev(p.dh), lane);
+                if constexpr (KIND == GRAD) {
+                    if (dh_packs) take_chunk<T>(dh_area, dh, lane);
+                    else get_chunk<T>(area, dh, static_cast<const T*>(p.dh) + row0 * p.F + col, p.F, rows, cols, lane);
+                }
                 if constexpr (PAIR) {
-                    add_bias<T>(g, p.bias[0], col, cols);
-                    add_bias<T>(u, p.bias[1], col, cols);
+                    if (p.bias[0]) add_bias(g, bias[0]);
+                    if (p.bias[1]) add_bias(u, bias[1]);
+                    ask(c + 2);
                 }
                 const bool bad = !ok || late.any();
                 if constexpr (KIND == FWD) {
@@ -579,17 +564,17 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                     for (int which = 0; which < 2; ++which) {
                         float v[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = which ? u[j] : g[j];
+                        for (int j = 0; j < 32; ++j) v[j] = std::is_same<T, __half>::value ? (which ? u[j] : g[j]) * up : which ? u[j] : g[j];
 #pragma unroll 1
-                        for (int part = 0; part < kParts<T>; ++part) {
-                            float r[32];
+                        for (int part = 0; part < PARTS; ++part) {
+                            put_chunk<O>(area, v, reinterpret_cast<O*>(p.grads) + ((which * PARTS + part) * p.M + row0) * p.ld + col, p.ld, rows, cols, true, lane);
+                            if (part + 1 < PARTS)   // what the parts so far leave, exact
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                r[j] = v[j] * up;
-                                if (kParts<T> > 1) v[j] -= to_f32(from_f32<O>(v[j]));   // exact: what the parts so far leave
-                            }
-                            put_chunk<O>(area, r, reinterpret_cast<O*>(p.grads) + ((which * kParts<T> + part) * p.M + row0) * p.ld + col, p.ld, rows,
-                                         cols, true, lane);
+                                for (int j = 0; j < 32; j += 2) {
+                                    const uint32_t w = pack2<O>(v[j], v[j + 1]);
+                                    const O* e = reinterpret_cast<const O*>(&w);
+                                    v[j] -= to_f32(e[0]), v[j + 1] -= to_f32(e[1]);
+                                }
                         }
                         if (p.sums) {
 #pragma unroll
@@ -614,6 +599,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             if constexpr (sizeof(T) == 4) {
                 constexpr int C = (WIDTH / 32 + 1) / 2;   // times 32 columns of this warp, added up over the runs
                 float g[C][32], u[PAIR ? C : 1][32];
+                ask(half);
                 for (int k = tile.first; k < tile.last; k += kRun<T>, ++n) {
                     const uint32_t acc = await();
                     if (half < WIDTH / 32) {

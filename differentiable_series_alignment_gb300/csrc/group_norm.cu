@@ -76,6 +76,8 @@ struct Layout {
     int entries, side;       // sums of a group in a row of threads; rows of them that a warp adds up side by side
     Div by_packs, by_lanes, by_cg, by_entries;
     size_t smem;
+    // rows of a thread among n positions from its first on
+    __device__ __forceinline__ int count(int n) const { return n > 0 ? lanes == 1 ? n : ((n - 1) >> 16) ? (n - 1) / lanes + 1 : (n - 1) / by_lanes + 1 : 0; }
 };
 
 __device__ __forceinline__ void cluster_sync_g() {
@@ -103,17 +105,16 @@ __device__ __forceinline__ void store_remote(const float* mine, int cta, float v
 // within a group they are one. red holds those of all threads, one row of threads after the other; a warp adds up a
 // group, then the CTAs' sums of it are exchanged. parts: [ctas][NV][items * groups], of this call alone. What becomes of a group's
 // sum is done once, by the thread that calls finish(which, item * groups + group, sum).
-template <int VEC, int NV, typename F>
-__device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], float* red, float* parts, const Layout& L, int cg, int rank, F finish)
+template <int VEC, bool WITHIN, int NV, typename F>
+__device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], float* red, float* parts, const Layout& L, int rank, F finish)
 {
     const int groups = L.groups, all = L.items * groups, rows = L.lanes, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool within = cg % VEC == 0;
-    const int across = within ? L.packs : L.width, n = L.entries;   // entries of a row, of a group's row
+    const int across = WITHIN ? L.packs : L.width, n = L.entries;   // entries of a row, of a group's row
     const bool mine = (int)threadIdx.x < L.items * rows * L.packs;
 #pragma unroll
     for (int w = 0; w < NV; ++w) {
-        float* to = red + w * kThreads * VEC;
-        if (mine && within) {
+        float* to = red + w * (WITHIN ? kThreads : kThreads * VEC);
+        if (mine && WITHIN) {
             Pair t = v[w][0];
 #pragma unroll
             for (int q = 1; q < kPairs<VEC>; ++q) t = add2(t, v[w][q]);
@@ -133,7 +134,7 @@ __device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], flo
     const int r0 = n < 32 ? lane / L.by_entries : 0, c0 = lane - r0 * n;
     for (int k = warp; k < NV * all; k += kWarpsG) {
         const int w = NV > 1 && k >= all ? 1 : 0, j = k - w * all, item = L.items > 1 ? j / groups : 0;
-        const float* first = red + w * kThreads * VEC + item * rows * across + (j - item * groups) * n;
+        const float* first = red + w * (WITHIN ? kThreads : kThreads * VEC) + item * rows * across + (j - item * groups) * n;
         float s = 0.f;
         if (r0 < side)
             for (int r = r0; r < rows; r += side)
@@ -156,15 +157,25 @@ __device__ __forceinline__ void group_sums(const Pair (&v)[NV][kPairs<VEC>], flo
     }
     __syncthreads();
 }
-// A thread's channels' entries of a group's [groups]
-template <int VEC> __device__ __forceinline__ void of_channels(const float* from, int c0, const Div& cg, Pair (&v)[kPairs<VEC>]) {
-    if (cg.by % VEC == 0) {
+// A thread's channels' entries of a group's [groups]: one for all of them where a pack lies within a group
+template <int VEC, bool WITHIN> constexpr int kOf = WITHIN ? 1 : kPairs<VEC>;
+template <int VEC, bool WITHIN> __device__ __forceinline__ void of_channels(const float* from, int c0, const Div& cg, Pair (&v)[kOf<VEC, WITHIN>]) {
+    if constexpr (WITHIN) {
         const float x = from[c0 / cg];
-#pragma unroll
-        for (int q = 0; q < kPairs<VEC>; ++q) v[q] = pk2(x, x);
+        v[0] = pk2(x, x);
     } else {
 #pragma unroll
         for (int q = 0; q < kPairs<VEC>; ++q) v[q] = pk2(from[(c0 + 2 * q) / cg], VEC > 1 ? from[(c0 + 2 * q + 1) / cg] : 0.f);
+    }
+}
+template <typename T, int VEC, bool WITHIN>
+__device__ __forceinline__ void less(const Pack<T, VEC>& v, const Pair (&m)[kOf<VEC, WITHIN>], Pair (&out)[kPairs<VEC>]) {
+    if constexpr (WITHIN) {
+        float x, y;
+        upk2(m[0], x, y);
+        plus<T, VEC>(v, -x, out);
+    } else {
+        minus<T, VEC>(v, m, out);
     }
 }
 
@@ -174,7 +185,20 @@ __device__ __forceinline__ void fetch16(void* dst, const void* src) {
 __device__ __forceinline__ void fetch4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// A thread's rows come in four groups, so that it has begun with the first when the last are still on their way.
+constexpr int kBatches = 4;
+__device__ __forceinline__ void mark_batch() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <typename F> __device__ __forceinline__ void by_batches(int rounds, F f) {
+    const int n = (rounds + kBatches - 1) / kBatches;
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+    f(0, n);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    f(n, 2 * n);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    f(2 * n, 3 * n);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    f(3 * n, rounds);
+}
 
 // What a thread has of a round of items: rows [first, first + rounds * lanes) of its batch element, every lanes-th.
 struct Place {
@@ -226,7 +250,7 @@ template <int VEC> __device__ __forceinline__ void read_floats(const float* from
     for (int q = 0; q < kPairs<VEC>; ++q) v[q] = VEC > 1 ? *reinterpret_cast<const Pair*>(from + 2 * q) : pk2(from[0], 0.f);
 }
 
-template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThreads, 3) group_fwd_kernel(const GroupNormParams p, const Layout L)
+template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_bounds__(kThreads, 3) group_fwd_kernel(const GroupNormParams p, const Layout L)
 {
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
@@ -249,35 +273,43 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         P* mine = reinterpret_cast<P*>(held) + threadIdx.x;
         const T* src = x + at.at;
         auto value = [&](int k) { return HELD ? mine[k * kThreads] : *reinterpret_cast<const P*>(src + k * step); };
+        const int rounds = L.count(there - at.first), last = L.count(at.last - at.first);   // of this thread
         if constexpr (HELD) {
-            const T* q = src;
-            P* to = mine;
+            const int n = (rounds + kBatches - 1) / kBatches;
+            for (int g = 0, k = 0; g < kBatches; ++g) {
 #pragma unroll 4
-            for (int s = at.first; s < there; s += L.lanes, q += step, to += kThreads) fetch16(to, q);
-            fetched();
+                for (; k < min(rounds, (g + 1) * n); ++k) fetch16(mine + k * kThreads, src + k * step);
+                mark_batch();
+            }
         }
-        Pair s[1][Q], mu[Q], rw[Q], bias[Q], d[Q];
+        Pair s[1][Q], mu[kOf<VEC, WITHIN>], rw[Q], bias[Q], d[Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) s[0][q] = mu[q] = pk2(0.f, 0.f);
+        for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
+        mu[0] = pk2(0.f, 0.f);
+        auto add = [&](int from, int to) {
+            to = min(to, rounds);
 #pragma unroll 2
-        for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            minus<T, VEC>(value(k), mu, d);
+            for (int k = from; k < to; ++k) {
+                plus<T, VEC>(value(k), 0.f, d);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) s[0][q] = add2(s[0][q], d[q]);
-        }
+                for (int q = 0; q < Q; ++q) s[0][q] = add2(s[0][q], d[q]);
+            }
+        };
+        if constexpr (HELD) by_batches(rounds, add);
+        else add(0, rounds);
         auto count = [&](int k) { return length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg; };
-        group_sums<VEC, 1>(s, red, parts, L, p.cg, rank, [&](int, int k, float sum) { stats[k] = count(k) > 0.f ? sum / count(k) : 0.f; });
+        group_sums<VEC, WITHIN, 1>(s, red, parts, L, rank, [&](int, int k, float sum) { stats[k] = count(k) > 0.f ? sum / count(k) : 0.f; });
         const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
-        of_channels<VEC>(mine_stats, c0, L.by_cg, mu);
+        of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, mu);
 #pragma unroll
         for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
 #pragma unroll 2
-        for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            minus<T, VEC>(value(k), mu, d);
+        for (int k = 0; k < rounds; ++k) {
+            less<T, VEC, WITHIN>(value(k), mu, d);
 #pragma unroll
             for (int q = 0; q < Q; ++q) s[0][q] = fma2(d[q], d[q], s[0][q]);
         }
-        group_sums<VEC, 1>(s, red, parts + L.ctas * all, L, p.cg, rank, [&](int, int k, float sum) {
+        group_sums<VEC, WITHIN, 1>(s, red, parts + L.ctas * all, L, rank, [&](int, int k, float sum) {
             const float r = count(k) > 0.f ? 1.f / sqrtf(sum / count(k) + p.eps) : 0.f;
             stats[all + k] = r;
             if (p.mean && rank == 0 && b0 + k / groups < p.B) {
@@ -287,13 +319,14 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         });
         read_floats<VEC>(weights + c0, rw);
         read_floats<VEC>(weights + L.width + c0, bias);
-        of_channels<VEC>(mine_stats + all, c0, L.by_cg, d);
+        Pair r[kOf<VEC, WITHIN>];
+        of_channels<VEC, WITHIN>(mine_stats + all, c0, L.by_cg, r);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], d[q]);
+        for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], r[WITHIN ? 0 : q]);
         T* dst = y + at.at;
-        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes, dst += step) {
-            if (i < there) {
-                minus<T, VEC>(value(k), mu, d);
+        for (int k = 0; k < last; ++k, dst += step) {
+            if (k < rounds) {
+                less<T, VEC, WITHIN>(value(k), mu, d);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) d[q] = fma2(d[q], rw[q], bias[q]);
                 activate_all<sizeof(T) == 4, false, Q>(p.activation, d);
@@ -306,7 +339,7 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     }
 }
 
-template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThreads, 2) group_bwd_kernel(const GroupNormParams p, const Layout L)
+template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_bounds__(kThreads, WITHIN ? 3 : 2) group_bwd_kernel(const GroupNormParams p, const Layout L)
 {
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
@@ -315,7 +348,7 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
     float* red = weights + 2 * L.width;
-    float* stats = red + 2 * kThreads * VEC;                // mean g, mean g xh
+    float* stats = red + (WITHIN && VEC > 1 ? 1 : 2) * kThreads * VEC;   // mean g, mean g xh
     float* parts = stats + 2 * all;
     const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
     T* dx = static_cast<T*>(p.dx);
@@ -325,7 +358,6 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
     const long long step = (long long)L.lanes * p.C;
     const int c0 = ((int)threadIdx.x - (int)threadIdx.x / L.by_packs * L.packs) * VEC;
     Pair w[Q], bias[Q], sum[2][Q];                          // of the weights' gradients
-    const Pair none[Q] = {};
     read_floats<VEC>(weights + c0, w);
     read_floats<VEC>(weights + L.width + c0, bias);
 #pragma unroll
@@ -339,28 +371,30 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         auto value = [&](int k, int which) {
             return HELD ? mine[(2 * k + which) * kThreads] : *reinterpret_cast<const P*>((which ? sd : sx) + k * step);
         };
+        const int rounds = L.count(there - at.first), last = L.count(at.last - at.first);
         if constexpr (HELD) {
-            const T *q = sx, *d = sd;
-            P* to = mine;
-#pragma unroll 4
-            for (int s = at.first; s < there; s += L.lanes, q += step, d += step, to += 2 * kThreads) {
-                fetch16(to, q);
-                fetch16(to + kThreads, d);
+            const int n = (rounds + kBatches - 1) / kBatches;
+            for (int g = 0, k = 0; g < kBatches; ++g) {
+#pragma unroll 2
+                for (; k < min(rounds, (g + 1) * n); ++k) {
+                    fetch16(mine + 2 * k * kThreads, sx + k * step);
+                    fetch16(mine + (2 * k + 1) * kThreads, sd + k * step);
+                }
+                mark_batch();
             }
         }
-        Pair mu[Q], r[Q], s[2][Q];
+        Pair mu[kOf<VEC, WITHIN>], r[kOf<VEC, WITHIN>], s[2][Q];
         const long long from = (long long)(at.on ? at.b : 0) * p.G + slab * groups;
-        of_channels<VEC>(p.mean + from, c0, L.by_cg, mu);
-        of_channels<VEC>(p.rstd + from, c0, L.by_cg, r);
-        if constexpr (HELD) fetched();
+        of_channels<VEC, WITHIN>(p.mean + from, c0, L.by_cg, mu);
+        of_channels<VEC, WITHIN>(p.rstd + from, c0, L.by_cg, r);
         // xh and dz of a pack
         auto values = [&](int k, Pair (&xh)[Q], Pair (&dz)[Q]) {
             Pair z[Q];
-            minus<T, VEC>(value(k, 0), mu, xh);
-            minus<T, VEC>(value(k, 1), none, dz);
+            less<T, VEC, WITHIN>(value(k, 0), mu, xh);
+            plus<T, VEC>(value(k, 1), 0.f, dz);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                xh[q] = mul2(xh[q], r[q]);
+                xh[q] = mul2(xh[q], r[WITHIN ? 0 : q]);
                 z[q] = fma2(xh[q], w[q], bias[q]);
             }
             activate_all<sizeof(T) == 4, true, Q>(p.activation, z);
@@ -369,34 +403,40 @@ template <typename T, int VEC, bool HELD> __global__ void __launch_bounds__(kThr
         };
 #pragma unroll
         for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = pk2(0.f, 0.f);
-        for (int k = 0, i = at.first; i < there; ++k, i += L.lanes) {
-            Pair xh[Q], dz[Q];
-            values(k, xh, dz);
+        auto add = [&](int from, int to) {
+            to = min(to, rounds);
+            for (int k = from; k < to; ++k) {
+                Pair xh[Q], dz[Q];
+                values(k, xh, dz);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                s[0][q] = add2(s[0][q], dz[q]);
-                s[1][q] = fma2(dz[q], xh[q], s[1][q]);
+                for (int q = 0; q < Q; ++q) {
+                    s[0][q] = add2(s[0][q], dz[q]);
+                    s[1][q] = fma2(dz[q], xh[q], s[1][q]);
+                }
             }
-        }
+        };
+        if constexpr (HELD) by_batches(rounds, add);
+        else add(0, rounds);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
             for (int k = 0; k < 2; ++k) sum[k][q] = add2(sum[k][q], s[k][q]), s[k][q] = mul2(s[k][q], w[q]);
         if (!dx) continue;
-        group_sums<VEC, 2>(s, red, parts + 2 * turn * L.ctas * all, L, p.cg, rank, [&](int which, int k, float t) {
+        group_sums<VEC, WITHIN, 2>(s, red, parts + 2 * turn * L.ctas * all, L, rank, [&](int which, int k, float t) {
             const float n = length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg;
             stats[which * all + k] = n > 0.f ? t / n : 0.f;
         });
         const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
-        of_channels<VEC>(mine_stats, c0, L.by_cg, s[0]);
-        of_channels<VEC>(mine_stats + all, c0, L.by_cg, s[1]);
+        Pair m1[kOf<VEC, WITHIN>], m2[kOf<VEC, WITHIN>];
+        of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, m1);
+        of_channels<VEC, WITHIN>(mine_stats + all, c0, L.by_cg, m2);
         T* dst = dx + at.at;
-        for (int k = 0, i = at.first; i < at.last; ++k, i += L.lanes, dst += step) {
+        for (int k = 0; k < last; ++k, dst += step) {
             Pair xh[Q], dz[Q];
-            if (i < there) {
+            if (k < rounds) {
                 values(k, xh, dz);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) dz[q] = mul2(r[q], sub2(sub2(mul2(dz[q], w[q]), s[0][q]), mul2(xh[q], s[1][q])));
+                for (int q = 0; q < Q; ++q) dz[q] = mul2(r[WITHIN ? 0 : q], sub2(sub2(mul2(dz[q], w[q]), m1[WITHIN ? 0 : q]), mul2(xh[q], m2[WITHIN ? 0 : q])));
             } else {
 #pragma unroll
                 for (int q = 0; q < Q; ++q) dz[q] = pk2(0.f, 0.f);
@@ -744,17 +784,20 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     // few items are spread over the SMs
     while (L.items > 1 && (long long)((p.B + L.items - 1) / L.items) * L.slabs < sms) L.items = (L.items + 1) / 2;
     const int arrays = backward ? 2 : 1;
-    const size_t sums = (2 * (size_t)L.width + (size_t)arrays * kThreads * L.vec + 2 * L.items * (L.width / p.cg)) * sizeof(float);
+    const bool one = p.cg % L.vec == 0 && L.vec > 1;             // sum of a thread for each of a group's
+    const size_t sums = (2 * (size_t)L.width + (size_t)(one ? 1 : arrays) * kThreads * L.vec + 2 * L.items * (L.width / p.cg)) * sizeof(float);
     auto bytes = [&](int ctas) {
         const size_t exchange = ctas > 1 ? (size_t)4 * ctas * (L.width / p.cg) * sizeof(float) : 0;
         const long long rounds = ((p.S + ctas - 1) / ctas + L.lanes - 1) / L.lanes;
         return std::pair<size_t, long long>(sums + exchange, rounds * kThreads * 16 * arrays);
     };
-    // CTAs of a cluster: until three fit on an SM side by side, and there are two an SM
+    // CTAs of a cluster: until three fit on an SM side by side, or, where there are fewer than two an SM, until a thread has
+    // eight rows: a cluster's exchanges take some 2 us
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
     while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes &&
-           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > 75 * 1024 || clusters * L.ctas < 2 * sms))
+           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > 75 * 1024 ||
+            (clusters * L.ctas < 2 * sms && p.S >= 16ll * L.ctas * L.lanes)))
         L.ctas *= 2;
     const auto need = bytes(L.ctas);
     L.part = (p.S + L.ctas - 1) / L.ctas;
@@ -816,8 +859,10 @@ cudaError_t launch_group_norm_forward(const GroupNormParams& p, int sms, cudaStr
         using T = decltype(t);
         constexpr int VEC = 16 / sizeof(T);
         if (L.small) return run_small<T, VEC, false>(p, L, s);
-        if (L.fits) return L.vec == 1 ? launch<group_fwd_kernel<T, 1, false>>(p, L, s) : L.held ? launch<group_fwd_kernel<T, VEC, true>>(p, L, s)
-                                                                                              : launch<group_fwd_kernel<T, VEC, false>>(p, L, s);
+        const bool within = p.cg % L.vec == 0;
+        if (L.fits && L.vec == 1) return launch<group_fwd_kernel<T, 1, false, true>>(p, L, s);
+        if (L.fits && L.held) return within ? launch<group_fwd_kernel<T, VEC, true, true>>(p, L, s) : launch<group_fwd_kernel<T, VEC, true, false>>(p, L, s);
+        if (L.fits) return within ? launch<group_fwd_kernel<T, VEC, false, true>>(p, L, s) : launch<group_fwd_kernel<T, VEC, false, false>>(p, L, s);
         group_fwd_any_kernel<T><<<p.B * p.G, kThreads, 0, s>>>(p);
         return cudaGetLastError();
     });
@@ -832,8 +877,10 @@ cudaError_t launch_group_norm_backward(const GroupNormParams& p0, int sms, cudaS
         using T = decltype(t);
         constexpr int VEC = 16 / sizeof(T);
         if (L.small) return run_small<T, VEC, true>(p, L, s);
-        if (L.fits) return L.vec == 1 ? launch<group_bwd_kernel<T, 1, false>>(p, L, s) : L.held ? launch<group_bwd_kernel<T, VEC, true>>(p, L, s)
-                                                                                              : launch<group_bwd_kernel<T, VEC, false>>(p, L, s);
+        const bool within = p.cg % L.vec == 0;
+        if (L.fits && L.vec == 1) return launch<group_bwd_kernel<T, 1, false, true>>(p, L, s);
+        if (L.fits && L.held) return within ? launch<group_bwd_kernel<T, VEC, true, true>>(p, L, s) : launch<group_bwd_kernel<T, VEC, true, false>>(p, L, s);
+        if (L.fits) return within ? launch<group_bwd_kernel<T, VEC, false, true>>(p, L, s) : launch<group_bwd_kernel<T, VEC, false, false>>(p, L, s);
         group_bwd_any_kernel<T><<<p.B * p.G, kThreads, 0, s>>>(p);
         return cudaGetLastError();
     });
