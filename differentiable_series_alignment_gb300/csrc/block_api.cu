@@ -34,7 +34,7 @@ sdtw_status check_group_norm(int B, int S, int G, int C, int dtype, int wdtype)
     if (C % G) return SDTW_ERR_SHAPE;
     if (!good_dtype(dtype) || !good_dtype(wdtype)) return SDTW_ERR_ARG;
     // 32-bit grids and counts of a group's values in fp32's and the workspace's reach
-    if (C > (1 << 24) || (long long)B * G > 0x7fffffffll || (long long)S * C > (1ll << 40) || (long long)B * C > (1ll << 40)) return SDTW_ERR_TOO_LARGE;
+    if (B > (1 << 30) || C > (1 << 24) || (long long)B * G > 0x7fffffffll || (long long)S * C > (1ll << 40) || (long long)B * C > (1ll << 40)) return SDTW_ERR_TOO_LARGE;
     return SDTW_OK;
 }
 

@@ -5,7 +5,7 @@
 //   dz = dy act'(z), g = dz w, dx = r (g - mean g - xh mean(g xh)), dw = sum dz xh, db = sum dz
 //
 // Memory bounds it: x is read once and y written once, x and dy once for dx. A slab, whole groups of a batch element's
-// channels at least 128 bytes wide, stays in the shared memory of a cluster of up to 16 CTAs that share its positions, from
+// channels at least 64 bytes wide, stays in the shared memory of a cluster of up to 16 CTAs that share its positions, from
 // its one load to its results; sums of its groups go between the CTAs through shared memory. The variance is the mean
 // square of centred values. A thread has the same channels throughout, and sums the weights' gradients in registers over
 // all that its CTA takes; the CTAs' sums are added by a second launch in a fixed order: the same bits every time. Slabs
@@ -179,6 +179,18 @@ __device__ __forceinline__ void less(const Pack<T, VEC>& v, const Pair (&m)[kOf<
     }
 }
 
+// s + v, channel by channel
+template <typename T, int VEC> __device__ __forceinline__ void add_onto(Pair (&s)[kPairs<VEC>], const Pack<T, VEC>& v) {
+#pragma unroll
+    for (int q = 0; q < kPairs<VEC>; ++q) {
+        float x, y;
+        upk2(s[q], x, y);
+        if constexpr (VEC == 1) x += to_f32(v.e[0]);
+        else if constexpr (sizeof(T) == 4) x += v.e[2 * q], y += v.e[2 * q + 1];
+        else add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+        s[q] = pk2(x, y);
+    }
+}
 __device__ __forceinline__ void fetch16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
@@ -288,12 +300,8 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         mu[0] = pk2(0.f, 0.f);
         auto add = [&](int from, int to) {
             to = min(to, rounds);
-#pragma unroll 2
-            for (int k = from; k < to; ++k) {
-                plus<T, VEC>(value(k), 0.f, d);
-#pragma unroll
-                for (int q = 0; q < Q; ++q) s[0][q] = add2(s[0][q], d[q]);
-            }
+#pragma unroll 4
+            for (int k = from; k < to; ++k) add_onto<T, VEC>(s[0], value(k));
         };
         if constexpr (HELD) by_batches(rounds, add);
         else add(0, rounds);
@@ -303,7 +311,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, mu);
 #pragma unroll
         for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < rounds; ++k) {
             less<T, VEC, WITHIN>(value(k), mu, d);
 #pragma unroll
@@ -469,19 +477,22 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 // sums need no barrier. A thread's group and channels stay the same over the batch elements that it takes, every
 // columns-th; the coming ones' packs are on their way to shared memory meanwhile, a thread's to places of its own.
 __device__ __forceinline__ float lane_sum(float v, int lanes) {
-    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// 1 / sqrt(v); for results of 16 bits by the approximation, within 2^-22
+template <bool EXACT> __device__ __forceinline__ float rsqrt_of(float v) { return EXACT ? 1.f / sqrtf(v) : rsqrtf(v); }
 constexpr int kSmallPacks = 2, kAhead = 3;
 
 template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds__(kThreads, (BWD ? 2 : 4) / K) group_small_kernel(const GroupNormParams p, const Layout L)
 {
     using P = Pack<T, VEC>;
     constexpr int Q = kPairs<VEC>;
-    const Pair none[Q] = {};
     const long long id = ((long long)blockIdx.x * kThreads + threadIdx.x) / L.lanes;
     const int lane = threadIdx.x % L.lanes, g = (int)(id % p.G), per = p.cg / VEC, packs = p.S * per;
-    const long long column = id / p.G, end = column < L.columns ? p.B : 0;   // the last CTA's threads may be too many
+    const int column = (int)(id / p.G), end = column < L.columns ? p.B : 0;   // the last CTA's threads may be too many
     const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
     T* out = static_cast<T*>(BWD ? p.dx : p.y);
     int row[K], c[K];
@@ -499,45 +510,52 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
         read_weights<VEC>(p.bias, c[k], p.wdtype, 0.f, t);
         pairs_of<VEC>(t, bias[k]);
     }
-    auto length = [&](long long b) { return b < end ? p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S : 0; };
+    auto length = [&](int b) { return b < end ? p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S : 0; };
     // [kAhead + 1][K][x, dy][kThreads] packs, and after them [kAhead + 1][mean, rstd][kThreads]
     extern __shared__ __align__(16) unsigned char held[];
     constexpr int N = BWD ? 2 : 1;
     float* stat = reinterpret_cast<float*>(held + (kAhead + 1) * K * N * kThreads * 16);
     auto slot = [&](int stage, int k, int which) { return reinterpret_cast<P*>(held) + ((stage * K + k) * N + which) * kThreads + threadIdx.x; };
-    auto send = [&](long long b, int stage) {
-        const int len = length(b);
+    // places of the batch element to send for, and of the one in work
+    const long long step = (long long)L.columns * p.S * p.C, element = (long long)p.S * p.C;
+    long long ahead = column * element, here = ahead, stats = column * p.G + g;
+    int place[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) place[k] = row[k] * p.C + c[k];
+    int sent = column;
+    auto send = [&](int stage) {
+        const int len = length(sent);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (has[k] && row[k] < len) {
-                const long long at = (b * p.S + row[k]) * p.C + c[k];
-                fetch16(slot(stage, k, 0), x + at);
-                if (BWD) fetch16(slot(stage, k, N - 1), dy + at);
+                fetch16(slot(stage, k, 0), x + ahead + place[k]);
+                if (BWD) fetch16(slot(stage, k, N - 1), dy + ahead + place[k]);
             }
         if (BWD && len > 0) {
-            fetch4(stat + 2 * stage * kThreads + threadIdx.x, p.mean + b * p.G + g);
-            fetch4(stat + (2 * stage + 1) * kThreads + threadIdx.x, p.rstd + b * p.G + g);
+            fetch4(stat + 2 * stage * kThreads + threadIdx.x, p.mean + (long long)sent * p.G + g);
+            fetch4(stat + (2 * stage + 1) * kThreads + threadIdx.x, p.rstd + (long long)sent * p.G + g);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        ahead += step, sent += L.columns;
     };
-    for (int k = 0; k < kAhead; ++k) send(column + (long long)k * L.columns, k);
+    for (int k = 0; k < kAhead; ++k) send(k);
     int stage = 0;
+    const float full = 1.f / ((float)p.S * (float)p.cg);
     // every lane of a warp makes the same number of rounds: the sums are collective
-    const long long most = (p.B + L.columns - 1) / L.columns;
-    for (long long turn = 0; turn < most; ++turn) {
-        const long long b = column + turn * L.columns;
+    const int most = (p.B + L.columns - 1) / L.columns;
+    for (int b = column, turn = 0; turn < most; ++turn, b += L.columns, here += step, stats += (long long)L.columns * p.G) {
         const int len = length(b);
         Pair v[K][Q], d[K][Q], s1 = pk2(0.f, 0.f), s2 = s1;
         bool in[K];
-        const float n = (float)len * (float)p.cg, inv = len ? 1.f / n : 0.f;
-        send(b + (long long)kAhead * L.columns, stage == 0 ? kAhead : stage - 1);   // where the last round's were
+        const float inv = len == p.S ? full : len ? 1.f / ((float)len * (float)p.cg) : 0.f;
+        send(stage == 0 ? kAhead : stage - 1);   // where the last round's were
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             in[k] = has[k] && row[k] < len;
             if (in[k]) {
-                minus<T, VEC>(*slot(stage, k, 0), none, v[k]);
-                if (BWD) minus<T, VEC>(*slot(stage, k, N - 1), none, d[k]);
+                plus<T, VEC>(*slot(stage, k, 0), 0.f, v[k]);
+                if (BWD) plus<T, VEC>(*slot(stage, k, N - 1), 0.f, d[k]);
             }
         }
         float mu = 0.f, r = 0.f;
@@ -560,8 +578,8 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
                         s2 = fma2(v[k][q], v[k][q], s2);
                     }
                 }
-            r = len ? 1.f / sqrtf(lane_sum(both(s2), L.lanes) * inv + p.eps) : 0.f;
-            if (p.mean && lane == 0 && b < end) p.mean[b * p.G + g] = mu, p.rstd[b * p.G + g] = r;
+            r = len ? rsqrt_of<sizeof(T) == 4>(lane_sum(both(s2), L.lanes) * inv + p.eps) : 0.f;
+            if (p.mean && lane == 0 && b < end) p.mean[stats] = mu, p.rstd[stats] = r;
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -601,7 +619,7 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
                         for (int q = 0; q < Q; ++q) v[k][q] = fma2(mul2(v[k][q], pk2(r, r)), w[k][q], bias[k][q]);
                         activate_all<sizeof(T) == 4, false, Q>(p.activation, v[k]);
                     }
-                    *reinterpret_cast<P*>(out + (b * p.S + row[k]) * p.C + c[k]) = rounded<T, VEC>(v[k]);
+                    *reinterpret_cast<P*>(out + here + place[k]) = rounded<T, VEC>(v[k]);
                 }
         }
     }
@@ -609,7 +627,7 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (has[k]) {
-                float* to = p.partial + 2 * (column * p.S + row[k]) * p.C + c[k];
+                float* to = p.partial + 2 * ((long long)column * p.S + row[k]) * p.C + c[k];
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     float u, v;
@@ -766,12 +784,13 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     }
     const long long whole = p.cg / gcd(p.cg, L.vec) * L.vec;    // channels of whole groups and whole packs
     L.width = (int)whole;
-    // at least 128 bytes a row, or all channels
+    // at least 64 bytes a row, or all channels: wider slabs take larger clusters (128 bytes: backward of 16 x 4096 x 512 bf16
+    // 98 us for 88), rows of 32 bytes 96
     for (long long j = 1; whole * j <= p.C; ++j)
         if (p.C % (whole * j) == 0) {
             if (j > 1 && whole * j > kThreads * L.vec) break;
             L.width = (int)(whole * j);
-            if (L.width * size >= 128) break;
+            if (L.width * size >= 64) break;
         }
     L.packs = L.width / L.vec;
     if (L.packs > kThreads) return L;
@@ -796,7 +815,7 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
     while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes &&
-           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > 75 * 1024 ||
+           ((long long)bytes(L.ctas).first + bytes(L.ctas).second > (L.ctas == 8 ? 112 : 75) * 1024 ||
             (clusters * L.ctas < 2 * sms && p.S >= 16ll * L.ctas * L.lanes)))
         L.ctas *= 2;
     const auto need = bytes(L.ctas);

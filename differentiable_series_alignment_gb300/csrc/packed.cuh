@@ -37,6 +37,18 @@ template <> __device__ __forceinline__ void add_pair<__half>(float& x, float& y,
         "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
         : "+f"(x), "+f"(y) : "r"(v));
 }
+// The same, from other values: x = v's low half + a, y = its high half + b.
+template <typename T> __device__ __forceinline__ void sum_pair(float& x, float& y, uint32_t v, float a, float b);
+template <> __device__ __forceinline__ void sum_pair<__nv_bfloat16>(float& x, float& y, uint32_t v, float a, float b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %3;\n\tadd.rn.f32.bf16 %1, hi, %4;\n\t}"
+        : "=f"(x), "=f"(y) : "r"(v), "f"(a), "f"(b));
+}
+template <> __device__ __forceinline__ void sum_pair<__half>(float& x, float& y, uint32_t v, float a, float b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.f16 %0, lo, %3;\n\tadd.rn.f32.f16 %1, hi, %4;\n\t}"
+        : "=f"(x), "=f"(y) : "r"(v), "f"(a), "f"(b));
+}
 __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -64,8 +76,8 @@ template <typename T, int VEC> __device__ __forceinline__ void plus(const Pack<T
         } else if constexpr (sizeof(T) == 4) {
             out[q] = add2(pk2(v.e[2 * q], v.e[2 * q + 1]), pk2(c, c));
         } else {
-            float x = c, y = c;
-            add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+            float x, y;
+            sum_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]), c, c);
             out[q] = pk2(x, y);
         }
     }
@@ -110,9 +122,9 @@ template <typename T, int VEC> __device__ __forceinline__ void minus(const Pack<
         } else if constexpr (sizeof(T) == 4) {
             out[q] = sub2(pk2(v.e[2 * q], v.e[2 * q + 1]), m[q]);
         } else {
-            x = -x, y = -y;
-            add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
-            out[q] = pk2(x, y);
+            float a, b;
+            sum_pair<T>(a, b, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]), -x, -y);
+            out[q] = pk2(a, b);
         }
     }
 }
