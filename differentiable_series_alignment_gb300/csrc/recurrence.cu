@@ -24,8 +24,8 @@ namespace sdtw {
 namespace {
 
 constexpr int kStep = SDTW_RECURRENCE_STEP;
-constexpr int kWarps = 8, kMostCtas = 16;   // of a CTA; of a cluster
-constexpr int kStages = 3;                  // of the forward pass's ring
+constexpr int kMostCtas = 16;   // of a cluster
+constexpr int kStages = 3;      // of the forward pass's ring
 
 __device__ __forceinline__ Pair pair(float v) { return pk2(v, v); }
 
@@ -183,32 +183,44 @@ template <typename T, int VEC, int ROWS> struct Rows<T, VEC, ROWS, true> {
         return value<T, VEC>(*reinterpret_cast<const typename Raw<T, VEC>::type*>(mine + i * 32 * VEC * (int)sizeof(T)));
     }
 };
-// [t0, t0 + kWarps ROWS) of an array into a stage: 16-byte pieces, `none` where there is nothing.
-template <typename T, int VEC, int ROWS>
-__device__ __forceinline__ void send_rows(unsigned char* stage, const T* first, int step, int there, int channels, uint32_t none) {
-    constexpr int bytes = 32 * VEC * sizeof(T), pieces = bytes / 16, per = 16 / sizeof(T);
+// [t0, t0 + WARPS ROWS) of an array into a stage: 16-byte pieces, `none` where there is nothing. first: the thread's channels of the
+// first row.
+template <typename T, int VEC, int ROWS, int WARPS>
+__device__ __forceinline__ void send_rows(unsigned char* stage, const T* first, int step, int there, bool on, uint32_t none) {
+    constexpr int bytes = 32 * VEC * sizeof(T), pieces = bytes / 16, each = WARPS * 32 / pieces;   // rows that the threads take at a time
+    static_assert(each * pieces == WARPS * 32, "whole rows");
+    const int row = threadIdx.x / pieces;
+    unsigned char* to = stage + threadIdx.x * 16;
+    first += (long long)row * step;
+    if (there >= WARPS * ROWS && on) {
 #pragma unroll
-    for (int q = 0; q < kWarps * ROWS * pieces / (kWarps * 32); ++q) {
-        const int j = threadIdx.x + q * kWarps * 32, row = j / pieces, piece = j % pieces;
-        unsigned char* to = stage + j * 16;
-        if (row < there && piece * per < channels)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(first + row * step + piece * per) : "memory");
-        else
-            *reinterpret_cast<uint4*>(to) = make_uint4(none, none, none, none);
+        for (int q = 0; q < WARPS * ROWS / each; ++q)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to + q * WARPS * 512)), "l"(first + q * each * step)
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int q = 0; q < WARPS * ROWS / each; ++q) {
+            if (row + q * each < there && on)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to + q * WARPS * 512)),
+                             "l"(first + q * each * step)
+                             : "memory");
+            else
+                *reinterpret_cast<uint4*>(to + q * WARPS * 512) = make_uint4(none, none, none, none);
+        }
     }
 }
 __device__ __forceinline__ void mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT> __device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // TIED: 1, 0, or -1: as the call says.
-template <typename T, int VEC, int ROWS, bool RING, int TIED>
-__global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const RecurrenceParams p, int ctas)
+template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(const RecurrenceParams p, int ctas)
 {
-    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? kWarps * ROWS * bytes : 0;
+    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     constexpr int turns = RING ? 1 : 2;                   // with a ring, all threads meet once more in a round
-    __shared__ Run run[turns][kWarps][32];
+    __shared__ Run run[turns][WARPS][32];
     __shared__ uint64_t s_bar[2];
-    extern __shared__ __align__(16) unsigned char ring[];   // [kStages][x, gate][kWarps ROWS][32 VEC], then [2][ctas][32] Runs
+    extern __shared__ __align__(16) unsigned char ring[];   // [kStages][x, gate][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + kStages * 2 * image);
     const sdtw_recurrence& a = p.a;
     const bool tied = TIED < 0 ? a.tied != 0 : TIED != 0;
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
     const bool on = c < a.C;
     const Element el(a, b);
     const long long bc = (long long)b * a.C + c;
-    const int per = ctas * kWarps * ROWS;                 // positions that the cluster takes at a time
+    const int per = ctas * WARPS * ROWS;                 // positions that the cluster takes at a time
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
     const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
     const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0];
@@ -228,15 +240,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
     if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = a.state && on ? load_f32<VEC>(a.state + bc) : pair(0.f);
-    const int t0 = rank * kWarps * ROWS;                  // the CTA's first position
+    const int t0 = rank * WARPS * ROWS;                  // the CTA's first position
     int t = t0 + warp * ROWS;
+    const int mine0 = c0 + threadIdx.x % (2 * VEC * (int)sizeof(T)) * (16 / (int)sizeof(T));   // channels of the pieces that this thread sends for
+    const bool sends = mine0 < a.C;
     auto send = [&](int round) {
         const int at = t0 + round * per;
         unsigned char* stage = ring + round % kStages * 2 * image;
         const long long r = el.row(at);
         if (round < rounds) {
-            send_rows<T, VEC, ROWS>(stage, x + r * a.x_stride[1] + c0, xs, el.len - at, a.C - c0, 0);
-            send_rows<T, VEC, ROWS>(stage + image, gate + r * a.gate_stride[1] + c0, gs, el.len - at, a.C - c0, open_bits<T>());
+            send_rows<T, VEC, ROWS, WARPS>(stage, x + r * a.x_stride[1] + mine0, xs, el.len - at, sends, 0);
+            send_rows<T, VEC, ROWS, WARPS>(stage + image, gate + r * a.gate_stride[1] + mine0, gs, el.len - at, sends, open_bits<T>());
         }
         mark();
     };
@@ -269,29 +283,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
         }
         run[turn % turns][warp][lane] = own;
         __syncthreads();
-        Run all{pair(1.f), pair(0.f)}, before = all;
+        // the runs before this warp's; the last warp goes on to the CTA's, and sends it around
+        Run before{pair(1.f), pair(0.f)};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) before = all;
-            const Run r = run[turn % turns][w][lane];
-            all.h = fma2(r.a, all.h, r.h);
-            all.a = mul2(all.a, r.a);
-        }
+        for (int w = 0; w < WARPS - 1; ++w)
+            if (w < warp) {
+                const Run r = run[turn % turns][w][lane];
+                before.h = fma2(r.a, before.h, r.h);
+                before.a = mul2(before.a, r.a);
+            }
         Pair h = carry;
         if (ctas > 1) {
             const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
             if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
-            if (!(p.skip && rank == 0))
-                for (int k = warp; k < ctas; k += kWarps) send_pairs(in_cta(slot, k), in_cta(bar, k), all.a, all.h);
+            if (warp == WARPS - 1 && !(p.skip && rank == 0)) {
+                const Pair all_a = mul2(before.a, own.a), all_h = fma2(own.a, before.h, own.h);
+                for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_h);
+            }
             if (ok) ok = wait_arrived(bar, (uint32_t)(round >> 1) & 1, p.wait_ns);
             if (!ok) carry = pair(__int_as_float(0x7fffffff));
+            const Run* r = total + turn * ctas * 32 + lane;
+#pragma unroll 4
             for (int k = 0; k < ctas; ++k) {
                 if (k == rank) h = carry;
-                const Run r = total[(turn * ctas + k) * 32 + lane];
-                carry = fma2(r.a, carry, r.h);
+                carry = fma2(r[k * 32].a, carry, r[k * 32].h);
             }
         } else {
-            carry = fma2(all.a, carry, all.h);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) carry = fma2(run[turn % turns][w][lane].a, carry, run[turn % turns][w][lane].h);
         }
         h = fma2(before.a, h, before.h);
         if (!on) continue;
@@ -314,21 +333,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_fwd_kernel(const Re
     }
     if (ctas > 1) cluster_sync();                         // no store may come to a CTA that has ended
     if (!on) return;
-    clear<T, VEC>(out, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
+    clear<T, VEC>(out, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
     if (p.last && rank == 0 && warp == 0) store_f32<VEC>(p.last + bc, carry);
 }
 
-template <typename T, int VEC, int ROWS, bool RING, int TIED>
-__global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const RecurrenceParams p, int ctas)
+template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(const RecurrenceParams p, int ctas)
 {
-    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? kWarps * ROWS * bytes : 0;
+    constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     constexpr int turns = RING ? 1 : 2;
-    __shared__ Run run[turns][kWarps][32];
-    __shared__ Pair back[turns][kWarps][32];
+    __shared__ Run run[turns][WARPS][32];
+    __shared__ Pair back[turns][WARPS][32];
     __shared__ uint64_t s_bar[2];
-    extern __shared__ __align__(16) unsigned char ring[];   // [2][x, gate, dh][kWarps ROWS][32 VEC], then [2][ctas][32] Runs
+    extern __shared__ __align__(16) unsigned char ring[];   // [2][x, gate, dh][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + 2 * 3 * image);
-    static_assert(kWarps * ROWS % kStep == 0 || kStep % (kWarps * ROWS) == 0, "kept states at CTAs' first positions");
+    static_assert(WARPS * ROWS % kStep == 0 || kStep % (WARPS * ROWS) == 0, "kept states at CTAs' first positions");
     const sdtw_recurrence& a = p.a;
     const bool tied = TIED < 0 ? a.tied != 0 : TIED != 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x % ctas;
@@ -337,7 +356,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
     const bool on = c < a.C;
     const Element el(a, b);
     const long long bc = (long long)b * a.C + c, base = (long long)b * a.N * a.C;
-    const int per = ctas * kWarps * ROWS;
+    const int per = ctas * WARPS * ROWS;
     const int steps = (a.N + kStep - 1) / kStep, rounds = (el.len + per - 1) / per;
     const int sign = el.reverse ? -1 : 1, xs = sign * (int)a.x_stride[1], gs = sign * (int)a.gate_stride[1], step = sign * a.C;
     const T* x = static_cast<const T*>(a.x) + b * a.x_stride[0];
@@ -348,15 +367,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
     if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = p.dlast && on ? load_f32<VEC>(p.dlast + bc) : pair(0.f);
-    const int t0 = rank * kWarps * ROWS;
+    const int t0 = rank * WARPS * ROWS;
+    const int mine0 = c0 + threadIdx.x % (2 * VEC * (int)sizeof(T)) * (16 / (int)sizeof(T));   // channels of the pieces that this thread sends for
+    const bool sends = mine0 < a.C;
     auto send = [&](int round) {
         const int at = t0 + round * per;
         unsigned char* stage = ring + (round & 1) * 3 * image;
         const long long r = el.row(at);
         if (round >= 0) {
-            send_rows<T, VEC, ROWS>(stage, x + r * a.x_stride[1] + c0, xs, el.len - at, a.C - c0, 0);
-            send_rows<T, VEC, ROWS>(stage + image, gate + r * a.gate_stride[1] + c0, gs, el.len - at, a.C - c0, open_bits<T>());
-            send_rows<T, VEC, ROWS>(stage + 2 * image, dh + r * a.C + c0, step, p.dh ? el.len - at : 0, a.C - c0, 0);
+            send_rows<T, VEC, ROWS, WARPS>(stage, x + r * a.x_stride[1] + mine0, xs, el.len - at, sends, 0);
+            send_rows<T, VEC, ROWS, WARPS>(stage + image, gate + r * a.gate_stride[1] + mine0, gs, el.len - at, sends, open_bits<T>());
+            send_rows<T, VEC, ROWS, WARPS>(stage + 2 * image, dh + r * a.C + mine0, step, p.dh ? el.len - at : 0, sends, 0);
         }
         mark();
     };
@@ -397,35 +418,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
         back[turn % turns][warp][lane] = r;
         state = kept(round - 1);
         __syncthreads();
-        // the state before the run, and what the later runs of the CTA hand back
+        // the state before the run, and what the later runs of the CTA hand back; the first warp goes on to the CTA's
         Run behind{pair(1.f), pair(0.f)};
-        Pair all_a = pair(1.f), all_r = pair(0.f);
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w == warp) behind = Run{all_a, all_r};
-            const Pair wa = run[turn % turns][w][lane].a;
-            all_r = fma2(wa, all_r, back[turn % turns][w][lane]);
-            all_a = mul2(all_a, wa);
-        }
-        for (int w = 0; w < warp; ++w) {
-            const Run q = run[turn % turns][w][lane];
-            h = fma2(q.a, h, q.h);
-        }
+        for (int w = WARPS - 1; w > 0; --w)
+            if (w > warp) {
+                const Pair wa = run[turn % turns][w][lane].a;
+                behind.h = fma2(wa, behind.h, back[turn % turns][w][lane]);
+                behind.a = mul2(behind.a, wa);
+            }
+#pragma unroll
+        for (int w = 0; w < WARPS - 1; ++w)
+            if (w < warp) h = fma2(run[turn % turns][w][lane].a, h, run[turn % turns][w][lane].h);
+        const Pair own_r = r;
         r = carry;
         if (ctas > 1) {
             const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
             if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
-            if (!(p.skip && rank == 0))
-                for (int k = warp; k < ctas; k += kWarps) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
+            if (warp == 0 && !(p.skip && rank == 0)) {
+                const Pair all_a = mul2(behind.a, own.a), all_r = fma2(own.a, behind.h, own_r);
+                for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
+            }
             if (ok) ok = wait_arrived(bar, (uint32_t)phase, p.wait_ns);
             if (!ok) carry = pair(__int_as_float(0x7fffffff));
+            const Run* q = total + turn * ctas * 32 + lane;
+#pragma unroll 4
             for (int k = ctas - 1; k >= 0; --k) {
                 if (k == rank) r = carry;
-                const Run q = total[(turn * ctas + k) * 32 + lane];
-                carry = fma2(q.a, carry, q.h);
+                carry = fma2(q[k * 32].a, carry, q[k * 32].h);
             }
         } else {
-            carry = fma2(all_a, carry, all_r);
+#pragma unroll
+            for (int w = WARPS - 1; w >= 0; --w) carry = fma2(run[turn % turns][w][lane].a, carry, back[turn % turns][w][lane]);
         }
         phase ^= turn;   // every second round
         turn ^= 1;
@@ -460,8 +484,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) recurrence_bwd_kernel(const Re
     }
     if (ctas > 1) cluster_sync();
     if (!on) return;
-    clear<T, VEC>(dx, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
-    clear<T, VEC>(dgate, a.C, rounds * per, a.N, rank * kWarps + warp, ctas * kWarps);
+    clear<T, VEC>(dx, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
+    clear<T, VEC>(dgate, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
     if (p.dstate && rank == 0 && warp == 0) store_f32<VEC>(p.dstate + bc, carry);
 }
 
@@ -496,7 +520,7 @@ template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) 
     if (p.last) store_f32<VEC>(p.last + bc, h);
 }
 
-template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas, size_t images, size_t totals, cudaStream_t s, const RecurrenceParams& p)
+template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas, int warps, size_t images, size_t totals, cudaStream_t s, const RecurrenceParams& p)
 {
     if (const cudaError_t e = allow_smem<Kernel>(images + kMostCtas * totals); e != cudaSuccess) return e;
     if (ctas > 8)
@@ -505,30 +529,40 @@ template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas,
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = (unsigned)ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.gridDim = dim3((unsigned)(clusters * ctas)), c.blockDim = dim3(kWarps * 32), c.stream = s, c.attrs = &at, c.numAttrs = ctas > 1 ? 1 : 0;
+    c.gridDim = dim3((unsigned)(clusters * ctas)), c.blockDim = dim3(warps * 32), c.stream = s, c.attrs = &at, c.numAttrs = ctas > 1 ? 1 : 0;
     c.dynamicSmemBytes = images + (ctas > 1 ? ctas * totals : 0);
     return cudaLaunchKernelEx(&c, Kernel, p, ctas);
 }
 
-// CTAs of a cluster: as many as it takes to have two a SM, no more than there are runs.
-int cluster_size(long long clusters, int N, int positions, int sms)
+// CTAs of a cluster: as many as it takes to fill the places that there are, no more than there are runs.
+int cluster_size(long long clusters, int N, int positions, long long places)
 {
     int k = 1;
-    while (k < kMostCtas && clusters * k < 2ll * sms && (long long)k * positions < N) k *= 2;
+    while (k < kMostCtas && clusters * k < places && (long long)k * positions < N) k *= 2;
     return k;
 }
 
 constexpr int kFewRows = 8;
 
+template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED> cudaError_t run_warps(const RecurrenceParams& p, bool backward, int ctas, cudaStream_t s)
+{
+    const sdtw_recurrence& a = p.a;
+    const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
+    constexpr size_t image = RING ? WARPS * ROWS * 32 * VEC * sizeof(T) : 0;
+    const size_t images = (backward ? 2 * 3 : kStages * 2) * image, totals = sizeof(Run) * 2 * 32;   // of a CTA of the cluster
+    if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p);
+    return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p);
+}
+// Two CTAs of eight warps an SM. Where the largest clusters leave half of these places empty, one of sixteen: a cluster then
+// takes twice the positions at a time, and what a round costs, some 3 us whatever its size, comes half as often.
 template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
     const sdtw_recurrence& a = p.a;
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
-    const int ctas = cluster_size(clusters, a.N, kWarps * ROWS, sms);
-    constexpr size_t image = RING ? kWarps * ROWS * 32 * VEC * sizeof(T) : 0;
-    const size_t images = (backward ? 2 * 3 : kStages * 2) * image, totals = sizeof(Run) * 2 * 32;   // of a CTA of the cluster
-    if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, RING, TIED>>(clusters, ctas, images, totals, s, p);
-    return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, RING, TIED>>(clusters, ctas, images, totals, s, p);
+    const int ctas = cluster_size(clusters, a.N, 8 * ROWS, 2 * sms);
+    if constexpr (RING)
+        if (clusters * ctas <= sms && a.N > 8ll * ROWS * ctas) return run_warps<T, VEC, ROWS, 16, RING, TIED>(p, backward, ctas, s);
+    return run_warps<T, VEC, ROWS, 8, RING, TIED>(p, backward, ctas, s);
 }
 template <typename T, int VEC> cudaError_t run_few(const RecurrenceParams& p, cudaStream_t s)
 {
