@@ -434,14 +434,16 @@ EncodeFn encode_fn()
 }  // namespace
 
 bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box)
+            const cuuint32_t* box, bool swizzled)
 {
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     const EncodeFn fn = encode_fn();
     auto go = [&] {
-        return fn(m, dtype == SDTW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-                  const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        const CUtensorMapDataType type = dtype == SDTW_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : dtype == SDTW_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        return fn(m, type, (cuuint32_t)rank, const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     if (!fn) return false;
     if (go() == CUDA_SUCCESS) return true;

@@ -286,9 +286,9 @@ struct Tiles {
 };
 
 // ---- host: tensor maps
-// A map of 16-bit elements with the 128-byte swizzle; strides in bytes, of all dimensions but the first.
+// A map with the 128-byte swizzle, or with rows as they are; strides in bytes, of all dimensions but the first.
 bool encode(CUtensorMap* m, int dtype, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box);
+            const cuuint32_t* box, bool swizzled = true);
 struct Maps {
     CUtensorMap q, k, v, dout;
 };

@@ -11,13 +11,15 @@
 // the same bits every time. The backward pass computes the states again from those that the forward pass kept, one in
 // SDTW_RECURRENCE_STEP positions: 3 reads and 2 writes where stored states would be another read.
 //
-// Coming positions are on their way to shared memory meanwhile (cp.async, rows of 16-byte pieces; sizes and addresses that
-// do not allow them are loaded by the lanes that use them). Pairs go between CTAs by stores that report to the receiver's
-// mbarrier: a cluster's own barrier also waits for the results that are on their way to memory.
+// Coming positions are on their way to shared memory meanwhile (TMA; sizes and addresses that do not allow it are loaded by
+// the lanes that use them). Pairs go between CTAs by stores that report to the receiver's mbarrier: a
+// cluster's own barrier also waits for the results that are on their way to memory.
 #include "activation.cuh"
+#include "attn_tc.cuh"
 #include "block.h"
 #include "packed.cuh"
 
+#include <initializer_list>
 #include <type_traits>
 
 namespace sdtw {
@@ -78,8 +80,8 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
 }
 
 // a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. EXACT, for
-// results of 32 bits: a is 0 and b 1 from e = 2^120 on; otherwise e ends at 2^126, which 16 bits of either do not show. A
-// NaN stays.
+// results of 32 bits: a is 0 and b 1 from e = 2^120 on. Otherwise e ends at 2^60, where b is 1 and a leaves 1e-18 of a state,
+// and two channels share a reciprocal, which bounded the kernels: 1 / s = t / (s t). A NaN stays.
 __device__ __forceinline__ float min_nan(float v, float most) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
@@ -100,9 +102,14 @@ template <bool EXACT, int VEC> __device__ __forceinline__ void gates(Pair z, Pai
     } else {
         float t0, t1;
         upk2(mul2(z, pair(-1.4426950408889634f)), t0, t1);
-        const Pair e = pk2(ex2(min_nan(t0, 126.f)), VEC > 1 ? ex2(min_nan(t1, 126.f)) : 0.f);
+        const Pair e = pk2(ex2(min_nan(t0, 60.f)), VEC > 1 ? ex2(min_nan(t1, 60.f)) : 0.f);
         upk2(add2(e, pair(1.f)), t0, t1);
-        a = pk2(reciprocal(t0), VEC > 1 ? reciprocal(t1) : 1.f);
+        if (VEC > 1) {
+            const float r = reciprocal(t0 * t1);
+            a = mul2(pk2(t1, t0), pk2(r, r));
+        } else {
+            a = pk2(reciprocal(t0), 1.f);
+        }
         b = mul2(e, a);
     }
 }
@@ -173,54 +180,43 @@ template <typename T, int VEC> __device__ __forceinline__ void clear(T* base, lo
     for (t += warp; t < N; t += warps) store<T, VEC>(base + t * C, pair(0.f));
 }
 
-// The CTA's positions of one array, as they lie in memory: by cp.async in a ring of stages, or in the lanes' registers.
+// The CTA's positions of one array, as they lie in memory: in a ring of stages in shared memory, or in the lanes' registers.
 template <typename T, int VEC, int ROWS, bool RING> struct Rows {
     typename Raw<T, VEC>::type raw[ROWS];
     __device__ __forceinline__ Pair at(int i, const unsigned char*) const { return value<T, VEC>(raw[i]); }
 };
 template <typename T, int VEC, int ROWS> struct Rows<T, VEC, ROWS, true> {
-    __device__ __forceinline__ Pair at(int i, const unsigned char* mine) const {
-        return value<T, VEC>(*reinterpret_cast<const typename Raw<T, VEC>::type*>(mine + i * 32 * VEC * (int)sizeof(T)));
-    }
+    __device__ __forceinline__ Pair at(int, const unsigned char* mine) const { return value<T, VEC>(*reinterpret_cast<const typename Raw<T, VEC>::type*>(mine)); }
 };
-// [t0, t0 + WARPS ROWS) of an array into a stage: 16-byte pieces, `none` where there is nothing. first: the thread's channels of the
-// first row.
-template <typename T, int VEC, int ROWS, int WARPS>
-__device__ __forceinline__ void send_rows(unsigned char* stage, const T* first, int step, int there, bool on, uint32_t none) {
-    constexpr int bytes = 32 * VEC * sizeof(T), pieces = bytes / 16, each = WARPS * 32 / pieces;   // rows that the threads take at a time
-    static_assert(each * pieces == WARPS * 32, "whole rows");
-    const int row = threadIdx.x / pieces;
-    unsigned char* to = stage + threadIdx.x * 16;
-    first += (long long)row * step;
-    if (there >= WARPS * ROWS && on) {
-#pragma unroll
-        for (int q = 0; q < WARPS * ROWS / each; ++q)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to + q * WARPS * 512)), "l"(first + q * each * step)
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int q = 0; q < WARPS * ROWS / each; ++q) {
-            if (row + q * each < there && on)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to + q * WARPS * 512)),
-                             "l"(first + q * each * step)
-                             : "memory");
-            else
-                *reinterpret_cast<uint4*>(to + q * WARPS * 512) = make_uint4(none, none, none, none);
-        }
-    }
+// What TMA loads from: (B, N, C) arrays in boxes of a CTA's positions by 32 lanes' channels.
+struct alignas(64) RecurrenceMaps {
+    CUtensorMap x, gate, dh;
+    int x_batch, gate_batch;   // 0: every batch element is the same one
+};
+__device__ __forceinline__ void load_box(unsigned char* to, const CUtensorMap* m, int c, int row, int b, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(m), "r"(bar), "r"(c), "r"(row), "r"(b)
+                 : "memory");
 }
-__device__ __forceinline__ void mark() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT> __device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+// Rows of a stage that stand for no position, as this lane will read them. Boxes that come there later come after it.
+template <typename T, int VEC, int ROWS> __device__ __forceinline__ void blank(unsigned char* mine, int step, int there, uint32_t none) {
+    for (int i = max(there, 0); i < ROWS; ++i) set_raw(*reinterpret_cast<typename Raw<T, VEC>::type*>(mine + i * step), none);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 
 // TIED: 1, 0, or -1: as the call says.
 template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(const RecurrenceParams p, int ctas)
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(const RecurrenceParams p, const __grid_constant__ RecurrenceMaps maps, int ctas)
 {
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     constexpr int turns = RING ? 1 : 2;                   // with a ring, all threads meet once more in a round
     __shared__ Run run[turns][WARPS][32];
-    __shared__ uint64_t s_bar[2];
-    extern __shared__ __align__(16) unsigned char ring[];   // [kStages][x, gate][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
+    __shared__ uint64_t s_bar[2 + kStages];               // of the exchange, by turns; of the stages
+    extern __shared__ __align__(128) unsigned char ring[];   // [kStages][x, gate][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + kStages * 2 * image);
     const sdtw_recurrence& a = p.a;
     const bool tied = TIED < 0 ? a.tied != 0 : TIED != 0;
@@ -237,35 +233,41 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
     const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0];
     T* out = static_cast<T*>(p.h) + (long long)b * a.N * a.C + c;
     const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
-    if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    if (threadIdx.x < 2 + kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = a.state && on ? load_f32<VEC>(a.state + bc) : pair(0.f);
     const int t0 = rank * WARPS * ROWS;                  // the CTA's first position
     int t = t0 + warp * ROWS;
-    const int mine0 = c0 + threadIdx.x % (2 * VEC * (int)sizeof(T)) * (16 / (int)sizeof(T));   // channels of the pieces that this thread sends for
-    const bool sends = mine0 < a.C;
+    // A box has its rows as they lie in memory: backwards in time, the other way round.
+    const int line = el.reverse ? -bytes : bytes;
     auto send = [&](int round) {
-        const int at = t0 + round * per;
+        if (round >= rounds || threadIdx.x != 0) return;
+        const int at = t0 + round * per, row = el.reverse ? el.len - at - WARPS * ROWS : at;
         unsigned char* stage = ring + round % kStages * 2 * image;
-        const long long r = el.row(at);
-        if (round < rounds) {
-            send_rows<T, VEC, ROWS, WARPS>(stage, x + r * a.x_stride[1] + mine0, xs, el.len - at, sends, 0);
-            send_rows<T, VEC, ROWS, WARPS>(stage + image, gate + r * a.gate_stride[1] + mine0, gs, el.len - at, sends, open_bits<T>());
-        }
-        mark();
+        const uint32_t bar = bars + 8 * (2 + round % kStages);
+        expect(bar, at < el.len ? 2 * image : 0);
+        if (at >= el.len) return;
+        load_box(stage, &maps.x, c0, row, b * maps.x_batch, bar);
+        load_box(stage + image, &maps.gate, c0, row, b * maps.gate_batch, bar);
     };
-    if constexpr (RING)
+    if constexpr (RING) {
+        __syncthreads();                                  // the barriers are there
         for (int k = 0; k < kStages - 1; ++k) send(k);
+    }
     if (ctas > 1) cluster_sync();                         // the others have begun, with barriers
     bool ok = true;
     for (int round = 0; round < rounds; ++round, t += per) {
         const int there = el.len - t, turn = round & 1;
         Rows<T, VEC, ROWS, RING> xr, gr;
-        const unsigned char* mine = ring + round % kStages * 2 * image + warp * ROWS * bytes + lane * VEC * sizeof(T);
+        unsigned char* mine = ring + round % kStages * 2 * image + (el.reverse ? WARPS * ROWS - 1 - warp * ROWS : warp * ROWS) * bytes + lane * VEC * sizeof(T);
         if constexpr (RING) {
-            landed<kStages - 2>();
-            __syncthreads();                              // everyone's pieces; and the stage before this one is read no more
+            __syncthreads();                              // the stage before this one is read no more
             send(round + kStages - 1);
+            if (!wait_arrived(bars + 8 * (2 + round % kStages), (uint32_t)(round / kStages) & 1, p.wait_ns)) ok = false;
+            if (there < ROWS) {
+                blank<T, VEC, ROWS>(mine, line, there, 0);
+                blank<T, VEC, ROWS>(mine + image, line, there, open_bits<T>());
+            }
         } else {
             const long long r = el.row(t);
             fetch<T, VEC, ROWS>(xr.raw, x + r * a.x_stride[1] + c, xs, on ? there : 0, 0);
@@ -276,8 +278,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             Pair o;
-            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image), f[i], o);
-            u[i] = tied ? mul2(o, xr.at(i, mine)) : xr.at(i, mine);
+            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image + i * line), f[i], o);
+            u[i] = tied ? mul2(o, xr.at(i, mine + i * line)) : xr.at(i, mine + i * line);
             own.a = mul2(own.a, f[i]);
             own.h = fma2(f[i], own.h, u[i]);
         }
@@ -286,27 +288,36 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
         // the runs before this warp's; the last warp goes on to the CTA's, and sends it around
         Run before{pair(1.f), pair(0.f)};
 #pragma unroll
-        for (int w = 0; w < WARPS - 1; ++w)
-            if (w < warp) {
-                const Run r = run[turn % turns][w][lane];
-                before.h = fma2(r.a, before.h, r.h);
-                before.a = mul2(before.a, r.a);
-            }
+        for (int w0 = 0; w0 < WARPS; w0 += 4) {
+            Run r[4];   // all on their way before the first is used
+#pragma unroll
+            for (int w = 0; w < 4; ++w) r[w] = run[turn % turns][w0 + w][lane];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (w0 + w < warp) {
+                    before.h = fma2(r[w].a, before.h, r[w].h);
+                    before.a = mul2(before.a, r[w].a);
+                }
+        }
         Pair h = carry;
         if (ctas > 1) {
             const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
-            if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
+            if (threadIdx.x == 0) expect(bar, ctas * 512);
             if (warp == WARPS - 1 && !(p.skip && rank == 0)) {
                 const Pair all_a = mul2(before.a, own.a), all_h = fma2(own.a, before.h, own.h);
                 for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_h);
             }
             if (ok) ok = wait_arrived(bar, (uint32_t)(round >> 1) & 1, p.wait_ns);
             if (!ok) carry = pair(__int_as_float(0x7fffffff));
-            const Run* r = total + turn * ctas * 32 + lane;
-#pragma unroll 4
-            for (int k = 0; k < ctas; ++k) {
-                if (k == rank) h = carry;
-                carry = fma2(r[k * 32].a, carry, r[k * 32].h);
+            for (int k0 = 0; k0 < ctas; k0 += 4) {
+                Run r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[k] = total[(turn * ctas + min(k0 + k, ctas - 1)) * 32 + lane];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h = k0 + k == rank ? carry : h;
+                    carry = k0 + k < ctas ? fma2(r[k].a, carry, r[k].h) : carry;
+                }
             }
         } else {
 #pragma unroll
@@ -338,14 +349,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
 }
 
 template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(const RecurrenceParams p, int ctas)
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(const RecurrenceParams p, const __grid_constant__ RecurrenceMaps maps, int ctas)
 {
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     constexpr int turns = RING ? 1 : 2;
     __shared__ Run run[turns][WARPS][32];
     __shared__ Pair back[turns][WARPS][32];
-    __shared__ uint64_t s_bar[2];
-    extern __shared__ __align__(16) unsigned char ring[];   // [2][x, gate, dh][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
+    __shared__ uint64_t s_bar[2 + 2];
+    extern __shared__ __align__(128) unsigned char ring[];   // [2][x, gate, dh][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + 2 * 3 * image);
     static_assert(WARPS * ROWS % kStep == 0 || kStep % (WARPS * ROWS) == 0, "kept states at CTAs' first positions");
     const sdtw_recurrence& a = p.a;
@@ -364,28 +375,30 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     const T* dh = static_cast<const T*>(p.dh) + base;
     T *dx = static_cast<T*>(p.dx) + base + c, *dgate = static_cast<T*>(p.dgate) + base + c;
     const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
-    if (threadIdx.x < 2) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    if (threadIdx.x < 4) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = p.dlast && on ? load_f32<VEC>(p.dlast + bc) : pair(0.f);
     const int t0 = rank * WARPS * ROWS;
-    const int mine0 = c0 + threadIdx.x % (2 * VEC * (int)sizeof(T)) * (16 / (int)sizeof(T));   // channels of the pieces that this thread sends for
-    const bool sends = mine0 < a.C;
+    const int line = el.reverse ? -bytes : bytes;
     auto send = [&](int round) {
-        const int at = t0 + round * per;
+        if (round < 0 || threadIdx.x != 0) return;
+        const int at = t0 + round * per, row = el.reverse ? el.len - at - WARPS * ROWS : at;
         unsigned char* stage = ring + (round & 1) * 3 * image;
-        const long long r = el.row(at);
-        if (round >= 0) {
-            send_rows<T, VEC, ROWS, WARPS>(stage, x + r * a.x_stride[1] + mine0, xs, el.len - at, sends, 0);
-            send_rows<T, VEC, ROWS, WARPS>(stage + image, gate + r * a.gate_stride[1] + mine0, gs, el.len - at, sends, open_bits<T>());
-            send_rows<T, VEC, ROWS, WARPS>(stage + 2 * image, dh + r * a.C + mine0, step, p.dh ? el.len - at : 0, sends, 0);
-        }
-        mark();
+        const uint32_t bar = bars + 8 * (2 + (round & 1));
+        expect(bar, at < el.len ? (p.dh ? 3 : 2) * image : 0);
+        if (at >= el.len) return;
+        load_box(stage, &maps.x, c0, row, b * maps.x_batch, bar);
+        load_box(stage + image, &maps.gate, c0, row, b * maps.gate_batch, bar);
+        if (p.dh) load_box(stage + 2 * image, &maps.dh, c0, row, b, bar);
     };
     auto kept = [&](int round) {   // the state before the CTA's first position
         const int at = t0 + round * per;
         return on && round >= 0 && at < el.len ? load_f32<VEC>(p.kept_in + ((long long)b * steps + at / kStep) * a.C + c) : pair(0.f);
     };
-    if constexpr (RING) send(rounds - 1);
+    if constexpr (RING) {
+        __syncthreads();
+        send(rounds - 1);
+    }
     Pair state = kept(rounds - 1);
     if (ctas > 1) cluster_sync();
     bool ok = true;
@@ -393,11 +406,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     for (int round = rounds - 1; round >= 0; --round) {
         const int t = t0 + round * per + warp * ROWS, there = on ? el.len - t : 0;
         Rows<T, VEC, ROWS, RING> xr, gr, dr;
-        const unsigned char* mine = ring + (round & 1) * 3 * image + warp * ROWS * bytes + lane * VEC * sizeof(T);
+        unsigned char* mine = ring + (round & 1) * 3 * image + (el.reverse ? WARPS * ROWS - 1 - warp * ROWS : warp * ROWS) * bytes + lane * VEC * sizeof(T);
         if constexpr (RING) {
-            landed<0>();
             __syncthreads();
             send(round - 1);
+            if (!wait_arrived(bars + 8 * (2 + (round & 1)), (uint32_t)((rounds - 1 - round) >> 1) & 1, p.wait_ns)) ok = false;
+            if (el.len - t < ROWS) {
+                blank<T, VEC, ROWS>(mine, line, el.len - t, 0);
+                blank<T, VEC, ROWS>(mine + image, line, el.len - t, open_bits<T>());
+            }
+            if (el.len - t < ROWS || !p.dh) blank<T, VEC, ROWS>(mine + 2 * image, line, p.dh ? el.len - t : 0, 0);
         } else {
             const long long r = el.row(t);
             fetch<T, VEC, ROWS>(xr.raw, x + r * a.x_stride[1] + c, xs, there, 0);
@@ -408,11 +426,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
         Run own{pair(1.f), pair(0.f)};
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image), f[i], o[i]);
-            const Pair v = xr.at(i, mine);
+            gates<sizeof(T) == 4, VEC>(gr.at(i, mine + image + i * line), f[i], o[i]);
+            const Pair v = xr.at(i, mine + i * line);
             own.a = mul2(own.a, f[i]);
             own.h = fma2(f[i], own.h, tied ? mul2(o[i], v) : v);
-            r = fma2(own.a, dr.at(i, mine + 2 * image), r);
+            r = fma2(own.a, dr.at(i, mine + 2 * image + i * line), r);
         }
         run[turn % turns][warp][lane] = own;
         back[turn % turns][warp][lane] = r;
@@ -421,33 +439,52 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
         // the state before the run, and what the later runs of the CTA hand back; the first warp goes on to the CTA's
         Run behind{pair(1.f), pair(0.f)};
 #pragma unroll
-        for (int w = WARPS - 1; w > 0; --w)
-            if (w > warp) {
-                const Pair wa = run[turn % turns][w][lane].a;
-                behind.h = fma2(wa, behind.h, back[turn % turns][w][lane]);
-                behind.a = mul2(behind.a, wa);
-            }
+        for (int w0 = WARPS - 4; w0 >= 0; w0 -= 4) {
+            Pair wa[4], wr[4];   // all on their way before the first is used
 #pragma unroll
-        for (int w = 0; w < WARPS - 1; ++w)
-            if (w < warp) h = fma2(run[turn % turns][w][lane].a, h, run[turn % turns][w][lane].h);
+            for (int w = 0; w < 4; ++w) wa[w] = run[turn % turns][w0 + w][lane].a, wr[w] = back[turn % turns][w0 + w][lane];
+#pragma unroll
+            for (int w = 3; w >= 0; --w)
+                if (w0 + w > warp) {
+                    behind.h = fma2(wa[w], behind.h, wr[w]);
+                    behind.a = mul2(behind.a, wa[w]);
+                }
+        }
         const Pair own_r = r;
         r = carry;
+        auto states = [&] {   // off the way of what the other CTAs wait for
+#pragma unroll
+            for (int w0 = 0; w0 < WARPS; w0 += 4) {
+                Run q[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) q[w] = run[turn % turns][w0 + w][lane];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    if (w0 + w < warp) h = fma2(q[w].a, h, q[w].h);
+            }
+        };
         if (ctas > 1) {
             const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
-            if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(ctas * 512) : "memory");
+            if (threadIdx.x == 0) expect(bar, ctas * 512);
             if (warp == 0 && !(p.skip && rank == 0)) {
                 const Pair all_a = mul2(behind.a, own.a), all_r = fma2(own.a, behind.h, own_r);
                 for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
             }
+            states();
             if (ok) ok = wait_arrived(bar, (uint32_t)phase, p.wait_ns);
             if (!ok) carry = pair(__int_as_float(0x7fffffff));
-            const Run* q = total + turn * ctas * 32 + lane;
-#pragma unroll 4
-            for (int k = ctas - 1; k >= 0; --k) {
-                if (k == rank) r = carry;
-                carry = fma2(q[k * 32].a, carry, q[k * 32].h);
+            for (int k0 = ctas - 1; k0 >= 0; k0 -= 4) {
+                Run q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = total[(turn * ctas + max(k0 - k, 0)) * 32 + lane];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    r = k0 - k == rank ? carry : r;
+                    carry = k0 - k >= 0 ? fma2(q[k].a, carry, q[k].h) : carry;
+                }
             }
         } else {
+            states();
 #pragma unroll
             for (int w = WARPS - 1; w >= 0; --w) carry = fma2(run[turn % turns][w][lane].a, carry, back[turn % turns][w][lane]);
         }
@@ -459,14 +496,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
         Pair w[ROWS];   // dgate_t / e_t
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const Pair v = xr.at(i, mine);
+            const Pair v = xr.at(i, mine + i * line);
             w[i] = mul2(mul2(f[i], o[i]), tied ? fma2(v, pair(-1.f), h) : h);
             h = fma2(f[i], h, tied ? mul2(o[i], v) : v);
         }
         auto go = [&](bool every) {
 #pragma unroll
             for (int i = ROWS - 1; i >= 0; --i) {
-                const Pair e = add2(dr.at(i, mine + 2 * image), r);
+                const Pair e = add2(dr.at(i, mine + 2 * image + i * line), r);
                 r = mul2(f[i], e);
                 if (every || i < there) {
                     store<T, VEC>(dx + row + i * step, tied ? mul2(o[i], e) : e);
@@ -520,7 +557,8 @@ template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) 
     if (p.last) store_f32<VEC>(p.last + bc, h);
 }
 
-template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas, int warps, size_t images, size_t totals, cudaStream_t s, const RecurrenceParams& p)
+template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas, int warps, size_t images, size_t totals, cudaStream_t s, const RecurrenceParams& p,
+                                                  const RecurrenceMaps& maps)
 {
     if (const cudaError_t e = allow_smem<Kernel>(images + kMostCtas * totals); e != cudaSuccess) return e;
     if (ctas > 8)
@@ -531,7 +569,17 @@ template <auto Kernel> cudaError_t launch_clusters(long long clusters, int ctas,
     at.val.clusterDim.x = (unsigned)ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
     c.gridDim = dim3((unsigned)(clusters * ctas)), c.blockDim = dim3(warps * 32), c.stream = s, c.attrs = &at, c.numAttrs = ctas > 1 ? 1 : 0;
     c.dynamicSmemBytes = images + (ctas > 1 ? ctas * totals : 0);
-    return cudaLaunchKernelEx(&c, Kernel, p, ctas);
+    return cudaLaunchKernelEx(&c, Kernel, p, maps, ctas);
+}
+
+bool map_positions(CUtensorMap* m, const RecurrenceParams& p, const void* base, long long batch, long long row, int channels, int positions)
+{
+    const sdtw_recurrence& a = p.a;
+    const int size = dtype_size(a.dtype);
+    const cuuint64_t dims[3] = {(cuuint64_t)a.C, (cuuint64_t)a.N, (cuuint64_t)(batch ? a.B : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)(a.N > 1 ? row * size : 16), (cuuint64_t)(a.B > 1 && batch ? batch * size : 16)};
+    const cuuint32_t box[3] = {(cuuint32_t)channels, (cuuint32_t)positions, 1};
+    return atc::encode(m, a.dtype, 3, base, dims, strides, box, false);
 }
 
 // CTAs of a cluster: as many as it takes to fill the places that there are, no more than there are runs.
@@ -550,8 +598,16 @@ template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED> cudaErr
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
     constexpr size_t image = RING ? WARPS * ROWS * 32 * VEC * sizeof(T) : 0;
     const size_t images = (backward ? 2 * 3 : kStages * 2) * image, totals = sizeof(Run) * 2 * 32;   // of a CTA of the cluster
-    if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p);
-    return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p);
+    RecurrenceMaps maps{};
+    if (RING) {
+        maps.x_batch = a.x_stride[0] != 0, maps.gate_batch = a.gate_stride[0] != 0;
+        if (!map_positions(&maps.x, p, a.x, a.x_stride[0], a.x_stride[1], 32 * VEC, WARPS * ROWS) ||
+            !map_positions(&maps.gate, p, a.gate, a.gate_stride[0], a.gate_stride[1], 32 * VEC, WARPS * ROWS) ||
+            (p.dh && !map_positions(&maps.dh, p, p.dh, (long long)a.N * a.C, a.C, 32 * VEC, WARPS * ROWS)))
+            return cudaErrorInvalidValue;
+    }
+    if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p, maps);
+    return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p, maps);
 }
 // Two CTAs of eight warps an SM. Where the largest clusters leave half of these places empty, one of sixteen: a cluster then
 // takes twice the positions at a time, and what a round costs, some 3 us whatever its size, comes half as often.
@@ -584,7 +640,9 @@ template <typename T> cudaError_t run(const RecurrenceParams& p, bool backward, 
     pairs = pairs && (backward ? on(p.dh, 2 * sizeof(T)) && on(p.dx, 2 * sizeof(T)) && on(p.dgate, 2 * sizeof(T)) && on(p.dlast, 8) && on(p.dstate, 8) && on(p.kept_in, 8)
                                : on(p.h, 2 * sizeof(T)) && on(p.last, 8) && on(p.kept, 8));
     if (!backward && a.N <= kFewRows) return pairs ? run_few<T, 2>(p, s) : run_few<T, 1>(p, s);
-    const bool ring = pairs && strides(pack) && on(a.x, 16) && on(a.gate, 16) && on(p.dh, 16);
+    bool ring = pairs && strides(pack) && on(a.x, 16) && on(a.gate, 16) && on(p.dh, 16);
+    for (const long long* st : {a.x_stride, a.gate_stride})
+        ring = ring && (a.N == 1 || st[1] > 0) && (a.B == 1 || (st[0] >= 0 && st[0] < (1ll << 36)));   // as tensor maps have them
     if (!ring) return run_rows<T, 1, 8, false, -1>(p, backward, sms, s);
     constexpr int ROWS = sizeof(T) == 4 ? 8 : 16;
     return a.tied ? run_rows<T, 2, ROWS, true, 1>(p, backward, sms, s) : run_rows<T, 2, ROWS, true, 0>(p, backward, sms, s);

@@ -478,7 +478,7 @@ Tensor group_norm(const Tensor& x_, int64_t groups, const Maybe& weight, const M
 
 // ---- gated recurrence
 // channels side by side, and rows of a stride that the kernels take
-Tensor with_channels(const Tensor& t) { return (t.stride(2) == 1 || t.size(2) == 1) && t.stride(1) <= 1 << 23 ? t : t.contiguous(); }
+Tensor with_channels(const Tensor& t) { return (t.stride(2) == 1 || t.size(2) == 1) && t.stride(1) > 0 && t.stride(1) <= 1 << 23 ? t : t.contiguous(); }
 
 sdtw_recurrence recurrence(const Tensor& x, const Tensor& gate, const Tensor& state, const Tensor& lengths, bool reverse, bool tied)
 {
