@@ -41,7 +41,7 @@ struct Seg {
     unsigned char a, map;
 };
 
-struct alignas(64) Params {
+struct Params {
     CUtensorMap a, b[2];
     Seg seg[2];
     int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks

@@ -13,7 +13,8 @@
 //
 // Coming positions are on their way to shared memory meanwhile (TMA; sizes and addresses that do not allow it are loaded by
 // the lanes that use them). Pairs go between CTAs by stores that report to the receiver's mbarrier: a
-// cluster's own barrier also waits for the results that are on their way to memory.
+// cluster's own barrier also waits for the results that are on their way to memory. One warp folds the CTAs' pairs and hands the
+// state on: read by every warp, they took 900 cycles of shared memory a round.
 #include "activation.cuh"
 #include "attn_tc.cuh"
 #include "block.h"
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kStep = SDTW_RECURRENCE_STEP;
 constexpr int kMostCtas = 16;   // of a cluster
-constexpr int kStages = 3;      // of the forward pass's ring
+constexpr int kStages = 3;      // of the forward pass's ring: coming, in work, and results on their way out
 
 __device__ __forceinline__ Pair pair(float v) { return pk2(v, v); }
 
@@ -189,8 +190,8 @@ template <typename T, int VEC, int ROWS> struct Rows<T, VEC, ROWS, true> {
     __device__ __forceinline__ Pair at(int, const unsigned char* mine) const { return value<T, VEC>(*reinterpret_cast<const typename Raw<T, VEC>::type*>(mine)); }
 };
 // What TMA loads from: (B, N, C) arrays in boxes of a CTA's positions by 32 lanes' channels.
-struct alignas(64) RecurrenceMaps {
-    CUtensorMap x, gate, dh;
+struct RecurrenceMaps {
+    CUtensorMap x, gate, dh, h;
     int x_batch, gate_batch;   // 0: every batch element is the same one
 };
 __device__ __forceinline__ void load_box(unsigned char* to, const CUtensorMap* m, int c, int row, int b, uint32_t bar) {
@@ -199,6 +200,12 @@ __device__ __forceinline__ void load_box(unsigned char* to, const CUtensorMap* m
                  "l"(m), "r"(bar), "r"(c), "r"(row), "r"(b)
                  : "memory");
 }
+__device__ __forceinline__ void store_box(const CUtensorMap* m, const unsigned char* from, int c, int row, int b) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(m),
+                 "r"((uint32_t)__cvta_generic_to_shared(from)), "r"(c), "r"(row), "r"(b)
+                 : "memory");
+}
+__device__ __forceinline__ void stored() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }   // shared memory is read no more
 // Rows of a stage that stand for no position, as this lane will read them. Boxes that come there later come after it.
 template <typename T, int VEC, int ROWS> __device__ __forceinline__ void blank(unsigned char* mine, int step, int there, uint32_t none) {
     for (int i = max(there, 0); i < ROWS; ++i) set_raw(*reinterpret_cast<typename Raw<T, VEC>::type*>(mine + i * step), none);
@@ -213,8 +220,8 @@ template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(const RecurrenceParams p, const __grid_constant__ RecurrenceMaps maps, int ctas)
 {
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
-    constexpr int turns = RING ? 1 : 2;                   // with a ring, all threads meet once more in a round
-    __shared__ Run run[turns][WARPS][32];
+    __shared__ Run run[WARPS][32];
+    __shared__ Pair s_in[32];                             // states before the CTA's positions
     __shared__ uint64_t s_bar[2 + kStages];               // of the exchange, by turns; of the stages
     extern __shared__ __align__(128) unsigned char ring[];   // [kStages][x, gate][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + kStages * 2 * image);
@@ -250,9 +257,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
         load_box(stage, &maps.x, c0, row, b * maps.x_batch, bar);
         load_box(stage + image, &maps.gate, c0, row, b * maps.gate_batch, bar);
     };
+    // results of whole tiles go out from x's place in their stage
+    auto whole = [&](int round) { return RING && round >= 0 && el.len - (t0 + round * per) >= WARPS * ROWS; };
+    auto put_out = [&](int round) {
+        if (!whole(round) || threadIdx.x != 0) return;
+        const int at = t0 + round * per;
+        store_box(&maps.h, ring + round % kStages * 2 * image, c0, el.reverse ? el.len - at - WARPS * ROWS : at, b);
+    };
     if constexpr (RING) {
         __syncthreads();                                  // the barriers are there
-        for (int k = 0; k < kStages - 1; ++k) send(k);
+        send(0);
     }
     if (ctas > 1) cluster_sync();                         // the others have begun, with barriers
     bool ok = true;
@@ -261,8 +275,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
         Rows<T, VEC, ROWS, RING> xr, gr;
         unsigned char* mine = ring + round % kStages * 2 * image + (el.reverse ? WARPS * ROWS - 1 - warp * ROWS : warp * ROWS) * bytes + lane * VEC * sizeof(T);
         if constexpr (RING) {
-            __syncthreads();                              // the stage before this one is read no more
-            send(round + kStages - 1);
+            __syncthreads();                              // the last round's results are in their stage
+            if (threadIdx.x == 0) stored();               // those of the round before it have left theirs, the next to be filled
+            put_out(round - 1);
+            send(round + 1);
             if (!wait_arrived(bars + 8 * (2 + round % kStages), (uint32_t)(round / kStages) & 1, p.wait_ns)) ok = false;
             if (there < ROWS) {
                 blank<T, VEC, ROWS>(mine, line, there, 0);
@@ -283,47 +299,61 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
             own.a = mul2(own.a, f[i]);
             own.h = fma2(f[i], own.h, u[i]);
         }
-        run[turn % turns][warp][lane] = own;
+        run[warp][lane] = own;
         __syncthreads();
-        // the runs before this warp's; the last warp goes on to the CTA's, and sends it around
+        // the runs before this warp's; the last warp goes on to the CTA's
         Run before{pair(1.f), pair(0.f)};
 #pragma unroll
-        for (int w0 = 0; w0 < WARPS; w0 += 4) {
-            Run r[4];   // all on their way before the first is used
+        for (int w0 = 0; w0 < WARPS; w0 += 4)
+            if (w0 < warp) {
+                Run r[4];   // all on their way before the first is used
 #pragma unroll
-            for (int w = 0; w < 4; ++w) r[w] = run[turn % turns][w0 + w][lane];
+                for (int w = 0; w < 4; ++w) r[w] = run[w0 + w][lane];
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-                if (w0 + w < warp) {
-                    before.h = fma2(r[w].a, before.h, r[w].h);
-                    before.a = mul2(before.a, r[w].a);
-                }
-        }
-        Pair h = carry;
-        if (ctas > 1) {
-            const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
-            if (threadIdx.x == 0) expect(bar, ctas * 512);
-            if (warp == WARPS - 1 && !(p.skip && rank == 0)) {
-                const Pair all_a = mul2(before.a, own.a), all_h = fma2(own.a, before.h, own.h);
-                for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_h);
+                for (int w = 0; w < 4; ++w)
+                    if (w0 + w < warp) {
+                        before.h = fma2(r[w].a, before.h, r[w].h);
+                        before.a = mul2(before.a, r[w].a);
+                    }
             }
-            if (ok) ok = wait_arrived(bar, (uint32_t)(round >> 1) & 1, p.wait_ns);
-            if (!ok) carry = pair(__int_as_float(0x7fffffff));
-            for (int k0 = 0; k0 < ctas; k0 += 4) {
-                Run r[4];
+        if (warp == WARPS - 1) {
+            const Pair all_a = mul2(before.a, own.a), all_h = fma2(own.a, before.h, own.h);
+            Pair in = carry;
+            if (ctas > 1) {
+                const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
+                if (lane == 0) expect(bar, ctas * 512);
+                if (!(p.skip && rank == 0))
+                    for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_h);
+                if (!wait_arrived(bar, (uint32_t)(round >> 1) & 1, ok ? p.wait_ns : 0)) ok = false;
+                if (!ok) carry = pair(__int_as_float(0x7fffffff));
+                for (int k0 = 0; k0 < ctas; k0 += 4) {
+                    Run r[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = total[(turn * ctas + min(k0 + k, ctas - 1)) * 32 + lane];
+                    for (int k = 0; k < 4; ++k) r[k] = total[(turn * ctas + min(k0 + k, ctas - 1)) * 32 + lane];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    h = k0 + k == rank ? carry : h;
-                    carry = k0 + k < ctas ? fma2(r[k].a, carry, r[k].h) : carry;
+                    for (int k = 0; k < 4; ++k) {
+                        in = k0 + k == rank ? carry : in;
+                        carry = k0 + k < ctas ? fma2(r[k].a, carry, r[k].h) : carry;
+                    }
                 }
+            } else {
+                if (!ok) in = pair(__int_as_float(0x7fffffff));
+                carry = fma2(all_a, in, all_h);
             }
-        } else {
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) carry = fma2(run[turn % turns][w][lane].a, carry, run[turn % turns][w][lane].h);
+            s_in[lane] = in;
         }
-        h = fma2(before.a, h, before.h);
+        __syncthreads();
+        Pair h = fma2(before.a, s_in[lane], before.h);
+        if (whole(round)) {
+            if (on && p.kept && t % kStep == 0) store_f32<VEC>(p.kept + ((long long)b * steps + t / kStep) * a.C + c, h);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                h = fma2(f[i], h, u[i]);
+                store<T, VEC>(reinterpret_cast<T*>(mine + i * line), h);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            continue;
+        }
         if (!on) continue;
         if (p.kept && t % kStep == 0 && t < a.N) store_f32<VEC>(p.kept + ((long long)b * steps + t / kStep) * a.C + c, h);
         T* dst = out + (long long)el.row(t) * a.C;
@@ -342,19 +372,23 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
             clear<T, VEC>(out, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
         }
     }
+    if constexpr (RING) {
+        __syncthreads();
+        put_out(rounds - 1);
+        if (threadIdx.x == 0) stored();
+    }
     if (ctas > 1) cluster_sync();                         // no store may come to a CTA that has ended
     if (!on) return;
     clear<T, VEC>(out, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
-    if (p.last && rank == 0 && warp == 0) store_f32<VEC>(p.last + bc, carry);
+    if (p.last && rank == 0 && warp == WARPS - 1) store_f32<VEC>(p.last + bc, carry);
 }
 
 template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(const RecurrenceParams p, const __grid_constant__ RecurrenceMaps maps, int ctas)
 {
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
-    constexpr int turns = RING ? 1 : 2;
-    __shared__ Run run[turns][WARPS][32];
-    __shared__ Pair back[turns][WARPS][32];
+    __shared__ Run run[WARPS][32];
+    __shared__ Pair back[WARPS][32], s_in[32];            // s_in: what the positions after the CTA's hand back
     __shared__ uint64_t s_bar[2 + 2];
     extern __shared__ __align__(128) unsigned char ring[];   // [2][x, gate, dh][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + 2 * 3 * image);
@@ -432,62 +466,64 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
             own.h = fma2(f[i], own.h, tied ? mul2(o[i], v) : v);
             r = fma2(own.a, dr.at(i, mine + 2 * image + i * line), r);
         }
-        run[turn % turns][warp][lane] = own;
-        back[turn % turns][warp][lane] = r;
+        run[warp][lane] = own;
+        back[warp][lane] = r;
         state = kept(round - 1);
         __syncthreads();
-        // the state before the run, and what the later runs of the CTA hand back; the first warp goes on to the CTA's
+        // what the later runs of the CTA hand back; the first warp goes on to the CTA's
         Run behind{pair(1.f), pair(0.f)};
 #pragma unroll
-        for (int w0 = WARPS - 4; w0 >= 0; w0 -= 4) {
-            Pair wa[4], wr[4];   // all on their way before the first is used
+        for (int w0 = WARPS - 4; w0 >= 0; w0 -= 4)
+            if (w0 + 3 > warp) {
+                Pair wa[4], wr[4];   // all on their way before the first is used
 #pragma unroll
-            for (int w = 0; w < 4; ++w) wa[w] = run[turn % turns][w0 + w][lane].a, wr[w] = back[turn % turns][w0 + w][lane];
+                for (int w = 0; w < 4; ++w) wa[w] = run[w0 + w][lane].a, wr[w] = back[w0 + w][lane];
 #pragma unroll
-            for (int w = 3; w >= 0; --w)
-                if (w0 + w > warp) {
-                    behind.h = fma2(wa[w], behind.h, wr[w]);
-                    behind.a = mul2(behind.a, wa[w]);
+                for (int w = 3; w >= 0; --w)
+                    if (w0 + w > warp) {
+                        behind.h = fma2(wa[w], behind.h, wr[w]);
+                        behind.a = mul2(behind.a, wa[w]);
+                    }
+            }
+        if (warp == 0) {
+            const Pair all_a = mul2(behind.a, own.a), all_r = fma2(own.a, behind.h, r);
+            Pair in = carry;
+            if (ctas > 1) {
+                const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
+                if (lane == 0) expect(bar, ctas * 512);
+                if (!(p.skip && rank == 0))
+                    for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
+                if (!wait_arrived(bar, (uint32_t)phase, ok ? p.wait_ns : 0)) ok = false;
+                if (!ok) carry = pair(__int_as_float(0x7fffffff));
+                for (int k0 = ctas - 1; k0 >= 0; k0 -= 4) {
+                    Run q[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = total[(turn * ctas + max(k0 - k, 0)) * 32 + lane];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        in = k0 - k == rank ? carry : in;
+                        carry = k0 - k >= 0 ? fma2(q[k].a, carry, q[k].h) : carry;
+                    }
                 }
+            } else {
+                if (!ok) in = pair(__int_as_float(0x7fffffff));
+                carry = fma2(all_a, in, all_r);
+            }
+            s_in[lane] = in;
         }
-        const Pair own_r = r;
-        r = carry;
-        auto states = [&] {   // off the way of what the other CTAs wait for
+        // the state before the run
 #pragma unroll
-            for (int w0 = 0; w0 < WARPS; w0 += 4) {
+        for (int w0 = 0; w0 < WARPS; w0 += 4)
+            if (w0 < warp) {
                 Run q[4];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) q[w] = run[turn % turns][w0 + w][lane];
+                for (int w = 0; w < 4; ++w) q[w] = run[w0 + w][lane];
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
                     if (w0 + w < warp) h = fma2(q[w].a, h, q[w].h);
             }
-        };
-        if (ctas > 1) {
-            const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
-            if (threadIdx.x == 0) expect(bar, ctas * 512);
-            if (warp == 0 && !(p.skip && rank == 0)) {
-                const Pair all_a = mul2(behind.a, own.a), all_r = fma2(own.a, behind.h, own_r);
-                for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
-            }
-            states();
-            if (ok) ok = wait_arrived(bar, (uint32_t)phase, p.wait_ns);
-            if (!ok) carry = pair(__int_as_float(0x7fffffff));
-            for (int k0 = ctas - 1; k0 >= 0; k0 -= 4) {
-                Run q[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) q[k] = total[(turn * ctas + max(k0 - k, 0)) * 32 + lane];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    r = k0 - k == rank ? carry : r;
-                    carry = k0 - k >= 0 ? fma2(q[k].a, carry, q[k].h) : carry;
-                }
-            }
-        } else {
-            states();
-#pragma unroll
-            for (int w = WARPS - 1; w >= 0; --w) carry = fma2(run[turn % turns][w][lane].a, carry, back[turn % turns][w][lane]);
-        }
+        __syncthreads();
+        r = s_in[lane];
         phase ^= turn;   // every second round
         turn ^= 1;
         r = fma2(behind.a, r, behind.h);
@@ -603,7 +639,8 @@ template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED> cudaErr
         maps.x_batch = a.x_stride[0] != 0, maps.gate_batch = a.gate_stride[0] != 0;
         if (!map_positions(&maps.x, p, a.x, a.x_stride[0], a.x_stride[1], 32 * VEC, WARPS * ROWS) ||
             !map_positions(&maps.gate, p, a.gate, a.gate_stride[0], a.gate_stride[1], 32 * VEC, WARPS * ROWS) ||
-            (p.dh && !map_positions(&maps.dh, p, p.dh, (long long)a.N * a.C, a.C, 32 * VEC, WARPS * ROWS)))
+            (p.dh && !map_positions(&maps.dh, p, p.dh, (long long)a.N * a.C, a.C, 32 * VEC, WARPS * ROWS)) ||
+            (!backward && !map_positions(&maps.h, p, p.h, (long long)a.N * a.C, a.C, 32 * VEC, WARPS * ROWS)))
             return cudaErrorInvalidValue;
     }
     if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p, maps);
@@ -640,7 +677,7 @@ template <typename T> cudaError_t run(const RecurrenceParams& p, bool backward, 
     pairs = pairs && (backward ? on(p.dh, 2 * sizeof(T)) && on(p.dx, 2 * sizeof(T)) && on(p.dgate, 2 * sizeof(T)) && on(p.dlast, 8) && on(p.dstate, 8) && on(p.kept_in, 8)
                                : on(p.h, 2 * sizeof(T)) && on(p.last, 8) && on(p.kept, 8));
     if (!backward && a.N <= kFewRows) return pairs ? run_few<T, 2>(p, s) : run_few<T, 1>(p, s);
-    bool ring = pairs && strides(pack) && on(a.x, 16) && on(a.gate, 16) && on(p.dh, 16);
+    bool ring = pairs && strides(pack) && on(a.x, 16) && on(a.gate, 16) && on(p.dh, 16) && on(p.h, 16);
     for (const long long* st : {a.x_stride, a.gate_stride})
         ring = ring && (a.N == 1 || st[1] > 0) && (a.B == 1 || (st[0] >= 0 && st[0] < (1ll << 36)));   // as tensor maps have them
     if (!ring) return run_rows<T, 1, 8, false, -1>(p, backward, sms, s);
