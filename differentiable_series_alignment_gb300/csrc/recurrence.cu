@@ -20,6 +20,7 @@
 #include "block.h"
 #include "packed.cuh"
 
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -618,14 +619,6 @@ bool map_positions(CUtensorMap* m, const RecurrenceParams& p, const void* base, 
     return atc::encode(m, a.dtype, 3, base, dims, strides, box, false);
 }
 
-// CTAs of a cluster: as many as it takes to fill the places that there are, no more than there are runs.
-int cluster_size(long long clusters, int N, int positions, long long places)
-{
-    int k = 1;
-    while (k < kMostCtas && clusters * k < places && (long long)k * positions < N) k *= 2;
-    return k;
-}
-
 constexpr int kFewRows = 8;
 
 template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED> cudaError_t run_warps(const RecurrenceParams& p, bool backward, int ctas, cudaStream_t s)
@@ -646,16 +639,49 @@ template <typename T, int VEC, int ROWS, int WARPS, bool RING, int TIED> cudaErr
     if (backward) return launch_clusters<recurrence_bwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p, maps);
     return launch_clusters<recurrence_fwd_kernel<T, VEC, ROWS, WARPS, RING, TIED>>(clusters, ctas, WARPS, images, totals, s, p, maps);
 }
-// Two CTAs of eight warps an SM. Where the largest clusters leave half of these places empty, one of sixteen: a cluster then
-// takes twice the positions at a time, and what a round costs, some 3 us whatever its size, comes half as often.
+// How many clusters of 2^i CTAs can be resident at once; asked once per device.
+template <auto Kernel> int resident(int i, int threads, size_t smem)
+{
+    static std::atomic<int> known[8][5];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>* place = dev < 8 ? &known[dev][i] : nullptr;
+    if (place && (n = place->load(std::memory_order_relaxed)) > 0) return n - 1;
+    if (allow_smem<Kernel>(smem) != cudaSuccess || (i > 3 && cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+        return 0;
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 1u << i, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.gridDim = dim3(1u << i), c.blockDim = dim3((unsigned)threads), c.dynamicSmemBytes = smem, c.attrs = &at, c.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &c) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (place) place->store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Few clusters are of CTAs of sixteen warps, one an SM, in the largest clusters of which all are resident at once: what a
+// round costs, some 2 us whatever its size, then comes least often (2 x 8192 x 264 fp16 forward: 14 us; with clusters of
+// twice as many CTAs of eight warps, which do not all fit, 22). Many take two CTAs of eight warps an SM, as many to a cluster
+// as fill these places (4 x 8192 x 1024 fp32 backward: 107 us, 121 with sixteen warps).
 template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
     const sdtw_recurrence& a = p.a;
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
-    const int ctas = cluster_size(clusters, a.N, 8 * ROWS, 2 * sms);
-    if constexpr (RING)
-        if (clusters * ctas <= sms && a.N > 8ll * ROWS * ctas) return run_warps<T, VEC, ROWS, 16, RING, TIED>(p, backward, ctas, s);
-    return run_warps<T, VEC, ROWS, 8, RING, TIED>(p, backward, ctas, s);
+    if constexpr (RING) {
+        constexpr size_t image = 16 * ROWS * 32 * VEC * sizeof(T), totals = sizeof(Run) * 2 * 32;
+        for (int i = 4; i >= 2 && 4 * clusters <= sms; --i) {
+            if (8ll * ROWS << i >= a.N) continue;              // half as many would do
+            const int n = backward ? resident<recurrence_bwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 6 * image + kMostCtas * totals)
+                                   : resident<recurrence_fwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 2 * kStages * image + kMostCtas * totals);
+            if (clusters <= n) return run_warps<T, VEC, ROWS, 16, RING, TIED>(p, backward, 1 << i, s);
+        }
+    }
+    int k = 1;
+    while (k < 8 && clusters * k < 2ll * sms && 8ll * ROWS * k < a.N) k *= 2;
+    return run_warps<T, VEC, ROWS, 8, RING, TIED>(p, backward, k, s);
 }
 template <typename T, int VEC> cudaError_t run_few(const RecurrenceParams& p, cudaStream_t s)
 {
