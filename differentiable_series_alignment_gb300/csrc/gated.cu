@@ -22,11 +22,11 @@ using gtc::kParts;
 // matter as long as both operands agree. Tiles of 128 rows on the tensor cores would be empty but for these.
 template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
 template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 template <> __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -49,17 +49,21 @@ template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_k
     const sdtw_gated& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, at = (lane & 3) * 8, f0 = blockIdx.x * 16;
     const int R = (int)a.R;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // volatile: in this order, before the products
     auto load = [&](const void* base, long long stride, int r, int rows, int k) {
-        return r < rows && k < a.K ? *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + r * stride + k) : zero;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                     : "l"(static_cast<const T*>(base) + r * stride + k), "r"((int)(r < rows && k < a.K)));
+        return v;
     };
     float acc[2][NT][4] = {};
     constexpr int AHEAD = NT == 4 ? 2 : 4;   // pieces whose loads are all on their way before the first product
-    for (int k0 = warp * 32; k0 < a.K; k0 += 256 * AHEAD) {
+    for (int k0 = warp * 32 * AHEAD; k0 < a.K; k0 += 256 * AHEAD) {   // a warp's pieces are neighbours: 256 bytes of a row
         uint4 w[AHEAD][2][2], x[AHEAD][NT];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int k = k0 + i * 256 + at;
+            const int k = k0 + i * 32 + at;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 w[i][0][h] = load(a.gate_weight, a.gate_stride, f0 + row + 8 * h, a.F, k);
@@ -97,42 +101,50 @@ template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_k
     }
 }
 
-// Few rows of fp32, or of any stride and address: a warp a feature, eight rows at a time, element by element.
-template <typename T> __global__ void __launch_bounds__(256) gated_dot_kernel(const GatedParams p)
+// Few rows of fp32, or of any stride and address: a warp two features, eight rows at a time, so that what it reads of x serves
+// four rows of weights; VEC neighbours of a row at a time where they are one aligned load.
+template <typename T, int VEC> __global__ void __launch_bounds__(256) gated_dot_kernel(const GatedParams p)
 {
+    using P = Pack<T, VEC>;
     const sdtw_gated& a = p.a;
-    const int lane = threadIdx.x & 31, f = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (f >= a.F) return;
-    const T* wg = static_cast<const T*>(a.gate_weight) + f * a.gate_stride;
-    const T* wu = static_cast<const T*>(a.up_weight) + f * a.up_stride;
-    const float bg = a.gate_bias ? to_f32(static_cast<const T*>(a.gate_bias)[f]) : 0.f;
-    const float bu = a.up_bias ? to_f32(static_cast<const T*>(a.up_bias)[f]) : 0.f;
+    const int lane = threadIdx.x & 31, f0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 2;
+    if (f0 >= a.F) return;
+    const T* w[4];   // gate and up of either feature
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long f = min(f0 + i / 2, a.F - 1);
+        w[i] = i % 2 ? static_cast<const T*>(a.up_weight) + f * a.up_stride : static_cast<const T*>(a.gate_weight) + f * a.gate_stride;
+    }
     for (int r0 = 0; r0 < a.R; r0 += 8) {
         const T* x[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) x[r] = static_cast<const T*>(a.x) + min((long long)r0 + r, a.R - 1) * a.x_stride;
-        float g[8] = {}, u[8] = {};
-#pragma unroll 4
-        for (int k = lane; k < a.K; k += 32) {
-            const float vg = to_f32(wg[k]), vu = to_f32(wu[k]);
+        float acc[4][8] = {};
+#pragma unroll 2
+        for (int k = lane * VEC; k < a.K; k += 32 * VEC) {
+            P wv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const P*>(w[i] + k);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const float xv = to_f32(x[r][k]);
-                g[r] = fmaf(vg, xv, g[r]);
-                u[r] = fmaf(vu, xv, u[r]);
+                const P xv = *reinterpret_cast<const P*>(x[r] + k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[i][r] = fmaf(to_f32(wv[i].e[e]), to_f32(xv.e[e]), acc[i][r]);
             }
         }
+        // the 32 sums over the lanes: lane 8 i + r receives that of acc[i][r]
+        float v[32];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                g[r] += __shfl_xor_sync(0xffffffffu, g[r], o);
-                u[r] += __shfl_xor_sync(0xffffffffu, u[r], o);
-            }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (lane == r && r0 + r < a.R)
-                static_cast<T*>(p.h)[(r0 + r) * (long long)a.F + f] = from_f32<T>(activate_by(a.activation, sizeof(T) == 4, g[r] + bg) * (u[r] + bu));
+        for (int j = 0; j < 32; ++j) v[j] = acc[j / 8][j % 8];
+        float s = gtc::column_sums(v, lane);
+        const int f = f0 + lane / 16, r = lane % 8;
+        const void* bias = lane / 8 % 2 ? a.up_bias : a.gate_bias;
+        if (bias && f < a.F) s += to_f32(static_cast<const T*>(bias)[f]);
+        const float u = __shfl_down_sync(0xffffffffu, s, 8);
+        if (lane / 8 % 2 == 0 && f < a.F && r0 + r < a.R)
+            static_cast<T*>(p.h)[(r0 + r) * (long long)a.F + f] = from_f32<T>(activate_by(a.activation, sizeof(T) == 4, s) * u);
     }
 }
 
@@ -373,7 +385,11 @@ cudaError_t launch_gated_forward(const GatedParams& p, void* ws, int sms, cudaSt
                     else gated_few_kernel<T, 4><<<grid, 256, 0, s>>>(p);
                     return cudaGetLastError();
                 }
-            gated_dot_kernel<T><<<tiles_of(a.F, 8), 256, 0, s>>>(p);
+            auto quad = [&](const void* q, long long stride) { return reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) == 0 && stride % 4 == 0; };
+            if (a.K % 4 == 0 && quad(a.x, a.x_stride) && quad(a.gate_weight, a.gate_stride) && quad(a.up_weight, a.up_stride))
+                gated_dot_kernel<T, 4><<<tiles_of(a.F, 16), 256, 0, s>>>(p);
+            else
+                gated_dot_kernel<T, 1><<<tiles_of(a.F, 16), 256, 0, s>>>(p);
             return cudaGetLastError();
         });
     const Plan plan = make_plan(p, ws, false, sms);
