@@ -54,7 +54,8 @@ sdtw_status check_gated(const sdtw_gated* a)
     if (a->R < 1 || a->K < 1 || a->F < 1) return SDTW_ERR_EMPTY;
     if (!a->x || !a->gate_weight || !a->up_weight || !good_dtype(a->dtype)) return SDTW_ERR_ARG;
     if (a->activation < SDTW_ACT_SILU || a->activation > SDTW_ACT_SIGMOID) return SDTW_ERR_ARG;
-    if (a->R > (1ll << 30) || a->K > (1 << 20) || a->F > (1 << 20)) return SDTW_ERR_TOO_LARGE;
+    // 32-bit coordinates, tiles and grids
+    if (a->R > (1ll << 30) || a->K > (1 << 20) || a->F > (1 << 20) || a->R * a->K > (1ll << 40) || a->R * a->F > (1ll << 38)) return SDTW_ERR_TOO_LARGE;
     return SDTW_OK;
 }
 

@@ -640,7 +640,7 @@ template <typename T, int VEC, int K, bool BWD> __global__ void __launch_bounds_
     }
 }
 
-// ---- groups too wide for the above: a CTA a group of a batch element
+// ---- groups too wide for the above: a CTA a group of a batch element, a thread a channel
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -651,32 +651,41 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     for (int w = 0; w < kThreads / 32; ++w) v += red[w];
     return v;
 }
+// A thread's sums are long here, and carry what their additions leave (Kahan).
+struct Sum {
+    float s = 0.f, left = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float y = v - left, t = s + y;
+        left = (t - s) - y;
+        s = t;
+    }
+};
 template <typename T> __global__ void __launch_bounds__(kThreads) group_fwd_any_kernel(const GroupNormParams p)
 {
     __shared__ float red[kThreads / 32];
     const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S;
-    const long long base = (long long)b * p.S * p.C + g * p.cg;
+    const long long base = (long long)b * p.S * p.C + (long long)g * p.cg;
     const T* x = static_cast<const T*>(p.x) + base;
     T* y = static_cast<T*>(p.y) + base;
-    const long long n = (long long)len * p.cg, all = (long long)p.S * p.cg;
-    auto at = [&](long long i) { return i / p.cg * p.C + i % p.cg; };
-    float s = 0.f;
-    for (long long i = threadIdx.x; i < n; i += kThreads) s += to_f32(x[at(i)]);
-    const float mu = n ? block_sum(s, red) / (float)n : 0.f;
-    float q = 0.f;
-    for (long long i = threadIdx.x; i < n; i += kThreads) {
-        const float d = to_f32(x[at(i)]) - mu;
-        q = fmaf(d, d, q);
-    }
-    const float r = n ? 1.f / sqrtf(block_sum(q, red) / (float)n + p.eps) : 0.f;
-    for (long long i = threadIdx.x; i < all; i += kThreads) {
-        float none, v = 0.f;
-        const int c = g * p.cg + (int)(i % p.cg);
-        if (i < n)
-            v = activate_as<sizeof(T) == 4, false>(p.activation, fmaf((to_f32(x[at(i)]) - mu) * r, wval(p.weight, c, p.wdtype, 1.f),
-                                                                      wval(p.bias, c, p.wdtype, 0.f)), none);
-        y[at(i)] = from_f32<T>(v);
+    const float n = (float)len * (float)p.cg;
+    Sum s, q;
+    for (int i = 0; i < len; ++i)
+        for (int c = threadIdx.x; c < p.cg; c += kThreads) s.add(to_f32(x[(long long)i * p.C + c]));
+    const float mu = len ? block_sum(s.s, red) / n : 0.f;
+    for (int i = 0; i < len; ++i)
+        for (int c = threadIdx.x; c < p.cg; c += kThreads) {
+            const float d = to_f32(x[(long long)i * p.C + c]) - mu;
+            q.add(d * d);
+        }
+    const float r = len ? 1.f / sqrtf(block_sum(q.s, red) / n + p.eps) : 0.f;
+    for (int c = threadIdx.x; c < p.cg; c += kThreads) {
+        const float w = r * wval(p.weight, g * p.cg + c, p.wdtype, 1.f), bias = wval(p.bias, g * p.cg + c, p.wdtype, 0.f);
+        for (int i = 0; i < p.S; ++i) {
+            float none;
+            const long long at = (long long)i * p.C + c;
+            y[at] = from_f32<T>(i < len ? activate_as<sizeof(T) == 4, false>(p.activation, fmaf(to_f32(x[at]) - mu, w, bias), none) : 0.f);
+        }
     }
     if (threadIdx.x == 0 && p.mean) p.mean[blockIdx.x] = mu, p.rstd[blockIdx.x] = r;
 }
@@ -686,48 +695,43 @@ template <typename T> __global__ void __launch_bounds__(kThreads) group_bwd_any_
     __shared__ float red[kThreads / 32];
     const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S;
-    const long long base = (long long)b * p.S * p.C + g * p.cg;
+    const long long base = (long long)b * p.S * p.C + (long long)g * p.cg;
     const T* x = static_cast<const T*>(p.x) + base;
     const T* dy = static_cast<const T*>(p.dy) + base;
-    const float mu = p.mean[blockIdx.x], r = p.rstd[blockIdx.x];
-    const float n = (float)len * p.cg;
-    float s1 = 0.f, s2 = 0.f;
-    auto value = [&](int i, int c, float& xh, float w) {
+    const float mu = p.mean[blockIdx.x], r = p.rstd[blockIdx.x], n = (float)len * (float)p.cg;
+    auto value = [&](long long at, float w, float bias, float& xh) {
         float slope;
-        xh = (to_f32(x[(long long)i * p.C + c]) - mu) * r;
-        activate_as<sizeof(T) == 4, true>(p.activation, fmaf(xh, w, wval(p.bias, g * p.cg + c, p.wdtype, 0.f)), slope);
-        return to_f32(dy[(long long)i * p.C + c]) * slope;
+        xh = (to_f32(x[at]) - mu) * r;
+        activate_as<sizeof(T) == 4, true>(p.activation, fmaf(xh, w, bias), slope);
+        return to_f32(dy[at]) * slope;
     };
-    for (int c = 0; c < p.cg; ++c) {
-        const float w = wval(p.weight, g * p.cg + c, p.wdtype, 1.f);
-        float dw = 0.f, db = 0.f, xh;
-        for (int i = threadIdx.x; i < len; i += kThreads) {
-            const float dz = value(i, c, xh, w);
-            db += dz;
-            dw = fmaf(dz, xh, dw);
+    Sum t1, t2;
+    float xh;
+    for (int c = threadIdx.x; c < p.cg; c += kThreads) {
+        const int channel = g * p.cg + c;
+        const float w = wval(p.weight, channel, p.wdtype, 1.f), bias = wval(p.bias, channel, p.wdtype, 0.f);
+        Sum dw, db;
+        for (int i = 0; i < len; ++i) {
+            const float dz = value((long long)i * p.C + c, w, bias, xh);
+            db.add(dz);
+            dw.add(dz * xh);
         }
-        dw = block_sum(dw, red);
-        db = block_sum(db, red);
-        s1 = fmaf(db, w, s1);
-        s2 = fmaf(dw, w, s2);
-        if (threadIdx.x == 0 && p.partial) {
-            p.partial[2ll * b * p.C + g * p.cg + c] = dw;
-            p.partial[(2ll * b + 1) * p.C + g * p.cg + c] = db;
-        }
+        t1.add(db.s * w);
+        t2.add(dw.s * w);
+        if (p.partial) p.partial[2ll * b * p.C + channel] = dw.s, p.partial[(2ll * b + 1) * p.C + channel] = db.s;
     }
     if (!p.dx) return;
+    const float s1 = block_sum(t1.s, red) / n, s2 = block_sum(t2.s, red) / n;
     T* dx = static_cast<T*>(p.dx) + base;
-    s1 /= n;
-    s2 /= n;
-    for (int c = 0; c < p.cg; ++c) {
-        const float w = wval(p.weight, g * p.cg + c, p.wdtype, 1.f);
-        for (int i = threadIdx.x; i < p.S; i += kThreads) {
-            float xh, v = 0.f;
+    for (int c = threadIdx.x; c < p.cg; c += kThreads) {
+        const float w = wval(p.weight, g * p.cg + c, p.wdtype, 1.f), bias = wval(p.bias, g * p.cg + c, p.wdtype, 0.f);
+        for (int i = 0; i < p.S; ++i) {
+            const long long at = (long long)i * p.C + c;
+            dx[at] = from_f32<T>(0.f);
             if (i < len) {
-                const float dz = value(i, c, xh, w);
-                v = r * (dz * w - s1 - xh * s2);
+                const float dz = value(at, w, bias, xh);
+                dx[at] = from_f32<T>(r * (dz * w - s1 - xh * s2));
             }
-            dx[(long long)i * p.C + c] = from_f32<T>(v);
         }
     }
 }

@@ -33,7 +33,8 @@ def norm_calls(lib, x=0x1000, y=0x2000, mean=0x3000, rstd=0x4000, B=2, S=3, G=2,
 @pytest.mark.parametrize("change,code", [
     (dict(B=0), EMPTY), (dict(S=0), EMPTY), (dict(G=0), EMPTY), (dict(C=0), EMPTY), (dict(C=7), SHAPE), (dict(dtype=3), ARG),
     (dict(wdtype=-1), ARG), (dict(activation=4), ARG), (dict(activation=-1), ARG), (dict(x=None), ARG), (dict(y=None), ARG),
-    (dict(mean=None), ARG), (dict(rstd=None), ARG), (dict(B=1 << 30, G=8), TOO_LARGE), (dict(C=1 << 25), TOO_LARGE)])
+    (dict(mean=None), ARG), (dict(rstd=None), ARG), (dict(B=1 << 30, G=8), TOO_LARGE),
+    (dict(B=(1 << 30) + 1, G=1), TOO_LARGE), (dict(C=1 << 25), TOO_LARGE)])
 def test_group_norm_refusals(lib, change, code):
     assert list(norm_calls(lib, **change)) == [code, code]
     if code in (EMPTY, SHAPE, TOO_LARGE) or "dtype" in change:
@@ -55,7 +56,8 @@ def test_group_norm_refuses_eps_and_workspaces(lib):
 
 @pytest.mark.parametrize("change,code", [
     (dict(B=0), EMPTY), (dict(N=0), EMPTY), (dict(C=0), EMPTY), (dict(x=None), ARG), (dict(gate=None), ARG), (dict(dtype=5), ARG),
-    (dict(N=1 << 30, C=1), TOO_LARGE), (dict(C=(1 << 30) + 1), TOO_LARGE)])
+    (dict(N=1 << 30, C=1), TOO_LARGE), (dict(C=(1 << 30) + 1), TOO_LARGE),
+    (dict(x_stride=(64, (1 << 23) + 1)), TOO_LARGE), (dict(gate_stride=(64, -(1 << 24))), TOO_LARGE)])
 def test_recurrence_refusals(lib, change, code):
     base = dict(x=0x1000, gate=0x2000, x_stride=(64, 8), gate_stride=(64, 8), state=None, lengths=None, B=2, N=3, C=8, dtype=0, reverse=0, tied=1)
     base.update(change)
@@ -83,7 +85,7 @@ def gated(lib, **change):
 
 @pytest.mark.parametrize("change,code", [
     (dict(R=0), EMPTY), (dict(K=0), EMPTY), (dict(F=0), EMPTY), (dict(x=None), ARG), (dict(up_weight=None), ARG), (dict(gate_weight=None), ARG),
-    (dict(dtype=9), ARG), (dict(activation=0), ARG), (dict(activation=5), ARG), (dict(R=1 << 40), TOO_LARGE), (dict(K=1 << 24), TOO_LARGE),
+    (dict(R=1 << 30, F=1 << 10), TOO_LARGE), (dict(dtype=9), ARG), (dict(activation=0), ARG), (dict(activation=5), ARG), (dict(R=1 << 40), TOO_LARGE), (dict(K=1 << 24), TOO_LARGE),
     (dict(F=1 << 24), TOO_LARGE)])
 def test_gated_refusals(lib, change, code):
     p = gated(lib, **change)

@@ -126,7 +126,7 @@ def norm_reference(x, G, w, b, dy, name, lengths, eps, wdtype):
 # batch, positions, groups, channels of a group
 NORM_SHAPES = [(1, 1, 1, 1), (2, 3, 1, 5), (3, 1, 4, 8), (16, 1, 8, 64), (700, 1, 2, 12), (5, 7, 3, 7), (2, 64, 8, 8), (4, 100, 5, 16),
                (3, 33, 33, 1), (1, 257, 64, 1), (2, 129, 12, 2), (1, 1021, 4, 24), (2, 2000, 2, 40), (1, 17, 1, 1000), (9, 5, 300, 1),
-               (1, 3, 2, 2050)]
+               (1, 3, 2, 2050), (2, 30, 2, 2064), (70, 1, 3, 512), (40, 2, 5, 64), (3, 4, 8, 128)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -195,6 +195,31 @@ def test_group_norm_off_16_bytes_and_constant_groups(package):
     assert torch.isfinite(dx).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(2, 4096, 4, 16), (1, 9000, 1, 256), (3, 2500, 6, 24), (2, 3000, 64, 1), (9000, 1, 4, 64), (3, 700, 3, 1003)], ids=str)
+def test_large_group_norms_against_64_bits(package, shape, dtype):
+    """Clusters, slabs that they cannot hold, many batch elements a CTA: in quadratic mean against 64 bits. 16-bit results
+    are as near as their own rounding; fp32's sums of a group add a few roundings of its values, 16 at the most here."""
+    B, S, G, cg = shape
+    gen = generator(1200 + S)
+    x, dy = randn(gen, B, S, G * cg, dtype=dtype, std=1.5, mean=0.5), randn(gen, B, S, G * cg, dtype=dtype)
+    w, b = randn(gen, G * cg, std=0.3, mean=1.0), randn(gen, G * cg, std=0.3)
+    leaves = [t.requires_grad_() for t in (x, w, b)]
+    y = package.group_norm(x, G, w, b, activation="silu")
+    got = (y, *torch.autograd.grad(y, leaves, dy))
+    wide = [t.detach().double().requires_grad_() for t in leaves]
+    t = wide[0].view(B, S, G, cg)
+    var, mean = torch.var_mean(t, dim=(1, 3), unbiased=False, keepdim=True)
+    z = ((t - mean) / torch.sqrt(var + 1e-5)).reshape(B, S, G * cg) * wide[1] + wide[2]
+    exact = z / (1 + torch.exp(-z))
+    for a, want, what in zip(got, (exact, *torch.autograd.grad(exact, wide, dy.double())), ("y", "dx", "dw", "db")):
+        error = ((a.detach().double() - want) ** 2).mean().sqrt()
+        own = ((want.to(a.dtype).double() - want) ** 2).mean().sqrt()
+        assert error <= (16 if a.dtype == F32 else 1.05) * own, (what, float(error / own))
+    again = package.group_norm(x, G, w, b, activation="silu")
+    assert torch.equal(again, y) and all(torch.equal(p, q) for p, q in zip(torch.autograd.grad(again, leaves, dy), got[1:]))
+
+
 # --- gated recurrence -----------------------------------------------------------------------------
 
 def recurrence_reference(x, gate, state, dh, dlast, lengths, reverse, tied):
@@ -242,7 +267,8 @@ def recurrence_reference(x, gate, state, dh, dlast, lengths, reverse, tied):
 
 
 RECURRENCE_SHAPES = [(1, 1, 1), (3, 1, 40), (2, 2, 7), (1, 8, 64), (2, 9, 33), (1, 17, 128), (3, 63, 24), (2, 64, 65), (2, 65, 64), (1, 127, 8),
-                     (5, 128, 72), (2, 129, 16), (1, 500, 130), (2, 1021, 40), (1, 2600, 264), (40, 70, 32), (3, 257, 250)]
+                     (5, 128, 72), (2, 129, 16), (1, 500, 130), (2, 1021, 40), (1, 2600, 264), (40, 70, 32), (3, 257, 250),
+                     (2, 4500, 72), (40, 1100, 64), (1, 4200, 8), (10, 1300, 200)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -371,7 +397,7 @@ def gated_reference(x, wg, wu, bg, bu, dh, name):
 # rows, K, F
 GATED_SHAPES = [(1, 1, 1), (1, 64, 64), (2, 5, 3), (3, 128, 200), (8, 256, 96), (9, 72, 130), (16, 1000, 40), (17, 33, 65), (33, 64, 128),
                 (64, 130, 48), (100, 96, 264), (129, 64, 72), (128, 200, 128), (250, 17, 129), (257, 264, 136), (300, 8, 8), (513, 72, 300),
-                (1000, 64, 256)]
+                (1000, 64, 256), (8, 8, 8), (24, 264, 72), (32, 1024, 48), (31, 36, 50)]
 GATED_ACTS = ("silu", "gelu", "relu", "sigmoid")
 
 
