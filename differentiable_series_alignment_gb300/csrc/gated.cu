@@ -248,6 +248,20 @@ struct Image {
     }
 };
 
+// Groups of 64 columns as a dimension, `groups` of them to a box of 64 rows; for columns that are whole groups.
+bool map_groups(const Image& m, CUtensorMap* to, int dtype, int groups)
+{
+    const cuuint64_t dims[4] = {64, (cuuint64_t)m.rows, (cuuint64_t)(m.cols / 64), (cuuint64_t)m.parts};
+    const cuuint64_t strides[3] = {(cuuint64_t)(m.rows > 1 ? m.pitch * 2 : 16), 128, (cuuint64_t)(m.parts > 1 ? m.pitch * 2 * m.rows : 16)};
+    const cuuint32_t box[4] = {64, 64, (cuuint32_t)groups, 1};
+    return atc::encode(to, dtype == SDTW_F32 ? SDTW_BF16 : dtype, 4, m.p, dims, strides, box);
+}
+// An MN-major operand of which a CTA takes `columns` columns
+bool map_mn(const Image& m, CUtensorMap* to, int dtype, int columns)
+{
+    return m.cols % 64 == 0 ? map_groups(m, to, dtype, columns / 64) : m.map(to, dtype, 64, 64);
+}
+
 struct Plan {
     Image x, w[2], grads;
     PackJob pack;
@@ -414,15 +428,18 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
     g.top = a.dtype == SDTW_F16 ? plan.top : nullptr;
     g.wait_ns = p.wait_ns;
     if (p.dx) {
-        if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, 64) || !plan.w[1].map(&g.b[1], a.dtype, 64, 64))
+        const int columns = plan.dx_nb == 256 ? 128 : plan.dx_nb;   // of a CTA
+        if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !map_mn(plan.w[0], &g.b[0], a.dtype, columns) || !map_mn(plan.w[1], &g.b[1], a.dtype, columns))
             return cudaErrorInvalidValue;
+        g.grouped_b = a.K % 64 == 0;
         g.segs = 2, g.seg[1] = gtc::Seg{(unsigned char)parts, 1}, g.blocks = tiles_of(a.F, 64);
         g.sets = 1, g.set0 = 0;
         g.M = a.R, g.N = a.K, g.out[0] = p.dx, g.shares = plan.shares;
         if ((e = gtc::run_dx(g, a.dtype, plan.dx_nb, sms, s)) != cudaSuccess) return e;
     }
     if (p.dgate_weight || p.dup_weight) {
-        if (!plan.grads.map(&g.a, a.dtype, 64, 64) || !plan.x.map(&g.b[0], a.dtype, 64, 64)) return cudaErrorInvalidValue;
+        if (!map_mn(plan.grads, &g.a, a.dtype, 128) || !map_mn(plan.x, &g.b[0], a.dtype, plan.dw_nb == 256 ? 128 : plan.dw_nb)) return cudaErrorInvalidValue;
+        g.grouped_a = a.F % 64 == 0, g.grouped_b = a.K % 64 == 0;
         g.b[1] = g.b[0];
         g.segs = 1, g.blocks = tiles_of(a.R, 64);
         g.set0 = p.dgate_weight ? 0 : 1, g.sets = p.dgate_weight && p.dup_weight ? 2 : 1;

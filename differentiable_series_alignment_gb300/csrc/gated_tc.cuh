@@ -45,6 +45,7 @@ struct Params {
     CUtensorMap a, b[2];
     Seg seg[2];
     int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks
+    bool grouped_a, grouped_b;                         // maps of MN-major operands have groups of 64 columns as a dimension
     int tiles_m, tiles_n, group, set0, sets, tiles;    // sets: DW's weights, from set0 on
     int whole, workers;                                // tiles summed whole; workers that share the others' sums (below)
     long long M;                                       // rows and columns of the result
@@ -95,6 +96,26 @@ __device__ __forceinline__ void tma3_pair(uint32_t dst, const CUtensorMap* m, in
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
+}
+__device__ __forceinline__ void tma4_pair(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// Rows [row, row + 64) of `groups` groups of 64 columns from col on, a group after the other: one copy where the columns are whole
+// groups, which the map then has as a dimension of their own.
+template <int CTAS, int GROUPS> __device__ __forceinline__ void load_groups(uint32_t dst, const CUtensorMap* m, bool grouped, int col, int row, int part, uint32_t bar) {
+    if (grouped) {
+        if constexpr (CTAS == 2) tma4_pair(dst, m, 0, row, col / 64, part, bar);
+        else tma4(dst, m, 0, row, col / 64, part, bar);
+    } else {
+#pragma unroll
+        for (int c = 0; c < GROUPS; ++c) {
+            if constexpr (CTAS == 2) tma3_pair(dst + c * kBlock * 128, m, col + c * 64, row, part, bar);
+            else tma3(dst + c * kBlock * 128, m, col + c * 64, row, part, bar);
+        }
+    }
 }
 template <int CTAS> __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
     if constexpr (CTAS == 2) tma3_pair(dst, m, c0, c1, c2, bar);
@@ -402,12 +423,14 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             Work work(p, worker, workers);
             for (Tile tile; ok && work.next(tile);) {
                 const int row = tile.m * Sh::rows + rank * kRows;
+                int seg = tile.first / p.blocks, block = tile.first - seg * p.blocks;
                 for (int k = tile.first; k < tile.last; ++k, ++i) {
                     const int e = i % Sh::stages;
                     if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, late);
                     if (!ok) break;
-                    const Seg sg = p.seg[k / p.blocks];
-                    const int at = k % p.blocks * kBlock;
+                    const Seg sg = p.seg[seg];
+                    const int at = block * kBlock;
+                    if (++block == p.blocks) block = 0, ++seg;
                     const uint32_t mine = smem_u32(&s_full[e]), bar = CTAS == 2 ? in_cta(mine, 0) : mine;
                     if (rank == 0) mbar_expect_tx(mine, CTAS * Sh::stage);
 #pragma unroll
@@ -415,9 +438,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                         const uint32_t a = ring + e * Sh::stage + part * kABytes;
                         const uint32_t b = ring + e * Sh::stage + PARTS * kABytes + part * Sh::b_bytes;
                         if constexpr (A_MN) {
-#pragma unroll
-                            for (int c = 0; c < kRows / 64; ++c)
-                                load3<CTAS>(a + c * kBlock * 128, &p.a, row + c * 64, at, sg.a + tile.set * PARTS + part, bar);
+                            load_groups<CTAS, kRows / 64>(a, &p.a, p.grouped_a, row, at, sg.a + tile.set * PARTS + part, bar);
                         } else {
                             load3<CTAS>(a, &p.a, at, row, sg.a + part, bar);
                         }
@@ -427,9 +448,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                             load3<CTAS>(b, &p.b[0], at, tile.n * WIDTH, part, bar);
                             load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, part, bar);
                         } else {
-#pragma unroll
-                            for (int c = 0; c < NB / CTAS / 64; ++c)
-                                load3<CTAS>(b + c * kBlock * 128, &p.b[sg.map], tile.n * NB + rank * (NB / CTAS) + c * 64, at, part, bar);
+                            load_groups<CTAS, NB / CTAS / 64>(b, &p.b[sg.map], p.grouped_b, tile.n * NB + rank * (NB / CTAS), at, part, bar);
                         }
                     }
                 }
