@@ -432,7 +432,7 @@ cudaError_t launch_gated_backward(const GatedParams& p, void* ws, int sms, cudaS
         if (!plan.grads.map(&g.a, a.dtype, 64, 128) || !map_mn(plan.w[0], &g.b[0], a.dtype, columns) || !map_mn(plan.w[1], &g.b[1], a.dtype, columns))
             return cudaErrorInvalidValue;
         g.grouped_b = a.K % 64 == 0;
-        g.segs = 2, g.seg[1] = gtc::Seg{(unsigned char)parts, 1}, g.blocks = tiles_of(a.F, 64);
+        g.segs = 2, g.seg[1].a = (unsigned char)parts, g.blocks = tiles_of(a.F, 64);
         g.sets = 1, g.set0 = 0;
         g.M = a.R, g.N = a.K, g.out[0] = p.dx, g.shares = plan.shares;
         if ((e = gtc::run_dx(g, a.dtype, plan.dx_nb, sms, s)) != cudaSuccess) return e;

@@ -36,9 +36,9 @@ enum Kind { FWD, GRAD, DX, DW };
 constexpr int kRows = 128, kBlock = 64;               // rows of a tile; length of a block of the sum
 constexpr uint32_t kABytes = kRows * kBlock * 2;
 
-// One piece of the sum: the first part of A, and the map of B.
+// One piece of the sum: the first part of A. The first piece takes the first map of B, the second the other.
 struct Seg {
-    unsigned char a, map;
+    unsigned char a;
 };
 
 struct Params {
@@ -418,62 +418,64 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     bool ok = true;
 
     if (warp == kLoad) {
-        if (lane == 0 && !p.skip) {
-            int i = 0;   // blocks sent for
-            Work work(p, worker, workers);
-            for (Tile tile; ok && work.next(tile);) {
-                const int row = tile.m * Sh::rows + rank * kRows;
-                int seg = tile.first / p.blocks, block = tile.first - seg * p.blocks;
-                for (int k = tile.first; k < tile.last; ++k, ++i) {
-                    const int e = i % Sh::stages;
-                    if (i >= Sh::stages) wait_for(ok, smem_u32(&s_empty[e]), (uint32_t)((i / Sh::stages - 1) & 1), p.wait_ns, late);
-                    if (!ok) break;
-                    const Seg sg = p.seg[seg];
-                    const int at = block * kBlock;
-                    if (++block == p.blocks) block = 0, ++seg;
+        // The whole warp goes through the blocks and one elected thread sends: behind a comparison of lane numbers a block's
+        // copies took longer to issue than its products to run.
+        int sent = 0, e = 0;   // blocks, and the place of the next
+        uint32_t parity = 1;   // of the place's last release; of the first round there is none
+        Work work(p, worker, workers);
+        for (Tile tile; ok && !p.skip && work.next(tile);) {
+            const int row = uniform(tile.m * Sh::rows + rank * kRows), col = uniform(tile.n * (PAIR ? WIDTH : NB)), set = uniform(tile.set);
+            const int last = uniform(tile.last), first = uniform(tile.first);
+            int seg = first / p.blocks, block = first - seg * p.blocks;
+            for (int k = first; k < last; ++k) {
+                if (sent >= Sh::stages) wait_warp(ok, smem_u32(&s_empty[e]), parity, p.wait_ns, late);
+                if (!ok) break;
+                if (elect_one()) {
+                    const int at = block * kBlock, first_a = seg ? p.seg[1].a : p.seg[0].a;
+                    const CUtensorMap* map_b = seg ? &p.b[1] : &p.b[0];   // a sum of two pieces has a map for either
                     const uint32_t mine = smem_u32(&s_full[e]), bar = CTAS == 2 ? in_cta(mine, 0) : mine;
                     if (rank == 0) mbar_expect_tx(mine, CTAS * Sh::stage);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         const uint32_t a = ring + e * Sh::stage + part * kABytes;
                         const uint32_t b = ring + e * Sh::stage + PARTS * kABytes + part * Sh::b_bytes;
-                        if constexpr (A_MN) {
-                            load_groups<CTAS, kRows / 64>(a, &p.a, p.grouped_a, row, at, sg.a + tile.set * PARTS + part, bar);
-                        } else {
-                            load3<CTAS>(a, &p.a, at, row, sg.a + part, bar);
-                        }
+                        if constexpr (A_MN) load_groups<CTAS, kRows / 64>(a, &p.a, p.grouped_a, row, at, first_a + set * PARTS + part, bar);
+                        else load3<CTAS>(a, &p.a, at, row, first_a + part, bar);
                         if constexpr (PAIR && CTAS == 2) {   // the first CTA has the gate's weights, the second the others
-                            load3<CTAS>(b, &p.b[rank], at, tile.n * WIDTH, part, bar);
+                            load3<CTAS>(b, rank ? &p.b[1] : &p.b[0], at, col, part, bar);
                         } else if constexpr (PAIR) {
-                            load3<CTAS>(b, &p.b[0], at, tile.n * WIDTH, part, bar);
-                            load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, tile.n * WIDTH, part, bar);
+                            load3<CTAS>(b, &p.b[0], at, col, part, bar);
+                            load3<CTAS>(b + Sh::b_bytes / 2, &p.b[1], at, col, part, bar);
                         } else {
-                            load_groups<CTAS, NB / CTAS / 64>(b, &p.b[sg.map], p.grouped_b, tile.n * NB + rank * (NB / CTAS), at, part, bar);
+                            load_groups<CTAS, NB / CTAS / 64>(b, map_b, p.grouped_b, col + rank * (NB / CTAS), at, part, bar);
                         }
                     }
                 }
+                __syncwarp();
+                if (++block == p.blocks) block = 0, ++seg;
+                if (++e == Sh::stages) e = 0, parity ^= 1;
+                ++sent;
             }
-            // no copy may be writing shared memory when the CTA ends
-            bool drained = true;   // a pair's are all reported to the first CTA, for which the second waits at the end
-            for (int k = max(0, i - Sh::stages); k < i && rank == 0; ++k)
-                wait_for(drained, smem_u32(&s_full[k % Sh::stages]), (uint32_t)((k / Sh::stages) & 1), p.wait_ns, late);
         }
-        __syncwarp();
+        // no copy may be writing shared memory when the CTA ends
+        bool drained = true;   // a pair's are all reported to the first CTA, for which the second waits at the end
+        for (int k = max(0, sent - Sh::stages); k < sent && rank == 0; ++k)
+            wait_warp(drained, smem_u32(&s_full[k % Sh::stages]), (uint32_t)((k / Sh::stages) & 1), p.wait_ns, late);
     } else if (warp == kIssue) {
         const uint32_t id = idesc2<O>(Sh::rows, NB, A_MN, B_MN);
-        int i = 0, n = 0;
+        int n = 0, e = 0;      // accumulators filled; the place of the next block
+        uint32_t parity = 0;   // of its arrival
         Work work(p, worker, workers);
         for (Tile tile; ok && rank == 0 && work.next(tile);) {
             const int first = uniform(tile.first), last = uniform(tile.last);
-            for (int k = first, in = 0; k < last; ++k, ++i) {   // in: of the run
+            for (int k = first, in = 0; k < last; ++k) {   // in: of the run
                 if (in == 0) {
                     if (n >= 2) wait_warp(ok, smem_u32(&s_free[n & 1]), (uint32_t)((n / 2 - 1) & 1), p.wait_ns, late);
                     fence_after_sync();
                 }
                 const uint32_t d = tmem + (n & 1) * NB;
                 const bool ends = k == last - 1 || in == kRun<T> - 1;
-                const int e = i % Sh::stages;
-                wait_warp(ok, smem_u32(&s_full[e]), (uint32_t)((i / Sh::stages) & 1), p.wait_ns, late);
+                wait_warp(ok, smem_u32(&s_full[e]), parity, p.wait_ns, late);
                 fence_after_sync();
                 if (ok && elect_one()) {
                     // pairs of parts, the smallest products first
@@ -493,6 +495,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                 __syncwarp();
                 in = ends ? 0 : in + 1;
                 n += ends;
+                if (++e == Sh::stages) e = 0, parity ^= 1;
             }
         }
         // every MMA has read its operands and written its result before the CTA ends
