@@ -556,11 +556,13 @@ def sdtw_groupnorm_backward(dy, x, weight, bias, lengths, mean, rstd, groups, ac
 
 
 def recurrence_problem(x, gate, state=None, lengths=None, reverse=False, tied=True) -> Recurrence:
-    """The sdtw_recurrence of these tensors, which the caller keeps alive while it is in use."""
+    """The sdtw_recurrence of these tensors, which it keeps alive."""
     B, N, C = x.shape
     stride = ctypes.c_longlong * 2
-    return Recurrence(x.data_ptr(), gate.data_ptr(), stride(x.stride(0), x.stride(1)), stride(gate.stride(0), gate.stride(1)),
-                      _ptr(state), _i32(lengths, "lengths"), B, N, C, _dtype(x, "x"), int(reverse), int(tied))
+    problem = Recurrence(x.data_ptr(), gate.data_ptr(), stride(x.stride(0), x.stride(1)), stride(gate.stride(0), gate.stride(1)),
+                         _ptr(state), _i32(lengths, "lengths"), B, N, C, _dtype(x, "x"), int(reverse), int(tied))
+    problem.tensors = (x, gate, state, lengths)
+    return problem
 
 
 def sdtw_recurrence_forward(problem: Recurrence, h, last, kept, stream=None):
@@ -574,10 +576,12 @@ def sdtw_recurrence_backward(problem: Recurrence, kept, dh, dlast, dx, dgate, ds
 
 
 def gated_problem(x, gate_weight, up_weight, gate_bias=None, up_bias=None, activation="silu") -> Gated:
-    """The sdtw_gated of these tensors (x (R, K)), which the caller keeps alive while it is in use."""
-    return Gated(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), _ptr(gate_bias), _ptr(up_bias), x.stride(0),
-                 gate_weight.stride(0), up_weight.stride(0), x.shape[0], x.shape[1], gate_weight.shape[0], _dtype(x, "x"),
-                 ACTIVATIONS[activation])
+    """The sdtw_gated of these tensors (x (R, K)), which it keeps alive."""
+    problem = Gated(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), _ptr(gate_bias), _ptr(up_bias), x.stride(0),
+                    gate_weight.stride(0), up_weight.stride(0), x.shape[0], x.shape[1], gate_weight.shape[0], _dtype(x, "x"),
+                    ACTIVATIONS[activation])
+    problem.tensors = (x, gate_weight, up_weight, gate_bias, up_bias)
+    return problem
 
 
 def sdtw_gated_workspace_bytes(problem: Gated, backward: bool = False) -> int:

@@ -499,12 +499,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
             }
         }
         // every MMA has read its operands and written its result before the CTA ends
-        if (lane == 0 && rank == 0) {
-            commit<CTAS>(smem_u32(&s_end));
+        if (rank == 0) {
+            if (elect_one()) commit<CTAS>(smem_u32(&s_end));   // by the thread that issued them
+            __syncwarp();
             bool fin = true;
-            wait_for(fin, smem_u32(&s_end), 0, p.wait_ns, late);
+            wait_warp(fin, smem_u32(&s_end), 0, p.wait_ns, late);
         }
-        __syncwarp();
     } else {
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
