@@ -104,21 +104,3 @@ def test_gated_refuses_missing_results_and_workspaces(lib):
     assert back(dh=None) == ARG and back(dx=None) == 0
     assert lib.sdtw_gated_workspace_bytes(p, True) > 0
     assert back(ws=None) == WORKSPACE and back(ws=0x100010) == WORKSPACE and back(n=64) == WORKSPACE
-
-
-def test_problems_keep_their_tensors(lib):
-    """A problem holds pointers alone as far as the library is concerned; the tensors have to live as long as it does."""
-    import gc
-    import weakref
-
-    def made():
-        x, gate, state = torch.zeros(2, 3, 4), torch.zeros(2, 3, 4), torch.zeros(2, 4)
-        rows, wg, wu, bias = torch.zeros(5, 4), torch.zeros(6, 4), torch.zeros(6, 4), torch.zeros(6)
-        return ((lib.recurrence_problem(x, gate, state), [weakref.ref(t) for t in (x, gate, state)]),
-                (lib.gated_problem(rows, wg, wu, bias), [weakref.ref(t) for t in (rows, wg, wu, bias)]))
-
-    problems = made()
-    gc.collect()
-    for problem, tensors in problems:
-        assert all(t() is not None for t in tensors)
-        del problem

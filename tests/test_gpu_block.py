@@ -745,3 +745,22 @@ def test_large_products_against_64_bits(package, dtype):
         own = ((right.to(dtype).double() - right) ** 2).mean().sqrt()
         assert error <= (64 if dtype == F32 else 1.02 if what in ("h", "dbg") else 1.6) * own, (what, float(error / own))
     assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(package.gated_linear(x, wg, wu, bg, activation="gelu"), leaves, dh), grads))
+
+
+def test_problems_keep_their_tensors():
+    """A problem holds pointers alone as far as the library is concerned; the tensors have to live as long as it does."""
+    import gc
+    import weakref
+
+    from differentiable_series_alignment_gb300 import _lib as lib
+
+    def made():
+        x, gate, state = (torch.zeros(s, device="cuda") for s in ((2, 3, 4), (2, 3, 4), (2, 4)))
+        rows, wg, wu, bias = (torch.zeros(s, device="cuda") for s in ((5, 4), (6, 4), (6, 4), (6,)))
+        return ((lib.recurrence_problem(x, gate, state), [weakref.ref(t) for t in (x, gate, state)]),
+                (lib.gated_problem(rows, wg, wu, bias), [weakref.ref(t) for t in (rows, wg, wu, bias)]))
+
+    problems = made()
+    gc.collect()
+    for problem, tensors in problems:
+        assert all(t() is not None for t in tensors)
