@@ -274,15 +274,16 @@ struct Plan {
 
 int tiles_of(long long n, int tile) { return (int)((n + tile - 1) / tile); }
 
-// Columns of an accumulator: as many as there are results for, fewer where wide tiles would leave SMs without one.
-int pick_nb(long long rows, long long cols, long long others, int sms, bool pair, int dtype)
+// Columns of an accumulator, by the least time that `time(columns)` expects: wide tiles need the fewest loads, narrow ones
+// reach more SMs (bf16 forward with 256, 128 and 64 columns: 16384 x 1024 to 4096 143, 236 and 434 us, 1024 x 512 to 1024 8.8, 6.3
+// and 7.8, 256 x 1024 to 4096 11.1, 8.3 and 11.5).
+template <typename F> int pick_nb(int dtype, F time)
 {
-    for (int nb = dtype == SDTW_F32 ? 128 : 256; nb > 64; nb /= 2) {
-        const int width = pair ? nb / 2 : nb;
-        const int ctas = nb == 256 ? 2 : 1;   // 256 columns are a pair's tile, of 256 rows
-        if (cols > width / 2 && rows > 128 * (ctas - 1) && (long long)tiles_of(rows, 128 * ctas) * tiles_of(cols, width) * others * ctas >= sms) return nb;
-    }
-    return 64;
+    int best = 0;
+    double least = 1e30;
+    for (int nb = dtype == SDTW_F32 ? 128 : 256; nb >= 64; nb /= 2)
+        if (const double t = time(nb); t < least) least = t, best = nb;
+    return best;
 }
 
 Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
@@ -322,7 +323,7 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
     // gradients alone may share its sums otherwise than both.
     size_t shares = 0;
     auto time = [&](int sets, int nb, size_t& bytes) {   // sets 0: dx
-        const int ctas = nb == 256 ? 2 : 1;
+        const int ctas = nb == 256 ? 2 : 1;   // 256 columns are a pair's tile, of 256 rows
         gtc::Params g{};
         g.segs = sets ? 1 : 2, g.blocks = sets ? tiles_of(a.R, 64) : tiles_of(a.F, 64);
         g.sets = sets ? sets : 1, g.M = sets ? a.F : a.R, g.N = a.K;
@@ -330,16 +331,10 @@ Plan make_plan(const GatedParams& p, void* ws, bool backward, int sms)
         bytes = gtc::share_bytes(g, 128 * ctas, nb);
         return t;
     };
-    for (int sets : {0, 2}) {
-        double least = 1e30;
-        for (int nb = a.dtype == SDTW_F32 ? 128 : 256; nb >= 64; nb /= 2) {
-            size_t bytes;
-            const double t = time(sets, nb, bytes);
-            if (t < least) least = t, (sets ? plan.dw_nb : plan.dx_nb) = nb;
-        }
-    }
+    size_t bytes;
+    plan.dx_nb = pick_nb(a.dtype, [&](int nb) { return time(0, nb, bytes); });
+    plan.dw_nb = pick_nb(a.dtype, [&](int nb) { return time(2, nb, bytes); });
     for (int sets : {0, 1, 2}) {
-        size_t bytes;
         time(sets, sets ? plan.dw_nb : plan.dx_nb, bytes);
         shares = std::max(shares, bytes);
     }
@@ -361,12 +356,17 @@ cudaError_t products(const GatedParams& p, const Plan& plan, bool grads, bool wa
 {
     const sdtw_gated& a = p.a;
     gtc::Params g{};
-    const int nb = pick_nb(a.R, a.F, 1, sms, true, a.dtype), width = nb / 2;
-    if (!plan.x.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, width) || !plan.w[1].map(&g.b[1], a.dtype, 64, width))
-        return cudaErrorInvalidValue;
     g.segs = 1, g.blocks = tiles_of(a.K, 64);
     g.sets = 1;
     g.M = a.R, g.N = g.F = a.F, g.activation = a.activation;
+    const int nb = pick_nb(a.dtype, [&](int n) {
+        gtc::Params t = g;
+        const int ctas = n == 256 ? 2 : 1;
+        return gtc::share_out(t, 128 * ctas, n / 2, n, plan.x.parts, sms / ctas, false);
+    });
+    const int width = nb / 2;
+    if (!plan.x.map(&g.a, a.dtype, 64, 128) || !plan.w[0].map(&g.b[0], a.dtype, 64, width) || !plan.w[1].map(&g.b[1], a.dtype, 64, width))
+        return cudaErrorInvalidValue;
     g.out[0] = p.h, g.bias[0] = a.gate_bias, g.bias[1] = a.up_bias, g.dh = p.dh;
     g.grads = static_cast<uint16_t*>(const_cast<void*>(plan.grads.p)), g.ld = plan.grads.pitch;
     g.sums = want_sums ? plan.sums : nullptr;

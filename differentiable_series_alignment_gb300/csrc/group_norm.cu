@@ -266,7 +266,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 {
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
-    constexpr int Q = kPairs<VEC>;
+    constexpr int Q = kPairs<VEC>, AHEAD = HELD ? 4 : 8;
     const int slab = blockIdx.y, rank = L.ctas > 1 ? cta_rank() : 0, column = L.ctas > 1 ? cluster_id() : blockIdx.x;
     const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * kThreads * 16 : 0));
@@ -300,7 +300,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         mu[0] = pk2(0.f, 0.f);
         auto add = [&](int from, int to) {
             to = min(to, rounds);
-#pragma unroll 4
+#pragma unroll AHEAD
             for (int k = from; k < to; ++k) add_onto<T, VEC>(s[0], value(k));
         };
         if constexpr (HELD) by_batches(rounds, add);
@@ -311,7 +311,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, mu);
 #pragma unroll
         for (int q = 0; q < Q; ++q) s[0][q] = pk2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll AHEAD
         for (int k = 0; k < rounds; ++k) {
             less<T, VEC, WITHIN>(value(k), mu, d);
 #pragma unroll
@@ -332,18 +332,27 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 #pragma unroll
         for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], r[WITHIN ? 0 : q]);
         T* dst = y + at.at;
-        for (int k = 0; k < last; ++k, dst += step) {
-            if (k < rounds) {
-                less<T, VEC, WITHIN>(value(k), mu, d);
+        auto put = [&](const P& v) {
+            less<T, VEC, WITHIN>(v, mu, d);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) d[q] = fma2(d[q], rw[q], bias[q]);
-                activate_all<sizeof(T) == 4, false, Q>(p.activation, d);
-            } else {
-#pragma unroll
-                for (int q = 0; q < Q; ++q) d[q] = pk2(0.f, 0.f);
-            }
+            for (int q = 0; q < Q; ++q) d[q] = fma2(d[q], rw[q], bias[q]);
+            activate_all<sizeof(T) == 4, false, Q>(p.activation, d);
             *reinterpret_cast<P*>(dst) = rounded<T, VEC>(d);
-        }
+            dst += step;
+        };
+        int k = 0;
+        if constexpr (!HELD)   // rows that are read again come four at a time
+            for (; k + 4 <= rounds; k += 4) {
+                P v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = value(k + i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) put(v[i]);
+            }
+        for (; k < rounds; ++k) put(value(k));
+#pragma unroll
+        for (int q = 0; q < Q; ++q) d[q] = pk2(0.f, 0.f);
+        for (; k < last; ++k, dst += step) *reinterpret_cast<P*>(dst) = rounded<T, VEC>(d);
     }
 }
 
@@ -351,7 +360,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 {
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
-    constexpr int Q = kPairs<VEC>;
+    constexpr int Q = kPairs<VEC>, AHEAD = HELD ? 1 : VEC == 1 ? 4 : 2;     // rows that come from memory at a time
     const int slab = blockIdx.y, rank = L.ctas > 1 ? cta_rank() : 0, column = L.ctas > 1 ? cluster_id() : blockIdx.x;
     const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
@@ -396,10 +405,10 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         of_channels<VEC, WITHIN>(p.mean + from, c0, L.by_cg, mu);
         of_channels<VEC, WITHIN>(p.rstd + from, c0, L.by_cg, r);
         // xh and dz of a pack
-        auto values = [&](int k, Pair (&xh)[Q], Pair (&dz)[Q]) {
+        auto values = [&](const P& vx, const P& vd, Pair (&xh)[Q], Pair (&dz)[Q]) {
             Pair z[Q];
-            less<T, VEC, WITHIN>(value(k, 0), mu, xh);
-            plus<T, VEC>(value(k, 1), 0.f, dz);
+            less<T, VEC, WITHIN>(vx, mu, xh);
+            plus<T, VEC>(vd, 0.f, dz);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 xh[q] = mul2(xh[q], r[WITHIN ? 0 : q]);
@@ -413,15 +422,25 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         for (int q = 0; q < Q; ++q) s[0][q] = s[1][q] = pk2(0.f, 0.f);
         auto add = [&](int from, int to) {
             to = min(to, rounds);
-            for (int k = from; k < to; ++k) {
+            auto take = [&](const P& vx, const P& vd) {
                 Pair xh[Q], dz[Q];
-                values(k, xh, dz);
+                values(vx, vd, xh, dz);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     s[0][q] = add2(s[0][q], dz[q]);
                     s[1][q] = fma2(dz[q], xh[q], s[1][q]);
                 }
-            }
+            };
+            int k = from;
+            if constexpr (AHEAD > 1)
+                for (; k + AHEAD <= to; k += AHEAD) {
+                    P vx[AHEAD], vd[AHEAD];
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) vx[i] = value(k + i, 0), vd[i] = value(k + i, 1);
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) take(vx[i], vd[i]);
+                }
+            for (; k < to; ++k) take(value(k, 0), value(k, 1));
         };
         if constexpr (HELD) by_batches(rounds, add);
         else add(0, rounds);
@@ -439,18 +458,28 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, m1);
         of_channels<VEC, WITHIN>(mine_stats + all, c0, L.by_cg, m2);
         T* dst = dx + at.at;
-        for (int k = 0; k < last; ++k, dst += step) {
+        auto put = [&](const P& vx, const P& vd) {
             Pair xh[Q], dz[Q];
-            if (k < rounds) {
-                values(k, xh, dz);
+            values(vx, vd, xh, dz);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) dz[q] = mul2(r[WITHIN ? 0 : q], sub2(sub2(mul2(dz[q], w[q]), m1[WITHIN ? 0 : q]), mul2(xh[q], m2[WITHIN ? 0 : q])));
-            } else {
-#pragma unroll
-                for (int q = 0; q < Q; ++q) dz[q] = pk2(0.f, 0.f);
-            }
+            for (int q = 0; q < Q; ++q) dz[q] = mul2(r[WITHIN ? 0 : q], sub2(sub2(mul2(dz[q], w[q]), m1[WITHIN ? 0 : q]), mul2(xh[q], m2[WITHIN ? 0 : q])));
             *reinterpret_cast<P*>(dst) = rounded<T, VEC>(dz);
-        }
+            dst += step;
+        };
+        int k = 0;
+        if constexpr (AHEAD > 1)
+            for (; k + AHEAD <= rounds; k += AHEAD) {
+                P vx[AHEAD], vd[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) vx[i] = value(k + i, 0), vd[i] = value(k + i, 1);
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) put(vx[i], vd[i]);
+            }
+        for (; k < rounds; ++k) put(value(k, 0), value(k, 1));
+        Pair none[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) none[q] = pk2(0.f, 0.f);
+        for (; k < last; ++k, dst += step) *reinterpret_cast<P*>(dst) = rounded<T, VEC>(none);
     }
     if (!p.partial) return;
     // the threads of a pack, one after the other

@@ -662,17 +662,19 @@ template <auto Kernel> int resident(int i, int threads, size_t smem)
     return n;
 }
 
-// Few clusters are of CTAs of sixteen warps, one an SM, in the largest clusters of which all are resident at once: what a
-// round costs, some 2 us whatever its size, then comes least often (2 x 8192 x 264 fp16 forward: 14 us; with clusters of
-// twice as many CTAs of eight warps, which do not all fit, 22). Many take two CTAs of eight warps an SM, as many to a cluster
-// as fill these places (4 x 8192 x 1024 fp32 backward: 107 us, 121 with sixteen warps).
+// Few clusters of long series are of CTAs of sixteen warps, one an SM, in the largest clusters of which all are resident at once:
+// what a round costs, some 2 us whatever its size, then comes least often (2 x 16383 x 264 fp16 forward: 23.4 us; with eight
+// warps and eight CTAs 28.5). What eight CTAs of eight warps take in one round is theirs (1 x 1024 x 64 bf16: 5.0 us, 6.4 with sixteen
+// warps). Many clusters take two CTAs of eight warps an SM, as many to a cluster as all find such places: those of a second turn
+// would run by themselves (bf16 forward with 1, 2, 4 and 8 CTAs: 4 x 8192 x 1024 82, 54, 40 and 46 us, 16 x 8192 x 1024 130,
+// 144, 141 and 162; the former with sixteen warps in fp32, backward, 121 for 97).
 template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
     const sdtw_recurrence& a = p.a;
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
     if constexpr (RING) {
         constexpr size_t image = 16 * ROWS * 32 * VEC * sizeof(T), totals = sizeof(Run) * 2 * 32;
-        for (int i = 4; i >= 2 && 4 * clusters <= sms; --i) {
+        for (int i = 4; i >= 2 && 4 * clusters <= sms && a.N > 64 * ROWS; --i) {
             if (8ll * ROWS << i >= a.N) continue;              // half as many would do
             const int n = backward ? resident<recurrence_bwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 6 * image + kMostCtas * totals)
                                    : resident<recurrence_fwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 2 * kStages * image + kMostCtas * totals);
@@ -680,7 +682,7 @@ template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_ro
         }
     }
     int k = 1;
-    while (k < 8 && clusters * k < 2ll * sms && 8ll * ROWS * k < a.N) k *= 2;
+    while (k < 8 && clusters * 2 * k <= 2ll * sms && 8ll * ROWS * k < a.N) k *= 2;
     return run_warps<T, VEC, ROWS, 8, RING, TIED>(p, backward, k, s);
 }
 template <typename T, int VEC> cudaError_t run_few(const RecurrenceParams& p, cudaStream_t s)
