@@ -186,9 +186,9 @@ template <typename T> __global__ void __launch_bounds__(256) gated_pack_kernel(c
         for (int k = 0; k < kParts<T>; ++k) {
             const uint2 u = make_uint2(pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3]));
             *reinterpret_cast<uint2*>(to + k * part) = u;
-            const O* e = reinterpret_cast<const O*>(&u);
+            const Halves<O> lo(u.x), hi(u.y);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) v[z] -= to_f32(e[z]);
+            for (int z = 0; z < 2; ++z) v[z] -= to_f32(lo.e[z]), v[2 + z] -= to_f32(hi.e[z]);
         }
     }
 }

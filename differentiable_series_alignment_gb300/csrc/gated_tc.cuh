@@ -298,9 +298,9 @@ template <typename O> __device__ __forceinline__ void read_chunk(uint32_t area, 
             if constexpr (sizeof(O) == 4) {
                 v[q * E + k] = __uint_as_float(u[k]);
             } else {
-                const O* e = reinterpret_cast<const O*>(&u[k]);
-                v[q * E + 2 * k] = to_f32(e[0]);
-                v[q * E + 2 * k + 1] = to_f32(e[1]);
+                const Halves<O> h(u[k]);
+                v[q * E + 2 * k] = to_f32(h.e[0]);
+                v[q * E + 2 * k + 1] = to_f32(h.e[1]);
             }
         }
     }
@@ -593,9 +593,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
                             if (part + 1 < PARTS)   // what the parts so far leave, exact
 #pragma unroll
                                 for (int j = 0; j < 32; j += 2) {
-                                    const uint32_t w = pack2<O>(v[j], v[j + 1]);
-                                    const O* e = reinterpret_cast<const O*>(&w);
-                                    v[j] -= to_f32(e[0]), v[j + 1] -= to_f32(e[1]);
+                                    const Halves<O> h(pack2<O>(v[j], v[j + 1]));
+                                    v[j] -= to_f32(h.e[0]), v[j + 1] -= to_f32(h.e[1]);
                                 }
                         }
                         if (p.sums) {

@@ -187,7 +187,7 @@ template <typename T, int VEC> __device__ __forceinline__ void add_onto(Pair (&s
         upk2(s[q], x, y);
         if constexpr (VEC == 1) x += to_f32(v.e[0]);
         else if constexpr (sizeof(T) == 4) x += v.e[2 * q], y += v.e[2 * q + 1];
-        else add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+        else add_pair<T>(x, y, word_of(&v.e[2 * q]));
         s[q] = pk2(x, y);
     }
 }
@@ -332,27 +332,29 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 #pragma unroll
         for (int q = 0; q < Q; ++q) rw[q] = mul2(rw[q], r[WITHIN ? 0 : q]);
         T* dst = y + at.at;
-        auto put = [&](const P& v) {
-            less<T, VEC, WITHIN>(v, mu, d);
+        auto put = [&](int k, const P& v) {
+            Pair z[Q];
+            less<T, VEC, WITHIN>(v, mu, z);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) d[q] = fma2(d[q], rw[q], bias[q]);
-            activate_all<sizeof(T) == 4, false, Q>(p.activation, d);
-            *reinterpret_cast<P*>(dst) = rounded<T, VEC>(d);
-            dst += step;
+            for (int q = 0; q < Q; ++q) z[q] = fma2(z[q], rw[q], bias[q]);
+            activate_all<sizeof(T) == 4, false, Q>(p.activation, z);
+            *reinterpret_cast<P*>(dst + k * step) = rounded<T, VEC>(z);
         };
-        int k = 0;
-        if constexpr (!HELD)   // rows that are read again come four at a time
-            for (; k + 4 <= rounds; k += 4) {
+        int first = 0;
+        if constexpr (!HELD) {   // rows that are read again come four at a time
+            for (; first + 4 <= rounds; first += 4) {
                 P v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = value(k + i);
+                for (int i = 0; i < 4; ++i) v[i] = value(first + i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) put(v[i]);
+                for (int i = 0; i < 4; ++i) put(first + i, v[i]);
             }
-        for (; k < rounds; ++k) put(value(k));
+        }
+#pragma unroll 4
+        for (int k = first; k < rounds; ++k) put(k, value(k));
 #pragma unroll
         for (int q = 0; q < Q; ++q) d[q] = pk2(0.f, 0.f);
-        for (; k < last; ++k, dst += step) *reinterpret_cast<P*>(dst) = rounded<T, VEC>(d);
+        for (int k = rounds; k < last; ++k) *reinterpret_cast<P*>(dst + k * step) = rounded<T, VEC>(d);
     }
 }
 
@@ -360,7 +362,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 {
     extern __shared__ __align__(16) unsigned char held[];   // [rounds][x, dy][kThreads] packs, then the weights and the sums
     using P = Pack<T, VEC>;
-    constexpr int Q = kPairs<VEC>, AHEAD = HELD ? 1 : VEC == 1 ? 4 : 2;     // rows that come from memory at a time
+    constexpr int Q = kPairs<VEC>, AHEAD = HELD ? 1 : 4;     // rows that come from memory at a time
     const int slab = blockIdx.y, rank = L.ctas > 1 ? cta_rank() : 0, column = L.ctas > 1 ? cluster_id() : blockIdx.x;
     const int groups = L.groups, all = L.items * groups;
     float* weights = reinterpret_cast<float*>(held + (HELD ? (size_t)L.rounds * 2 * kThreads * 16 : 0));
@@ -431,16 +433,17 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
                     s[1][q] = fma2(dz[q], xh[q], s[1][q]);
                 }
             };
-            int k = from;
-            if constexpr (AHEAD > 1)
-                for (; k + AHEAD <= to; k += AHEAD) {
+            if constexpr (AHEAD > 1) {
+                for (; from + AHEAD <= to; from += AHEAD) {
                     P vx[AHEAD], vd[AHEAD];
 #pragma unroll
-                    for (int i = 0; i < AHEAD; ++i) vx[i] = value(k + i, 0), vd[i] = value(k + i, 1);
+                    for (int i = 0; i < AHEAD; ++i) vx[i] = value(from + i, 0), vd[i] = value(from + i, 1);
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i) take(vx[i], vd[i]);
                 }
-            for (; k < to; ++k) take(value(k, 0), value(k, 1));
+            }
+#pragma unroll 2
+            for (int k = from; k < to; ++k) take(value(k, 0), value(k, 1));
         };
         if constexpr (HELD) by_batches(rounds, add);
         else add(0, rounds);
@@ -458,28 +461,29 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         of_channels<VEC, WITHIN>(mine_stats, c0, L.by_cg, m1);
         of_channels<VEC, WITHIN>(mine_stats + all, c0, L.by_cg, m2);
         T* dst = dx + at.at;
-        auto put = [&](const P& vx, const P& vd) {
+        auto put = [&](int k, const P& vx, const P& vd) {
             Pair xh[Q], dz[Q];
             values(vx, vd, xh, dz);
 #pragma unroll
             for (int q = 0; q < Q; ++q) dz[q] = mul2(r[WITHIN ? 0 : q], sub2(sub2(mul2(dz[q], w[q]), m1[WITHIN ? 0 : q]), mul2(xh[q], m2[WITHIN ? 0 : q])));
-            *reinterpret_cast<P*>(dst) = rounded<T, VEC>(dz);
-            dst += step;
+            *reinterpret_cast<P*>(dst + k * step) = rounded<T, VEC>(dz);
         };
-        int k = 0;
-        if constexpr (AHEAD > 1)
-            for (; k + AHEAD <= rounds; k += AHEAD) {
+        int first = 0;
+        if constexpr (AHEAD > 1) {
+            for (; first + AHEAD <= rounds; first += AHEAD) {
                 P vx[AHEAD], vd[AHEAD];
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) vx[i] = value(k + i, 0), vd[i] = value(k + i, 1);
+                for (int i = 0; i < AHEAD; ++i) vx[i] = value(first + i, 0), vd[i] = value(first + i, 1);
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) put(vx[i], vd[i]);
+                for (int i = 0; i < AHEAD; ++i) put(first + i, vx[i], vd[i]);
             }
-        for (; k < rounds; ++k) put(value(k, 0), value(k, 1));
+        }
+#pragma unroll 2
+        for (int k = first; k < rounds; ++k) put(k, value(k, 0), value(k, 1));
         Pair none[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) none[q] = pk2(0.f, 0.f);
-        for (; k < last; ++k, dst += step) *reinterpret_cast<P*>(dst) = rounded<T, VEC>(none);
+        for (int k = rounds; k < last; ++k) *reinterpret_cast<P*>(dst + k * step) = rounded<T, VEC>(none);
     }
     if (!p.partial) return;
     // the threads of a pack, one after the other

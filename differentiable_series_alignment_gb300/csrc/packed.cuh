@@ -11,6 +11,18 @@
 
 namespace sdtw {
 
+// Two neighbouring 16-bit elements as one word, and a word's two elements. By copies: a compiler takes an element and a word
+// for different objects, and may drop the store of one that is read as the other.
+template <typename T> __device__ __forceinline__ uint32_t word_of(const T* e) {
+    uint32_t w;
+    memcpy(&w, e, 4);
+    return w;
+}
+template <typename T> struct Halves {
+    T e[2];
+    __device__ __forceinline__ explicit Halves(uint32_t w) { memcpy(e, &w, 4); }
+};
+
 // two fp32 values rounded to 16 bits each, lo in the low half
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
@@ -77,7 +89,7 @@ template <typename T, int VEC> __device__ __forceinline__ void plus(const Pack<T
             out[q] = add2(pk2(v.e[2 * q], v.e[2 * q + 1]), pk2(c, c));
         } else {
             float x, y;
-            sum_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]), c, c);
+            sum_pair<T>(x, y, word_of(&v.e[2 * q]), c, c);
             out[q] = pk2(x, y);
         }
     }
@@ -90,7 +102,10 @@ template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> rounded(c
         upk2(v[q], x, y);
         if constexpr (VEC == 1) o.e[0] = from_f32<T>(x);
         else if constexpr (sizeof(T) == 4) o.e[2 * q] = x, o.e[2 * q + 1] = y;
-        else *reinterpret_cast<uint32_t*>(&o.e[2 * q]) = pack2<T>(x, y);
+        else {
+            const Halves<T> h(pack2<T>(x, y));
+            o.e[2 * q] = h.e[0], o.e[2 * q + 1] = h.e[1];
+        }
     }
     return o;
 }
@@ -102,7 +117,7 @@ template <typename T, int VEC> __device__ __forceinline__ Pair sum_onto(Pair s, 
     for (int q = 0; q < kPairs<VEC>; ++q) {
         if constexpr (VEC == 1) x += to_f32(v.e[0]);
         else if constexpr (sizeof(T) == 4) x += v.e[2 * q], y += v.e[2 * q + 1];
-        else add_pair<T>(x, y, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]));
+        else add_pair<T>(x, y, word_of(&v.e[2 * q]));
     }
     return pk2(x, y);
 }
@@ -123,7 +138,7 @@ template <typename T, int VEC> __device__ __forceinline__ void minus(const Pack<
             out[q] = sub2(pk2(v.e[2 * q], v.e[2 * q + 1]), m[q]);
         } else {
             float a, b;
-            sum_pair<T>(a, b, *reinterpret_cast<const uint32_t*>(&v.e[2 * q]), -x, -y);
+            sum_pair<T>(a, b, word_of(&v.e[2 * q]), -x, -y);
             out[q] = pk2(a, b);
         }
     }

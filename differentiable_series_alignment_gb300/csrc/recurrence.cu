@@ -59,8 +59,8 @@ template <typename T, int VEC> __device__ __forceinline__ Pair value(typename Ra
         if constexpr (VEC == 2) return r;
         else return pk2(__uint_as_float(r), 0.f);
     } else {
-        const T* e = reinterpret_cast<const T*>(&r);
-        return pk2(to_f32(e[0]), VEC > 1 ? to_f32(e[1]) : 0.f);
+        const Halves<T> h(r);
+        return pk2(to_f32(h.e[0]), VEC > 1 ? to_f32(h.e[1]) : 0.f);
     }
 }
 template <typename T, int VEC> __device__ __forceinline__ void store(T* p, Pair v) {
@@ -70,7 +70,7 @@ template <typename T, int VEC> __device__ __forceinline__ void store(T* p, Pair 
         float x, y;
         upk2(v, x, y);
         if constexpr (VEC == 1) *p = from_f32<T>(x);
-        else *reinterpret_cast<uint32_t*>(p) = pack2<T>(x, y);
+        else *reinterpret_cast<Pack<T, 2>*>(p) = rounded<T, 2>({v});
     }
 }
 template <int VEC> __device__ __forceinline__ Pair load_f32(const float* p) { return VEC == 1 ? pk2(p[0], 0.f) : *reinterpret_cast<const Pair*>(p); }
