@@ -1,7 +1,6 @@
 // block_api.cu -- the C ABI of group norm, gated recurrence and gated linear units: validation on the host before any
 // launch, and launches on the caller's stream.
 #include <cmath>
-#include <cstdlib>
 
 #include "block.h"
 #include "kernels.h"
@@ -44,7 +43,9 @@ sdtw_status check_recurrence(const sdtw_recurrence* a)
     if (a->B < 1 || a->N < 1 || a->C < 1) return SDTW_ERR_EMPTY;
     if (!a->x || !a->gate || !good_dtype(a->dtype)) return SDTW_ERR_ARG;
     // 32-bit positions and grids, and offsets of 128 positions
-    if (a->N >= (1 << 30) || a->C > (1 << 23) || std::llabs(a->x_stride[1]) > (1 << 23) || std::llabs(a->gate_stride[1]) > (1 << 23) || (long long)a->B * ((a->C + 31ll) / 32) > 0x7fffffffll) return SDTW_ERR_TOO_LARGE;
+    const auto far = [](long long stride) { return stride > (1 << 23) || stride < -(1 << 23); };
+    if (a->N >= (1 << 30) || a->C > (1 << 23) || far(a->x_stride[1]) || far(a->gate_stride[1]) || (long long)a->B * ((a->C + 31ll) / 32) > 0x7fffffffll)
+        return SDTW_ERR_TOO_LARGE;
     return SDTW_OK;
 }
 

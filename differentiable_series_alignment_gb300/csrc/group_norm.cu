@@ -10,6 +10,11 @@
 // square of centred values. A thread has the same channels throughout, and sums the weights' gradients in registers over
 // all that its CTA takes; the CTAs' sums are added by a second launch in a fixed order: the same bits every time. Slabs
 // that a cluster cannot hold are read again, from the cache where it has them.
+//
+// Measured: 16 x 4096 x 512 bf16 by 32 groups with SiLU 45 us forward (3.0 TB/s), 86 backward (2.3); 64 such 151 and 303; 65535 rows of
+// 1024 by groups of 128 73 and 99 (3.7 and 4.1 TB/s). Not memory bounds these but instructions (three passes over a
+// pack, an exponential and a reciprocal an element in each that needs the activation) and the barriers between passes. Slabs
+// kept in shared memory take 43 and 84 us where reading them again takes 57 and 100.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -341,7 +346,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
             *reinterpret_cast<P*>(dst + k * step) = rounded<T, VEC>(z);
         };
         int first = 0;
-        if constexpr (!HELD) {   // rows that are read again come four at a time
+        if constexpr (!HELD) {   // rows that are read again come four at a time (2 x 8192 x 512 fp32: 28 us, one by one 38)
             for (; first + 4 <= rounds; first += 4) {
                 P v[4];
 #pragma unroll
@@ -507,7 +512,8 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
 }
 
 // ---- groups of a few positions (normalising row by row): a group is `lanes` lanes of a warp, at most two packs each, whose
-// sums need no barrier. A thread's group and channels stay the same over the batch elements that it takes, every
+// sums need no barrier (65535 rows of 1024 by groups of 128 bf16: 70 us forward and 97 backward, as slabs 486 and 458; 16 rows of
+// 512 forward: 3.1 and 4.2). A thread's group and channels stay the same over the batch elements that it takes, every
 // columns-th; the coming ones' packs are on their way to shared memory meanwhile, a thread's to places of its own.
 __device__ __forceinline__ float lane_sum(float v, int lanes) {
 #pragma unroll
@@ -848,7 +854,8 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
         return std::pair<size_t, long long>(sums + exchange, rounds * kThreads * 16 * arrays);
     };
     // CTAs of a cluster: until three fit on an SM side by side, or, where there are fewer than two an SM, until a thread has
-    // eight rows: a cluster's exchanges take some 2 us
+    // eight rows: a cluster's exchanges take some 2 us (16 x 4096 x 512 bf16 with 1, 2, 4, 8 and 16 CTAs: forward 69, 61,
+    // 43, 59 and 107 us, of which this takes 4; backward 118, 112, 123, 85 and 140, of which it takes 8)
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
     while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes &&

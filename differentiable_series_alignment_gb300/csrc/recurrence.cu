@@ -15,6 +15,10 @@
 // the lanes that use them). Pairs go between CTAs by stores that report to the receiver's mbarrier: a
 // cluster's own barrier also waits for the results that are on their way to memory. One warp folds the CTAs' pairs and hands the
 // state on: read by every warp, they took 900 cycles of shared memory a round.
+//
+// Measured: 16 x 8192 x 1024 bf16 132 us forward (6.1 TB/s) and 255 backward (5.3); 4 such 43 and 78; 4 in fp32 73 and 99 (6.8 TB/s of
+// a copy's 6.8); 2 x 16383 x 264 fp16 23 and 43. Memory bounds the many; the few by their rounds, which pass the
+// state on one after the other. Loaded by the lanes that use them, 4 x 8192 x 1024 takes 127 and 189 us (ring: 40 and 76).
 #include "activation.cuh"
 #include "attn_tc.cuh"
 #include "block.h"
@@ -563,7 +567,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     if (p.dstate && rank == 0 && warp == 0) store_f32<VEC>(p.dstate + bc, carry);
 }
 
-// A few new samples: a thread has its channels' positions from first to last, all of them on their way at once.
+// A few new samples: a thread has its channels' positions from first to last, all of them on their way at once (64 x 1 x 1024 bf16:
+// 1.8 us, by the scan 12.4; 4096 x 8 x 1024: 37 us, 681).
 template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) recurrence_few_kernel(const RecurrenceParams p)
 {
     const sdtw_recurrence& a = p.a;

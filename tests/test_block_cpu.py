@@ -57,7 +57,8 @@ def test_group_norm_refuses_eps_and_workspaces(lib):
 @pytest.mark.parametrize("change,code", [
     (dict(B=0), EMPTY), (dict(N=0), EMPTY), (dict(C=0), EMPTY), (dict(x=None), ARG), (dict(gate=None), ARG), (dict(dtype=5), ARG),
     (dict(N=1 << 30, C=1), TOO_LARGE), (dict(C=(1 << 30) + 1), TOO_LARGE),
-    (dict(x_stride=(64, (1 << 23) + 1)), TOO_LARGE), (dict(gate_stride=(64, -(1 << 24))), TOO_LARGE)])
+    (dict(x_stride=(64, (1 << 23) + 1)), TOO_LARGE), (dict(gate_stride=(64, -(1 << 24))), TOO_LARGE),
+    (dict(x_stride=(64, -(1 << 63))), TOO_LARGE)])
 def test_recurrence_refusals(lib, change, code):
     base = dict(x=0x1000, gate=0x2000, x_stride=(64, 8), gate_stride=(64, 8), state=None, lengths=None, B=2, N=3, C=8, dtype=0, reverse=0, tied=1)
     base.update(change)

@@ -764,3 +764,57 @@ def test_problems_keep_their_tensors():
     gc.collect()
     for problem, tensors in problems:
         assert all(t() is not None for t in tensors)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_overlapping_rows(package, dtype):
+    """Windows of one series as rows: a stride shorter than a row."""
+    gen = generator(51)
+    series = randn(gen, 8 * 300 + 64, dtype=dtype)
+    windows = series.unfold(0, 64, 8)                                             # (301, 64), a row every 8
+    wg, wu = (randn(gen, 96, 64, dtype=dtype, std=0.1) for _ in range(2))
+    check_gated(package, windows, wg, wu, None, None, randn(gen, 301, 96, dtype=dtype), "silu")
+    few = series[:8 * 7 + 64].unfold(0, 64, 8)
+    assert torch.equal(package.gated_linear(few, wg, wu), package.gated_linear(few.contiguous(), wg, wu))
+    x, gate = windows[None], series.flip(0).unfold(0, 64, 8)[None]
+    dh = randn(gen, 1, 301, 64, dtype=dtype)
+    outs = []
+    for a, b in ((x, gate), (x.contiguous(), gate.contiguous())):
+        a, b = a.detach().requires_grad_(), b.detach().requires_grad_()
+        h = package.gated_recurrence(a, b)
+        outs.append((h, *torch.autograd.grad(h, (a, b), dh)))
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+
+
+def test_the_same_tensor_twice(package):
+    gen = generator(52)
+    x, w = randn(gen, 70, 40), randn(gen, 48, 40, std=0.2)
+    dh = randn(gen, 70, 48)
+    want, bound = gated_reference(x, w, w, None, None, dh, "silu")
+    w.requires_grad_()
+    h = package.gated_linear(x, w, w)
+    within(h, want[0], bound[0], "h")
+    within(torch.autograd.grad(h, w, dh)[0], want[2] + want[3], bound[2] + bound[3] + U * (want[2] + want[3]).abs(), "dw")
+    x = randn(gen, 2, 90, 24)
+    dh = randn(gen, 2, 90, 24)
+    want, bound = recurrence_reference(x, x, None, dh, None, None, False, True)
+    x.requires_grad_()
+    got = torch.autograd.grad(package.gated_recurrence(x, x), x, dh)[0]
+    within(got, want[2] + want[3], bound[2] + bound[3] + U * (want[2] + want[3]).abs(), "dx + dgate")
+
+
+def test_second_derivatives_are_refused(package):
+    x = randn(generator(53), 3, 5, 16).requires_grad_()
+    w = randn(generator(53), 8, 16).requires_grad_()
+    for y in (package.group_norm(x, 4), package.gated_recurrence(x, x), package.gated_linear(x, w, w)):
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            torch.autograd.grad(y.sum(), x, create_graph=True)
+
+
+# one accumulator of 256, of 128 and of 64 columns is what the least time asks for
+@pytest.mark.parametrize("shape", [(2048, 64, 4096), (1024, 64, 1024), (128, 72, 256)], ids=str)
+def test_widths_of_accumulators(package, shape):
+    R, K, F = shape
+    gen = generator(54)
+    x, wg, wu = randn(gen, R, K, dtype=BF16), randn(gen, F, K, dtype=BF16, std=K ** -0.5), randn(gen, F, K, dtype=BF16, std=K ** -0.5)
+    check_gated(package, x, wg, wu, randn(gen, F, dtype=BF16, std=0.5), None, randn(gen, R, F, dtype=BF16), "gelu")
