@@ -20,9 +20,8 @@
 // first of a pair issues for both.
 //
 // Measured, 16384 x 1024 to 4096 bf16: FWD 140 us (1960 TFLOP/s; a library's product of x with both weights alone 143),
-// GRAD 145, DX 186, DW 218 in a backward pass of 549. The tensor pipe bounds them, and the power that it takes: one at a time, 2048 to
-// 2048 features, FWD, GRAD and DX run in 147, 152 and 148 us with the pipe 85 % busy. DW in 167 (75 %): workers that
-// share tiles stand at different rows, and dg is read twice (650 MB). fp32, 16384 x 64 to 256: 26 us forward, 85 backward, bound by the
+// GRAD 150, DX 178, DW 182 in a backward pass of 514. The tensor pipe bounds them, and the power that it takes: one at a time, 2048 to
+// 2048 features, FWD, GRAD and DX run in 147, 152 and 148 us with the pipe 85 % busy. fp32, 16384 x 64 to 256: 26 us forward, 85 backward, bound by the
 // epilogue of two blocks of sum (three parts of dg and du are written) and the launches around it.
 #pragma once
 #include <algorithm>
@@ -53,7 +52,7 @@ struct Params {
     int segs, blocks;                                  // the sum: segs pieces of `blocks` blocks
     bool grouped_a, grouped_b;                         // maps of MN-major operands have groups of 64 columns as a dimension
     int tiles_m, tiles_n, group, set0, sets, tiles;    // sets: DW's weights, from set0 on
-    int whole, workers;                                // tiles summed whole; workers that share the others' sums (below)
+    int whole, cuts;                                   // tiles summed whole; pieces of the others' sums, or 0 (below)
     long long M;                                       // rows and columns of the result
     int N, F, activation;
     void* out[2];                                      // FWD h; DX dx; DW both weights' gradients
@@ -62,7 +61,7 @@ struct Params {
     uint16_t* grads;
     long long ld;
     float* sums;                                       // GRAD, with biases: [M / 32][2 F] column sums of 32 rows
-    float* shares;                                     // DX, DW: [2 workers][rows of a tile][its columns]
+    float* shares;                                     // DX, DW: [cuts][tiles not summed whole][rows of a tile][its columns]
     const unsigned* top;                               // fp16: bits of the largest |dh|, by which dg and du are scaled
     unsigned long long wait_ns;
     int skip;                                          // test hook: nothing is loaded
@@ -205,33 +204,27 @@ struct Tile {
         m = group * G + in - n * rows;
     }
 };
-// What a worker (a CTA, or a pair) does: every workers-th of the whole tiles, as many as all have alike, and a part of the
-// blocks of those that are left, which all share evenly: the end of one tile's sum and the beginning of the next one's at the most.
-// Parts go to memory in fp32 and are added up, in the workers' order, by a launch of their own.
+// What a worker (a CTA, or a pair) does: every workers-th of the whole tiles, as many as all have alike, and of the pieces of the
+// sums of those that are left. A piece's tiles follow one another, so that workers read the same rows of an operand at the same
+// time: where each worker had a range of its own of one tile's sum, DW of 16384 x 1024 to 4096 read dg twice and a half and took 218 us
+// for 182. Pieces go to memory in fp32 and are added up, in their order, by a launch of their own.
 struct Work {
     const Params& p;
-    int t, stride, share;
-    long long u, end;
-    __device__ __forceinline__ Work(const Params& p_, int worker, int workers) : p(p_), t(worker), stride(workers), share(2 * worker), u(0), end(0) {
-        const long long units = (long long)(p.tiles - p.whole) * p.segs * p.blocks;
-        if (worker < p.workers) u = units * worker / p.workers, end = units * (worker + 1) / p.workers;
-    }
+    int t, stride, left;
+    __device__ __forceinline__ Work(const Params& p_, int worker, int workers) : p(p_), t(worker), stride(workers), left(p_.tiles - p_.whole) {}
     __device__ __forceinline__ bool next(Tile& tile) {
         const int total = p.segs * p.blocks;
         if (t < p.whole) {
             tile.place(p, t);
             tile.first = 0, tile.last = total, tile.share = -1;
-            t += stride;
-            return true;
+        } else {
+            const int q = t - p.whole, cut = p.cuts ? q / left : 1;
+            if (cut >= p.cuts) return false;
+            tile.place(p, p.whole + q - cut * left);
+            tile.first = (int)((long long)total * cut / p.cuts), tile.last = (int)((long long)total * (cut + 1) / p.cuts);
+            tile.share = q;
         }
-        if (u >= end) return false;
-        const int k = (int)(u / total);
-        tile.place(p, p.whole + k);
-        tile.first = (int)(u - (long long)k * total);
-        tile.last = (int)min((long long)total, tile.first + (end - u));
-        tile.share = tile.first == 0 && tile.last == total ? -1 : share;
-        ++share;
-        u += tile.last - tile.first;
+        t += stride;
         return true;
     }
 };
@@ -685,18 +678,8 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_
     tile.place(p, p.whole + blockIdx.x);
     T* out = static_cast<T*>(p.out[tile.set]);
     if (!out) return;
-    const long long total = (long long)p.segs * p.blocks, units = (p.tiles - p.whole) * total, lo = blockIdx.x * total, hi = lo + total;
-    auto start = [&](long long w) { return units * w / p.workers; };
-    long long w0 = lo * p.workers / units, w1 = hi * p.workers / units;   // the first worker with a part of it, and the one behind the last
-    while (w0 > 0 && start(w0) > lo) --w0;
-    while (start(w0 + 1) <= lo) ++w0;
-    while (w1 > w0 + 1 && start(w1 - 1) >= hi) --w1;
-    while (w1 < p.workers && start(w1) < hi) ++w1;
-    if (w1 == w0 + 1 && start(w0) <= lo) return;           // it alone: written whole
-    // a worker's first part is of the tile that its range begins in
-    const int count = (int)(w1 - w0), per = (count + 3) / 4, from = min(group * per, count), to = min(from + per, count);
-    const float* first = p.shares + (2 * w0 + (start(w0) < lo ? 1 : 0)) * ROWS * NB;
-    const float* parts = p.shares + 2 * w0 * ROWS * NB;
+    const int left = p.tiles - p.whole, per = (p.cuts + 3) / 4, from = min(group * per, p.cuts), to = min(from + per, p.cuts);
+    const float* parts = p.shares + (long long)blockIdx.x * ROWS * NB;
     const bool vec = p.N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0;
     for (int k = blockIdx.y; k < PIECES; k += gridDim.y) {
         const int e = (k * 64 + lane) * 4, r = e / NB, c = e % NB;
@@ -707,7 +690,7 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_
         if (in) {
 #pragma unroll 8
             for (int w = from; w < to; ++w) {
-                const float4 v = *reinterpret_cast<const float4*>((w == 0 ? first : parts + 2ll * w * ROWS * NB) + e);
+                const float4 v = *reinterpret_cast<const float4*>(parts + (long long)w * left * ROWS * NB + e);
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
         }
@@ -731,29 +714,30 @@ template <typename T, int NB> __global__ void __launch_bounds__(256) gated_join_
     }
 }
 
-// How many tiles there are and how they are shared out. Sharing pays where the blocks that it saves the last round take longer
-// than the shares' way through memory and another launch (GRAD and DX of 256 x 1024 to 4096 bf16: 31 us, unshared 46; of 16384 rows,
-// where the last of many rounds counts little, 333 and 336). Returns about how long it all takes, in us: a block takes 0.34 at 256
-// columns, 0.22 and 0.15 at 128 and 64 (loads bound these), in three parts 1 and 0.7, a tile 1.5 besides.
+// How many tiles there are and how they are shared out. Cutting sums pays where the blocks that it saves the last round take longer
+// than the pieces' way through memory and another launch (GRAD and DX of 256 x 1024 to 4096 bf16: 31 us, uncut 46). Returns about
+// how long it all takes, in us: a block takes 0.34 at 256 columns, 0.22 and 0.15 at 128 and 64 (loads bound these), in
+// three parts 1 and 0.7, a tile 1.5 besides.
 inline double share_out(Params& p, int rows, int width, int nb, int parts, int workers, bool share)
 {
     p.tiles_m = (int)((p.M + rows - 1) / rows), p.tiles_n = (p.N + width - 1) / width;
     const int side = std::min(p.tiles_n, 9);
     p.group = (workers + side - 1) / side;
     p.tiles = p.tiles_m * p.tiles_n * p.sets;
-    p.whole = p.tiles, p.workers = 0;
-    const int left = p.tiles % workers, rounds = p.tiles / workers;
-    const long long total = (long long)p.segs * p.blocks;
-    const double block = parts > 1 ? (nb == 128 ? 1. : 0.7) : nb == 256 ? 0.34 : nb == 128 ? 0.22 : 0.15, whole = rounds * (1.5 + block * (double)total);
-    const double last = left ? 1.5 + block * (double)total : 0.;
+    p.whole = p.tiles, p.cuts = 0;
+    const int left = p.tiles % workers, rounds = p.tiles / workers, total = p.segs * p.blocks;
+    const double block = parts > 1 ? (nb == 128 ? 1. : 0.7) : nb == 256 ? 0.34 : nb == 128 ? 0.22 : 0.15, whole = rounds * (1.5 + block * total);
+    double last = left ? 1.5 + block * total : 0.;
     if (!share || left == 0) return whole + last;
-    const int sharers = (int)std::max<long long>(left, std::min<long long>(workers, left * total / (parts > 1 ? 1 : 4)));   // four blocks at the least
-    const double shared = 1.5 + block * (double)((left * total + sharers - 1) / sharers) + 5. + 4e-6 * sharers * rows * width * sizeof(float) / 8.;
-    if (shared >= last) return whole + last;
-    p.whole = p.tiles - left, p.workers = sharers;
-    return whole + shared;
+    for (int r = 1; r <= 6; ++r) {                         // as many pieces as take r rounds, of four blocks at the least
+        const int cuts = std::min(r * workers / left, total / (parts > 1 ? 1 : 4));
+        if (cuts < 2) continue;
+        const double t = r * (1.5 + block * ((total + cuts - 1) / cuts)) + 4. + 3e-7 * cuts * left * rows * width * sizeof(float);
+        if (t < last) last = t, p.cuts = cuts, p.whole = p.tiles - left;
+    }
+    return whole + last;
 }
-inline size_t share_bytes(const Params& p, int rows, int width) { return p.workers ? (size_t)2 * p.workers * rows * width * sizeof(float) : 0; }
+inline size_t share_bytes(const Params& p, int rows, int width) { return (size_t)p.cuts * (p.tiles - p.whole) * rows * width * sizeof(float); }
 
 template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cudaStream_t s)
 {
@@ -765,12 +749,12 @@ template <int KIND, typename T, int NB> cudaError_t run(Params& p, int sms, cuda
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = Sh::ctas, at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    const int busy = p.whole ? std::max(std::min(p.whole, workers), p.workers) : p.workers;
+    const int busy = (int)std::min<long long>(workers, std::max((long long)p.whole, (long long)p.cuts * (p.tiles - p.whole)));
     c.gridDim = dim3((unsigned)(busy * Sh::ctas)), c.blockDim = dim3(kThreadsG), c.dynamicSmemBytes = Sh::smem;
     c.stream = s, c.attrs = &at, c.numAttrs = Sh::ctas > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&c, gated_tc_kernel<KIND, T, NB>, (const Params&)p);
     if constexpr (KIND == DX || KIND == DW)
-        if (e == cudaSuccess && p.workers) {
+        if (e == cudaSuccess && p.cuts) {
             const int tiles = p.tiles - p.whole, pieces = Sh::rows * NB / 4 / 64;
             return launch_behind(gated_join_kernel<T, NB>, dim3((unsigned)tiles, (unsigned)std::min(pieces, std::max(1, 8 * sms / tiles))), 256, s, p);
         }
