@@ -85,6 +85,13 @@ struct Layout {
     __device__ __forceinline__ int count(int n) const { return n > 0 ? lanes == 1 ? n : ((n - 1) >> 16) ? (n - 1) / lanes + 1 : (n - 1) / by_lanes + 1 : 0; }
 };
 
+// The cluster's CTAs have begun: told at a kernel's start, waited for before the first store to another's shared memory, when the
+// loads are on their way
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begun() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync_g() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -280,8 +287,8 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
     float* parts = stats + 2 * all;
     const T* x = static_cast<const T*>(p.x);
     T* y = static_cast<T*>(p.y);
+    if (L.ctas > 1) cluster_begin();
     take_weights(weights, p, L, slab);
-    if (L.ctas > 1) cluster_sync_g();                       // the others have begun
     const long long step = (long long)L.lanes * p.C;
     const int c0 = ((int)threadIdx.x - (int)threadIdx.x / L.by_packs * L.packs) * VEC;
     for (int b0 = column * L.items; b0 < p.B; b0 += L.columns * L.items) {
@@ -310,6 +317,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         };
         if constexpr (HELD) by_batches(rounds, add);
         else add(0, rounds);
+        if (L.ctas > 1) cluster_begun();                    // a cluster has one batch element
         auto count = [&](int k) { return length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg; };
         group_sums<VEC, WITHIN, 1>(s, red, parts, L, rank, [&](int, int k, float sum) { stats[k] = count(k) > 0.f ? sum / count(k) : 0.f; });
         const float* mine_stats = stats + (at.item < L.items ? at.item * groups : 0);
@@ -376,9 +384,9 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
     float* parts = stats + 2 * all;
     const T *x = static_cast<const T*>(p.x), *dy = static_cast<const T*>(p.dy);
     T* dx = static_cast<T*>(p.dx);
+    if (L.ctas > 1) cluster_begin();
     take_weights(weights, p, L, slab);
-    if (L.ctas > 1) cluster_sync_g();
-    else __syncthreads();
+    __syncthreads();
     const long long step = (long long)L.lanes * p.C;
     const int c0 = ((int)threadIdx.x - (int)threadIdx.x / L.by_packs * L.packs) * VEC;
     Pair w[Q], bias[Q], sum[2][Q];                          // of the weights' gradients
@@ -456,6 +464,7 @@ template <typename T, int VEC, bool HELD, bool WITHIN> __global__ void __launch_
         for (int q = 0; q < Q; ++q)
 #pragma unroll
             for (int k = 0; k < 2; ++k) sum[k][q] = add2(sum[k][q], s[k][q]), s[k][q] = mul2(s[k][q], w[q]);
+        if (L.ctas > 1) cluster_begun();                    // a cluster has one batch element
         if (!dx) continue;
         group_sums<VEC, WITHIN, 2>(s, red, parts + 2 * turn * L.ctas * all, L, rank, [&](int which, int k, float t) {
             const float n = length_of(p, L.items > 1 ? b0 + k / groups : b0) * (float)p.cg;
