@@ -4,8 +4,6 @@
 #include "encoder.h"
 #include "packed.cuh"
 
-#include <type_traits>
-
 namespace sdtw {
 
 __device__ __forceinline__ float reciprocal(float v) {
@@ -71,17 +69,6 @@ template <int ACT, bool EXACT, bool SLOPE> __device__ __forceinline__ Pair activ
         const float v = activate<ACT, EXACT, SLOPE>(y, slope);
         y = SLOPE ? slope : v;
         return pk2(x, y);
-    }
-}
-
-// f(std::integral_constant<int, activation>)
-template <typename F> __host__ __device__ __forceinline__ auto with_activation(int activation, F f) {
-    switch (activation) {
-        case SDTW_ACT_SILU: return f(std::integral_constant<int, SDTW_ACT_SILU>());
-        case SDTW_ACT_GELU: return f(std::integral_constant<int, SDTW_ACT_GELU>());
-        case SDTW_ACT_RELU: return f(std::integral_constant<int, SDTW_ACT_RELU>());
-        case SDTW_ACT_SIGMOID: return f(std::integral_constant<int, SDTW_ACT_SIGMOID>());
-        default: return f(std::integral_constant<int, SDTW_ACT_NONE>());
     }
 }
 

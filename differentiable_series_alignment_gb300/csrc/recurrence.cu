@@ -667,10 +667,11 @@ template <auto Kernel> int resident(int i, int threads, size_t smem)
     return n;
 }
 
-// Few clusters of long series are of CTAs of sixteen warps, one an SM, in the largest clusters of which all are resident at once:
-// what a round costs, some 2 us whatever its size, then comes least often (2 x 16383 x 264 fp16 forward: 23.4 us; with eight
-// warps and eight CTAs 28.5). What eight CTAs of eight warps take in one round is theirs (1 x 1024 x 64 bf16: 5.0 us, 6.4 with sixteen
-// warps). Many clusters take two CTAs of eight warps an SM, as many to a cluster as all find such places: those of a second turn
+// Few clusters of long series are of CTAs of sixteen warps, one an SM, sixteen CTAs to a cluster or eight, where all are resident at
+// once: what a round costs, some 2 us whatever its size, then comes least often (2 x 16383 x 264 fp16 forward: 23.4 us, with eight
+// warps and eight CTAs 28.5; 1 x 8192 x 768 fp32 22 and 30). Four such CTAs lose to eight of eight warps, with as many positions
+// (2 x 8192 x 640 bf16: 22.8 and 40.6 us for 21.1 and 36.5), and so do they all where one round is enough (1 x 1024 x 64 bf16: 6.4 us
+// for 5.0). Many clusters take two CTAs of eight warps an SM, as many to a cluster as all find such places: those of a second turn
 // would run by themselves (bf16 forward with 1, 2, 4 and 8 CTAs: 4 x 8192 x 1024 82, 54, 40 and 46 us, 16 x 8192 x 1024 130,
 // 144, 141 and 162; the former with sixteen warps in fp32, backward, 121 for 97).
 template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
@@ -679,7 +680,7 @@ template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_ro
     const long long clusters = (long long)a.B * ((a.C + 32 * VEC - 1) / (32 * VEC));
     if constexpr (RING) {
         constexpr size_t image = 16 * ROWS * 32 * VEC * sizeof(T), totals = sizeof(Run) * 2 * 32;
-        for (int i = 4; i >= 2 && 4 * clusters <= sms && a.N > 64 * ROWS; --i) {
+        for (int i = 4; i >= 3 && 8 * clusters <= sms && a.N > 64 * ROWS; --i) {
             if (8ll * ROWS << i >= a.N) continue;              // half as many would do
             const int n = backward ? resident<recurrence_bwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 6 * image + kMostCtas * totals)
                                    : resident<recurrence_fwd_kernel<T, VEC, ROWS, 16, RING, TIED>>(i, 512, 2 * kStages * image + kMostCtas * totals);

@@ -818,3 +818,18 @@ def test_widths_of_accumulators(package, shape):
     gen = generator(54)
     x, wg, wu = randn(gen, R, K, dtype=BF16), randn(gen, F, K, dtype=BF16, std=K ** -0.5), randn(gen, F, K, dtype=BF16, std=K ** -0.5)
     check_gated(package, x, wg, wu, randn(gen, F, dtype=BF16, std=0.5), None, randn(gen, R, F, dtype=BF16), "gelu")
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("shape", [(3, 2200, 264), (6, 1500, 200), (1, 2049, 64), (1, 1025, 128)], ids=str)
+def test_recurrences_of_some_clusters(package, shape, dtype):
+    """Between the few clusters that take sixteen CTAs and the many: eight CTAs, of sixteen warps or of eight."""
+    gen = generator(55)
+    B, N, C = shape
+    x, gate = (randn(gen, B, N, C, dtype=dtype, mean=m, std=s).requires_grad_() for m, s in ((0.0, 1.0), (2.0, 2.0)))
+    state, dh, dlast = randn(gen, B, C).requires_grad_(), randn(gen, B, N, C, dtype=dtype), randn(gen, B, C)
+    want, bound = recurrence_reference(x, gate, state, dh, dlast, None, False, True)
+    h, last = package.gated_recurrence(x, gate, state, return_state=True)
+    grads = torch.autograd.grad((h, last), (x, gate, state), (dh, dlast))
+    for got, wanted, limit, what in zip((h, last, *grads), want, bound, ("h", "last", "dx", "dgate", "dstate")):
+        within(got, wanted, limit, what)
