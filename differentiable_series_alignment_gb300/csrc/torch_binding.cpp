@@ -653,7 +653,7 @@ Tensor gated_linear(const Tensor& x_, const Tensor& wg_, const Tensor& wu_, cons
     }
     // rows of any stride where features are contiguous; what does not flatten to that is copied
     auto rows = [](const Tensor& t) { return t.stride(1) == 1 || t.size(1) == 1 ? t : t.contiguous(); };
-    const Tensor x = rows(x_.reshape({x_.numel() / K, K})), wg = rows(wg_), wu = rows(wu_);
+    const Tensor x = rows(x_.dim() == 2 ? x_ : x_.reshape({x_.numel() / K, K})), wg = rows(wg_), wu = rows(wu_);
     if (bg.defined()) bg = packed(bg);
     if (bu.defined()) bu = packed(bu);
     const Tensor h = recording({x, wg, wu, bg, bu}) ? GatedLinear::apply(x, wg, wu, given(bg), given(bu), activation)
