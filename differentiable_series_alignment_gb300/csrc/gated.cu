@@ -20,7 +20,7 @@ using gtc::kParts;
 // weights; its eight warps share the sum, 32 of it at a time. In those a lane holds 8 neighbours of its row for both
 // operands, and takes them as the fragments of two products: which of the sum's terms a position stands for does not
 // matter as long as both operands agree. Tiles of 128 rows on the tensor cores would be empty but for these (bf16, 1024 to 4096: 8, 16
-// and 32 rows 3.9, 4.8 and 6.0 us with the weights in the cache, 16 from memory 7.9; by tiles 10.4, 10.4 and 9.5; by the dots below 7.8
+// and 32 rows 3.9, 4.8 and 6.0 us with the weights in the cache; by tiles 10.4, 10.4 and 9.5; by the dots below 7.8
 // and 13.3 for 8 and 16). From memory its 16.8 MB of weights bound it, whose loads all leave at once and only once.
 template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
 template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
