@@ -813,6 +813,8 @@ template <typename F> cudaError_t with_type(int dtype, F f) {
     return f(__half());
 }
 
+constexpr size_t kSlabBytes = 220 * 1024;   // of a CTA's shared memory
+
 Div div_by(int d) { return Div{(unsigned)((0x100000000ull + d - 1) / d), d}; }   // of 1: not multiplied by
 
 long long gcd(long long a, long long b) { return b ? gcd(b, a % b) : a; }
@@ -865,16 +867,18 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     // CTAs of a cluster: until three fit on an SM side by side, or, where there are fewer than two an SM, until a thread has
     // eight rows: a cluster's exchanges take some 2 us (16 x 4096 x 512 bf16 with 1, 2, 4, 8 and 16 CTAs: forward 69, 61,
     // 43, 59 and 107 us, of which this takes 4; backward 118, 112, 123, 85 and 140, of which it takes 8)
+    // What the CTAs exchange has to fit: up to 64 KB for 16 CTAs and 256 groups, but a slab that is all of 2008 channels, each its own group,
+    // takes 32 KB for every CTA.
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
-    while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes &&
+    while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes && bytes(2 * L.ctas).first <= kSlabBytes &&
            ((long long)bytes(L.ctas).first + bytes(L.ctas).second > (L.ctas == 8 ? 112 : 75) * 1024 ||
             (clusters * L.ctas < 2 * sms && p.S >= 16ll * L.ctas * L.lanes)))
         L.ctas *= 2;
     const auto need = bytes(L.ctas);
     L.part = (p.S + L.ctas - 1) / L.ctas;
     L.rounds = (L.part + L.lanes - 1) / L.lanes;
-    L.held = L.vec > 1 && (long long)need.first + need.second <= 220 * 1024;
+    L.held = L.vec > 1 && (long long)need.first + need.second <= (long long)kSlabBytes;
     L.smem = need.first + (L.held ? (size_t)need.second : 0);
     L.groups = L.width / p.cg;
     L.entries = p.cg % L.vec == 0 ? p.cg / L.vec : p.cg;

@@ -833,3 +833,22 @@ def test_recurrences_of_some_clusters(package, shape, dtype):
     grads = torch.autograd.grad((h, last), (x, gate, state), (dh, dlast))
     for got, wanted, limit, what in zip((h, last, *grads), want, bound, ("h", "last", "dx", "dgate", "dstate")):
         within(got, wanted, limit, what)
+
+
+# --- what the shared memory of a cluster's exchange takes
+
+@pytest.mark.parametrize("shape,dtype", [((1, 4096, 2008, 1), BF16), ((2, 2100, 1004, 1), F32), ((1, 300, 1016, 1), F16), ((3, 700, 772, 2), BF16)],
+                         ids=str)
+def test_group_norm_of_many_groups_in_a_slab(package, shape, dtype):
+    """Channels of whose divisors none makes a narrow slab: a slab is all of them, with up to 2008 groups, and what a cluster's
+    CTAs exchange of these has to fit their shared memory."""
+    B, S, G, cg = shape
+    gen = generator(1300 + S)
+    x = randn(gen, B, S, G * cg, dtype=dtype, std=1.5, mean=0.5).requires_grad_()
+    w, b = (randn(gen, G * cg, std=0.3, mean=m).requires_grad_() for m in (1.0, 0.0))
+    dy = randn(gen, B, S, G * cg, dtype=dtype)
+    y = package.group_norm(x, G, w, b, activation="silu")
+    grads = torch.autograd.grad(y, (x, w, b), dy)
+    want, bound = norm_reference(x.detach(), G, w, b, dy, "silu", None, 1e-5, F32)
+    for got, wanted, limit, what in zip((y, *grads), want, bound, ("y", "dx", "dw", "db")):
+        within(got, wanted, limit, what)
