@@ -16,7 +16,7 @@
 // cluster's own barrier also waits for the results that are on their way to memory. One warp folds the CTAs' pairs and hands the
 // state on: read by every warp, they took 900 cycles of shared memory a round.
 //
-// Measured: 16 x 8192 x 1024 bf16 132 us forward (6.1 TB/s) and 255 backward (5.3); 4 such 43 and 78; 4 in fp32 73 and 99 (6.8 TB/s of
+// Measured: 16 x 8192 x 1024 bf16 133 us forward (6.1 TB/s) and 249 backward (5.4); 4 such 43 and 78; 4 in fp32 73 and 99 (6.8 TB/s of
 // a copy's 6.8); 2 x 16383 x 264 fp16 23 and 43. Memory bounds the many; the few by their rounds, which pass the
 // state on one after the other. Loaded by the lanes that use them, 4 x 8192 x 1024 takes 127 and 189 us (ring: 40 and 76).
 #include "activation.cuh"
@@ -86,8 +86,9 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
 }
 
 // a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. EXACT, for
-// results of 32 bits: a is 0 and b 1 from e = 2^120 on. Otherwise e ends at 2^60, where b is 1 and a leaves 1e-18 of a state,
-// and two channels share a reciprocal, which bounded the kernels: 1 / s = t / (s t). A NaN stays.
+// results of 32 bits: a is 0 and b 1 from e = 2^120 on. Otherwise e ends at 2^60, where b is 1 and a leaves 1e-18 of a state.
+// A NaN stays, and in its channel, by a reciprocal for each: two channels that share one, 1 / s = t / (s t), share its rounding and a
+// NaN too. It costs 2 x 16383 x 264 fp16 26.6 us for 24.7 forward, and 16 x 8192 x 1024 bf16 none (133 us; backward 249 for 258).
 __device__ __forceinline__ float min_nan(float v, float most) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
@@ -110,12 +111,7 @@ template <bool EXACT, int VEC> __device__ __forceinline__ void gates(Pair z, Pai
         upk2(mul2(z, pair(-1.4426950408889634f)), t0, t1);
         const Pair e = pk2(ex2(min_nan(t0, 60.f)), VEC > 1 ? ex2(min_nan(t1, 60.f)) : 0.f);
         upk2(add2(e, pair(1.f)), t0, t1);
-        if (VEC > 1) {
-            const float r = reciprocal(t0 * t1);
-            a = mul2(pk2(t1, t0), pk2(r, r));
-        } else {
-            a = pk2(reciprocal(t0), 1.f);
-        }
+        a = pk2(reciprocal(t0), VEC > 1 ? reciprocal(t1) : 1.f);
         b = mul2(e, a);
     }
 }

@@ -852,3 +852,40 @@ def test_group_norm_of_many_groups_in_a_slab(package, shape, dtype):
     want, bound = norm_reference(x.detach(), G, w, b, dy, "silu", None, 1e-5, F32)
     for got, wanted, limit, what in zip((y, *grads), want, bound, ("y", "dx", "dw", "db")):
         within(got, wanted, limit, what)
+
+
+# --- channels by themselves
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(3, 1, 16), (2, 7, 24), (3, 150, 64), (1, 2600, 72), (2, 90, 33), (2, 300, 42)], ids=str)
+@pytest.mark.parametrize("tied", [True, False])
+def test_a_gate_that_is_no_number_stays_in_its_channel(package, shape, dtype, tied):
+    """NaN and infinities in one channel's gate: the others are what they are without, bit for bit. Single samples, few, whole
+    tiles by TMA, and channels that lanes load one by one."""
+    B, N, C = shape
+    gen = generator(2100 + N)
+    x, gate, dh = (randn(gen, B, N, C, dtype=dtype, mean=m) for m in (0.0, 1.0, 0.0))
+    state, dlast = randn(gen, B, C), randn(gen, B, C)
+
+    def run(gate):
+        leaves = [t.detach().clone().requires_grad_() for t in (x, gate, state)]
+        h, last = package.gated_recurrence(*leaves, tied=tied, return_state=True)
+        return [h.detach(), last.detach(), *torch.autograd.grad((h, last), leaves, (dh, dlast))]
+
+    clean = run(gate)
+    for c, value in ((4, math.nan), (5, math.nan), (4, math.inf), (5, -math.inf), (C - 1, math.nan)):
+        for t in {0, N // 2}:
+            spoilt = gate.clone()
+            spoilt[0, t, c] = value
+            got = run(spoilt)
+            mine = torch.zeros(B, C, dtype=torch.bool, device="cuda")
+            mine[0, c] = True
+            for a, b, what in zip(got, clean, ("h", "last", "dx", "dgate", "dstate")):
+                other = ~mine if a.dim() == 2 else (~mine)[:, None].expand_as(a)
+                assert torch.equal(a[other], b[other]), (what, c, value, t)
+            if math.isnan(value):
+                assert torch.isnan(got[0][0, t:, c]).all() and torch.isnan(got[1][0, c]), (c, t)
+                assert torch.equal(got[0][0, :t, c], clean[0][0, :t, c])
+                assert torch.isnan(got[4][0, c]) and torch.isnan(got[3][0, t, c])
+            else:
+                assert not torch.isnan(got[0]).any() and not torch.isnan(got[2]).any()
