@@ -16,7 +16,7 @@
 // cluster's own barrier also waits for the results that are on their way to memory. One warp folds the CTAs' pairs and hands the
 // state on: read by every warp, they took 900 cycles of shared memory a round.
 //
-// Measured: 16 x 8192 x 1024 bf16 133 us forward (6.1 TB/s) and 249 backward (5.4); 4 such 43 and 78; 4 in fp32 73 and 99 (6.8 TB/s of
+// Measured: 16 x 8192 x 1024 bf16 133 us forward (6.1 TB/s) and 257 backward (5.2); 4 such 43 and 80; 4 in fp32 69 and 113 (5.8 and 5.9 TB/s of
 // a copy's 6.8); 2 x 16383 x 264 fp16 23 and 43. Memory bounds the many; the few by their rounds, which pass the
 // state on one after the other. Loaded by the lanes that use them, 4 x 8192 x 1024 takes 127 and 189 us (ring: 40 and 76).
 #include "activation.cuh"
@@ -86,34 +86,20 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
 }
 
 // a = 1 / (1 + e), b = 1 - a = e a with e = exp(-gate): neither loses digits where the other is near 1. EXACT, for
-// results of 32 bits: a is 0 and b 1 from e = 2^120 on. Otherwise e ends at 2^60, where b is 1 and a leaves 1e-18 of a state.
+// results of 32 bits, takes expf. Beyond e = 2^126 a is 0, a closed gate: smaller ones than that are no normal numbers. b is
+// 1 there, where e may be infinite.
 // A NaN stays, and in its channel, by a reciprocal for each: two channels that share one, 1 / s = t / (s t), share its rounding and a
-// NaN too. It costs 2 x 16383 x 264 fp16 26.6 us for 24.7 forward, and 16 x 8192 x 1024 bf16 none (133 us; backward 249 for 258).
-__device__ __forceinline__ float min_nan(float v, float most) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
-    return r;
-}
+// NaN too. It costs 2 x 16383 x 264 fp16 25.6 us for 24.7 forward, and 16 x 8192 x 1024 bf16 none (133 and 257 us).
 template <bool EXACT, int VEC> __device__ __forceinline__ void gates(Pair z, Pair& a, Pair& b) {
-    if constexpr (EXACT) {
-        float g[2], f[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
-        upk2(z, g[0], g[1]);
+    float t[2], e[2] = {}, f[2] = {}, o[2] = {};
+    upk2(EXACT ? z : mul2(z, pair(-1.4426950408889634f)), t[0], t[1]);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float e = expf(-g[k]);
-            const bool closed = g[k] < -83.f;
-            f[k] = closed ? 0.f : reciprocal(1.f + e);
-            o[k] = closed ? 1.f : e * f[k];
-        }
-        a = pk2(f[0], f[1]), b = pk2(o[0], o[1]);
-    } else {
-        float t0, t1;
-        upk2(mul2(z, pair(-1.4426950408889634f)), t0, t1);
-        const Pair e = pk2(ex2(min_nan(t0, 60.f)), VEC > 1 ? ex2(min_nan(t1, 60.f)) : 0.f);
-        upk2(add2(e, pair(1.f)), t0, t1);
-        a = pk2(reciprocal(t0), VEC > 1 ? reciprocal(t1) : 1.f);
-        b = mul2(e, a);
+    for (int k = 0; k < VEC; ++k) {
+        e[k] = EXACT ? expf(-t[k]) : ex2(t[k]);
+        f[k] = reciprocal(1.f + e[k]);
+        o[k] = e[k] > 0x1p125f ? 1.f : e[k] * f[k];
     }
+    a = pk2(f[0], f[1]), b = pk2(o[0], o[1]);
 }
 
 // A batch element's positions, in the order of the recurrence

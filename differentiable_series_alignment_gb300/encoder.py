@@ -139,7 +139,8 @@ def gated_recurrence(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor | 
     (B, C) fp32 is h before the first position, None: zeros. return_state gives (h, state after the last position), fp32:
     a series goes on from it, sample by sample (N = 1) or in pieces of any length. lengths (B,), bounded by N, makes a
     padded batch: positions from lengths[b] on may hold anything, take no part, and are 0 in h and in the gradients.
-    reverse runs from an element's last position to its first. The recurrence is carried in fp32."""
+    reverse runs from an element's last position to its first. The recurrence is carried in fp32; a gate below -87.3 drops
+    the state, one of -inf too where the state is finite."""
     out = _lib.binding().gated_recurrence(x, gate, state, lengths, reverse, tied, return_state)
     return tuple(out) if return_state else out[0]
 

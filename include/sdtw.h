@@ -434,7 +434,8 @@ sdtw_status sdtw_groupnorm_backward(const void* dy, const void* x, const void* w
  * Strides of batch and position (at most 2^23) in elements; channels are contiguous. state (B, C) fp32 contiguous is h before the first
  * position, NULL: zeros. lengths (DEVICE int array (B,), clamped to [0, N]; NULL: N) makes a padded batch: positions
  * from lengths[b] on may hold anything and take no part. reverse != 0 runs from the last of an element's positions to
- * the first. States are carried in fp32. */
+ * the first. States are carried in fp32. Channels do not touch one another: a NaN stays in its own. a_t below
+ * 2^-126 (gates below -87.3) is 0: the state before is dropped, whatever its size. */
 typedef struct {
     const void *x, *gate;
     long long x_stride[2], gate_stride[2];

@@ -889,3 +889,54 @@ def test_a_gate_that_is_no_number_stays_in_its_channel(package, shape, dtype, ti
                 assert torch.isnan(got[4][0, c]) and torch.isnan(got[3][0, t, c])
             else:
                 assert not torch.isnan(got[0]).any() and not torch.isnan(got[2]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("N", [1, 5, 200])
+@pytest.mark.parametrize("C", [16, 15])
+@pytest.mark.parametrize("tied", [True, False])
+def test_gates_at_the_ends_of_their_range(package, dtype, N, C, tied):
+    """Neighbouring channels at opposite extremes. A gate that is wide open keeps the state, one that is closed drops it, however
+    large it is: both factors are as near as their own rounding wherever fp32 has normal numbers (exp(-87) and up)."""
+    values = [math.inf, -math.inf, 200.0, -200.0, -math.inf, 30.0, -50.0, 60.0, -64.0, -200.0, 0.0, -86.0, -85.0, -41.0, -42.0, math.inf][:C]
+    z = torch.tensor(values, device="cuda").to(dtype)
+    gen = generator(2200 + N)
+    gate = z.expand(2, N, C).contiguous().requires_grad_()
+    x = randn(gen, 2, N, C, dtype=dtype).requires_grad_()
+    state = torch.full((2, C), 1e25, device="cuda")
+    state[0] = randn(gen, C)
+    state[1, 11:13] = 1e37
+    state.requires_grad_()
+    dh, dlast = randn(gen, 2, N, C, dtype=dtype), randn(gen, 2, C)
+    h, last = package.gated_recurrence(x, gate, state, tied=tied, return_state=True)
+    dx, dgate, dstate = torch.autograd.grad((h, last), (x, gate, state), (dh, dlast))
+    wide = z.double()
+    a, o = torch.sigmoid(wide), torch.sigmoid(-wide)
+    e = torch.where(torch.isinf(wide), torch.zeros_like(wide), (wide.abs() + 8) * 2.0 ** -22)
+    f, m, d = state.detach().double(), state.detach().double().abs(), torch.zeros(2, C, dtype=torch.float64, device="cuda")
+    want, limit = (torch.empty(2, N, C, dtype=torch.float64, device="cuda") for _ in range(2))
+    floor = 2.0 ** -126
+    for t in range(N):
+        u = (o if tied else 1.0) * x.detach().double()[:, t]
+        d = a * d + a * m * (o * e + 16 * U) + u.abs() * (a * e + 16 * U) + floor * (1 + m)
+        f, m = a * f + u, a * m + u.abs()
+        want[:, t], limit[:, t] = f, d + UT[dtype] * f.abs() + TINY[dtype]
+    top = torch.finfo(dtype).max
+    fits = want.abs() < 0.99 * top                     # fp16 has no 1e25
+    got = torch.where(fits, h.double(), torch.zeros_like(want))
+    within(got, torch.where(fits, want, torch.zeros_like(want)), limit, "h")
+    assert torch.isinf(h[want.abs() > 1.01 * top]).all()
+    within(last, f, d + U * f.abs() + floor, "last")
+    g, md, dd = dlast.double(), dlast.double().abs(), torch.zeros_like(d)
+    for t in reversed(range(N)):
+        g, md = g + dh.double()[:, t], md + dh.double()[:, t].abs()
+        dd = dd + 8 * U * md
+        right = g * (o if tied else 1.0)
+        within(dx[:, t], right, dd * (o if tied else 1.0) + right.abs() * (a * e + 16 * U + UT[dtype]) + TINY[dtype] + floor * md, f"dx {t}")
+        dd = a * dd + a * md * (o * e + 8 * U) + floor * md
+        g, md = a * g, a * md
+    within(dstate, g, dd + U * g.abs() + floor, "dstate")
+    open_ = torch.isinf(wide)
+    assert torch.equal(dgate[..., open_], torch.zeros_like(dgate[..., open_]))
+    closed = wide < -150
+    assert torch.equal(h[..., closed], x[..., closed])
