@@ -62,7 +62,7 @@ struct Params {
     long long ld;
     float* sums;                                       // GRAD, with biases: [M / 32][2 F] column sums of 32 rows
     float* shares;                                     // DX, DW: [cuts][tiles not summed whole][rows of a tile][its columns]
-    const unsigned* top;                               // fp16: bits of the largest |dh|, by which dg and du are scaled
+    const unsigned* top;                               // fp16: what dg and du are scaled by (grads_scale)
     unsigned long long wait_ns;
     int skip;                                          // test hook: nothing is loaded
 };
@@ -384,6 +384,27 @@ template <bool EXACT, bool GRADS> __device__ __forceinline__ void gate_by(int ac
     }
 }
 
+// fp16 keeps dg and du times a power of two, so that as much of what they are ends neither beyond 65504 nor among the subnormal
+// numbers as its range allows. |u| <= |x| |Wu| + |bu| by the rows' norms, |g| alike, |act(g)| <= |g| (a sigmoid's: 1) and the slopes are
+// at most 1.13: |dg| and |du| are below |dh| (1.13 |u| + |act(g)|), which comes to [2^14, 2^15). Values 2^-28 of that still have all their
+// bits. The bound is some sqrt(K) / 4 above what there is. By the largest |dh| alone, brought to [1/4, 1/2), one entry
+// of 2000 among 1e-2 left the other rows' dx 30 times as far off as their rounding.
+// top: bits of the largest |dh|, of the largest squared norm of a row of x, Wg and Wu, of the largest |bg| and |bu|.
+constexpr int kTops = 6;
+__device__ __forceinline__ float grads_scale(const unsigned* top, int activation) {
+    auto at = [&](int i) { return __uint_as_float(top[i]); };
+    const float dh = at(0), g = sqrtf(at(1) * at(2)) + at(4), u = sqrtf(at(1) * at(3)) + at(5);
+    const float most = dh * (1.13f * u + (activation == SDTW_ACT_SIGMOID ? fmaxf(g, 1.f) : g));
+    int exponent = 0;
+    if (most > 0.f && most < INFINITY) {
+        frexpf(most, &exponent);
+        return ldexpf(1.f, 15 - exponent);
+    }
+    if (!(dh > 0.f && dh < INFINITY)) return 1.f;
+    frexpf(dh, &exponent);   // infinities and NaN among the operands: the others' results may still be finite
+    return ldexpf(1.f, -1 - exponent);
+}
+
 // T: the call's type. NB: columns of the accumulator; FWD and GRAD have NB / 2 features of either product in them.
 template <int KIND, typename T, int NB>
 __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_constant__ Params p)
@@ -507,14 +528,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gated_tc_kernel(const __grid_con
     } else {
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t area = ring + Sh::stages * Sh::stage + warp * Sh::area;
-        // dg and du are kept times a power of two that brings the largest |dh| to [1/4, 1/2), so that small upstream gradients
-        // do not end among fp16's subnormal numbers
-        float up = 1.f;
-        if (std::is_same<T, __half>::value && p.top) {
-            const float top = __half2float(__ushort_as_half((unsigned short)*p.top));
-            int exponent = 0;
-            if (top > 0.f && top < INFINITY) frexpf(top, &exponent), up = ldexpf(1.f, -1 - exponent);
-        }
+        const float up = std::is_same<T, __half>::value && p.top ? grads_scale(p.top, p.activation) : 1.f;
         const float down = 1.f / up;
         // 16-bit pieces of dh have half of the area to themselves; fp32's are taken before results are put there
         const uint32_t dh_area = sizeof(T) == 2 ? area + 2048 : area;

@@ -940,3 +940,60 @@ def test_gates_at_the_ends_of_their_range(package, dtype, N, C, tied):
     assert torch.equal(dgate[..., open_], torch.zeros_like(dgate[..., open_]))
     closed = wide < -150
     assert torch.equal(h[..., closed], x[..., closed])
+
+
+# --- fp16 gradients over a wide range
+
+def test_large_gradients_of_some_rows_leave_the_others_exact(package):
+    """fp16: dg and du are scaled by one power of two. A row of dh that is 2^18 times the others must not push theirs below fp16's
+    normal numbers: each row's dx is as near as in test_results_are_as_near_as_their_rounding."""
+    gen = generator(25)
+    R, K, F = 600, 256, 384
+    x, wg, wu = randn(gen, R, K, dtype=F16), *(randn(gen, F, K, dtype=F16, std=K ** -0.5) for _ in range(2))
+    for large, at in ((2000.0, (7, 11)), (30000.0, (7, slice(0, 2))), (0.0, (0, 0))):
+        dh = randn(gen, R, F, dtype=F16, std=1e-2)
+        dh[at] = large
+        want, _ = gated_reference(x, wg, wu, None, None, dh, "silu")
+        leaf = x.detach().requires_grad_()
+        (dx,) = torch.autograd.grad(package.gated_linear(leaf, wg, wu), leaf, dh)
+        others = torch.arange(R, device="cuda") != at[0]
+        error, own = (((t.double() - want[1])[others] ** 2).mean().sqrt() for t in (dx, want[1].to(F16)))
+        assert error <= 1.6 * own, (large, float(error / own))
+        if large < 4000:                                # what is off by less than a step of fp16 unscaled
+            check_gated(package, x, wg, wu, None, None, dh, "silu")
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "relu", "sigmoid"])
+def test_fp16_gradients_do_not_overflow_on_their_way(package, name):
+    """dg and du beyond 65504 whose products with small weights are not: dx is finite, and right."""
+    gen = generator(26)
+    R, K, F = 100, 64, 96
+    x = randn(gen, R, K, dtype=F16, std=8.0)
+    wg, wu = randn(gen, F, K, dtype=F16, std=2.0 ** -9), randn(gen, F, K, dtype=F16, std=K ** -0.5)
+    bg, bu = randn(gen, F, dtype=F16), randn(gen, F, dtype=F16)
+    wu[:5] *= 8
+    dh = randn(gen, R, F, dtype=F16, std=3e-2)
+    dh[:, :5] = 3000.0                                  # u of these: up to 200
+    want, bound = gated_reference(x, wg, wu, bg, bu, dh, name)
+    assert float((dh.double()[:, :5] * (x.double() @ wu.double().T + bu.double())[:, :5]).abs().max()) > 4 * 65504
+    leaf = x.detach().requires_grad_()
+    (dx,) = torch.autograd.grad(package.gated_linear(leaf, wg, wu, bg, bu, activation=name), leaf, dh)
+    keep = want[1].abs() < 65000
+    assert float(keep.double().mean()) > 0.3
+    within(torch.where(keep, dx.double(), 0.0), torch.where(keep, want[1], 0.0), bound[1], "dx")
+
+
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_fp16_rows_that_are_no_numbers_leave_the_others(package, value):
+    """A row of x or of a weight that is not finite has no norm to scale dg and du by; the other rows' dx are right all the same."""
+    gen = generator(27)
+    R, K, F = 150, 64, 96
+    x, wg, wu = randn(gen, R, K, dtype=F16), *(randn(gen, F, K, dtype=F16, std=K ** -0.5) for _ in range(2))
+    dh = randn(gen, R, F, dtype=F16, std=1e-2)
+    want, bound = gated_reference(x, wg, wu, None, None, dh, "silu")
+    x[3, 5] = value
+    leaf = x.detach().requires_grad_()
+    (dx,) = torch.autograd.grad(package.gated_linear(leaf, wg, wu), leaf, dh)
+    others = torch.arange(R, device="cuda") != 3
+    within(dx[others], want[1][others], bound[1][others], "dx")
+    assert not torch.isfinite(dx[3]).all()
