@@ -52,10 +52,11 @@ template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_k
     const sdtw_gated& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, at = (lane & 3) * 8, f0 = blockIdx.x * 16;
     const int R = (int)a.R;
-    // volatile: in this order, before the products
+    // volatile: in this order, before the products. Not by the read-only path (ld.global.nc): this kernel begins before the one in front of
+    // it has ended, which may be writing these operands.
     auto load = [&](const void* base, long long stride, int r, int rows, int k) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
                      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
                      : "l"(static_cast<const T*>(base) + r * stride + k), "r"((int)(r < rows && k < a.K)));
         return v;

@@ -997,3 +997,49 @@ def test_fp16_rows_that_are_no_numbers_leave_the_others(package, value):
     others = torch.arange(R, device="cuda") != 3
     within(dx[others], want[1][others], bound[1][others], "dx")
     assert not torch.isfinite(dx[3]).all()
+
+
+# --- few rows, launched behind what comes before them
+
+def test_few_rows_behind_other_work(package):
+    """The kernels of few rows begin before what is in front of them on the stream has ended: behind a copy, behind a kernel that
+    rewrites the weights or the rows in place, on several streams at once, and in graphs."""
+    gen = generator(61)
+    for dtype, K in ((BF16, 1024), (F16, 250), (F32, 512)):
+        x = [randn(gen, 16, K, dtype=dtype) for _ in range(4)]
+        w = [randn(gen, 512, K, dtype=dtype, std=K ** -0.5) for _ in range(4)]
+        want = [[package.gated_linear(a, b, b).clone() for b in w] for a in x]
+        torch.cuda.synchronize()
+        a, b = x[0].clone(), w[0].clone()
+        for turn in range(40):
+            i, j = turn % 4, turn // 4 % 4
+            a.copy_(x[i])
+            if turn % 2:
+                b.copy_(w[j])
+            else:
+                b.zero_()
+                b.add_(w[j])
+            assert torch.equal(package.gated_linear(a, b, b), want[i][j]), (dtype, turn)
+        streams, got = [torch.cuda.Stream() for _ in range(4)], [[] for _ in range(4)]
+        torch.cuda.synchronize()
+        for turn in range(5):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    own = w[i] * 1.0
+                    own.add_(0)
+                    got[i].append(package.gated_linear(x[(i + turn) % 4], own, own))
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[i][t], want[(i + t) % 4][i]) for i in range(4) for t in range(5))
+        # a graph: a copy in front of a call, the call, another on its result
+        a, b, graph = x[0].clone(), w[0].clone(), torch.cuda.CUDAGraph()
+        square = randn(gen, 512, 512, dtype=dtype, std=0.05)
+        source = x[0].clone()
+        with torch.cuda.graph(graph):
+            a.copy_(source)
+            h = package.gated_linear(a, b, b)
+            out = package.gated_linear(h, square, square)
+        for i in (2, 1, 3):
+            source.copy_(x[i])
+            b.copy_(w[i])
+            graph.replay()
+            assert torch.equal(h, want[i][i]) and torch.equal(out, package.gated_linear(want[i][i], square, square))
