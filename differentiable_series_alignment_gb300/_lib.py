@@ -440,8 +440,8 @@ def sdtw_last_device_status(ws, stream=None) -> int:
     return int(load().sdtw_last_device_status(_ptr(ws), _stream(stream)))
 
 
-def sdtw_debug_set_wait(seconds: float, skip_publish: bool = False):
-    load().sdtw_debug_set_wait(float(seconds), 1 if skip_publish else 0)
+def sdtw_debug_set_wait(seconds: float, skip_publish: int = 0):
+    load().sdtw_debug_set_wait(float(seconds), int(skip_publish))
 
 
 def sdtw_debug_set_options(warps_fwd: int = 0, warps_bwd: int = 0, dist_simt: bool = False,

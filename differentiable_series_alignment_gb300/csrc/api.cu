@@ -1115,7 +1115,7 @@ const char* sdtw_status_string(sdtw_status s)
 void sdtw_debug_set_wait(double seconds, int skip_publish)
 {
     g_wait_ns = (seconds > 0.0) ? (unsigned long long)(seconds * 1e9) : kDefaultWaitNs;
-    g_skip_publish = skip_publish ? 1 : 0;
+    g_skip_publish = skip_publish == 2 ? 2 : skip_publish ? 1 : 0;
 }
 
 sdtw_status sdtw_debug_exp2_neg(const float* x, float* out, int n, void* stream)

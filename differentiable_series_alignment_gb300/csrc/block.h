@@ -29,7 +29,7 @@ struct RecurrenceParams {
     void *dx, *dgate;
     float* dstate;
     unsigned long long wait_ns;   // of a wait within a cluster
-    int skip;                     // test hook: a cluster's first CTA sends nothing
+    int skip;                     // test hook, of a cluster's first CTA. 1: it sends nothing; 2: one of its warps alone gives up a wait
 };
 cudaError_t launch_recurrence_forward(const RecurrenceParams& p, int sms, cudaStream_t s);
 cudaError_t launch_recurrence_backward(const RecurrenceParams& p, int sms, cudaStream_t s);

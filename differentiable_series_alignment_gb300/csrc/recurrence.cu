@@ -136,17 +136,30 @@ __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Bounded: false, and the status word set, when it ran out.
-__device__ __forceinline__ bool wait_arrived(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+// Bounded: false, the status word set and the CTA's `late` too, when it ran out. Who gave up a wait may have read what was not there, and
+// others go on from it: at its end the cluster makes NaN of all its results.
+__device__ __forceinline__ bool wait_arrived(uint32_t bar, uint32_t parity, unsigned long long limit_ns, int& late) {
     if (arrived(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     while (!arrived(bar, parity))
         if (global_ns() - t0 > limit_ns) {
             atomicOr(&g_status, kStatusTimeout);
+            *static_cast<volatile int*>(&late) = 1;
             return false;
         }
     return true;
 }
+// All threads of the cluster, at its end: no store may come to a CTA that has ended. Whether one of them was late.
+__device__ __forceinline__ bool any_late(int& late, int ctas) {
+    __syncthreads();
+    if (ctas > 1) {
+        if (*static_cast<volatile int*>(&late) && (int)threadIdx.x < ctas)
+            asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(in_cta((uint32_t)__cvta_generic_to_shared(&late), (int)threadIdx.x)) : "memory");
+        cluster_sync();
+    }
+    return *static_cast<volatile int*>(&late) != 0;
+}
+__device__ __forceinline__ Pair not_a_number() { return pk2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)); }
 
 struct alignas(16) Run {   // h -> a h + h0
     Pair a, h;
@@ -209,7 +222,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     __shared__ Run run[WARPS][32];
     __shared__ Pair s_in[32];                             // states before the CTA's positions
-    __shared__ uint64_t s_bar[2 + kStages];               // of the exchange, by turns; of the stages
+    __shared__ uint64_t s_bar[2 + kStages + 1];           // of the exchange, by turns; of the stages; one that nothing arrives at
+    __shared__ int s_late;
     extern __shared__ __align__(128) unsigned char ring[];   // [kStages][x, gate][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + kStages * 2 * image);
     const sdtw_recurrence& a = p.a;
@@ -227,7 +241,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
     const T* gate = static_cast<const T*>(a.gate) + b * a.gate_stride[0];
     T* out = static_cast<T*>(p.h) + (long long)b * a.N * a.C + c;
     const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
-    if (threadIdx.x < 2 + kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    if (threadIdx.x == 0) s_late = 0;
+    if (threadIdx.x < 2 + kStages + 1) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = a.state && on ? load_f32<VEC>(a.state + bc) : pair(0.f);
     const int t0 = rank * WARPS * ROWS;                  // the CTA's first position
@@ -256,6 +271,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
         send(0);
     }
     if (ctas > 1) cluster_sync();                         // the others have begun, with barriers
+    if (RING && p.skip == 2 && rank == 0 && warp == 1) wait_arrived(bars + 8 * (2 + kStages), 0, p.wait_ns, s_late);
     bool ok = true;
     for (int round = 0; round < rounds; ++round, t += per) {
         const int there = el.len - t, turn = round & 1;
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
             if (threadIdx.x == 0) stored();               // those of the round before it have left theirs, the next to be filled
             put_out(round - 1);
             send(round + 1);
-            if (!wait_arrived(bars + 8 * (2 + round % kStages), (uint32_t)(round / kStages) & 1, p.wait_ns)) ok = false;
+            wait_arrived(bars + 8 * (2 + round % kStages), (uint32_t)(round / kStages) & 1, p.wait_ns, s_late);
             if (there < ROWS) {
                 blank<T, VEC, ROWS>(mine, line, there, 0);
                 blank<T, VEC, ROWS>(mine + image, line, there, open_bits<T>());
@@ -309,10 +325,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
             if (ctas > 1) {
                 const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
                 if (lane == 0) expect(bar, ctas * 512);
-                if (!(p.skip && rank == 0))
+                if (!(p.skip == 1 && rank == 0))
                     for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_h);
-                if (!wait_arrived(bar, (uint32_t)(round >> 1) & 1, ok ? p.wait_ns : 0)) ok = false;
-                if (!ok) carry = pair(__int_as_float(0x7fffffff));
+                if (!wait_arrived(bar, (uint32_t)(round >> 1) & 1, ok ? p.wait_ns : 0, s_late)) ok = false;
                 for (int k0 = 0; k0 < ctas; k0 += 4) {
                     Run r[4];
 #pragma unroll
@@ -324,7 +339,6 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
                     }
                 }
             } else {
-                if (!ok) in = pair(__int_as_float(0x7fffffff));
                 carry = fma2(all_a, in, all_h);
             }
             s_in[lane] = in;
@@ -364,7 +378,18 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_fwd_kernel(
         put_out(rounds - 1);
         if (threadIdx.x == 0) stored();
     }
-    if (ctas > 1) cluster_sync();                         // no store may come to a CTA that has ended
+    if (any_late(s_late, ctas)) {
+        if (RING && threadIdx.x == 0) {   // loads on their way come before the CTA ends, and results are written, not only read
+            for (int k = max(0, rounds - kStages); k < rounds; ++k) wait_arrived(bars + 8 * (2 + k % kStages), (uint32_t)(k / kStages) & 1, p.wait_ns, s_late);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        carry = not_a_number();
+        for (t = t0 + warp * ROWS; on && t < el.len; t += per) {
+            if (p.kept && t % kStep == 0) store_f32<VEC>(p.kept + ((long long)b * steps + t / kStep) * a.C + c, carry);
+            for (int i = 0; i < min(ROWS, el.len - t); ++i) store<T, VEC>(out + (long long)el.row(t + i) * a.C, carry);
+        }
+    }
     if (!on) return;
     clear<T, VEC>(out, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
     if (p.last && rank == 0 && warp == WARPS - 1) store_f32<VEC>(p.last + bc, carry);
@@ -376,7 +401,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     constexpr int bytes = 32 * VEC * sizeof(T), image = RING ? WARPS * ROWS * bytes : 0;
     __shared__ Run run[WARPS][32];
     __shared__ Pair back[WARPS][32], s_in[32];            // s_in: what the positions after the CTA's hand back
-    __shared__ uint64_t s_bar[2 + 2];
+    __shared__ uint64_t s_bar[2 + 2 + 1];                 // as in the forward pass
+    __shared__ int s_late;
     extern __shared__ __align__(128) unsigned char ring[];   // [2][x, gate, dh][WARPS ROWS][32 VEC], then [2][ctas][32] Runs
     Run* total = reinterpret_cast<Run*>(ring + 2 * 3 * image);
     static_assert(WARPS * ROWS % kStep == 0 || kStep % (WARPS * ROWS) == 0, "kept states at CTAs' first positions");
@@ -396,7 +422,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     const T* dh = static_cast<const T*>(p.dh) + base;
     T *dx = static_cast<T*>(p.dx) + base + c, *dgate = static_cast<T*>(p.dgate) + base + c;
     const uint32_t bars = (uint32_t)__cvta_generic_to_shared(s_bar);
-    if (threadIdx.x < 4) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
+    if (threadIdx.x == 0) s_late = 0;
+    if (threadIdx.x < 5) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * threadIdx.x) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Pair carry = p.dlast && on ? load_f32<VEC>(p.dlast + bc) : pair(0.f);
     const int t0 = rank * WARPS * ROWS;
@@ -422,6 +449,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
     }
     Pair state = kept(rounds - 1);
     if (ctas > 1) cluster_sync();
+    if (RING && p.skip == 2 && rank == 0 && warp == 1) wait_arrived(bars + 8 * 4, 0, p.wait_ns, s_late);
     bool ok = true;
     int turn = 0, phase = 0;
     for (int round = rounds - 1; round >= 0; --round) {
@@ -431,7 +459,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
         if constexpr (RING) {
             __syncthreads();
             send(round - 1);
-            if (!wait_arrived(bars + 8 * (2 + (round & 1)), (uint32_t)((rounds - 1 - round) >> 1) & 1, p.wait_ns)) ok = false;
+            wait_arrived(bars + 8 * (2 + (round & 1)), (uint32_t)((rounds - 1 - round) >> 1) & 1, p.wait_ns, s_late);
             if (el.len - t < ROWS) {
                 blank<T, VEC, ROWS>(mine, line, el.len - t, 0);
                 blank<T, VEC, ROWS>(mine + image, line, el.len - t, open_bits<T>());
@@ -478,10 +506,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
             if (ctas > 1) {
                 const uint32_t bar = bars + 8 * turn, slot = (uint32_t)__cvta_generic_to_shared(&total[(turn * ctas + rank) * 32 + lane]);
                 if (lane == 0) expect(bar, ctas * 512);
-                if (!(p.skip && rank == 0))
+                if (!(p.skip == 1 && rank == 0))
                     for (int k = 0; k < ctas; ++k) send_pairs(in_cta(slot, k), in_cta(bar, k), all_a, all_r);
-                if (!wait_arrived(bar, (uint32_t)phase, ok ? p.wait_ns : 0)) ok = false;
-                if (!ok) carry = pair(__int_as_float(0x7fffffff));
+                if (!wait_arrived(bar, (uint32_t)phase, ok ? p.wait_ns : 0, s_late)) ok = false;
                 for (int k0 = ctas - 1; k0 >= 0; k0 -= 4) {
                     Run q[4];
 #pragma unroll
@@ -493,7 +520,6 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
                     }
                 }
             } else {
-                if (!ok) in = pair(__int_as_float(0x7fffffff));
                 carry = fma2(all_a, in, all_r);
             }
             s_in[lane] = in;
@@ -542,7 +568,17 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
             clear<T, VEC>(dgate, a.C, max(t, el.len), min(t + ROWS, a.N), 0, 1);
         }
     }
-    if (ctas > 1) cluster_sync();
+    if (any_late(s_late, ctas)) {
+        if (RING && threadIdx.x == 0)
+            for (int k = min(rounds, 2) - 1; k >= 0; --k) wait_arrived(bars + 8 * (2 + (k & 1)), (uint32_t)((rounds - 1 - k) >> 1) & 1, p.wait_ns, s_late);
+        carry = not_a_number();
+        for (int t = t0 + warp * ROWS; on && t < el.len; t += per)
+            for (int i = 0; i < min(ROWS, el.len - t); ++i) {
+                const long long at = (long long)el.row(t + i) * a.C;
+                store<T, VEC>(dx + at, carry);
+                store<T, VEC>(dgate + at, carry);
+            }
+    }
     if (!on) return;
     clear<T, VEC>(dx, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);
     clear<T, VEC>(dgate, a.C, rounds * per, a.N, rank * WARPS + warp, ctas * WARPS);

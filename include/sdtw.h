@@ -281,8 +281,8 @@ const char* sdtw_status_string(sdtw_status s);
  * tiles run out of time and the call reports SDTW_ERR_TIMEOUT through
  * sdtw_last_device_status. The next attention on the tensor cores takes it too: 1
  * withholds all that its kernel would load, 2 lets a single chain of waits run out,
- * reported by sdtw_encoder_status. So does the next recurrence (what a cluster's first
- * CTA would send to the others) or gated unit of more than 32 rows or backward (all
+ * reported by sdtw_encoder_status. So does the next recurrence (1: what a cluster's first
+ * CTA would send to the others; 2: a wait of one warp for loads) or gated unit of more than 32 rows or backward (all
  * that its first products would load). No GPU fault is involved. Process-wide. */
 void sdtw_debug_set_wait(double seconds, int skip_publish);
 

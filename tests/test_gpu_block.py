@@ -1043,3 +1043,40 @@ def test_few_rows_behind_other_work(package):
             b.copy_(w[i])
             graph.replay()
             assert torch.equal(h, want[i][i]) and torch.equal(out, package.gated_linear(want[i][i], square, square))
+
+
+@pytest.mark.parametrize("shape", [(1, 2000, 64), (400, 70, 64), (2, 5000, 64)], ids=str)
+@pytest.mark.parametrize("which", [1, 2], ids=["exchange", "loads"])
+def test_recurrence_waits_that_run_out(package, shape, which):
+    """Whoever gives up a wait, the warp that folds the others' runs or one that does not: all results of the cluster are NaN, forward
+    and backward, the status says so, and the next call is right again."""
+    B, N, C = shape
+    if B == 400 and which == 1:
+        pytest.skip("one CTA sends nothing")
+    gen = generator(71)
+    lengths = torch.full((B,), N - 1, device="cuda", dtype=torch.int32)
+    x, gate = (randn(gen, *shape, dtype=BF16, mean=m).requires_grad_() for m in (0.0, 1.0))
+    state, dh, dlast = randn(gen, B, C).requires_grad_(), randn(gen, *shape, dtype=BF16), randn(gen, B, C)
+    run = lambda: package.gated_recurrence(x, gate, state, lengths=lengths, return_state=True)  # noqa: E731
+    back = lambda out: torch.autograd.grad(out, (x, gate, state), (dh, dlast))  # noqa: E731
+    want = run()
+    grads = back(want)
+    assert package.sdtw_encoder_status() == 0
+    try:
+        for forward in (True, False):
+            out = None if forward else run()
+            torch.cuda.synchronize()
+            package.sdtw_debug_set_wait(0.02, which)
+            got = run() if forward else back(out)
+            assert package.sdtw_encoder_status() == 7 and package.sdtw_encoder_status() == 0
+            package.sdtw_debug_set_wait(0.0, 0)
+            for t in got:
+                t = t.detach()
+                if t.dim() == 3:
+                    assert torch.equal(t[:, N - 1:], torch.zeros_like(t[:, N - 1:]))
+                    t = t[:, :N - 1]
+                assert torch.isnan(t).all()
+    finally:
+        package.sdtw_debug_set_wait(0.0, 0)
+    again = run()
+    assert all(torch.equal(a, b) for a, b in zip((*again, *back(again)), (*want, *grads)))
