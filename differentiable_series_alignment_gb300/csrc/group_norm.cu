@@ -840,12 +840,8 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     L.width = (int)whole;
     // at least 64 bytes a row, or all channels: wider slabs take larger clusters (128 bytes: backward of 16 x 4096 x 512 bf16
     // 98 us for 88), rows of 32 bytes 96
-    for (long long j = 1; whole * j <= p.C; ++j)
-        if (p.C % (whole * j) == 0) {
-            if (j > 1 && whole * j > kThreads * L.vec) break;
-            L.width = (int)(whole * j);
-            if (L.width * size >= 64) break;
-        }
+    for (long long j = 1; whole * j <= std::min(p.C, kThreads * L.vec) && L.width * size < 64; ++j)
+        if (p.C % (whole * j) == 0) L.width = (int)(whole * j);
     L.packs = L.width / L.vec;
     if (L.packs > kThreads) return L;
     L.slabs = p.C / L.width;

@@ -105,3 +105,12 @@ def test_gated_refuses_missing_results_and_workspaces(lib):
     assert back(dh=None) == ARG and back(dx=None) == 0
     assert lib.sdtw_gated_workspace_bytes(p, True) > 0
     assert back(ws=None) == WORKSPACE and back(ws=0x100010) == WORKSPACE and back(n=64) == WORKSPACE
+
+
+def test_slabs_of_a_prime_number_of_channels_are_chosen_quickly(lib):
+    """The width of a slab is looked for among those that a CTA can have, not up to the channels, by which 100 calls took 12 s."""
+    import time
+    start = time.monotonic()
+    for _ in range(100):
+        assert lib.load().sdtw_groupnorm_workspace_bytes(1, 2, 16777213, 16777213, 1, 1) == 2 * 16777213 * 4
+    assert time.monotonic() - start < 2.0
