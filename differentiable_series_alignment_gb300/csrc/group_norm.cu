@@ -238,7 +238,7 @@ struct Place {
         on = item < L.items && b < p.B;
         len = !on ? 0 : p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S;
         first = rank * L.part + row;
-        last = on ? min(p.S, (rank + 1) * L.part) : 0;
+        last = on ? (int)min((long long)p.S, (rank + 1ll) * L.part) : 0;
         at = ((long long)b * p.S + first) * p.C + slab * L.width + pack * L.vec;
     }
 };
@@ -857,7 +857,7 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     const size_t sums = (2 * (size_t)L.width + (size_t)(one ? 1 : arrays) * kThreads * L.vec + 2 * L.items * (L.width / p.cg)) * sizeof(float);
     auto bytes = [&](int ctas) {
         const size_t exchange = ctas > 1 ? (size_t)4 * ctas * (L.width / p.cg) * sizeof(float) : 0;
-        const long long rounds = ((p.S + ctas - 1) / ctas + L.lanes - 1) / L.lanes;
+        const long long rounds = ((p.S - 1ll + ctas) / ctas + L.lanes - 1) / L.lanes;
         return std::pair<size_t, long long>(sums + exchange, rounds * kThreads * 16 * arrays);
     };
     // CTAs of a cluster: until three fit on an SM side by side, or, where there are fewer than two an SM, until a thread has
@@ -867,13 +867,13 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     // takes 32 KB for every CTA.
     L.ctas = 1;
     const long long clusters = (long long)((p.B + L.items - 1) / L.items) * L.slabs;
-    while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2 * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes && bytes(2 * L.ctas).first <= kSlabBytes &&
+    while (L.ctas < kMostCtas && L.items == 1 && (p.S + 2ll * L.ctas - 1) / (2 * L.ctas) >= 2 * L.lanes && bytes(2 * L.ctas).first <= kSlabBytes &&
            ((long long)bytes(L.ctas).first + bytes(L.ctas).second > (L.ctas == 8 ? 112 : 75) * 1024 ||
             (clusters * L.ctas < 2 * sms && p.S >= 16ll * L.ctas * L.lanes)))
         L.ctas *= 2;
     const auto need = bytes(L.ctas);
-    L.part = (p.S + L.ctas - 1) / L.ctas;
-    L.rounds = (L.part + L.lanes - 1) / L.lanes;
+    L.part = (int)((p.S - 1ll + L.ctas) / L.ctas);
+    L.rounds = (int)((L.part + L.lanes - 1ll) / L.lanes);
     L.held = L.vec > 1 && (long long)need.first + need.second <= (long long)kSlabBytes;
     L.smem = need.first + (L.held ? (size_t)need.second : 0);
     L.groups = L.width / p.cg;

@@ -1080,3 +1080,19 @@ def test_recurrence_waits_that_run_out(package, shape, which):
         package.sdtw_debug_set_wait(0.0, 0)
     again = run()
     assert all(torch.equal(a, b) for a, b in zip((*again, *back(again)), (*want, *grads)))
+
+
+def test_group_norm_of_as_many_positions_as_32_bits_count(package):
+    """One channel over 2^31 - 1 positions, all 0 but for some at both ends and in the middle: the mean is 0 to a part in 10^7 of the
+    deviation, and what is not 0 is where it was."""
+    S = 2 ** 31 - 1
+    x = torch.zeros(1, S, 1, device="cuda", dtype=BF16)
+    at = torch.tensor([0, 1, S // 2, S - 17, S - 16, S - 2, S - 1], device="cuda")
+    x[0, at, 0] = torch.tensor([1.0, -2.0, 3.0, 4.0, -5.0, 6.0, -7.0], device="cuda", dtype=BF16)
+    y = package.group_norm(x, 1, eps=1.0)
+    assert torch.equal(y[0, at, 0], x[0, at, 0])              # a variance of 7e-8 beside eps = 1
+    rest = y.view(-1)
+    assert all(float(c.abs().sum(dtype=torch.float64)) <= 28.1 for c in rest.split(1 << 29))
+    assert int((rest.abs() > 1e-6).sum()) == 7
+    del x, y, rest
+    torch.cuda.empty_cache()
