@@ -154,7 +154,8 @@ def gated_linear(x: torch.Tensor, gate_weight: torch.Tensor, up_weight: torch.Te
     Neither product is stored: the backward pass computes both again. Sums are fp32; in bf16 and fp16 the
     gradients of the two products are rounded to the type before the products that consume them: gradients are some 1.4
     times as far from exact as their own rounding. In fp16 they are scaled by one power of two, which keeps all bits of values down
-    to 2^-28 of a bound of the largest one, some sqrt(K) / 4 times that. Products of more than 32 rows of float32 take its values in three parts,
-    of which infinities and values beyond 3.38e38 give NaN."""
+    to 2^-28 of a bound of the largest one, some sqrt(K) / 4 times that. float32 values are taken in three
+    parts by forward passes of more than 32 rows, and by backward passes of any number, which compute the forward products again:
+    infinities and values beyond 3.396e38 give NaN there, where a forward pass of at most 32 rows takes them as they are."""
     code = _activation(activation, ("silu", "gelu", "relu", "sigmoid"))
     return _lib.binding().gated_linear(x, gate_weight, up_weight, gate_bias, up_bias, code)

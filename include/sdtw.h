@@ -462,7 +462,8 @@ sdtw_status sdtw_recurrence_backward(const sdtw_recurrence* a, const float* kept
 /* A gated linear unit, the first half of a gated feed-forward block: x (R, K), gate_weight and up_weight (F, K) with
  * contiguous features and any row strides (in elements), gate_bias and up_bias (F,) or NULL, all of type `dtype`,
  *   h = act(x gate_weight^T + gate_bias) * (x up_weight^T + up_bias)   (R, F).
- * activation is SILU, GELU, RELU or SIGMOID. */
+ * activation is SILU, GELU, RELU or SIGMOID. Values of SDTW_F32 are taken in three bf16 parts by forward passes of more than 32
+ * rows and by all backward passes: infinities and values beyond 3.396e38 give NaN there. */
 typedef struct {
     const void *x, *gate_weight, *up_weight, *gate_bias, *up_bias;
     long long x_stride, gate_stride, up_stride;

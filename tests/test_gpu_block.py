@@ -1096,3 +1096,29 @@ def test_group_norm_of_as_many_positions_as_32_bits_count(package):
     assert int((rest.abs() > 1e-6).sum()) == 7
     del x, y, rest
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("value", [math.inf, 3.395e38, 3.4e38])
+def test_fp32_values_without_three_parts(package, value):
+    """A forward pass of at most 32 rows of fp32 takes a weight as it is. More rows, and every backward pass, take it in three bf16 parts,
+    which infinities and what rounds to one in bf16, from (2 - 2^-8) 2^127 = 3.3961e38 on, have not: NaN where such a value takes
+    part, and all else right."""
+    gen = generator(28)
+    R, K, F = 8, 64, 40
+    x, wg, wu, dh = randn(gen, R, K), *(randn(gen, F, K, std=K ** -0.5) for _ in range(2)), randn(gen, R, F)
+    x[:, 3] = 2.0 ** -20
+    want, bound = gated_reference(x, wg, wu, None, None, dh, "silu")
+    wu[5, 3] = value
+    x, wg, wu = (t.requires_grad_() for t in (x, wg, wu))
+    h = package.gated_linear(x, wg, wu)
+    others = torch.arange(F, device="cuda") != 5
+    within(h[:, others], want[0][:, others], bound[0][:, others], "h")
+    assert not torch.isnan(h).any() and torch.isinf(h[:, 5]).all() == math.isinf(value)
+    dx, dwg, dwu = torch.autograd.grad(h, (x, wg, wu), dh)
+    none = value >= (2 - 2.0 ** -8) * 2.0 ** 127
+    assert torch.isnan(dx).all() if none else not torch.isnan(dx).any()
+    assert torch.isnan(dwg[5]).all() if none else torch.isfinite(dwg[5]).all()
+    within(dwg[others], want[2][others], bound[2][others], "dgate_weight")
+    within(dwu, want[3], bound[3], "dup_weight")                # needs g alone
+    many = package.gated_linear(x.repeat(5, 1), wg, wu)
+    assert torch.isnan(many[:, 5]).all() == none and not torch.isnan(many[:, others]).any()
