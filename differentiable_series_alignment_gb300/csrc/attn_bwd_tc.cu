@@ -210,7 +210,8 @@ __device__ __forceinline__ void dkv_cta(const AttnParams& p, const Maps& maps, c
             }
             // dV takes dO, dK takes Q
             const uint32_t rows_img = ring + (uint32_t)pe * 2 * Sh::tile + (grad ? 0 : Sh::tile);
-            wait_warp(ok, ready, (uint32_t)(i & 1), p.skip == 2 && i + 1 == tiles ? 0 : p.wait_ns, late);   // (test hook)
+            if (p.skip == 2 && i + 1 == tiles) late.set(), ok = false;   // test hook: gives up
+            wait_warp(ok, ready, (uint32_t)(i & 1), p.wait_ns, late);
             // dK and the next dP^T would interleave with the next S^T, which the warps wait for first. Only
             // the order in the queue hangs on this, so it waits a while and no longer.
             if (!APART && grad && i + 1 < tiles)
@@ -462,7 +463,8 @@ __device__ __forceinline__ void dq_cta(const AttnParams& p, const Maps& maps, co
                     upstream();
                 }
                 const uint32_t kimg = ring + (uint32_t)e_k * Sh::tile;
-                wait_warp(ok, smem_u32(&s_ds[j & 1]), (uint32_t)((j >> 1) & 1), p.skip == 2 && j + 1 == tiles ? 0 : p.wait_ns, late);
+                if (p.skip == 2 && j + 1 == tiles) late.set(), ok = false;
+                wait_warp(ok, smem_u32(&s_ds[j & 1]), (uint32_t)((j >> 1) & 1), p.wait_ns, late);
                 clear_tail(j, kimg);
                 fence_after_sync();
                 if (ok && elect_one()) {
