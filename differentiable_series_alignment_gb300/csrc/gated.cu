@@ -20,7 +20,7 @@ using gtc::kParts;
 // weights; its eight warps share the sum, 32 of it at a time. In those a lane holds 8 neighbours of its row for both
 // operands, and takes them as the fragments of two products: which of the sum's terms a position stands for does not
 // matter as long as both operands agree. Tiles of 128 rows on the tensor cores would be empty but for these (bf16, 1024 to 4096: 8, 16
-// and 32 rows 3.9, 4.8 and 6.0 us with the weights in the cache; by tiles 10.4, 10.4 and 9.5; by the dots below 7.8
+// and 32 rows 3.3, 4.3 and 5.5 us with the weights in the cache; by tiles 10.4, 10.4 and 9.5; by the dots below 7.8
 // and 13.3 for 8 and 16). From memory its 16.8 MB of weights bound it, whose loads all leave at once and only once.
 template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1);
 template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -107,7 +107,8 @@ template <typename T, int NT> __global__ void __launch_bounds__(256) gated_few_k
 
 // Few rows of fp32, or of any stride and address: a warp two features, eight rows at a time, so that what it reads of x serves
 // four rows of weights; VEC neighbours of a row at a time where they are one aligned load. (1024 to 4096 fp32: 8 rows 10 us, 32 rows 40;
-// by tiles 42 and 42. 16 rows of 1022 bf16: 16, by tiles 24. The products bound it.)
+// by tiles 42 and 42. 16 rows of 1022 bf16: 15, by tiles 24. Its loads bound
+// it, 12 of 16 bytes to 128 multiply-adds of a lane: 32 rows are 14 TFLOP/s of the FP32 pipe's 74.)
 template <typename T, int VEC> __global__ void __launch_bounds__(256) gated_dot_kernel(const GatedParams p)
 {
     using P = Pack<T, VEC>;
@@ -200,8 +201,8 @@ template <typename T> __global__ void __launch_bounds__(256) gated_pack_kernel(c
 }
 
 // ---- fp16: what bounds dg and du (gtc::grads_scale): the largest |dh|, |bias| and squared norms of rows. The maximum of bit patterns
-// does not depend on their order. A backward pass of 1021 x 250 to 683 takes 46 us with it, 43 with |dh| alone; of 128 x 1024 to 4096
-// 47 and 43, of 16384 rows 574 and 573.
+// does not depend on their order. A backward pass of 1021 x 250 to 683, launched call by call, takes 46 us with it, 43 with |dh| alone; of 128 x
+// 1024 to 4096 47 and 43, of 16384 rows 574 and 573.
 struct Ranges {
     const __half *dh, *rows[3], *bias[2];   // rows of x and of both weights
     long long n, stride[3], count[3];
@@ -441,7 +442,8 @@ size_t gated_workspace(const GatedParams& p, bool backward, int sms)
 cudaError_t launch_gated_forward(const GatedParams& p, void* ws, int sms, cudaStream_t s)
 {
     const sdtw_gated& a = p.a;
-    // launched behind the kernels before them: a call of 16 rows, 1024 to 4096 bf16, then takes 4.7 us of 6.2, from memory 6.4 of 8.2
+    // launched behind the kernels before them: one call of 16 rows, 1024 to 4096 bf16, after the other takes 4.3 us then, 4.6 without;
+    // launched one by one, from memory, 6.4 and 8.2
     if (gated_is_few(p))
         return with_type(a.dtype, [&](auto t) {
             using T = decltype(t);

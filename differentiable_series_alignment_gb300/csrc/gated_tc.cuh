@@ -21,7 +21,7 @@
 //
 // Measured, 16384 x 1024 to 4096 bf16: FWD 140 us (1960 TFLOP/s; a library's product of x with both weights alone 143),
 // GRAD 150, DX 178, DW 182 in a backward pass of 514. The tensor pipe bounds them, and the power that it takes: one at a time, 2048 to
-// 2048 features, FWD, GRAD and DX run in 147, 152 and 148 us with the pipe 85 % busy. fp32, 16384 x 64 to 256: 26 us forward, 85 backward, bound by the
+// 2048 features, FWD, GRAD and DX run in 147, 152 and 148 us with the pipe 85 % busy. fp32, 16384 x 64 to 256: 18 us forward, 65 backward, bound by the
 // epilogue of two blocks of sum (three parts of dg and du are written) and the launches around it.
 #pragma once
 #include <algorithm>

@@ -11,10 +11,10 @@
 // all that its CTA takes; the CTAs' sums are added by a second launch in a fixed order: the same bits every time. Slabs
 // that a cluster cannot hold are read again, from the cache where it has them.
 //
-// Measured: 16 x 4096 x 512 bf16 by 32 groups with SiLU 45 us forward (3.0 TB/s), 86 backward (2.3); 64 such 151 and 303; 65535 rows of
-// 1024 by groups of 128 73 and 99 (3.7 and 4.1 TB/s). Not memory bounds these but instructions (three passes over a
-// pack, an exponential and a reciprocal an element in each that needs the activation) and the barriers between passes. Slabs
-// kept in shared memory take 43 and 84 us where reading them again takes 57 and 100.
+// Measured: 16 x 4096 x 512 bf16 by 32 groups with SiLU 41 us forward (3.3 TB/s), 85 backward (2.4); 64 such 147 and 306; 65535 rows of
+// 1024 by groups of 128 70 and 97 (3.8 and 4.1 TB/s). Not memory bounds these but instructions (three passes over a
+// pack, an exponential and a reciprocal an element in each that needs the activation) and the barriers between passes. Reading slabs again
+// in place of keeping them takes 47 and 100 us, 64 such 176 and 405.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -862,7 +862,8 @@ Layout layout(const GroupNormParams& p, bool backward, bool packs, int sms)
     };
     // CTAs of a cluster: until three fit on an SM side by side, or, where there are fewer than two an SM, until a thread has
     // eight rows: a cluster's exchanges take some 2 us (16 x 4096 x 512 bf16 with 1, 2, 4, 8 and 16 CTAs: forward 69, 61,
-    // 43, 59 and 107 us, of which this takes 4; backward 118, 112, 123, 85 and 140, of which it takes 8)
+    // 43, 59 and 107 us, of which this takes 4; backward 118, 112, 123, 85 and 140, of which it takes 8). Two an SM are enough for eight
+    // CTAs, as sixteen cost more (16 x 5000 x 512: backward 113 us, with sixteen 156; 16 x 12000: forward 121 and 149).
     // What the CTAs exchange has to fit: up to 64 KB for 16 CTAs and 256 groups, but a slab that is all of 2008 channels, each its own group,
     // takes 32 KB for every CTA.
     L.ctas = 1;

@@ -16,9 +16,9 @@
 // cluster's own barrier also waits for the results that are on their way to memory. One warp folds the CTAs' pairs and hands the
 // state on: read by every warp, they took 900 cycles of shared memory a round.
 //
-// Measured: 16 x 8192 x 1024 bf16 133 us forward (6.1 TB/s) and 257 backward (5.2); 4 such 43 and 80; 4 in fp32 69 and 113 (5.8 and 5.9 TB/s of
-// a copy's 6.8); 2 x 16383 x 264 fp16 23 and 43. Memory bounds the many; the few by their rounds, which pass the
-// state on one after the other. Loaded by the lanes that use them, 4 x 8192 x 1024 takes 127 and 189 us (ring: 40 and 76).
+// Measured: 16 x 8192 x 1024 bf16 132 us forward (6.1 TB/s) and 242 backward (5.6); 4 such 41 and 71; 4 in fp32 68 and 112 (5.9 and 6.0 TB/s of
+// a copy's 6.8); 2 x 16383 x 264 fp16 24 and 40. Memory bounds the many; the few by their rounds, which pass the
+// state on one after the other. Loaded by the lanes that use them, 4 x 8192 x 1023 takes 123 and 187 us.
 #include "activation.cuh"
 #include "attn_tc.cuh"
 #include "block.h"
@@ -89,7 +89,7 @@ template <int VEC> __device__ __forceinline__ void store_f32(float* p, Pair v) {
 // results of 32 bits, takes expf. Beyond e = 2^126 a is 0, a closed gate: smaller ones than that are no normal numbers. b is
 // 1 there, where e may be infinite.
 // A NaN stays, and in its channel, by a reciprocal for each: two channels that share one, 1 / s = t / (s t), share its rounding and a
-// NaN too. It costs 2 x 16383 x 264 fp16 25.6 us for 24.7 forward, and 16 x 8192 x 1024 bf16 none (133 and 257 us).
+// NaN too. It cost 2 x 16383 x 264 fp16 25.6 us for 24.7 forward, and 16 x 8192 x 1024 bf16 nothing.
 template <bool EXACT, int VEC> __device__ __forceinline__ void gates(Pair z, Pair& a, Pair& b) {
     float t[2], e[2] = {}, f[2] = {}, o[2] = {};
     upk2(EXACT ? z : mul2(z, pair(-1.4426950408889634f)), t[0], t[1]);
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) recurrence_bwd_kernel(
 }
 
 // A few new samples: a thread has its channels' positions from first to last, all of them on their way at once (64 x 1 x 1024 bf16:
-// 1.8 us, by the scan 12.4; 4096 x 8 x 1024: 37 us, 681).
+// 1.7 us, by the scan 12.4; 4096 x 8 x 1024: 39 us, 681). Their backward pass is the scan's: 19 and 1070 us.
 template <typename T, int VEC, int ROWS> __global__ void __launch_bounds__(128) recurrence_few_kernel(const RecurrenceParams p)
 {
     const sdtw_recurrence& a = p.a;
@@ -686,12 +686,12 @@ template <auto Kernel> int resident(int i, int threads, size_t smem)
 }
 
 // Few clusters of long series are of CTAs of sixteen warps, one an SM, sixteen CTAs to a cluster or eight, where all are resident at
-// once: what a round costs, some 2 us whatever its size, then comes least often (2 x 16383 x 264 fp16 forward: 23.4 us, with eight
-// warps and eight CTAs 28.5; 1 x 8192 x 768 fp32 22 and 30). Four such CTAs lose to eight of eight warps, with as many positions
-// (2 x 8192 x 640 bf16: 22.8 and 40.6 us for 21.1 and 36.5), and so do they all where one round is enough (1 x 1024 x 64 bf16: 6.4 us
-// for 5.0). Many clusters take two CTAs of eight warps an SM, as many to a cluster as all find such places: those of a second turn
-// would run by themselves (bf16 forward with 1, 2, 4 and 8 CTAs: 4 x 8192 x 1024 82, 54, 40 and 46 us, 16 x 8192 x 1024 130,
-// 144, 141 and 162; the former with sixteen warps in fp32, backward, 121 for 97).
+// once: what a round costs, some 2 us whatever its size, then comes least often (2 x 16383 x 264 fp16, ten clusters of eight:
+// 24.0 and 39.7 us, with eight warps 29.0 and 43.3; 1 x 8192 x 768 fp32 20.3 and 32.7, 25.8 and 34.3). Four such CTAs lose to eight of
+// eight warps, with as many positions (2 x 8192 x 640 bf16: 22.8 and 40.6 us for 21.1 and 36.5), and so do they all where one round is
+// enough (1 x 1024 x 64 bf16: 6.4 us for 5.0). Many clusters take two CTAs of eight warps an SM, as many to a cluster as all find such
+// places: those of a second turn would run by themselves (bf16 forward with 1, 2, 4 and 8 CTAs: 4 x 8192 x 1024 82, 54, 40 and 46 us, 16 x
+// 8192 x 1024 130, 144, 141 and 162; the former with sixteen warps in fp32, backward, 121 for 97).
 template <typename T, int VEC, int ROWS, bool RING, int TIED> cudaError_t run_rows(const RecurrenceParams& p, bool backward, int sms, cudaStream_t s)
 {
     const sdtw_recurrence& a = p.a;
