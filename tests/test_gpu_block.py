@@ -1045,14 +1045,12 @@ def test_few_rows_behind_other_work(package):
             assert torch.equal(h, want[i][i]) and torch.equal(out, package.gated_linear(want[i][i], square, square))
 
 
-@pytest.mark.parametrize("shape", [(1, 2000, 64), (400, 70, 64), (2, 5000, 64)], ids=str)
-@pytest.mark.parametrize("which", [1, 2], ids=["exchange", "loads"])
+# 1: a cluster's first CTA sends nothing (there have to be several); 2: one warp gives up its loads
+@pytest.mark.parametrize("shape,which", [((1, 2000, 64), 1), ((2, 5000, 64), 1), ((1, 2000, 64), 2), ((2, 5000, 64), 2), ((400, 70, 64), 2)], ids=str)
 def test_recurrence_waits_that_run_out(package, shape, which):
     """Whoever gives up a wait, the warp that folds the others' runs or one that does not: all results of the cluster are NaN, forward
     and backward, the status says so, and the next call is right again."""
     B, N, C = shape
-    if B == 400 and which == 1:
-        pytest.skip("one CTA sends nothing")
     gen = generator(71)
     lengths = torch.full((B,), N - 1, device="cuda", dtype=torch.int32)
     x, gate = (randn(gen, *shape, dtype=BF16, mean=m).requires_grad_() for m in (0.0, 1.0))
@@ -1122,3 +1120,30 @@ def test_fp32_values_without_three_parts(package, value):
     within(dwu, want[3], bound[3], "dup_weight")                # needs g alone
     many = package.gated_linear(x.repeat(5, 1), wg, wu)
     assert torch.isnan(many[:, 5]).all() == none and not torch.isnan(many[:, others]).any()
+
+
+def test_captured_fp16_gradients_follow_their_inputs(package):
+    """What fp16's gradients are scaled by is found anew in every replay."""
+    gen = generator(62)
+    R, K, F = 300, 72, 136
+    x, wg, wu = randn(gen, R, K, dtype=F16), *(randn(gen, F, K, dtype=F16, std=K ** -0.5) for _ in range(2))
+    dh = randn(gen, R, F, dtype=F16)
+    run = lambda: torch.autograd.grad(package.gated_linear(*leaves), leaves, dh)  # noqa: E731
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for scale in (2.0 ** -14, 1.0, 2.0 ** 4, 2.0 ** -8):
+        dh.copy_(randn(gen, R, F, dtype=F16, std=scale))
+        with torch.no_grad():
+            x.copy_(randn(gen, R, K, dtype=F16, std=0.5))
+        graph.replay()
+        want, _ = gated_reference(x.detach(), wg.detach(), wu.detach(), None, None, dh, "silu")
+        for g, exact, what in zip(got, want[1:], ("dx", "dwg", "dwu")):
+            error, own = (((t.double() - exact) ** 2).mean().sqrt() for t in (g, exact.to(F16)))
+            assert error <= 1.6 * own, (what, scale, float(error / own))
